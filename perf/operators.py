@@ -302,7 +302,7 @@ def _tables(s):
     ends = add.cumsum(0)
     need = torch.where(done, 0, ((seq + add + bs - 1) // bs - held).clamp_min(0))
     before = need.cumsum(0) - need
-    given = ~done & (before + need <= free)
+    given = ~done & ((need == 0) | (before + need <= free))
     gone = torch.where(done, held, 0)
     taken = torch.where(given, need, 0).sum()
     # blocks that the requests take, into their rows; blocks of the ended ones, behind the free ones
