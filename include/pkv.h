@@ -82,6 +82,8 @@ typedef enum { PKV_KV_BF16 = 0, PKV_KV_FP8_E4M3 = 1, PKV_KV_INT8 = 2 } pkv_kv_dt
 #define PKV_DEVERR_SLOT 0x2u         /* slot_mapping entry outside [-1, NB*bs) */
 #define PKV_DEVERR_CONTEXT_LEN 0x4u  /* context length outside [0, MB*bs] */
 #define PKV_DEVERR_TIMEOUT 0x8u      /* a bounded wait on a copy gave up */
+#define PKV_DEVERR_NO_BLOCKS 0x10u   /* too few free blocks for a request's new tokens */
+#define PKV_DEVERR_TREE 0x20u        /* a drafted tree's node count, parent or accepted path */
 
 /* Shape of one paged cache (both K and V).  Supported: block_size 16 or 32;
  * head_dim 64 or 128 for bf16, 128 for E4M3 and INT8. */
@@ -318,6 +320,167 @@ pkv_status pkv_decode_multi_describe(const pkv_cache_desc* cache, int32_t batch,
                                      int32_t num_query_tokens, int32_t num_q_heads,
                                      int32_t max_blocks_per_seq, const pkv_decode_opts* opts,
                                      pkv_decode_plan* plan);
+
+/*
+ * Attention of the nodes of a drafted tree over the paged cache: the
+ * verification step of speculative decoding when the draft proposes a tree
+ * of continuations instead of one ([PC] "How does speculative decoding
+ * interact with KV-cache compression?"; the pages show a linear draft).
+ *
+ * The last m_b of the n = context_lens[b] cached tokens of sequence b are the
+ * nodes of its tree, in any order in which a node comes after its parent
+ * (node u at position base + u, base = n - m_b).  Row t of q is node t:
+ *   out[b][t][h][:] = sum_j softmax_j(scale * q[b][t][h] . K_j) V_j,
+ *   over the j with 0 <= j < base and the j = base + u >= 0 of the nodes u
+ *   whose bit is set in row t of the tree's mask.
+ * Rows t >= m_b, and rows that attend to nothing, are zeros.  K and V of
+ * nodes that a row does not attend to have no influence on it, whatever they
+ * hold.  A row that attends to a node whose V holds a NaN or an infinity is
+ * NaN in every column.
+ *
+ *   q, out         device bf16 [B][T][Hq][D] (must not overlap), T = num_query_tokens
+ *                  in 1..PKV_MAX_QUERY_TOKENS, the most nodes of a sequence.
+ *   tree_mask      device uint32 [tree_batch][T][ceil(T / 32)]: bit u % 32 of
+ *                  word u / 32 of row t says that node t attends to node u
+ *                  (pkv_tree_masks makes it from the parents; any bits may be
+ *                  set).  Bits of nodes >= m_b are ignored.
+ *   tree_batch     batch, or 1: one tree for every sequence.
+ *   node_counts    device int32 [B]: m_b, in 0..T; NULL: T each.  A count out
+ *                  of range sets PKV_DEVERR_TREE; the sequence's rows are zeros.
+ *   workspace      pkv_decode_tree_workspace_bytes() bytes.
+ *   everything else as in pkv_paged_decode_multi, PKV_MATH_TC with T = 1 too.
+ */
+pkv_status pkv_paged_decode_tree(const pkv_cache_desc* cache,
+                                 const void* q, int32_t batch, int32_t num_query_tokens,
+                                 int32_t num_q_heads,
+                                 const void* k_cache, const void* v_cache,
+                                 const float* k_scale, const float* v_scale,
+                                 const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                 const int32_t* context_lens,
+                                 const uint32_t* tree_mask, int32_t tree_batch,
+                                 const int32_t* node_counts,
+                                 const int32_t* kv_group_ptr, int32_t num_layers, int32_t layer,
+                                 float scale, void* out,
+                                 void* workspace, size_t workspace_bytes,
+                                 const pkv_decode_opts* opts, void* stream);
+
+/* Workspace bytes and launch plan of pkv_paged_decode_tree. */
+size_t pkv_decode_tree_workspace_bytes(const pkv_cache_desc* cache, int32_t batch,
+                                       int32_t num_query_tokens, int32_t num_q_heads,
+                                       int32_t max_blocks_per_seq, const pkv_decode_opts* opts);
+pkv_status pkv_decode_tree_describe(const pkv_cache_desc* cache, int32_t batch,
+                                    int32_t num_query_tokens, int32_t num_q_heads,
+                                    int32_t max_blocks_per_seq, const pkv_decode_opts* opts,
+                                    pkv_decode_plan* plan);
+
+/*
+ * Masks and positions of drafted trees from their nodes' parents, once per
+ * step (every layer's pkv_paged_decode_tree then reads the masks).
+ *   parents      device int32 [B][T]: parent of node t, in -1..t-1 (-1: the
+ *                node follows the last token before the tree).  Another value
+ *                sets PKV_DEVERR_TREE and is taken as -1.
+ *   context_lens device int32 [B]: tokens including the nodes; NULL: positions
+ *                count from the tree's start.
+ *   node_counts  device int32 [B] in 0..T; NULL: T each.  A count out of range
+ *                sets PKV_DEVERR_TREE and is taken as 0.
+ *   mask         device uint32 [B][T][ceil(T / 32)] (written): node t attends
+ *                to itself and to what its parent attends to; rows past the
+ *                count are 0.
+ *   positions    device int32 [B][T] (written), or NULL: context_lens[b] -
+ *                count + the node's depth, at least 0; 0 past the count.
+ * T in 1..PKV_MAX_QUERY_TOKENS.  One kernel launch (none when B == 0).
+ */
+pkv_status pkv_tree_masks(const int32_t* parents, const int32_t* context_lens,
+                          const int32_t* node_counts, int32_t batch, int32_t num_nodes,
+                          uint32_t* mask, int32_t* positions, void* stream);
+
+/* Largest batch of pkv_extend_tables. */
+#define PKV_MAX_TABLE_REQUESTS 16384
+
+/*
+ * Block tables, slot mapping and positions of a step's new tokens, on the GPU
+ * ([BW] "Continuous Batching": a growing sequence takes blocks from the free
+ * pool, an ended one gives its blocks back).
+ *
+ * Request b holds block_counts[b] blocks, the first entries of its table row,
+ * with seq_lens[b] tokens in them.
+ *   new_lens[b] >= 0: the request adds that many tokens.  It takes
+ *     max(0, ceil((seq + new) / bs) - block_counts[b]) blocks off the head of
+ *     the free ring, in request order, and appends them to its row.
+ *   new_lens[b] == -1: the request has ended.  Its blocks, but for the first
+ *     borrowed_counts[b] (blocks that it shares and does not own), go behind
+ *     the free ring's tail in row order; its count becomes 0.  Its row's
+ *     entries stay as they are.
+ * A request is refused, with nothing of it changed and all its tokens' slots
+ * -1, when too few blocks are free (PKV_DEVERR_NO_BLOCKS; then no later
+ * request that needs blocks gets any), when its token rows do not fit
+ * (PKV_DEVERR_SLOT), or when its numbers are not valid (a negative length, new_lens
+ * below -1, seq + new above MB * bs, a count outside 0..MB, more tokens than
+ * blocks: PKV_DEVERR_CONTEXT_LEN).  Blocks that requests give back are not
+ * taken in the same call.  No block may be owned by two requests.
+ *
+ *   block_size, max_blocks_per_seq (MB), num_blocks (NB)   as in the cache.
+ *   seq_lens, new_lens  device int32 [B].
+ *   borrowed_counts     device int32 [B], or NULL: none.
+ *   block_tables        device int32 [B][MB], extended in place.
+ *   block_counts        device int32 [B].
+ *   new_block_counts    device int32 [B] (written); may be block_counts.
+ *   free_ring           device int32 [NB]: a ring of free block ids, in place.
+ *   free_state          device int32 [4]: the ring's head, the number of free
+ *                       blocks, and two zeros that the call uses and leaves zero.
+ *                       A head outside 0..NB-1, or a count that with the
+ *                       returned blocks is above NB, sets PKV_DEVERR_BLOCK_ID
+ *                       and refuses every request.
+ *   new_free_state      device int32 [4] (written); may be free_state.
+ *   context_lens        device int32 [B] (written): seq + new; 0 for ended
+ *                       and refused requests (inactive in a decode).
+ *   query_starts        device int32 [B + 1] (written): first token row of
+ *                       each request (sums of the new_lens >= 0, at most N).
+ *   slot_mapping        device int64 [N] (written), N = max_tokens: slot of
+ *                       every token row, for pkv_kv_append; -1 for the rows
+ *                       of refused requests and rows past the last request's.
+ *   positions           device int32 [N] (written), or NULL: the token's
+ *                       position in its sequence; 0 where the slot is -1.
+ * The arrays that are written must not overlap any other, but for the two
+ * that may be updated in place.  Calls that may run at the same time need
+ * separate state.  B in 0..PKV_MAX_TABLE_REQUESTS.  One kernel launch.
+ */
+pkv_status pkv_extend_tables(int32_t batch, int32_t block_size, int32_t max_blocks_per_seq,
+                             int32_t num_blocks, const int32_t* seq_lens, const int32_t* new_lens,
+                             const int32_t* borrowed_counts, int32_t* block_tables,
+                             const int32_t* block_counts, int32_t* new_block_counts,
+                             int32_t* free_ring, int32_t* free_state, int32_t* new_free_state,
+                             int32_t* context_lens, int32_t* query_starts,
+                             int64_t* slot_mapping, int32_t* positions, int32_t max_tokens,
+                             void* stream);
+
+/*
+ * After a drafted tree was verified: move the accepted path's tokens together,
+ * in every cache slot of k_cache and v_cache.  For i < accept_counts[b] the K
+ * and V rows of node accept_idx[b][i] move to position base + i (base =
+ * context_lens[b] - nodes, as in pkv_paged_decode_tree), and seq_lens[b]
+ * becomes base + accept_counts[b], the tokens that the sequence keeps.
+ *   accept_idx     device int32 [B][max_accept]: the accepted nodes, strictly
+ *                  increasing (a path's nodes come after their parents).
+ *   accept_counts  device int32 [B], in 0..min(max_accept, nodes).
+ *   context_lens, node_counts, num_nodes (T)  as for pkv_paged_decode_tree.
+ *   k_scale, v_scale   E4M3 / INT8 caches.  A row that moves to a page with
+ *                  other parameters is requantised: code value x scale in
+ *                  fp32, then as pkv_kv_append.
+ *   seq_lens       device int32 [B] (written; must not overlap context_lens).
+ * A sequence with a count, a node or a block id out of range, or nodes that do
+ * not increase, keeps its cache as it is and gets seq_lens[b] = base (0 if that
+ * is not valid either), with PKV_DEVERR_TREE, _CONTEXT_LEN or _BLOCK_ID.
+ * max_accept in 1..PKV_MAX_QUERY_TOKENS.  Blocks of the moved rows must belong
+ * to one sequence only.  One kernel launch (none when B == 0).
+ */
+pkv_status pkv_compact_tokens(const pkv_cache_desc* cache, const int32_t* accept_idx,
+                              const int32_t* accept_counts, int32_t max_accept, int32_t batch,
+                              const int32_t* context_lens, const int32_t* node_counts,
+                              int32_t num_nodes, const int32_t* block_tables,
+                              int32_t max_blocks_per_seq, void* k_cache, void* v_cache,
+                              const float* k_scale, const float* v_scale, int32_t* seq_lens,
+                              void* stream);
 
 /* Size of the library's built-in decode workspace (see below). */
 #define PKV_STATIC_WORKSPACE_MAX_BYTES ((size_t)16 << 20)

@@ -13,10 +13,18 @@ Layouts (see the header for the full contract):
   k_scale, v_scale  float32 [S][NB][Hkv] (FP8 cache only);
   q, out            bfloat16 [B][Hq][D];
   block_tables      int32 [B][MB];  context_lens int32 [B];
-  kv_group_ptr      host int32 [L] (shared-with pointer per layer).
+  kv_group_ptr      host int32 [L] (shared-with pointer per layer);
+  tree_mask         int32 [B or 1][T][ceil(T / 32)], the bits of a drafted tree's nodes.
+
+A step of speculative decoding with drafted trees:
+  :func:`extend_tables` (blocks and slots for the nodes), :func:`kv_append`,
+  :func:`tree_masks` (what each node sees, and its position),
+  :func:`paged_decode_tree` per layer, and, once the target model has chosen
+  a path, :func:`compact_tokens`.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -33,6 +41,7 @@ STATUS_NAMES = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "alignment"
 KV_BF16, KV_FP8_E4M3, KV_INT8 = 0, 1, 2
 MATH_AUTO, MATH_FFMA, MATH_MMA, MATH_TC = 0, 1, 2, 3
 DEVERR_BLOCK_ID, DEVERR_SLOT, DEVERR_CONTEXT_LEN, DEVERR_TIMEOUT = 1, 2, 4, 8
+DEVERR_NO_BLOCKS, DEVERR_TREE = 16, 32
 
 
 class PkvError(RuntimeError):
@@ -104,6 +113,19 @@ def load() -> ctypes.CDLL:
         lib.pkv_append_and_decode.restype = ctypes.c_int
         lib.pkv_append_and_decode.argtypes = [pdesc, P, P, P, i32, P, i32, i32, i32, P, P, P, P, P, i32, P,
                                               P, i32, i32, f32, P, P, sz, popts, P]
+        lib.pkv_paged_decode_tree.restype = ctypes.c_int
+        lib.pkv_paged_decode_tree.argtypes = [pdesc, P, i32, i32, i32, P, P, P, P, P, i32, P, P, i32, P, P, i32,
+                                              i32, f32, P, P, sz, popts, P]
+        lib.pkv_decode_tree_workspace_bytes.restype = sz
+        lib.pkv_decode_tree_workspace_bytes.argtypes = [pdesc, i32, i32, i32, i32, popts]
+        lib.pkv_decode_tree_describe.restype = ctypes.c_int
+        lib.pkv_decode_tree_describe.argtypes = [pdesc, i32, i32, i32, i32, popts, ctypes.POINTER(DecodePlan)]
+        lib.pkv_tree_masks.restype = ctypes.c_int
+        lib.pkv_tree_masks.argtypes = [P, P, P, i32, i32, P, P, P]
+        lib.pkv_extend_tables.restype = ctypes.c_int
+        lib.pkv_extend_tables.argtypes = [i32, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, P, P, P, i32, P]
+        lib.pkv_compact_tokens.restype = ctypes.c_int
+        lib.pkv_compact_tokens.argtypes = [pdesc, P, P, i32, i32, P, P, i32, P, i32, P, P, P, P, P, P]
         lib.pkv_paged_decode_static_workspace.restype = ctypes.c_int
         lib.pkv_paged_decode_static_workspace.argtypes = [pdesc, P, i32, i32, P, P, P, P, P, i32, P,
                                                           P, i32, i32, f32, P, popts, P]
@@ -169,6 +191,21 @@ def _need_cuda(name: str, t: torch.Tensor, dtype=None):
         raise PkvError(1, f"{name} must be {dtype}, got {t.dtype}")
 
 
+def _need_here(name: str, t: torch.Tensor, dtype, shape=None):
+    """_need_cuda, on the current device (where the call launches), of this
+    shape."""
+    _need_cuda(name, t, dtype)
+    if t.get_device() != torch.cuda.current_device():
+        raise PkvError(1, f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise PkvError(1, f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _allocating_on(stream):
+    """Context in which new tensors belong to the stream that a call launches on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _need_page_params(desc: CacheDesc, t: Optional[torch.Tensor], name: str):
     """E4M3: fp32 [S][NB][Hkv]; INT8: fp32 [S][NB][Hkv][2] (scale, zero)."""
     _need_cuda(name, t, torch.float32)
@@ -230,34 +267,36 @@ def decode_opts(partition_blocks: int = 0, math: int = MATH_AUTO, warps: int = 0
 
 def decode_workspace_bytes(k_cache: torch.Tensor, batch: int, num_q_heads: int,
                            max_blocks_per_seq: int, opts: Optional[DecodeOpts] = None,
-                           query_tokens: int = 1) -> int:
+                           query_tokens: int = 1, tree: bool = False) -> int:
     desc = cache_desc(k_cache)
-    n = load().pkv_decode_multi_workspace_bytes(ctypes.byref(desc), int(batch), int(query_tokens),
-                                                int(num_q_heads), int(max_blocks_per_seq),
-                                                ctypes.byref(opts) if opts is not None else None)
+    lib = load()
+    fn = lib.pkv_decode_tree_workspace_bytes if tree else lib.pkv_decode_multi_workspace_bytes
+    n = fn(ctypes.byref(desc), int(batch), int(query_tokens), int(num_q_heads), int(max_blocks_per_seq),
+           ctypes.byref(opts) if opts is not None else None)
     if n == 0:
         raise PkvError(1, "bad arguments for the decode workspace")
     return int(n)
 
 
 def decode_plan(k_cache: torch.Tensor, batch: int, num_q_heads: int, max_blocks_per_seq: int,
-                opts: Optional[DecodeOpts] = None, query_tokens: int = 1) -> dict:
+                opts: Optional[DecodeOpts] = None, query_tokens: int = 1, tree: bool = False) -> dict:
     """The resolved launch plan of a decode call (host only, nothing launched)."""
     desc = cache_desc(k_cache)
     plan = DecodePlan()
-    _check(load().pkv_decode_multi_describe(ctypes.byref(desc), int(batch), int(query_tokens),
-                                            int(num_q_heads), int(max_blocks_per_seq),
-                                            ctypes.byref(opts) if opts is not None else None,
-                                            ctypes.byref(plan)))
+    lib = load()
+    fn = lib.pkv_decode_tree_describe if tree else lib.pkv_decode_multi_describe
+    _check(fn(ctypes.byref(desc), int(batch), int(query_tokens), int(num_q_heads), int(max_blocks_per_seq),
+              ctypes.byref(opts) if opts is not None else None, ctypes.byref(plan)))
     return {f: getattr(plan, f) for f, _ in DecodePlan._fields_}
 
 
 def new_decode_workspace(k_cache: torch.Tensor, batch: int, num_q_heads: int,
                          max_blocks_per_seq: int, opts: Optional[DecodeOpts] = None,
-                         query_tokens: int = 1) -> torch.Tensor:
+                         query_tokens: int = 1, tree: bool = False) -> torch.Tensor:
     """Zero-filled device workspace for :func:`paged_decode` (or, with
-    ``query_tokens`` T, :func:`paged_decode_multi`)."""
-    n = decode_workspace_bytes(k_cache, batch, num_q_heads, max_blocks_per_seq, opts, query_tokens)
+    ``query_tokens`` T, :func:`paged_decode_multi`; with ``tree``,
+    :func:`paged_decode_tree`)."""
+    n = decode_workspace_bytes(k_cache, batch, num_q_heads, max_blocks_per_seq, opts, query_tokens, tree)
     return torch.zeros(n, dtype=torch.uint8, device=k_cache.device)
 
 
@@ -320,6 +359,48 @@ def _marshal_decode(q, k_cache, v_cache, block_tables, context_lens, kv_group_pt
     return lib.pkv_paged_decode, (ctypes.byref(desc), _ptr(q), B, Hq) + tail, out, workspace
 
 
+def _marshal_tree(q, k_cache, v_cache, block_tables, context_lens, tree_mask, node_counts, kv_group_ptr, layer,
+                  scale, out, workspace, k_scale, v_scale, opts, stream=None):
+    """As _marshal_decode, for a drafted-tree decode."""
+    desc = cache_desc(k_cache)
+    _need_here("q", q, torch.bfloat16)
+    if q.dim() != 4:
+        raise PkvError(1, "q must be [B][T][Hq][D]")
+    B, T, Hq, D = q.shape
+    if D != desc.head_dim:
+        raise PkvError(1, "q does not match the cache's head_dim")
+    _need_here("k_cache", k_cache, k_cache.dtype)
+    _need_here("v_cache", v_cache, k_cache.dtype, tuple(k_cache.shape))
+    _need_here("block_tables", block_tables, torch.int32)
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise PkvError(1, f"block_tables must be [{B}][MB]")
+    MB = block_tables.shape[1]
+    _need_here("context_lens", context_lens, torch.int32, (B,))
+    _need_here("tree_mask", tree_mask, torch.int32)
+    if tree_mask.dim() != 3 or tree_mask.shape[0] not in (1, B) or tree_mask.shape[1:] != (T, (T + 31) // 32):
+        raise PkvError(1, f"tree_mask must be [{B} or 1][{T}][{(T + 31) // 32}], got {list(tree_mask.shape)}")
+    if node_counts is not None:
+        _need_here("node_counts", node_counts, torch.int32, (B,))
+    if desc.dtype != KV_BF16:
+        _need_page_params(desc, k_scale, "k_scale")
+        _need_page_params(desc, v_scale, "v_scale")
+    with _allocating_on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            n = decode_workspace_bytes(k_cache, B, Hq, MB, opts, T, tree=True)
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    _need_here("out", out, torch.bfloat16, (B, T, Hq, D))
+    _need_here("workspace", workspace, workspace.dtype)
+    gp = (ctypes.c_int32 * len(kv_group_ptr))(*[int(x) for x in kv_group_ptr])
+    args = (ctypes.byref(desc), _ptr(q), B, T, Hq, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(block_tables), MB, _ptr(context_lens), _ptr(tree_mask), int(tree_mask.shape[0]), _ptr(node_counts),
+            gp, len(kv_group_ptr), int(layer), float(D ** -0.5 if scale is None else scale), _ptr(out),
+            _ptr(workspace), workspace.numel() * workspace.element_size(),
+            ctypes.byref(opts) if opts is not None else None)
+    return load().pkv_paged_decode_tree, args, out, workspace
+
+
 def paged_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                  block_tables: torch.Tensor, context_lens: torch.Tensor,
                  kv_group_ptr: Sequence[int] = (0,), layer: int = 0,
@@ -371,10 +452,30 @@ def append_and_decode(k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: to
     return out
 
 
+def paged_decode_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      block_tables: torch.Tensor, context_lens: torch.Tensor, tree_mask: torch.Tensor,
+                      node_counts: Optional[torch.Tensor] = None,
+                      kv_group_ptr: Sequence[int] = (0,), layer: int = 0,
+                      scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None,
+                      k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                      opts: Optional[DecodeOpts] = None, stream=None) -> torch.Tensor:
+    """Attention of the nodes of a drafted tree, q [B][T][Hq][D] (bf16): the
+    last ``node_counts[b]`` (default T) of the context_lens[b] cached tokens
+    are the sequence's nodes; row t attends to every token before them and to
+    the nodes whose bits are set in row t of ``tree_mask`` (int32 [B or
+    1][T][ceil(T / 32)], see :func:`tree_masks`).  Rows past the count are
+    zeros.  Returns out [B][T][Hq][D]."""
+    fn, args, out, _ = _marshal_tree(q, k_cache, v_cache, block_tables, context_lens, tree_mask, node_counts,
+                                     kv_group_ptr, layer, scale, out, workspace, k_scale, v_scale, opts, stream)
+    _check(fn(*args, _stream_handle(stream)))
+    return out
+
+
 class PreparedDecode:
-    """A decode call (:func:`paged_decode`, :func:`paged_decode_multi`, or
+    """A decode call (:func:`paged_decode`, :func:`paged_decode_multi`,
     :func:`append_and_decode` when ``k_new`` / ``v_new`` / ``slot_mapping``
-    are given) whose arguments were checked and marshalled once.  Each call
+    are given, or :func:`paged_decode_tree` when ``tree_mask`` is) whose arguments were checked and marshalled once.  Each call
     of the object enqueues the same launch again, reading whatever the bound
     tensors hold at that time: the pattern of a serving loop whose step
     buffers stay in place (as under CUDA graph capture) and whose host cost
@@ -384,13 +485,22 @@ class PreparedDecode:
 
     def __init__(self, q, k_cache, v_cache, block_tables, context_lens, kv_group_ptr=(0,), layer=0,
                  scale=None, out=None, workspace=None, k_scale=None, v_scale=None, opts=None,
-                 k_new=None, v_new=None, slot_mapping=None, stream=None):
-        fn, args, out, workspace = _marshal_decode(q, k_cache, v_cache, block_tables, context_lens,
-                                                   kv_group_ptr, layer, scale, out, workspace, k_scale,
-                                                   v_scale, opts, k_new, v_new, slot_mapping)
+                 k_new=None, v_new=None, slot_mapping=None, stream=None, tree_mask=None, node_counts=None):
+        if tree_mask is not None:
+            if k_new is not None or v_new is not None or slot_mapping is not None:
+                raise PkvError(1, "a drafted-tree decode does not append: call kv_append before it")
+            fn, args, out, workspace = _marshal_tree(q, k_cache, v_cache, block_tables, context_lens, tree_mask,
+                                                     node_counts, kv_group_ptr, layer, scale, out, workspace,
+                                                     k_scale, v_scale, opts, stream)
+        elif node_counts is not None:
+            raise PkvError(1, "node_counts without tree_mask")
+        else:
+            fn, args, out, workspace = _marshal_decode(q, k_cache, v_cache, block_tables, context_lens,
+                                                       kv_group_ptr, layer, scale, out, workspace, k_scale,
+                                                       v_scale, opts, k_new, v_new, slot_mapping)
         self._fn, self._args = fn, args
         self._keep = (q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, opts, k_new,
-                      v_new, slot_mapping)
+                      v_new, slot_mapping, tree_mask, node_counts)
         self.out, self.workspace = out, workspace
         self._stream = None if stream is None else _stream_handle(stream)
 
@@ -400,6 +510,198 @@ class PreparedDecode:
         if st != PKV_OK:
             _check(st)
         return self.out
+
+
+# ---------------------------------------------------------------------------
+# drafted trees and block tables (each _marshal_* checks one call's arguments
+# and returns the C function, its arguments without the stream, the result,
+# and the tensors to keep alive)
+# ---------------------------------------------------------------------------
+def _marshal_tree_masks(parents, context_lens=None, node_counts=None, mask=None, positions=None, stream=None):
+    _need_here("parents", parents, torch.int32)
+    if parents.dim() != 2:
+        raise PkvError(1, "parents must be [B][T]")
+    B, T = parents.shape
+    if not 1 <= T <= MAX_QUERY_TOKENS:
+        raise PkvError(1, f"parents must have 1..{MAX_QUERY_TOKENS} nodes, got {T}")
+    for name, t in (("context_lens", context_lens), ("node_counts", node_counts)):
+        if t is not None:
+            _need_here(name, t, torch.int32, (B,))
+    W = (T + 31) // 32
+    with _allocating_on(stream):
+        if mask is None:
+            mask = torch.empty((B, T, W), dtype=torch.int32, device=parents.device)
+        if positions is None:
+            positions = torch.empty((B, T), dtype=torch.int32, device=parents.device)
+    _need_here("mask", mask, torch.int32, (B, T, W))
+    _need_here("positions", positions, torch.int32, (B, T))
+    args = (_ptr(parents), _ptr(context_lens), _ptr(node_counts), B, T, _ptr(mask), _ptr(positions))
+    return load().pkv_tree_masks, args, (mask, positions), (parents, context_lens, node_counts)
+
+
+def tree_masks(parents: torch.Tensor, context_lens: Optional[torch.Tensor] = None,
+               node_counts: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+               positions: Optional[torch.Tensor] = None, stream=None):
+    """Masks and positions of drafted trees from ``parents`` (int32 [B][T],
+    parent of node t in -1..t-1): (mask int32 [B][T][ceil(T / 32)], positions
+    int32 [B][T]).  Node t sees itself and what its parent sees; its position
+    is the number of tokens before the tree (context_lens[b] - node_counts[b])
+    plus its depth."""
+    fn, args, result, _ = _marshal_tree_masks(parents, context_lens, node_counts, mask, positions, stream)
+    _check(fn(*args, _stream_handle(stream)))
+    return result
+
+
+def new_free_ring(block_ids, num_blocks: int, device="cuda"):
+    """(free_ring int32 [num_blocks], free_state int32 [4]) of
+    :func:`extend_tables` with these free block ids, first to be taken first."""
+    ids = torch.as_tensor(block_ids, dtype=torch.int32).reshape(-1)
+    if ids.numel() > num_blocks:
+        raise PkvError(1, f"{ids.numel()} free blocks in a pool of {num_blocks}")
+    ring = torch.full((int(num_blocks),), -1, dtype=torch.int32)
+    ring[:ids.numel()] = ids.cpu()
+    state = torch.tensor([0, ids.numel(), 0, 0], dtype=torch.int32)
+    return ring.to(device), state.to(device)
+
+
+def _marshal_extend_tables(seq_lens, new_lens, block_tables, block_counts, free_ring, free_state, block_size, max_tokens,
+                           borrowed_counts=None, new_block_counts=None, new_free_state=None, context_lens=None,
+                           query_starts=None, slot_mapping=None, positions=None, stream=None):
+    i32 = torch.int32
+    _need_here("block_tables", block_tables, i32)
+    if block_tables.dim() != 2:
+        raise PkvError(1, "block_tables must be [B][MB]")
+    B, MB = block_tables.shape
+    N = int(max_tokens)
+    if N < 0:
+        raise PkvError(1, f"max_tokens {N} < 0")
+    new_block_counts = block_counts if new_block_counts is None else new_block_counts
+    new_free_state = free_state if new_free_state is None else new_free_state
+    for name, t in (("seq_lens", seq_lens), ("new_lens", new_lens), ("block_counts", block_counts),
+                    ("new_block_counts", new_block_counts)):
+        _need_here(name, t, i32, (B,))
+    if borrowed_counts is not None:
+        _need_here("borrowed_counts", borrowed_counts, i32, (B,))
+    _need_here("free_ring", free_ring, i32)
+    if free_ring.dim() != 1:
+        raise PkvError(1, "free_ring must be [NB]")
+    _need_here("free_state", free_state, i32, (4,))
+    _need_here("new_free_state", new_free_state, i32, (4,))
+    dev = block_tables.device
+    with _allocating_on(stream):
+        if context_lens is None:
+            context_lens = torch.empty((B,), dtype=i32, device=dev)
+        if query_starts is None:
+            query_starts = torch.empty((B + 1,), dtype=i32, device=dev)
+        if slot_mapping is None:
+            slot_mapping = torch.empty((N,), dtype=torch.int64, device=dev)
+        if positions is None:
+            positions = torch.empty((N,), dtype=i32, device=dev)
+    _need_here("context_lens", context_lens, i32, (B,))
+    _need_here("query_starts", query_starts, i32, (B + 1,))
+    _need_here("slot_mapping", slot_mapping, torch.int64, (N,))
+    _need_here("positions", positions, i32, (N,))
+    args = (B, int(block_size), MB, free_ring.shape[0], _ptr(seq_lens), _ptr(new_lens), _ptr(borrowed_counts),
+            _ptr(block_tables), _ptr(block_counts), _ptr(new_block_counts), _ptr(free_ring), _ptr(free_state),
+            _ptr(new_free_state), _ptr(context_lens), _ptr(query_starts), _ptr(slot_mapping), _ptr(positions), N)
+    return (load().pkv_extend_tables, args, (context_lens, query_starts, slot_mapping, positions),
+            (seq_lens, new_lens, borrowed_counts, block_tables, block_counts, new_block_counts, free_ring, free_state,
+             new_free_state))
+
+
+def extend_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_tables: torch.Tensor,
+                  block_counts: torch.Tensor, free_ring: torch.Tensor, free_state: torch.Tensor, block_size: int,
+                  max_tokens: int, borrowed_counts: Optional[torch.Tensor] = None,
+                  new_block_counts: Optional[torch.Tensor] = None, new_free_state: Optional[torch.Tensor] = None,
+                  context_lens: Optional[torch.Tensor] = None, query_starts: Optional[torch.Tensor] = None,
+                  slot_mapping: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None, stream=None):
+    """Blocks, slots and positions for the tokens that each request adds this
+    step (int32 new_lens [B]; -1: the request has ended and gives its blocks
+    back), all on the GPU.  Request b has seq_lens[b] tokens in its
+    block_counts[b] blocks; free blocks come from the ring of
+    :func:`new_free_ring`.  block_tables and the ring are updated in place,
+    the counts and the ring's state too unless ``new_block_counts`` /
+    ``new_free_state`` are given.  Returns (context_lens [B], query_starts
+    [B + 1], slot_mapping int64 [max_tokens], positions [max_tokens]).  A
+    request that cannot be served has context length 0 and slots -1, and
+    :func:`read_device_error` says why (see pkv_extend_tables in the
+    header)."""
+    fn, args, result, _ = _marshal_extend_tables(seq_lens, new_lens, block_tables, block_counts, free_ring, free_state,
+                                                 block_size, max_tokens, borrowed_counts, new_block_counts,
+                                                 new_free_state, context_lens, query_starts, slot_mapping, positions,
+                                                 stream)
+    _check(fn(*args, _stream_handle(stream)))
+    return result
+
+
+def _marshal_compact_tokens(accept_idx, accept_counts, context_lens, block_tables, k_cache, v_cache, num_nodes,
+                            node_counts=None, k_scale=None, v_scale=None, seq_lens=None, stream=None):
+    desc = cache_desc(k_cache)
+    i32 = torch.int32
+    _need_here("k_cache", k_cache, k_cache.dtype)
+    _need_here("v_cache", v_cache, k_cache.dtype, tuple(k_cache.shape))
+    _need_here("accept_idx", accept_idx, i32)
+    if accept_idx.dim() != 2:
+        raise PkvError(1, "accept_idx must be [B][max_accept]")
+    B, A = accept_idx.shape
+    _need_here("accept_counts", accept_counts, i32, (B,))
+    _need_here("context_lens", context_lens, i32, (B,))
+    _need_here("block_tables", block_tables, i32)
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise PkvError(1, f"block_tables must be [{B}][MB]")
+    if node_counts is not None:
+        _need_here("node_counts", node_counts, i32, (B,))
+    if desc.dtype != KV_BF16:
+        _need_page_params(desc, k_scale, "k_scale")
+        _need_page_params(desc, v_scale, "v_scale")
+    if seq_lens is None:
+        with _allocating_on(stream):
+            seq_lens = torch.empty((B,), dtype=i32, device=k_cache.device)
+    _need_here("seq_lens", seq_lens, i32, (B,))
+    args = (ctypes.byref(desc), _ptr(accept_idx), _ptr(accept_counts), A, B, _ptr(context_lens), _ptr(node_counts),
+            int(num_nodes), _ptr(block_tables), block_tables.shape[1], _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+            _ptr(v_scale), _ptr(seq_lens))
+    return (load().pkv_compact_tokens, args, seq_lens,
+            (accept_idx, accept_counts, context_lens, node_counts, block_tables, k_cache, v_cache, k_scale, v_scale))
+
+
+def compact_tokens(accept_idx: torch.Tensor, accept_counts: torch.Tensor, context_lens: torch.Tensor,
+                   block_tables: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, num_nodes: int,
+                   node_counts: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None,
+                   v_scale: Optional[torch.Tensor] = None, seq_lens: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """Keep the accepted path of each verified tree: the K and V rows of nodes
+    accept_idx[b][:accept_counts[b]] (strictly increasing) move, in every
+    cache slot, to the positions from the tree's start on.  ``num_nodes`` is T
+    of :func:`paged_decode_tree`.  Returns seq_lens [B], the tokens that each
+    sequence keeps."""
+    fn, args, result, _ = _marshal_compact_tokens(accept_idx, accept_counts, context_lens, block_tables, k_cache, v_cache,
+                                                  num_nodes, node_counts, k_scale, v_scale, seq_lens, stream)
+    _check(fn(*args, _stream_handle(stream)))
+    return result
+
+
+class PreparedCall:
+    """A call of :func:`tree_masks`, :func:`extend_tables` or
+    :func:`compact_tokens` (``op``, then its arguments) checked and marshalled
+    once, like :class:`PreparedDecode`: each call of the object enqueues the
+    same launch again on whatever the bound tensors hold, and returns the
+    bound result tensors."""
+
+    def __init__(self, op, *args, stream=None, **kwargs):
+        marshal = {tree_masks: _marshal_tree_masks, extend_tables: _marshal_extend_tables,
+                   compact_tokens: _marshal_compact_tokens}.get(op)
+        if marshal is None:
+            raise PkvError(1, "PreparedCall takes tree_masks, extend_tables or compact_tokens")
+        self._fn, self._args, self.result, self._keep = marshal(*args, stream=stream, **kwargs)
+        self._stream = None if stream is None else _stream_handle(stream)
+
+    def __call__(self, stream=None):
+        h = _stream_handle(stream) if (stream is not None or self._stream is None) else self._stream
+        st = self._fn(*self._args, h)
+        if st != PKV_OK:
+            _check(st)
+        return self.result
 
 
 def copy_blocks(src_k: torch.Tensor, src_v: torch.Tensor, dst_k: torch.Tensor,

@@ -1,0 +1,155 @@
+// Accepted draft tokens moved together, in every cache slot.
+//
+// A verified draft of m nodes occupies positions base .. base + m - 1 of its
+// sequence (base = n - m).  Of it the path idx[0] < idx[1] < ... is kept: the
+// K and V rows of node idx[i] move to position base + i.  As idx[i] >= i, a
+// row's new place never lies behind its old one, and no later row is read from
+// a place that an earlier one was written to; so a thread that moves one
+// 16-byte chunk of the rows in order, eight loads before their stores, needs
+// no other ordering.
+//
+// One-byte pages: a row that moves to a page with the same parameters keeps
+// its codes; else each code's value (code x scale, for INT8 (code - zero) x
+// scale, in fp32) is quantised with the new page's parameters as an append
+// does.
+//
+// One CTA per (sequence, cache slot) takes all KV heads of K and V: bound by
+// HBM, 2 x the moved rows' bytes.
+#include <algorithm>
+
+#include "kv_append.cuh"
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+
+constexpr int kCompactThreads = 256;
+constexpr int kCompactBatch = 8;  // rows in flight per thread
+
+template <int KV>
+__device__ __forceinline__ uint4 requantise(uint4 x, const float* params, size_t src, size_t dst) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  if constexpr (KV == PKV_KV_FP8_E4M3) {
+    const float s = __ldg(params + src), d = __ldg(params + dst);
+    if (__float_as_uint(s) == __float_as_uint(d)) return x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h[2];
+      e4m3x4_to_f16x2x2(w[i], h[0], h[1]);
+      uint32_t o = 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+        const float2 v = make_float2(__fdiv_rn(__fmul_rn(f.x, s), d), __fdiv_rn(__fmul_rn(f.y, s), d));
+        o |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3)) << (16 * k);
+      }
+      w[i] = o;
+    }
+  } else if constexpr (KV == PKV_KV_INT8) {
+    const float2 s = __ldg(reinterpret_cast<const float2*>(params) + src);
+    const float2 d = __ldg(reinterpret_cast<const float2*>(params) + dst);
+    if (__float_as_uint(s.x) == __float_as_uint(d.x) && __float_as_uint(s.y) == __float_as_uint(d.y)) return x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t o = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float code = static_cast<float>(static_cast<int8_t>(w[i] >> (8 * k)));
+        o |= int8_code(__fmul_rn(__fsub_rn(code, s.y), s.x), d.x, d.y) << (8 * k);
+      }
+      w[i] = o;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int KV>  // pkv_kv_dtype
+__global__ void __launch_bounds__(kCompactThreads) compact_tokens_kernel(const CompactArgs a) {
+  __shared__ int64_t s_src[PKV_MAX_QUERY_TOKENS], s_dst[PKV_MAX_QUERY_TOKENS];  // block * bs + token, per row
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x;
+  const int b = blockIdx.x / a.S, slot = blockIdx.x - b * a.S;
+  const int n = a.context_lens[b], take = a.counts[b];
+  const int nodes = a.node_counts != nullptr ? a.node_counts[b] : a.T;
+  const int base = n - nodes;
+  unsigned err = 0;
+  if (n < 0 || n > a.MB * a.bs) err |= PKV_DEVERR_CONTEXT_LEN;
+  else if (nodes < 0 || nodes > a.T || take < 0 || take > min(a.A, nodes) || (take > 0 && base < 0)) err |= PKV_DEVERR_TREE;
+  if (err == 0) {
+    for (int i = tid; i < take; i += blockDim.x) {
+      const int u = a.idx[static_cast<size_t>(b) * a.A + i];
+      const int before = i > 0 ? a.idx[static_cast<size_t>(b) * a.A + i - 1] : -1;
+      if (u <= before || u >= nodes) {
+        err |= PKV_DEVERR_TREE;
+      } else if (u != i) {
+        const int ps = base + u, pd = base + i;
+        const int es = a.block_tables[static_cast<size_t>(b) * a.MB + ps / a.bs];
+        const int ed = a.block_tables[static_cast<size_t>(b) * a.MB + pd / a.bs];
+        if (static_cast<unsigned>(es) >= static_cast<unsigned>(a.NB) || static_cast<unsigned>(ed) >= static_cast<unsigned>(a.NB))
+          err |= PKV_DEVERR_BLOCK_ID;
+        s_src[i] = static_cast<int64_t>(es) * a.bs + ps % a.bs;
+        s_dst[i] = static_cast<int64_t>(ed) * a.bs + pd % a.bs;
+      } else {
+        s_src[i] = s_dst[i] = -1;  // stays where it is
+      }
+    }
+  }
+  // a sequence with anything wrong stays as it is (every thread learns of it)
+  const bool wrong = __syncthreads_or(err != 0);
+  if (slot == 0) {
+    if (err) atomicOr(a.err, err);
+    if (tid == 0) {
+      const bool lens_ok = n >= 0 && n <= a.MB * a.bs && nodes >= 0 && nodes <= a.T;
+      a.seq_lens[b] = !wrong && take > 0 ? base + take : (lens_ok ? max(base, 0) : 0);
+    }
+  }
+  if (wrong || take == 0) return;
+  int first = 0;  // leading rows that stay (idx[i] == i only up to the first that moves)
+  while (first < take && s_src[first] < 0) ++first;
+  constexpr int kElem = KV == PKV_KV_BF16 ? 2 : 1;
+  const int row_chunks = a.D * kElem / 16;
+  const int per_tensor = a.Hkv * row_chunks;
+  for (int c = tid; c < 2 * per_tensor; c += blockDim.x) {
+    const bool is_v = c >= per_tensor;
+    const int r = is_v ? c - per_tensor : c;
+    const int h = r / row_chunks, chunk = r - h * row_chunks;
+    uint4* cache = reinterpret_cast<uint4*>(is_v ? a.vc : a.kc);
+    const float* params = is_v ? a.vs : a.ks;
+    const int64_t slot_pages = static_cast<int64_t>(slot) * a.NB;
+    auto page_of = [&](int64_t token) { return (slot_pages + token / a.bs) * a.Hkv + h; };
+    auto chunk_of = [&](int64_t token) { return (page_of(token) * a.bs + token % a.bs) * row_chunks + chunk; };
+    for (int i0 = first; i0 < take; i0 += kCompactBatch) {
+      uint4 x[kCompactBatch];
+#pragma unroll
+      for (int k = 0; k < kCompactBatch; ++k)
+        if (i0 + k < take) x[k] = cache[chunk_of(s_src[i0 + k])];
+#pragma unroll
+      for (int k = 0; k < kCompactBatch; ++k)
+        if (i0 + k < take) {
+          const int64_t src = s_src[i0 + k], dst = s_dst[i0 + k];
+          if constexpr (KV != PKV_KV_BF16) x[k] = requantise<KV>(x[k], params, page_of(src), page_of(dst));
+          cache[chunk_of(dst)] = x[k];
+        }
+    }
+  }
+}
+
+cudaError_t launch_compact_tokens(int kv_dtype, const CompactArgs& a, cudaStream_t stream) {
+  const int chunks = 2 * a.Hkv * a.D * (kv_dtype == PKV_KV_BF16 ? 2 : 1) / 16;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * static_cast<unsigned>(a.S));
+  cfg.blockDim = dim3(static_cast<unsigned>(std::min(kCompactThreads, (chunks + 31) / 32 * 32)));
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto kernel = kv_dtype == PKV_KV_INT8        ? compact_tokens_kernel<PKV_KV_INT8>
+                : kv_dtype == PKV_KV_FP8_E4M3 ? compact_tokens_kernel<PKV_KV_FP8_E4M3>
+                                              : compact_tokens_kernel<PKV_KV_BF16>;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace pkv

@@ -36,6 +36,9 @@ const void* decode_kernel_mt_bf16(int D, int bs, int gt);
 const void* decode_kernel_mt_1byte(int kv_dtype, int bs, int gt);
 const void* decode_kernel_tc(int bs, bool rot, int kv_dtype);
 const void* decode_kernel_tc2(int bs);
+const void* decode_kernel_tree_mma(int kv_dtype, int D, int bs, int gt);
+const void* decode_kernel_tree_tc(int bs, bool rot, int kv_dtype);
+const void* decode_kernel_tree_tc2(int bs);
 
 // ---------------------------------------------------------------------------
 // planner: one CTA validates context lengths, counts each sequence's
@@ -50,15 +53,84 @@ constexpr int kPlanThreads = 1024;
 // in-kernel merge is serial per (sequence, KV head) and lands in the tail).
 constexpr int kFusedMergeMaxParts = 4;
 
+// What the planner of a drafted-tree decode also does: sequences with an
+// invalid node count become inactive, and CTAs 1.. look for nodes whose V row
+// holds a NaN or an infinity.
+struct TreePlan {
+  const int32_t* node_counts;   // NULL: T each
+  const int32_t* block_tables;
+  const uint8_t* v;             // the cache slot's V pages
+  uint32_t* poison;             // [B][Hkv][words]
+  int T, words, Hkv, MB, NB, bs, row_bytes, e4m3;
+};
+
+// One warp per (sequence, KV head, word of 32 nodes): the word's bits of nodes
+// whose V row is not finite.  A row takes row_bytes / 16 lanes, 16 bytes each,
+// so the warp reads 2 to 4 rows at a time, and the 8 to 16 loads of a lane are
+// independent.  A NaN there would reach every query row of a tile through
+// 0 x NaN, also those that do not attend to the node, so the attention kernels
+// leave these V rows out and set the rows that attend to them to NaN.  The
+// rows come out of L2 again when the kernel reads the pages; the scan adds
+// T x Hkv rows a sequence to the planner's reads (4 MB for 64 sequences of 32
+// nodes and 8 KV heads of 256 bytes).
+__device__ __forceinline__ void tree_scan_values(const TreePlan& t, const int32_t* __restrict__ context_lens, int B, int max_ctx,
+                                                 int64_t warp0, int64_t nwarps) {
+  const int lane = threadIdx.x & 31;
+  const int lanes = t.row_bytes / 16;  // lanes of one row
+  const int per = 32 / lanes;          // rows at a time
+  const int sub = lane / lanes, chunk = lane % lanes;
+  const int64_t items = static_cast<int64_t>(B) * t.Hkv * t.words;
+  for (int64_t it = warp0; it < items; it += nwarps) {
+    const int w = static_cast<int>(it % t.words);
+    const int64_t bh = it / t.words;
+    const int h = static_cast<int>(bh % t.Hkv), b = static_cast<int>(bh / t.Hkv);
+    const int n = context_lens[b];
+    const int nodes = t.node_counts != nullptr ? t.node_counts[b] : t.T;
+    uint32_t word = 0u;
+    if (n >= 0 && n <= max_ctx && nodes >= 0 && nodes <= t.T) {
+#pragma unroll 4
+      for (int r = 0; r < 32; r += per) {
+        const int u = 32 * w + r + sub;
+        const int pos = n - nodes + u;
+        bool odd = false;
+        if (u < nodes && pos >= 0) {
+          const int blk = t.block_tables[static_cast<size_t>(b) * t.MB + pos / t.bs];
+          if (static_cast<unsigned>(blk) < static_cast<unsigned>(t.NB)) {
+            const size_t row = (static_cast<size_t>(blk) * t.Hkv + h) * t.bs + pos % t.bs;
+            const uint4 x = *reinterpret_cast<const uint4*>(t.v + row * t.row_bytes + 16 * chunk);
+            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (t.e4m3) {  // NaN: every bit but the sign set
+#pragma unroll
+                for (int k = 0; k < 4; ++k) odd |= ((v[i] >> (8 * k)) & 0x7fu) == 0x7fu;
+              } else {  // bf16: exponent all ones
+                odd |= (v[i] & 0x7f80u) == 0x7f80u || (v[i] & 0x7f800000u) == 0x7f800000u;
+              }
+            }
+          }
+        }
+        const uint32_t votes = __ballot_sync(kFull, odd);
+        for (int k = 0; k < per; ++k) {
+          const uint32_t group = lanes == 32 ? ~0u : (1u << lanes) - 1u;
+          if ((votes >> (k * lanes)) & group) word |= 1u << (r + k);
+        }
+      }
+    }
+    if (lane == 0) t.poison[it] = word;
+  }
+}
+
 // KV >= 0: CTAs 1.. of the same launch first run a KV append of that kind
 // (pkv_kv_dtype), so that a decode step's append and plan cost one launch.
-template <int KV>
+// TREE: they scan the V rows of the drafted nodes instead.
+template <int KV, bool TREE = false>
 __global__ void __launch_bounds__(kPlanThreads)
     plan_kernel(const int32_t* __restrict__ context_lens, int B, int num_arrive /* B * Hkv * NT */,
                 int max_ctx, int tokens_per_part, int half_from /* sequences from here: */,
                 int tokens_per_part_half /* partitions of this many tokens */, int32_t* work_counter, int32_t* unit_start,
                 int32_t* ctx_eff, int32_t* part_seq, int32_t* arrive, __nv_bfloat16* out,
-                int row_elems /* T * Hq * D */, unsigned* err, const AppendArgs app) {
+                int row_elems /* T * Hq * D */, unsigned* err, const AppendArgs app, const TreePlan tree) {
   __shared__ int warp_tot[kPlanThreads / 32];
   __shared__ int carry_s;
   pdl_trigger();
@@ -70,10 +142,17 @@ __global__ void __launch_bounds__(kPlanThreads)
       return;
     }
   }
+  if constexpr (TREE) {
+    if (blockIdx.x > 0) {  // block-uniform, as above
+      tree_scan_values(tree, context_lens, B, max_ctx, (blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5),
+                       static_cast<int64_t>(gridDim.x - 1) * (kPlanThreads / 32));
+      return;
+    }
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) carry_s = 0;
   __syncthreads();
-  bool bad_any = false;
+  bool bad_any = false, bad_nodes = false;
   for (int base = 0; base < B; base += kPlanThreads) {
     const int b = base + tid;
     int parts = 0;
@@ -82,6 +161,12 @@ __global__ void __launch_bounds__(kPlanThreads)
       if (c < 0 || c > max_ctx) {
         bad_any = true;
         c = 0;
+      }
+      if constexpr (TREE) {
+        if (tree.node_counts != nullptr && (tree.node_counts[b] < 0 || tree.node_counts[b] > tree.T)) {
+          bad_nodes = true;
+          c = 0;
+        }
       }
       ctx_eff[b] = c;
       const int tpp = b >= half_from ? tokens_per_part_half : tokens_per_part;
@@ -118,6 +203,9 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
   for (int i = tid; i < num_arrive; i += kPlanThreads) arrive[i] = 0;
   if (__syncthreads_or(bad_any) && tid == 0) atomicOr(err, PKV_DEVERR_CONTEXT_LEN);
+  if constexpr (TREE) {
+    if (__syncthreads_or(bad_nodes) && tid == 0) atomicOr(err, PKV_DEVERR_TREE);
+  }
   // the sequence of every global partition (one warp per sequence), so that
   // a decode unit finds its sequence with one load
   for (int b = warp; b < B; b += kPlanThreads / 32)
@@ -290,7 +378,7 @@ __global__ void __launch_bounds__(kMergeRowsPerCta * 32)
 // ---------------------------------------------------------------------------
 static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-WorkspaceLayout workspace_layout(int B, int T, int Hq, int Hkv, int NT, int D, int pmax) {
+WorkspaceLayout workspace_layout(int B, int T, int Hq, int Hkv, int NT, int D, int pmax, int tree_words) {
   WorkspaceLayout w{};
   size_t off = 0;
   w.counter = off;
@@ -308,6 +396,8 @@ WorkspaceLayout workspace_layout(int B, int T, int Hq, int Hkv, int NT, int D, i
   off = align_up(off + sizeof(float) * 2 * parts, 256);
   w.part_o = off;
   off = align_up(off + sizeof(float) * D * parts, 256);
+  w.poison = off;
+  off = align_up(off + sizeof(uint32_t) * static_cast<size_t>(B) * Hkv * tree_words, 256);
   w.total = off;
   return w;
 }
@@ -328,7 +418,12 @@ size_t decode_smem_bytes(int kv_fp8, int D, int bs, int warps, int stages, int t
 
 // gt: query rows per tile; mt: multi-token kernel (T > 1); tc2: the
 // tcgen05 kernel for pairs of row tiles.
-static const void* pick_kernel(int kv_dtype, int D, int bs, int math, int gt, bool mt, bool tc2 = false) {
+static const void* pick_kernel(int kv_dtype, int D, int bs, int math, int gt, bool mt, bool tc2, bool tree) {
+  if (tree) {
+    if (math == PKV_MATH_TC && tc2) return kv_dtype == PKV_KV_BF16 && D == 128 ? decode_kernel_tree_tc2(bs) : nullptr;
+    if (math == PKV_MATH_TC) return D == 128 ? decode_kernel_tree_tc(bs, gt <= kTcRotMaxRows, kv_dtype) : nullptr;
+    return math == PKV_MATH_MMA ? decode_kernel_tree_mma(kv_dtype, D, bs, gt) : nullptr;
+  }
   if (math == PKV_MATH_TC && tc2) return (kv_dtype == PKV_KV_BF16 && D == 128) ? decode_kernel_tc2(bs) : nullptr;
   if (math == PKV_MATH_TC) return D == 128 ? decode_kernel_tc(bs, gt <= kTcRotMaxRows, kv_dtype) : nullptr;
   if (mt) {
@@ -392,7 +487,7 @@ static cudaError_t ctas_per_sm(const void* fn, int threads, size_t smem, int* ou
 }
 
 int decode_ctas_per_sm(const DecodeLaunch& L, size_t smem) {
-  const void* fn = pick_kernel(L.kv_dtype, L.D, L.bs, L.math, L.G * L.Tt, L.T > 1, L.tc2 != 0);
+  const void* fn = pick_kernel(L.kv_dtype, L.D, L.bs, L.math, L.G * L.Tt, L.T > 1, L.tc2 != 0, L.tree != 0);
   int n = 0;
   if (fn == nullptr || ctas_per_sm(fn, L.warps * 32, smem, &n) != cudaSuccess) return 0;
   return n;
@@ -400,7 +495,7 @@ int decode_ctas_per_sm(const DecodeLaunch& L, size_t smem) {
 
 cudaError_t launch_decode(const DecodeLaunch& L, int* launched) {
   *launched = 0;
-  const void* fn = pick_kernel(L.kv_dtype, L.D, L.bs, L.math, L.G * L.Tt, L.T > 1, L.tc2 != 0);
+  const void* fn = pick_kernel(L.kv_dtype, L.D, L.bs, L.math, L.G * L.Tt, L.T > 1, L.tc2 != 0, L.tree != 0);
   if (fn == nullptr) return cudaErrorInvalidDeviceFunction;
   const size_t smem = decode_smem_bytes(L.kv_fp8, L.D, L.bs, L.warps, L.stages, L.tc, L.tc2);
   int per_sm = 0;
@@ -428,13 +523,33 @@ cudaError_t launch_decode(const DecodeLaunch& L, int* launched) {
     cfg.numAttrs = 1;
     const AppendArgs none{};
     const AppendArgs& app = L.append != nullptr ? *L.append : none;
-    auto plan = L.append == nullptr                ? plan_kernel<-1>
+    TreePlan tree{};
+    if (L.tree) {
+      tree.node_counts = L.node_counts;
+      tree.block_tables = L.block_tables;
+      tree.v = static_cast<const uint8_t*>(L.v_cache);
+      tree.poison = L.poison;
+      tree.T = L.T;
+      tree.words = L.tree_words;
+      tree.Hkv = L.Hkv;
+      tree.MB = L.MB;
+      tree.NB = L.NB;
+      tree.bs = L.bs;
+      tree.row_bytes = L.D * (L.kv_fp8 ? 1 : 2);
+      tree.e4m3 = L.kv_dtype == PKV_KV_FP8_E4M3;
+      if (L.kv_dtype != PKV_KV_INT8) {
+        const long long items = static_cast<long long>(L.B) * L.Hkv * L.tree_words;
+        cfg.gridDim = dim3(static_cast<unsigned>(1 + std::min<long long>((items + kPlanThreads / 32 - 1) / (kPlanThreads / 32), 1 << 16)));
+      }
+    }
+    auto plan = L.tree                             ? plan_kernel<-1, true>
+                : L.append == nullptr              ? plan_kernel<-1>
                 : L.append_kind == PKV_KV_INT8      ? plan_kernel<PKV_KV_INT8>
                 : L.append_kind == PKV_KV_FP8_E4M3  ? plan_kernel<PKV_KV_FP8_E4M3>
                                                     : plan_kernel<PKV_KV_BF16>;
     e = cudaLaunchKernelEx(&cfg, plan, L.context_lens, L.B, L.B * L.Hkv * L.NT, L.MB * L.bs,
                            L.ppu * L.bs, L.half_from, L.ppu_half * L.bs, L.work_counter, L.unit_start, L.ctx_eff, L.part_seq, L.arrive,
-                           static_cast<__nv_bfloat16*>(L.out), L.T * L.Hq * L.D, L.err, app);
+                           static_cast<__nv_bfloat16*>(L.out), L.T * L.Hq * L.D, L.err, app, tree);
     if (e != cudaSuccess) return e;
     *launched += 1;
   }
@@ -484,6 +599,13 @@ cudaError_t launch_decode(const DecodeLaunch& L, int* launched) {
   p.fused_merge = (!L.tc && L.pmax <= kFusedMergeMaxParts) ? 1 : 0;
   p.row_base = L.row_base;
   p.scale_log2 = L.scale_log2;
+  if (L.tree) {
+    p.tree.mask = L.tree_mask;
+    p.tree.node_counts = L.node_counts;
+    p.tree.poison = L.kv_dtype != PKV_KV_INT8 ? L.poison : nullptr;
+    p.tree.words = L.tree_words;
+    p.tree.stride = L.tree_stride;
+  }
   CUtensorMap kmap = L.kmap, vmap = L.vmap, pmap = L.pmap, omap = L.omap, qmap = L.qmap;
   void* args_mma[] = {&kmap, &vmap, &p};
   void* args_tc[] = {&kmap, &vmap, &pmap, &omap, &p};  // + the partial and output store maps

@@ -41,6 +41,7 @@
 #pragma once
 
 #include "pkv_device.cuh"
+#include "tree_mask.cuh"
 
 namespace pkv {
 
@@ -66,7 +67,14 @@ struct DecodeParams {
   int fused_merge;  // 1: the last warp of a (sequence, KV head) merges; 0: the merge kernel does
   int row_base;
   float scale_log2;
+  TreeArgs tree;  // drafted trees (TREE kernels)
 };
+
+// Nodes of sequence b (TREE kernels; the planner made sequences with an
+// invalid count inactive).
+__device__ __forceinline__ int tree_nodes(const DecodeParams& p, int b) {
+  return p.tree.node_counts != nullptr ? __ldg(p.tree.node_counts + b) : p.T;
+}
 
 // Query row `row` (0..15) of row tile `tile` of KV head `kvh`: query token
 // t = tile * Tt + row / G, query head h = kvh * G + row % G.  False for rows
@@ -250,10 +258,12 @@ __device__ __forceinline__ void mma_int8_unbias(MmaState<D, BS, FP8, HI>& st) {
 // softmax scale * log2(e) (* the page's K scale for one-byte pages);
 // `vscale` = the page's V scale (one-byte pages); `kc`, `vc` = the page's
 // INT8 biases 1152 + zero of K and V.
-template <int D, int BS, bool FP8, bool HI, bool I8>
+// TREE: rv[r] holds instead the bits of the tokens that row g + 8r attends to,
+// and `keep` those of the page's tokens whose V row takes part.
+template <int D, int BS, bool FP8, bool HI, bool I8, bool TREE = false>
 __device__ __forceinline__ void mma_page(MmaState<D, BS, FP8, HI>& st, uint8_t* stage, int valid,
                                          const int (&rv)[HI ? 2 : 1], bool partial, float sl,
-                                         float vscale, float kc, float vc, int lane) {
+                                         float vscale, float kc, float vc, int lane, uint32_t keep = 0u) {
   using Geo = PageGeom<D, BS, FP8>;
   constexpr int kR = HI ? 2 : 1;
   constexpr int kC = 2 * kR;
@@ -307,7 +317,8 @@ __device__ __forceinline__ void mma_page(MmaState<D, BS, FP8, HI>& st, uint8_t* 
 #pragma unroll
       for (int e = 0; e < kC; ++e) {
         const int tok = qk_token<FP8>(nt, 2 * tig + (e & 1));
-        const float v = (tok < rv[e >> 1]) ? fmaf(s[nt][e], sl, kb[e >> 1]) : -INFINITY;
+        const bool seen = TREE ? ((static_cast<uint32_t>(rv[e >> 1]) >> tok) & 1u) != 0u : tok < rv[e >> 1];
+        const float v = seen ? fmaf(s[nt][e], sl, kb[e >> 1]) : -INFINITY;
         s[nt][e] = v;
         mx[e >> 1] = fmaxf(mx[e >> 1], v);
       }
@@ -389,11 +400,11 @@ __device__ __forceinline__ void mma_page(MmaState<D, BS, FP8, HI>& st, uint8_t* 
   // Rows of V past the sequence end may hold anything (E4M3 and bf16: even
   // NaN); P is 0 there but 0 * NaN is NaN, so clear them before the product.
   // Every INT8 byte is a finite value.
-  if (!I8 && valid < BS) {
+  if (!I8 && (TREE ? keep != (BS == 32 ? ~0u : (1u << (BS & 31)) - 1u) : valid < BS)) {
     uint8_t* vp = stage + Geo::kTensorBytes;
     for (int idx = lane; idx < Geo::kTensorBytes / 16; idx += 32) {
       const int row = (idx % (Geo::kRegionBytes / 16)) / 8;
-      if (row >= valid) reinterpret_cast<uint4*>(vp)[idx] = make_uint4(0, 0, 0, 0);
+      if (TREE ? !((keep >> row) & 1u) : row >= valid) reinterpret_cast<uint4*>(vp)[idx] = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -446,9 +457,11 @@ __device__ __forceinline__ void mma_page(MmaState<D, BS, FP8, HI>& st, uint8_t* 
   }
 }
 
-template <int D, int BS, bool FP8, bool HI, bool MT>
+// row_state (TREE): see TreeRow.
+template <int D, int BS, bool FP8, bool HI, bool MT, bool TREE = false>
 __device__ __forceinline__ void mma_finish(MmaState<D, BS, FP8, HI>& st, const DecodeParams& p,
-                                           int b, int kvh, int tile, int pidx, int nparts, int lane) {
+                                           int b, int kvh, int tile, int pidx, int nparts, int lane,
+                                           const int (&row_state)[HI ? 2 : 1]) {
   constexpr int kR = HI ? 2 : 1;
   const int g = lane >> 2, tig = lane & 3;
 #pragma unroll
@@ -460,6 +473,12 @@ __device__ __forceinline__ void mma_finish(MmaState<D, BS, FP8, HI>& st, const D
   for (int r = 0; r < kR; ++r) {
     int t, h;
     if (!tile_row<MT>(p, kvh, tile, g + 8 * r, t, h)) continue;
+    if constexpr (TREE) {
+      if (row_state[r] != kTreeRowNormal) {
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) st.o[n][2 * r] = st.o[n][2 * r + 1] = tree_row_value(row_state[r]);
+      }
+    }
     const size_t qrow = static_cast<size_t>(b * p.T + t) * p.Hq + h;
     if (nparts == 1) {
       const float inv = st.l[r] > 0.f ? 1.f / st.l[r] : 0.f;
@@ -816,8 +835,9 @@ __device__ __forceinline__ bool unit_bad(const UnitPages& u, int j) {
 // the kernel
 // ---------------------------------------------------------------------------
 // MT: multi-token queries (T >= 1, row tiles, per-row causal limits);
-// false: single-token kernels, T = 1 only.
-template <int D, int BS, bool FP8, int MATH, int GT, bool I8 = false, bool MT = false>
+// false: single-token kernels, T = 1 only.  TREE (with MT): the query tokens
+// are the nodes of a drafted tree; per-row masks in place of causal limits.
+template <int D, int BS, bool FP8, int MATH, int GT, bool I8 = false, bool MT = false, bool TREE = false>
 __global__ void __launch_bounds__(256, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap, const DecodeParams p) {
@@ -907,14 +927,34 @@ __global__ void __launch_bounds__(256, 1)
       if constexpr (I8) mma_int8_prepare(st);
       // causal limits: query row g + 8r attends to positions < lim[r];
       // lim_min is the smallest over the tile (T = 1: both are ctx)
+      // (TREE: both are the tokens before the tree, for rows past the
+      // sequence's nodes too, whose output is zero whatever they attend to;
+      // mrow[r]: the row's mask words)
       int lim[kR];
+      int row_state[kR];
+      const uint32_t* mrow[kR];
+      const uint32_t* prow = nullptr;
+      int base = 0, lim_min = MT ? ctx - p.T + 1 + tile * p.Tt : ctx;
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
         int t, h;
-        tile_row<MT>(p, kvh, tile, (lane >> 2) + 8 * r, t, h);
-        lim[r] = MT ? ctx - p.T + 1 + min(t, p.T - 1) : ctx;
+        const bool in_tile = tile_row<MT>(p, kvh, tile, (lane >> 2) + 8 * r, t, h);
+        row_state[r] = kTreeRowNormal;
+        mrow[r] = nullptr;
+        if constexpr (TREE) {
+          const int nodes = tree_nodes(p, b);
+          base = ctx - nodes;
+          const bool live = in_tile && t < nodes;
+          lim[r] = lim_min = base;
+          if (live) mrow[r] = p.tree.mask + static_cast<size_t>(b) * p.tree.stride + static_cast<size_t>(t) * p.tree.words;
+          else row_state[r] = kTreeRowZero;
+        } else {
+          lim[r] = MT ? ctx - p.T + 1 + min(t, p.T - 1) : ctx;
+        }
       }
-      const int lim_min = MT ? ctx - p.T + 1 + tile * p.Tt : ctx;
+      if constexpr (TREE) {
+        if (p.tree.poison != nullptr) prow = p.tree.poison + static_cast<size_t>(b * p.Hkv + kvh) * p.tree.words;
+      }
       for (int j = 0; j < npages; ++j) {
         const uint32_t s = it % static_cast<uint32_t>(R);
         const bool landed = mbar_wait_bounded(&bars[s], (it / R) & 1u, kWaitLimitNs);
@@ -931,11 +971,34 @@ __global__ void __launch_bounds__(256, 1)
         }
         const int pos0 = t0 + j * BS;
         int rv[kR];
-#pragma unroll
-        for (int r = 0; r < kR; ++r) rv[r] = MT ? min(valid, lim[r] - pos0) : valid;
         const bool partial = MT ? (valid < BS || lim_min - pos0 < BS) : valid < BS;
-        mma_page<D, BS, FP8, kHi, I8>(st, ring + static_cast<size_t>(s) * Geo::kStageBytes, valid, rv,
-                                      partial, p.scale_log2 * ksc, vsc, kc, vc, lane);
+        uint32_t keep = 0u;
+        if constexpr (TREE) {
+          const uint32_t vmask = low_bits32(valid);
+          keep = vmask;
+          if (partial) {
+            const int u0 = pos0 - base;
+            const bool nodes_here = u0 + BS > 0;
+            const uint32_t bad_v = nodes_here && prow != nullptr ? tree_window32(prow, p.tree.words, u0) : 0u;
+            keep = vmask & ~bad_v;
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+              uint32_t see = low_bits32(lim[r] - pos0);
+              if (nodes_here && mrow[r] != nullptr) see |= tree_window32(mrow[r], p.tree.words, u0);
+              see &= vmask;
+              if (see & bad_v) row_state[r] = kTreeRowNan;
+              rv[r] = static_cast<int>(see & keep);
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < kR; ++r) rv[r] = static_cast<int>(vmask);
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < kR; ++r) rv[r] = MT ? min(valid, lim[r] - pos0) : valid;
+        }
+        mma_page<D, BS, FP8, kHi, I8, TREE>(st, ring + static_cast<size_t>(s) * Geo::kStageBytes, valid, rv,
+                                            partial, p.scale_log2 * ksc, vsc, kc, vc, lane, keep);
         fence_proxy_async_smem();  // this lane's reads of the stage precede the refill
         __syncwarp();
         if (j + R < npages) { issue(j + R, it + R); ++issued; }
@@ -944,7 +1007,7 @@ __global__ void __launch_bounds__(256, 1)
       }
       if (!timed_out) {
         if constexpr (I8) mma_int8_unbias(st);
-        mma_finish<D, BS, FP8, kHi, MT>(st, p, b, kvh, tile, pidx, nparts, lane);
+        mma_finish<D, BS, FP8, kHi, MT, TREE>(st, p, b, kvh, tile, pidx, nparts, lane, row_state);
         if (nparts > 1 && p.fused_merge) arrive_and_merge<D, MT>(p, b, kvh, tile, nparts, lane);
       }
     } else {

@@ -7,6 +7,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -105,6 +106,33 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool scales_aligned(int dtype, const void* a, const void* b) {
   const uintptr_t m = dtype == PKV_KV_INT8 ? 7u : 3u;
   return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & m) == 0;
+}
+
+bool aligned4(std::initializer_list<const void*> ps) {
+  uintptr_t all = 0;
+  for (const void* p : ps) all |= reinterpret_cast<uintptr_t>(p);
+  return (all & 3u) == 0;
+}
+
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+
+// Whether no array of `written` overlaps another one of them or one of `read`
+// (NULL and empty arrays overlap nothing).
+bool disjoint(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p != nullptr && b.p != nullptr && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (const Span* w = written.begin(); w != written.end(); ++w) {
+    for (const Span* v = w + 1; v != written.end(); ++v)
+      if (meet(*w, *v)) return false;
+    for (const Span& r : read)
+      if (meet(*w, r)) return false;
+  }
+  return true;
 }
 
 bool env_flag(const char* name) {
@@ -364,7 +392,7 @@ pkv_status pkv_kv_append(const pkv_cache_desc* cache, int32_t slot, const void* 
 // Resolve options into a full launch configuration (no device work).
 static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t T, int32_t Hq,
                                  int32_t MB, const pkv_decode_opts* opts, int num_sms,
-                                 pkv::DecodeLaunch* L) {
+                                 pkv::DecodeLaunch* L, bool tree = false) {
   pkv_status st = check_cache_desc(c);
   if (st != PKV_OK) return st;
   if (batch < 0) return fail(PKV_ERR_INVALID_ARG, "batch %d < 0", batch);
@@ -383,7 +411,7 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
   // tcgen05 tiles: multi-token calls with head_dim 128 (one-byte caches as
   // exact code values: E4M3 K pages as they are, the other pages widened to
   // f16 in shared memory)
-  const bool tc_ok = c->head_dim == 128 && T > 1 && G <= 128;
+  const bool tc_ok = c->head_dim == 128 && (T > 1 || tree) && G <= 128;
   // measured on GB300 (Llama-8B layer, G 4): mma.sync tiles are faster up to
   // 16 rows per KV head (172 us at 4 tokens, one tile), tcgen05 tiles from 32
   // rows on (kernel 173 vs 234 us at 8 tokens, 173 vs 451 at 16, 183 vs 865
@@ -398,7 +426,7 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
   if (math != PKV_MATH_MMA && math != PKV_MATH_FFMA && math != PKV_MATH_TC)
     return fail(PKV_ERR_INVALID_ARG, "math %d", math);
   const bool tc = math == PKV_MATH_TC;
-  if (math == PKV_MATH_FFMA && T > 1)
+  if (math == PKV_MATH_FFMA && (T > 1 || tree))
     return fail(PKV_ERR_UNSUPPORTED, "multi-token queries need the mma back-end");
   if (static_cast<long long>(batch) * T * Hq * c->head_dim >= (1LL << 31))
     return fail(PKV_ERR_UNSUPPORTED, "batch x query tokens x heads x head_dim too large");
@@ -524,6 +552,10 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
     }
   }
   *L = pkv::DecodeLaunch{};
+  L->tree = tree ? 1 : 0;
+  L->tree_words = tree ? (T + 31) / 32 : 0;
+  if (tree && static_cast<long long>(batch) * L->tree_words * std::max(T, c->num_kv_heads) >= (1LL << 31))
+    return fail(PKV_ERR_UNSUPPORTED, "batch x nodes x mask words too large");
   L->B = batch;
   L->Hq = Hq;
   L->Hkv = c->num_kv_heads;
@@ -551,19 +583,31 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
 }
 
 static pkv::WorkspaceLayout layout_of(const pkv::DecodeLaunch& L) {
-  return pkv::workspace_layout(L.B, L.T, L.Hq, L.Hkv, L.NT, L.D, L.pmax);
+  return pkv::workspace_layout(L.B, L.T, L.Hq, L.Hkv, L.NT, L.D, L.pmax, L.tree_words);
+}
+
+static size_t workspace_bytes_of(const pkv_cache_desc* cache, int32_t batch, int32_t num_query_tokens,
+                                 int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                 const pkv_decode_opts* opts, bool tree) {
+  pkv::DecodeLaunch L;
+  // The partition size (and so the workspace) must not depend on the device
+  // the call later runs on: size with the largest SM count this build targets.
+  if (resolve_decode(cache, batch, num_query_tokens, num_q_heads, max_blocks_per_seq, opts, 152, &L, tree) !=
+      PKV_OK)
+    return 0;
+  return layout_of(L).total;
 }
 
 size_t pkv_decode_multi_workspace_bytes(const pkv_cache_desc* cache, int32_t batch,
                                         int32_t num_query_tokens, int32_t num_q_heads,
                                         int32_t max_blocks_per_seq, const pkv_decode_opts* opts) {
-  pkv::DecodeLaunch L;
-  // The partition size (and so the workspace) must not depend on the device
-  // the call later runs on: size with the largest SM count this build targets.
-  if (resolve_decode(cache, batch, num_query_tokens, num_q_heads, max_blocks_per_seq, opts, 152, &L) !=
-      PKV_OK)
-    return 0;
-  return layout_of(L).total;
+  return workspace_bytes_of(cache, batch, num_query_tokens, num_q_heads, max_blocks_per_seq, opts, false);
+}
+
+size_t pkv_decode_tree_workspace_bytes(const pkv_cache_desc* cache, int32_t batch,
+                                       int32_t num_query_tokens, int32_t num_q_heads,
+                                       int32_t max_blocks_per_seq, const pkv_decode_opts* opts) {
+  return workspace_bytes_of(cache, batch, num_query_tokens, num_q_heads, max_blocks_per_seq, opts, true);
 }
 
 size_t pkv_decode_workspace_bytes(const pkv_cache_desc* cache, int32_t batch, int32_t num_q_heads,
@@ -571,14 +615,13 @@ size_t pkv_decode_workspace_bytes(const pkv_cache_desc* cache, int32_t batch, in
   return pkv_decode_multi_workspace_bytes(cache, batch, 1, num_q_heads, max_blocks_per_seq, opts);
 }
 
-pkv_status pkv_decode_multi_describe(const pkv_cache_desc* cache, int32_t batch,
-                                     int32_t num_query_tokens, int32_t num_q_heads,
-                                     int32_t max_blocks_per_seq, const pkv_decode_opts* opts,
-                                     pkv_decode_plan* plan) {
+static pkv_status describe(const pkv_cache_desc* cache, int32_t batch, int32_t num_query_tokens,
+                           int32_t num_q_heads, int32_t max_blocks_per_seq, const pkv_decode_opts* opts,
+                           pkv_decode_plan* plan, bool tree) {
   if (plan == nullptr) return fail(PKV_ERR_INVALID_ARG, "plan is NULL");
   pkv::DecodeLaunch L;
   pkv_status st = resolve_decode(cache, batch, num_query_tokens, num_q_heads, max_blocks_per_seq, opts,
-                                 152, &L);
+                                 152, &L, tree);
   if (st != PKV_OK) return st;
   plan->partition_blocks = L.ppu;
   plan->max_partitions = L.pmax;
@@ -592,6 +635,20 @@ pkv_status pkv_decode_multi_describe(const pkv_cache_desc* cache, int32_t batch,
   plan->query_tokens_per_tile = L.Tt;
   plan->row_tiles = L.NT;
   return PKV_OK;
+}
+
+pkv_status pkv_decode_multi_describe(const pkv_cache_desc* cache, int32_t batch,
+                                     int32_t num_query_tokens, int32_t num_q_heads,
+                                     int32_t max_blocks_per_seq, const pkv_decode_opts* opts,
+                                     pkv_decode_plan* plan) {
+  return describe(cache, batch, num_query_tokens, num_q_heads, max_blocks_per_seq, opts, plan, false);
+}
+
+pkv_status pkv_decode_tree_describe(const pkv_cache_desc* cache, int32_t batch,
+                                    int32_t num_query_tokens, int32_t num_q_heads,
+                                    int32_t max_blocks_per_seq, const pkv_decode_opts* opts,
+                                    pkv_decode_plan* plan) {
+  return describe(cache, batch, num_query_tokens, num_q_heads, max_blocks_per_seq, opts, plan, true);
 }
 
 pkv_status pkv_decode_describe(const pkv_cache_desc* cache, int32_t batch, int32_t num_q_heads,
@@ -610,6 +667,13 @@ struct AppendRequest {
   int32_t num_tokens;
 };
 
+// The trees of a drafted-tree call.
+struct TreeRequest {
+  const uint32_t* mask;
+  int32_t tree_batch;
+  const int32_t* node_counts;
+};
+
 static pkv_status decode_call(const pkv_cache_desc* cache, const void* q, int32_t batch,
                               int32_t num_query_tokens, int32_t num_q_heads, const void* k_cache,
                               const void* v_cache, const float* k_scale, const float* v_scale,
@@ -617,11 +681,14 @@ static pkv_status decode_call(const pkv_cache_desc* cache, const void* q, int32_
                               const int32_t* context_lens, const int32_t* kv_group_ptr,
                               int32_t num_layers, int32_t layer, float scale, void* out,
                               void* workspace, size_t workspace_bytes,
-                              const pkv_decode_opts* opts, void* stream, const AppendRequest* req) {
+                              const pkv_decode_opts* opts, void* stream, const AppendRequest* req,
+                              const TreeRequest* tree = nullptr) {
   pkv::DecodeLaunch L;
   pkv_status st = resolve_decode(cache, batch, num_query_tokens, num_q_heads, max_blocks_per_seq, opts,
-                                 152, &L);
+                                 152, &L, tree != nullptr);
   if (st != PKV_OK) return st;
+  if (tree != nullptr && tree->tree_batch != 1 && tree->tree_batch != batch)
+    return fail(PKV_ERR_INVALID_ARG, "tree_batch %d is neither 1 nor the batch %d", tree->tree_batch, batch);
   if (kv_group_ptr == nullptr || num_layers < 1 || layer < 0 || layer >= num_layers)
     return fail(PKV_ERR_INVALID_ARG, "layer %d / num_layers %d / kv_group_ptr", layer, num_layers);
   const int32_t slot = kv_group_ptr[layer];
@@ -643,6 +710,11 @@ static pkv_status decode_call(const pkv_cache_desc* cache, const void* q, int32_
     return fail(PKV_ERR_ALIGNMENT, "q, out, caches and workspace must be 16-byte aligned");
   if ((reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(context_lens) & 3u))
     return fail(PKV_ERR_ALIGNMENT, "block_tables and context_lens must be 4-byte aligned");
+  if (tree != nullptr) {
+    if (tree->mask == nullptr) return fail(PKV_ERR_INVALID_ARG, "tree_mask is NULL");
+    if ((reinterpret_cast<uintptr_t>(tree->mask) & 3u) || (reinterpret_cast<uintptr_t>(tree->node_counts) & 3u))
+      return fail(PKV_ERR_ALIGNMENT, "tree_mask and node_counts must be 4-byte aligned");
+  }
   const size_t qbytes = static_cast<size_t>(batch) * num_query_tokens * num_q_heads * cache->head_dim * 2;
   const uintptr_t qa = reinterpret_cast<uintptr_t>(q), oa = reinterpret_cast<uintptr_t>(out);
   if (qa < oa + qbytes && oa < qa + qbytes) return fail(PKV_ERR_INVALID_ARG, "out overlaps q");
@@ -690,6 +762,14 @@ static pkv_status decode_call(const pkv_cache_desc* cache, const void* q, int32_
   L.arrive = reinterpret_cast<int32_t*>(ws + wl.arrive);
   L.part_ml = reinterpret_cast<float*>(ws + wl.part_ml);
   L.part_o = reinterpret_cast<float*>(ws + wl.part_o);
+  if (tree != nullptr) {
+    L.tree_mask = tree->mask;
+    L.node_counts = tree->node_counts;
+    L.tree_stride = tree->tree_batch == 1 ? 0 : num_query_tokens * L.tree_words;
+    L.poison = reinterpret_cast<uint32_t*>(ws + wl.poison);
+    L.v_cache = static_cast<const uint8_t*>(v_cache) + static_cast<size_t>(slot) * cache->num_blocks * cache->num_kv_heads *
+                                                           cache->block_size * cache->head_dim * (fp8 ? 1 : 2);
+  }
   if (L.tc && !L.tc2 && L.pmax > 1 &&
       (st = encode_partial_map(&L.pmap, L.part_o, batch, L.T, L.Hq, L.pmax, L.D, L.G, L.Tt)) != PKV_OK)
     return st;
@@ -763,6 +843,130 @@ pkv_status pkv_paged_decode(const pkv_cache_desc* cache, const void* q, int32_t 
                                 block_tables, max_blocks_per_seq, context_lens, kv_group_ptr,
                                 num_layers, layer, scale, out, workspace, workspace_bytes, opts,
                                 stream);
+}
+
+pkv_status pkv_paged_decode_tree(const pkv_cache_desc* cache, const void* q, int32_t batch,
+                                 int32_t num_query_tokens, int32_t num_q_heads, const void* k_cache,
+                                 const void* v_cache, const float* k_scale, const float* v_scale,
+                                 const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                 const int32_t* context_lens, const uint32_t* tree_mask,
+                                 int32_t tree_batch, const int32_t* node_counts,
+                                 const int32_t* kv_group_ptr, int32_t num_layers, int32_t layer,
+                                 float scale, void* out, void* workspace, size_t workspace_bytes,
+                                 const pkv_decode_opts* opts, void* stream) {
+  const TreeRequest tree{tree_mask, tree_batch, node_counts};
+  return decode_call(cache, q, batch, num_query_tokens, num_q_heads, k_cache, v_cache, k_scale, v_scale,
+                     block_tables, max_blocks_per_seq, context_lens, kv_group_ptr, num_layers, layer, scale,
+                     out, workspace, workspace_bytes, opts, stream, nullptr, &tree);
+}
+
+pkv_status pkv_tree_masks(const int32_t* parents, const int32_t* context_lens, const int32_t* node_counts,
+                          int32_t batch, int32_t num_nodes, uint32_t* mask, int32_t* positions,
+                          void* stream) {
+  if (batch < 0) return fail(PKV_ERR_INVALID_ARG, "batch %d < 0", batch);
+  if (num_nodes < 1 || num_nodes > PKV_MAX_QUERY_TOKENS)
+    return fail(PKV_ERR_INVALID_ARG, "num_nodes %d outside 1..%d", num_nodes, PKV_MAX_QUERY_TOKENS);
+  if (batch == 0) return PKV_OK;
+  if (!parents || !mask) return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned4({parents, context_lens, node_counts, mask, positions}))
+    return fail(PKV_ERR_ALIGNMENT, "every array must be 4-byte aligned");
+  const size_t nodes = static_cast<size_t>(batch) * num_nodes * 4, words = nodes * ((num_nodes + 31) / 32);
+  const size_t lens = static_cast<size_t>(batch) * 4;
+  if (!disjoint({{mask, words}, {positions, nodes}}, {{parents, nodes}, {context_lens, lens}, {node_counts, lens}}))
+    return fail(PKV_ERR_INVALID_ARG, "mask and positions must not overlap other arrays");
+  DeviceInfo dev;
+  pkv_status st = device_info(&dev);
+  if (st != PKV_OK) return st;
+  const pkv::TreeMaskArgs a{parents, context_lens, node_counts, mask, positions, dev.err_word, batch, num_nodes};
+  cudaError_t e = pkv::launch_tree_masks(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "tree_masks launch");
+  return PKV_OK;
+}
+
+pkv_status pkv_extend_tables(int32_t batch, int32_t block_size, int32_t max_blocks_per_seq,
+                             int32_t num_blocks, const int32_t* seq_lens, const int32_t* new_lens,
+                             const int32_t* borrowed_counts, int32_t* block_tables,
+                             const int32_t* block_counts, int32_t* new_block_counts,
+                             int32_t* free_ring, int32_t* free_state, int32_t* new_free_state,
+                             int32_t* context_lens, int32_t* query_starts, int64_t* slot_mapping,
+                             int32_t* positions, int32_t max_tokens, void* stream) {
+  if (batch < 0 || batch > PKV_MAX_TABLE_REQUESTS)
+    return fail(PKV_ERR_INVALID_ARG, "batch %d outside 0..%d", batch, PKV_MAX_TABLE_REQUESTS);
+  if (block_size != 16 && block_size != 32)
+    return fail(PKV_ERR_UNSUPPORTED, "block_size %d (supported: 16, 32)", block_size);
+  if (max_blocks_per_seq < 1 || num_blocks < 1 || max_tokens < 0)
+    return fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq %d, num_blocks %d, max_tokens %d", max_blocks_per_seq,
+                num_blocks, max_tokens);
+  if (static_cast<long long>(batch) * max_blocks_per_seq >= (1LL << 31) || num_blocks >= (1 << 30) ||
+      static_cast<long long>(max_blocks_per_seq) * block_size >= (1LL << 31) || max_tokens >= (1 << 30))
+    return fail(PKV_ERR_UNSUPPORTED, "tables, pool or token rows too large");
+  if ((batch > 0 && (!seq_lens || !new_lens || !block_tables || !block_counts || !new_block_counts || !context_lens)) ||
+      !free_ring || !free_state || !new_free_state || !query_starts || (max_tokens > 0 && !slot_mapping))
+    return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned4({seq_lens, new_lens, borrowed_counts, block_tables, block_counts, new_block_counts, free_ring, free_state,
+                 new_free_state, context_lens, query_starts, positions}) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0)
+    return fail(PKV_ERR_ALIGNMENT, "arrays must be 4-byte aligned, slot_mapping 8-byte");
+  const size_t lens = static_cast<size_t>(batch) * 4, rows = static_cast<size_t>(max_tokens);
+  const size_t tables = lens * max_blocks_per_seq, ring = static_cast<size_t>(num_blocks) * 4;
+  // the counts and the ring's state may be updated in place
+  if (!disjoint({{block_tables, tables}, {free_ring, ring}, {free_state, 16}, {context_lens, lens}, {query_starts, lens + 4},
+                 {slot_mapping, rows * 8}, {positions, rows * 4}, {new_block_counts, lens},
+                 {new_free_state == free_state ? nullptr : new_free_state, 16}},
+                {{seq_lens, lens}, {new_lens, lens}, {borrowed_counts, lens},
+                 {new_block_counts == block_counts ? nullptr : block_counts, lens}}))
+    return fail(PKV_ERR_INVALID_ARG, "arrays that are written overlap other arrays");
+  DeviceInfo dev;
+  pkv_status st = device_info(&dev);
+  if (st != PKV_OK) return st;
+  const pkv::ExtendArgs a{seq_lens,  new_lens,       borrowed_counts, block_tables, block_counts,
+                          new_block_counts, free_ring, free_state,     new_free_state, context_lens,
+                          query_starts, slot_mapping, positions,      dev.err_word, batch,
+                          max_blocks_per_seq, num_blocks, block_size, max_tokens};
+  cudaError_t e = pkv::launch_extend_tables(a, dev.num_sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "extend_tables launch");
+  return PKV_OK;
+}
+
+pkv_status pkv_compact_tokens(const pkv_cache_desc* cache, const int32_t* accept_idx,
+                              const int32_t* accept_counts, int32_t max_accept, int32_t batch,
+                              const int32_t* context_lens, const int32_t* node_counts, int32_t num_nodes,
+                              const int32_t* block_tables, int32_t max_blocks_per_seq, void* k_cache,
+                              void* v_cache, const float* k_scale, const float* v_scale, int32_t* seq_lens,
+                              void* stream) {
+  pkv_status st = check_cache_desc(cache);
+  if (st != PKV_OK) return st;
+  if (batch < 0) return fail(PKV_ERR_INVALID_ARG, "batch %d < 0", batch);
+  if (num_nodes < 1 || num_nodes > PKV_MAX_QUERY_TOKENS || max_accept < 1 || max_accept > PKV_MAX_QUERY_TOKENS)
+    return fail(PKV_ERR_INVALID_ARG, "num_nodes %d, max_accept %d outside 1..%d", num_nodes, max_accept,
+                PKV_MAX_QUERY_TOKENS);
+  if (max_blocks_per_seq < 1) return fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq %d < 1", max_blocks_per_seq);
+  if (static_cast<long long>(max_blocks_per_seq) * cache->block_size >= (1LL << 31) ||
+      static_cast<long long>(batch) * cache->num_slots >= (1LL << 31))
+    return fail(PKV_ERR_UNSUPPORTED, "max_blocks_per_seq or batch x cache slots too large");
+  if (batch == 0) return PKV_OK;
+  const bool fp8 = cache->dtype != PKV_KV_BF16;  // one-byte elements (E4M3 or INT8)
+  if (!accept_idx || !accept_counts || !context_lens || !block_tables || !k_cache || !v_cache || !seq_lens)
+    return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (fp8 && (!k_scale || !v_scale)) return fail(PKV_ERR_INVALID_ARG, "E4M3 and INT8 caches need k_scale and v_scale");
+  if (fp8 && !scales_aligned(cache->dtype, k_scale, v_scale))
+    return fail(PKV_ERR_ALIGNMENT, "k_scale and v_scale must be 4-byte (E4M3) or 8-byte (INT8) aligned");
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return fail(PKV_ERR_ALIGNMENT, "caches must be 16-byte aligned");
+  if (!aligned4({accept_idx, accept_counts, context_lens, node_counts, block_tables, seq_lens}))
+    return fail(PKV_ERR_ALIGNMENT, "index and length arrays must be 4-byte aligned");
+  const size_t lens = static_cast<size_t>(batch) * 4;
+  if (!disjoint({{seq_lens, lens}}, {{accept_idx, lens * max_accept}, {accept_counts, lens}, {context_lens, lens},
+                                     {node_counts, lens}, {block_tables, lens * max_blocks_per_seq}}))
+    return fail(PKV_ERR_INVALID_ARG, "seq_lens must not overlap other arrays");
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != PKV_OK) return st;
+  const pkv::CompactArgs a{accept_idx, accept_counts, context_lens, node_counts, block_tables, seq_lens,
+                           static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), fp8 ? k_scale : nullptr,
+                           fp8 ? v_scale : nullptr, dev.err_word, batch, max_accept, num_nodes, max_blocks_per_seq,
+                           cache->num_slots, cache->num_blocks, cache->num_kv_heads, cache->block_size, cache->head_dim};
+  cudaError_t e = pkv::launch_compact_tokens(cache->dtype, a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "compact_tokens launch");
+  return PKV_OK;
 }
 
 pkv_status pkv_copy_blocks(const pkv_cache_desc* cache, const void* src_k, const void* src_v,

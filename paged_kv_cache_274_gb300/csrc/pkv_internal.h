@@ -68,15 +68,24 @@ struct DecodeLaunch {
   cudaStream_t stream;
   int num_sms;
   cudaEvent_t ev_start, ev_end;  // optional, recorded around the decode kernel
+  // drafted tree (pkv_paged_decode_tree): the query tokens are nodes, masked
+  // by tree_mask [B or 1][T][tree_words]; node_counts [B] or NULL (T each)
+  int tree;
+  const uint32_t* tree_mask;
+  const int32_t* node_counts;
+  int tree_words, tree_stride;  // words per mask row; between sequences (0: one tree for all)
+  uint32_t* poison;             // workspace: [B][Hkv][tree_words] nodes with a non-finite V row
+  const void* v_cache;          // the V pages, for the planner's scan
   const AppendArgs* append;  // optional: append run by the planner launch (the decode sees it)
   int append_kind;           // pkv_kv_dtype of that append
 };
 
 // Workspace layout for one decode call.
 struct WorkspaceLayout {
-  size_t counter, unit_start, ctx_eff, part_seq, arrive, part_ml, part_o, total;
+  size_t counter, unit_start, ctx_eff, part_seq, arrive, part_ml, part_o, poison, total;
 };
-WorkspaceLayout workspace_layout(int B, int T, int Hq, int Hkv, int NT, int D, int pmax);
+// tree_words: words of a tree-mask row (0: no drafted tree).
+WorkspaceLayout workspace_layout(int B, int T, int Hq, int Hkv, int NT, int D, int pmax, int tree_words);
 
 // Programmatic dependent launch on (default) or off (PKV_PDL=0).
 bool pdl_enabled();
@@ -113,6 +122,55 @@ cudaError_t launch_copy_blocks(const void* src_k, const void* src_v, const float
                                float* dst_ks, float* dst_vs, int dst_nb, const int32_t* pairs,
                                int count, int64_t block_bytes, int scales_per_block,
                                int num_sms, unsigned* err, cudaStream_t stream);
+
+// Node masks and positions of drafted trees.
+struct TreeMaskArgs {
+  const int32_t* parents;       // [B][T]
+  const int32_t* context_lens;  // [B], NULL: 0
+  const int32_t* node_counts;   // [B], NULL: T each
+  uint32_t* mask;               // [B][T][ceil(T / 32)]
+  int32_t* positions;           // [B][T], NULL: not wanted
+  unsigned* err;
+  int B, T;
+};
+cudaError_t launch_tree_masks(const TreeMaskArgs& a, cudaStream_t stream);
+
+// Block tables, slot mapping and positions of a step's new tokens.
+struct ExtendArgs {
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  const int32_t* borrowed;  // [B], NULL: none
+  int32_t* block_tables;
+  const int32_t* counts_in;
+  int32_t* counts_out;
+  int32_t* ring;
+  int32_t* state_in;  // head, free blocks, CTAs arrived (scratch)
+  int32_t* state_out;
+  int32_t* context_lens;
+  int32_t* query_starts;
+  int64_t* slots;
+  int32_t* positions;  // NULL: not wanted
+  unsigned* err;
+  int B, MB, NB, bs, N;
+};
+cudaError_t launch_extend_tables(const ExtendArgs& a, int num_sms, cudaStream_t stream);
+
+// Accepted draft tokens moved behind the tokens before the draft.
+struct CompactArgs {
+  const int32_t* idx;     // [B][A]
+  const int32_t* counts;  // [B]
+  const int32_t* context_lens;
+  const int32_t* node_counts;  // [B], NULL: T each
+  const int32_t* block_tables;
+  int32_t* seq_lens;
+  uint8_t* kc;
+  uint8_t* vc;
+  const float* ks;  // page parameters (one-byte caches)
+  const float* vs;
+  unsigned* err;
+  int B, A, T, MB, S, NB, Hkv, bs, D;
+};
+cudaError_t launch_compact_tokens(int kv_dtype, const CompactArgs& a, cudaStream_t stream);
 
 // Read-only probe: sums the 32-bit words of `bytes` bytes (a multiple of 16,
 // 16-byte aligned) into *sum; one launch of up to 8 CTAs per SM.
