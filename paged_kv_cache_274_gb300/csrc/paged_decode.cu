@@ -21,6 +21,7 @@
 #include "paged_decode_tc.cuh"
 #include "paged_decode_tc2.cuh"
 #include "pkv_internal.h"
+#include "tree_scan.cuh"
 
 namespace pkv {
 
@@ -37,8 +38,6 @@ const void* decode_kernel_mt_1byte(int kv_dtype, int bs, int gt);
 const void* decode_kernel_tc(int bs, bool rot, int kv_dtype);
 const void* decode_kernel_tc2(int bs);
 const void* decode_kernel_tree_mma(int kv_dtype, int D, int bs, int gt);
-const void* decode_kernel_tree_tc(int bs, bool rot, int kv_dtype);
-const void* decode_kernel_tree_tc2(int bs);
 
 // ---------------------------------------------------------------------------
 // planner: one CTA validates context lengths, counts each sequence's
@@ -53,84 +52,17 @@ constexpr int kPlanThreads = 1024;
 // in-kernel merge is serial per (sequence, KV head) and lands in the tail).
 constexpr int kFusedMergeMaxParts = 4;
 
-// What the planner of a drafted-tree decode also does: sequences with an
-// invalid node count become inactive, and CTAs 1.. look for nodes whose V row
-// holds a NaN or an infinity.
-struct TreePlan {
-  const int32_t* node_counts;   // NULL: T each
-  const int32_t* block_tables;
-  const uint8_t* v;             // the cache slot's V pages
-  uint32_t* poison;             // [B][Hkv][words]
-  int T, words, Hkv, MB, NB, bs, row_bytes, e4m3;
-};
-
-// One warp per (sequence, KV head, word of 32 nodes): the word's bits of nodes
-// whose V row is not finite.  A row takes row_bytes / 16 lanes, 16 bytes each,
-// so the warp reads 2 to 4 rows at a time, and the 8 to 16 loads of a lane are
-// independent.  A NaN there would reach every query row of a tile through
-// 0 x NaN, also those that do not attend to the node, so the attention kernels
-// leave these V rows out and set the rows that attend to them to NaN.  The
-// rows come out of L2 again when the kernel reads the pages; the scan adds
-// T x Hkv rows a sequence to the planner's reads (4 MB for 64 sequences of 32
-// nodes and 8 KV heads of 256 bytes).
-__device__ __forceinline__ void tree_scan_values(const TreePlan& t, const int32_t* __restrict__ context_lens, int B, int max_ctx,
-                                                 int64_t warp0, int64_t nwarps) {
-  const int lane = threadIdx.x & 31;
-  const int lanes = t.row_bytes / 16;  // lanes of one row
-  const int per = 32 / lanes;          // rows at a time
-  const int sub = lane / lanes, chunk = lane % lanes;
-  const int64_t items = static_cast<int64_t>(B) * t.Hkv * t.words;
-  for (int64_t it = warp0; it < items; it += nwarps) {
-    const int w = static_cast<int>(it % t.words);
-    const int64_t bh = it / t.words;
-    const int h = static_cast<int>(bh % t.Hkv), b = static_cast<int>(bh / t.Hkv);
-    const int n = context_lens[b];
-    const int nodes = t.node_counts != nullptr ? t.node_counts[b] : t.T;
-    uint32_t word = 0u;
-    if (n >= 0 && n <= max_ctx && nodes >= 0 && nodes <= t.T) {
-#pragma unroll 4
-      for (int r = 0; r < 32; r += per) {
-        const int u = 32 * w + r + sub;
-        const int pos = n - nodes + u;
-        bool odd = false;
-        if (u < nodes && pos >= 0) {
-          const int blk = t.block_tables[static_cast<size_t>(b) * t.MB + pos / t.bs];
-          if (static_cast<unsigned>(blk) < static_cast<unsigned>(t.NB)) {
-            const size_t row = (static_cast<size_t>(blk) * t.Hkv + h) * t.bs + pos % t.bs;
-            const uint4 x = *reinterpret_cast<const uint4*>(t.v + row * t.row_bytes + 16 * chunk);
-            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (t.e4m3) {  // NaN: every bit but the sign set
-#pragma unroll
-                for (int k = 0; k < 4; ++k) odd |= ((v[i] >> (8 * k)) & 0x7fu) == 0x7fu;
-              } else {  // bf16: exponent all ones
-                odd |= (v[i] & 0x7f80u) == 0x7f80u || (v[i] & 0x7f800000u) == 0x7f800000u;
-              }
-            }
-          }
-        }
-        const uint32_t votes = __ballot_sync(kFull, odd);
-        for (int k = 0; k < per; ++k) {
-          const uint32_t group = lanes == 32 ? ~0u : (1u << lanes) - 1u;
-          if ((votes >> (k * lanes)) & group) word |= 1u << (r + k);
-        }
-      }
-    }
-    if (lane == 0) t.poison[it] = word;
-  }
-}
-
 // KV >= 0: CTAs 1.. of the same launch first run a KV append of that kind
 // (pkv_kv_dtype), so that a decode step's append and plan cost one launch.
-// TREE: they scan the V rows of the drafted nodes instead.
+// TREE: sequences with an invalid node count become inactive, and the CTAs
+// scan the V rows of the drafted nodes (tree_scan.cuh).
 template <int KV, bool TREE = false>
 __global__ void __launch_bounds__(kPlanThreads)
     plan_kernel(const int32_t* __restrict__ context_lens, int B, int num_arrive /* B * Hkv * NT */,
                 int max_ctx, int tokens_per_part, int half_from /* sequences from here: */,
                 int tokens_per_part_half /* partitions of this many tokens */, int32_t* work_counter, int32_t* unit_start,
                 int32_t* ctx_eff, int32_t* part_seq, int32_t* arrive, __nv_bfloat16* out,
-                int row_elems /* T * Hq * D */, unsigned* err, const AppendArgs app, const TreePlan tree) {
+                int row_elems /* T * Hq * D */, unsigned* err, const AppendArgs app, const TreeScan tree) {
   __shared__ int warp_tot[kPlanThreads / 32];
   __shared__ int carry_s;
   pdl_trigger();
@@ -144,7 +76,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
   if constexpr (TREE) {
     if (blockIdx.x > 0) {  // block-uniform, as above
-      tree_scan_values(tree, context_lens, B, max_ctx, (blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5),
+      tree_scan_values(tree, (blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5),
                        static_cast<int64_t>(gridDim.x - 1) * (kPlanThreads / 32));
       return;
     }
@@ -419,11 +351,8 @@ size_t decode_smem_bytes(int kv_fp8, int D, int bs, int warps, int stages, int t
 // gt: query rows per tile; mt: multi-token kernel (T > 1); tc2: the
 // tcgen05 kernel for pairs of row tiles.
 static const void* pick_kernel(int kv_dtype, int D, int bs, int math, int gt, bool mt, bool tc2, bool tree) {
-  if (tree) {
-    if (math == PKV_MATH_TC && tc2) return kv_dtype == PKV_KV_BF16 && D == 128 ? decode_kernel_tree_tc2(bs) : nullptr;
-    if (math == PKV_MATH_TC) return D == 128 ? decode_kernel_tree_tc(bs, gt <= kTcRotMaxRows, kv_dtype) : nullptr;
-    return math == PKV_MATH_MMA ? decode_kernel_tree_mma(kv_dtype, D, bs, gt) : nullptr;
-  }
+  // (drafted trees on tcgen05 have a launch of their own, launch_tree_attend)
+  if (tree) return math == PKV_MATH_MMA ? decode_kernel_tree_mma(kv_dtype, D, bs, gt) : nullptr;
   if (math == PKV_MATH_TC && tc2) return (kv_dtype == PKV_KV_BF16 && D == 128) ? decode_kernel_tc2(bs) : nullptr;
   if (math == PKV_MATH_TC) return D == 128 ? decode_kernel_tc(bs, gt <= kTcRotMaxRows, kv_dtype) : nullptr;
   if (mt) {
@@ -523,24 +452,10 @@ cudaError_t launch_decode(const DecodeLaunch& L, int* launched) {
     cfg.numAttrs = 1;
     const AppendArgs none{};
     const AppendArgs& app = L.append != nullptr ? *L.append : none;
-    TreePlan tree{};
+    TreeScan tree{};
     if (L.tree) {
-      tree.node_counts = L.node_counts;
-      tree.block_tables = L.block_tables;
-      tree.v = static_cast<const uint8_t*>(L.v_cache);
-      tree.poison = L.poison;
-      tree.T = L.T;
-      tree.words = L.tree_words;
-      tree.Hkv = L.Hkv;
-      tree.MB = L.MB;
-      tree.NB = L.NB;
-      tree.bs = L.bs;
-      tree.row_bytes = L.D * (L.kv_fp8 ? 1 : 2);
-      tree.e4m3 = L.kv_dtype == PKV_KV_FP8_E4M3;
-      if (L.kv_dtype != PKV_KV_INT8) {
-        const long long items = static_cast<long long>(L.B) * L.Hkv * L.tree_words;
-        cfg.gridDim = dim3(static_cast<unsigned>(1 + std::min<long long>((items + kPlanThreads / 32 - 1) / (kPlanThreads / 32), 1 << 16)));
-      }
+      tree = tree_scan_of(L, L.poison);
+      cfg.gridDim = dim3(1 + tree_scan_ctas(L, kPlanThreads / 32));
     }
     auto plan = L.tree                             ? plan_kernel<-1, true>
                 : L.append == nullptr              ? plan_kernel<-1>

@@ -154,16 +154,6 @@ __device__ __forceinline__ float tree_ext64(const uint32_t (&v)[kTcTokens]) {
   return kMax ? fmaxf(w, t[7]) : fminf(w, t[7]);
 }
 
-// A row's output where it is not O / l (TreeRow), and the warp converged again
-// for the collective TMEM accesses that follow: without it, one compilation ran
-// the next tcgen05.ld with the lanes of such rows split off.
-__device__ __forceinline__ void tree_fix_row(int row_state, uint32_t (&ov)[32]) {
-  const uint32_t fixed = __float_as_uint(tree_row_value(row_state));
-#pragma unroll
-  for (int e = 0; e < 32; ++e) ov[e] = row_state != kTreeRowNormal ? fixed : ov[e];
-  __syncwarp();
-}
-
 // A unit as the descriptor slot holds it.
 struct TcUnit {
   int u, b, pidx, nparts, ctx, kvh, tile, t0, t1, npages, nsteps;
@@ -223,9 +213,7 @@ __device__ __forceinline__ void widen_stage(uint8_t* stage, uint32_t region, int
   }
 }
 
-// TREE: the query tokens are the nodes of a drafted tree; per-row masks in
-// place of causal limits (tree_mask.cuh).
-template <int BS, bool kRot, int KV = PKV_KV_BF16, bool TREE = false>
+template <int BS, bool kRot, int KV = PKV_KV_BF16>
 // Two CTAs per SM: a sub-partition's 16384 registers hold four of the 14
 // (16 with a converter warp) warps at 128 registers a thread.
 __global__ void __launch_bounds__(tc_threads(KV), 2)
@@ -819,7 +807,6 @@ __global__ void __launch_bounds__(tc_threads(KV), 2)
       const int k = i & 1;
       int nsteps, t0, t1, lim;  // steps, token range, keys of this row: positions < lim
       bool row_ok;
-      int tree_base = 0, mrow = 0, prow = 0, row_state = kTreeRowNormal;  // TREE
       {
         const TcUnit U = read_unit(k);
         int t = 0, h = 0;
@@ -827,21 +814,7 @@ __global__ void __launch_bounds__(tc_threads(KV), 2)
         nsteps = U.nsteps;
         t0 = U.t0;
         t1 = U.t1;
-        if constexpr (TREE) {
-          // lim: the tokens before the tree, for rows past the sequence's
-          // nodes too (their output is zero whatever they attend to, and the
-          // steps before the tree stay free of masks); mrow / prow: the row's
-          // mask words and the KV head's words of non-finite V rows
-          const int nodes = tree_nodes(p, U.b);
-          tree_base = U.ctx - nodes;
-          row_ok = row_ok && t < nodes;
-          lim = tree_base;
-          mrow = U.b * p.tree.stride + t * p.tree.words;
-          prow = (U.b * p.Hkv + U.kvh) * p.tree.words;
-          row_state = row_ok ? kTreeRowNormal : kTreeRowZero;
-        } else {
-          lim = U.ctx - p.T + 1 + t;
-        }
+        lim = U.ctx - p.T + 1 + t;
       }
       const volatile uint8_t* bad = slot_bad(k);
       bool has_next = false;
@@ -865,18 +838,6 @@ __global__ void __launch_bounds__(tc_threads(KV), 2)
         for (int q = 0; q < PPI; ++q)
           if (bad[j * PPI + q]) vmask &= ~(((1ull << BS) - 1ull) << (q * BS));
         const int nrow = lim - pos0;
-        if constexpr (TREE) {
-          rmask = low_bits64(nrow);
-          if (pos0 + kTcTokens > tree_base) {  // the step holds nodes
-            const int u0 = pos0 - tree_base;
-            const uint64_t bad_v = p.tree.poison != nullptr ? tree_window64(p.tree.poison + prow, p.tree.words, u0) & vmask : 0ull;
-            if (row_ok) rmask |= tree_window64(p.tree.mask + mrow, p.tree.words, u0);
-            if (rmask & bad_v) row_state = kTreeRowNan;
-            vmask &= ~bad_v;
-          }
-          rmask &= vmask;
-          return;
-        }
         rmask = row_ok ? (vmask & (nrow >= kTcTokens ? ~0ull : (nrow <= 0 ? 0ull : ((1ull << nrow) - 1ull)))) : 0ull;
       };
       // the step's masked extremum of the raw scores -> running maximum; a
@@ -1149,7 +1110,6 @@ __global__ void __launch_bounds__(tc_threads(KV), 2)
             uint32_t ov[32];
             tc_ld32(t_lane + kTcOCol + 64 * k2 + 32 * hh, ov);
             tc_wait_ld();
-            if constexpr (TREE) tree_fix_row(row_state, ov);
 #pragma unroll
             for (int c4 = 0; c4 < 4; ++c4) {
               const float* f = reinterpret_cast<const float*>(ov + 8 * c4);
@@ -1195,7 +1155,6 @@ __global__ void __launch_bounds__(tc_threads(KV), 2)
 #pragma unroll
             for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * vmx);
           }
-          if constexpr (TREE) tree_fix_row(row_state, ov);
           if (k >= 2 && !warp_wait(stg_free, (nfree + k - 2) & 1u, false)) {
             timed_out = true;
             break;

@@ -144,9 +144,7 @@ __device__ __forceinline__ void tc_wait_ld_regs16(uint32_t (&v)[16]) {
       : "memory");
 }
 
-// TREE: the query tokens are the nodes of a drafted tree; per-row masks in
-// place of causal limits (tree_mask.cuh).
-template <int BS, bool TREE = false>
+template <int BS>
 __global__ void __launch_bounds__(kT2Threads, 1)
     paged_decode_tc2_kernel(const __grid_constant__ CUtensorMap kmap,
                             const __grid_constant__ CUtensorMap vmap,
@@ -500,28 +498,11 @@ __global__ void __launch_bounds__(kT2Threads, 1)
       // only what the steps need stays in registers; the output re-reads the
       // unit from its slot (the slot is released after the output)
       int lim, nsteps, t0, t1;  // lim: keys of this row are positions < lim
-      int tree_base = 0, mrow = -1, prow = 0, row_state = kTreeRowNormal;  // TREE
       {
         const TcUnit U = read_unit(k);
         if (U.u >= total_units) break;
         int t = 0, h = 0;
-        const bool in_tile = tile_row<true>(p, U.kvh, U.tile + i, r, t, h);
-        if constexpr (TREE) {
-          // lim: the tokens before the tree, for rows past the sequence's
-          // nodes too (their output is zero whatever they attend to, and the
-          // steps before the tree stay free of masks); mrow / prow: the row's
-          // mask words (-1: a row without) and the KV head's words of
-          // non-finite V rows
-          const int nodes = tree_nodes(p, U.b);
-          tree_base = U.ctx - nodes;
-          const bool live = in_tile && t < nodes;
-          lim = tree_base;
-          mrow = live ? U.b * p.tree.stride + t * p.tree.words : -1;
-          prow = (U.b * p.Hkv + U.kvh) * p.tree.words;
-          row_state = live ? kTreeRowNormal : kTreeRowZero;
-        } else {
-          lim = in_tile ? U.ctx - p.T + 1 + t : INT_MIN / 2;
-        }
+        lim = tile_row<true>(p, U.kvh, U.tile + i, r, t, h) ? U.ctx - p.T + 1 + t : INT_MIN / 2;
         nsteps = U.nsteps;
         t0 = U.t0;
         t1 = U.t1;
@@ -544,13 +525,6 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         tc_fence_after_sync();
         float factor = 1.f;
         bool grow = false;
-        uint64_t bad0 = 0ull, bad1 = 0ull;  // TREE: tokens of the step with a non-finite V row
-        if constexpr (TREE) {
-          if (p.tree.poison != nullptr && pos0 + kT2Tokens > tree_base) {
-            bad0 = tree_window64(p.tree.poison + prow, p.tree.words, pos0 - tree_base);
-            bad1 = tree_window64(p.tree.poison + prow, p.tree.words, pos0 - tree_base + 64);
-          }
-        }
         if (__all_sync(kFull, full)) {
           // every token of the step is every row's (the common case): the
           // row's 128 scores in one round trip, kept in registers
@@ -615,22 +589,8 @@ __global__ void __launch_bounds__(kT2Threads, 1)
               if (q * BS < 64) rm0 &= ~pm; else rm1 &= ~pm;
             }
           const int nr = lim - pos0;
-          if constexpr (TREE) {
-            uint64_t see0 = low_bits64(nr), see1 = low_bits64(nr - 64);
-            if (mrow >= 0 && pos0 + kT2Tokens > tree_base) {
-              see0 |= tree_window64(p.tree.mask + mrow, p.tree.words, pos0 - tree_base);
-              see1 |= tree_window64(p.tree.mask + mrow, p.tree.words, pos0 - tree_base + 64);
-            }
-            rm0 &= see0;
-            rm1 &= see1;
-            if ((rm0 & bad0) | (rm1 & bad1)) row_state = kTreeRowNan;
-            rm0 &= ~bad0;
-            rm1 &= ~bad1;
-            __syncwarp();  // the TMEM loads below are warp-collective
-          } else {
-            rm0 &= nr >= 64 ? ~0ull : (nr <= 0 ? 0ull : ((1ull << nr) - 1ull));
-            rm1 &= nr >= 128 ? ~0ull : (nr <= 64 ? 0ull : ((1ull << (nr - 64)) - 1ull));
-          }
+          rm0 &= nr >= 64 ? ~0ull : (nr <= 0 ? 0ull : ((1ull << nr) - 1ull));
+          rm1 &= nr >= 128 ? ~0ull : (nr <= 64 ? 0ull : ((1ull << (nr - 64)) - 1ull));
           const float ext_init = c >= 0.f ? -INFINITY : INFINITY;
           float ext = ext_init;
 #pragma unroll 1
@@ -700,11 +660,10 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         // anything and P is 0 there: once V(g) has landed, thread r of each
         // tile clears token row r (each tile's P . V waits only for its own
         // softmax warps; both tiles write the same zeros)
-        const bool stale = nvs < kT2Tokens || badw != 0 || (TREE && (bad0 | bad1) != 0ull);
+        const bool stale = nvs < kT2Tokens || badw != 0;
         if (stale) {
           if (!mbar_wait_bounded(&v_full[g % kT2Stages], (g / kT2Stages) & 1u, kWaitLimitNs)) timed_out = true;
-          if (!timed_out && (r >= nvs || ((badw >> (8 * (r / BS))) & 0xffu) ||
-                             (TREE && (((r < 64 ? bad0 : bad1) >> (r & 63)) & 1ull)))) {
+          if (!timed_out && (r >= nvs || ((badw >> (8 * (r / BS))) & 0xffu))) {
             uint8_t* vb = sm + T2Layout::kV + (g % kT2Stages) * T2Layout::kTile + r * 128;
 #pragma unroll
             for (int cc = 0; cc < 8; ++cc) {
@@ -742,7 +701,6 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         uint32_t ov[32];
         tc_ld32(t_o + cc, ov);
         tc_wait_ld_regs(ov);
-        if constexpr (TREE) tree_fix_row(row_state, ov);
         if (row_ok) {
           if (direct) {
             uint4* dst = reinterpret_cast<uint4*>(p.out + qrow * D + cc);

@@ -411,7 +411,8 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
   // tcgen05 tiles: multi-token calls with head_dim 128 (one-byte caches as
   // exact code values: E4M3 K pages as they are, the other pages widened to
   // f16 in shared memory)
-  const bool tc_ok = c->head_dim == 128 && (T > 1 || tree) && G <= 128;
+  // (drafted trees: head_dim 64 and single nodes too)
+  const bool tc_ok = tree ? G <= 128 : c->head_dim == 128 && T > 1 && G <= 128;
   // measured on GB300 (Llama-8B layer, G 4): mma.sync tiles are faster up to
   // 16 rows per KV head (172 us at 4 tokens, one tile), tcgen05 tiles from 32
   // rows on (kernel 173 vs 234 us at 8 tokens, 173 vs 451 at 16, 183 vs 865
@@ -445,7 +446,10 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
   // a pair of tiles per CTA with 8 softmax warps, an MMA warp and two copy
   // warps, 2-stage K and V rings of 128 tokens -- PKV_TC_PAIR=0 keeps the
   // one-tile kernel there)
-  const bool tc2 = tc && NT >= 2 && c->dtype == PKV_KV_BF16 && env_int("PKV_TC_PAIR", 1) != 0;
+  const bool tc2 = tc && !tree && NT >= 2 && c->dtype == PKV_KV_BF16 && env_int("PKV_TC_PAIR", 1) != 0;
+  // drafted trees on tcgen05 (tree_attend.cuh): one CTA per SM, one or a pair
+  // of row tiles each, equal shares of 128-token steps instead of partitions
+  const bool tree_tc = tree && tc;
   int warps = tc2 ? pkv::kTcPairWarps
               : tc ? (c->dtype == PKV_KV_BF16 ? 7 : 8)  // + the converter warp of one-byte caches
                    : (o.warps_per_cta != 0 ? o.warps_per_cta : env_int("PKV_DECODE_WARPS", 4));
@@ -453,7 +457,12 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
   if (stages == 0) stages = stage_bytes >= (8u << 10) ? 2 : 3;
   if (!tc && (warps < 1 || warps > 8)) return fail(PKV_ERR_INVALID_ARG, "warps_per_cta %d outside 1..8", warps);
   if (stages < 2 || stages > 8) return fail(PKV_ERR_INVALID_ARG, "stages %d outside 2..8", stages);
-  const size_t smem = pkv::decode_smem_bytes(fp8, c->head_dim, c->block_size, warps, stages, tc, tc2);
+  if (tree_tc) {
+    warps = c->dtype == PKV_KV_BF16 ? 12 : 16;
+    stages = 2;
+  }
+  const size_t smem = tree_tc ? pkv::tree_attend_smem_bytes(c->dtype, c->head_dim, NT > 1)
+                              : pkv::decode_smem_bytes(fp8, c->head_dim, c->block_size, warps, stages, tc, tc2);
   if (smem > 227u * 1024u)
     return fail(PKV_ERR_INVALID_ARG, "warps x stages need %zu bytes of shared memory", smem);
   int ppu = o.partition_blocks != 0 ? o.partition_blocks : env_int("PKV_DECODE_PARTITION_BLOCKS", 0);
@@ -462,7 +471,10 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
   const int ppu_max = tc ? pkv::kTcUnitMaxPages : 64;
   if (ppu < 0 || ppu > ppu_max) return fail(PKV_ERR_INVALID_ARG, "partition_blocks %d outside 1..%d", ppu, ppu_max);
   const bool auto_ppu = ppu == 0;
-  if (ppu == 0) {
+  const int tree_min_blocks = ppu;
+  if (tree_tc) {
+    ppu = MB;  // no partitions of a fixed length
+  } else if (ppu == 0) {
     // The decode is a persistent grid of W streaming warps pulling units of
     // work; its time follows how full the last round of units is.  Estimate
     // W from shared memory and about 200 registers a thread, count units for
@@ -532,7 +544,7 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
     }
   }
   ppu = std::min(ppu, MB);
-  if ((MB + ppu - 1) / ppu > 65536)
+  if (!tree_tc && (MB + ppu - 1) / ppu > 65536)
     return fail(PKV_ERR_UNSUPPORTED, "more than 65536 partitions per sequence; raise partition_blocks");
   // The tile-pair kernel runs one unit per SM at a time, units of equal
   // length: when the last round of units would be at most half full, the
@@ -554,6 +566,13 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
   *L = pkv::DecodeLaunch{};
   L->tree = tree ? 1 : 0;
   L->tree_words = tree ? (T + 31) / 32 : 0;
+  if (tree_tc) {
+    L->tree_tc = 1;
+    // pairs of row tiles side by side: the CTAs of one share read the same
+    // pages, at the same time
+    L->tree_shares = std::max(1, num_sms / (NT > 1 ? (NT + 1) / 2 : 1));
+    L->tree_min_steps = std::max(1, tree_min_blocks * c->block_size / 128);
+  }
   if (tree && static_cast<long long>(batch) * L->tree_words * std::max(T, c->num_kv_heads) >= (1LL << 31))
     return fail(PKV_ERR_UNSUPPORTED, "batch x nodes x mask words too large");
   L->B = batch;
@@ -582,6 +601,11 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
   return PKV_OK;
 }
 
+static size_t workspace_total(const pkv::DecodeLaunch& L) {
+  if (L.tree_tc) return pkv::tree_workspace(L.B, L.Hkv, L.D, L.NT, L.tree_words, L.tree_shares).total;
+  return pkv::workspace_layout(L.B, L.T, L.Hq, L.Hkv, L.NT, L.D, L.pmax, L.tree_words).total;
+}
+
 static pkv::WorkspaceLayout layout_of(const pkv::DecodeLaunch& L) {
   return pkv::workspace_layout(L.B, L.T, L.Hq, L.Hkv, L.NT, L.D, L.pmax, L.tree_words);
 }
@@ -595,7 +619,7 @@ static size_t workspace_bytes_of(const pkv_cache_desc* cache, int32_t batch, int
   if (resolve_decode(cache, batch, num_query_tokens, num_q_heads, max_blocks_per_seq, opts, 152, &L, tree) !=
       PKV_OK)
     return 0;
-  return layout_of(L).total;
+  return workspace_total(L);
 }
 
 size_t pkv_decode_multi_workspace_bytes(const pkv_cache_desc* cache, int32_t batch,
@@ -630,8 +654,10 @@ static pkv_status describe(const pkv_cache_desc* cache, int32_t batch, int32_t n
   plan->stages = L.stages;
   // the merge kernel runs above 4 partitions (tcgen05 kernel: above 1)
   plan->kernels_per_call = L.pmax > (L.tc ? 1 : 4) ? 3 : 2;
-  plan->workspace_bytes = layout_of(L).total;
-  plan->smem_bytes_per_cta = pkv::decode_smem_bytes(L.kv_fp8, L.D, L.bs, L.warps, L.stages, L.tc, L.tc2);
+  if (L.tree_tc) plan->kernels_per_call = L.tree_shares > 1 ? 3 : 2;
+  plan->workspace_bytes = workspace_total(L);
+  plan->smem_bytes_per_cta = L.tree_tc ? pkv::tree_attend_smem_bytes(L.kv_dtype, L.D, L.NT > 1)
+                                       : pkv::decode_smem_bytes(L.kv_fp8, L.D, L.bs, L.warps, L.stages, L.tc, L.tc2);
   plan->query_tokens_per_tile = L.Tt;
   plan->row_tiles = L.NT;
   return PKV_OK;
@@ -718,9 +744,10 @@ static pkv_status decode_call(const pkv_cache_desc* cache, const void* q, int32_
   const size_t qbytes = static_cast<size_t>(batch) * num_query_tokens * num_q_heads * cache->head_dim * 2;
   const uintptr_t qa = reinterpret_cast<uintptr_t>(q), oa = reinterpret_cast<uintptr_t>(out);
   if (qa < oa + qbytes && oa < qa + qbytes) return fail(PKV_ERR_INVALID_ARG, "out overlaps q");
+  const size_t need = workspace_total(L);
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(PKV_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace_bytes);
   const pkv::WorkspaceLayout wl = layout_of(L);
-  if (workspace == nullptr || workspace_bytes < wl.total)
-    return fail(PKV_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", wl.total, workspace_bytes);
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   DeviceInfo dev_info;
@@ -770,10 +797,12 @@ static pkv_status decode_call(const pkv_cache_desc* cache, const void* q, int32_
     L.v_cache = static_cast<const uint8_t*>(v_cache) + static_cast<size_t>(slot) * cache->num_blocks * cache->num_kv_heads *
                                                            cache->block_size * cache->head_dim * (fp8 ? 1 : 2);
   }
-  if (L.tc && !L.tc2 && L.pmax > 1 &&
+  if (L.tree_tc) {
+    if (cache->dtype == PKV_KV_BF16 && (st = encode_query_map(&L.qmap, q, batch, L.T, L.Hq, L.D, L.G, L.Tt)) != PKV_OK) return st;
+  } else if (L.tc && !L.tc2 && L.pmax > 1 &&
       (st = encode_partial_map(&L.pmap, L.part_o, batch, L.T, L.Hq, L.pmax, L.D, L.G, L.Tt)) != PKV_OK)
     return st;
-  if (L.tc && !L.tc2 && (st = encode_output_map(&L.omap, out, batch, L.T, L.Hq, L.D, L.G, L.Tt)) != PKV_OK)
+  if (L.tc && !L.tc2 && !L.tree_tc && (st = encode_output_map(&L.omap, out, batch, L.T, L.Hq, L.D, L.G, L.Tt)) != PKV_OK)
     return st;
   if (L.tc2 && (st = encode_query_map(&L.qmap, q, batch, L.T, L.Hq, L.D, L.G, L.Tt)) != PKV_OK) return st;
   L.err = dev->err_word;
@@ -795,7 +824,7 @@ static pkv_status decode_call(const pkv_cache_desc* cache, const void* q, int32_
     L.append_kind = cache->dtype;
   }
   int launched = 0;
-  cudaError_t e = pkv::launch_decode(L, &launched);
+  cudaError_t e = L.tree_tc ? pkv::launch_tree_attend(L, ws, &launched) : pkv::launch_decode(L, &launched);
   if (e != cudaSuccess) return cuda_fail(e, "paged_decode launch");
   return PKV_OK;
 }

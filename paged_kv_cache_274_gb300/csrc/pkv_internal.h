@@ -76,6 +76,9 @@ struct DecodeLaunch {
   int tree_words, tree_stride;  // words per mask row; between sequences (0: one tree for all)
   uint32_t* poison;             // workspace: [B][Hkv][tree_words] nodes with a non-finite V row
   const void* v_cache;          // the V pages, for the planner's scan
+  int tree_tc;                  // 1: the tcgen05 drafted-tree kernels (launch_tree_attend)
+  int tree_shares;              // most work shares (CTAs per pair of row tiles)
+  int tree_min_steps;           // fewest 128-token steps of a share
   const AppendArgs* append;  // optional: append run by the planner launch (the decode sees it)
   int append_kind;           // pkv_kv_dtype of that append
 };
@@ -122,6 +125,15 @@ cudaError_t launch_copy_blocks(const void* src_k, const void* src_v, const float
                                float* dst_ks, float* dst_vs, int dst_nb, const int32_t* pairs,
                                int count, int64_t block_bytes, int scales_per_block,
                                int num_sms, unsigned* err, cudaStream_t stream);
+
+// The tcgen05 drafted-tree attention: workspace, shared memory per CTA, launch
+// (planner, attention, merge).
+struct TreeWorkspace {
+  size_t shares, ctx_eff, start, bounds, poison, part_ml, part_o, total;
+};
+TreeWorkspace tree_workspace(int B, int Hkv, int D, int NT, int tree_words, int max_shares);
+size_t tree_attend_smem_bytes(int kv_dtype, int D, int pair);
+cudaError_t launch_tree_attend(const DecodeLaunch& L, uint8_t* workspace, int* launched_kernels);
 
 // Node masks and positions of drafted trees.
 struct TreeMaskArgs {

@@ -1,0 +1,386 @@
+// Planner, merge and launch of the tcgen05 drafted-tree attention
+// (tree_attend.cuh), and its kernel instances.
+#include <algorithm>
+#include <mutex>
+#include <vector>
+
+#include "tree_attend.cuh"
+#include "tree_scan.cuh"
+
+namespace pkv {
+
+// ---------------------------------------------------------------------------
+// planner
+// ---------------------------------------------------------------------------
+constexpr int kTreePlanThreads = 1024;
+constexpr int kTreePlanSmem = 2048;  // sequences whose prefix sums are searched in shared memory
+
+struct TreePlanArgs {
+  const int32_t* context_lens;
+  const int32_t* node_counts;  // NULL: T each
+  int32_t* ctx_eff;            // [B] validated lengths
+  long long* start;            // [B + 1] steps x KV heads before each sequence
+  TreeBound* bounds;           // [max_shares + 1]
+  int32_t* shares;
+  __nv_bfloat16* out;
+  unsigned* err;
+  int B, T, Hkv, max_ctx, row_elems /* T * Hq * D */;
+  int max_shares, min_steps;
+};
+
+// CTA 0: lengths, the prefix sums of the sequences' steps, the shares'
+// boundaries, zeros for inactive sequences.  Other CTAs: tree_scan_values.
+//
+// A boundary within `near` steps of an item's start or end moves there: the
+// partial it would leave costs more than the imbalance.
+__global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreePlanArgs a, const TreeScan scan) {
+  pdl_trigger();
+  pdl_wait();
+  if (blockIdx.x > 0) {  // block-uniform: these CTAs never reach the barriers below
+    tree_scan_values(scan, (blockIdx.x - 1) * (kTreePlanThreads / 32) + (threadIdx.x >> 5),
+                     static_cast<int64_t>(gridDim.x - 1) * (kTreePlanThreads / 32));
+    return;
+  }
+  __shared__ long long warp_tot[kTreePlanThreads / 32];
+  __shared__ long long carry_s;
+  __shared__ long long start_s[kTreePlanSmem + 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) carry_s = 0;
+  __syncthreads();
+  unsigned err = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kTreePlanThreads) {
+    const int b = b0 + tid;
+    long long steps = 0;
+    if (b < a.B) {
+      int c = a.context_lens[b];
+      const int nodes = a.node_counts != nullptr ? a.node_counts[b] : a.T;
+      if (c < 0 || c > a.max_ctx) {
+        err |= PKV_DEVERR_CONTEXT_LEN;
+        c = 0;
+      }
+      if (nodes < 0 || nodes > a.T) {
+        err |= PKV_DEVERR_TREE;
+        c = 0;
+      }
+      if (nodes == 0) c = 0;  // every row is zero
+      a.ctx_eff[b] = c;
+      steps = static_cast<long long>((c + kTreeTokens - 1) / kTreeTokens) * a.Hkv;
+    }
+    long long x = steps;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_tot[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+      long long w = warp_tot[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(kFull, w, o);
+        if (lane >= o) w += y;
+      }
+      warp_tot[lane] = w;
+    }
+    __syncthreads();
+    const long long before = carry_s + (warp > 0 ? warp_tot[warp - 1] : 0) + x - steps;
+    if (b < a.B) {
+      a.start[b] = before;
+      if (a.B <= kTreePlanSmem) start_s[b] = before;
+    }
+    __syncthreads();
+    if (tid == kTreePlanThreads - 1) carry_s += warp_tot[31];
+    __syncthreads();
+  }
+  if (err) atomicOr(a.err, err);
+  const long long total = carry_s;
+  if (tid == 0) {
+    a.start[a.B] = total;
+    if (a.B <= kTreePlanSmem) start_s[a.B] = total;
+  }
+  __syncthreads();
+  const long long* start = a.B <= kTreePlanSmem ? start_s : a.start;
+  // shares of at least min_steps steps
+  const int shares = static_cast<int>(min(static_cast<long long>(a.max_shares), (total + a.min_steps - 1) / a.min_steps));
+  if (tid == 0) *a.shares = shares;
+  const long long near = shares > 0 ? min(2ll, total / shares / 4) : 0;
+  for (int s = tid; s <= shares; s += kTreePlanThreads) {
+    TreeBound r{shares > 0 ? total * s / shares : 0, a.B, 0, 0, 0};
+    if (s < shares) {
+      int lo = 0, hi = a.B - 1;  // the sequence with start[lo] <= pos < start[lo + 1]
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid + 1] > r.pos) hi = mid; else lo = mid + 1;
+      }
+      const long long in = r.pos - start[lo];
+      const int nt = static_cast<int>((start[lo + 1] - start[lo]) / a.Hkv);
+      r.b = lo;
+      r.kvh = static_cast<int>(in / nt);
+      r.step = static_cast<int>(in - static_cast<long long>(r.kvh) * nt);
+      if (r.step > 0 && r.step <= near) {
+        r.pos -= r.step;
+        r.step = 0;
+      } else if (r.step > 0 && nt - r.step <= near) {
+        r.pos += nt - r.step;
+        r.step = 0;
+        if (++r.kvh == a.Hkv) {  // (the next sequences may be inactive: whoever starts here skips them)
+          r.kvh = 0;
+          ++r.b;
+        }
+      }
+    }
+    a.bounds[s] = r;
+  }
+  // zeros for inactive sequences (one warp per sequence)
+  for (int b = warp; b < a.B; b += kTreePlanThreads / 32) {
+    if (a.ctx_eff[b] != 0) continue;
+    uint4* o = reinterpret_cast<uint4*>(a.out + static_cast<size_t>(b) * a.row_elems);
+    for (int i = lane; i < a.row_elems / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// merge: out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p over the partials
+// of an item that shares split.  The share in which the item starts leaves it
+// as its last unit; the shares after it continue it with their first unit
+// until one ends it.  One CTA per (share, row tiles of a CTA, quarter of the
+// rows), a warp per row.
+// ---------------------------------------------------------------------------
+constexpr int kTreeMergeThreads = 256;
+constexpr int kTreeMergeSplit = 4;
+
+struct TreeMergeArgs {
+  const int32_t* ctx_eff;
+  const TreeBound* bounds;
+  const int32_t* shares;
+  const float2* part_ml;
+  const float* part_o;
+  __nv_bfloat16* out;
+  int Hq, G, T, Tt, NP, tiles /* per CTA */;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kTreeMergeThreads) tree_merge_kernel(const TreeMergeArgs a) {
+  constexpr int kPer = D / 32;
+  pdl_trigger();
+  pdl_wait();
+  const int quarter = blockIdx.x % kTreeMergeSplit;
+  const int cta = blockIdx.x / kTreeMergeSplit;
+  const int share = cta / a.NP, pair = cta - share * a.NP;
+  const int shares = *a.shares;
+  if (share + 1 >= shares) return;  // the last share splits nothing
+  const TreeBound next = a.bounds[share + 1];
+  if (next.step == 0) return;  // an item starts there
+  const long long item = next.pos - next.step;
+  const TreeBound mine = a.bounds[share];
+  if (item < mine.pos) return;  // the item started in an earlier share
+  const long long item_end = item + (a.ctx_eff[next.b] + kTreeTokens - 1) / kTreeTokens;
+  int last = share + 1;  // the share that ends the item
+  while (a.bounds[last + 1].pos < item_end) ++last;
+  const int parts = last - share + 1;
+  const int rows = a.tiles * kTaRows;
+  // the owner's partial is its first unit's place if the share starts with the item
+  const size_t first = (static_cast<size_t>(cta) * 2 + (item == mine.pos ? 0 : 1)) * rows;
+  const size_t stride = static_cast<size_t>(a.NP) * 2 * rows;  // from a share's partials to the next one's
+  const size_t cont = (static_cast<size_t>(cta) * 2) * rows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int rr = quarter + kTreeMergeSplit * warp; rr < rows; rr += kTreeMergeSplit * (kTreeMergeThreads / 32)) {
+    const int r = rr % kTaRows, tile = (a.tiles == 2 ? 2 * pair : 0) + rr / kTaRows;
+    const int tl = r / a.G, t = tile * a.Tt + tl;
+    if (tl >= a.Tt || t >= a.T) continue;
+    auto at = [&](int p) { return (p == 0 ? first : cont + stride * p) + rr; };
+    float M = -INFINITY;
+    for (int p = lane; p < parts; p += 32) M = fmaxf(M, a.part_ml[at(p)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    float acc[kPer], sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+      const float2 ml = a.part_ml[at(p)];
+      // (an empty partial has O = 0, or the row's fixed value)
+      const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+      sum = fmaf(w, ml.y, sum);
+      const float* src = a.part_o + at(p) * D + lane * kPer;
+      if constexpr (kPer == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        acc[0] = fmaf(w, v.x, acc[0]);
+        acc[1] = fmaf(w, v.y, acc[1]);
+        acc[2] = fmaf(w, v.z, acc[2]);
+        acc[3] = fmaf(w, v.w, acc[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        acc[0] = fmaf(w, v.x, acc[0]);
+        acc[1] = fmaf(w, v.y, acc[1]);
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    __nv_bfloat16* o = a.out + (static_cast<size_t>(next.b * a.T + t) * a.Hq + next.kvh * a.G + (r - tl * a.G)) * D + lane * kPer;
+#pragma unroll
+    for (int j = 0; j < kPer; j += 2)
+      *reinterpret_cast<__nv_bfloat162*>(o + j) = __floats2bfloat162_rn(acc[j] * inv, acc[j + 1] * inv);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+template <int D, int KV, bool PAIR>
+static const void* attend_instance(int bs) {
+  return bs == 16 ? reinterpret_cast<const void*>(&tree_attend_kernel<D, 16, KV, PAIR>)
+                  : reinterpret_cast<const void*>(&tree_attend_kernel<D, 32, KV, PAIR>);
+}
+
+struct TreeKernel {
+  const void* fn;
+  size_t smem;
+  int threads;
+};
+template <int D, int KV>
+static TreeKernel attend_kernel(int bs, bool pair) {
+  return pair ? TreeKernel{attend_instance<D, KV, true>(bs), TaLayout<D, KV, true>::kBytes, ta_threads(KV)}
+              : TreeKernel{attend_instance<D, KV, false>(bs), TaLayout<D, KV, false>::kBytes, ta_threads(KV)};
+}
+static TreeKernel pick(int kv_dtype, int D, int bs, bool pair) {
+  if (kv_dtype == PKV_KV_FP8_E4M3) return attend_kernel<128, PKV_KV_FP8_E4M3>(bs, pair);
+  if (kv_dtype == PKV_KV_INT8) return attend_kernel<128, PKV_KV_INT8>(bs, pair);
+  return D == 64 ? attend_kernel<64, PKV_KV_BF16>(bs, pair) : attend_kernel<128, PKV_KV_BF16>(bs, pair);
+}
+
+size_t tree_attend_smem_bytes(int kv_dtype, int D, int pair) { return pick(kv_dtype, D, 16, pair != 0).smem; }
+
+static size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+TreeWorkspace tree_workspace(int B, int Hkv, int D, int NT, int tree_words, int max_shares) {
+  const int NP = NT > 1 ? (NT + 1) / 2 : 1, tiles = NT > 1 ? 2 : 1;
+  const size_t rows = static_cast<size_t>(max_shares) * NP * 2 * tiles * kTaRows;
+  TreeWorkspace w{};
+  size_t off = 0;
+  w.shares = off;
+  off += 256;
+  w.ctx_eff = off;
+  off = align_up(off + sizeof(int32_t) * static_cast<size_t>(B));
+  w.start = off;
+  off = align_up(off + sizeof(long long) * (static_cast<size_t>(B) + 1));
+  w.bounds = off;
+  off = align_up(off + sizeof(TreeBound) * (static_cast<size_t>(max_shares) + 1));
+  w.poison = off;
+  off = align_up(off + sizeof(uint32_t) * static_cast<size_t>(B) * Hkv * tree_words);
+  w.part_ml = off;
+  off = align_up(off + sizeof(float2) * rows);
+  w.part_o = off;
+  off = align_up(off + sizeof(float) * D * rows);
+  w.total = off;
+  return w;
+}
+
+// Raises a kernel's dynamic shared memory limit, once per (device, context, kernel).
+static cudaError_t allow_smem(const void* fn, size_t smem) {
+  struct Entry {
+    int dev;
+    void* ctx;
+    const void* fn;
+  };
+  static std::mutex mu;
+  static std::vector<Entry> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  void* ctx = current_context();
+  std::lock_guard<std::mutex> lock(mu);
+  for (const Entry& x : done)
+    if (x.dev == dev && x.ctx == ctx && ctx != nullptr && x.fn == fn) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess) done.push_back(Entry{dev, current_context(), fn});
+  return e;
+}
+
+cudaError_t launch_tree_attend(const DecodeLaunch& L, uint8_t* ws, int* launched) {
+  const bool pair = L.NT > 1;
+  const int NP = pair ? (L.NT + 1) / 2 : 1;
+  const TreeKernel k = pick(L.kv_dtype, L.D, L.bs, pair);
+  cudaError_t e = allow_smem(k.fn, k.smem);
+  if (e != cudaSuccess) return e;
+  const TreeWorkspace w = tree_workspace(L.B, L.Hkv, L.D, L.NT, L.tree_words, L.tree_shares);
+  int32_t* shares = reinterpret_cast<int32_t*>(ws + w.shares);
+  int32_t* ctx_eff = reinterpret_cast<int32_t*>(ws + w.ctx_eff);
+  TreeBound* bounds = reinterpret_cast<TreeBound*>(ws + w.bounds);
+  uint32_t* poison = reinterpret_cast<uint32_t*>(ws + w.poison);
+
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = L.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+
+  // 1. planner
+  TreePlanArgs pa{L.context_lens, L.node_counts, ctx_eff, reinterpret_cast<long long*>(ws + w.start), bounds, shares,
+                  static_cast<__nv_bfloat16*>(L.out), L.err, L.B, L.T, L.Hkv, L.MB * L.bs, L.T * L.Hq * L.D,
+                  L.tree_shares, L.tree_min_steps};
+  const TreeScan scan = tree_scan_of(L, poison);
+  cfg.gridDim = dim3(1 + tree_scan_ctas(L, kTreePlanThreads / 32));
+  cfg.blockDim = dim3(kTreePlanThreads);
+  e = cudaLaunchKernelEx(&cfg, tree_plan_kernel, pa, scan);
+  if (e != cudaSuccess) return e;
+  *launched += 1;
+
+  // 2. attention: one CTA per share and row-tile pair
+  TaParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(L.q);
+  p.out = static_cast<__nv_bfloat16*>(L.out);
+  p.block_tables = L.block_tables;
+  p.k_scale = L.k_scale;
+  p.v_scale = L.v_scale;
+  p.ctx_eff = ctx_eff;
+  p.bounds = bounds;
+  p.shares = shares;
+  p.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
+  p.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  p.err = L.err;
+  p.tree.mask = L.tree_mask;
+  p.tree.node_counts = L.node_counts;
+  p.tree.poison = L.kv_dtype != PKV_KV_INT8 ? poison : nullptr;
+  p.tree.words = L.tree_words;
+  p.tree.stride = L.tree_stride;
+  p.Hq = L.Hq;
+  p.Hkv = L.Hkv;
+  p.G = L.G;
+  p.T = L.T;
+  p.Tt = L.Tt;
+  p.NT = L.NT;
+  p.NP = NP;
+  p.MB = L.MB;
+  p.NB = L.NB;
+  p.row_base = L.row_base;
+  p.scale_log2 = L.scale_log2;
+  CUtensorMap kmap = L.kmap, vmap = L.vmap, qmap = L.qmap;
+  void* args[] = {&kmap, &vmap, &qmap, &p};
+  cfg.gridDim = dim3(static_cast<unsigned>(L.tree_shares * NP));
+  cfg.blockDim = dim3(k.threads);
+  cfg.dynamicSmemBytes = k.smem;
+  cfg.numAttrs = (L.ev_start == nullptr) ? 1 : 0;  // an event between them: no overlap with the planner
+  if (L.ev_start != nullptr && (e = cudaEventRecord(L.ev_start, L.stream)) != cudaSuccess) return e;
+  e = cudaLaunchKernelExC(&cfg, k.fn, args);
+  if (e != cudaSuccess) return e;
+  if (L.ev_end != nullptr && (e = cudaEventRecord(L.ev_end, L.stream)) != cudaSuccess) return e;
+  *launched += 1;
+
+  // 3. merge of the items that shares split
+  if (L.tree_shares > 1) {
+    const TreeMergeArgs ma{ctx_eff, bounds, shares, p.part_ml, p.part_o, p.out, L.Hq, L.G, L.T, L.Tt, NP, pair ? 2 : 1};
+    cfg.gridDim = dim3(static_cast<unsigned>((L.tree_shares - 1) * NP * kTreeMergeSplit));
+    cfg.blockDim = dim3(kTreeMergeThreads);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = (L.ev_end == nullptr) ? 1 : 0;
+    e = L.D == 64 ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<64>, ma) : cudaLaunchKernelEx(&cfg, tree_merge_kernel<128>, ma);
+    if (e != cudaSuccess) return e;
+    *launched += 1;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace pkv

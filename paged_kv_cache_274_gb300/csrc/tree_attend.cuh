@@ -1,0 +1,1016 @@
+// Attention of drafted-tree nodes over the paged cache on the 5th-generation
+// tensor cores (tcgen05 + TMEM): bf16 caches of head_dim 64 and 128, E4M3 and
+// INT8 caches of head_dim 128.
+//
+// A sequence of n cached tokens whose last m are tree nodes has T x G (node,
+// head) rows per KV head; row t attends to the base = n - m tokens before the
+// tree and to the nodes of its mask row (tree_mask.cuh).  The rows form tiles
+// of 128 (M of the MMA); the cache is stepped through 128 tokens at a time.
+//
+// What bounds it: with one tile of rows the cache bytes.  128 tokens of one KV
+// head are 64 KiB (bf16, D 128) or 32 KiB (one byte), about 2800 or 1400
+// cycles of one SM's share of HBM, against 1024 cycles of tensor pipe for
+// S = Q K^T and O += P V and some 700 issue cycles of softmax per
+// sub-partition.  With two and more tiles the tensor pipe.
+//
+// One CTA per SM, no CTA-wide barrier inside the loop:
+//   * Two streams of softmax warps (four warps each, one row per thread), each
+//     with its own S and O in tensor memory (S0 S1 O0 O1, 128 columns each), so
+//     that the products of one stream run while the other's softmax does.
+//     PAIR: the streams hold two row tiles of one KV head and read every step
+//     of the cache together.  Otherwise there is one row tile, stream 0 takes
+//     the even steps and stream 1 the odd ones, and a work unit ends with the
+//     sum of the two (as split-K partials would be joined).
+//   * One thread issues, step after step, PV_i of the stream's step before and
+//     S_i of this one; P (16 bits) overwrites the S columns it came from and is
+//     the A operand of PV.  tcgen05 operations of one thread complete in order,
+//     so S_i never overwrites a P_i that is still read.
+//   * A K copy warp walks the CTA's share of the work, publishes a descriptor
+//     per step (page ids, page parameters) in a ring, and copies K pages; a V
+//     copy warp copies V pages; for bf16 caches a query warp the query tiles.
+//   * One-byte caches add four converter warps: they rewrite V pages (and INT8
+//     K pages) in their stage as exact 16-bit code values, and the query rows
+//     in the type of the K operand (E4M3 K pages feed the products as they
+//     are, against a query of two E4M3 parts).  One warp per sub-partition,
+//     because the conversion instruction issues at a quarter rate: a single
+//     converter warp took 1500 cycles per 64 tokens.  The page scales multiply
+//     the scores and P.
+//
+// Work split ("stream-K"): the steps of all (sequence, KV head) items in a row
+// are cut into equal shares, one per SM, whatever the lengths; a share that
+// starts or ends inside an item leaves partials (m, l, O) for the merge
+// kernel, at most two per CTA.  Boundaries near an item's ends move there.
+// The shares depend on the lengths only, so results do not vary between runs.
+//
+// The running maximum is lazy (moved when it grows by more than 2^8), so O is
+// rarely rescaled.  S, m, l and O are fp32; P is rounded to bf16 (bf16 caches:
+// both operands of a product have one type) or f16 (one-byte caches).  Every
+// wait is bounded; a CTA that gives up records PKV_DEVERR_TIMEOUT, lets its own
+// copies and products finish (bounded) and frees its tensor memory.
+#pragma once
+
+#include <cstddef>
+
+#include "paged_decode_tc2.cuh"
+#include "tree_plan.cuh"
+
+namespace pkv {
+
+constexpr int kTaRows = 128;    // query rows per tile
+constexpr int kTaRing = 8;      // step descriptors: a step's is read until its softmax is done, at most 5 steps back
+constexpr uint32_t kTaCols = 512;  // TMEM: S0 0, S1 128, O0 256, O1 384
+
+struct TaParams {
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  const int32_t* block_tables;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* ctx_eff;
+  const TreeBound* bounds;  // [shares + 1]
+  const int32_t* shares;    // number of shares in use
+  float2* part_ml;          // [CTA][2][tiles per CTA x 128]
+  float* part_o;            // [CTA][2][tiles per CTA x 128][D]
+  unsigned* err;
+  TreeArgs tree;
+  int Hq, Hkv, G, T, Tt, NT, NP, MB, NB, row_base;
+  float scale_log2;
+};
+
+// One step's descriptor in the ring.
+struct TaStep {
+  int n;      // steps of the work unit (0: no more work)
+  int b, kvh;
+  int t0, t1;  // the unit's tokens
+  int part;    // 0: the unit is its whole item; else 1 + index of the CTA's partial
+  int np;      // pages of this step
+  int ctx;
+  int pages[8];
+  uint8_t bad[8];   // page id out of range
+  float vmax;       // one-byte caches: largest |v scale| of the step's pages
+  int pad;
+  float4 par[8];    // one-byte caches: k scale, k zero, v scale, v zero per page
+};
+
+__host__ __device__ constexpr int ta_threads(int kv) { return kv == PKV_KV_BF16 ? 384 : 512; }
+
+template <int D, int KV, bool PAIR>
+struct TaLayout {  // byte offsets from the 1024-aligned shared-memory base
+  static constexpr bool kOneByte = KV != PKV_KV_BF16;
+  static constexpr bool kF8K = KV == PKV_KV_FP8_E4M3;
+  static constexpr uint32_t kRegion = kTreeTokens * 128;      // 128 rows of 128 bytes
+  static constexpr uint32_t kTile = (D / 64) * kRegion;       // 128 rows of D 16-bit values
+  static constexpr uint32_t kKTile = kF8K ? kRegion : kTile;  // E4M3 K: codes
+  static constexpr int kQTiles = PAIR ? 2 : 1;
+  // stages: as many as fit beside the query tiles
+  static constexpr int kKStages = D == 64 ? 4 : kF8K ? 4 : (KV == PKV_KV_INT8 && PAIR) ? 2 : 3;
+  static constexpr int kVStages = D == 64 ? 4 : (kF8K && !PAIR) ? 3 : 2;
+  static constexpr uint32_t kQ = 0;  // E4M3: the two parts of a tile, kRegion each
+  static constexpr uint32_t kK = kQ + kQTiles * kTile;
+  static constexpr uint32_t kV = kK + kKStages * kKTile;
+  static constexpr uint32_t kBars = kV + kVStages * kTile;
+  // k_full k_free tma_k [K], v_full v_free tma_v [V], s_full p_full o_full
+  // o_free [2], step_full [ring], q_full q_free q_read x_full mma_drain
+  static constexpr int kNumBars = 3 * kKStages + 3 * kVStages + 8 + kTaRing + 5;
+  static constexpr uint32_t kMisc = kBars + 8 * kNumBars;
+  static constexpr uint32_t kRing = (kMisc + 4 + 15) & ~15u;
+  static constexpr uint32_t kStep = kOneByte ? sizeof(TaStep) : offsetof(TaStep, par);
+  static constexpr uint32_t kXml = kRing + kTaRing * kStep;  // one tile: (m, l) of both streams' rows
+  static constexpr uint32_t kQrow = kXml + (PAIR ? 0 : 2 * kTaRows * 8 + 16);
+  // one-byte caches: (2^kq, sum of q) per query row
+  static constexpr uint32_t kEnd = kQrow + (kOneByte ? kQTiles * kTaRows * 8 : 0);
+  static constexpr size_t kBytes = 1024 + kEnd;
+  static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
+  static_assert(sizeof(TaStep) % 16 == 0 && offsetof(TaStep, par) % 16 == 0, "");
+};
+
+// D[tmem] (+)= A[smem] . B[smem]^T with E4M3 operands (kind::f8f6f4); one thread.
+__device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u));
+}
+
+template <int D, int BS, int KV, bool PAIR>
+__global__ void __launch_bounds__(ta_threads(KV), 1)
+    tree_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                       const __grid_constant__ CUtensorMap qmap,  // bf16: q [B][T][Hq][D], box 64 x G x Tt
+                       const TaParams p) {
+  using L = TaLayout<D, KV, PAIR>;
+  constexpr bool kOneByte = L::kOneByte, kF8K = L::kF8K, kI8 = KV == PKV_KV_INT8;
+  static_assert(!kOneByte || D == 128, "one-byte pages need head_dim 128");
+  constexpr int PPI = kTreeTokens / BS;  // pages per step
+  constexpr int KS = L::kKStages, VS = L::kVStages;
+  constexpr int kHalves = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // Barrier phases: k_* and v_* rings by the CTA's running step index g (stage
+  // g % stages), step_full by g % ring; s_full and p_full once per step of a
+  // stream; q_full, q_free, q_read, o_free, x_full once per unit; o_full[1] once per
+  // unit with a step for stream 1.  Each barrier's next use depends on the wait
+  // for its previous phase, so no waiter is ever two phases behind.
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + L::kBars);  // K of the step ready for the products
+  uint64_t* k_free = k_full + KS;   // the step's S done
+  uint64_t* tma_k = k_free + KS;    // INT8: K codes landed
+  uint64_t* v_full = tma_k + KS;
+  uint64_t* v_free = v_full + VS;   // the step's PV done
+  uint64_t* tma_v = v_free + VS;    // one-byte: V codes landed
+  uint64_t* s_full = tma_v + VS;    // [stream] S_i (and every product before it) done
+  uint64_t* p_full = s_full + 2;    // [stream] P_i in TMEM, stale V rows cleared
+  uint64_t* o_full = p_full + 2;    // [stream] the unit's last PV_i done
+  uint64_t* o_free = o_full + 2;    // [stream] the unit's O_i read
+  uint64_t* step_full = o_free + 2; // [ring] descriptor written
+  uint64_t* q_full = step_full + kTaRing;
+  uint64_t* q_free = q_full + 1;    // the unit's last S done
+  uint64_t* q_read = q_free + 1;    // one-byte: the unit's row factors read by every softmax warp
+  uint64_t* x_full = q_read + 1;    // one tile: both streams' (m, l) written
+  uint64_t* mma_drain = x_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kMisc);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < KS; ++s) {
+      mbar_init(&k_full[s], kI8 ? 4 : 1);  // INT8: four converter warps
+      mbar_init(&k_free[s], 1);
+      mbar_init(&tma_k[s], 1);
+    }
+    for (int s = 0; s < VS; ++s) {
+      mbar_init(&v_full[s], kOneByte ? 4 : 1);
+      mbar_init(&v_free[s], 1);
+      mbar_init(&tma_v[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 4);  // one lane per warp of the stream
+      mbar_init(&o_full[s], 1);
+      mbar_init(&o_free[s], PAIR ? 4 : 8);
+    }
+    for (int s = 0; s < kTaRing; ++s) mbar_init(&step_full[s], 1);
+    mbar_init(q_full, kOneByte ? 4 : 1);
+    mbar_init(q_free, 1);
+    mbar_init(q_read, 8);
+    mbar_init(x_full, 8);
+    mbar_init(mma_drain, 1);
+    fence_mbar_init();
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+    if (!kOneByte) prefetch_tensormap(&qmap);
+  }
+  if (warp == 0) tc_alloc(tmem_slot, kTaCols);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();
+  pdl_wait();
+
+  const int share = blockIdx.x / p.NP, pair = blockIdx.x - share * p.NP;
+  bool timed_out = false;
+  uint32_t k_issued = 0, v_issued = 0, q_loads = 0, mma_issued = 0;  // for the drain after a timeout
+
+  auto step_at = [&](uint32_t g) { return reinterpret_cast<volatile TaStep*>(sm + L::kRing + (g % kTaRing) * L::kStep); };
+  // this warp waits (lane 0, bounded) for phase `parity` of `bar`; false on timeout
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+    int ok = 1;
+    if (lane == 0) ok = mbar_wait_bounded(bar, parity, kWaitLimitNs) ? 1 : 0;
+    return __shfl_sync(kFull, ok, 0) != 0;
+  };
+  auto wait_step = [&](uint32_t g) { return warp_wait(&step_full[g % kTaRing], (g / kTaRing) & 1u); };
+
+  // one-byte caches share the registers out anew: 2 x 128 x 168 for the softmax
+  // warpgroups + 2 x 128 x 88 = 512 x 128 at the launch
+  if (warp >= 8 && warp < 12) {
+  if constexpr (kOneByte) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == 9) {
+    // K copy warp: the share's units, a descriptor and the K pages per step
+    uint32_t g = 0;
+    int b = 0, kvh = 0, j0 = 0;
+    long long pos = 0, end = 0;
+    if (share < __ldg(p.shares)) {
+      pos = p.bounds[share].pos;
+      end = p.bounds[share + 1].pos;
+      b = p.bounds[share].b;
+      kvh = p.bounds[share].kvh;
+      j0 = p.bounds[share].step;
+    }
+    const uint64_t policy = p.NP > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+    bool first_unit = true;
+    while (pos < end && !timed_out) {
+      const int ctx = __ldg(p.ctx_eff + b);
+      const int nt = (ctx + kTreeTokens - 1) / kTreeTokens;
+      if (nt == 0) {  // an inactive sequence
+        ++b;
+        continue;
+      }
+      const int n = static_cast<int>(min(static_cast<long long>(nt - j0), end - pos));
+      const int t0 = j0 * kTreeTokens, t1 = min(ctx, (j0 + n) * kTreeTokens);
+      const int part = (j0 == 0 && n == nt) ? 0 : (first_unit ? 1 : 2);
+      first_unit = false;
+      const int npages = (t1 - t0 + BS - 1) / BS;
+      const int* trow = p.block_tables + static_cast<size_t>(b) * p.MB + t0 / BS;
+      // lane i holds page i of a run of 32 pages, and of the next run
+      auto load_ids = [&](int q) { return q < npages ? __ldg(trow + q) : 0; };
+      auto load_par = [&](int q, int id) {
+        float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+        if constexpr (kOneByte) {
+          if (q < npages && static_cast<unsigned>(id) < static_cast<unsigned>(p.NB)) {
+            const size_t pi = static_cast<size_t>(id) * p.Hkv + kvh;
+            if constexpr (kI8) {
+              const float2 kp = __ldg(reinterpret_cast<const float2*>(p.k_scale) + pi);
+              const float2 vp = __ldg(reinterpret_cast<const float2*>(p.v_scale) + pi);
+              r = make_float4(kp.x, kp.y, vp.x, vp.y);
+            } else {
+              r = make_float4(__ldg(p.k_scale + pi), 0.f, __ldg(p.v_scale + pi), 0.f);
+            }
+          }
+        }
+        return r;
+      };
+      int id = load_ids(lane), id_next = load_ids(lane + 32);
+      float4 par = load_par(lane, id), par_next = load_par(lane + 32, id_next);
+      for (int j = 0; j < n; ++j, ++g) {
+        const int q0 = j * PPI;  // the step's first page
+        if (q0 > 0 && (q0 & 31) == 0) {
+          id = id_next;
+          par = par_next;
+          id_next = load_ids(q0 + 32 + lane);
+          par_next = load_par(q0 + 32 + lane, id_next);
+        }
+        if (g >= KS && !warp_wait(&k_free[g % KS], ((g - KS) / KS) & 1u)) {
+          timed_out = true;
+          break;
+        }
+        volatile TaStep* st = step_at(g);
+        const int np = min(PPI, npages - q0);
+        const int q = lane - (q0 & 31);  // this lane's page of the step
+        const bool mine = q >= 0 && q < np;
+        const bool bad = mine && static_cast<unsigned>(id) >= static_cast<unsigned>(p.NB);
+        const int phys = bad ? 0 : id;
+        if (q >= 0 && q < PPI) {
+          st->pages[q] = phys;
+          st->bad[q] = bad ? 1 : 0;
+          if constexpr (kOneByte) *reinterpret_cast<float4*>(const_cast<float4*>(&st->par[q])) = mine ? par : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (bad) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+        if constexpr (kOneByte) {
+          const uint32_t vm = __reduce_max_sync(kFull, mine ? __float_as_uint(fabsf(par.z)) : 0u);
+          if (lane == 0) st->vmax = __uint_as_float(vm);
+        }
+        if (lane == 0) {
+          st->n = n;
+          st->b = b;
+          st->kvh = kvh;
+          st->t0 = t0;
+          st->t1 = t1;
+          st->part = part;
+          st->np = np;
+          st->ctx = ctx;
+        }
+        uint8_t* dst = sm + L::kK + (g % KS) * L::kKTile;
+        uint64_t* bar = kI8 ? &tma_k[g % KS] : &k_full[g % KS];
+        if (lane == 0) {
+          fence_proxy_async_smem();  // INT8: the converters wrote the stage before
+          mbar_arrive_expect_tx(bar, static_cast<uint32_t>(np) * (kOneByte ? 128u : 128u * kHalves) * BS);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&step_full[g % kTaRing]);  // release: the descriptor
+        if (mine) {
+          const int row = p.row_base + (phys * p.Hkv + kvh) * BS;
+          if constexpr (kOneByte) {
+            tma_load_2d(dst + (kF8K ? 0 : L::kRegion) + q * BS * 128, &kmap, bar, 0, row, policy);
+          } else {
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) tma_load_2d(dst + h * L::kRegion + q * BS * 128, &kmap, bar, 64 * h, row, policy);
+          }
+        }
+        k_issued = g + 1;
+      }
+      pos += n;
+      j0 = 0;
+      if (++kvh == p.Hkv) {
+        kvh = 0;
+        ++b;
+      }
+    }
+    if (!timed_out) {  // no more work
+      if (g >= KS && !warp_wait(&k_free[g % KS], ((g - KS) / KS) & 1u)) timed_out = true;
+      if (lane == 0 && !timed_out) {
+        step_at(g)->n = 0;
+        mbar_arrive(&step_full[g % kTaRing]);
+      }
+    }
+  } else if (warp == 10) {
+    // V copy warp: V pages of each step
+    const uint64_t policy = p.NP > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+    for (uint32_t g = 0;; ++g) {
+      if (!wait_step(g)) {
+        timed_out = true;
+        break;
+      }
+      const volatile TaStep* st = step_at(g);
+      if (st->n == 0) break;
+      const int kvh = st->kvh, np = st->np;
+      if (g >= VS && !warp_wait(&v_free[g % VS], ((g - VS) / VS) & 1u)) {
+        timed_out = true;
+        break;
+      }
+      uint8_t* dst = sm + L::kV + (g % VS) * L::kTile;
+      uint64_t* bar = kOneByte ? &tma_v[g % VS] : &v_full[g % VS];
+      if (lane == 0) {
+        fence_proxy_async_smem();  // after the clearing of stale rows and the converters' writes
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(np) * (kOneByte ? 128u : 128u * kHalves) * BS);
+      }
+      __syncwarp();
+      if (lane < np) {
+        const int row = p.row_base + (st->pages[lane] * p.Hkv + kvh) * BS;
+        if constexpr (kOneByte) {
+          tma_load_2d(dst + L::kRegion + lane * BS * 128, &vmap, bar, 0, row, policy);
+        } else {
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) tma_load_2d(dst + h * L::kRegion + lane * BS * 128, &vmap, bar, 64 * h, row, policy);
+        }
+      }
+      v_issued = g + 1;
+    }
+  } else if (warp == 11) {
+    if constexpr (!kOneByte) {
+      // query warp (bf16 caches): each unit's query tiles, once the products
+      // with the ones before are done
+      uint32_t g0 = 0;
+      for (;;) {
+        // the products first: only then is the next unit's descriptor at most
+        // one turn of the ring away (two turns look alike)
+        if ((q_loads > 0 && !warp_wait(q_free, (q_loads - 1) & 1u)) || !wait_step(g0)) {
+          timed_out = true;
+          break;
+        }
+        const volatile TaStep* st = step_at(g0);
+        const int n = st->n, b = st->b, kvh = st->kvh;
+        if (n == 0) break;
+        if (lane == 0) mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(L::kQTiles * kHalves) * 128u * static_cast<uint32_t>(p.G * p.Tt));
+        __syncwarp();
+        if (lane < L::kQTiles * kHalves) {  // rows past T are zero-filled
+          const int i = lane / kHalves, half = lane % kHalves;
+          tma_load_4d(sm + L::kQ + i * L::kTile + half * L::kRegion, &qmap, q_full, 64 * half, kvh * p.G, (2 * pair + i) * p.Tt, b);
+        }
+        ++q_loads;
+        g0 += static_cast<uint32_t>(n);
+      }
+    }
+  } else if (warp == 8) {
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = kF8K       ? tc_idesc_e4m3_f32(kTaRows, kTreeTokens)
+                                   : kOneByte ? tc_idesc_f16_f32(kTaRows, kTreeTokens)
+                                              : tc_idesc_bf16_f32(kTaRows, kTreeTokens);
+      constexpr uint32_t kIdescO = kOneByte ? tc_idesc_f16_f32(kTaRows, D, /*b_mn_major=*/true)
+                                            : tc_idesc_bf16_f32(kTaRows, D, /*b_mn_major=*/true);
+      const uint32_t q_addr = smem_addr(sm + L::kQ), k_addr = smem_addr(sm + L::kK), v_addr = smem_addr(sm + L::kV);
+      // S_i = Q . K^T; A and B K-major with the 128-byte swizzle, 32 bytes of
+      // each row per product
+      auto issue_s = [&](int i, uint32_t g) {
+        const uint32_t qa = q_addr + (PAIR ? i : 0) * L::kTile;
+        const uint32_t ka = k_addr + (g % KS) * L::kKTile;
+        if constexpr (kF8K) {  // both parts of the query against the same codes
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc_mma_e4m3(tmem + 128u * i, tc_smem_desc(qa + (kk >> 2) * L::kRegion + (kk & 3) * 32, 16, 1024, 2),
+                        tc_smem_desc(ka + (kk & 3) * 32, 16, 1024, 2), kIdescS, kk > 0);
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * L::kRegion + (kk & 3) * 32;
+            tc_mma_bf16(tmem + 128u * i, tc_smem_desc(qa + off, 16, 1024, 2), tc_smem_desc(ka + off, 16, 1024, 2), kIdescS, kk > 0);
+          }
+        }
+        ++mma_issued;
+      };
+      // O_i (+)= P_i . V: P of tokens 16kk .. 16kk + 15 in columns 8kk .. +7 of
+      // S_i, V MN-major as the pages hold it (64-d halves kRegion apart,
+      // 8-token groups 1024 B apart)
+      uint32_t pc[2] = {0, 0};  // P tiles taken, per stream
+      auto issue_pv = [&](int i, uint32_t g, bool first, uint32_t iu) -> bool {
+        if (!mbar_wait_fast(&p_full[i], pc[i] & 1u, kWaitLimitNs)) return false;
+        ++pc[i];
+        if ((!PAIR || i == 0) && !mbar_wait_fast(&v_full[g % VS], (g / VS) & 1u, kWaitLimitNs)) return false;
+        if (first && iu > 0 && !mbar_wait_fast(&o_free[i], (iu - 1) & 1u, kWaitLimitNs)) return false;
+        tc_fence_after_sync();
+        const uint32_t va = v_addr + (g % VS) * L::kTile;
+#pragma unroll
+        for (int kk = 0; kk < kTreeTokens / 16; ++kk)
+          tc_mma_bf16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk, tc_smem_desc(va + kk * 2048, L::kRegion, 1024, 2), kIdescO,
+                         !first || kk > 0);
+        ++mma_issued;
+        if (!PAIR || i == 1) tc_commit(&v_free[g % VS]);
+        return true;
+      };
+      uint32_t g0 = 0;
+      bool ok = true;
+      for (uint32_t iu = 0;; ++iu) {
+        if (!(ok = mbar_wait_fast(&step_full[g0 % kTaRing], (g0 / kTaRing) & 1u, kWaitLimitNs))) break;
+        const int n = step_at(g0)->n;
+        if (n == 0) break;
+        if (!(ok = mbar_wait_fast(q_full, iu & 1u, kWaitLimitNs))) break;
+        const int events = PAIR ? 2 * n : n;
+        for (int e = 0; ok && e < events; ++e) {
+          const int i = e & 1, k = e >> 1;  // stream, its step
+          const uint32_t g = g0 + (PAIR ? k : e);
+          if (!PAIR || i == 0) {
+            if (!(ok = mbar_wait_fast(&k_full[g % KS], (g / KS) & 1u, kWaitLimitNs))) break;
+            tc_fence_after_sync();
+          }
+          if (k > 0 && !(ok = issue_pv(i, g0 + (PAIR ? k - 1 : e - 2), k == 1, iu))) break;
+          issue_s(i, g);
+          tc_commit(&s_full[i]);
+          if (!PAIR || i == 1) tc_commit(&k_free[g % KS]);
+          if (e == events - 1) tc_commit(q_free);
+        }
+        // the last products of both streams, the earlier step's first
+        for (int x = 0; ok && x < 2; ++x) {
+          const int i = (!PAIR && (n & 1)) ? 1 - x : x;
+          const int ni = PAIR ? n : (n + 1 - i) / 2;  // the stream's steps
+          if (ni == 0) continue;
+          if (!(ok = issue_pv(i, g0 + (PAIR ? n - 1 : 2 * (ni - 1) + i), ni == 1, iu))) break;
+          tc_commit(&o_full[i]);
+        }
+        if (!ok) break;
+        g0 += static_cast<uint32_t>(n);
+      }
+      if (!ok) timed_out = true;
+    }
+    __syncwarp();
+  }
+  } else if (warp >= 12) {
+    if constexpr (kOneByte) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      // converter warps: 32 rows each of a unit's query tiles, then of its
+      // steps' K (INT8) and V; K of a step before V of the step before it, the
+      // order that the products need them in
+      const int cw = warp - 12;
+      auto convert = [&](bool is_k, uint32_t g) -> bool {
+        uint64_t* landed = is_k ? &tma_k[g % KS] : &tma_v[g % VS];
+        if (!warp_wait(landed, is_k ? (g / KS) & 1u : (g / VS) & 1u)) return false;
+        uint8_t* st = (is_k ? sm + L::kK + (g % KS) * L::kKTile : sm + L::kV + (g % VS) * L::kTile) + cw * 32 * 128;
+        const volatile TaStep* sp = step_at(g);
+        const int rows = sp->np * BS - 32 * cw;  // of the step's pages
+        uint32_t zc[1] = {0u};
+        if (is_k) {
+          widen_stage<KV, 32, kI8>(st, L::kRegion, lane, zc, rows);
+        } else {
+          if constexpr (kI8) {
+            if (lane < rows) zc[0] = int8_zero_const(const_cast<const TaStep*>(sp)->par[(32 * cw + lane) / BS].w);
+          }
+          widen_stage<KV, 32>(st, L::kRegion, lane, zc, rows);
+        }
+        fence_proxy_async_smem();  // read by the tensor cores
+        __syncwarp();
+        if (lane == 0) mbar_arrive(is_k ? &k_full[g % KS] : &v_full[g % VS]);
+        return true;
+      };
+      uint32_t g0 = 0;
+      for (uint32_t iu = 0;; ++iu) {
+        if (!wait_step(g0)) {
+          timed_out = true;
+          break;
+        }
+        const int n = step_at(g0)->n, b = step_at(g0)->b, kvh = step_at(g0)->kvh;
+        if (n == 0) break;
+        // the query tiles of the unit before are done with, and every softmax
+        // warp has seen its q_full: a stream without a step in that unit would
+        // otherwise be overtaken by this unit's (two phases look alike)
+        if (iu > 0 && !(warp_wait(q_free, (iu - 1) & 1u) && warp_wait(q_read, (iu - 1) & 1u))) {
+          timed_out = true;
+          break;
+        }
+        // Query row scaled by 2^-kq, in the type of the K operand.  INT8: f16,
+        // largest |q| in [2^14, 2^15), exact within 2^-10 of it.  E4M3: largest
+        // |q'| in [2^7, 2^8) as qh = e4m3(q') and ql = e4m3(q' - qh): a bf16
+        // q' has 8 significant bits, 4 in each part, so the sum is exact from
+        // 2^-2 up and within 2^-10 below
+        float2* qrow = reinterpret_cast<float2*>(sm + L::kQrow);
+        const int r = 32 * cw + lane;
+        for (int i = 0; i < L::kQTiles; ++i) {
+          const int tl = r / p.G, t = (2 * pair + i) * p.Tt + tl;
+          const bool in = tl < p.Tt && t < p.T;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              p.q + (static_cast<size_t>(b * p.T + (in ? t : 0)) * p.Hq + kvh * p.G + (in ? r - tl * p.G : 0)) * D);
+          uint32_t mx = 0;  // largest |q| as bf16 bits
+#pragma unroll 8
+          for (int c = 0; c < 16; ++c) {
+            const uint4 w = __ldg(src + c);
+            const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx = max(mx, max(w4[e] & 0x7fffu, (w4[e] >> 16) & 0x7fffu));
+          }
+          if (!in) mx = 0;
+          const int kq = mx == 0 ? 0 : max(-100, min(100, static_cast<int>(mx >> 7) - 127 - (kF8K ? 7 : 14)));
+          const float sc = in ? __uint_as_float(static_cast<uint32_t>(127 - kq) << 23) : 0.f;  // 2^-kq; 0: no row
+          float qsum = 0.f;
+          uint8_t* qt = sm + L::kQ + i * L::kTile;
+#pragma unroll 2
+          for (int c2 = 0; c2 < 8; ++c2) {  // 16 elements
+            uint32_t wh[4], wl[4], wf[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint4 w = __ldg(src + 2 * c2 + h);
+              const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 v = make_float2(in ? bf16lo_to_f32(w4[e]) * sc : 0.f, in ? bf16hi_to_f32(w4[e]) * sc : 0.f);
+                if constexpr (kF8K) {
+                  const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+                  const float2 hv = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3)));
+                  const __nv_fp8x2_storage_t lo =
+                      __nv_cvt_float2_to_fp8x2(make_float2(v.x - hv.x, v.y - hv.y), __NV_SATFINITE, __NV_E4M3);
+                  const int k = 2 * h + (e >> 1), s = 16 * (e & 1);
+                  wh[k] = (s ? wh[k] : 0u) | static_cast<uint32_t>(hi) << s;
+                  wl[k] = (s ? wl[k] : 0u) | static_cast<uint32_t>(lo) << s;
+                } else {
+                  const uint32_t f = pack_f16x2(v.x, v.y);
+                  wf[4 * h + e] = f;
+                  const float2 fv = __half22float2(*reinterpret_cast<const __half2*>(&f));
+                  qsum += fv.x + fv.y;
+                }
+              }
+            }
+            if constexpr (kF8K) {
+              uint8_t* d = qt + r * 128 + ((c2 ^ (r & 7)) << 4);
+              *reinterpret_cast<uint4*>(d) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+              *reinterpret_cast<uint4*>(d + L::kRegion) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+            } else {
+              uint8_t* d = qt + (c2 >> 2) * L::kRegion + r * 128;
+              const int c = 2 * (c2 & 3);
+              *reinterpret_cast<uint4*>(d + ((c ^ (r & 7)) << 4)) = make_uint4(wf[0], wf[1], wf[2], wf[3]);
+              *reinterpret_cast<uint4*>(d + (((c + 1) ^ (r & 7)) << 4)) = make_uint4(wf[4], wf[5], wf[6], wf[7]);
+            }
+          }
+          qrow[i * kTaRows + r] = make_float2(__uint_as_float(static_cast<uint32_t>(127 + kq) << 23), qsum);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        bool ok = !kI8 || convert(true, g0);
+        for (int j = 0; ok && j < n; ++j) {
+          const uint32_t g = g0 + j;
+          if (kI8 && j + 1 < n) ok = wait_step(g + 1) && convert(true, g + 1);
+          if (ok) ok = wait_step(g) && convert(false, g);
+        }
+        if (!ok) {
+          timed_out = true;
+          break;
+        }
+        g0 += static_cast<uint32_t>(n);
+      }
+    }
+  } else {
+    if constexpr (kOneByte) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    // softmax warps: stream i, row r of its tile in TMEM lane r
+    const int i = warp >> 2, r = tid & 127;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + 128u * i;
+    const uint32_t t_o = tmem + lane_base + 256u;  // O0; O1 is 128 columns on
+    const float c = p.scale_log2;
+    const float cs = kOneByte ? 1.f : c;  // one-byte scores are scaled before the maximum
+    const int tile = PAIR ? 2 * pair + i : 0;
+    const int tl = r / p.G, t = tile * p.Tt + tl;
+    const bool in_tile = tl < p.Tt && t < p.T;
+    // a warp without rows only keeps the barriers' counts and clears stale V rows
+    const bool warp_dead = !__any_sync(kFull, in_tile);
+    uint32_t g0 = 0, steps = 0, units1 = 0;  // steps of this stream, units with a step for stream 1
+    bool ok = true;
+    for (uint32_t iu = 0; ok; ++iu) {
+      if (!wait_step(g0)) {
+        ok = false;
+        break;
+      }
+      int n, b, kvh, t0, t1, part, base, mrow, prow, row_state;
+      {
+        const volatile TaStep* st = step_at(g0);
+        n = st->n;
+        if (n == 0) break;
+        b = st->b;
+        kvh = st->kvh;
+        t0 = st->t0;
+        t1 = st->t1;
+        part = st->part;
+        const int nodes = p.tree.node_counts != nullptr ? __ldg(p.tree.node_counts + b) : p.T;
+        base = st->ctx - nodes;
+        const bool live = in_tile && t < nodes;
+        mrow = live ? b * p.tree.stride + t * p.tree.words : -1;
+        prow = (b * p.Hkv + kvh) * p.tree.words;
+        row_state = live ? kTreeRowNormal : kTreeRowZero;
+      }
+      float cq = c, qsum = 0.f, vref = 1.f, inv_vref = 1.f;
+      if constexpr (kOneByte) {
+        if (!warp_wait(q_full, iu & 1u)) {
+          ok = false;
+          break;
+        }
+        const float2 qr = reinterpret_cast<const float2*>(sm + L::kQrow)[(PAIR ? i * kTaRows : 0) + r];
+        cq = c * qr.x;
+        qsum = qr.y;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_read);
+      }
+      bool vset = false;
+      float m = -INFINITY, l = 0.f;  // log2-domain lazy running maximum and sum of this row
+      const int ni = PAIR ? n : (n + 1 - i) / 2;  // this stream's steps
+      for (int k = 0; k < ni; ++k, ++steps) {
+        const int j = PAIR ? k : 2 * k + i;
+        const uint32_t g = g0 + j;
+        const int pos0 = t0 + j * kTreeTokens;
+        const int nvs = t1 - pos0;  // tokens of the step in the sequence
+        if (!wait_step(g)) {
+          ok = false;
+          break;
+        }
+        const TaStep* st = const_cast<const TaStep*>(step_at(g));
+        const uint64_t badw = PPI == 8 ? *reinterpret_cast<const volatile uint64_t*>(st->bad)
+                                       : *reinterpret_cast<const volatile uint32_t*>(st->bad);
+        uint64_t bad0 = 0ull, bad1 = 0ull;  // nodes with a non-finite V row
+        const bool nodes_here = pos0 + kTreeTokens > base;
+        if (nodes_here && p.tree.poison != nullptr) {
+          bad0 = tree_window64(p.tree.poison + prow, p.tree.words, pos0 - base);
+          bad1 = tree_window64(p.tree.poison + prow, p.tree.words, pos0 - base + 64);
+        }
+        // every token of the step is every row's (rows past the sequence's
+        // nodes too: their output is zero whatever they attend to)
+        const bool full = nvs >= kTreeTokens && !nodes_here && badw == 0;
+        bool vgrow = false;
+        float factor = 1.f;
+        if constexpr (kOneByte) {
+          // P carries v_scale / vref: vref moves when a step's scales are more
+          // than 2^6 above it, so that P stays below 2^14
+          const float vm = *reinterpret_cast<const volatile float*>(&st->vmax);
+          if (vm > (vset ? 64.f * vref : 0.f)) {
+            if (vset) {  // (until then every page's scale was 0, and O is)
+              factor = vref / vm;
+              vgrow = true;
+            }
+            vset = true;
+            vref = vm;
+            inv_vref = 1.f / vm;
+          }
+        }
+        if (!warp_wait(&s_full[i], steps & 1u)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        bool grow = false;
+        // one-byte: 32 scores of columns 32 cq32 .. +31 scaled to log2 units
+        auto scale32 = [&](uint32_t (&x)[32], int c32) {
+          if constexpr (kOneByte) {
+#pragma unroll
+            for (int h = 0; h < 32 / BS; ++h) {
+              const float4 pr = st->par[(32 * c32) / BS + h];
+              const float ck = cq * pr.x;
+              const float add = kI8 ? -(kInt8Bias + pr.y) * qsum * ck : 0.f;  // the biased K codes
+#pragma unroll
+              for (int e = 0; e < BS; e += 2) {
+                const int t2 = h * BS + e;
+                float a0, a1;
+                if constexpr (kI8)
+                  ffma2(a0, a1, __uint_as_float(x[t2]), __uint_as_float(x[t2 + 1]), ck, ck, add, add);
+                else
+                  fmul2(a0, a1, __uint_as_float(x[t2]), __uint_as_float(x[t2 + 1]), ck, ck);
+                x[t2] = __float_as_uint(a0);
+                x[t2 + 1] = __float_as_uint(a1);
+              }
+            }
+          }
+        };
+        auto vratio = [&](int c32, int e) -> float { return kOneByte ? st->par[(32 * c32 + e) / BS].z * inv_vref : 1.f; };
+        auto move_max = [&](float smax) {
+          grow = (m == -INFINITY) ? (smax != -INFINITY) : (smax > m + 8.f);
+          if (grow) {
+            const float f = (m == -INFINITY) ? 0.f : ex2_approx(m - smax);
+            factor *= f;
+            l *= f;
+            m = smax;
+          }
+        };
+        if (warp_dead) {
+        } else if (full) {
+          uint32_t x0[32], x1[32], x2[32], x3[32];
+          tc_ld32(t_s, x0);
+          tc_ld32(t_s + 32, x1);
+          tc_ld32(t_s + 64, x2);
+          tc_ld32(t_s + 96, x3);
+          tc_wait_ld_regs(x0);  // one wait for the four loads
+          tc_regs_loaded(x1);
+          tc_regs_loaded(x2);
+          tc_regs_loaded(x3);
+          scale32(x0, 0);
+          scale32(x1, 1);
+          scale32(x2, 2);
+          scale32(x3, 3);
+          const float ext = cs >= 0.f ? fmaxf(fmaxf(tree_ext32<true>(x0), tree_ext32<true>(x1)), fmaxf(tree_ext32<true>(x2), tree_ext32<true>(x3)))
+                                      : fminf(fminf(tree_ext32<false>(x0), tree_ext32<false>(x1)), fminf(tree_ext32<false>(x2), tree_ext32<false>(x3)));
+          move_max(ext * cs);
+          const float neg_m = (m == -INFINITY) ? 0.f : -m;
+          float ps[2] = {0.f, 0.f};
+          auto write_p = [&](const uint32_t (&x)[32], int c32) {
+            uint32_t pw[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float a0, a1;
+              ffma2(a0, a1, __uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), cs, cs, neg_m, neg_m);
+              const float p0 = ex2_approx(a0);
+              const float p1 = ex2_approx(a1);
+              fadd2(ps[0], ps[1], ps[0], ps[1], p0, p1);
+              if constexpr (kOneByte) {
+                const float vr = vratio(c32, 2 * e);
+                float b0, b1;
+                fmul2(b0, b1, p0, p1, vr, vr);
+                pw[e] = pack_f16x2(b0, b1);
+              } else {
+                pw[e] = pack_bf16x2(p0, p1);
+              }
+            }
+            tc_st16(t_s + 16 * c32, pw);
+          };
+          write_p(x0, 0);
+          write_p(x1, 1);
+          write_p(x2, 2);
+          write_p(x3, 3);
+          l += ps[0] + ps[1];
+        } else {
+          // a step with masked tokens (the sequence's end, nodes, bad pages):
+          // 32 scores at a time, the masked maximum first, then P (a chunk's P
+          // goes over columns whose scores are already read)
+          uint64_t rm0 = low_bits64(nvs), rm1 = low_bits64(nvs - 64);
+#pragma unroll
+          for (int q = 0; q < PPI; ++q)
+            if ((badw >> (8 * q)) & 0xffu) {
+              const uint64_t pm = ((1ull << BS) - 1ull) << ((q * BS) & 63);
+              if (q * BS < 64) rm0 &= ~pm; else rm1 &= ~pm;
+            }
+          uint64_t see0 = low_bits64(base - pos0), see1 = low_bits64(base - pos0 - 64);
+          if (nodes_here && mrow >= 0) {
+            see0 |= tree_window64(p.tree.mask + mrow, p.tree.words, pos0 - base);
+            see1 |= tree_window64(p.tree.mask + mrow, p.tree.words, pos0 - base + 64);
+          }
+          rm0 &= see0;
+          rm1 &= see1;
+          if (((rm0 & bad0) | (rm1 & bad1)) && row_state == kTreeRowNormal) row_state = kTreeRowNan;
+          rm0 &= ~bad0;
+          rm1 &= ~bad1;
+          __syncwarp();  // the TMEM accesses below are warp-collective
+          const float ext_init = cs >= 0.f ? -INFINITY : INFINITY;
+          float ext = ext_init;
+#pragma unroll 1
+          for (int c32 = 0; c32 < 4; ++c32) {
+            uint32_t x[32];
+            tc_ld32(t_s + 32 * c32, x);
+            const uint64_t r64 = c32 < 2 ? rm0 : rm1;
+            const uint32_t mk = (c32 & 1) ? static_cast<uint32_t>(r64 >> 32) : static_cast<uint32_t>(r64);
+            tc_wait_ld_regs(x);
+            scale32(x, c32);
+#pragma unroll
+            for (int kk = 0; kk < 32; ++kk) {
+              const float v = ((mk >> kk) & 1u) ? __uint_as_float(x[kk]) : ext_init;
+              ext = cs >= 0.f ? fmaxf(ext, v) : fminf(ext, v);
+            }
+          }
+          move_max((rm0 | rm1) != 0ull ? ext * cs : -INFINITY);
+          const float neg_m = (m == -INFINITY) ? 0.f : -m;
+          float ps0 = 0.f, ps1 = 0.f;
+          __syncwarp();
+#pragma unroll 1
+          for (int c32 = 0; c32 < 4; ++c32) {
+            uint32_t x[32];
+            tc_ld32(t_s + 32 * c32, x);
+            const uint64_t r64 = c32 < 2 ? rm0 : rm1;
+            const uint32_t mk = (c32 & 1) ? static_cast<uint32_t>(r64 >> 32) : static_cast<uint32_t>(r64);
+            tc_wait_ld_regs(x);
+            scale32(x, c32);
+            uint32_t pw[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float a0, a1;
+              ffma2(a0, a1, __uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), cs, cs, neg_m, neg_m);
+              float p0 = ex2_approx(a0);
+              float p1 = ex2_approx(a1);
+              p0 = ((mk >> (2 * e)) & 1u) ? p0 : 0.f;
+              p1 = ((mk >> (2 * e + 1)) & 1u) ? p1 : 0.f;
+              fadd2(ps0, ps1, ps0, ps1, p0, p1);
+              if constexpr (kOneByte) {
+                // (a masked token's page may have no finite scale: 0 x that would be NaN)
+                const float vr = vratio(c32, 2 * e);
+                pw[e] = pack_f16x2(p0 != 0.f ? p0 * vr : 0.f, p1 != 0.f ? p1 * vr : 0.f);
+              } else {
+                pw[e] = pack_bf16x2(p0, p1);
+              }
+            }
+            tc_st16(t_s + 16 * c32, pw);
+          }
+          l += ps0 + ps1;
+        }
+        // O_i of the steps before, rarely (quiescent: PV_i of the step before
+        // was done before this S_i, the next waits for p_full)
+        if (k > 0 && !warp_dead && __any_sync(kFull, grow || vgrow)) {
+#pragma unroll 1
+          for (int oc = 0; oc < D; oc += 32) {
+            uint32_t ov[32];
+            tc_ld32(t_o + 128u * i + oc, ov);
+            tc_wait_ld_regs(ov);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float a, b2;
+              fmul2(a, b2, __uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), factor, factor);
+              ov[e] = __float_as_uint(a);
+              ov[e + 1] = __float_as_uint(b2);
+            }
+            tc_st32(t_o + 128u * i + oc, ov);
+          }
+        }
+        // V rows of tokens outside the sequence or of a bad page may hold
+        // anything, and nodes' V rows that are not finite would reach every
+        // row, while P is 0 there: once V has landed, thread r clears row r (a
+        // pair's streams write the same zeros)
+        if (nvs < kTreeTokens || badw != 0 || (bad0 | bad1) != 0ull) {
+          if (!warp_wait(&v_full[g % VS], (g / VS) & 1u)) {
+            ok = false;
+            break;
+          }
+          if (r >= nvs || ((badw >> (8 * (r / BS))) & 0xffu) || (((r < 64 ? bad0 : bad1) >> (r & 63)) & 1ull)) {
+            uint8_t* vb = sm + L::kV + (g % VS) * L::kTile + r * 128;
+#pragma unroll
+            for (int cc = 0; cc < 8; ++cc)
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h) *reinterpret_cast<uint4*>(vb + h * L::kRegion + 16 * cc) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();  // read by the tensor cores
+          __syncwarp();
+        }
+        tc_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[i]);
+      }
+      if (!ok) break;
+
+      // the unit's output: O / l as bf16, or a partial (m, l, O)
+      if (PAIR) {
+        if (!warp_wait(&o_full[i], iu & 1u)) ok = false;
+      } else {
+        // both streams' last products; their completion also means that the
+        // (m, l) exchanged for the unit before have been read
+        if (!warp_wait(&o_full[0], iu & 1u)) ok = false;
+        if (ok && n > 1 && !warp_wait(&o_full[1], units1 & 1u)) ok = false;
+        if (n > 1) ++units1;
+      }
+      if (!ok) break;
+      // a row that attends to a node with a non-finite V row is NaN in every
+      // column, also those that the other stream's warps write: through its sum
+      if (row_state == kTreeRowNan) l = tree_row_value(kTreeRowNan);
+      if (row_state == kTreeRowZero) {  // whatever its query held
+        m = -INFINITY;
+        l = 0.f;
+      }
+      float f0 = kOneByte ? vref : 1.f, f1 = 0.f;
+      if constexpr (!PAIR) {
+        float2* xml = reinterpret_cast<float2*>(sm + L::kXml);
+        float* xv = reinterpret_cast<float*>(xml + 2 * kTaRows);
+        xml[i * kTaRows + r] = make_float2(m, l);
+        if (kOneByte && r == 0) xv[i] = vref;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x_full);
+        if (!warp_wait(x_full, iu & 1u)) {
+          ok = false;
+          break;
+        }
+        const float2 other = xml[(1 - i) * kTaRows + r];
+        const float m0 = i == 0 ? m : other.x, m1 = i == 0 ? other.x : m;
+        const float l0 = i == 0 ? l : other.y, l1 = i == 0 ? other.y : l;
+        m = fmaxf(m0, m1);
+        f0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - m);
+        f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m);
+        l = f0 * l0 + f1 * l1;
+        if constexpr (kOneByte) {  // O_i is in units of its stream's vref
+          f0 *= xv[0];
+          f1 *= xv[1];
+        }
+      }
+      tc_fence_after_sync();
+      if (!warp_dead) {
+        const int h = kvh * p.G + (r - tl * p.G);
+        const size_t qrow = static_cast<size_t>(b * p.T + t) * p.Hq + h;
+        const size_t prow_o = (static_cast<size_t>(blockIdx.x) * 2 + (part - 1)) * (L::kQTiles * kTaRows) + (PAIR ? i * kTaRows : 0) + r;
+        if (part == 0) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          f0 *= inv;
+          f1 *= inv;
+        }
+        const int c0 = PAIR ? 0 : i * (D / 2), c1 = PAIR ? D : c0 + D / 2;
+#pragma unroll 1
+        for (int cc = c0; cc < c1; cc += 32) {
+          uint32_t ov[32];
+          tc_ld32(t_o + (PAIR ? 128u * i : 0u) + cc, ov);
+          tc_wait_ld_regs(ov);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f0);
+          if (!PAIR && n > 1) {
+            uint32_t o1[32];
+            tc_ld32(t_o + 128u + cc, o1);
+            tc_wait_ld_regs(o1);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(ov[e])));
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = row_state == kTreeRowZero ? 0u : ov[e];
+          if (in_tile) {
+            if (part == 0) {
+              uint4* dst = reinterpret_cast<uint4*>(p.out + qrow * D + cc);
+#pragma unroll
+              for (int c8 = 0; c8 < 4; ++c8) {
+                const float* f = reinterpret_cast<const float*>(ov + 8 * c8);
+                dst[c8] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+              }
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow_o * D + cc);
+#pragma unroll
+              for (int c4 = 0; c4 < 8; ++c4) dst[c4] = make_uint4(ov[4 * c4], ov[4 * c4 + 1], ov[4 * c4 + 2], ov[4 * c4 + 3]);
+            }
+          }
+          __syncwarp();  // the next TMEM load is warp-collective
+        }
+        if (in_tile && part != 0 && (PAIR || i == 0)) p.part_ml[prow_o] = make_float2(m, l);
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&o_free[i]);
+        if (!PAIR) mbar_arrive(&o_free[1 - i]);
+      }
+      g0 += static_cast<uint32_t>(n);
+    }
+    if (!ok) timed_out = true;
+  }
+
+  timed_out = __syncthreads_or(timed_out) != 0;  // every role has left its loop
+  if (timed_out) {
+    if (tid == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+    // each role lets its own copies and products still in flight finish
+    // (bounded) before the shared and tensor memory are released
+    if (warp == 9 && lane == 0)
+      for (uint32_t g = k_issued > KS ? k_issued - KS : 0; g < k_issued; ++g)
+        mbar_wait_bounded(kI8 ? &tma_k[g % KS] : &k_full[g % KS], (g / KS) & 1u, kWaitLimitNs / 16);
+    if (warp == 10 && lane == 0) {
+      for (uint32_t g = v_issued > VS ? v_issued - VS : 0; g < v_issued; ++g)
+        mbar_wait_bounded(kOneByte ? &tma_v[g % VS] : &v_full[g % VS], (g / VS) & 1u, kWaitLimitNs / 16);
+    }
+    if (warp == 11 && lane == 0 && q_loads > 0) mbar_wait_bounded(q_full, (q_loads - 1) & 1u, kWaitLimitNs / 16);
+    if (warp == 8 && lane == 0 && mma_issued > 0) {  // one commit covers every product issued
+      tc_commit(mma_drain);
+      mbar_wait_bounded(mma_drain, 0, kWaitLimitNs / 16);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tc_dealloc(tmem, kTaCols);
+}
+
+}  // namespace pkv

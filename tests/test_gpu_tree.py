@@ -97,6 +97,59 @@ def test_ragged_counts_and_any_bits(D, Hq, Hkv, T, dtype, math):
         assert (out[3, T - 1:] == 0).all() and (out[4, 7:] == 0).all()
 
 
+@pytest.mark.parametrize("T,dtype,D,lens", [
+    (24, "bf16", 128, [5000, 1, 24, 130, 0, 3000, 700]), (24, "fp8", 128, [129, 6000, 24, 2000]), (30, "int8a", 128, [6000, 31, 128, 999]),
+    (70, "bf16", 128, [4100, 70, 90, 1500]), (24, "bf16", 64, [24, 25, 7000, 128, 129]), (70, "fp8", 128, [2100, 70, 300]),
+    (60, "int8", 128, [60, 1900, 300]), (24, "bf16", 128, [16000])])
+@pytest.mark.parametrize("share", [0, 24, 250])
+def test_shares_of_uneven_lengths(T, dtype, D, lens, share):
+    # shares start and end anywhere in the items, short items among long ones;
+    # share: fewest blocks of a share (0: one step; 250: few CTAs, whole items)
+    c = random_case(7400 + T + D + len(lens), len(lens), 12, 3, D, 16, lens, kv_dtype=dtype)
+    dc = DeviceCase(c)
+    nodes = np.minimum(np.array(lens), T).astype(np.int32)
+    q = normal_bf16_bits(7401, (c.B, T, 12, D))
+    see, _ = _trees(7402, c.B, T, nodes)
+    opts = pkv.decode_opts(partition_blocks=share, math=pkv.MATH_TC)
+    out = _attend(dc, q, see, nodes, opts=opts)
+    assert pkv.read_device_error() == 0
+    assert_tree_close(bf16_dev_to_f64(out), *_reference(dc, q, see, nodes), f"share {share}")
+    again = _attend(dc, q, see, nodes, opts=opts)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", ["fp8", "int8a"])
+@pytest.mark.parametrize("order", ["up", "down", "mixed", "zero first"])
+def test_page_scales_over_three_decades(dtype, order):
+    # V page scales that grow, fall or jump along the sequence, and pages of zeros before the first others
+    T, lens = 24, [900, 333]
+    c = random_case(7450, 2, 16, 4, 128, 16, lens, kv_dtype=dtype)
+    rng = np.random.Generator(np.random.PCG64(7451))
+    for b, n in enumerate(lens):
+        pages = c.block_tables[b, :-(-n // 16)]
+        f = 10.0 ** rng.uniform(-3, 0, len(pages))
+        f = np.sort(f) if order == "up" else np.sort(f)[::-1] if order == "down" else f
+        f = np.where(np.arange(len(pages)) < 9, 0.0, f) if order == "zero first" else f
+        scale = c.v_scale[0, pages] if dtype == "fp8" else c.v_scale[0, pages][..., 0]
+        new = (scale * f[:, None]).astype(np.float32)
+        if dtype == "fp8":
+            c.v_scale[0, pages] = new
+        else:
+            c.v_scale[0, pages, :, 0] = new
+    stored = [c.k_scale.copy(), c.v_scale.copy()]
+    c.v_scale = np.where(c.v_scale == 0, np.float32(1), c.v_scale) if dtype == "fp8" else c.v_scale
+    if dtype == "int8a":
+        c.v_scale[..., 0] = np.where(c.v_scale[..., 0] == 0, np.float32(1), c.v_scale[..., 0])
+    dc = DeviceCase(c)
+    c.v_scale = stored[1]
+    dc.vs = to_dev(c.v_scale)
+    q = normal_bf16_bits(7452, (2, T, 16, 128))
+    see, nodes = _trees(7453, 2, T)
+    for share in (0, 1000):
+        out = _attend(dc, q, see, nodes, opts=pkv.decode_opts(partition_blocks=min(share, 256), math=pkv.MATH_TC))
+        assert_tree_close(bf16_dev_to_f64(out), *_reference(dc, q, see, nodes), f"{order} {share}")
+
+
 @pytest.mark.parametrize("dtype,T,math", [("bf16", 6, pkv.MATH_MMA), ("bf16", 20, pkv.MATH_TC), ("bf16", 60, pkv.MATH_TC), ("fp8", 20, pkv.MATH_TC)])
 def test_fewer_tokens_than_nodes(dtype, T, math):
     # nodes before position 0 do not exist; the others are attended to as the mask says
@@ -115,7 +168,7 @@ def test_fewer_tokens_than_nodes(dtype, T, math):
     (64, 8, 8, 20, "bf16", pkv.MATH_MMA), (128, 32, 8, 24, "fp8", pkv.MATH_TC), (128, 32, 8, 3, "fp8", pkv.MATH_MMA),
     (128, 32, 8, 24, "int8a", pkv.MATH_TC)])
 @pytest.mark.parametrize("ppu", [0, 3])
-def test_chain_gives_the_causal_bits(D, Hq, Hkv, T, dtype, math, ppu):
+def test_chain_gives_the_causal_result(D, Hq, Hkv, T, dtype, math, ppu):
     lens = [T, T + 5, 300, 1000]
     c = random_case(7700 + T + D, 4, Hq, Hkv, D, 16, lens, kv_dtype=dtype)
     dc = DeviceCase(c)
@@ -126,7 +179,11 @@ def test_chain_gives_the_causal_bits(D, Hq, Hkv, T, dtype, math, ppu):
     multi = pkv.paged_decode_multi(to_dev_bf16(q), dc.k, dc.v, dc.bt, dc.cl, c.kv_group_ptr.tolist(), 0, c.scale,
                                    k_scale=dc.ks, v_scale=dc.vs, opts=opts)
     torch.cuda.synchronize()
-    assert torch.equal(tree.view(torch.int16), multi.view(torch.int16))
+    if pkv.decode_plan(dc.k, 4, Hq, c.MB, opts, T, tree=True)["math"] == pkv.MATH_MMA:  # the same tiles and partitions
+        assert torch.equal(tree.view(torch.int16), multi.view(torch.int16))
+    ref = _reference(dc, q, see, np.full(4, T))
+    assert_tree_close(bf16_dev_to_f64(tree), *ref, "tree")
+    assert_tree_close(bf16_dev_to_f64(multi), *ref, "causal")
 
 
 @pytest.mark.parametrize("T", [3, 20, 60])

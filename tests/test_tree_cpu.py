@@ -45,12 +45,27 @@ def test_tree_plans(lib):
     assert _plan(lib, _desc(), 8, 1, 32, 64, pkv.decode_opts(math=pkv.MATH_FFMA))[0] == 2
     assert _plan(lib, _desc(), 8, 0, 32, 64)[0] == 1
     assert _plan(lib, _desc(), 8, pkv.MAX_QUERY_TOKENS + 1, 32, 64)[0] == 1
-    # the workspace adds a word of 32 nodes per (sequence, KV head)
+    # mma.sync: the workspace adds a word of 32 nodes per (sequence, KV head)
     d = _desc()
-    multi = lib.pkv_decode_multi_workspace_bytes(ctypes.byref(d), 64, 33, 32, 64, None)
-    tree = lib.pkv_decode_tree_workspace_bytes(ctypes.byref(d), 64, 33, 32, 64, None)
+    mma = pkv.decode_opts(math=pkv.MATH_MMA)
+    multi = lib.pkv_decode_multi_workspace_bytes(ctypes.byref(d), 64, 33, 32, 64, ctypes.byref(mma))
+    tree = lib.pkv_decode_tree_workspace_bytes(ctypes.byref(d), 64, 33, 32, 64, ctypes.byref(mma))
     assert tree == multi + 64 * 8 * 2 * 4
     assert lib.pkv_decode_tree_workspace_bytes(ctypes.byref(d), 64, 0, 32, 64, None) == 0
+
+
+@pytest.mark.parametrize("dtype,D", [(0, 128), (0, 64), (1, 128), (2, 128)])
+@pytest.mark.parametrize("T", [9, 32, 33, 512])
+def test_tcgen05_tree_plans(lib, dtype, D, T):
+    st, plan = _plan(lib, _desc(dtype=dtype, head_dim=D), 8, T, 32, 64)
+    assert st == 0 and plan.math == pkv.MATH_TC and plan.kernels_per_call == (3 if T <= 512 else 2)
+    assert plan.smem_bytes_per_cta <= 227 * 1024 and plan.warps_per_cta == (12 if dtype == 0 else 16)
+    assert plan.row_tiles == -(-T // min(T, 32))
+    # partials: at most two per CTA, whatever the lengths
+    rows = 128 if plan.row_tiles == 1 else 256
+    assert plan.workspace_bytes < 152 * 2 * rows * (D + 2) * 4 + (1 << 20)
+    st, longer = _plan(lib, _desc(dtype=dtype, head_dim=D, num_blocks=100000), 8, T, 32, 8192)
+    assert st == 0 and longer.workspace_bytes == plan.workspace_bytes
 
 
 def _attend(lib, **kw):
@@ -67,7 +82,7 @@ def _attend(lib, **kw):
     (dict(mask=None), 1), (dict(TB=3), 1), (dict(TB=0), 1), (dict(T=0), 1), (dict(T=513), 1), (dict(Hq=12), 1), (dict(q=None), 1),
     (dict(mask=ctypes.c_void_p(0x600002)), 3), (dict(nodes=ctypes.c_void_p(0x600001)), 3), (dict(out=_p(1)), 1), (dict(ws=None), 6),
     (dict(wsb=64), 6), (dict(scale=float("inf")), 1), (dict(layer=1), 1), (dict(desc=_desc(head_dim=64, dtype=1)), 2),
-    (dict(desc=_desc(head_dim=64, num_kv_heads=1)), 2),  # 32 heads on one 64-wide KV head
+    (dict(desc=_desc(num_kv_heads=1), Hq=129), 2),       # 129 heads on one KV head
     (dict(desc=_desc(dtype=1)), 1)])                     # E4M3 without scales
 def test_attention_refusals(lib, bad, status):
     assert _attend(lib, **bad) == status
