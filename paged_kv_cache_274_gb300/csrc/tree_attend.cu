@@ -13,6 +13,7 @@ namespace pkv {
 // planner
 // ---------------------------------------------------------------------------
 constexpr int kTreePlanThreads = 1024;
+constexpr int kTreeItemSteps = 2;    // cost of an item besides its steps, in steps
 constexpr int kTreePlanSmem = 2048;  // sequences whose prefix sums are searched in shared memory
 
 struct TreePlanArgs {
@@ -25,14 +26,17 @@ struct TreePlanArgs {
   __nv_bfloat16* out;
   unsigned* err;
   int B, T, Hkv, max_ctx, row_elems /* T * Hq * D */;
-  int max_shares, min_steps;
+  int max_shares, min_steps, item_steps;
 };
 
 // CTA 0: lengths, the prefix sums of the sequences' steps, the shares'
 // boundaries, zeros for inactive sequences.  Other CTAs: tree_scan_values.
 //
-// A boundary within `near` steps of an item's start or end moves there: the
-// partial it would leave costs more than the imbalance.
+// Shares are equal in cost: an item's steps plus item_steps for its start and
+// output (measured: a batch of short and long sequences left SMs idle for half
+// the time with shares equal in steps).  A boundary within `near` steps of an
+// item's start or end moves there: the partial it would leave costs more than
+// the imbalance.
 __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreePlanArgs a, const TreeScan scan) {
   pdl_trigger();
   pdl_wait();
@@ -64,7 +68,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
       }
       if (nodes == 0) c = 0;  // every row is zero
       a.ctx_eff[b] = c;
-      steps = static_cast<long long>((c + kTreeTokens - 1) / kTreeTokens) * a.Hkv;
+      steps = c == 0 ? 0 : static_cast<long long>((c + kTreeTokens - 1) / kTreeTokens + a.item_steps) * a.Hkv;
     }
     long long x = steps;
 #pragma unroll
@@ -104,27 +108,26 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
   // shares of at least min_steps steps
   const int shares = static_cast<int>(min(static_cast<long long>(a.max_shares), (total + a.min_steps - 1) / a.min_steps));
   if (tid == 0) *a.shares = shares;
-  const long long near = shares > 0 ? min(2ll, total / shares / 4) : 0;
+  const int near = shares > 0 ? static_cast<int>(min(2ll, total / shares / 4)) : 0;
   for (int s = tid; s <= shares; s += kTreePlanThreads) {
-    TreeBound r{shares > 0 ? total * s / shares : 0, a.B, 0, 0, 0};
+    TreeBound r{a.B, 0, 0, 0};
     if (s < shares) {
+      const long long pos = total * s / shares;
       int lo = 0, hi = a.B - 1;  // the sequence with start[lo] <= pos < start[lo + 1]
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (start[mid + 1] > r.pos) hi = mid; else lo = mid + 1;
+        if (start[mid + 1] > pos) hi = mid; else lo = mid + 1;
       }
-      const long long in = r.pos - start[lo];
-      const int nt = static_cast<int>((start[lo + 1] - start[lo]) / a.Hkv);
+      const long long in = pos - start[lo];
+      const int cost = static_cast<int>((start[lo + 1] - start[lo]) / a.Hkv), nt = cost - a.item_steps;
       r.b = lo;
-      r.kvh = static_cast<int>(in / nt);
-      r.step = static_cast<int>(in - static_cast<long long>(r.kvh) * nt);
-      if (r.step > 0 && r.step <= near) {
-        r.pos -= r.step;
+      r.kvh = static_cast<int>(in / cost);
+      r.step = max(0, static_cast<int>(in - static_cast<long long>(r.kvh) * cost) - a.item_steps);
+      if (r.step <= near) {
         r.step = 0;
-      } else if (r.step > 0 && nt - r.step <= near) {
-        r.pos += nt - r.step;
+      } else if (nt - r.step <= near) {
         r.step = 0;
-        if (++r.kvh == a.Hkv) {  // (the next sequences may be inactive: whoever starts here skips them)
+        if (++r.kvh == a.Hkv) {  // (the next sequences may be inactive: whoever starts there skips them)
           r.kvh = 0;
           ++r.b;
         }
@@ -151,7 +154,6 @@ constexpr int kTreeMergeThreads = 256;
 constexpr int kTreeMergeSplit = 4;
 
 struct TreeMergeArgs {
-  const int32_t* ctx_eff;
   const TreeBound* bounds;
   const int32_t* shares;
   const float2* part_ml;
@@ -172,16 +174,18 @@ __global__ void __launch_bounds__(kTreeMergeThreads) tree_merge_kernel(const Tre
   if (share + 1 >= shares) return;  // the last share splits nothing
   const TreeBound next = a.bounds[share + 1];
   if (next.step == 0) return;  // an item starts there
-  const long long item = next.pos - next.step;
   const TreeBound mine = a.bounds[share];
-  if (item < mine.pos) return;  // the item started in an earlier share
-  const long long item_end = item + (a.ctx_eff[next.b] + kTreeTokens - 1) / kTreeTokens;
-  int last = share + 1;  // the share that ends the item
-  while (a.bounds[last + 1].pos < item_end) ++last;
+  const bool same = mine.b == next.b && mine.kvh == next.kvh;
+  if (same && mine.step > 0) return;  // the item started in an earlier share
+  int last = share + 1;               // the share that ends the item
+  for (; last + 1 < shares; ++last) {
+    const TreeBound e = a.bounds[last + 1];
+    if (e.b != next.b || e.kvh != next.kvh || e.step == 0) break;
+  }
   const int parts = last - share + 1;
   const int rows = a.tiles * kTaRows;
   // the owner's partial is its first unit's place if the share starts with the item
-  const size_t first = (static_cast<size_t>(cta) * 2 + (item == mine.pos ? 0 : 1)) * rows;
+  const size_t first = (static_cast<size_t>(cta) * 2 + (same ? 0 : 1)) * rows;
   const size_t stride = static_cast<size_t>(a.NP) * 2 * rows;  // from a share's partials to the next one's
   const size_t cont = (static_cast<size_t>(cta) * 2) * rows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -320,7 +324,7 @@ cudaError_t launch_tree_attend(const DecodeLaunch& L, uint8_t* ws, int* launched
   // 1. planner
   TreePlanArgs pa{L.context_lens, L.node_counts, ctx_eff, reinterpret_cast<long long*>(ws + w.start), bounds, shares,
                   static_cast<__nv_bfloat16*>(L.out), L.err, L.B, L.T, L.Hkv, L.MB * L.bs, L.T * L.Hq * L.D,
-                  L.tree_shares, L.tree_min_steps};
+                  L.tree_shares, L.tree_min_steps, kTreeItemSteps};
   const TreeScan scan = tree_scan_of(L, poison);
   cfg.gridDim = dim3(1 + tree_scan_ctas(L, kTreePlanThreads / 32));
   cfg.blockDim = dim3(kTreePlanThreads);
@@ -371,7 +375,7 @@ cudaError_t launch_tree_attend(const DecodeLaunch& L, uint8_t* ws, int* launched
 
   // 3. merge of the items that shares split
   if (L.tree_shares > 1) {
-    const TreeMergeArgs ma{ctx_eff, bounds, shares, p.part_ml, p.part_o, p.out, L.Hq, L.G, L.T, L.Tt, NP, pair ? 2 : 1};
+    const TreeMergeArgs ma{bounds, shares, p.part_ml, p.part_o, p.out, L.Hq, L.G, L.T, L.Tt, NP, pair ? 2 : 1};
     cfg.gridDim = dim3(static_cast<unsigned>((L.tree_shares - 1) * NP * kTreeMergeSplit));
     cfg.blockDim = dim3(kTreeMergeThreads);
     cfg.dynamicSmemBytes = 0;

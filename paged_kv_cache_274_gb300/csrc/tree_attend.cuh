@@ -87,9 +87,12 @@ struct TaStep {
   int ctx;
   int pages[8];
   uint8_t bad[8];   // page id out of range
-  float vmax;       // one-byte caches: largest |v scale| of the step's pages
-  int pad;
-  float4 par[8];    // one-byte caches: k scale, k zero, v scale, v zero per page
+  int plain;        // every k scale >= 0 and every v scale > 0 (and finite)
+  float vref;       // one-byte caches: P carries v scale / vref
+  // one-byte caches, per page: k scale, INT8 K bias 1152 + zero, v scale /
+  // vref and its log2
+  float4 par[8];
+  float vzero[8];   // INT8: V zero point
 };
 
 __host__ __device__ constexpr int ta_threads(int kv) { return kv == PKV_KV_BF16 ? 384 : 512; }
@@ -131,6 +134,43 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, ui
       "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u));
+}
+
+// Largest of 16 scores (bit patterns of floats) from x[o] on.
+__device__ __forceinline__ float max16(const uint32_t (&x)[32], int o) {
+  auto f = [&](int i) { return __uint_as_float(x[o + i]); };
+  const float a = fmax3f(f(0), f(1), f(2)), b = fmax3f(f(3), f(4), f(5)), c = fmax3f(f(6), f(7), f(8));
+  const float d = fmax3f(f(9), f(10), f(11)), e = fmax3f(f(12), f(13), f(14));
+  return fmax3f(fmax3f(a, b, c), fmax3f(d, e, f(15)), a);
+}
+
+// Rewrite 32 token rows (one per lane) of a stage whose one-byte codes lie in
+// the upper half (row r's 128 codes at region + 128 r) as 16-bit code values
+// in both halves (16-byte chunks XOR-swizzled by row % 8), as widen_stage does,
+// in loops: with everything unrolled the kernel's hot code no longer fits the
+// instruction cache.  Codes 0-63 go to the lower half, which holds no codes;
+// codes 64-127 are read before any chunk of the upper half is written.
+template <int KV, bool kBiased>
+__device__ __forceinline__ void widen_rows(uint8_t* stage, uint32_t region, int lane, uint32_t zc, int valid_rows) {
+  if (lane >= valid_rows) return;
+  const int sw = lane & 7;
+  uint8_t* hi = stage + region + lane * 128;
+  uint8_t* lo = stage + lane * 128;
+  uint4 o0, o1, x[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) x[c] = *reinterpret_cast<const uint4*>(hi + (((c + 4) ^ sw) << 4));
+#pragma unroll 2
+  for (int c = 0; c < 4; ++c) {
+    widen16<KV, kBiased>(*reinterpret_cast<const uint4*>(hi + ((c ^ sw) << 4)), zc, o0, o1);
+    *reinterpret_cast<uint4*>(lo + (((2 * c) ^ sw) << 4)) = o0;
+    *reinterpret_cast<uint4*>(lo + (((2 * c + 1) ^ sw) << 4)) = o1;
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    widen16<KV, kBiased>(x[c], zc, o0, o1);
+    *reinterpret_cast<uint4*>(hi + (((2 * c) ^ sw) << 4)) = o0;
+    *reinterpret_cast<uint4*>(hi + (((2 * c + 1) ^ sw) << 4)) = o1;
+  }
 }
 
 template <int D, int BS, int KV, bool PAIR>
@@ -226,28 +266,27 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
   if (warp == 9) {
     // K copy warp: the share's units, a descriptor and the K pages per step
     uint32_t g = 0;
-    int b = 0, kvh = 0, j0 = 0;
-    long long pos = 0, end = 0;
+    TreeBound at{0, 0, 0, 0}, end{0, 0, 0, 0};
     if (share < __ldg(p.shares)) {
-      pos = p.bounds[share].pos;
-      end = p.bounds[share + 1].pos;
-      b = p.bounds[share].b;
-      kvh = p.bounds[share].kvh;
-      j0 = p.bounds[share].step;
+      at = p.bounds[share];
+      end = p.bounds[share + 1];
     }
+    int b = at.b, kvh = at.kvh, j0 = at.step;
     const uint64_t policy = p.NP > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
     bool first_unit = true;
-    while (pos < end && !timed_out) {
+    float vref = 0.f;
+    while (!timed_out && (b < end.b || (b == end.b && (kvh < end.kvh || (kvh == end.kvh && j0 < end.step))))) {
       const int ctx = __ldg(p.ctx_eff + b);
       const int nt = (ctx + kTreeTokens - 1) / kTreeTokens;
       if (nt == 0) {  // an inactive sequence
         ++b;
         continue;
       }
-      const int n = static_cast<int>(min(static_cast<long long>(nt - j0), end - pos));
+      const int n = (b == end.b && kvh == end.kvh ? end.step : nt) - j0;
       const int t0 = j0 * kTreeTokens, t1 = min(ctx, (j0 + n) * kTreeTokens);
       const int part = (j0 == 0 && n == nt) ? 0 : (first_unit ? 1 : 2);
       first_unit = false;
+      vref = 0.f;  // of the unit; 0: no page with a scale yet
       const int npages = (t1 - t0 + BS - 1) / BS;
       const int* trow = p.block_tables + static_cast<size_t>(b) * p.MB + t0 / BS;
       // lane i holds page i of a run of 32 pages, and of the next run
@@ -288,16 +327,25 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         const bool mine = q >= 0 && q < np;
         const bool bad = mine && static_cast<unsigned>(id) >= static_cast<unsigned>(p.NB);
         const int phys = bad ? 0 : id;
+        bool plain = true;
+        if constexpr (kOneByte) {
+          // vref moves when a step's v scales are more than 2^6 above it, so
+          // that P, below 2^8, stays below 2^14 in f16
+          const float vm = __uint_as_float(__reduce_max_sync(kFull, mine ? __float_as_uint(fabsf(par.z)) : 0u));
+          if (vm > 64.f * vref) vref = vm;
+          const float ratio = mine && vref > 0.f ? par.z / vref : 0.f;
+          plain = __all_sync(kFull, !mine || (par.x >= 0.f && par.x < INFINITY && par.z > 0.f && par.z < INFINITY));
+          if (q >= 0 && q < PPI) {
+            const_cast<TaStep*>(step_at(g))->par[q] =
+                make_float4(mine ? par.x : 0.f, kInt8Bias + (mine ? par.y : 0.f), ratio, mine ? __log2f(ratio) : 0.f);
+            st->vzero[q] = mine ? par.w : 0.f;
+          }
+        }
         if (q >= 0 && q < PPI) {
           st->pages[q] = phys;
           st->bad[q] = bad ? 1 : 0;
-          if constexpr (kOneByte) *reinterpret_cast<float4*>(const_cast<float4*>(&st->par[q])) = mine ? par : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         if (bad) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
-        if constexpr (kOneByte) {
-          const uint32_t vm = __reduce_max_sync(kFull, mine ? __float_as_uint(fabsf(par.z)) : 0u);
-          if (lane == 0) st->vmax = __uint_as_float(vm);
-        }
         if (lane == 0) {
           st->n = n;
           st->b = b;
@@ -307,6 +355,8 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           st->part = part;
           st->np = np;
           st->ctx = ctx;
+          st->plain = plain ? 1 : 0;
+          st->vref = vref;
         }
         uint8_t* dst = sm + L::kK + (g % KS) * L::kKTile;
         uint64_t* bar = kI8 ? &tma_k[g % KS] : &k_full[g % KS];
@@ -327,7 +377,6 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         }
         k_issued = g + 1;
       }
-      pos += n;
       j0 = 0;
       if (++kvh == p.Hkv) {
         kvh = 0;
@@ -406,22 +455,26 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
                                               : tc_idesc_bf16_f32(kTaRows, kTreeTokens);
       constexpr uint32_t kIdescO = kOneByte ? tc_idesc_f16_f32(kTaRows, D, /*b_mn_major=*/true)
                                             : tc_idesc_bf16_f32(kTaRows, D, /*b_mn_major=*/true);
-      const uint32_t q_addr = smem_addr(sm + L::kQ), k_addr = smem_addr(sm + L::kK), v_addr = smem_addr(sm + L::kV);
+      // operand descriptors of stage 0; a later stage or slice adds its byte
+      // offset / 16 to the start-address field
+      const uint64_t q_desc = tc_smem_desc(smem_addr(sm + L::kQ), 16, 1024, 2);
+      const uint64_t k_desc = tc_smem_desc(smem_addr(sm + L::kK), 16, 1024, 2);
+      const uint64_t v_desc = tc_smem_desc(smem_addr(sm + L::kV), L::kRegion, 1024, 2);
       // S_i = Q . K^T; A and B K-major with the 128-byte swizzle, 32 bytes of
-      // each row per product
-      auto issue_s = [&](int i, uint32_t g) {
-        const uint32_t qa = q_addr + (PAIR ? i : 0) * L::kTile;
-        const uint32_t ka = k_addr + (g % KS) * L::kKTile;
-        if constexpr (kF8K) {  // both parts of the query against the same codes
+      // each row per product.  (Loops of two products: the issuing thread's
+      // code is fetched anew each step, between the softmax warps'.)
+      auto issue_s = [&](int i, uint32_t stage) {
+        const uint64_t qd = q_desc + (PAIR ? i * (L::kTile >> 4) : 0u), kd = k_desc + stage * (L::kKTile >> 4);
+        constexpr int kParts = kF8K ? 2 : kHalves;  // regions of the query: E4M3 both parts against the same codes
+#pragma unroll 1
+        for (int h = 0; h < kParts; ++h) {
+          const uint64_t qh = qd + h * (L::kRegion >> 4), kh = kd + (kF8K ? 0u : h * (L::kRegion >> 4));
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc_mma_e4m3(tmem + 128u * i, tc_smem_desc(qa + (kk >> 2) * L::kRegion + (kk & 3) * 32, 16, 1024, 2),
-                        tc_smem_desc(ka + (kk & 3) * 32, 16, 1024, 2), kIdescS, kk > 0);
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * L::kRegion + (kk & 3) * 32;
-            tc_mma_bf16(tmem + 128u * i, tc_smem_desc(qa + off, 16, 1024, 2), tc_smem_desc(ka + off, 16, 1024, 2), kIdescS, kk > 0);
+          for (int kk = 0; kk < 4; ++kk) {
+            if constexpr (kF8K)
+              tc_mma_e4m3(tmem + 128u * i, qh + 2 * kk, kh + 2 * kk, kIdescS, h > 0 || kk > 0);
+            else
+              tc_mma_bf16(tmem + 128u * i, qh + 2 * kk, kh + 2 * kk, kIdescS, h > 0 || kk > 0);
           }
         }
         ++mma_issued;
@@ -430,19 +483,28 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       // S_i, V MN-major as the pages hold it (64-d halves kRegion apart,
       // 8-token groups 1024 B apart)
       uint32_t pc[2] = {0, 0};  // P tiles taken, per stream
-      auto issue_pv = [&](int i, uint32_t g, bool first, uint32_t iu) -> bool {
+      uint32_t ks = 0, kph = 0, vs = 0, vph = 0;  // stage and phase of the next K and V
+      auto issue_pv = [&](int i, bool first, uint32_t iu) -> bool {
         if (!mbar_wait_fast(&p_full[i], pc[i] & 1u, kWaitLimitNs)) return false;
         ++pc[i];
-        if ((!PAIR || i == 0) && !mbar_wait_fast(&v_full[g % VS], (g / VS) & 1u, kWaitLimitNs)) return false;
+        if ((!PAIR || i == 0) && !mbar_wait_fast(&v_full[vs], vph, kWaitLimitNs)) return false;
         if (first && iu > 0 && !mbar_wait_fast(&o_free[i], (iu - 1) & 1u, kWaitLimitNs)) return false;
         tc_fence_after_sync();
-        const uint32_t va = v_addr + (g % VS) * L::kTile;
+        const uint64_t vd = v_desc + vs * (L::kTile >> 4);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int kk = 0; kk < kTreeTokens / 16; ++kk)
-          tc_mma_bf16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk, tc_smem_desc(va + kk * 2048, L::kRegion, 1024, 2), kIdescO,
-                         !first || kk > 0);
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_bf16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 32u * h + 8u * kk, vd + (h * 4 + kk) * (2048 >> 4), kIdescO,
+                           !first || h > 0 || kk > 0);
         ++mma_issued;
-        if (!PAIR || i == 1) tc_commit(&v_free[g % VS]);
+        if (!PAIR || i == 1) {
+          tc_commit(&v_free[vs]);
+          if (++vs == VS) {
+            vs = 0;
+            vph ^= 1u;
+          }
+        }
         return true;
       };
       uint32_t g0 = 0;
@@ -455,15 +517,18 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         const int events = PAIR ? 2 * n : n;
         for (int e = 0; ok && e < events; ++e) {
           const int i = e & 1, k = e >> 1;  // stream, its step
-          const uint32_t g = g0 + (PAIR ? k : e);
-          if (!PAIR || i == 0) {
-            if (!(ok = mbar_wait_fast(&k_full[g % KS], (g / KS) & 1u, kWaitLimitNs))) break;
-            tc_fence_after_sync();
-          }
-          if (k > 0 && !(ok = issue_pv(i, g0 + (PAIR ? k - 1 : e - 2), k == 1, iu))) break;
-          issue_s(i, g);
+          if (k > 0 && !(ok = issue_pv(i, k == 1, iu))) break;
+          if ((!PAIR || i == 0) && !(ok = mbar_wait_fast(&k_full[ks], kph, kWaitLimitNs))) break;
+          tc_fence_after_sync();
+          issue_s(i, ks);
           tc_commit(&s_full[i]);
-          if (!PAIR || i == 1) tc_commit(&k_free[g % KS]);
+          if (!PAIR || i == 1) {
+            tc_commit(&k_free[ks]);
+            if (++ks == KS) {
+              ks = 0;
+              kph ^= 1u;
+            }
+          }
           if (e == events - 1) tc_commit(q_free);
         }
         // the last products of both streams, the earlier step's first
@@ -471,7 +536,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           const int i = (!PAIR && (n & 1)) ? 1 - x : x;
           const int ni = PAIR ? n : (n + 1 - i) / 2;  // the stream's steps
           if (ni == 0) continue;
-          if (!(ok = issue_pv(i, g0 + (PAIR ? n - 1 : 2 * (ni - 1) + i), ni == 1, iu))) break;
+          if (!(ok = issue_pv(i, ni == 1, iu))) break;
           tc_commit(&o_full[i]);
         }
         if (!ok) break;
@@ -494,14 +559,14 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         uint8_t* st = (is_k ? sm + L::kK + (g % KS) * L::kKTile : sm + L::kV + (g % VS) * L::kTile) + cw * 32 * 128;
         const volatile TaStep* sp = step_at(g);
         const int rows = sp->np * BS - 32 * cw;  // of the step's pages
-        uint32_t zc[1] = {0u};
+        uint32_t zc = 0u;
         if (is_k) {
-          widen_stage<KV, 32, kI8>(st, L::kRegion, lane, zc, rows);
+          widen_rows<KV, kI8>(st, L::kRegion, lane, zc, rows);
         } else {
           if constexpr (kI8) {
-            if (lane < rows) zc[0] = int8_zero_const(const_cast<const TaStep*>(sp)->par[(32 * cw + lane) / BS].w);
+            if (lane < rows) zc = int8_zero_const(sp->vzero[(32 * cw + lane) / BS]);
           }
-          widen_stage<KV, 32>(st, L::kRegion, lane, zc, rows);
+          widen_rows<KV, false>(st, L::kRegion, lane, zc, rows);
         }
         fence_proxy_async_smem();  // read by the tensor cores
         __syncwarp();
@@ -641,7 +706,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         prow = (b * p.Hkv + kvh) * p.tree.words;
         row_state = live ? kTreeRowNormal : kTreeRowZero;
       }
-      float cq = c, qsum = 0.f, vref = 1.f, inv_vref = 1.f;
+      float cq = c, qsum = 0.f, vref = 1.f;
       if constexpr (kOneByte) {
         if (!warp_wait(q_full, iu & 1u)) {
           ok = false;
@@ -653,7 +718,6 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(q_read);
       }
-      bool vset = false;
       float m = -INFINITY, l = 0.f;  // log2-domain lazy running maximum and sum of this row
       const int ni = PAIR ? n : (n + 1 - i) / 2;  // this stream's steps
       for (int k = 0; k < ni; ++k, ++steps) {
@@ -680,20 +744,17 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         bool vgrow = false;
         float factor = 1.f;
         if constexpr (kOneByte) {
-          // P carries v_scale / vref: vref moves when a step's scales are more
-          // than 2^6 above it, so that P stays below 2^14
-          const float vm = *reinterpret_cast<const volatile float*>(&st->vmax);
-          if (vm > (vset ? 64.f * vref : 0.f)) {
-            if (vset) {  // (until then every page's scale was 0, and O is)
-              factor = vref / vm;
+          const float vnew = *reinterpret_cast<const volatile float*>(&st->vref);
+          if (vnew != vref) {  // (0 until a page has a scale: O is 0 so far)
+            if (k > 0 && vref != 0.f) {
+              factor = vref / vnew;
               vgrow = true;
             }
-            vset = true;
-            vref = vm;
-            inv_vref = 1.f / vm;
+            vref = vnew;
           }
         }
-        if (!warp_wait(&s_full[i], steps & 1u)) {
+        const bool plain = c >= 0.f && (!kOneByte || *reinterpret_cast<const volatile int*>(&st->plain) != 0);
+        if (!__all_sync(kFull, mbar_wait_bounded(&s_full[i], steps & 1u, kWaitLimitNs))) {
           ok = false;
           break;
         }
@@ -706,7 +767,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             for (int h = 0; h < 32 / BS; ++h) {
               const float4 pr = st->par[(32 * c32) / BS + h];
               const float ck = cq * pr.x;
-              const float add = kI8 ? -(kInt8Bias + pr.y) * qsum * ck : 0.f;  // the biased K codes
+              const float add = kI8 ? -pr.y * qsum * ck : 0.f;  // the biased K codes
 #pragma unroll
               for (int e = 0; e < BS; e += 2) {
                 const int t2 = h * BS + e;
@@ -721,7 +782,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             }
           }
         };
-        auto vratio = [&](int c32, int e) -> float { return kOneByte ? st->par[(32 * c32 + e) / BS].z * inv_vref : 1.f; };
+        auto vratio = [&](int c32, int e) -> float { return kOneByte ? st->par[(32 * c32 + e) / BS].z : 1.f; };
         auto move_max = [&](float smax) {
           grow = (m == -INFINITY) ? (smax != -INFINITY) : (smax > m + 8.f);
           if (grow) {
@@ -732,7 +793,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           }
         };
         if (warp_dead) {
-        } else if (full) {
+        } else if (full && plain) {
           uint32_t x0[32], x1[32], x2[32], x3[32];
           tc_ld32(t_s, x0);
           tc_ld32(t_s + 32, x1);
@@ -742,32 +803,53 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           tc_regs_loaded(x1);
           tc_regs_loaded(x2);
           tc_regs_loaded(x3);
-          scale32(x0, 0);
-          scale32(x1, 1);
-          scale32(x2, 2);
-          scale32(x3, 3);
-          const float ext = cs >= 0.f ? fmaxf(fmaxf(tree_ext32<true>(x0), tree_ext32<true>(x1)), fmaxf(tree_ext32<true>(x2), tree_ext32<true>(x3)))
-                                      : fminf(fminf(tree_ext32<false>(x0), tree_ext32<false>(x1)), fminf(tree_ext32<false>(x2), tree_ext32<false>(x3)));
+          // page coefficients: a score in log2 units is x ck + add, P x v scale
+          // / vref is 2^(score - m + lv)
+          auto page = [&](int c32, int h, float& ck, float& add, float& lv) {
+            const float4 pr = st->par[(32 * c32) / BS + h];
+            ck = cq * pr.x;
+            add = kI8 ? -pr.y * qsum * ck : 0.f;
+            lv = pr.w;
+          };
+          auto ext32 = [&](const uint32_t (&x)[32], int c32) -> float {
+            if constexpr (!kOneByte) {
+              return tree_ext32<true>(x);
+            } else if constexpr (BS == 32) {
+              float ck, add, lv;
+              page(c32, 0, ck, add, lv);
+              return fmaf(tree_ext32<true>(x), ck, add);
+            } else {
+              float ck, add, lv;
+              page(c32, 0, ck, add, lv);
+              const float e0 = fmaf(max16(x, 0), ck, add);
+              page(c32, 1, ck, add, lv);
+              return fmaxf(e0, fmaf(max16(x, 16), ck, add));
+            }
+          };
+          const float ext = fmaxf(fmaxf(ext32(x0, 0), ext32(x1, 1)), fmaxf(ext32(x2, 2), ext32(x3, 3)));
           move_max(ext * cs);
           const float neg_m = (m == -INFINITY) ? 0.f : -m;
-          float ps[2] = {0.f, 0.f};
           auto write_p = [&](const uint32_t (&x)[32], int c32) {
             uint32_t pw[16];
+            float ps[2] = {0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float a0, a1;
-              ffma2(a0, a1, __uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), cs, cs, neg_m, neg_m);
-              const float p0 = ex2_approx(a0);
-              const float p1 = ex2_approx(a1);
-              fadd2(ps[0], ps[1], ps[0], ps[1], p0, p1);
-              if constexpr (kOneByte) {
-                const float vr = vratio(c32, 2 * e);
-                float b0, b1;
-                fmul2(b0, b1, p0, p1, vr, vr);
-                pw[e] = pack_f16x2(b0, b1);
-              } else {
-                pw[e] = pack_bf16x2(p0, p1);
+            for (int h = 0; h < (kOneByte ? 32 / BS : 1); ++h) {
+              constexpr int kRun = kOneByte ? BS : 32;  // scores with the same coefficients
+              float ck = cs, add = 0.f, lv = 0.f;
+              if constexpr (kOneByte) page(c32, h, ck, add, lv);
+              const float b = add + neg_m + lv;
+              if (kOneByte) ps[0] = ps[1] = 0.f;
+#pragma unroll
+              for (int e = 0; e < kRun / 2; ++e) {
+                const int k2 = h * kRun + 2 * e;
+                float a0, a1;
+                ffma2(a0, a1, __uint_as_float(x[k2]), __uint_as_float(x[k2 + 1]), ck, ck, b, b);
+                const float p0 = ex2_approx(a0);
+                const float p1 = ex2_approx(a1);
+                fadd2(ps[0], ps[1], ps[0], ps[1], p0, p1);
+                pw[k2 / 2] = kOneByte ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
               }
+              l = kOneByte ? fmaf(ps[0] + ps[1], ex2_approx(-lv), l) : l + (ps[0] + ps[1]);
             }
             tc_st16(t_s + 16 * c32, pw);
           };
@@ -775,9 +857,9 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           write_p(x1, 1);
           write_p(x2, 2);
           write_p(x3, 3);
-          l += ps[0] + ps[1];
         } else {
-          // a step with masked tokens (the sequence's end, nodes, bad pages):
+          // a step with masked tokens (the sequence's end, nodes, bad pages),
+          // or a negative scale:
           // 32 scores at a time, the masked maximum first, then P (a chunk's P
           // goes over columns whose scores are already read)
           uint64_t rm0 = low_bits64(nvs), rm1 = low_bits64(nvs - 64);

@@ -12,9 +12,8 @@ constexpr int kTreeTokens = 128;  // tokens of a step
 
 // Start of a share of the steps of all (sequence, KV head) items in a row.
 struct TreeBound {
-  long long pos;  // steps before it
-  int b, kvh;     // item
-  int step;       // step of the item (0: the share starts with the item)
+  int b, kvh;  // item (b = batch, kvh = 0: the end)
+  int step;    // step of the item (0: the share starts with the item)
   int pad;
 };
 
