@@ -136,6 +136,25 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, ui
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u));
 }
 
+// Waits for phase `parity` of `bar`; false after about two seconds.  Few
+// instructions, because the kernel has some forty of these: the hardware
+// suspends the thread for up to a microsecond per try.
+constexpr int kTaTries = 1 << 21;
+__device__ __forceinline__ bool ta_wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t addr = smem_addr(bar);
+#pragma unroll 1
+  for (int n = 0; n < kTaTries; ++n) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
+}
+
 // Largest of 16 scores (bit patterns of floats) from x[o] on.
 __device__ __forceinline__ float max16(const uint32_t (&x)[32], int o) {
   auto f = [&](int i) { return __uint_as_float(x[o + i]); };
@@ -254,7 +273,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
   // this warp waits (lane 0, bounded) for phase `parity` of `bar`; false on timeout
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
     int ok = 1;
-    if (lane == 0) ok = mbar_wait_bounded(bar, parity, kWaitLimitNs) ? 1 : 0;
+    if (lane == 0) ok = ta_wait(bar, parity) ? 1 : 0;
     return __shfl_sync(kFull, ok, 0) != 0;
   };
   auto wait_step = [&](uint32_t g) { return warp_wait(&step_full[g % kTaRing], (g / kTaRing) & 1u); };
@@ -485,10 +504,10 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       uint32_t pc[2] = {0, 0};  // P tiles taken, per stream
       uint32_t ks = 0, kph = 0, vs = 0, vph = 0;  // stage and phase of the next K and V
       auto issue_pv = [&](int i, bool first, uint32_t iu) -> bool {
-        if (!mbar_wait_fast(&p_full[i], pc[i] & 1u, kWaitLimitNs)) return false;
+        if (!ta_wait(&p_full[i], pc[i] & 1u)) return false;
         ++pc[i];
-        if ((!PAIR || i == 0) && !mbar_wait_fast(&v_full[vs], vph, kWaitLimitNs)) return false;
-        if (first && iu > 0 && !mbar_wait_fast(&o_free[i], (iu - 1) & 1u, kWaitLimitNs)) return false;
+        if ((!PAIR || i == 0) && !ta_wait(&v_full[vs], vph)) return false;
+        if (first && iu > 0 && !ta_wait(&o_free[i], (iu - 1) & 1u)) return false;
         tc_fence_after_sync();
         const uint64_t vd = v_desc + vs * (L::kTile >> 4);
 #pragma unroll 1
@@ -510,15 +529,15 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       uint32_t g0 = 0;
       bool ok = true;
       for (uint32_t iu = 0;; ++iu) {
-        if (!(ok = mbar_wait_fast(&step_full[g0 % kTaRing], (g0 / kTaRing) & 1u, kWaitLimitNs))) break;
+        if (!(ok = ta_wait(&step_full[g0 % kTaRing], (g0 / kTaRing) & 1u))) break;
         const int n = step_at(g0)->n;
         if (n == 0) break;
-        if (!(ok = mbar_wait_fast(q_full, iu & 1u, kWaitLimitNs))) break;
+        if (!(ok = ta_wait(q_full, iu & 1u))) break;
         const int events = PAIR ? 2 * n : n;
         for (int e = 0; ok && e < events; ++e) {
           const int i = e & 1, k = e >> 1;  // stream, its step
           if (k > 0 && !(ok = issue_pv(i, k == 1, iu))) break;
-          if ((!PAIR || i == 0) && !(ok = mbar_wait_fast(&k_full[ks], kph, kWaitLimitNs))) break;
+          if ((!PAIR || i == 0) && !(ok = ta_wait(&k_full[ks], kph))) break;
           tc_fence_after_sync();
           issue_s(i, ks);
           tc_commit(&s_full[i]);
@@ -754,7 +773,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           }
         }
         const bool plain = c >= 0.f && (!kOneByte || *reinterpret_cast<const volatile int*>(&st->plain) != 0);
-        if (!__all_sync(kFull, mbar_wait_bounded(&s_full[i], steps & 1u, kWaitLimitNs))) {
+        if (!__all_sync(kFull, ta_wait(&s_full[i], steps & 1u))) {
           ok = false;
           break;
         }
