@@ -458,7 +458,7 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
   if (!tc && (warps < 1 || warps > 8)) return fail(PKV_ERR_INVALID_ARG, "warps_per_cta %d outside 1..8", warps);
   if (stages < 2 || stages > 8) return fail(PKV_ERR_INVALID_ARG, "stages %d outside 2..8", stages);
   if (tree_tc) {
-    warps = c->dtype == PKV_KV_BF16 ? 12 : 16;
+    warps = c->dtype == PKV_KV_BF16 ? 20 : 24;
     stages = 2;
   }
   const size_t smem = tree_tc ? pkv::tree_attend_smem_bytes(c->dtype, c->head_dim, NT > 1)

@@ -280,8 +280,10 @@ TreeWorkspace tree_workspace(int B, int Hkv, int D, int NT, int tree_words, int 
   return w;
 }
 
-// Raises a kernel's dynamic shared memory limit, once per (device, context, kernel).
-static cudaError_t allow_smem(const void* fn, size_t smem) {
+// Raises a kernel's dynamic shared memory limit, once per (device, context,
+// kernel); checks that it is launched with the registers that its warps share
+// out (a warp that waits for more than there are would wait forever).
+static cudaError_t allow_smem(const void* fn, size_t smem, int regs) {
   struct Entry {
     int dev;
     void* ctx;
@@ -297,15 +299,20 @@ static cudaError_t allow_smem(const void* fn, size_t smem) {
   for (const Entry& x : done)
     if (x.dev == dev && x.ctx == ctx && ctx != nullptr && x.fn == fn) return cudaSuccess;
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e == cudaSuccess) done.push_back(Entry{dev, current_context(), fn});
-  return e;
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes at{};
+  e = cudaFuncGetAttributes(&at, fn);
+  if (e != cudaSuccess) return e;
+  if (at.numRegs != regs) return cudaErrorInvalidKernelImage;
+  done.push_back(Entry{dev, current_context(), fn});
+  return cudaSuccess;
 }
 
 cudaError_t launch_tree_attend(const DecodeLaunch& L, uint8_t* ws, int* launched) {
   const bool pair = L.NT > 1;
   const int NP = pair ? (L.NT + 1) / 2 : 1;
   const TreeKernel k = pick(L.kv_dtype, L.D, L.bs, pair);
-  cudaError_t e = allow_smem(k.fn, k.smem);
+  cudaError_t e = allow_smem(k.fn, k.smem, ta_launch_regs(L.kv_dtype));
   if (e != cudaSuccess) return e;
   const TreeWorkspace w = tree_workspace(L.B, L.Hkv, L.D, L.NT, L.tree_words, L.tree_shares);
   int32_t* shares = reinterpret_cast<int32_t*>(ws + w.shares);

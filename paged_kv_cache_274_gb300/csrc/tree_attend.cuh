@@ -95,7 +95,17 @@ struct TaStep {
   float vzero[8];   // INT8: V zero point
 };
 
-__host__ __device__ constexpr int ta_threads(int kv) { return kv == PKV_KV_BF16 ? 384 : 512; }
+// 16 softmax warps, the issuing, K copy, V copy and query warps, and for
+// one-byte caches four converter warps
+__host__ __device__ constexpr int ta_threads(int kv) { return kv == PKV_KV_BF16 ? 640 : 768; }
+// Registers a thread at the launch (65,536 / threads, a multiple of 8), and
+// after the warps have shared them out.
+__host__ __device__ constexpr int ta_launch_regs(int kv) { return kv == PKV_KV_BF16 ? 96 : 80; }
+constexpr int kTaRoleRegs = 64;
+__host__ __device__ constexpr int ta_soft_regs(int kv) {
+  return (ta_threads(kv) * ta_launch_regs(kv) - (ta_threads(kv) - 512) * kTaRoleRegs) / 512;
+}
+static_assert(ta_soft_regs(PKV_KV_BF16) == 104 && ta_soft_regs(PKV_KV_INT8) == 88, "multiples of 8");
 
 template <int D, int KV, bool PAIR>
 struct TaLayout {  // byte offsets from the 1024-aligned shared-memory base
@@ -106,7 +116,7 @@ struct TaLayout {  // byte offsets from the 1024-aligned shared-memory base
   static constexpr uint32_t kKTile = kF8K ? kRegion : kTile;  // E4M3 K: codes
   static constexpr int kQTiles = PAIR ? 2 : 1;
   // stages: as many as fit beside the query tiles
-  static constexpr int kKStages = D == 64 ? 4 : kF8K ? 4 : (KV == PKV_KV_INT8 && PAIR) ? 2 : 3;
+  static constexpr int kKStages = D == 64 ? 4 : kF8K ? (PAIR ? 3 : 4) : PAIR ? 2 : 3;
   static constexpr int kVStages = D == 64 ? 4 : (kF8K && !PAIR) ? 3 : 2;
   static constexpr uint32_t kQ = 0;  // E4M3: the two parts of a tile, kRegion each
   static constexpr uint32_t kK = kQ + kQTiles * kTile;
@@ -118,8 +128,11 @@ struct TaLayout {  // byte offsets from the 1024-aligned shared-memory base
   static constexpr uint32_t kMisc = kBars + 8 * kNumBars;
   static constexpr uint32_t kRing = (kMisc + 4 + 15) & ~15u;
   static constexpr uint32_t kStep = kOneByte ? sizeof(TaStep) : offsetof(TaStep, par);
-  static constexpr uint32_t kXml = kRing + kTaRing * kStep;  // one tile: (m, l) of both streams' rows
-  static constexpr uint32_t kQrow = kXml + (PAIR ? 0 : 2 * kTaRows * 8 + 16);
+  // exchanged among the softmax warps: [stream][half][128] maxima (a pair's
+  // streams: sums too); one tile: [stream][half][128] sums, [stream][128] m,
+  // [stream] vref, apart because a stream may be in the next unit already
+  static constexpr uint32_t kXml = kRing + kTaRing * kStep;
+  static constexpr uint32_t kQrow = kXml + 4 * kTaRows * 4 + (PAIR ? 0 : 6 * kTaRows * 4 + 16);
   // one-byte caches: (2^kq, sum of q) per query row
   static constexpr uint32_t kEnd = kQrow + (kOneByte ? kQTiles * kTaRows * 8 : 0);
   static constexpr size_t kBytes = 1024 + kEnd;
@@ -153,6 +166,39 @@ __device__ __forceinline__ bool ta_wait(uint64_t* bar, uint32_t parity) {
     if (done) return true;
   }
   return false;
+}
+
+// Barrier of `threads` threads (whole warps) on hardware barrier `id`; true if
+// any of them says so.
+__device__ __forceinline__ bool bar_red_or(int id, int threads, bool any) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(any ? 1u : 0u), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+// Whole warp: 8 registers to consecutive TMEM columns, 16 from them.
+__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tc_regs_loaded16(uint32_t (&v)[16]) {
+  asm volatile(""
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                 "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
 }
 
 // Largest of 16 scores (bit patterns of floats) from x[o] on.
@@ -242,15 +288,15 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 4);  // one lane per warp of the stream
+      mbar_init(&p_full[s], 8);  // one lane per warp of the stream
       mbar_init(&o_full[s], 1);
-      mbar_init(&o_free[s], PAIR ? 4 : 8);
+      mbar_init(&o_free[s], PAIR ? 8 : 16);
     }
     for (int s = 0; s < kTaRing; ++s) mbar_init(&step_full[s], 1);
     mbar_init(q_full, kOneByte ? 4 : 1);
     mbar_init(q_free, 1);
-    mbar_init(q_read, 8);
-    mbar_init(x_full, 8);
+    mbar_init(q_read, 16);
+    mbar_init(x_full, 16);
     mbar_init(mma_drain, 1);
     fence_mbar_init();
     prefetch_tensormap(&kmap);
@@ -278,11 +324,11 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
   };
   auto wait_step = [&](uint32_t g) { return warp_wait(&step_full[g % kTaRing], (g / kTaRing) & 1u); };
 
-  // one-byte caches share the registers out anew: 2 x 128 x 168 for the softmax
-  // warpgroups + 2 x 128 x 88 = 512 x 128 at the launch
-  if (warp >= 8 && warp < 12) {
-  if constexpr (kOneByte) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == 9) {
+  // the registers are shared out anew: 512 x ta_soft_regs for the softmax
+  // warps and the others' kTaRoleRegs add up to the launch's
+  if (warp >= 16 && warp < 20) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTaRoleRegs));
+  if (warp == 17) {
     // K copy warp: the share's units, a descriptor and the K pages per step
     uint32_t g = 0;
     TreeBound at{0, 0, 0, 0}, end{0, 0, 0, 0};
@@ -409,7 +455,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         mbar_arrive(&step_full[g % kTaRing]);
       }
     }
-  } else if (warp == 10) {
+  } else if (warp == 18) {
     // V copy warp: V pages of each step
     const uint64_t policy = p.NP > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
     for (uint32_t g = 0;; ++g) {
@@ -442,7 +488,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       }
       v_issued = g + 1;
     }
-  } else if (warp == 11) {
+  } else if (warp == 19) {
     if constexpr (!kOneByte) {
       // query warp (bf16 caches): each unit's query tiles, once the products
       // with the ones before are done
@@ -467,7 +513,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         g0 += static_cast<uint32_t>(n);
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == 16) {
     if (lane == 0) {
       constexpr uint32_t kIdescS = kF8K       ? tc_idesc_e4m3_f32(kTaRows, kTreeTokens)
                                    : kOneByte ? tc_idesc_f16_f32(kTaRows, kTreeTokens)
@@ -565,13 +611,13 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
     }
     __syncwarp();
   }
-  } else if (warp >= 12) {
+  } else if (warp >= 20) {
     if constexpr (kOneByte) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTaRoleRegs));
       // converter warps: 32 rows each of a unit's query tiles, then of its
       // steps' K (INT8) and V; K of a step before V of the step before it, the
       // order that the products need them in
-      const int cw = warp - 12;
+      const int cw = warp - 20;
       auto convert = [&](bool is_k, uint32_t g) -> bool {
         uint64_t* landed = is_k ? &tma_k[g % KS] : &tma_v[g % VS];
         if (!warp_wait(landed, is_k ? (g / KS) & 1u : (g / VS) & 1u)) return false;
@@ -688,24 +734,32 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       }
     }
   } else {
-    if constexpr (kOneByte) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-    // softmax warps: stream i, row r of its tile in TMEM lane r
-    const int i = warp >> 2, r = tid & 127;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(ta_soft_regs(KV)));
+    // softmax warps: stream i, row r of its tile in TMEM lane r, half hh of
+    // the step's tokens.  Two warps share 32 rows: both hold the same running
+    // maximum of a row, and each the sum of its own half.
+    const int i = warp >> 3, hh = (warp >> 2) & 1, r = 32 * (warp & 3) + lane;
+    const int pair_bar = 1 + (warp & 3) + 4 * i;  // named barrier of the two warps
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_base + 128u * i;
     const uint32_t t_o = tmem + lane_base + 256u;  // O0; O1 is 128 columns on
     const float c = p.scale_log2;
-    const float cs = kOneByte ? 1.f : c;  // one-byte scores are scaled before the maximum
     const int tile = PAIR ? 2 * pair + i : 0;
     const int tl = r / p.G, t = tile * p.Tt + tl;
     const bool in_tile = tl < p.Tt && t < p.T;
-    // a warp without rows only keeps the barriers' counts and clears stale V rows
+    // warps without rows only keep the barriers' counts and clear stale V rows
     const bool warp_dead = !__any_sync(kFull, in_tile);
+    float* xch = reinterpret_cast<float*>(sm + L::kXml);
+    float* x_mine = xch + (2 * i + hh) * kTaRows + r;
+    const float* x_other = xch + (2 * i + (hh ^ 1)) * kTaRows + r;
     uint32_t g0 = 0, steps = 0, units1 = 0;  // steps of this stream, units with a step for stream 1
-    bool ok = true;
-    for (uint32_t iu = 0; ok; ++iu) {
-      if (!wait_step(g0)) {
-        ok = false;
+    // A wait of this warp gave up: it waits for nothing more, and leaves with
+    // the warp that shares its rows, at their next barrier
+    bool fail = false, left = false;
+    for (uint32_t iu = 0;; ++iu) {
+      if (!wait_step(g0)) fail = true;
+      if (bar_red_or(pair_bar, 64, fail)) {
+        fail = true;
         break;
       }
       int n, b, kvh, t0, t1, part, base, mrow, prow, row_state;
@@ -727,27 +781,21 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       }
       float cq = c, qsum = 0.f, vref = 1.f;
       if constexpr (kOneByte) {
-        if (!warp_wait(q_full, iu & 1u)) {
-          ok = false;
-          break;
-        }
+        if (!fail && !warp_wait(q_full, iu & 1u)) fail = true;
         const float2 qr = reinterpret_cast<const float2*>(sm + L::kQrow)[(PAIR ? i * kTaRows : 0) + r];
         cq = c * qr.x;
         qsum = qr.y;
         __syncwarp();
         if (lane == 0) mbar_arrive(q_read);
       }
-      float m = -INFINITY, l = 0.f;  // log2-domain lazy running maximum and sum of this row
+      float m = -INFINITY, l = 0.f;  // log2-domain lazy running maximum of the row, sum of this half
       const int ni = PAIR ? n : (n + 1 - i) / 2;  // this stream's steps
       for (int k = 0; k < ni; ++k, ++steps) {
         const int j = PAIR ? k : 2 * k + i;
         const uint32_t g = g0 + j;
         const int pos0 = t0 + j * kTreeTokens;
         const int nvs = t1 - pos0;  // tokens of the step in the sequence
-        if (!wait_step(g)) {
-          ok = false;
-          break;
-        }
+        if (!fail && !wait_step(g)) fail = true;
         const TaStep* st = const_cast<const TaStep*>(step_at(g));
         const uint64_t badw = PPI == 8 ? *reinterpret_cast<const volatile uint64_t*>(st->bad)
                                        : *reinterpret_cast<const volatile uint32_t*>(st->bad);
@@ -760,6 +808,20 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         // every token of the step is every row's (rows past the sequence's
         // nodes too: their output is zero whatever they attend to)
         const bool full = nvs >= kTreeTokens && !nodes_here && badw == 0;
+        // bits of this half's tokens that the row attends to
+        uint64_t rm = ~0ull;
+        if (!full) {
+          rm = low_bits64(nvs - 64 * hh);
+#pragma unroll
+          for (int q = 0; q < PPI / 2; ++q)
+            if ((badw >> (8 * (q + hh * (PPI / 2)))) & 0xffu) rm &= ~(((1ull << BS) - 1ull) << (q * BS));
+          uint64_t see = low_bits64(base - pos0 - 64 * hh);
+          if (nodes_here && mrow >= 0) see |= tree_window64(p.tree.mask + mrow, p.tree.words, pos0 - base + 64 * hh);
+          rm &= see;
+          const uint64_t badh = hh ? bad1 : bad0;
+          if ((rm & badh) && row_state == kTreeRowNormal) row_state = kTreeRowNan;
+          rm &= ~badh;
+        }
         bool vgrow = false;
         float factor = 1.f;
         if constexpr (kOneByte) {
@@ -772,67 +834,28 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             vref = vnew;
           }
         }
-        const bool plain = c >= 0.f && (!kOneByte || *reinterpret_cast<const volatile int*>(&st->plain) != 0);
-        if (!__all_sync(kFull, ta_wait(&s_full[i], steps & 1u))) {
-          ok = false;
-          break;
-        }
+        // no masks, and scales that keep the order of the raw scores
+        const bool fast = full && c >= 0.f && (!kOneByte || *reinterpret_cast<const volatile int*>(&st->plain) != 0);
+        if (!fail && !__all_sync(kFull, ta_wait(&s_full[i], steps & 1u))) fail = true;
         tc_fence_after_sync();
-        bool grow = false;
-        // one-byte: 32 scores of columns 32 cq32 .. +31 scaled to log2 units
-        auto scale32 = [&](uint32_t (&x)[32], int c32) {
-          if constexpr (kOneByte) {
-#pragma unroll
-            for (int h = 0; h < 32 / BS; ++h) {
-              const float4 pr = st->par[(32 * c32) / BS + h];
-              const float ck = cq * pr.x;
-              const float add = kI8 ? -pr.y * qsum * ck : 0.f;  // the biased K codes
-#pragma unroll
-              for (int e = 0; e < BS; e += 2) {
-                const int t2 = h * BS + e;
-                float a0, a1;
-                if constexpr (kI8)
-                  ffma2(a0, a1, __uint_as_float(x[t2]), __uint_as_float(x[t2 + 1]), ck, ck, add, add);
-                else
-                  fmul2(a0, a1, __uint_as_float(x[t2]), __uint_as_float(x[t2 + 1]), ck, ck);
-                x[t2] = __float_as_uint(a0);
-                x[t2 + 1] = __float_as_uint(a1);
-              }
-            }
-          }
-        };
-        auto vratio = [&](int c32, int e) -> float { return kOneByte ? st->par[(32 * c32 + e) / BS].z : 1.f; };
-        auto move_max = [&](float smax) {
-          grow = (m == -INFINITY) ? (smax != -INFINITY) : (smax > m + 8.f);
-          if (grow) {
-            const float f = (m == -INFINITY) ? 0.f : ex2_approx(m - smax);
-            factor *= f;
-            l *= f;
-            m = smax;
-          }
-        };
-        if (warp_dead) {
-        } else if (full && plain) {
-          uint32_t x0[32], x1[32], x2[32], x3[32];
-          tc_ld32(t_s, x0);
-          tc_ld32(t_s + 32, x1);
-          tc_ld32(t_s + 64, x2);
-          tc_ld32(t_s + 96, x3);
-          tc_wait_ld_regs(x0);  // one wait for the four loads
+        if (!warp_dead) {
+          uint32_t x0[32], x1[32];
+          tc_ld32(t_s + 64u * hh, x0);
+          tc_ld32(t_s + 64u * hh + 32u, x1);
+          tc_wait_ld_regs(x0);
           tc_regs_loaded(x1);
-          tc_regs_loaded(x2);
-          tc_regs_loaded(x3);
-          // page coefficients: a score in log2 units is x ck + add, P x v scale
-          // / vref is 2^(score - m + lv)
+          // coefficients of the scores of page h of the half's 32 tokens c32:
+          // a score in log2 units is x ck + add, P x v scale / vref is
+          // 2^(score - m + lv)
           auto page = [&](int c32, int h, float& ck, float& add, float& lv) {
-            const float4 pr = st->par[(32 * c32) / BS + h];
+            const float4 pr = st->par[(64 * hh + 32 * c32) / BS + h];
             ck = cq * pr.x;
-            add = kI8 ? -pr.y * qsum * ck : 0.f;
+            add = kI8 ? -pr.y * qsum * ck : 0.f;  // the biased K codes
             lv = pr.w;
           };
-          auto ext32 = [&](const uint32_t (&x)[32], int c32) -> float {
+          auto ext32 = [&](const uint32_t (&x)[32], int c32) -> float {  // largest score, in log2 units
             if constexpr (!kOneByte) {
-              return tree_ext32<true>(x);
+              return tree_ext32<true>(x) * c;
             } else if constexpr (BS == 32) {
               float ck, add, lv;
               page(c32, 0, ck, add, lv);
@@ -845,143 +868,129 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
               return fmaxf(e0, fmaf(max16(x, 16), ck, add));
             }
           };
-          const float ext = fmaxf(fmaxf(ext32(x0, 0), ext32(x1, 1)), fmaxf(ext32(x2, 2), ext32(x3, 3)));
-          move_max(ext * cs);
-          const float neg_m = (m == -INFINITY) ? 0.f : -m;
-          auto write_p = [&](const uint32_t (&x)[32], int c32) {
-            uint32_t pw[16];
-            float ps[2] = {0.f, 0.f};
+          // any scales and masks: scores to log2 units, -inf where masked
+          auto scaled = [&](uint32_t (&x)[32], int c32, uint32_t mk) -> float {
+            float ext = -INFINITY;
 #pragma unroll
             for (int h = 0; h < (kOneByte ? 32 / BS : 1); ++h) {
-              constexpr int kRun = kOneByte ? BS : 32;  // scores with the same coefficients
-              float ck = cs, add = 0.f, lv = 0.f;
+              constexpr int kRun = kOneByte ? BS : 32;
+              float ck = c, add = 0.f, lv;
               if constexpr (kOneByte) page(c32, h, ck, add, lv);
-              const float b = add + neg_m + lv;
-              if (kOneByte) ps[0] = ps[1] = 0.f;
 #pragma unroll
-              for (int e = 0; e < kRun / 2; ++e) {
-                const int k2 = h * kRun + 2 * e;
+              for (int e = h * kRun; e < (h + 1) * kRun; ++e) {
+                const float v = ((mk >> e) & 1u) ? fmaf(__uint_as_float(x[e]), ck, add) : -INFINITY;
+                x[e] = __float_as_uint(v);
+                ext = fmaxf(ext, v);
+              }
+            }
+            return ext;
+          };
+          float smax;
+          if (fast) {
+            smax = fmaxf(ext32(x0, 0), ext32(x1, 1));
+          } else {
+            smax = scaled(x0, 0, static_cast<uint32_t>(rm));
+            smax = fmaxf(smax, scaled(x1, 1, static_cast<uint32_t>(rm >> 32)));
+          }
+          // lazy maximum: moved when the row's exceeds it by more than 2^8.
+          // The barrier also means that both warps have read their scores, so
+          // that P may go over them.
+          const bool want = m == -INFINITY ? smax != -INFINITY : smax > m + 8.f;
+          bool grow = false;
+          if (bar_red_or(pair_bar, 64, want || fail)) {
+            *x_mine = smax;
+            if (bar_red_or(pair_bar, 64, fail)) {
+              fail = left = true;
+              break;
+            }
+            smax = fmaxf(smax, *x_other);
+            grow = m == -INFINITY ? smax != -INFINITY : smax > m + 8.f;
+            if (grow) {
+              const float f = (m == -INFINITY) ? 0.f : ex2_approx(m - smax);
+              factor *= f;
+              l *= f;
+              m = smax;
+            }
+            __syncwarp();
+          }
+          const float neg_m = (m == -INFINITY) ? 0.f : -m;
+          auto write_p = [&](const uint32_t (&x)[32], int c32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // 16 scores
+              uint32_t pw[8];
+              float ck = c, add = 0.f, lv = 0.f;
+              if constexpr (kOneByte) page(c32, BS == 32 ? 0 : h, ck, add, lv);
+              const float bias = add + neg_m + lv;
+              float ps0 = 0.f, ps1 = 0.f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int k2 = 16 * h + 2 * e;
                 float a0, a1;
-                ffma2(a0, a1, __uint_as_float(x[k2]), __uint_as_float(x[k2 + 1]), ck, ck, b, b);
+                ffma2(a0, a1, __uint_as_float(x[k2]), __uint_as_float(x[k2 + 1]), ck, ck, bias, bias);
                 const float p0 = ex2_approx(a0);
                 const float p1 = ex2_approx(a1);
-                fadd2(ps[0], ps[1], ps[0], ps[1], p0, p1);
-                pw[k2 / 2] = kOneByte ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+                fadd2(ps0, ps1, ps0, ps1, p0, p1);
+                pw[e] = kOneByte ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
               }
-              l = kOneByte ? fmaf(ps[0] + ps[1], ex2_approx(-lv), l) : l + (ps[0] + ps[1]);
+              l = kOneByte ? fmaf(ps0 + ps1, ex2_approx(-lv), l) : l + (ps0 + ps1);
+              tc_st8(t_s + 32u * hh + 16 * c32 + 8 * h, pw);
             }
-            tc_st16(t_s + 16 * c32, pw);
           };
-          write_p(x0, 0);
-          write_p(x1, 1);
-          write_p(x2, 2);
-          write_p(x3, 3);
-        } else {
-          // a step with masked tokens (the sequence's end, nodes, bad pages),
-          // or a negative scale:
-          // 32 scores at a time, the masked maximum first, then P (a chunk's P
-          // goes over columns whose scores are already read)
-          uint64_t rm0 = low_bits64(nvs), rm1 = low_bits64(nvs - 64);
+          auto write_scaled = [&](const uint32_t (&x)[32], int c32) {  // scores in log2 units
 #pragma unroll
-          for (int q = 0; q < PPI; ++q)
-            if ((badw >> (8 * q)) & 0xffu) {
-              const uint64_t pm = ((1ull << BS) - 1ull) << ((q * BS) & 63);
-              if (q * BS < 64) rm0 &= ~pm; else rm1 &= ~pm;
-            }
-          uint64_t see0 = low_bits64(base - pos0), see1 = low_bits64(base - pos0 - 64);
-          if (nodes_here && mrow >= 0) {
-            see0 |= tree_window64(p.tree.mask + mrow, p.tree.words, pos0 - base);
-            see1 |= tree_window64(p.tree.mask + mrow, p.tree.words, pos0 - base + 64);
-          }
-          rm0 &= see0;
-          rm1 &= see1;
-          if (((rm0 & bad0) | (rm1 & bad1)) && row_state == kTreeRowNormal) row_state = kTreeRowNan;
-          rm0 &= ~bad0;
-          rm1 &= ~bad1;
-          __syncwarp();  // the TMEM accesses below are warp-collective
-          const float ext_init = cs >= 0.f ? -INFINITY : INFINITY;
-          float ext = ext_init;
-#pragma unroll 1
-          for (int c32 = 0; c32 < 4; ++c32) {
-            uint32_t x[32];
-            tc_ld32(t_s + 32 * c32, x);
-            const uint64_t r64 = c32 < 2 ? rm0 : rm1;
-            const uint32_t mk = (c32 & 1) ? static_cast<uint32_t>(r64 >> 32) : static_cast<uint32_t>(r64);
-            tc_wait_ld_regs(x);
-            scale32(x, c32);
+            for (int h = 0; h < 2; ++h) {
+              uint32_t pw[8];
+              const float vr = kOneByte ? st->par[(64 * hh + 32 * c32 + 16 * h) / BS].z : 1.f;
 #pragma unroll
-            for (int kk = 0; kk < 32; ++kk) {
-              const float v = ((mk >> kk) & 1u) ? __uint_as_float(x[kk]) : ext_init;
-              ext = cs >= 0.f ? fmaxf(ext, v) : fminf(ext, v);
-            }
-          }
-          move_max((rm0 | rm1) != 0ull ? ext * cs : -INFINITY);
-          const float neg_m = (m == -INFINITY) ? 0.f : -m;
-          float ps0 = 0.f, ps1 = 0.f;
-          __syncwarp();
-#pragma unroll 1
-          for (int c32 = 0; c32 < 4; ++c32) {
-            uint32_t x[32];
-            tc_ld32(t_s + 32 * c32, x);
-            const uint64_t r64 = c32 < 2 ? rm0 : rm1;
-            const uint32_t mk = (c32 & 1) ? static_cast<uint32_t>(r64 >> 32) : static_cast<uint32_t>(r64);
-            tc_wait_ld_regs(x);
-            scale32(x, c32);
-            uint32_t pw[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float a0, a1;
-              ffma2(a0, a1, __uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), cs, cs, neg_m, neg_m);
-              float p0 = ex2_approx(a0);
-              float p1 = ex2_approx(a1);
-              p0 = ((mk >> (2 * e)) & 1u) ? p0 : 0.f;
-              p1 = ((mk >> (2 * e + 1)) & 1u) ? p1 : 0.f;
-              fadd2(ps0, ps1, ps0, ps1, p0, p1);
-              if constexpr (kOneByte) {
+              for (int e = 0; e < 8; ++e) {
+                const float p0 = ex2_approx(__uint_as_float(x[16 * h + 2 * e]) + neg_m);
+                const float p1 = ex2_approx(__uint_as_float(x[16 * h + 2 * e + 1]) + neg_m);
+                l += p0 + p1;
                 // (a masked token's page may have no finite scale: 0 x that would be NaN)
-                const float vr = vratio(c32, 2 * e);
-                pw[e] = pack_f16x2(p0 != 0.f ? p0 * vr : 0.f, p1 != 0.f ? p1 * vr : 0.f);
-              } else {
-                pw[e] = pack_bf16x2(p0, p1);
+                pw[e] = kOneByte ? pack_f16x2(p0 != 0.f ? p0 * vr : 0.f, p1 != 0.f ? p1 * vr : 0.f) : pack_bf16x2(p0, p1);
               }
+              tc_st8(t_s + 32u * hh + 16 * c32 + 8 * h, pw);
             }
-            tc_st16(t_s + 16 * c32, pw);
+          };
+          if (fast) {
+            write_p(x0, 0);
+            write_p(x1, 1);
+          } else {
+            write_scaled(x0, 0);
+            write_scaled(x1, 1);
           }
-          l += ps0 + ps1;
-        }
-        // O_i of the steps before, rarely (quiescent: PV_i of the step before
-        // was done before this S_i, the next waits for p_full)
-        if (k > 0 && !warp_dead && __any_sync(kFull, grow || vgrow)) {
+          // O_i of the steps before, rarely, half of the columns by each warp
+          // (quiescent: PV_i of the step before was done before this S_i, the
+          // next waits for p_full)
+          if (k > 0 && __any_sync(kFull, grow || vgrow)) {
 #pragma unroll 1
-          for (int oc = 0; oc < D; oc += 32) {
-            uint32_t ov[32];
-            tc_ld32(t_o + 128u * i + oc, ov);
-            tc_wait_ld_regs(ov);
+            for (int oc = hh * (D / 2); oc < (hh + 1) * (D / 2); oc += 32) {
+              uint32_t ov[32];
+              tc_ld32(t_o + 128u * i + oc, ov);
+              tc_wait_ld_regs(ov);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float a, b2;
-              fmul2(a, b2, __uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), factor, factor);
-              ov[e] = __float_as_uint(a);
-              ov[e + 1] = __float_as_uint(b2);
+              for (int e = 0; e < 32; e += 2) {
+                float a, b2;
+                fmul2(a, b2, __uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), factor, factor);
+                ov[e] = __float_as_uint(a);
+                ov[e + 1] = __float_as_uint(b2);
+              }
+              tc_st32(t_o + 128u * i + oc, ov);
             }
-            tc_st32(t_o + 128u * i + oc, ov);
           }
         }
         // V rows of tokens outside the sequence or of a bad page may hold
         // anything, and nodes' V rows that are not finite would reach every
-        // row, while P is 0 there: once V has landed, thread r clears row r (a
-        // pair's streams write the same zeros)
+        // row, while P is 0 there: once V has landed, the threads of row r
+        // clear it (a pair's streams write the same zeros)
         if (nvs < kTreeTokens || badw != 0 || (bad0 | bad1) != 0ull) {
-          if (!warp_wait(&v_full[g % VS], (g / VS) & 1u)) {
-            ok = false;
-            break;
-          }
-          if (r >= nvs || ((badw >> (8 * (r / BS))) & 0xffu) || (((r < 64 ? bad0 : bad1) >> (r & 63)) & 1ull)) {
-            uint8_t* vb = sm + L::kV + (g % VS) * L::kTile + r * 128;
+          if (!fail && !warp_wait(&v_full[g % VS], (g / VS) & 1u)) fail = true;
+          if (fail) {
+          } else if (r >= nvs || ((badw >> (8 * (r / BS))) & 0xffu) || (((r < 64 ? bad0 : bad1) >> (r & 63)) & 1ull)) {
+            // 64-d half hh (head_dim 64: 32 d)
+            uint8_t* vb = sm + L::kV + (g % VS) * L::kTile + r * 128 + (kHalves == 2 ? hh * L::kRegion : hh * 64);
 #pragma unroll
-            for (int cc = 0; cc < 8; ++cc)
-#pragma unroll
-              for (int h = 0; h < kHalves; ++h) *reinterpret_cast<uint4*>(vb + h * L::kRegion + 16 * cc) = make_uint4(0, 0, 0, 0);
+            for (int cc = 0; cc < 4 * kHalves; ++cc) *reinterpret_cast<uint4*>(vb + 16 * cc) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();  // read by the tensor cores
           __syncwarp();
@@ -991,41 +1000,48 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[i]);
       }
-      if (!ok) break;
+      if (left) break;
 
       // the unit's output: O / l as bf16, or a partial (m, l, O)
-      if (PAIR) {
-        if (!warp_wait(&o_full[i], iu & 1u)) ok = false;
-      } else {
-        // both streams' last products; their completion also means that the
-        // (m, l) exchanged for the unit before have been read
-        if (!warp_wait(&o_full[0], iu & 1u)) ok = false;
-        if (ok && n > 1 && !warp_wait(&o_full[1], units1 & 1u)) ok = false;
-        if (n > 1) ++units1;
-      }
-      if (!ok) break;
       // a row that attends to a node with a non-finite V row is NaN in every
-      // column, also those that the other stream's warps write: through its sum
+      // column, also those that other warps write: through its sum
       if (row_state == kTreeRowNan) l = tree_row_value(kTreeRowNan);
       if (row_state == kTreeRowZero) {  // whatever its query held
         m = -INFINITY;
         l = 0.f;
       }
       float f0 = kOneByte ? vref : 1.f, f1 = 0.f;
-      if constexpr (!PAIR) {
-        float2* xml = reinterpret_cast<float2*>(sm + L::kXml);
-        float* xv = reinterpret_cast<float*>(xml + 2 * kTaRows);
-        xml[i * kTaRows + r] = make_float2(m, l);
-        if (kOneByte && r == 0) xv[i] = vref;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(x_full);
-        if (!warp_wait(x_full, iu & 1u)) {
-          ok = false;
+      if constexpr (PAIR) {
+        if (!fail && !warp_wait(&o_full[i], iu & 1u)) fail = true;
+        *x_mine = l;
+        if (bar_red_or(pair_bar, 64, fail)) {
+          fail = true;
           break;
         }
-        const float2 other = xml[(1 - i) * kTaRows + r];
-        const float m0 = i == 0 ? m : other.x, m1 = i == 0 ? other.x : m;
-        const float l0 = i == 0 ? l : other.y, l1 = i == 0 ? other.y : l;
+        l += *x_other;
+      } else {
+        // both streams' last products; their completion also means that what
+        // was exchanged for the unit before has been read
+        if (!fail && !warp_wait(&o_full[0], iu & 1u)) fail = true;
+        if (n > 1) {
+          if (!fail && !warp_wait(&o_full[1], units1 & 1u)) fail = true;
+          ++units1;
+        }
+        float* xl = xch + 4 * kTaRows;  // [stream][half][128]
+        float* xm = xl + 4 * kTaRows;   // [stream][128]
+        float* xv = xm + 2 * kTaRows;   // [stream]
+        xl[(2 * i + hh) * kTaRows + r] = l;
+        if (hh == 0) xm[i * kTaRows + r] = m;
+        if (kOneByte && hh == 0 && r == 0) xv[i] = vref;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x_full);
+        if (!fail && !warp_wait(x_full, iu & 1u)) fail = true;
+        if (bar_red_or(pair_bar, 64, fail)) {
+          fail = true;
+          break;
+        }
+        const float m0 = xm[r], m1 = xm[kTaRows + r];
+        const float l0 = xl[r] + xl[kTaRows + r], l1 = xl[2 * kTaRows + r] + xl[3 * kTaRows + r];
         m = fmaxf(m0, m1);
         f0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - m);
         f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m);
@@ -1045,40 +1061,45 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           f0 *= inv;
           f1 *= inv;
         }
-        const int c0 = PAIR ? 0 : i * (D / 2), c1 = PAIR ? D : c0 + D / 2;
+        // a pair's warp: half of its tile's columns; else a quarter of the one tile's
+        constexpr int kCols = PAIR ? D / 2 : D / 4;
+        const int c0 = (PAIR ? hh : 2 * i + hh) * kCols;
 #pragma unroll 1
-        for (int cc = c0; cc < c1; cc += 32) {
-          uint32_t ov[32];
-          tc_ld32(t_o + (PAIR ? 128u * i : 0u) + cc, ov);
-          tc_wait_ld_regs(ov);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f0);
+        for (int cc = c0; cc < c0 + kCols; cc += 16) {
+          uint32_t ov[16];
+          tc_ld16(t_o + (PAIR ? 128u * i : 0u) + cc, ov);
           if (!PAIR && n > 1) {
-            uint32_t o1[32];
-            tc_ld32(t_o + 128u + cc, o1);
-            tc_wait_ld_regs(o1);
+            uint32_t o1[16];
+            tc_ld16(t_o + 128u + cc, o1);
+            tc_wait_ld_regs16(ov);
+            tc_regs_loaded16(o1);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(ov[e])));
+            for (int e = 0; e < 16; ++e)
+              ov[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(ov[e]) * f0));
+          } else {
+            tc_wait_ld_regs16(ov);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f0);
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) ov[e] = row_state == kTreeRowZero ? 0u : ov[e];
+          for (int e = 0; e < 16; ++e) ov[e] = row_state == kTreeRowZero ? 0u : ov[e];
           if (in_tile) {
             if (part == 0) {
               uint4* dst = reinterpret_cast<uint4*>(p.out + qrow * D + cc);
 #pragma unroll
-              for (int c8 = 0; c8 < 4; ++c8) {
+              for (int c8 = 0; c8 < 2; ++c8) {
                 const float* f = reinterpret_cast<const float*>(ov + 8 * c8);
                 dst[c8] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
               }
             } else {
               uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow_o * D + cc);
 #pragma unroll
-              for (int c4 = 0; c4 < 8; ++c4) dst[c4] = make_uint4(ov[4 * c4], ov[4 * c4 + 1], ov[4 * c4 + 2], ov[4 * c4 + 3]);
+              for (int c4 = 0; c4 < 4; ++c4) dst[c4] = make_uint4(ov[4 * c4], ov[4 * c4 + 1], ov[4 * c4 + 2], ov[4 * c4 + 3]);
             }
           }
           __syncwarp();  // the next TMEM load is warp-collective
         }
-        if (in_tile && part != 0 && (PAIR || i == 0)) p.part_ml[prow_o] = make_float2(m, l);
+        if (in_tile && part != 0 && hh == 0 && (PAIR || i == 0)) p.part_ml[prow_o] = make_float2(m, l);
       }
       tc_fence_before_sync();
       __syncwarp();
@@ -1088,7 +1109,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       }
       g0 += static_cast<uint32_t>(n);
     }
-    if (!ok) timed_out = true;
+    if (fail) timed_out = true;
   }
 
   timed_out = __syncthreads_or(timed_out) != 0;  // every role has left its loop
@@ -1096,15 +1117,15 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
     if (tid == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
     // each role lets its own copies and products still in flight finish
     // (bounded) before the shared and tensor memory are released
-    if (warp == 9 && lane == 0)
+    if (warp == 17 && lane == 0)
       for (uint32_t g = k_issued > KS ? k_issued - KS : 0; g < k_issued; ++g)
         mbar_wait_bounded(kI8 ? &tma_k[g % KS] : &k_full[g % KS], (g / KS) & 1u, kWaitLimitNs / 16);
-    if (warp == 10 && lane == 0) {
+    if (warp == 18 && lane == 0) {
       for (uint32_t g = v_issued > VS ? v_issued - VS : 0; g < v_issued; ++g)
         mbar_wait_bounded(kOneByte ? &tma_v[g % VS] : &v_full[g % VS], (g / VS) & 1u, kWaitLimitNs / 16);
     }
-    if (warp == 11 && lane == 0 && q_loads > 0) mbar_wait_bounded(q_full, (q_loads - 1) & 1u, kWaitLimitNs / 16);
-    if (warp == 8 && lane == 0 && mma_issued > 0) {  // one commit covers every product issued
+    if (warp == 19 && lane == 0 && q_loads > 0) mbar_wait_bounded(q_full, (q_loads - 1) & 1u, kWaitLimitNs / 16);
+    if (warp == 16 && lane == 0 && mma_issued > 0) {  // one commit covers every product issued
       tc_commit(mma_drain);
       mbar_wait_bounded(mma_drain, 0, kWaitLimitNs / 16);
     }

@@ -59,7 +59,7 @@ def test_tree_plans(lib):
 def test_tcgen05_tree_plans(lib, dtype, D, T):
     st, plan = _plan(lib, _desc(dtype=dtype, head_dim=D), 8, T, 32, 64)
     assert st == 0 and plan.math == pkv.MATH_TC and plan.kernels_per_call == (3 if T <= 512 else 2)
-    assert plan.smem_bytes_per_cta <= 227 * 1024 and plan.warps_per_cta == (12 if dtype == 0 else 16)
+    assert plan.smem_bytes_per_cta <= 227 * 1024 and plan.warps_per_cta == (20 if dtype == 0 else 24)
     assert plan.row_tiles == -(-T // min(T, 32))
     # partials: at most two per CTA, whatever the lengths
     rows = 128 if plan.row_tiles == 1 else 256
