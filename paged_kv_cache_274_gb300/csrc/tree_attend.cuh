@@ -77,6 +77,11 @@ struct TaParams {
   float scale_log2;
 };
 
+// Step flags; a step without any is every row's in whole, with scores whose
+// order the page scales keep.
+constexpr int kStepMasked = 1;  // the sequence's end, nodes, or a bad page
+constexpr int kStepScales = 2;  // a k scale < 0, a v scale <= 0, or one that is not finite
+
 // One step's descriptor in the ring.
 struct TaStep {
   int n;      // steps of the work unit (0: no more work)
@@ -87,7 +92,7 @@ struct TaStep {
   int ctx;
   int pages[8];
   uint8_t bad[8];   // page id out of range
-  int plain;        // every k scale >= 0 and every v scale > 0 (and finite)
+  int flags;        // kStepMasked, kStepScales
   float vref;       // one-byte caches: P carries v scale / vref
   // one-byte caches, per page: k scale, INT8 K bias 1152 + zero, v scale /
   // vref and its log2
@@ -353,6 +358,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       first_unit = false;
       vref = 0.f;  // of the unit; 0: no page with a scale yet
       const int npages = (t1 - t0 + BS - 1) / BS;
+      const int base = ctx - (p.tree.node_counts != nullptr ? __ldg(p.tree.node_counts + b) : p.T);
       const int* trow = p.block_tables + static_cast<size_t>(b) * p.MB + t0 / BS;
       // lane i holds page i of a run of 32 pages, and of the next run
       auto load_ids = [&](int q) { return q < npages ? __ldg(trow + q) : 0; };
@@ -411,6 +417,8 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           st->bad[q] = bad ? 1 : 0;
         }
         if (bad) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+        const int seen = min(t1, base) - (t0 + j * kTreeTokens);  // tokens of the step that every row attends to
+        const int flags = (seen < kTreeTokens || __any_sync(kFull, bad) ? kStepMasked : 0) | (plain ? 0 : kStepScales);
         if (lane == 0) {
           st->n = n;
           st->b = b;
@@ -420,7 +428,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           st->part = part;
           st->np = np;
           st->ctx = ctx;
-          st->plain = plain ? 1 : 0;
+          st->flags = flags;
           st->vref = vref;
         }
         uint8_t* dst = sm + L::kK + (g % KS) * L::kKTile;
@@ -795,22 +803,20 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         const uint32_t g = g0 + j;
         const int pos0 = t0 + j * kTreeTokens;
         const int nvs = t1 - pos0;  // tokens of the step in the sequence
-        if (!fail && !wait_step(g)) fail = true;
+        if (!fail && !ta_wait(&step_full[g % kTaRing], (g / kTaRing) & 1u)) fail = true;
         const TaStep* st = const_cast<const TaStep*>(step_at(g));
-        const uint64_t badw = PPI == 8 ? *reinterpret_cast<const volatile uint64_t*>(st->bad)
-                                       : *reinterpret_cast<const volatile uint32_t*>(st->bad);
-        uint64_t bad0 = 0ull, bad1 = 0ull;  // nodes with a non-finite V row
-        const bool nodes_here = pos0 + kTreeTokens > base;
-        if (nodes_here && p.tree.poison != nullptr) {
-          bad0 = tree_window64(p.tree.poison + prow, p.tree.words, pos0 - base);
-          bad1 = tree_window64(p.tree.poison + prow, p.tree.words, pos0 - base + 64);
-        }
-        // every token of the step is every row's (rows past the sequence's
-        // nodes too: their output is zero whatever they attend to)
-        const bool full = nvs >= kTreeTokens && !nodes_here && badw == 0;
-        // bits of this half's tokens that the row attends to
-        uint64_t rm = ~0ull;
-        if (!full) {
+        const int flags = *reinterpret_cast<const volatile int*>(&st->flags);
+        uint64_t badw = 0ull, bad0 = 0ull, bad1 = 0ull;  // bad pages; nodes with a non-finite V row
+        uint64_t rm = ~0ull;                             // this half's tokens that the row attends to
+        // (rows past the sequence's nodes attend to every token before them
+        // too: their output is zero whatever they attend to)
+        if (flags & kStepMasked) {
+          badw = PPI == 8 ? *reinterpret_cast<const volatile uint64_t*>(st->bad) : *reinterpret_cast<const volatile uint32_t*>(st->bad);
+          const bool nodes_here = pos0 + kTreeTokens > base;
+          if (nodes_here && p.tree.poison != nullptr) {
+            bad0 = tree_window64(p.tree.poison + prow, p.tree.words, pos0 - base);
+            bad1 = tree_window64(p.tree.poison + prow, p.tree.words, pos0 - base + 64);
+          }
           rm = low_bits64(nvs - 64 * hh);
 #pragma unroll
           for (int q = 0; q < PPI / 2; ++q)
@@ -834,9 +840,9 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             vref = vnew;
           }
         }
-        // no masks, and scales that keep the order of the raw scores
-        const bool fast = full && c >= 0.f && (!kOneByte || *reinterpret_cast<const volatile int*>(&st->plain) != 0);
-        if (!fail && !__all_sync(kFull, ta_wait(&s_full[i], steps & 1u))) fail = true;
+        const bool fast = flags == 0 && c >= 0.f;
+        if (!fail && !ta_wait(&s_full[i], steps & 1u)) fail = true;
+        __syncwarp();
         tc_fence_after_sync();
         if (!warp_dead) {
           uint32_t x0[32], x1[32];
@@ -914,14 +920,19 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             __syncwarp();
           }
           const float neg_m = (m == -INFINITY) ? 0.f : -m;
+          float ps0 = 0.f, ps1 = 0.f;
           auto write_p = [&](const uint32_t (&x)[32], int c32) {
+            float ck = c, add = 0.f, lv = 0.f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {  // 16 scores
+              if constexpr (kOneByte) {
+                if (h == 0 || BS == 16) {
+                  page(c32, h, ck, add, lv);
+                  ps0 = ps1 = 0.f;
+                }
+              }
               uint32_t pw[8];
-              float ck = c, add = 0.f, lv = 0.f;
-              if constexpr (kOneByte) page(c32, BS == 32 ? 0 : h, ck, add, lv);
               const float bias = add + neg_m + lv;
-              float ps0 = 0.f, ps1 = 0.f;
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const int k2 = 16 * h + 2 * e;
@@ -932,7 +943,9 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
                 fadd2(ps0, ps1, ps0, ps1, p0, p1);
                 pw[e] = kOneByte ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
               }
-              l = kOneByte ? fmaf(ps0 + ps1, ex2_approx(-lv), l) : l + (ps0 + ps1);
+              if constexpr (kOneByte) {
+                if (h == 1 || BS == 16) l = fmaf(ps0 + ps1, ex2_approx(-lv), l);
+              }
               tc_st8(t_s + 32u * hh + 16 * c32 + 8 * h, pw);
             }
           };
@@ -955,6 +968,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           if (fast) {
             write_p(x0, 0);
             write_p(x1, 1);
+            if constexpr (!kOneByte) l += ps0 + ps1;
           } else {
             write_scaled(x0, 0);
             write_scaled(x1, 1);
@@ -983,7 +997,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         // anything, and nodes' V rows that are not finite would reach every
         // row, while P is 0 there: once V has landed, the threads of row r
         // clear it (a pair's streams write the same zeros)
-        if (nvs < kTreeTokens || badw != 0 || (bad0 | bad1) != 0ull) {
+        if ((flags & kStepMasked) && (nvs < kTreeTokens || badw != 0 || (bad0 | bad1) != 0ull)) {
           if (!fail && !warp_wait(&v_full[g % VS], (g / VS) & 1u)) fail = true;
           if (fail) {
           } else if (r >= nvs || ((badw >> (8 * (r / BS))) & 0xffu) || (((r < 64 ? bad0 : bad1) >> (r & 63)) & 1ull)) {
