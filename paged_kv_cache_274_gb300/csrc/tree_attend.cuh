@@ -173,6 +173,13 @@ __device__ __forceinline__ bool ta_wait(uint64_t* bar, uint32_t parity) {
   return false;
 }
 
+// One lane of the converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+
 // Barrier of `threads` threads (whole warps) on hardware barrier `id`; true if
 // any of them says so.
 __device__ __forceinline__ bool bar_red_or(int id, int threads, bool any) {
@@ -522,7 +529,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       }
     }
   } else if (warp == 16) {
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t kIdescS = kF8K       ? tc_idesc_e4m3_f32(kTaRows, kTreeTokens)
                                    : kOneByte ? tc_idesc_f16_f32(kTaRows, kTreeTokens)
                                               : tc_idesc_bf16_f32(kTaRows, kTreeTokens);
@@ -1139,7 +1146,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         mbar_wait_bounded(kOneByte ? &tma_v[g % VS] : &v_full[g % VS], (g / VS) & 1u, kWaitLimitNs / 16);
     }
     if (warp == 19 && lane == 0 && q_loads > 0) mbar_wait_bounded(q_full, (q_loads - 1) & 1u, kWaitLimitNs / 16);
-    if (warp == 16 && lane == 0 && mma_issued > 0) {  // one commit covers every product issued
+    if (warp == 16 && mma_issued > 0) {  // one commit covers every product issued
       tc_commit(mma_drain);
       mbar_wait_bounded(mma_drain, 0, kWaitLimitNs / 16);
     }
