@@ -106,11 +106,11 @@ __host__ __device__ constexpr int ta_threads(int kv) { return kv == PKV_KV_BF16 
 // Registers a thread at the launch (65,536 / threads, a multiple of 8), and
 // after the warps have shared them out.
 __host__ __device__ constexpr int ta_launch_regs(int kv) { return kv == PKV_KV_BF16 ? 96 : 80; }
-constexpr int kTaRoleRegs = 64;
+constexpr int kTaRoleRegs = 48;
 __host__ __device__ constexpr int ta_soft_regs(int kv) {
-  return (ta_threads(kv) * ta_launch_regs(kv) - (ta_threads(kv) - 512) * kTaRoleRegs) / 512;
+  return (ta_threads(kv) * ta_launch_regs(kv) - (ta_threads(kv) - 512) * kTaRoleRegs) / 512 / 8 * 8;
 }
-static_assert(ta_soft_regs(PKV_KV_BF16) == 104 && ta_soft_regs(PKV_KV_INT8) == 88, "multiples of 8");
+static_assert(ta_soft_regs(PKV_KV_BF16) == 104 && ta_soft_regs(PKV_KV_INT8) == 96, "");
 
 template <int D, int KV, bool PAIR>
 struct TaLayout {  // byte offsets from the 1024-aligned shared-memory base
