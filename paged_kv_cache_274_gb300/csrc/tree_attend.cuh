@@ -559,9 +559,9 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         }
         ++mma_issued;
       };
-      // O_i (+)= P_i . V: P of tokens 16kk .. 16kk + 15 in columns 8kk .. +7 of
-      // S_i, V MN-major as the pages hold it (64-d halves kRegion apart,
-      // 8-token groups 1024 B apart)
+      // O_i (+)= P_i . V: P of a half's tokens 16kk .. 16kk + 15 in columns
+      // 8kk .. +7 of the half's 64 columns of S_i, V MN-major as the pages hold
+      // it (64-d halves kRegion apart, 8-token groups 1024 B apart)
       uint32_t pc[2] = {0, 0};  // P tiles taken, per stream
       uint32_t ks = 0, kph = 0, vs = 0, vph = 0;  // stage and phase of the next K and V
       auto issue_pv = [&](int i, bool first, uint32_t iu) -> bool {
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_bf16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 32u * h + 8u * kk, vd + (h * 4 + kk) * (2048 >> 4), kIdescO,
+            tc_mma_bf16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 64u * h + 8u * kk, vd + (h * 4 + kk) * (2048 >> 4), kIdescO,
                            !first || h > 0 || kk > 0);
         ++mma_issued;
         if (!PAIR || i == 1) {
@@ -852,9 +852,10 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         __syncwarp();
         tc_fence_after_sync();
         if (!warp_dead) {
+          const uint32_t t_h = t_s + 64u * hh;  // this half's scores, then its P over them
           uint32_t x0[32], x1[32];
-          tc_ld32(t_s + 64u * hh, x0);
-          tc_ld32(t_s + 64u * hh + 32u, x1);
+          tc_ld32(t_h, x0);
+          tc_ld32(t_h + 32u, x1);
           tc_wait_ld_regs(x0);
           tc_regs_loaded(x1);
           // coefficients of the scores of page h of the half's 32 tokens c32:
@@ -905,9 +906,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             smax = scaled(x0, 0, static_cast<uint32_t>(rm));
             smax = fmaxf(smax, scaled(x1, 1, static_cast<uint32_t>(rm >> 32)));
           }
-          // lazy maximum: moved when the row's exceeds it by more than 2^8.
-          // The barrier also means that both warps have read their scores, so
-          // that P may go over them.
+          // lazy maximum: moved when the row's exceeds it by more than 2^8
           const bool want = m == -INFINITY ? smax != -INFINITY : smax > m + 8.f;
           bool grow = false;
           if (bar_red_or(pair_bar, 64, want || fail)) {
@@ -953,7 +952,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
               if constexpr (kOneByte) {
                 if (h == 1 || BS == 16) l = fmaf(ps0 + ps1, ex2_approx(-lv), l);
               }
-              tc_st8(t_s + 32u * hh + 16 * c32 + 8 * h, pw);
+              tc_st8(t_h + 16 * c32 + 8 * h, pw);
             }
           };
           auto write_scaled = [&](const uint32_t (&x)[32], int c32) {  // scores in log2 units
@@ -969,13 +968,23 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
                 // (a masked token's page may have no finite scale: 0 x that would be NaN)
                 pw[e] = kOneByte ? pack_f16x2(p0 != 0.f ? p0 * vr : 0.f, p1 != 0.f ? p1 * vr : 0.f) : pack_bf16x2(p0, p1);
               }
-              tc_st8(t_s + 32u * hh + 16 * c32 + 8 * h, pw);
+              tc_st8(t_h + 16 * c32 + 8 * h, pw);
             }
           };
           if (fast) {
-            write_p(x0, 0);
-            write_p(x1, 1);
-            if constexpr (!kOneByte) l += ps0 + ps1;
+            if constexpr (kOneByte) {
+              // one-byte caches: the second 32 scores are read again, so that
+              // 32 registers less are held meanwhile (the first 32's P covers
+              // only columns that are done with)
+              write_p(x0, 0);
+              tc_ld32(t_h + 32u, x1);
+              tc_wait_ld_regs(x1);
+              write_p(x1, 1);
+            } else {
+              write_p(x0, 0);
+              write_p(x1, 1);
+              l += ps0 + ps1;
+            }
           } else {
             write_scaled(x0, 0);
             write_scaled(x1, 1);
