@@ -101,14 +101,15 @@ struct TaStep {
 };
 
 // 16 softmax warps, the issuing, K copy, V copy and query warps, and for
-// one-byte caches four converter warps
-__host__ __device__ constexpr int ta_threads(int kv) { return kv == PKV_KV_BF16 ? 640 : 768; }
+// one-byte caches the converter warps
+constexpr int kConvWarps = 8;
+__host__ __device__ constexpr int ta_threads(int kv) { return kv == PKV_KV_BF16 ? 640 : 640 + 32 * kConvWarps; }
 // Registers a thread at the launch (65,536 / threads, a multiple of 8), and
 // after the warps have shared them out.
-__host__ __device__ constexpr int ta_launch_regs(int kv) { return kv == PKV_KV_BF16 ? 96 : 80; }
-constexpr int kTaRoleRegs = 48;
+__host__ __device__ constexpr int ta_launch_regs(int kv) { return kv == PKV_KV_BF16 ? 96 : 72; }
+__host__ __device__ constexpr int ta_role_regs(int kv) { return kv == PKV_KV_BF16 ? 48 : 40; }
 __host__ __device__ constexpr int ta_soft_regs(int kv) {
-  return (ta_threads(kv) * ta_launch_regs(kv) - (ta_threads(kv) - 512) * kTaRoleRegs) / 512 / 8 * 8;
+  return (ta_threads(kv) * ta_launch_regs(kv) - (ta_threads(kv) - 512) * ta_role_regs(kv)) / 512 / 8 * 8;
 }
 static_assert(ta_soft_regs(PKV_KV_BF16) == 104 && ta_soft_regs(PKV_KV_INT8) == 96, "");
 
@@ -221,32 +222,28 @@ __device__ __forceinline__ float max16(const uint32_t (&x)[32], int o) {
   return fmax3f(fmax3f(a, b, c), fmax3f(d, e, f(15)), a);
 }
 
-// Rewrite 32 token rows (one per lane) of a stage whose one-byte codes lie in
-// the upper half (row r's 128 codes at region + 128 r) as 16-bit code values
-// in both halves (16-byte chunks XOR-swizzled by row % 8), as widen_stage does,
-// in loops: with everything unrolled the kernel's hot code no longer fits the
-// instruction cache.  Codes 0-63 go to the lower half, which holds no codes;
-// codes 64-127 are read before any chunk of the upper half is written.
+// Rewrite 16 token rows of a stage whose one-byte codes lie in the upper half
+// (row r's 128 codes at region + 128 r) as 16-bit code values in both halves
+// (16-byte chunks XOR-swizzled by row % 8).  Whole warp: lanes 0-15 take codes
+// 0-63 of a row each, which go to the lower half, the others codes 64-127; the
+// warp reads all of its codes before it writes.
 template <int KV, bool kBiased>
 __device__ __forceinline__ void widen_rows(uint8_t* stage, uint32_t region, int lane, uint32_t zc, int valid_rows) {
-  if (lane >= valid_rows) return;
-  const int sw = lane & 7;
-  uint8_t* hi = stage + region + lane * 128;
-  uint8_t* lo = stage + lane * 128;
-  uint4 o0, o1, x[4];
+  const int row = lane & 15, half = lane >> 4, sw = row & 7;
+  const uint8_t* from = stage + region + row * 128;
+  uint8_t* to = stage + half * region + row * 128;
+  uint4 x[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) x[c] = *reinterpret_cast<const uint4*>(hi + (((c + 4) ^ sw) << 4));
-#pragma unroll 2
-  for (int c = 0; c < 4; ++c) {
-    widen16<KV, kBiased>(*reinterpret_cast<const uint4*>(hi + ((c ^ sw) << 4)), zc, o0, o1);
-    *reinterpret_cast<uint4*>(lo + (((2 * c) ^ sw) << 4)) = o0;
-    *reinterpret_cast<uint4*>(lo + (((2 * c + 1) ^ sw) << 4)) = o1;
-  }
+  for (int c = 0; c < 4; ++c) x[c] = *reinterpret_cast<const uint4*>(from + (((4 * half + c) ^ sw) << 4));
+  __syncwarp();
+  if (row < valid_rows) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    widen16<KV, kBiased>(x[c], zc, o0, o1);
-    *reinterpret_cast<uint4*>(hi + (((2 * c) ^ sw) << 4)) = o0;
-    *reinterpret_cast<uint4*>(hi + (((2 * c + 1) ^ sw) << 4)) = o1;
+    for (int c = 0; c < 4; ++c) {
+      uint4 o0, o1;
+      widen16<KV, kBiased>(x[c], zc, o0, o1);
+      *reinterpret_cast<uint4*>(to + (((2 * c) ^ sw) << 4)) = o0;
+      *reinterpret_cast<uint4*>(to + (((2 * c + 1) ^ sw) << 4)) = o1;
+    }
   }
 }
 
@@ -289,12 +286,12 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
 
   if (tid == 0) {
     for (int s = 0; s < KS; ++s) {
-      mbar_init(&k_full[s], kI8 ? 4 : 1);  // INT8: four converter warps
+      mbar_init(&k_full[s], kI8 ? kConvWarps : 1);
       mbar_init(&k_free[s], 1);
       mbar_init(&tma_k[s], 1);
     }
     for (int s = 0; s < VS; ++s) {
-      mbar_init(&v_full[s], kOneByte ? 4 : 1);
+      mbar_init(&v_full[s], kOneByte ? kConvWarps : 1);
       mbar_init(&v_free[s], 1);
       mbar_init(&tma_v[s], 1);
     }
@@ -305,7 +302,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       mbar_init(&o_free[s], PAIR ? 8 : 16);
     }
     for (int s = 0; s < kTaRing; ++s) mbar_init(&step_full[s], 1);
-    mbar_init(q_full, kOneByte ? 4 : 1);
+    mbar_init(q_full, kOneByte ? kConvWarps : 1);
     mbar_init(q_free, 1);
     mbar_init(q_read, 16);
     mbar_init(x_full, 16);
@@ -337,9 +334,9 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
   auto wait_step = [&](uint32_t g) { return warp_wait(&step_full[g % kTaRing], (g / kTaRing) & 1u); };
 
   // the registers are shared out anew: 512 x ta_soft_regs for the softmax
-  // warps and the others' kTaRoleRegs add up to the launch's
+  // warps and the others' ta_role_regs add up to the launch's
   if (warp >= 16 && warp < 20) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTaRoleRegs));
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ta_role_regs(KV)));
   if (warp == 17) {
     // K copy warp: the share's units, a descriptor and the K pages per step
     uint32_t g = 0;
@@ -628,23 +625,25 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
   }
   } else if (warp >= 20) {
     if constexpr (kOneByte) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTaRoleRegs));
-      // converter warps: 32 rows each of a unit's query tiles, then of its
-      // steps' K (INT8) and V; K of a step before V of the step before it, the
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ta_role_regs(KV)));
+      // converter warps: 32 rows of a query tile each (one tile: the first
+      // four), then 16 rows each of the steps' K (INT8) and V; K of a step before V of the step before it, the
       // order that the products need them in
       const int cw = warp - 20;
+      constexpr int kRows = kTreeTokens / kConvWarps;
+      static_assert(kRows == 16, "");
       auto convert = [&](bool is_k, uint32_t g) -> bool {
         uint64_t* landed = is_k ? &tma_k[g % KS] : &tma_v[g % VS];
         if (!warp_wait(landed, is_k ? (g / KS) & 1u : (g / VS) & 1u)) return false;
-        uint8_t* st = (is_k ? sm + L::kK + (g % KS) * L::kKTile : sm + L::kV + (g % VS) * L::kTile) + cw * 32 * 128;
+        uint8_t* st = (is_k ? sm + L::kK + (g % KS) * L::kKTile : sm + L::kV + (g % VS) * L::kTile) + cw * kRows * 128;
         const volatile TaStep* sp = step_at(g);
-        const int rows = sp->np * BS - 32 * cw;  // of the step's pages
+        const int rows = sp->np * BS - kRows * cw;  // of the step's pages
         uint32_t zc = 0u;
         if (is_k) {
           widen_rows<KV, kI8>(st, L::kRegion, lane, zc, rows);
         } else {
           if constexpr (kI8) {
-            if (lane < rows) zc = int8_zero_const(sp->vzero[(32 * cw + lane) / BS]);
+            if ((lane & 15) < rows) zc = int8_zero_const(sp->vzero[(kRows * cw) / BS]);
           }
           widen_rows<KV, false>(st, L::kRegion, lane, zc, rows);
         }
@@ -674,8 +673,8 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         // q' has 8 significant bits, 4 in each part, so the sum is exact from
         // 2^-2 up and within 2^-10 below
         float2* qrow = reinterpret_cast<float2*>(sm + L::kQrow);
-        const int r = 32 * cw + lane;
-        for (int i = 0; i < L::kQTiles; ++i) {
+        const int r = 32 * (cw & 3) + lane;
+        if (const int i = cw >> 2; i < L::kQTiles) {
           const int tl = r / p.G, t = (2 * pair + i) * p.Tt + tl;
           const bool in = tl < p.Tt && t < p.T;
           const uint4* src = reinterpret_cast<const uint4*>(
