@@ -2,6 +2,7 @@
 // (tree_attend.cuh), and its kernel instances.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 #include <vector>
 
 #include "tree_attend.cuh"
@@ -105,23 +106,27 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
   }
   __syncthreads();
   const long long* start = a.B <= kTreePlanSmem ? start_s : a.start;
+  // quotients of what mostly fits 32 bits
+  auto div = [](long long x, int d) -> long long {
+    return (x >> 32) != 0 ? x / d : static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(d));
+  };
   // shares of at least min_steps steps
-  const int shares = static_cast<int>(min(static_cast<long long>(a.max_shares), (total + a.min_steps - 1) / a.min_steps));
+  const int shares = static_cast<int>(min(static_cast<long long>(a.max_shares), div(total + a.min_steps - 1, a.min_steps)));
   if (tid == 0) *a.shares = shares;
-  const int near = shares > 0 ? static_cast<int>(min(2ll, total / shares / 4)) : 0;
+  const int near = shares > 0 ? static_cast<int>(min(2ll, div(total, shares) / 4)) : 0;
   for (int s = tid; s <= shares; s += kTreePlanThreads) {
     TreeBound r{a.B, 0, 0, 0};
     if (s < shares) {
-      const long long pos = total * s / shares;
+      const long long pos = div(total * s, shares);
       int lo = 0, hi = a.B - 1;  // the sequence with start[lo] <= pos < start[lo + 1]
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (start[mid + 1] > pos) hi = mid; else lo = mid + 1;
       }
       const long long in = pos - start[lo];
-      const int cost = static_cast<int>((start[lo + 1] - start[lo]) / a.Hkv), nt = cost - a.item_steps;
+      const int cost = static_cast<int>(div(start[lo + 1] - start[lo], a.Hkv)), nt = cost - a.item_steps;
       r.b = lo;
-      r.kvh = static_cast<int>(in / cost);
+      r.kvh = static_cast<int>(div(in, cost));
       r.step = max(0, static_cast<int>(in - static_cast<long long>(r.kvh) * cost) - a.item_steps);
       if (r.step <= near) {
         r.step = 0;
@@ -137,7 +142,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
   }
   // zeros for inactive sequences (one warp per sequence)
   for (int b = warp; b < a.B; b += kTreePlanThreads / 32) {
-    if (a.ctx_eff[b] != 0) continue;
+    if (start[b + 1] != start[b]) continue;
     uint4* o = reinterpret_cast<uint4*>(a.out + static_cast<size_t>(b) * a.row_elems);
     for (int i = lane; i < a.row_elems / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
   }
@@ -147,11 +152,16 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
 // merge: out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p over the partials
 // of an item that shares split.  The share in which the item starts leaves it
 // as its last unit; the shares after it continue it with their first unit
-// until one ends it.  One CTA per (share, row tiles of a CTA, quarter of the
-// rows), a warp per row.
+// until one ends it.
+//
+// One CTA per (share, row tiles of a CTA, 16 rows), a warp per two rows.  The
+// partials are in L2 and few, so it is a chain of loads: bounds, a lane each,
+// then m and l of up to 16 parts of both rows by one load of the warp, next to
+// the rows of the first four parts.
 // ---------------------------------------------------------------------------
 constexpr int kTreeMergeThreads = 256;
-constexpr int kTreeMergeSplit = 4;
+constexpr int kTreeMergeRows = 2;                                        // of a warp
+constexpr int kTreeMergeCta = kTreeMergeThreads / 32 * kTreeMergeRows;   // of a CTA
 
 struct TreeMergeArgs {
   const TreeBound* bounds;
@@ -163,68 +173,107 @@ struct TreeMergeArgs {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kTreeMergeThreads) tree_merge_kernel(const TreeMergeArgs a) {
-  constexpr int kPer = D / 32;
+__global__ void __launch_bounds__(kTreeMergeThreads, 3) tree_merge_kernel(const TreeMergeArgs a) {
+  constexpr int kPer = D / 32, kRows = kTreeMergeRows, kLanes = 32 / kRows, kBatch = 4;
   pdl_trigger();
   pdl_wait();
-  const int quarter = blockIdx.x % kTreeMergeSplit;
-  const int cta = blockIdx.x / kTreeMergeSplit;
+  const int rows = a.tiles * kTaRows, slices = rows / kTreeMergeCta;
+  const int slice = blockIdx.x % slices;
+  const int cta = blockIdx.x / slices;
   const int share = cta / a.NP, pair = cta - share * a.NP;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the grid leaves out the last share that the workspace has room for)
   const int shares = *a.shares;
+  const TreeBound mine = a.bounds[share], next = a.bounds[share + 1];
   if (share + 1 >= shares) return;  // the last share splits nothing
-  const TreeBound next = a.bounds[share + 1];
-  if (next.step == 0) return;  // an item starts there
-  const TreeBound mine = a.bounds[share];
+  if (next.step == 0) return;       // an item starts there
   const bool same = mine.b == next.b && mine.kvh == next.kvh;
   if (same && mine.step > 0) return;  // the item started in an earlier share
   int last = share + 1;               // the share that ends the item
-  for (; last + 1 < shares; ++last) {
-    const TreeBound e = a.bounds[last + 1];
-    if (e.b != next.b || e.kvh != next.kvh || e.step == 0) break;
+  for (;;) {
+    const int s = last + 1 + lane;
+    bool ends = true;
+    if (s < shares) {
+      const TreeBound e = a.bounds[s];
+      ends = e.b != next.b || e.kvh != next.kvh || e.step == 0;
+    }
+    const unsigned found = __ballot_sync(kFull, ends);
+    last += found ? __ffs(found) - 1 : 32;
+    if (found) break;
   }
   const int parts = last - share + 1;
-  const int rows = a.tiles * kTaRows;
   // the owner's partial is its first unit's place if the share starts with the item
   const size_t first = (static_cast<size_t>(cta) * 2 + (same ? 0 : 1)) * rows;
   const size_t stride = static_cast<size_t>(a.NP) * 2 * rows;  // from a share's partials to the next one's
   const size_t cont = (static_cast<size_t>(cta) * 2) * rows;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int rr = quarter + kTreeMergeSplit * warp; rr < rows; rr += kTreeMergeSplit * (kTreeMergeThreads / 32)) {
-    const int r = rr % kTaRows, tile = (a.tiles == 2 ? 2 * pair : 0) + rr / kTaRows;
-    const int tl = r / a.G, t = tile * a.Tt + tl;
-    if (tl >= a.Tt || t >= a.T) continue;
-    auto at = [&](int p) { return (p == 0 ? first : cont + stride * p) + rr; };
-    float M = -INFINITY;
-    for (int p = lane; p < parts; p += 32) M = fmaxf(M, a.part_ml[at(p)].x);
+  const int rr0 = slice * kTreeMergeCta + warp * kRows;
+  const int tile = (a.tiles == 2 ? 2 * pair : 0) + rr0 / kTaRows;
+  unsigned live = 0;  // rows with a node
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-    float acc[kPer], sum = 0.f;
+  for (int k = 0; k < kRows; ++k) {
+    const int tl = (rr0 + k) % kTaRows / a.G;
+    if (tl < a.Tt && tile * a.Tt + tl < a.T) live |= 1u << k;
+  }
+  if (live == 0) return;
+  auto at = [&](int k, int p) { return (p == 0 ? first : cont + stride * p) + rr0 + k; };
+  using Vec = std::conditional_t<kPer == 4, float4, float2>;
+  auto load = [&](int k, int p) -> Vec {
+    Vec v{};
+    if (p < parts && ((live >> k) & 1u)) v = *reinterpret_cast<const Vec*>(a.part_o + at(k, p) * D + lane * kPer);
+    return v;
+  };
+  Vec v[kBatch][kRows];  // parts at a time
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-      const float2 ml = a.part_ml[at(p)];
-      // (an empty partial has O = 0, or the row's fixed value)
-      const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-      sum = fmaf(w, ml.y, sum);
-      const float* src = a.part_o + at(p) * D + lane * kPer;
-      if constexpr (kPer == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-        acc[2] = fmaf(w, v.z, acc[2]);
-        acc[3] = fmaf(w, v.w, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-      }
+  for (int q = 0; q < kBatch; ++q)
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) v[q][k] = load(k, q);
+  const int mk = lane / kLanes, mp = lane % kLanes;  // this lane's row and part
+  auto load_ml = [&](int p) { return p < parts && ((live >> mk) & 1u) ? a.part_ml[at(mk, p)] : make_float2(-INFINITY, 0.f); };
+  float2 ml = load_ml(mp);
+  float M = ml.x;
+  for (int p = mp + kLanes; p < parts; p += kLanes) M = fmaxf(M, load_ml(p).x);
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+  float acc[kRows][kPer], sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kRows; ++k)
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) acc[k][j] = 0.f;
+  for (int p0 = 0; p0 < parts; p0 += kLanes) {
+    if (p0 > 0) ml = load_ml(p0 + mp);
+    // (an empty partial has O = 0, or the row's fixed value)
+    const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+    sum = fmaf(w, ml.y, sum);
+    const int pn = min(kLanes, parts - p0);
+    for (int pp = 0; pp < pn; pp += kBatch) {
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q)
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          const float wq = __shfl_sync(kFull, w, kLanes * k + pp + q);  // (0 past the last part, and its row zeros)
+          const float* x = reinterpret_cast<const float*>(&v[q][k]);
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) acc[k][j] = fmaf(wq, x[j], acc[k][j]);
+          v[q][k] = load(k, p0 + pp + kBatch + q);
+        }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    __nv_bfloat16* o = a.out + (static_cast<size_t>(next.b * a.T + t) * a.Hq + next.kvh * a.G + (r - tl * a.G)) * D + lane * kPer;
+  }
 #pragma unroll
-    for (int j = 0; j < kPer; j += 2)
-      *reinterpret_cast<__nv_bfloat162*>(o + j) = __floats2bfloat162_rn(acc[j] * inv, acc[j + 1] * inv);
+  for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  const float inv_mine = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const float inv = __shfl_sync(kFull, inv_mine, kLanes * k);
+    if (!((live >> k) & 1u)) continue;
+    const int r = (rr0 + k) % kTaRows, tl = r / a.G;
+    __nv_bfloat16* o = a.out + (static_cast<size_t>(next.b * a.T + tile * a.Tt + tl) * a.Hq + next.kvh * a.G + (r - tl * a.G)) * D + lane * kPer;
+    uint32_t w[kPer / 2];
+#pragma unroll
+    for (int j = 0; j < kPer; j += 2) w[j / 2] = pack_bf16x2(acc[k][j] * inv, acc[k][j + 1] * inv);
+    if constexpr (kPer == 4)
+      *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(o) = w[0];
   }
 }
 
@@ -383,7 +432,7 @@ cudaError_t launch_tree_attend(const DecodeLaunch& L, uint8_t* ws, int* launched
   // 3. merge of the items that shares split
   if (L.tree_shares > 1) {
     const TreeMergeArgs ma{bounds, shares, p.part_ml, p.part_o, p.out, L.Hq, L.G, L.T, L.Tt, NP, pair ? 2 : 1};
-    cfg.gridDim = dim3(static_cast<unsigned>((L.tree_shares - 1) * NP * kTreeMergeSplit));
+    cfg.gridDim = dim3(static_cast<unsigned>((L.tree_shares - 1) * NP * (ma.tiles * kTaRows / kTreeMergeCta)));
     cfg.blockDim = dim3(kTreeMergeThreads);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = (L.ev_end == nullptr) ? 1 : 0;

@@ -364,7 +364,16 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       const int npages = (t1 - t0 + BS - 1) / BS;
       const int base = ctx - (p.tree.node_counts != nullptr ? __ldg(p.tree.node_counts + b) : p.T);
       const int* trow = p.block_tables + static_cast<size_t>(b) * p.MB + t0 / BS;
-      // lane i holds page i of a run of 32 pages, and of the next run
+      if constexpr (kOneByte) {  // the unit's queries, which the converters read once the unit before is done
+        const int lines = 2 * p.G;
+        for (int x = lane; x < L::kQTiles * p.Tt * lines; x += 32) {
+          const int t = 2 * pair * p.Tt + x / lines;
+          if (t < p.T)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (static_cast<size_t>(b * p.T + t) * p.Hq + kvh * p.G) * D + x % lines * 64));
+        }
+      }
+      // lane i holds page i of a run of 32 pages, and of the next run (its id:
+      // of the two next)
       auto load_ids = [&](int q) { return q < npages ? __ldg(trow + q) : 0; };
       auto load_par = [&](int q, int id) {
         float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -382,15 +391,16 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         }
         return r;
       };
-      int id = load_ids(lane), id_next = load_ids(lane + 32);
+      int id = load_ids(lane), id_next = load_ids(lane + 32), id_after = load_ids(lane + 64);
       float4 par = load_par(lane, id), par_next = load_par(lane + 32, id_next);
       for (int j = 0; j < n; ++j, ++g) {
         const int q0 = j * PPI;  // the step's first page
         if (q0 > 0 && (q0 & 31) == 0) {
           id = id_next;
           par = par_next;
-          id_next = load_ids(q0 + 32 + lane);
+          id_next = id_after;
           par_next = load_par(q0 + 32 + lane, id_next);
+          id_after = load_ids(q0 + 64 + lane);
         }
         if (g >= KS && !warp_wait(&k_free[g % KS], ((g - KS) / KS) & 1u)) {
           timed_out = true;
@@ -626,8 +636,8 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
   } else if (warp >= 20) {
     if constexpr (kOneByte) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ta_role_regs(KV)));
-      // converter warps: 32 rows of a query tile each (one tile: the first
-      // four), then 16 rows each of the steps' K (INT8) and V; K of a step before V of the step before it, the
+      // converter warps: 16 rows each of a unit's query tiles, then of its
+      // steps' K (INT8) and V; K of a step before V of the step before it, the
       // order that the products need them in
       const int cw = warp - 20;
       constexpr int kRows = kTreeTokens / kConvWarps;
@@ -672,64 +682,65 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         // |q'| in [2^7, 2^8) as qh = e4m3(q') and ql = e4m3(q' - qh): a bf16
         // q' has 8 significant bits, 4 in each part, so the sum is exact from
         // 2^-2 up and within 2^-10 below
+        // Two lanes a row: 64 elements each, to 16 bits (f16 holds every q'
+        // above 2^-14 exactly) and from there to the two parts.
         float2* qrow = reinterpret_cast<float2*>(sm + L::kQrow);
-        const int r = 32 * (cw & 3) + lane;
-        if (const int i = cw >> 2; i < L::kQTiles) {
+        const int r = kRows * cw + (lane & 15), half = lane >> 4;
+#pragma unroll 1
+        for (int i = 0; i < L::kQTiles; ++i) {
           const int tl = r / p.G, t = (2 * pair + i) * p.Tt + tl;
           const bool in = tl < p.Tt && t < p.T;
           const uint4* src = reinterpret_cast<const uint4*>(
-              p.q + (static_cast<size_t>(b * p.T + (in ? t : 0)) * p.Hq + kvh * p.G + (in ? r - tl * p.G : 0)) * D);
-          uint32_t mx = 0;  // largest |q| as bf16 bits
-#pragma unroll 8
-          for (int c = 0; c < 16; ++c) {
-            const uint4 w = __ldg(src + c);
-            const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+              p.q + (static_cast<size_t>(b * p.T + (in ? t : 0)) * p.Hq + kvh * p.G + (in ? r - tl * p.G : 0)) * D + 64 * half);
+          uint32_t mx = 0;  // largest |q| as bf16 bits, of both 16-bit halves
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx = max(mx, max(w4[e] & 0x7fffu, (w4[e] >> 16) & 0x7fffu));
+          for (int c = 0; c < 8; ++c) {
+            const uint4 w = __ldg(src + c);
+            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
           }
+          mx = max(mx & 0xffffu, mx >> 16);
+          mx = max(mx, __shfl_xor_sync(kFull, mx, 16));
           if (!in) mx = 0;
           const int kq = mx == 0 ? 0 : max(-100, min(100, static_cast<int>(mx >> 7) - 127 - (kF8K ? 7 : 14)));
-          const float sc = in ? __uint_as_float(static_cast<uint32_t>(127 - kq) << 23) : 0.f;  // 2^-kq; 0: no row
+          const float sc = __uint_as_float(static_cast<uint32_t>(127 - kq) << 23);  // 2^-kq
           float qsum = 0.f;
-          uint8_t* qt = sm + L::kQ + i * L::kTile;
+          uint8_t* qt = sm + L::kQ + i * L::kTile + r * 128 + (kF8K ? 0u : half * L::kRegion);
 #pragma unroll 2
-          for (int c2 = 0; c2 < 8; ++c2) {  // 16 elements
-            uint32_t wh[4], wl[4], wf[8];
+          for (int c2 = 0; c2 < 4; ++c2) {  // 16 elements
+            uint32_t wf[8], wl[4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint4 w = __ldg(src + 2 * c2 + h);
-              const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+              const uint32_t w4[4] = {in ? w.x : 0u, in ? w.y : 0u, in ? w.z : 0u, in ? w.w : 0u};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float2 v = make_float2(in ? bf16lo_to_f32(w4[e]) * sc : 0.f, in ? bf16hi_to_f32(w4[e]) * sc : 0.f);
+                const uint32_t f = pack_f16x2(bf16lo_to_f32(w4[e]) * sc, bf16hi_to_f32(w4[e]) * sc);
                 if constexpr (kF8K) {
-                  const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-                  const float2 hv = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3)));
-                  const __nv_fp8x2_storage_t lo =
-                      __nv_cvt_float2_to_fp8x2(make_float2(v.x - hv.x, v.y - hv.y), __NV_SATFINITE, __NV_E4M3);
+                  const __half2_raw fr = *reinterpret_cast<const __half2_raw*>(&f);
+                  const __nv_fp8x2_storage_t hi = __nv_cvt_halfraw2_to_fp8x2(fr, __NV_SATFINITE, __NV_E4M3);
+                  const __half2 rest = __hsub2(__half2(fr), __half2(__nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3)));
+                  const __nv_fp8x2_storage_t lo = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(rest), __NV_SATFINITE, __NV_E4M3);
                   const int k = 2 * h + (e >> 1), s = 16 * (e & 1);
-                  wh[k] = (s ? wh[k] : 0u) | static_cast<uint32_t>(hi) << s;
+                  wf[k] = (s ? wf[k] : 0u) | static_cast<uint32_t>(hi) << s;
                   wl[k] = (s ? wl[k] : 0u) | static_cast<uint32_t>(lo) << s;
                 } else {
-                  const uint32_t f = pack_f16x2(v.x, v.y);
                   wf[4 * h + e] = f;
                   const float2 fv = __half22float2(*reinterpret_cast<const __half2*>(&f));
                   qsum += fv.x + fv.y;
                 }
               }
             }
-            if constexpr (kF8K) {
-              uint8_t* d = qt + r * 128 + ((c2 ^ (r & 7)) << 4);
-              *reinterpret_cast<uint4*>(d) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-              *reinterpret_cast<uint4*>(d + L::kRegion) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
-            } else {
-              uint8_t* d = qt + (c2 >> 2) * L::kRegion + r * 128;
-              const int c = 2 * (c2 & 3);
-              *reinterpret_cast<uint4*>(d + ((c ^ (r & 7)) << 4)) = make_uint4(wf[0], wf[1], wf[2], wf[3]);
-              *reinterpret_cast<uint4*>(d + (((c + 1) ^ (r & 7)) << 4)) = make_uint4(wf[4], wf[5], wf[6], wf[7]);
-            }
+            const int c = kF8K ? 4 * half + c2 : 2 * c2;
+            *reinterpret_cast<uint4*>(qt + ((c ^ (r & 7)) << 4)) = make_uint4(wf[0], wf[1], wf[2], wf[3]);
+            if constexpr (kF8K)
+              *reinterpret_cast<uint4*>(qt + L::kRegion + ((c ^ (r & 7)) << 4)) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+            else
+              *reinterpret_cast<uint4*>(qt + (((c + 1) ^ (r & 7)) << 4)) = make_uint4(wf[4], wf[5], wf[6], wf[7]);
           }
-          qrow[i * kTaRows + r] = make_float2(__uint_as_float(static_cast<uint32_t>(127 + kq) << 23), qsum);
+          qsum += __shfl_xor_sync(kFull, qsum, 16);
+          // (a row with an infinity or NaN is NaN, as E4M3 codes cannot hold it)
+          const float back = mx < 0x7f80u ? __uint_as_float(static_cast<uint32_t>(127 + kq) << 23) : __uint_as_float(0x7fffffffu);
+          if (half == 0) qrow[i * kTaRows + r] = make_float2(back, qsum);
         }
         fence_proxy_async_smem();
         __syncwarp();
