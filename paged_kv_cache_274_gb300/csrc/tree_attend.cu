@@ -14,8 +14,14 @@ namespace pkv {
 // planner
 // ---------------------------------------------------------------------------
 constexpr int kTreePlanThreads = 1024;
-constexpr int kTreeItemSteps = 2;    // cost of an item besides its steps, in steps
 constexpr int kTreePlanSmem = 2048;  // sequences whose prefix sums are searched in shared memory
+
+// Cost of an item besides its steps, in steps: its queries, the pipeline that
+// drains and fills again, its output.  Measured on 160 steps a CTA cut into 1
+// to 16 items: 3 to 4 us an item of bf16 caches, 8 of one-byte ones (a step:
+// 0.7 to 1.0, 1.3 to 1.7 us).  With 2 for all, ragged batches took 74 instead
+// of 65 us (head_dim 64), 241 instead of 225 (INT8); 6 and 9 change nothing.
+static int tree_item_steps(int kv_dtype, bool pair) { return pair ? 3 : kv_dtype == PKV_KV_BF16 ? 4 : 6; }
 
 struct TreePlanArgs {
   const int32_t* context_lens;
@@ -380,7 +386,7 @@ cudaError_t launch_tree_attend(const DecodeLaunch& L, uint8_t* ws, int* launched
   // 1. planner
   TreePlanArgs pa{L.context_lens, L.node_counts, ctx_eff, reinterpret_cast<long long*>(ws + w.start), bounds, shares,
                   static_cast<__nv_bfloat16*>(L.out), L.err, L.B, L.T, L.Hkv, L.MB * L.bs, L.T * L.Hq * L.D,
-                  L.tree_shares, L.tree_min_steps, kTreeItemSteps};
+                  L.tree_shares, L.tree_min_steps, tree_item_steps(L.kv_dtype, pair)};
   const TreeScan scan = tree_scan_of(L, poison);
   cfg.gridDim = dim3(1 + tree_scan_ctas(L, kTreePlanThreads / 32));
   cfg.blockDim = dim3(kTreePlanThreads);
