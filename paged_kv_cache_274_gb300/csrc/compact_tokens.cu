@@ -65,7 +65,9 @@ __device__ __forceinline__ uint4 requantise(uint4 x, const float* params, size_t
 
 template <int KV>  // pkv_kv_dtype
 __global__ void __launch_bounds__(kCompactThreads) compact_tokens_kernel(const CompactArgs a) {
-  __shared__ int64_t s_src[PKV_MAX_QUERY_TOKENS], s_dst[PKV_MAX_QUERY_TOKENS];  // block * bs + token, per row
+  // per row: blocks (-1: stays where it is) and places in them
+  __shared__ int s_src[PKV_MAX_QUERY_TOKENS], s_dst[PKV_MAX_QUERY_TOKENS];
+  __shared__ uint16_t s_from[PKV_MAX_QUERY_TOKENS], s_to[PKV_MAX_QUERY_TOKENS];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x;
@@ -84,14 +86,17 @@ __global__ void __launch_bounds__(kCompactThreads) compact_tokens_kernel(const C
         err |= PKV_DEVERR_TREE;
       } else if (u != i) {
         const int ps = base + u, pd = base + i;
-        const int es = a.block_tables[static_cast<size_t>(b) * a.MB + ps / a.bs];
-        const int ed = a.block_tables[static_cast<size_t>(b) * a.MB + pd / a.bs];
+        const int js = ps / a.bs, jd = pd / a.bs;
+        const int es = a.block_tables[static_cast<size_t>(b) * a.MB + js];
+        const int ed = a.block_tables[static_cast<size_t>(b) * a.MB + jd];
         if (static_cast<unsigned>(es) >= static_cast<unsigned>(a.NB) || static_cast<unsigned>(ed) >= static_cast<unsigned>(a.NB))
           err |= PKV_DEVERR_BLOCK_ID;
-        s_src[i] = static_cast<int64_t>(es) * a.bs + ps % a.bs;
-        s_dst[i] = static_cast<int64_t>(ed) * a.bs + pd % a.bs;
+        s_src[i] = es;
+        s_dst[i] = ed;
+        s_from[i] = static_cast<uint16_t>(ps - js * a.bs);
+        s_to[i] = static_cast<uint16_t>(pd - jd * a.bs);
       } else {
-        s_src[i] = s_dst[i] = -1;  // stays where it is
+        s_src[i] = -1;
       }
     }
   }
@@ -117,19 +122,19 @@ __global__ void __launch_bounds__(kCompactThreads) compact_tokens_kernel(const C
     uint4* cache = reinterpret_cast<uint4*>(is_v ? a.vc : a.kc);
     const float* params = is_v ? a.vs : a.ks;
     const int64_t slot_pages = static_cast<int64_t>(slot) * a.NB;
-    auto page_of = [&](int64_t token) { return (slot_pages + token / a.bs) * a.Hkv + h; };
-    auto chunk_of = [&](int64_t token) { return (page_of(token) * a.bs + token % a.bs) * row_chunks + chunk; };
+    auto page_of = [&](int block) { return (slot_pages + block) * a.Hkv + h; };
+    auto chunk_of = [&](int block, int token) { return (page_of(block) * a.bs + token) * row_chunks + chunk; };
     for (int i0 = first; i0 < take; i0 += kCompactBatch) {
       uint4 x[kCompactBatch];
 #pragma unroll
       for (int k = 0; k < kCompactBatch; ++k)
-        if (i0 + k < take) x[k] = cache[chunk_of(s_src[i0 + k])];
+        if (i0 + k < take) x[k] = cache[chunk_of(s_src[i0 + k], s_from[i0 + k])];
 #pragma unroll
       for (int k = 0; k < kCompactBatch; ++k)
         if (i0 + k < take) {
-          const int64_t src = s_src[i0 + k], dst = s_dst[i0 + k];
-          if constexpr (KV != PKV_KV_BF16) x[k] = requantise<KV>(x[k], params, page_of(src), page_of(dst));
-          cache[chunk_of(dst)] = x[k];
+          const int dst = s_dst[i0 + k];
+          if constexpr (KV != PKV_KV_BF16) x[k] = requantise<KV>(x[k], params, page_of(s_src[i0 + k]), page_of(dst));
+          cache[chunk_of(dst, s_to[i0 + k])] = x[k];
         }
     }
   }

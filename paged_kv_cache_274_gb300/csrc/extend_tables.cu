@@ -16,7 +16,8 @@
 // the CTAs share the token rows, the taken and the returned blocks, each found
 // by binary search in its prefix sums.  Counts and the ring's head may be
 // updated in place although every CTA reads them: the CTA that arrives last,
-// when all others have read theirs, writes them.
+// when all others have read theirs, writes them (with one CTA, or arrays apart,
+// nobody waits).
 #include <algorithm>
 
 #include "pkv_device.cuh"
@@ -25,6 +26,7 @@
 namespace pkv {
 
 constexpr int kExtThreads = 512;
+constexpr int kExtRun = 4;  // token rows of a thread where there are many
 
 struct ExtRequest {
   int seq, add, held, need, gone, borrowed;
@@ -71,6 +73,7 @@ __global__ void __launch_bounds__(kExtThreads) extend_tables_kernel(const Extend
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
   pdl_wait();
+  const int head = a.state_in[0], free_blocks = a.state_in[1];
 
   // prefix sums: a run of consecutive requests per thread, one scan over the threads
   const int per = (B + kExtThreads - 1) / kExtThreads;
@@ -127,7 +130,6 @@ __global__ void __launch_bounds__(kExtThreads) extend_tables_kernel(const Extend
   }
   __syncthreads();
 
-  const int head = a.state_in[0], free_blocks = a.state_in[1];
   const bool pool_ok = head >= 0 && head < a.NB && free_blocks >= 0 &&
                        static_cast<long long>(free_blocks) + rel[B] <= a.NB;
   auto ring_at = [&](int k) -> uint32_t {  // position head + k, k < 2 NB
@@ -146,27 +148,56 @@ __global__ void __launch_bounds__(kExtThreads) extend_tables_kernel(const Extend
   unsigned err = 0;
   const int first = blockIdx.x * kExtThreads + tid, stride = gridDim.x * kExtThreads;
 
-  // token rows
-  for (int i = first; i < N; i += stride) {
-    long long slot = -1;
-    int pos = 0;
-    if (i < tok[B]) {
-      const int b = ext_find(tok, B, i);
-      const ExtRequest r = ext_request(a, b);
-      if (granted(b, r)) {
-        const int p = r.seq + (i - tok[b]);
-        const int j = p / a.bs;
-        const int id = j < r.held ? a.block_tables[static_cast<size_t>(b) * a.MB + j] : a.ring[ring_at(blk[b] + j - r.held)];
-        if (static_cast<uint32_t>(id) < NB) {
-          slot = static_cast<long long>(id) * a.bs + (p - j * a.bs);
-          pos = p;
-        } else {
-          err |= PKV_DEVERR_BLOCK_ID;
-        }
+  // token rows: one per thread, or runs of kExtRun where there are many, which
+  // mostly share their request and their block
+  const int run = N > stride ? kExtRun : 1;
+  const bool vec = run == kExtRun && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0 && (reinterpret_cast<uintptr_t>(a.positions) & 15) == 0;
+  for (long long i0 = static_cast<long long>(first) * run; i0 < N; i0 += static_cast<long long>(stride) * run) {
+    long long slot[kExtRun];
+    int pos[kExtRun];
+    int b = -1, b_end = 0, block = -1, id = 0;
+    bool ok = false;
+    ExtRequest r{};
+#pragma unroll
+    for (int u = 0; u < kExtRun; ++u) {
+      slot[u] = -1;
+      pos[u] = 0;
+      if (u >= run || i0 + u >= tok[B]) continue;
+      const int i = static_cast<int>(i0 + u);
+      if (b < 0 || i >= b_end) {
+        b = ext_find(tok, B, i);
+        b_end = tok[b + 1];
+        r = ext_request(a, b);
+        ok = granted(b, r);
+        block = -1;
+      }
+      if (!ok) continue;
+      const int p = r.seq + (i - tok[b]);
+      const int j = p / a.bs;
+      if (j != block) {
+        block = j;
+        id = j < r.held ? a.block_tables[static_cast<size_t>(b) * a.MB + j] : a.ring[ring_at(blk[b] + j - r.held)];
+      }
+      if (static_cast<uint32_t>(id) < NB) {
+        slot[u] = static_cast<long long>(id) * a.bs + (p - j * a.bs);
+        pos[u] = p;
+      } else {
+        err |= PKV_DEVERR_BLOCK_ID;
       }
     }
-    a.slots[i] = slot;
-    if (a.positions != nullptr) a.positions[i] = pos;
+    if (vec && i0 + kExtRun <= N) {
+      longlong2* s2 = reinterpret_cast<longlong2*>(a.slots + i0);
+      s2[0] = make_longlong2(slot[0], slot[1]);
+      s2[1] = make_longlong2(slot[2], slot[3]);
+      if (a.positions != nullptr) *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kExtRun; ++u)
+        if (u < run && i0 + u < N) {
+          a.slots[i0 + u] = slot[u];
+          if (a.positions != nullptr) a.positions[i0 + u] = pos[u];
+        }
+    }
   }
   if (pool_ok) {
     // taken blocks, into the requests' rows of the table (entries past those
@@ -201,14 +232,21 @@ __global__ void __launch_bounds__(kExtThreads) extend_tables_kernel(const Extend
   }
   if (err) atomicOr(a.err, err);
 
-  // counts and the ring's state: by the last CTA, once all have read them
+  // Counts and the ring's state, once every CTA has read them: by the only
+  // CTA, by the first where they do not go where they came from, else by the
+  // last one to arrive.
   __syncthreads();
-  if (tid == 0) {
-    __threadfence();
-    last_s = atomicInc(reinterpret_cast<unsigned*>(a.state_in) + 2, gridDim.x - 1) == gridDim.x - 1;  // wraps to 0
+  const bool apart = a.counts_out != a.counts_in && a.state_out != a.state_in;
+  if (gridDim.x > 1 && !apart) {
+    if (tid == 0) {
+      __threadfence();
+      last_s = atomicInc(reinterpret_cast<unsigned*>(a.state_in) + 2, gridDim.x - 1) == gridDim.x - 1;  // wraps to 0
+    }
+    __syncthreads();
+    if (!last_s) return;
+  } else if (blockIdx.x > 0) {
+    return;
   }
-  __syncthreads();
-  if (!last_s) return;
   int taken = 0;
   for (int b = tid; b < B; b += kExtThreads) {
     const ExtRequest r = ext_request(a, b);
@@ -236,7 +274,7 @@ cudaError_t launch_extend_tables(const ExtendArgs& a, int num_sms, cudaStream_t 
     const cudaError_t e = cudaFuncSetAttribute(extend_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  const int grid = std::max(1, std::min(num_sms, std::max((a.N + kExtThreads - 1) / kExtThreads, (a.B + 63) / 64)));
+  const int grid = std::max(1, std::min(num_sms, std::max((a.N + kExtThreads - 1) / kExtThreads, (a.B + 255) / 256)));
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
