@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
   __shared__ long long warp_tot[kTreePlanThreads / 32];
   __shared__ long long carry_s;
   __shared__ long long start_s[kTreePlanSmem + 1];
+  __shared__ int ctx_s[kTreePlanSmem];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) carry_s = 0;
   __syncthreads();
@@ -75,6 +76,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
       }
       if (nodes == 0) c = 0;  // every row is zero
       a.ctx_eff[b] = c;
+      if (a.B <= kTreePlanSmem) ctx_s[b] = c;
       steps = c == 0 ? 0 : static_cast<long long>((c + kTreeTokens - 1) / kTreeTokens + a.item_steps) * a.Hkv;
     }
     long long x = steps;
@@ -144,6 +146,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
         }
       }
     }
+    if (r.b < a.B) r.ctx = a.B <= kTreePlanSmem ? ctx_s[r.b] : a.ctx_eff[r.b];
     a.bounds[s] = r;
   }
   // zeros for inactive sequences (one warp per sequence)

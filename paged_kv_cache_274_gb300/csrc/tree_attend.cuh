@@ -341,16 +341,20 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
     // K copy warp: the share's units, a descriptor and the K pages per step
     uint32_t g = 0;
     TreeBound at{0, 0, 0, 0}, end{0, 0, 0, 0};
-    if (share < __ldg(p.shares)) {
-      at = p.bounds[share];
-      end = p.bounds[share + 1];
+    {  // (loaded side by side: every share has its place)
+      const int shares = __ldg(p.shares);
+      const TreeBound b0 = p.bounds[share], b1 = p.bounds[share + 1];
+      if (share < shares) {
+        at = b0;
+        end = b1;
+      }
     }
     int b = at.b, kvh = at.kvh, j0 = at.step;
     const uint64_t policy = p.NP > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
     bool first_unit = true;
     float vref = 0.f;
     while (!timed_out && (b < end.b || (b == end.b && (kvh < end.kvh || (kvh == end.kvh && j0 < end.step))))) {
-      const int ctx = __ldg(p.ctx_eff + b);
+      const int ctx = b == at.b ? at.ctx : __ldg(p.ctx_eff + b);
       const int nt = (ctx + kTreeTokens - 1) / kTreeTokens;
       if (nt == 0) {  // an inactive sequence
         ++b;

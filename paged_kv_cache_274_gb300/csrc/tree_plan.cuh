@@ -14,7 +14,7 @@ constexpr int kTreeTokens = 128;  // tokens of a step
 struct TreeBound {
   int b, kvh;  // item (b = batch, kvh = 0: the end)
   int step;    // step of the item (0: the share starts with the item)
-  int pad;
+  int ctx;   // the sequence's validated length
 };
 
 }  // namespace pkv
