@@ -417,7 +417,14 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
   // 16 rows per KV head (172 us at 4 tokens, one tile), tcgen05 tiles from 32
   // rows on (kernel 173 vs 234 us at 8 tokens, 173 vs 451 at 16, 183 vs 865
   // at 32, 583 vs 3402 at 128)
-  if (math == PKV_MATH_AUTO) math = (tc_ok && static_cast<long long>(T) * G > 16) ? PKV_MATH_TC : PKV_MATH_MMA;
+  // drafted trees, 8 KV heads, mma.sync against tcgen05: bf16 with head_dim 128
+  // no case for mma.sync (8 rows: 30 vs 15 us for 1 x 1024 tokens, 25 vs 24 for
+  // 1 x 16384, 173 vs 168 for 64 x 4096); head_dim 64 up to 8 rows (64 x 4096:
+  // 91 vs 113 us, 16 rows: 106 vs 112, and 36 vs 22 for 16 x 1024); one-byte
+  // caches up to 16 rows (64 x 4096: E4M3 155 vs 190 us, INT8 145 vs 239; 20
+  // rows: 264 vs 190, 248 vs 239)
+  const long long mma_rows = !tree || c->dtype != PKV_KV_BF16 ? 16 : c->head_dim == 64 ? 8 : 0;
+  if (math == PKV_MATH_AUTO) math = (tc_ok && static_cast<long long>(T) * G > mma_rows) ? PKV_MATH_TC : PKV_MATH_MMA;
   if (math == PKV_MATH_TC && !tc_ok)
     return fail(PKV_ERR_UNSUPPORTED, "tcgen05 tiles need T > 1, head_dim 128 and G <= 128");
   if (math == PKV_MATH_MMA && G > 16)
@@ -458,7 +465,7 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
   if (!tc && (warps < 1 || warps > 8)) return fail(PKV_ERR_INVALID_ARG, "warps_per_cta %d outside 1..8", warps);
   if (stages < 2 || stages > 8) return fail(PKV_ERR_INVALID_ARG, "stages %d outside 2..8", stages);
   if (tree_tc) {
-    warps = c->dtype == PKV_KV_BF16 ? 20 : 24;
+    warps = c->dtype == PKV_KV_BF16 ? 20 : 28;
     stages = 2;
   }
   const size_t smem = tree_tc ? pkv::tree_attend_smem_bytes(c->dtype, c->head_dim, NT > 1)

@@ -35,11 +35,12 @@ def _plan(lib, d, B, T, Hq, MB, opts=None):
 
 
 def test_tree_plans(lib):
-    st, plan = _plan(lib, _desc(), 8, 1, 32, 64)
-    assert st == 0 and plan.math == pkv.MATH_MMA
-    st, plan = _plan(lib, _desc(num_kv_heads=1), 8, 1, 32, 64)   # 32 heads on one KV head, one node
-    assert st == 0 and plan.math == pkv.MATH_TC
-    st, plan = _plan(lib, _desc(), 8, 32, 32, 64)
+    # rows (nodes x heads of a KV head) up to which mma.sync is chosen
+    for dtype, D, rows in ((0, 128, 0), (0, 64, 8), (1, 128, 16), (2, 128, 16)):
+        for T in (1, 2, 3, 4, 5, 32):
+            st, plan = _plan(lib, _desc(dtype=dtype, head_dim=D), 8, T, 32, 64)
+            assert st == 0 and plan.math == (pkv.MATH_MMA if 4 * T <= rows else pkv.MATH_TC)
+    st, plan = _plan(lib, _desc(dtype=1, num_kv_heads=1), 8, 1, 32, 64)   # 32 heads on one KV head, one node
     assert st == 0 and plan.math == pkv.MATH_TC
     assert _plan(lib, _desc(), 8, 4, 32, 64, pkv.decode_opts(math=pkv.MATH_FFMA))[0] == 2
     assert _plan(lib, _desc(), 8, 1, 32, 64, pkv.decode_opts(math=pkv.MATH_FFMA))[0] == 2
@@ -59,7 +60,7 @@ def test_tree_plans(lib):
 def test_tcgen05_tree_plans(lib, dtype, D, T):
     st, plan = _plan(lib, _desc(dtype=dtype, head_dim=D), 8, T, 32, 64)
     assert st == 0 and plan.math == pkv.MATH_TC and plan.kernels_per_call == (3 if T <= 512 else 2)
-    assert plan.smem_bytes_per_cta <= 227 * 1024 and plan.warps_per_cta == (20 if dtype == 0 else 24)
+    assert plan.smem_bytes_per_cta <= 227 * 1024 and plan.warps_per_cta == (20 if dtype == 0 else 28)
     assert plan.row_tiles == -(-T // min(T, 32))
     # partials: at most two per CTA, whatever the lengths
     rows = 128 if plan.row_tiles == 1 else 256
