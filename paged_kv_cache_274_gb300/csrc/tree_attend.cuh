@@ -7,34 +7,45 @@
 // tree and to the nodes of its mask row (tree_mask.cuh).  The rows form tiles
 // of 128 (M of the MMA); the cache is stepped through 128 tokens at a time.
 //
-// What bounds it: with one tile of rows the cache bytes.  128 tokens of one KV
-// head are 64 KiB (bf16, D 128) or 32 KiB (one byte), about 2800 or 1400
-// cycles of one SM's share of HBM, against 1024 cycles of tensor pipe for
-// S = Q K^T and O += P V and some 700 issue cycles of softmax per
-// sub-partition.  With two and more tiles the tensor pipe.
+// What bounds it: with one tile of rows the cache bytes, 64 KiB (bf16, D 128)
+// or 32 KiB (one byte) per 128 tokens of one KV head, 1.47 or 0.73 us of an
+// SM's share of the measured HBM rate, next to 0.67 us of tensor pipe (at the
+// measured bf16 rate) for S = Q K^T and O += P V; with two tiles the tensor
+// pipe, 1.34 us.  Measured per step of 128 tokens with the cache in L2: bf16
+// 0.87 to 1.0 us with one tile, 1.65 with two (D 64: 0.70 to 0.76, 1.42), E4M3
+// 1.22 to 1.4 and 2.35, INT8 1.6 to 1.75 and 3.4.  So bf16 batches of one tile
+// run at HBM speed (64 sequences of 2048 to 4096 tokens, 32 nodes, 8 KV heads:
+// 158 us with plan and merge, 0.79 of the copy rate), long contexts with many
+// rows at 0.63 of the bf16 peak (4 x 32k tokens, 64 nodes, 8 heads a KV head:
+// 220 us), and one-byte caches at the issue rate of the sub-partitions: 1600
+// instructions a step each, against 940 of bf16 caches, for the page scales
+// and the widening.
 //
 // One CTA per SM, no CTA-wide barrier inside the loop:
-//   * Two streams of softmax warps (four warps each, one row per thread), each
-//     with its own S and O in tensor memory (S0 S1 O0 O1, 128 columns each), so
-//     that the products of one stream run while the other's softmax does.
-//     PAIR: the streams hold two row tiles of one KV head and read every step
-//     of the cache together.  Otherwise there is one row tile, stream 0 takes
-//     the even steps and stream 1 the odd ones, and a work unit ends with the
-//     sum of the two (as split-K partials would be joined).
+//   * Two streams of eight softmax warps, each stream with its own S and O in
+//     tensor memory (S0 S1 O0 O1, 128 columns each), so that the products of
+//     one run while the other's softmax does.  Two warps share 32 rows, one
+//     half of the step's tokens each: a row's exponentials then take half as
+//     long between S and PV (one warp per 32 rows: 90 instead of 79 us for the
+//     D 64 batch).  PAIR: the streams hold two row tiles of one KV head and
+//     read every step of the cache together.  Otherwise there is one row tile,
+//     stream 0 takes the even steps and stream 1 the odd ones, and a work unit
+//     ends with the sum of the two (as split-K partials would be joined).
 //   * One thread issues, step after step, PV_i of the stream's step before and
 //     S_i of this one; P (16 bits) overwrites the S columns it came from and is
 //     the A operand of PV.  tcgen05 operations of one thread complete in order,
-//     so S_i never overwrites a P_i that is still read.
+//     so S_i never overwrites a P_i that is still read.  (Measured and left:
+//     three S buffers with one O, 0.95 instead of 0.87 us a step; PV of the
+//     first 32 tokens of each half while the others' P is made, 1.71 instead
+//     of 1.65 for two tiles.)
 //   * A K copy warp walks the CTA's share of the work, publishes a descriptor
 //     per step (page ids, page parameters) in a ring, and copies K pages; a V
 //     copy warp copies V pages; for bf16 caches a query warp the query tiles.
-//   * One-byte caches add four converter warps: they rewrite V pages (and INT8
+//   * One-byte caches add eight converter warps: they rewrite V pages (and INT8
 //     K pages) in their stage as exact 16-bit code values, and the query rows
 //     in the type of the K operand (E4M3 K pages feed the products as they
-//     are, against a query of two E4M3 parts).  One warp per sub-partition,
-//     because the conversion instruction issues at a quarter rate: a single
-//     converter warp took 1500 cycles per 64 tokens.  The page scales multiply
-//     the scores and P.
+//     are, against a query of two E4M3 parts).  Four of them took 2.25 instead
+//     of 1.68 us an INT8 step.  The page scales multiply the scores and P.
 //
 // Work split ("stream-K"): the steps of all (sequence, KV head) items in a row
 // are cut into equal shares, one per SM, whatever the lengths; a share that
