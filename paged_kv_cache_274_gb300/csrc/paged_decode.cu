@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   if constexpr (TREE) {
     if (blockIdx.x > 0) {  // block-uniform, as above
       tree_scan_values(tree, (blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5),
-                       static_cast<int64_t>(gridDim.x - 1) * (kPlanThreads / 32));
+                       static_cast<int>(gridDim.x - 1) * (kPlanThreads / 32));
       return;
     }
   }

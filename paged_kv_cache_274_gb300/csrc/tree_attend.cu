@@ -36,6 +36,11 @@ struct TreePlanArgs {
   int max_shares, min_steps, item_steps;
 };
 
+// Quotients of what mostly fits 32 bits, in one place.
+__device__ __noinline__ long long plan_div(long long x, int d) {
+  return (x >> 32) != 0 ? x / d : static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(d));
+}
+
 // CTA 0: lengths, the prefix sums of the sequences' steps, the shares'
 // boundaries, zeros for inactive sequences.  Other CTAs: tree_scan_values.
 //
@@ -49,7 +54,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
   pdl_wait();
   if (blockIdx.x > 0) {  // block-uniform: these CTAs never reach the barriers below
     tree_scan_values(scan, (blockIdx.x - 1) * (kTreePlanThreads / 32) + (threadIdx.x >> 5),
-                     static_cast<int64_t>(gridDim.x - 1) * (kTreePlanThreads / 32));
+                     static_cast<int>(gridDim.x - 1) * (kTreePlanThreads / 32));
     return;
   }
   __shared__ long long warp_tot[kTreePlanThreads / 32];
@@ -60,6 +65,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
   if (tid == 0) carry_s = 0;
   __syncthreads();
   unsigned err = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.B; b0 += kTreePlanThreads) {
     const int b = b0 + tid;
     long long steps = 0;
@@ -114,27 +120,25 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
   }
   __syncthreads();
   const long long* start = a.B <= kTreePlanSmem ? start_s : a.start;
-  // quotients of what mostly fits 32 bits
-  auto div = [](long long x, int d) -> long long {
-    return (x >> 32) != 0 ? x / d : static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(d));
-  };
   // shares of at least min_steps steps
-  const int shares = static_cast<int>(min(static_cast<long long>(a.max_shares), div(total + a.min_steps - 1, a.min_steps)));
+  const int shares = static_cast<int>(min(static_cast<long long>(a.max_shares), plan_div(total + a.min_steps - 1, a.min_steps)));
   if (tid == 0) *a.shares = shares;
-  const int near = shares > 0 ? static_cast<int>(min(2ll, div(total, shares) / 4)) : 0;
+  const int near = shares > 0 ? static_cast<int>(min(2ll, plan_div(total, shares) / 4)) : 0;
+#pragma unroll 1
   for (int s = tid; s <= shares; s += kTreePlanThreads) {
     TreeBound r{a.B, 0, 0, 0};
     if (s < shares) {
-      const long long pos = div(total * s, shares);
+      const long long pos = plan_div(total * s, shares);
       int lo = 0, hi = a.B - 1;  // the sequence with start[lo] <= pos < start[lo + 1]
+#pragma unroll 1
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (start[mid + 1] > pos) hi = mid; else lo = mid + 1;
       }
       const long long in = pos - start[lo];
-      const int cost = static_cast<int>(div(start[lo + 1] - start[lo], a.Hkv)), nt = cost - a.item_steps;
+      const int cost = static_cast<int>(plan_div(start[lo + 1] - start[lo], a.Hkv)), nt = cost - a.item_steps;
       r.b = lo;
-      r.kvh = static_cast<int>(div(in, cost));
+      r.kvh = static_cast<int>(plan_div(in, cost));
       r.step = max(0, static_cast<int>(in - static_cast<long long>(r.kvh) * cost) - a.item_steps);
       if (r.step <= near) {
         r.step = 0;
@@ -150,9 +154,11 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
     a.bounds[s] = r;
   }
   // zeros for inactive sequences (one warp per sequence)
+#pragma unroll 1
   for (int b = warp; b < a.B; b += kTreePlanThreads / 32) {
     if (start[b + 1] != start[b]) continue;
     uint4* o = reinterpret_cast<uint4*>(a.out + static_cast<size_t>(b) * a.row_elems);
+#pragma unroll 1
     for (int i = lane; i < a.row_elems / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
   }
 }
@@ -199,6 +205,7 @@ __global__ void __launch_bounds__(kTreeMergeThreads, 3) tree_merge_kernel(const 
   const bool same = mine.b == next.b && mine.kvh == next.kvh;
   if (same && mine.step > 0) return;  // the item started in an earlier share
   int last = share + 1;               // the share that ends the item
+#pragma unroll 1
   for (;;) {
     const int s = last + 1 + lane;
     bool ends = true;
@@ -240,6 +247,7 @@ __global__ void __launch_bounds__(kTreeMergeThreads, 3) tree_merge_kernel(const 
   auto load_ml = [&](int p) { return p < parts && ((live >> mk) & 1u) ? a.part_ml[at(mk, p)] : make_float2(-INFINITY, 0.f); };
   float2 ml = load_ml(mp);
   float M = ml.x;
+#pragma unroll 1
   for (int p = mp + kLanes; p < parts; p += kLanes) M = fmaxf(M, load_ml(p).x);
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
@@ -248,12 +256,14 @@ __global__ void __launch_bounds__(kTreeMergeThreads, 3) tree_merge_kernel(const 
   for (int k = 0; k < kRows; ++k)
 #pragma unroll
     for (int j = 0; j < kPer; ++j) acc[k][j] = 0.f;
+#pragma unroll 1
   for (int p0 = 0; p0 < parts; p0 += kLanes) {
     if (p0 > 0) ml = load_ml(p0 + mp);
     // (an empty partial has O = 0, or the row's fixed value)
     const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
     sum = fmaf(w, ml.y, sum);
     const int pn = min(kLanes, parts - p0);
+#pragma unroll 1
     for (int pp = 0; pp < pn; pp += kBatch) {
 #pragma unroll
       for (int q = 0; q < kBatch; ++q)

@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       const int* trow = p.block_tables + static_cast<size_t>(b) * p.MB + t0 / BS;
       if constexpr (kOneByte) {  // the unit's queries, which the converters read once the unit before is done
         const int lines = 2 * p.G;
+#pragma unroll 1
         for (int x = lane; x < L::kQTiles * p.Tt * lines; x += 32) {
           const int t = 2 * pair * p.Tt + x / lines;
           if (t < p.T)
@@ -408,6 +409,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       };
       int id = load_ids(lane), id_next = load_ids(lane + 32), id_after = load_ids(lane + 64);
       float4 par = load_par(lane, id), par_next = load_par(lane + 32, id_next);
+#pragma unroll 1
       for (int j = 0; j < n; ++j, ++g) {
         const int q0 = j * PPI;  // the step's first page
         if (q0 > 0 && (q0 & 31) == 0) {
@@ -437,7 +439,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           plain = __all_sync(kFull, !mine || (par.x >= 0.f && par.x < INFINITY && par.z > 0.f && par.z < INFINITY));
           if (q >= 0 && q < PPI) {
             const_cast<TaStep*>(step_at(g))->par[q] =
-                make_float4(mine ? par.x : 0.f, kInt8Bias + (mine ? par.y : 0.f), ratio, mine ? __log2f(ratio) : 0.f);
+                make_float4(mine ? par.x : 0.f, kInt8Bias + (mine ? par.y : 0.f), ratio, ratio > 0.f ? __log2f(ratio) : 0.f);
             st->vzero[q] = mine ? par.w : 0.f;
           }
         }
@@ -617,6 +619,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         if (n == 0) break;
         if (!(ok = ta_wait(q_full, iu & 1u))) break;
         const int events = PAIR ? 2 * n : n;
+#pragma unroll 1
         for (int e = 0; ok && e < events; ++e) {
           const int i = e & 1, k = e >> 1;  // stream, its step
           if (k > 0 && !(ok = issue_pv(i, k == 1, iu))) break;
@@ -634,6 +637,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           if (e == events - 1) tc_commit(q_free);
         }
         // the last products of both streams, the earlier step's first
+#pragma unroll 1
         for (int x = 0; ok && x < 2; ++x) {
           const int i = (!PAIR && (n & 1)) ? 1 - x : x;
           const int ni = PAIR ? n : (n + 1 - i) / 2;  // the stream's steps
@@ -720,7 +724,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           const float sc = __uint_as_float(static_cast<uint32_t>(127 - kq) << 23);  // 2^-kq
           float qsum = 0.f;
           uint8_t* qt = sm + L::kQ + i * L::kTile + r * 128 + (kF8K ? 0u : half * L::kRegion);
-#pragma unroll 2
+#pragma unroll 1
           for (int c2 = 0; c2 < 4; ++c2) {  // 16 elements
             uint32_t wf[8], wl[4];
 #pragma unroll
@@ -761,6 +765,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
         bool ok = !kI8 || convert(true, g0);
+#pragma unroll 1
         for (int j = 0; ok && j < n; ++j) {
           const uint32_t g = g0 + j;
           if (kI8 && j + 1 < n) ok = wait_step(g + 1) && convert(true, g + 1);
@@ -830,6 +835,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       }
       float m = -INFINITY, l = 0.f;  // log2-domain lazy running maximum of the row, sum of this half
       const int ni = PAIR ? n : (n + 1 - i) / 2;  // this stream's steps
+#pragma unroll 1
       for (int k = 0; k < ni; ++k, ++steps) {
         const int j = PAIR ? k : 2 * k + i;
         const uint32_t g = g0 + j;
@@ -872,12 +878,39 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             vref = vnew;
           }
         }
-        const bool fast = flags == 0 && c >= 0.f;
+        const bool plain = flags == 0 && c >= 0.f;  // (a lower scale turns the order of the scores)
         if (!fail && !ta_wait(&s_full[i], steps & 1u)) fail = true;
         __syncwarp();
         tc_fence_after_sync();
         if (!warp_dead) {
           const uint32_t t_h = t_s + 64u * hh;  // this half's scores, then its P over them
+          if (!plain) {
+            // Scores to log2 units, -inf where masked, back to where they
+            // came from.  Once or twice an item, so a short loop: code that
+            // runs rarely costs its fetch, some 20 cycles an instruction.
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t y[16];
+              tc_ld16(t_h + 16u * q, y);
+              tc_wait_ld_regs16(y);
+              float ck = c, add = 0.f;
+              if constexpr (kOneByte) {
+                const float4 pr = st->par[(64 * hh + 16 * q) / BS];
+                ck = cq * pr.x;
+                if constexpr (kI8) add = -pr.y * qsum * ck;
+              }
+              const uint32_t mk = static_cast<uint32_t>(rm >> (16 * q));
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t z[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  z[e] = __float_as_uint(((mk >> (8 * h + e)) & 1u) ? fmaf(__uint_as_float(y[8 * h + e]), ck, add) : -INFINITY);
+                tc_st8(t_h + 16u * q + 8u * h, z);
+              }
+            }
+            tc_wait_st();
+          }
           uint32_t x0[32], x1[32];
           tc_ld32(t_h, x0);
           tc_ld32(t_h + 32u, x1);
@@ -888,13 +921,14 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           // 2^(score - m + lv)
           auto page = [&](int c32, int h, float& ck, float& add, float& lv) {
             const float4 pr = st->par[(64 * hh + 32 * c32) / BS + h];
-            ck = cq * pr.x;
-            add = kI8 ? -pr.y * qsum * ck : 0.f;  // the biased K codes
+            ck = plain ? cq * pr.x : 1.f;
+            add = kI8 && plain ? -pr.y * qsum * ck : 0.f;  // the biased K codes
             lv = pr.w;
           };
+          const float c_u = plain ? c : 1.f;
           auto ext32 = [&](const uint32_t (&x)[32], int c32) -> float {  // largest score, in log2 units
             if constexpr (!kOneByte) {
-              return tree_ext32<true>(x) * c;
+              return tree_ext32<true>(x) * c_u;
             } else if constexpr (BS == 32) {
               float ck, add, lv;
               page(c32, 0, ck, add, lv);
@@ -907,30 +941,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
               return fmaxf(e0, fmaf(max16(x, 16), ck, add));
             }
           };
-          // any scales and masks: scores to log2 units, -inf where masked
-          auto scaled = [&](uint32_t (&x)[32], int c32, uint32_t mk) -> float {
-            float ext = -INFINITY;
-#pragma unroll
-            for (int h = 0; h < (kOneByte ? 32 / BS : 1); ++h) {
-              constexpr int kRun = kOneByte ? BS : 32;
-              float ck = c, add = 0.f, lv;
-              if constexpr (kOneByte) page(c32, h, ck, add, lv);
-#pragma unroll
-              for (int e = h * kRun; e < (h + 1) * kRun; ++e) {
-                const float v = ((mk >> e) & 1u) ? fmaf(__uint_as_float(x[e]), ck, add) : -INFINITY;
-                x[e] = __float_as_uint(v);
-                ext = fmaxf(ext, v);
-              }
-            }
-            return ext;
-          };
-          float smax;
-          if (fast) {
-            smax = fmaxf(ext32(x0, 0), ext32(x1, 1));
-          } else {
-            smax = scaled(x0, 0, static_cast<uint32_t>(rm));
-            smax = fmaxf(smax, scaled(x1, 1, static_cast<uint32_t>(rm >> 32)));
-          }
+          float smax = fmaxf(ext32(x0, 0), ext32(x1, 1));
           // lazy maximum: moved when the row's exceeds it by more than 2^8
           const bool want = m == -INFINITY ? smax != -INFINITY : smax > m + 8.f;
           bool grow = false;
@@ -953,7 +964,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           const float neg_m = (m == -INFINITY) ? 0.f : -m;
           float ps0 = 0.f, ps1 = 0.f;
           auto write_p = [&](const uint32_t (&x)[32], int c32) {
-            float ck = c, add = 0.f, lv = 0.f;
+            float ck = c_u, add = 0.f, lv = 0.f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {  // 16 scores
               if constexpr (kOneByte) {
@@ -980,23 +991,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
               tc_st8(t_h + 16 * c32 + 8 * h, pw);
             }
           };
-          auto write_scaled = [&](const uint32_t (&x)[32], int c32) {  // scores in log2 units
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t pw[8];
-              const float vr = kOneByte ? st->par[(64 * hh + 32 * c32 + 16 * h) / BS].z : 1.f;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float p0 = ex2_approx(__uint_as_float(x[16 * h + 2 * e]) + neg_m);
-                const float p1 = ex2_approx(__uint_as_float(x[16 * h + 2 * e + 1]) + neg_m);
-                l += p0 + p1;
-                // (a masked token's page may have no finite scale: 0 x that would be NaN)
-                pw[e] = kOneByte ? pack_f16x2(p0 != 0.f ? p0 * vr : 0.f, p1 != 0.f ? p1 * vr : 0.f) : pack_bf16x2(p0, p1);
-              }
-              tc_st8(t_h + 16 * c32 + 8 * h, pw);
-            }
-          };
-          if (fast) {
+          if (!kOneByte || !(flags & kStepScales)) {
             if constexpr (kOneByte) {
               // one-byte caches: the second 32 scores are read again, so that
               // 32 registers less are held meanwhile (the first 32's P covers
@@ -1011,8 +1006,23 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
               l += ps0 + ps1;
             }
           } else {
-            write_scaled(x0, 0);
-            write_scaled(x1, 1);
+            // a page's v scale is zero, negative or not finite
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t y[16], pw[8];
+              tc_ld16(t_h + 16u * q, y);
+              tc_wait_ld_regs16(y);
+              const float vr = st->par[(64 * hh + 16 * q) / BS].z;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float p0 = ex2_approx(__uint_as_float(y[2 * e]) + neg_m);
+                const float p1 = ex2_approx(__uint_as_float(y[2 * e + 1]) + neg_m);
+                l += p0 + p1;
+                // (a masked token's page may have no finite scale: 0 x that would be NaN)
+                pw[e] = pack_f16x2(p0 != 0.f ? p0 * vr : 0.f, p1 != 0.f ? p1 * vr : 0.f);
+              }
+              tc_st8(t_h + 8u * q, pw);
+            }
           }
           // O_i of the steps before, rarely, half of the columns by each warp
           // (quiescent: PV_i of the step before was done before this S_i, the
@@ -1121,23 +1131,25 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         const int c0 = (PAIR ? hh : 2 * i + hh) * kCols;
 #pragma unroll 1
         for (int cc = c0; cc < c0 + kCols; cc += 16) {
-          uint32_t ov[16];
+          uint32_t ov[16], o1[16];
           tc_ld16(t_o + (PAIR ? 128u * i : 0u) + cc, ov);
-          if (!PAIR && n > 1) {
-            uint32_t o1[16];
+          if constexpr (!PAIR) {  // (O1 of a unit with one step holds anything)
             tc_ld16(t_o + 128u + cc, o1);
-            tc_wait_ld_regs16(ov);
-            tc_regs_loaded16(o1);
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              ov[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(ov[e]) * f0));
-          } else {
-            tc_wait_ld_regs16(ov);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f0);
           }
+          tc_wait_ld_regs16(ov);
+          if constexpr (!PAIR) tc_regs_loaded16(o1);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) ov[e] = row_state == kTreeRowZero ? 0u : ov[e];
+          for (int e = 0; e < 16; e += 2) {
+            float a, b2;
+            fmul2(a, b2, __uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), f0, f0);
+            if constexpr (!PAIR) {
+              const float z0 = n > 1 ? __uint_as_float(o1[e]) : 0.f, z1 = n > 1 ? __uint_as_float(o1[e + 1]) : 0.f;
+              a = fmaf(z0, f1, a);
+              b2 = fmaf(z1, f1, b2);
+            }
+            ov[e] = row_state == kTreeRowZero ? 0u : __float_as_uint(a);
+            ov[e + 1] = row_state == kTreeRowZero ? 0u : __float_as_uint(b2);
+          }
           if (in_tile) {
             if (part == 0) {
               uint4* dst = reinterpret_cast<uint4*>(p.out + qrow * D + cc);
@@ -1173,9 +1185,11 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
     // each role lets its own copies and products still in flight finish
     // (bounded) before the shared and tensor memory are released
     if (warp == 17 && lane == 0)
+#pragma unroll 1
       for (uint32_t g = k_issued > KS ? k_issued - KS : 0; g < k_issued; ++g)
         mbar_wait_bounded(kI8 ? &tma_k[g % KS] : &k_full[g % KS], (g / KS) & 1u, kWaitLimitNs / 16);
     if (warp == 18 && lane == 0) {
+#pragma unroll 1
       for (uint32_t g = v_issued > VS ? v_issued - VS : 0; g < v_issued; ++g)
         mbar_wait_bounded(kOneByte ? &tma_v[g % VS] : &v_full[g % VS], (g / VS) & 1u, kWaitLimitNs / 16);
     }

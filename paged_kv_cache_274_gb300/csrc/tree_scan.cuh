@@ -28,19 +28,13 @@ struct TreeScan {
   int B, T, words, Hkv, MB, NB, bs, row_bytes, e4m3;
 };
 
-// 16 bytes of a V row with a value that is not finite.
+// 16 bytes of a V row with a value that is not finite.  E4M3: NaN has every
+// bit but the sign set; adding 1 to seven set bits carries into the eighth.
+// bf16: the exponent is all ones; likewise with its lowest bit.
 __device__ __forceinline__ bool not_finite(const uint4& x, bool e4m3) {
-  const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-  uint32_t odd = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (e4m3) {  // NaN: every bit but the sign set; adding 1 to 7 set bits carries into the eighth
-      odd |= ((v[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-    } else {     // bf16: exponent all ones; likewise with its lowest bit
-      odd |= ((v[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-    }
-  }
-  return odd != 0u;
+  const uint32_t bits = e4m3 ? 0x7f7f7f7fu : 0x7f807f80u, one = e4m3 ? 0x01010101u : 0x00800080u;
+  const uint32_t top = e4m3 ? 0x80808080u : 0x80008000u;
+  return ((((x.x & bits) + one) | ((x.y & bits) + one) | ((x.z & bits) + one) | ((x.w & bits) + one)) & top) != 0u;
 }
 
 template <int kLanes>  // lanes of one row
@@ -58,7 +52,7 @@ __device__ __forceinline__ uint32_t tree_scan_word(const TreeScan& t, int b, int
     }
   }
   uint32_t word = 0u;
-#pragma unroll
+#pragma unroll 1
   for (int r0 = 0; r0 < 32; r0 += 8 * kRows) {
     uint4 x[8];
 #pragma unroll
@@ -80,12 +74,12 @@ __device__ __forceinline__ uint32_t tree_scan_word(const TreeScan& t, int b, int
 }
 
 // Words warp0, warp0 + nwarps, ... of the B x Hkv x words.
-__device__ __forceinline__ void tree_scan_values(const TreeScan& t, int64_t warp0, int64_t nwarps) {
-  const int64_t items = static_cast<int64_t>(t.B) * t.Hkv * t.words;
-  for (int64_t it = warp0; it < items; it += nwarps) {
-    const int w = static_cast<int>(it % t.words);
-    const int64_t bh = it / t.words;
-    const int h = static_cast<int>(bh % t.Hkv), b = static_cast<int>(bh / t.Hkv);
+__device__ __forceinline__ void tree_scan_values(const TreeScan& t, int warp0, int nwarps) {
+  const unsigned items = static_cast<unsigned>(t.B) * t.Hkv * t.words;  // (less than 2^31, as the host checks)
+#pragma unroll 1
+  for (unsigned i = warp0; i < items; i += nwarps) {
+    const int it = static_cast<int>(i), bh = it / t.words, w = it - bh * t.words;
+    const int b = bh / t.Hkv, h = bh - b * t.Hkv;
     const int n = t.context_lens[b];
     const int nodes = t.node_counts != nullptr ? t.node_counts[b] : t.T;
     uint32_t word = 0u;
