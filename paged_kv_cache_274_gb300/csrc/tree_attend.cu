@@ -53,20 +53,20 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
   pdl_trigger();
   pdl_wait();
   if (blockIdx.x > 0) {  // block-uniform: these CTAs never reach the barriers below
-    tree_scan_values(scan, (blockIdx.x - 1) * (kTreePlanThreads / 32) + (threadIdx.x >> 5),
-                     static_cast<int>(gridDim.x - 1) * (kTreePlanThreads / 32));
+    tree_scan_values(scan, (blockIdx.x - 1) * (blockDim.x / 32) + (threadIdx.x >> 5),
+                     static_cast<int>(gridDim.x - 1) * (blockDim.x / 32));
     return;
   }
   __shared__ long long warp_tot[kTreePlanThreads / 32];
   __shared__ long long carry_s;
   __shared__ long long start_s[kTreePlanSmem + 1];
   __shared__ int ctx_s[kTreePlanSmem];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   if (tid == 0) carry_s = 0;
   __syncthreads();
   unsigned err = 0;
 #pragma unroll 1
-  for (int b0 = 0; b0 < a.B; b0 += kTreePlanThreads) {
+  for (int b0 = 0; b0 < a.B; b0 += threads) {
     const int b = b0 + tid;
     long long steps = 0;
     if (b < a.B) {
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
     if (lane == 31) warp_tot[warp] = x;
     __syncthreads();
     if (warp == 0) {
-      long long w = warp_tot[lane];
+      long long w = lane < threads / 32 ? warp_tot[lane] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(kFull, w, o);
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
       if (a.B <= kTreePlanSmem) start_s[b] = before;
     }
     __syncthreads();
-    if (tid == kTreePlanThreads - 1) carry_s += warp_tot[31];
+    if (tid == 0) carry_s += warp_tot[31];
     __syncthreads();
   }
   if (err) atomicOr(a.err, err);
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
   if (tid == 0) *a.shares = shares;
   const int near = shares > 0 ? static_cast<int>(min(2ll, plan_div(total, shares) / 4)) : 0;
 #pragma unroll 1
-  for (int s = tid; s <= shares; s += kTreePlanThreads) {
+  for (int s = tid; s <= shares; s += threads) {
     TreeBound r{a.B, 0, 0, 0};
     if (s < shares) {
       const long long pos = plan_div(total * s, shares);
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
   }
   // zeros for inactive sequences (one warp per sequence)
 #pragma unroll 1
-  for (int b = warp; b < a.B; b += kTreePlanThreads / 32) {
+  for (int b = warp; b < a.B; b += threads / 32) {
     if (start[b + 1] != start[b]) continue;
     uint4* o = reinterpret_cast<uint4*>(a.out + static_cast<size_t>(b) * a.row_elems);
 #pragma unroll 1
@@ -401,8 +401,10 @@ cudaError_t launch_tree_attend(const DecodeLaunch& L, uint8_t* ws, int* launched
                   static_cast<__nv_bfloat16*>(L.out), L.err, L.B, L.T, L.Hkv, L.MB * L.bs, L.T * L.Hq * L.D,
                   L.tree_shares, L.tree_min_steps, tree_item_steps(L.kv_dtype, pair)};
   const TreeScan scan = tree_scan_of(L, poison);
-  cfg.gridDim = dim3(1 + tree_scan_ctas(L, kTreePlanThreads / 32));
-  cfg.blockDim = dim3(kTreePlanThreads);
+  // (a thread per share, or sequence: a CTA of 1024 takes longer to start)
+  const int plan_threads = L.B <= 192 ? 192 : kTreePlanThreads;
+  cfg.gridDim = dim3(1 + tree_scan_ctas(L, plan_threads / 32));
+  cfg.blockDim = dim3(plan_threads);
   e = cudaLaunchKernelEx(&cfg, tree_plan_kernel, pa, scan);
   if (e != cudaSuccess) return e;
   *launched += 1;

@@ -100,7 +100,7 @@ inline TreeScan tree_scan_of(const DecodeLaunch& L, uint32_t* poison) {
 inline unsigned tree_scan_ctas(const DecodeLaunch& L, int warps_per_cta) {
   if (L.kv_dtype == PKV_KV_INT8) return 0;
   const long long items = static_cast<long long>(L.B) * L.Hkv * L.tree_words;
-  return static_cast<unsigned>(std::min<long long>((items + warps_per_cta - 1) / warps_per_cta, 151));
+  return static_cast<unsigned>(std::min<long long>((items + warps_per_cta - 1) / warps_per_cta, 151 * 32 / warps_per_cta));
 }
 
 }  // namespace pkv
