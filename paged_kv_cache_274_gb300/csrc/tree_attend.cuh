@@ -13,11 +13,11 @@
 // measured bf16 rate) for S = Q K^T and O += P V; with two tiles the tensor
 // pipe, 1.34 us.  Measured per step of 128 tokens with the cache in L2: bf16
 // 0.87 to 1.0 us with one tile, 1.65 with two (D 64: 0.70 to 0.76, 1.42), E4M3
-// 1.22 to 1.4 and 2.35, INT8 1.6 to 1.75 and 3.4.  So bf16 batches of one tile
+// 1.15 to 1.35 and 2.3, INT8 1.7 to 1.85 and 2.8.  So bf16 batches of one tile
 // run at HBM speed (64 sequences of 2048 to 4096 tokens, 32 nodes, 8 KV heads:
-// 158 us with plan and merge, 0.79 of the copy rate), long contexts with many
-// rows at 0.63 of the bf16 peak (4 x 32k tokens, 64 nodes, 8 heads a KV head:
-// 220 us), and one-byte caches at the issue rate of the sub-partitions: 1600
+// 156 us with plan and merge, 0.80 of the copy rate), long contexts with many
+// rows at 0.64 of the bf16 peak (4 x 32k tokens, 64 nodes, 8 heads a KV head:
+// 218 us), and one-byte caches at the issue rate of the sub-partitions: 1600
 // instructions a step each, against 940 of bf16 caches, for the page scales
 // and the widening.
 //
@@ -268,6 +268,9 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
   static_assert(!kOneByte || D == 128, "one-byte pages need head_dim 128");
   constexpr int PPI = kTreeTokens / BS;  // pages per step
   constexpr int KS = L::kKStages, VS = L::kVStages;
+  // INT8 converter warps of K, and of V: a pair's four each (2.87 us a step;
+  // all eight for both 3.4), one tile's all eight (1.6 us a step; four each 2.1)
+  constexpr int kKWarps = PAIR ? kConvWarps / 2 : kConvWarps;
   constexpr int kHalves = D / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -297,12 +300,12 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
 
   if (tid == 0) {
     for (int s = 0; s < KS; ++s) {
-      mbar_init(&k_full[s], kI8 ? kConvWarps : 1);
+      mbar_init(&k_full[s], kI8 ? kKWarps : 1);
       mbar_init(&k_free[s], 1);
       mbar_init(&tma_k[s], 1);
     }
     for (int s = 0; s < VS; ++s) {
-      mbar_init(&v_full[s], kOneByte ? kConvWarps : 1);
+      mbar_init(&v_full[s], kI8 ? kKWarps : kOneByte ? kConvWarps : 1);
       mbar_init(&v_free[s], 1);
       mbar_init(&tma_v[s], 1);
     }
@@ -656,25 +659,30 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
     if constexpr (kOneByte) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ta_role_regs(KV)));
       // converter warps: 16 rows each of a unit's query tiles, then of its
-      // steps' K (INT8) and V; K of a step before V of the step before it, the
-      // order that the products need them in
+      // steps' V and INT8 K
       const int cw = warp - 20;
       constexpr int kRows = kTreeTokens / kConvWarps;
       static_assert(kRows == 16, "");
       auto convert = [&](bool is_k, uint32_t g) -> bool {
         uint64_t* landed = is_k ? &tma_k[g % KS] : &tma_v[g % VS];
         if (!warp_wait(landed, is_k ? (g / KS) & 1u : (g / VS) & 1u)) return false;
-        uint8_t* st = (is_k ? sm + L::kK + (g % KS) * L::kKTile : sm + L::kV + (g % VS) * L::kTile) + cw * kRows * 128;
+        constexpr int kRuns = kI8 ? kConvWarps / kKWarps : 1;
+        const int row0 = kRows * kRuns * (kI8 ? cw % kKWarps : cw);
+        uint8_t* st = (is_k ? sm + L::kK + (g % KS) * L::kKTile : sm + L::kV + (g % VS) * L::kTile) + row0 * 128;
         const volatile TaStep* sp = step_at(g);
-        const int rows = sp->np * BS - kRows * cw;  // of the step's pages
-        uint32_t zc = 0u;
-        if (is_k) {
-          widen_rows<KV, kI8>(st, L::kRegion, lane, zc, rows);
-        } else {
-          if constexpr (kI8) {
-            if ((lane & 15) < rows) zc = int8_zero_const(sp->vzero[(kRows * cw) / BS]);
+        const int rows = sp->np * BS - row0;  // of the step's pages
+#pragma unroll 1
+        for (int x = 0; x < kRuns; ++x) {
+          const int left = rows - x * kRows;
+          if (is_k) {
+            widen_rows<KV, kI8>(st + x * kRows * 128, L::kRegion, lane, 0u, left);
+          } else {
+            uint32_t zc = 0u;
+            if constexpr (kI8) {
+              if ((lane & 15) < left) zc = int8_zero_const(sp->vzero[(row0 + x * kRows) / BS]);
+            }
+            widen_rows<KV, false>(st + x * kRows * 128, L::kRegion, lane, zc, left);
           }
-          widen_rows<KV, false>(st, L::kRegion, lane, zc, rows);
         }
         fence_proxy_async_smem();  // read by the tensor cores
         __syncwarp();
@@ -764,12 +772,14 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
-        bool ok = !kI8 || convert(true, g0);
+        constexpr bool kBoth = kI8 && kKWarps == kConvWarps;
+        bool ok = !kBoth || convert(true, g0);
 #pragma unroll 1
         for (int j = 0; ok && j < n; ++j) {
           const uint32_t g = g0 + j;
-          if (kI8 && j + 1 < n) ok = wait_step(g + 1) && convert(true, g + 1);
-          if (ok) ok = wait_step(g) && convert(false, g);
+          // K of a step before V of the step before it, the order that the products need them in
+          if (kBoth && j + 1 < n) ok = wait_step(g + 1) && convert(true, g + 1);
+          if (ok) ok = wait_step(g) && convert(kI8 && !kBoth && cw < kKWarps, g);
         }
         if (!ok) {
           timed_out = true;
