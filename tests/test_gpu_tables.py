@@ -58,7 +58,8 @@ class Tables:
 
 
 @pytest.mark.parametrize("B,bs,hi,new_hi,done", [(1, 16, 0, 1, 0.0), (1, 16, 100, 4000, 0.0), (7, 32, 300, 40, 0.3), (100, 16, 1000, 9, 0.2),
-                                                  (513, 16, 200, 33, 0.1), (1500, 32, 90, 3, 0.5), (40, 16, 50, 3000, 0.1)])
+                                                  (513, 16, 200, 33, 0.1), (1500, 32, 90, 3, 0.5), (40, 16, 50, 3000, 0.1),
+                                                  (60, 16, 50, 4001, 0.0)])  # more rows than threads: runs of rows
 @pytest.mark.parametrize("in_place", [True, False])
 def test_steps_of_many_requests(B, bs, hi, new_hi, done, in_place):
     # several steps in a row: requests grow, end, and others start in their rows

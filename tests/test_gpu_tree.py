@@ -150,6 +150,67 @@ def test_page_scales_over_three_decades(dtype, order):
         assert_tree_close(bf16_dev_to_f64(out), *_reference(dc, q, see, nodes), f"{order} {share}")
 
 
+@pytest.mark.parametrize("dtype", ["fp8", "int8a"])
+@pytest.mark.parametrize("T", [24, 60])
+@pytest.mark.parametrize("turn", [1, -1])
+def test_page_scales_of_any_sign(dtype, T, turn):
+    # negative K scales, negative and zero V scales, a negative softmax scale; some steps have only plain ones
+    lens = [T, 700, 130, 1500]
+    c = random_case(7460 + T, 4, 16, 4, 128, 16, lens, kv_dtype=dtype)
+    dc = DeviceCase(c)
+    rng = np.random.Generator(np.random.PCG64(7461))
+    for s, signs in ((c.k_scale, [1, 1, -1]), (c.v_scale, [1, 1, -1, 0, 0.25])):
+        f = rng.choice(signs, s.shape[1:3]).astype(np.float32)
+        f[c.block_tables[3, :40]] = 1  # the long sequence's first five steps
+        if dtype == "fp8":
+            s *= f
+        else:
+            s[..., 0] *= f
+    dc.ks, dc.vs = to_dev(c.k_scale), to_dev(c.v_scale)
+    c.scale *= turn
+    q = normal_bf16_bits(7462, (4, T, 16, 128))
+    see, nodes = _trees(7463, 4, T)
+    for share in (0, 256):
+        out = _attend(dc, q, see, nodes, opts=pkv.decode_opts(partition_blocks=share, math=pkv.MATH_TC))
+        assert_tree_close(bf16_dev_to_f64(out), *_reference(dc, q, see, nodes), f"share {share}")
+
+
+@pytest.mark.parametrize("dtype,D,T", [("bf16", 128, 24), ("bf16", 128, 60), ("bf16", 64, 24), ("fp8", 128, 24), ("fp8", 128, 60),
+                                       ("int8a", 128, 24)])
+def test_non_finite_queries_stay_in_their_rows(dtype, D, T):
+    c = random_case(7470 + T, 2, 16, 4, D, 16, [T + 3, 400], kv_dtype=dtype)
+    dc = DeviceCase(c)
+    q = normal_bf16_bits(7471, (2, T, 16, D))
+    see, nodes = _trees(7472, 2, T)
+    want = _reference(dc, q, see, nodes)
+    bad = [(0, 0, 3, 5, 0x7F80), (0, T - 1, 15, D - 1, 0xFF80), (1, 7, 0, 0, BF16_NAN)]
+    for b, t, h, d, bits in bad:
+        q[b, t, h, d] = bits
+    got = bf16_dev_to_f64(_attend(dc, q, see, nodes, opts=pkv.decode_opts(math=pkv.MATH_TC)))
+    for b, t, h, _, _ in bad:
+        assert np.isnan(got[b, t, h]).all()
+        got[b, t, h] = want[0][b, t, h]
+    assert_tree_close(got, *want, dtype)
+
+
+@pytest.mark.parametrize("B", [192, 193, 1100, 2100])
+def test_batches_of_many_short_sequences(B):
+    # some without tokens; more sequences than the planner has threads, or room in shared memory
+    T, rng = 3, np.random.Generator(np.random.PCG64(B))
+    lens = rng.integers(0, 50, B)
+    lens[rng.random(B) < 0.2] = 0
+    lens[B // 2] = 900
+    c = random_case(7480 + B, B, 8, 2, 64, 16, lens.tolist())
+    dc = DeviceCase(c)
+    nodes = np.minimum(lens, rng.integers(0, T + 1, B)).astype(np.int32)
+    q = normal_bf16_bits(7481, (B, T, 8, 64))
+    see, _ = _trees(7482, B, T, nodes)
+    out = _attend(dc, q, see, nodes)
+    assert pkv.decode_plan(dc.k, B, 8, c.MB, None, T, tree=True)["math"] == pkv.MATH_TC
+    assert pkv.read_device_error() == 0
+    assert_tree_close(bf16_dev_to_f64(out), *_reference(dc, q, see, nodes), f"B={B}")
+
+
 @pytest.mark.parametrize("dtype,T,math", [("bf16", 6, pkv.MATH_MMA), ("bf16", 20, pkv.MATH_TC), ("bf16", 60, pkv.MATH_TC), ("fp8", 20, pkv.MATH_TC)])
 def test_fewer_tokens_than_nodes(dtype, T, math):
     # nodes before position 0 do not exist; the others are attended to as the mask says
