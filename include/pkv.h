@@ -348,7 +348,11 @@ pkv_status pkv_decode_multi_describe(const pkv_cache_desc* cache, int32_t batch,
  *   node_counts    device int32 [B]: m_b, in 0..T; NULL: T each.  A count out
  *                  of range sets PKV_DEVERR_TREE; the sequence's rows are zeros.
  *   workspace      pkv_decode_tree_workspace_bytes() bytes.
- *   everything else as in pkv_paged_decode_multi, PKV_MATH_TC with T = 1 too.
+ *   opts           PKV_MATH_TC takes T = 1 and head_dim 64 too (bf16), and
+ *                  shares of equal work instead of partitions:
+ *                  partition_blocks is the fewest blocks of a share, warps
+ *                  and stages have no effect.
+ *   everything else as in pkv_paged_decode_multi.
  */
 pkv_status pkv_paged_decode_tree(const pkv_cache_desc* cache,
                                  const void* q, int32_t batch, int32_t num_query_tokens,
