@@ -13,7 +13,7 @@
 // measured bf16 rate) for S = Q K^T and O += P V; with two tiles the tensor
 // pipe, 1.34 us.  Measured per step of 128 tokens with the cache in L2: bf16
 // 0.87 to 1.0 us with one tile, 1.65 with two (D 64: 0.70 to 0.76, 1.42), E4M3
-// 1.15 to 1.35 and 2.3, INT8 1.7 to 1.85 and 2.8.  So bf16 batches of one tile
+// 1.15 to 1.35 and 2.3, INT8 1.65 to 1.75 and 2.7.  So bf16 batches of one tile
 // run at HBM speed (64 sequences of 2048 to 4096 tokens, 32 nodes, 8 KV heads:
 // 156 us with plan and merge, 0.80 of the copy rate), long contexts with many
 // rows at 0.64 of the bf16 peak (4 x 32k tokens, 64 nodes, 8 heads a KV head:
@@ -170,6 +170,7 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, ui
 // instructions, because the kernel has some forty of these: the hardware
 // suspends the thread for up to a microsecond per try.
 constexpr int kTaTries = 1 << 21;
+constexpr int kConvTries = 1 << 24;  // of 100 ns and more
 __device__ __forceinline__ bool ta_wait(uint64_t* bar, uint32_t parity) {
   const uint32_t addr = smem_addr(bar);
 #pragma unroll 1
@@ -268,9 +269,6 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
   static_assert(!kOneByte || D == 128, "one-byte pages need head_dim 128");
   constexpr int PPI = kTreeTokens / BS;  // pages per step
   constexpr int KS = L::kKStages, VS = L::kVStages;
-  // INT8 converter warps of K, and of V: a pair's four each (2.87 us a step;
-  // all eight for both 3.4), one tile's all eight (1.6 us a step; four each 2.1)
-  constexpr int kKWarps = PAIR ? kConvWarps / 2 : kConvWarps;
   constexpr int kHalves = D / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -300,12 +298,12 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
 
   if (tid == 0) {
     for (int s = 0; s < KS; ++s) {
-      mbar_init(&k_full[s], kI8 ? kKWarps : 1);
+      mbar_init(&k_full[s], kI8 ? kConvWarps : 1);
       mbar_init(&k_free[s], 1);
       mbar_init(&tma_k[s], 1);
     }
     for (int s = 0; s < VS; ++s) {
-      mbar_init(&v_full[s], kI8 ? kKWarps : kOneByte ? kConvWarps : 1);
+      mbar_init(&v_full[s], kOneByte ? kConvWarps : 1);
       mbar_init(&v_free[s], 1);
       mbar_init(&tma_v[s], 1);
     }
@@ -432,57 +430,71 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         const bool mine = q >= 0 && q < np;
         const bool bad = mine && static_cast<unsigned>(id) >= static_cast<unsigned>(p.NB);
         const int phys = bad ? 0 : id;
-        bool plain = true;
-        if constexpr (kOneByte) {
-          // vref moves when a step's v scales are more than 2^6 above it, so
-          // that P, below 2^8, stays below 2^14 in f16
-          const float vm = __uint_as_float(__reduce_max_sync(kFull, mine ? __float_as_uint(fabsf(par.z)) : 0u));
-          if (vm > 64.f * vref) vref = vm;
-          const float ratio = mine && vref > 0.f ? par.z / vref : 0.f;
-          plain = __all_sync(kFull, !mine || (par.x >= 0.f && par.x < INFINITY && par.z > 0.f && par.z < INFINITY));
-          if (q >= 0 && q < PPI) {
-            const_cast<TaStep*>(step_at(g))->par[q] =
-                make_float4(mine ? par.x : 0.f, kInt8Bias + (mine ? par.y : 0.f), ratio, ratio > 0.f ? __log2f(ratio) : 0.f);
-            st->vzero[q] = mine ? par.w : 0.f;
+        auto copy = [&]() {
+          uint8_t* dst = sm + L::kK + (g % KS) * L::kKTile;
+          uint64_t* bar = kI8 ? &tma_k[g % KS] : &k_full[g % KS];
+          if (lane == 0) {
+            fence_proxy_async_smem();  // INT8: the converters wrote the stage before
+            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(np) * (kOneByte ? 128u : 128u * kHalves) * BS);
           }
-        }
-        if (q >= 0 && q < PPI) {
-          st->pages[q] = phys;
-          st->bad[q] = bad ? 1 : 0;
-        }
-        if (bad) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
-        const int seen = min(t1, base) - (t0 + j * kTreeTokens);  // tokens of the step that every row attends to
-        const int flags = (seen < kTreeTokens || __any_sync(kFull, bad) ? kStepMasked : 0) | (plain ? 0 : kStepScales);
-        if (lane == 0) {
-          st->n = n;
-          st->b = b;
-          st->kvh = kvh;
-          st->t0 = t0;
-          st->t1 = t1;
-          st->part = part;
-          st->np = np;
-          st->ctx = ctx;
-          st->flags = flags;
-          st->vref = vref;
-        }
-        uint8_t* dst = sm + L::kK + (g % KS) * L::kKTile;
-        uint64_t* bar = kI8 ? &tma_k[g % KS] : &k_full[g % KS];
-        if (lane == 0) {
-          fence_proxy_async_smem();  // INT8: the converters wrote the stage before
-          mbar_arrive_expect_tx(bar, static_cast<uint32_t>(np) * (kOneByte ? 128u : 128u * kHalves) * BS);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&step_full[g % kTaRing]);  // release: the descriptor
-        if (mine) {
-          const int row = p.row_base + (phys * p.Hkv + kvh) * BS;
-          if constexpr (kOneByte) {
-            tma_load_2d(dst + (kF8K ? 0 : L::kRegion) + q * BS * 128, &kmap, bar, 0, row, policy);
-          } else {
+          __syncwarp();
+          if (mine) {
+            const int row = p.row_base + (phys * p.Hkv + kvh) * BS;
+            if constexpr (kOneByte) {
+              tma_load_2d(dst + (kF8K ? 0 : L::kRegion) + q * BS * 128, &kmap, bar, 0, row, policy);
+            } else {
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h) tma_load_2d(dst + h * L::kRegion + q * BS * 128, &kmap, bar, 64 * h, row, policy);
+              for (int h = 0; h < kHalves; ++h) tma_load_2d(dst + h * L::kRegion + q * BS * 128, &kmap, bar, 64 * h, row, policy);
+            }
           }
+          k_issued = g + 1;
+        };
+        auto describe = [&]() {
+          bool plain = true;
+          if constexpr (kOneByte) {
+            // vref moves when a step's v scales are more than 2^6 above it, so
+            // that P, below 2^8, stays below 2^14 in f16
+            const float vm = __uint_as_float(__reduce_max_sync(kFull, mine ? __float_as_uint(fabsf(par.z)) : 0u));
+            if (vm > 64.f * vref) vref = vm;
+            const float ratio = mine && vref > 0.f ? par.z / vref : 0.f;
+            plain = __all_sync(kFull, !mine || (par.x >= 0.f && par.x < INFINITY && par.z > 0.f && par.z < INFINITY));
+            if (q >= 0 && q < PPI) {
+              const_cast<TaStep*>(step_at(g))->par[q] =
+                  make_float4(mine ? par.x : 0.f, kInt8Bias + (mine ? par.y : 0.f), ratio, ratio > 0.f ? __log2f(ratio) : 0.f);
+              st->vzero[q] = mine ? par.w : 0.f;
+            }
+          }
+          if (q >= 0 && q < PPI) {
+            st->pages[q] = phys;
+            st->bad[q] = bad ? 1 : 0;
+          }
+          if (bad) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+          const int seen = min(t1, base) - (t0 + j * kTreeTokens);  // tokens of the step that every row attends to
+          const int flags = (seen < kTreeTokens || __any_sync(kFull, bad) ? kStepMasked : 0) | (plain ? 0 : kStepScales);
+          if (lane == 0) {
+            st->n = n;
+            st->b = b;
+            st->kvh = kvh;
+            st->t0 = t0;
+            st->t1 = t1;
+            st->part = part;
+            st->np = np;
+            st->ctx = ctx;
+            st->flags = flags;
+            st->vref = vref;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&step_full[g % kTaRing]);  // release: the descriptor
+        };
+        // one-byte caches: the descriptor takes some 1500 cycles, so the copy
+        // first; bf16: the queries wait for the descriptor
+        if constexpr (kOneByte) {
+          copy();
+          describe();
+        } else {
+          describe();
+          copy();
         }
-        k_issued = g + 1;
       }
       j0 = 0;
       if (++kvh == p.Hkv) {
@@ -663,31 +675,23 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       const int cw = warp - 20;
       constexpr int kRows = kTreeTokens / kConvWarps;
       static_assert(kRows == 16, "");
-      auto convert = [&](bool is_k, uint32_t g) -> bool {
-        uint64_t* landed = is_k ? &tma_k[g % KS] : &tma_v[g % VS];
-        if (!warp_wait(landed, is_k ? (g / KS) & 1u : (g / VS) & 1u)) return false;
-        constexpr int kRuns = kI8 ? kConvWarps / kKWarps : 1;
-        const int row0 = kRows * kRuns * (kI8 ? cw % kKWarps : cw);
+      auto convert = [&](bool is_k, uint32_t g) {
+        const int row0 = kRows * cw;
         uint8_t* st = (is_k ? sm + L::kK + (g % KS) * L::kKTile : sm + L::kV + (g % VS) * L::kTile) + row0 * 128;
         const volatile TaStep* sp = step_at(g);
         const int rows = sp->np * BS - row0;  // of the step's pages
-#pragma unroll 1
-        for (int x = 0; x < kRuns; ++x) {
-          const int left = rows - x * kRows;
-          if (is_k) {
-            widen_rows<KV, kI8>(st + x * kRows * 128, L::kRegion, lane, 0u, left);
-          } else {
-            uint32_t zc = 0u;
-            if constexpr (kI8) {
-              if ((lane & 15) < left) zc = int8_zero_const(sp->vzero[(row0 + x * kRows) / BS]);
-            }
-            widen_rows<KV, false>(st + x * kRows * 128, L::kRegion, lane, zc, left);
+        if (is_k) {
+          widen_rows<KV, kI8>(st, L::kRegion, lane, 0u, rows);
+        } else {
+          uint32_t zc = 0u;
+          if constexpr (kI8) {
+            if ((lane & 15) < rows) zc = int8_zero_const(sp->vzero[row0 / BS]);
           }
+          widen_rows<KV, false>(st, L::kRegion, lane, zc, rows);
         }
         fence_proxy_async_smem();  // read by the tensor cores
         __syncwarp();
         if (lane == 0) mbar_arrive(is_k ? &k_full[g % KS] : &v_full[g % VS]);
-        return true;
       };
       uint32_t g0 = 0;
       for (uint32_t iu = 0;; ++iu) {
@@ -772,15 +776,32 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
-        constexpr bool kBoth = kI8 && kKWarps == kConvWarps;
-        bool ok = !kBoth || convert(true, g0);
-#pragma unroll 1
-        for (int j = 0; ok && j < n; ++j) {
-          const uint32_t g = g0 + j;
-          // K of a step before V of the step before it, the order that the products need them in
-          if (kBoth && j + 1 < n) ok = wait_step(g + 1) && convert(true, g + 1);
-          if (ok) ok = wait_step(g) && convert(kI8 && !kBoth && cw < kKWarps, g);
+        // Each warp takes what has landed: K of a step before V of the step
+        // before it, the order that the products need them in, but whichever
+        // is there first (in that order alone: INT8 1.72 instead of 1.65 us a
+        // step, 2.8 or more instead of 2.67 for two tiles).
+        auto there = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_test_wait(bar, parity)) != 0; };
+        int jk = kI8 ? 0 : n, jv = 0, tries = 0;  // next K and V of the unit
+        while (jk < n || jv < n) {
+          const uint32_t gk = g0 + jk, gv = g0 + jv;
+          auto k_there = [&]() { return jk < n && there(&step_full[gk % kTaRing], (gk / kTaRing) & 1u) && there(&tma_k[gk % KS], (gk / KS) & 1u); };
+          auto v_there = [&]() { return jv < n && there(&step_full[gv % kTaRing], (gv / kTaRing) & 1u) && there(&tma_v[gv % VS], (gv / VS) & 1u); };
+          const bool k_first = kI8 && jk <= jv + 1;
+          const bool take_k = kI8 && ((k_first && k_there()) || (!k_first && !v_there() && k_there()));
+          if (take_k) {
+            convert(true, gk);
+            ++jk;
+            tries = 0;
+          } else if (v_there()) {
+            convert(false, gv);
+            ++jv;
+            tries = 0;
+          } else {
+            if (++tries > kConvTries) break;
+            __nanosleep(20);
+          }
         }
+        const bool ok = jk == n && jv == n;
         if (!ok) {
           timed_out = true;
           break;
