@@ -410,6 +410,32 @@ def test_other_stream_and_prepared():
     assert pkv.read_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype,T", [("bf16", 24), ("int8a", 24), ("fp8", 60)])
+def test_calls_at_the_same_time(dtype, T):
+    # two streams, a workspace each: persistent kernels that fill the GPU take turns, and change nothing of each other's
+    calls, refs = [], []
+    for i, lens in enumerate(([T, 900, 2500], [1400, T + 1, 60])):
+        c = random_case(8500 + i, 3, 16, 4, 128, 16, lens, kv_dtype=dtype)
+        dc = DeviceCase(c)
+        q = to_dev_bf16(normal_bf16_bits(8501 + i, (3, T, 16, 128)))
+        see, _ = _trees(8502 + i, 3, T)
+        mask = to_dev(pack(see))
+        refs.append(pkv.paged_decode_tree(q, dc.k, dc.v, dc.bt, dc.cl, mask, k_scale=dc.ks, v_scale=dc.vs))
+        n = pkv.decode_workspace_bytes(dc.k, 3, 16, c.MB, None, T, tree=True)
+        calls.append(pkv.PreparedDecode(q, dc.k, dc.v, dc.bt, dc.cl, k_scale=dc.ks, v_scale=dc.vs, tree_mask=mask,
+                                        stream=torch.cuda.Stream(), workspace=torch.empty(n, dtype=torch.uint8, device=DEV)))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for call in calls:
+            call.out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        outs = [[call() for call in calls] for _ in range(5)][-1]
+        torch.cuda.synchronize()
+        for o, ref in zip(outs, refs):
+            assert torch.equal(o.view(torch.int16), ref.view(torch.int16))
+    assert pkv.read_device_error() == 0
+
+
 def test_two_graphs_with_one_workspace():
     # replayed one after the other, each gives its own results
     cases, graphs = [], []
