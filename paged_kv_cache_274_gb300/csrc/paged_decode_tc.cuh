@@ -71,6 +71,7 @@
 #pragma once
 
 #include "paged_decode.cuh"
+#include "stage_ring.h"
 
 namespace pkv {
 
@@ -98,9 +99,9 @@ struct TcLayout {  // byte offsets from the 1024-aligned shared-memory base
   static constexpr uint32_t kV = kK + kTcKStages * kTile;    // V ring
   static constexpr uint32_t kBars = kV + kTcVStages * kTile;
   // full_k[4], kp_free[4], full_v[2], v_free[2], s_done, s_free, p_ready[4],
-  // q_ready, slot_full[2], slot_free[2], stg_full, stg_free, o_ready,
+  // q_ready, slot_full[2], slot_free[2], stg_full[2], stg_free, o_ready,
   // mma_drain, then for one-byte caches tma_k[4], tma_v[2] (codes landed)
-  static constexpr int kNumBars = 3 * kTcKStages + 2 * kTcVStages + 3 + 4 + 4 + kTcKStages + kTcVStages;
+  static constexpr int kNumBars = 3 * kTcKStages + 2 * kTcVStages + 3 + 4 + kStageBars + 3 + kTcKStages + kTcVStages;
   static constexpr uint32_t kMisc = kBars + 8 * kNumBars;    // TMEM base
   static constexpr uint32_t kSlots = kMisc + 16;             // 2 unit slots
   static constexpr uint32_t kSlotPages = 32;                 // after 8 int32 of descriptor
@@ -235,8 +236,8 @@ __global__ void __launch_bounds__(tc_threads(KV), 2)
   // index g (K stage and full_k[] / kp_free[] / p_ready[] by g % 4, V stage
   // and full_v[] / v_free[] by g % 2, s_done / s_free once per step) or by
   // the unit index i (slot_full[] / slot_free[] by i % 2, q_ready and o_ready
-  // once per unit) or by the output chunks (stg_full once per chunk, stg_free
-  // twice per split-K unit).
+  // once per unit) or by the output chunks (stg_full[] as stage_ring.h says,
+  // stg_free twice per split-K unit).
   // Every barrier completes one phase per use, and a waiter is never two
   // phases away from the phase it waits for (a parity wait cannot tell them
   // apart): each next use of a barrier depends on the wait.  p_ready has one
@@ -252,8 +253,8 @@ __global__ void __launch_bounds__(tc_threads(KV), 2)
   uint64_t* q_ready = p_ready + kTcKStages;   // the unit's query tile in TMEM
   uint64_t* slot_full = q_ready + 1;          // [2] unit slot written
   uint64_t* slot_free = slot_full + 2;        // [2] unit slot released by every reader
-  uint64_t* stg_full = slot_free + 2;         // a chunk of the unit's output staged by every compute warp
-  uint64_t* stg_free = stg_full + 1;          // split-K partials: a store has read its staging buffer
+  uint64_t* stg_full = slot_free + 2;         // [2] a chunk of the unit's output staged by every compute warp
+  uint64_t* stg_free = stg_full + kStageBars;  // split-K partials: a store has read its staging buffer
   uint64_t* o_ready = stg_free + 1;           // a unit's last P . V done: O final, its K and V stages idle
   uint64_t* mma_drain = o_ready + 1;          // after a timeout: every product issued is done
   uint64_t* tma_k = mma_drain + 1;            // [4] one-byte caches: K(g)'s codes landed (then full_k: widened)
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(tc_threads(KV), 2)
       for (int s = 0; s < kTcKStages; ++s) mbar_init(&tma_k[s], 1);
       for (int s = 0; s < kTcVStages; ++s) mbar_init(&tma_v[s], 1);
     }
-    mbar_init(stg_full, kTcComputeWarps);
+    for (int s = 0; s < kStageBars; ++s) mbar_init(&stg_full[s], kTcComputeWarps);
     mbar_init(stg_free, 1);
     mbar_init(o_ready, 1);
     mbar_init(mma_drain, 1);
@@ -861,6 +862,7 @@ __global__ void __launch_bounds__(tc_threads(KV), 2)
       auto rescale_o = [&](float factor, uint32_t g) -> bool {
         if (!mbar_wait_spin(&v_free[(g - 1) % kTcVStages], ((g - 1) / kTcVStages) & 1u, kWaitLimitNs))
           timed_out = true;
+        __syncwarp();  // each thread waited by itself; the TMEM loads are warp-collective
         tc_fence_after_sync();
 #pragma unroll 1
         for (int cc = 0; cc < D; cc += 32) {
@@ -1120,15 +1122,16 @@ __global__ void __launch_bounds__(tc_threads(KV), 2)
           }
           fence_proxy_async_smem();  // read by the tensor-map store
           __syncwarp();
-          if (lane == 0) mbar_arrive(stg_full);
+          if (lane == 0) mbar_arrive(&stg_full[stage_bar(nchunk)]);
           if (tid == 0) {
-            if (mbar_wait_spin(stg_full, nchunk & 1u, kWaitLimitNs)) {
+            if (mbar_wait_spin(&stg_full[stage_bar(nchunk)], stage_parity(nchunk), kWaitLimitNs)) {
               tma_store_4d(&omap, buf, 64 * k2, U.kvh * p.G, U.tile * p.Tt, U.b);
               bulk_commit();
             } else {
               timed_out = true;
             }
           }
+          __syncwarp();  // the next TMEM load is warp-collective
         }
         // both stages go back to the copy warps once the stores have read them
         if (tid == 0 && !timed_out) {
@@ -1166,9 +1169,9 @@ __global__ void __launch_bounds__(tc_threads(KV), 2)
                 make_uint4(ov[4 * c4], ov[4 * c4 + 1], ov[4 * c4 + 2], ov[4 * c4 + 3]);
           fence_proxy_async_smem();  // read by the tensor-map store
           __syncwarp();
-          if (lane == 0) mbar_arrive(stg_full);
+          if (lane == 0) mbar_arrive(&stg_full[stage_bar(nchunk)]);
           if (tid == 0) {
-            if (mbar_wait_spin(stg_full, nchunk & 1u, kWaitLimitNs)) {
+            if (mbar_wait_spin(&stg_full[stage_bar(nchunk)], stage_parity(nchunk), kWaitLimitNs)) {
               tma_store_5d(&pmap, buf, cc, U.pidx, U.kvh * p.G, U.tile * p.Tt, U.b);
               bulk_commit();
               if (k == 1 || k == 2) {  // the store of chunk k - 1 has read its buffer
@@ -1179,6 +1182,7 @@ __global__ void __launch_bounds__(tc_threads(KV), 2)
               timed_out = true;
             }
           }
+          __syncwarp();  // the next TMEM load is warp-collective
         }
         nfree += 2;
         if (row_ok) *reinterpret_cast<float2*>(p.part_ml + 2 * (qrow * p.pmax + U.pidx)) = make_float2(m, l);
