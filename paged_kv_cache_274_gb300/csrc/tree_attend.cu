@@ -36,19 +36,11 @@ struct TreePlanArgs {
   int max_shares, min_steps, item_steps;
 };
 
-// Quotients of what mostly fits 32 bits, in one place.
-__device__ __noinline__ long long plan_div(long long x, int d) {
-  return (x >> 32) != 0 ? x / d : static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(d));
-}
-
 // CTA 0: lengths, the prefix sums of the sequences' steps, the shares'
 // boundaries, zeros for inactive sequences.  Other CTAs: tree_scan_values.
 //
-// Shares are equal in cost: an item's steps plus item_steps for its start and
-// output (measured: a batch of short and long sequences left SMs idle for half
-// the time with shares equal in steps).  A boundary within `near` steps of an
-// item's start or end moves there: the partial it would leave costs more than
-// the imbalance.
+// (Shares are equal in cost, tree_bound: with shares equal in steps a batch of
+// short and long sequences left SMs idle for half the time.)
 __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreePlanArgs a, const TreeScan scan) {
   pdl_trigger();
   pdl_wait();
@@ -83,7 +75,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
       if (nodes == 0) c = 0;  // every row is zero
       a.ctx_eff[b] = c;
       if (a.B <= kTreePlanSmem) ctx_s[b] = c;
-      steps = c == 0 ? 0 : static_cast<long long>((c + kTreeTokens - 1) / kTreeTokens + a.item_steps) * a.Hkv;
+      steps = tree_cost(c, a.item_steps, a.Hkv);
     }
     long long x = steps;
 #pragma unroll
@@ -120,36 +112,11 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
   }
   __syncthreads();
   const long long* start = a.B <= kTreePlanSmem ? start_s : a.start;
-  // shares of at least min_steps steps
-  const int shares = static_cast<int>(min(static_cast<long long>(a.max_shares), plan_div(total + a.min_steps - 1, a.min_steps)));
+  const int shares = tree_share_count(total, a.min_steps, a.max_shares);
   if (tid == 0) *a.shares = shares;
-  const int near = shares > 0 ? static_cast<int>(min(2ll, plan_div(total, shares) / 4)) : 0;
 #pragma unroll 1
   for (int s = tid; s <= shares; s += threads) {
-    TreeBound r{a.B, 0, 0, 0};
-    if (s < shares) {
-      const long long pos = plan_div(total * s, shares);
-      int lo = 0, hi = a.B - 1;  // the sequence with start[lo] <= pos < start[lo + 1]
-#pragma unroll 1
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid + 1] > pos) hi = mid; else lo = mid + 1;
-      }
-      const long long in = pos - start[lo];
-      const int cost = static_cast<int>(plan_div(start[lo + 1] - start[lo], a.Hkv)), nt = cost - a.item_steps;
-      r.b = lo;
-      r.kvh = static_cast<int>(plan_div(in, cost));
-      r.step = max(0, static_cast<int>(in - static_cast<long long>(r.kvh) * cost) - a.item_steps);
-      if (r.step <= near) {
-        r.step = 0;
-      } else if (nt - r.step <= near) {
-        r.step = 0;
-        if (++r.kvh == a.Hkv) {  // (the next sequences may be inactive: whoever starts there skips them)
-          r.kvh = 0;
-          ++r.b;
-        }
-      }
-    }
+    TreeBound r = tree_bound(s, shares, total, start, a.B, a.Hkv, a.item_steps);
     if (r.b < a.B) r.ctx = a.B <= kTreePlanSmem ? ctx_s[r.b] : a.ctx_eff[r.b];
     a.bounds[s] = r;
   }
@@ -201,26 +168,19 @@ __global__ void __launch_bounds__(kTreeMergeThreads, 3) tree_merge_kernel(const 
   // (the grid leaves out the last share that the workspace has room for)
   const int shares = *a.shares;
   const TreeBound mine = a.bounds[share], next = a.bounds[share + 1];
-  if (share + 1 >= shares) return;  // the last share splits nothing
-  if (next.step == 0) return;       // an item starts there
-  const bool same = mine.b == next.b && mine.kvh == next.kvh;
-  if (same && mine.step > 0) return;  // the item started in an earlier share
-  int last = share + 1;               // the share that ends the item
+  if (!tree_splits(mine, next, share, shares)) return;
+  int last = share + 1;  // the share that ends the item
 #pragma unroll 1
   for (;;) {
     const int s = last + 1 + lane;
     bool ends = true;
-    if (s < shares) {
-      const TreeBound e = a.bounds[s];
-      ends = e.b != next.b || e.kvh != next.kvh || e.step == 0;
-    }
+    if (s < shares) ends = tree_item_ends(next, a.bounds[s]);
     const unsigned found = __ballot_sync(kFull, ends);
     last += found ? __ffs(found) - 1 : 32;
     if (found) break;
   }
   const int parts = last - share + 1;
-  // the owner's partial is its first unit's place if the share starts with the item
-  const size_t first = (static_cast<size_t>(cta) * 2 + (same ? 0 : 1)) * rows;
+  const size_t first = (static_cast<size_t>(cta) * 2 + tree_split_place(mine, next)) * rows;
   const size_t stride = static_cast<size_t>(a.NP) * 2 * rows;  // from a share's partials to the next one's
   const size_t cont = (static_cast<size_t>(cta) * 2) * rows;
   const int rr0 = slice * kTreeMergeCta + warp * kRows;

@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       }
       const int n = (b == end.b && kvh == end.kvh ? end.step : nt) - j0;
       const int t0 = j0 * kTreeTokens, t1 = min(ctx, (j0 + n) * kTreeTokens);
-      const int part = (j0 == 0 && n == nt) ? 0 : (first_unit ? 1 : 2);
+      const int part = tree_unit_part(j0, n, nt, first_unit);
       first_unit = false;
       vref = 0.f;  // of the unit; 0: no page with a scale yet
       const int npages = (t1 - t0 + BS - 1) / BS;
