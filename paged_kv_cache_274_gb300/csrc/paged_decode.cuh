@@ -478,6 +478,9 @@ __device__ __forceinline__ void mma_finish(MmaState<D, BS, FP8, HI>& st, const D
 #pragma unroll
         for (int n = 0; n < D / 8; ++n) st.o[n][2 * r] = st.o[n][2 * r + 1] = tree_row_value(row_state[r]);
       }
+      // the merges leave out partials without a maximum: a row may have none
+      // because it attends to NaNs alone
+      if (row_state[r] != kTreeRowZero && st.m[r] == -INFINITY && (row_state[r] == kTreeRowNan || st.l[r] != st.l[r])) st.m[r] = 0.f;
     }
     const size_t qrow = static_cast<size_t>(b * p.T + t) * p.Hq + h;
     if (nparts == 1) {
