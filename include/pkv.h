@@ -335,8 +335,8 @@ pkv_status pkv_decode_multi_describe(const pkv_cache_desc* cache, int32_t batch,
  *   whose bit is set in row t of the tree's mask.
  * Rows t >= m_b, and rows that attend to nothing, are zeros.  K and V of
  * nodes that a row does not attend to have no influence on it, whatever they
- * hold.  A row that attends to a node whose V holds a NaN or an infinity is
- * NaN in every column.
+ * hold.  A row that attends to a node whose V holds a NaN or an infinity, or to
+ * any token of a page whose v scale is not finite, is NaN in every column.
  *
  *   q, out         device bf16 [B][T][Hq][D] (must not overlap), T = num_query_tokens
  *                  in 1..PKV_MAX_QUERY_TOKENS, the most nodes of a sequence.

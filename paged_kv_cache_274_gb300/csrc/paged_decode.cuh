@@ -996,6 +996,14 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
             for (int r = 0; r < kR; ++r) rv[r] = static_cast<int>(vmask);
           }
+          // a page with a v scale that is not finite: NaN for the rows that
+          // attend to any of its tokens, out of the others' products (0 x NaN)
+          if (FP8 && !(fabsf(vsc) < INFINITY)) {
+            vsc = 0.f;
+#pragma unroll
+            for (int r = 0; r < kR; ++r)
+              if (rv[r] != 0 && row_state[r] == kTreeRowNormal) row_state[r] = kTreeRowNan;
+          }
         } else {
 #pragma unroll
           for (int r = 0; r < kR; ++r) rv[r] = MT ? min(valid, lim[r] - pos0) : valid;

@@ -453,10 +453,13 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           bool plain = true;
           if constexpr (kOneByte) {
             // vref moves when a step's v scales are more than 2^6 above it, so
-            // that P, below 2^8, stays below 2^14 in f16
-            const float vm = __uint_as_float(__reduce_max_sync(kFull, mine ? __float_as_uint(fabsf(par.z)) : 0u));
+            // that P, below 2^8, stays below 2^14 in f16.  A scale that is
+            // not finite takes no part; P of its page's tokens is NaN, in the
+            // rows that attend to them
+            const bool finite = fabsf(par.z) < INFINITY;
+            const float vm = __uint_as_float(__reduce_max_sync(kFull, mine && finite ? __float_as_uint(fabsf(par.z)) : 0u));
             if (vm > 64.f * vref) vref = vm;
-            const float ratio = mine && vref > 0.f ? par.z / vref : 0.f;
+            const float ratio = !mine ? 0.f : !finite ? __uint_as_float(0x7fffffffu) : vref > 0.f ? par.z / vref : 0.f;
             plain = __all_sync(kFull, !mine || (par.x >= 0.f && par.x < INFINITY && par.z > 0.f && par.z < INFINITY));
             if (q >= 0 && q < PPI) {
               const_cast<TaStep*>(step_at(g))->par[q] =
@@ -1044,13 +1047,14 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
               tc_ld16(t_h + 16u * q, y);
               tc_wait_ld_regs16(y);
               const float vr = st->par[(64 * hh + 16 * q) / BS].z;
+              const uint32_t mk = static_cast<uint32_t>(rm >> (16 * q));
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const float p0 = ex2_approx(__uint_as_float(y[2 * e]) + neg_m);
                 const float p1 = ex2_approx(__uint_as_float(y[2 * e + 1]) + neg_m);
                 l += p0 + p1;
                 // (a masked token's page may have no finite scale: 0 x that would be NaN)
-                pw[e] = pack_f16x2(p0 != 0.f ? p0 * vr : 0.f, p1 != 0.f ? p1 * vr : 0.f);
+                pw[e] = pack_f16x2(((mk >> (2 * e)) & 1u) ? p0 * vr : 0.f, ((mk >> (2 * e + 1)) & 1u) ? p1 * vr : 0.f);
               }
               tc_st8(t_h + 8u * q, pw);
             }

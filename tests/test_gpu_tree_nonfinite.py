@@ -38,3 +38,40 @@ def test_rows_that_attend_to_nans_alone(dtype, D, T, math, what):
         assert pkv.read_device_error() == 0
         assert np.isnan(got[bad]).all(), f"share {share}"
         assert_tree_close(np.where(bad[..., None, None], clean, got), clean, wabs, f"share {share}")
+
+
+@pytest.mark.parametrize("dtype", ["fp8", "int8a"])
+@pytest.mark.parametrize("T,math", [(4, pkv.MATH_MMA), (24, pkv.MATH_MMA), (24, pkv.MATH_TC), (60, pkv.MATH_TC)])
+@pytest.mark.parametrize("which,bad", [("v", np.nan), ("v", np.inf), ("v", -np.inf), ("k", np.nan), ("v and k", np.nan)])
+def test_scales_that_are_not_finite(dtype, T, math, which, bad):
+    # the pages of the last nodes: in the same step as every other page, in a
+    # later step, and in a sequence that is nothing but nodes
+    Hq, Hkv, late = 16, 4, T - 2 if T < 16 else 16
+    lens = [32 - late % 16 + T, 608 - late % 16 + T, T]
+    c = random_case(7490 + T, 3, Hq, Hkv, 128, 16, lens, kv_dtype=dtype)
+    dc = DeviceCase(c)
+    q = normal_bf16_bits(7491, (3, T, Hq, 128))
+    nodes = np.full(3, T, np.int32)
+    see, _ = visible(random_parents(np.random.Generator(np.random.PCG64(7492)), 3, T, 40), nodes)
+    clean, wabs = tree_attention(q, dc.k_host, dc.v_host, c.block_tables, c.context_lens, see, nodes, c.scale, c.k_scale, c.v_scale)
+    touched = np.zeros((3, T), bool)
+    for b, n in enumerate(lens):
+        page = (n - 1) // 16
+        first = max(0, page * 16 - (n - T))  # its first node
+        if n - T > page * 16 or (n == T and T < 16):  # (holds tokens that every row attends to, or is the only page)
+            continue
+        touched[b] = see[b, :, first:].any(1)
+        for s in ([c.v_scale] if which == "v" else [c.k_scale] if which == "k" else [c.v_scale, c.k_scale]):
+            if dtype == "fp8":
+                s[0, c.block_tables[b, page]] = bad
+            else:
+                s[0, c.block_tables[b, page], :, 0] = bad
+    assert touched.any() and not touched.all()
+    dc.ks, dc.vs = to_dev(c.k_scale), to_dev(c.v_scale)
+    for share in (0, 1, 256 if math == pkv.MATH_TC else 64):
+        out = pkv.paged_decode_tree(to_dev_bf16(q), dc.k, dc.v, dc.bt, dc.cl, to_dev(pack(see)), scale=c.scale, k_scale=dc.ks,
+                                    v_scale=dc.vs, opts=pkv.decode_opts(partition_blocks=share, math=math))
+        got = bf16_dev_to_f64(out)
+        assert pkv.read_device_error() == 0
+        assert np.isnan(got[touched]).all(), f"share {share}"
+        assert_tree_close(np.where(touched[..., None, None], clean, got), clean, wabs, f"share {share}")
