@@ -477,6 +477,11 @@ pkv_status pkv_extend_tables(int32_t batch, int32_t block_size, int32_t max_bloc
  * is not valid either), with PKV_DEVERR_TREE, _CONTEXT_LEN or _BLOCK_ID.
  * max_accept in 1..PKV_MAX_QUERY_TOKENS.  Blocks of the moved rows must belong
  * to one sequence only.  One kernel launch (none when B == 0).
+ *
+ * An inactive sequence (context_lens[b] 0) with nothing accepted gets
+ * seq_lens[b] = 0.  That is right for a request that has ended; one that
+ * pkv_extend_tables has refused still has its tokens, so a loop over both calls
+ * uses pkv_compact_tokens_kept.
  */
 pkv_status pkv_compact_tokens(const pkv_cache_desc* cache, const int32_t* accept_idx,
                               const int32_t* accept_counts, int32_t max_accept, int32_t batch,
@@ -485,6 +490,25 @@ pkv_status pkv_compact_tokens(const pkv_cache_desc* cache, const int32_t* accept
                               int32_t max_blocks_per_seq, void* k_cache, void* v_cache,
                               const float* k_scale, const float* v_scale, int32_t* seq_lens,
                               void* stream);
+
+/*
+ * pkv_compact_tokens of a step whose tables came from pkv_extend_tables: the
+ * requests that were refused there keep their length.
+ *   new_lens, prev_seq_lens   device int32 [B]: new_lens and seq_lens of that
+ *                  call.  A sequence with context_lens[b] 0 is not looked at
+ *                  (whatever its node and accept counts hold): seq_lens[b]
+ *                  becomes 0 if new_lens[b] is -1, else prev_seq_lens[b].
+ *   seq_lens       may be prev_seq_lens (updated in place).
+ *   everything else as in pkv_compact_tokens.
+ */
+pkv_status pkv_compact_tokens_kept(const pkv_cache_desc* cache, const int32_t* accept_idx,
+                                   const int32_t* accept_counts, int32_t max_accept, int32_t batch,
+                                   const int32_t* context_lens, const int32_t* node_counts,
+                                   int32_t num_nodes, const int32_t* block_tables,
+                                   int32_t max_blocks_per_seq, void* k_cache, void* v_cache,
+                                   const float* k_scale, const float* v_scale,
+                                   const int32_t* new_lens, const int32_t* prev_seq_lens,
+                                   int32_t* seq_lens, void* stream);
 
 /* Size of the library's built-in decode workspace (see below). */
 #define PKV_STATIC_WORKSPACE_MAX_BYTES ((size_t)16 << 20)

@@ -20,7 +20,8 @@ A step of speculative decoding with drafted trees:
   :func:`extend_tables` (blocks and slots for the nodes), :func:`kv_append`,
   :func:`tree_masks` (what each node sees, and its position),
   :func:`paged_decode_tree` per layer, and, once the target model has chosen
-  a path, :func:`compact_tokens`.
+  a path, :func:`compact_tokens` (with the step's ``new_lens`` and
+  ``prev_seq_lens``, so that a request without room keeps its tokens).
 """
 from __future__ import annotations
 
@@ -126,6 +127,8 @@ def load() -> ctypes.CDLL:
         lib.pkv_extend_tables.argtypes = [i32, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, P, P, P, i32, P]
         lib.pkv_compact_tokens.restype = ctypes.c_int
         lib.pkv_compact_tokens.argtypes = [pdesc, P, P, i32, i32, P, P, i32, P, i32, P, P, P, P, P, P]
+        lib.pkv_compact_tokens_kept.restype = ctypes.c_int
+        lib.pkv_compact_tokens_kept.argtypes = [pdesc, P, P, i32, i32, P, P, i32, P, i32, P, P, P, P, P, P, P, P]
         lib.pkv_paged_decode_static_workspace.restype = ctypes.c_int
         lib.pkv_paged_decode_static_workspace.argtypes = [pdesc, P, i32, i32, P, P, P, P, P, i32, P,
                                                           P, i32, i32, f32, P, popts, P]
@@ -645,8 +648,9 @@ def extend_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_tables: 
     ``new_free_state`` are given.  Returns (context_lens [B], query_starts
     [B + 1], slot_mapping int64 [max_tokens], positions [max_tokens]).  A
     request that cannot be served has context length 0 and slots -1, and
-    :func:`read_device_error` says why (see pkv_extend_tables in the
-    header)."""
+    :func:`read_device_error` says why (see pkv_extend_tables in the header);
+    it keeps its blocks and its seq_lens[b] tokens, which the caller passes
+    again with the next step."""
     fn, args, result, _ = _marshal_extend_tables(seq_lens, new_lens, block_tables, block_counts, free_ring, free_state,
                                                  block_size, max_tokens, borrowed_counts, new_block_counts,
                                                  new_free_state, context_lens, query_starts, slot_mapping, positions,
@@ -656,7 +660,8 @@ def extend_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_tables: 
 
 
 def _marshal_compact_tokens(accept_idx, accept_counts, context_lens, block_tables, k_cache, v_cache, num_nodes,
-                            node_counts=None, k_scale=None, v_scale=None, seq_lens=None, stream=None):
+                            node_counts=None, k_scale=None, v_scale=None, seq_lens=None, stream=None, new_lens=None,
+                            prev_seq_lens=None):
     desc = cache_desc(k_cache)
     i32 = torch.int32
     _need_here("k_cache", k_cache, k_cache.dtype)
@@ -675,29 +680,45 @@ def _marshal_compact_tokens(accept_idx, accept_counts, context_lens, block_table
     if desc.dtype != KV_BF16:
         _need_page_params(desc, k_scale, "k_scale")
         _need_page_params(desc, v_scale, "v_scale")
+    if (new_lens is None) != (prev_seq_lens is None):
+        raise PkvError(1, "new_lens and prev_seq_lens go together")
+    if new_lens is not None:
+        _need_here("new_lens", new_lens, i32, (B,))
+        _need_here("prev_seq_lens", prev_seq_lens, i32, (B,))
     if seq_lens is None:
         with _allocating_on(stream):
             seq_lens = torch.empty((B,), dtype=i32, device=k_cache.device)
     _need_here("seq_lens", seq_lens, i32, (B,))
     args = (ctypes.byref(desc), _ptr(accept_idx), _ptr(accept_counts), A, B, _ptr(context_lens), _ptr(node_counts),
             int(num_nodes), _ptr(block_tables), block_tables.shape[1], _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-            _ptr(v_scale), _ptr(seq_lens))
-    return (load().pkv_compact_tokens, args, seq_lens,
-            (accept_idx, accept_counts, context_lens, node_counts, block_tables, k_cache, v_cache, k_scale, v_scale))
+            _ptr(v_scale))
+    keep = (accept_idx, accept_counts, context_lens, node_counts, block_tables, k_cache, v_cache, k_scale, v_scale)
+    if new_lens is None:
+        return load().pkv_compact_tokens, args + (_ptr(seq_lens),), seq_lens, keep
+    return (load().pkv_compact_tokens_kept, args + (_ptr(new_lens), _ptr(prev_seq_lens), _ptr(seq_lens)), seq_lens,
+            keep + (new_lens, prev_seq_lens))
 
 
 def compact_tokens(accept_idx: torch.Tensor, accept_counts: torch.Tensor, context_lens: torch.Tensor,
                    block_tables: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, num_nodes: int,
                    node_counts: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None,
                    v_scale: Optional[torch.Tensor] = None, seq_lens: Optional[torch.Tensor] = None,
-                   stream=None) -> torch.Tensor:
+                   stream=None, new_lens: Optional[torch.Tensor] = None,
+                   prev_seq_lens: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Keep the accepted path of each verified tree: the K and V rows of nodes
     accept_idx[b][:accept_counts[b]] (strictly increasing) move, in every
     cache slot, to the positions from the tree's start on.  ``num_nodes`` is T
     of :func:`paged_decode_tree`.  Returns seq_lens [B], the tokens that each
-    sequence keeps."""
+    sequence keeps.
+
+    An inactive sequence (context_lens[b] 0) gets 0.  With ``new_lens`` and
+    ``prev_seq_lens``, the new_lens and seq_lens of the step's
+    :func:`extend_tables`, that holds for requests that have ended only: those
+    that were refused there keep prev_seq_lens[b], whatever their node and
+    accept counts hold.  ``seq_lens`` may be ``prev_seq_lens`` itself."""
     fn, args, result, _ = _marshal_compact_tokens(accept_idx, accept_counts, context_lens, block_tables, k_cache, v_cache,
-                                                  num_nodes, node_counts, k_scale, v_scale, seq_lens, stream)
+                                                  num_nodes, node_counts, k_scale, v_scale, seq_lens, stream, new_lens,
+                                                  prev_seq_lens)
     _check(fn(*args, _stream_handle(stream)))
     return result
 

@@ -77,6 +77,10 @@ __global__ void __launch_bounds__(kCompactThreads) compact_tokens_kernel(const C
   const int b = blockIdx.x / a.S, slot = blockIdx.x - b * a.S;
   const int n = a.context_lens[b], take = a.counts[b];
   const int nodes = a.node_counts != nullptr ? a.node_counts[b] : a.T;
+  if (n == 0 && a.prev_lens != nullptr) {  // refused by extend_tables, or ended (block-uniform)
+    if (slot == 0 && tid == 0) a.seq_lens[b] = a.new_lens[b] == -1 ? 0 : a.prev_lens[b];
+    return;
+  }
   const int base = n - nodes;
   unsigned err = 0;
   if (n < 0 || n > a.MB * a.bs) err |= PKV_DEVERR_CONTEXT_LEN;

@@ -964,12 +964,14 @@ pkv_status pkv_extend_tables(int32_t batch, int32_t block_size, int32_t max_bloc
   return PKV_OK;
 }
 
-pkv_status pkv_compact_tokens(const pkv_cache_desc* cache, const int32_t* accept_idx,
-                              const int32_t* accept_counts, int32_t max_accept, int32_t batch,
-                              const int32_t* context_lens, const int32_t* node_counts, int32_t num_nodes,
-                              const int32_t* block_tables, int32_t max_blocks_per_seq, void* k_cache,
-                              void* v_cache, const float* k_scale, const float* v_scale, int32_t* seq_lens,
-                              void* stream) {
+// new_lens, prev_lens: both or none (pkv_compact_tokens_kept).
+static pkv_status compact_call(const pkv_cache_desc* cache, const int32_t* accept_idx,
+                               const int32_t* accept_counts, int32_t max_accept, int32_t batch,
+                               const int32_t* context_lens, const int32_t* node_counts, int32_t num_nodes,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq, void* k_cache,
+                               void* v_cache, const float* k_scale, const float* v_scale,
+                               const int32_t* new_lens, const int32_t* prev_lens, int32_t* seq_lens,
+                               void* stream) {
   pkv_status st = check_cache_desc(cache);
   if (st != PKV_OK) return st;
   if (batch < 0) return fail(PKV_ERR_INVALID_ARG, "batch %d < 0", batch);
@@ -988,21 +990,46 @@ pkv_status pkv_compact_tokens(const pkv_cache_desc* cache, const int32_t* accept
   if (fp8 && !scales_aligned(cache->dtype, k_scale, v_scale))
     return fail(PKV_ERR_ALIGNMENT, "k_scale and v_scale must be 4-byte (E4M3) or 8-byte (INT8) aligned");
   if (!aligned16(k_cache) || !aligned16(v_cache)) return fail(PKV_ERR_ALIGNMENT, "caches must be 16-byte aligned");
-  if (!aligned4({accept_idx, accept_counts, context_lens, node_counts, block_tables, seq_lens}))
+  if (!aligned4({accept_idx, accept_counts, context_lens, node_counts, block_tables, new_lens, prev_lens, seq_lens}))
     return fail(PKV_ERR_ALIGNMENT, "index and length arrays must be 4-byte aligned");
   const size_t lens = static_cast<size_t>(batch) * 4;
   if (!disjoint({{seq_lens, lens}}, {{accept_idx, lens * max_accept}, {accept_counts, lens}, {context_lens, lens},
-                                     {node_counts, lens}, {block_tables, lens * max_blocks_per_seq}}))
+                                     {node_counts, lens}, {block_tables, lens * max_blocks_per_seq}, {new_lens, lens},
+                                     {prev_lens == seq_lens ? nullptr : prev_lens, lens}}))
     return fail(PKV_ERR_INVALID_ARG, "seq_lens must not overlap other arrays");
   DeviceInfo dev;
   if ((st = device_info(&dev)) != PKV_OK) return st;
-  const pkv::CompactArgs a{accept_idx, accept_counts, context_lens, node_counts, block_tables, seq_lens,
+  const pkv::CompactArgs a{accept_idx, accept_counts, context_lens, node_counts, block_tables, new_lens, prev_lens, seq_lens,
                            static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), fp8 ? k_scale : nullptr,
                            fp8 ? v_scale : nullptr, dev.err_word, batch, max_accept, num_nodes, max_blocks_per_seq,
                            cache->num_slots, cache->num_blocks, cache->num_kv_heads, cache->block_size, cache->head_dim};
   cudaError_t e = pkv::launch_compact_tokens(cache->dtype, a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "compact_tokens launch");
   return PKV_OK;
+}
+
+pkv_status pkv_compact_tokens(const pkv_cache_desc* cache, const int32_t* accept_idx,
+                              const int32_t* accept_counts, int32_t max_accept, int32_t batch,
+                              const int32_t* context_lens, const int32_t* node_counts, int32_t num_nodes,
+                              const int32_t* block_tables, int32_t max_blocks_per_seq, void* k_cache,
+                              void* v_cache, const float* k_scale, const float* v_scale, int32_t* seq_lens,
+                              void* stream) {
+  return compact_call(cache, accept_idx, accept_counts, max_accept, batch, context_lens, node_counts, num_nodes,
+                      block_tables, max_blocks_per_seq, k_cache, v_cache, k_scale, v_scale, nullptr, nullptr, seq_lens,
+                      stream);
+}
+
+pkv_status pkv_compact_tokens_kept(const pkv_cache_desc* cache, const int32_t* accept_idx,
+                                   const int32_t* accept_counts, int32_t max_accept, int32_t batch,
+                                   const int32_t* context_lens, const int32_t* node_counts, int32_t num_nodes,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq, void* k_cache,
+                                   void* v_cache, const float* k_scale, const float* v_scale,
+                                   const int32_t* new_lens, const int32_t* prev_seq_lens, int32_t* seq_lens,
+                                   void* stream) {
+  if (batch > 0 && (!new_lens || !prev_seq_lens)) return fail(PKV_ERR_INVALID_ARG, "new_lens or prev_seq_lens is NULL");
+  return compact_call(cache, accept_idx, accept_counts, max_accept, batch, context_lens, node_counts, num_nodes,
+                      block_tables, max_blocks_per_seq, k_cache, v_cache, k_scale, v_scale, new_lens, prev_seq_lens,
+                      seq_lens, stream);
 }
 
 pkv_status pkv_copy_blocks(const pkv_cache_desc* cache, const void* src_k, const void* src_v,

@@ -174,7 +174,9 @@ struct CompactArgs {
   const int32_t* context_lens;
   const int32_t* node_counts;  // [B], NULL: T each
   const int32_t* block_tables;
-  int32_t* seq_lens;
+  const int32_t* new_lens;   // [B] with prev_lens: what an inactive sequence keeps;
+  const int32_t* prev_lens;  // both NULL: nothing
+  int32_t* seq_lens;         // may be prev_lens
   uint8_t* kc;
   uint8_t* vc;
   const float* ks;  // page parameters (one-byte caches)
