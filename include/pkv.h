@@ -414,7 +414,9 @@ pkv_status pkv_tree_masks(const int32_t* parents, const int32_t* context_lens,
  *   new_lens[b] == -1: the request has ended.  Its blocks, but for the first
  *     borrowed_counts[b] (blocks that it shares and does not own), go behind
  *     the free ring's tail in row order; its count becomes 0.  Its row's
- *     entries stay as they are.
+ *     entries stay as they are.  If one of the blocks to give back is no
+ *     block (outside 0..NB-1: PKV_DEVERR_BLOCK_ID) it gives none back and
+ *     keeps its count, so that the ring never holds such an id.
  * A request is refused, with nothing of it changed and all its tokens' slots
  * -1, when too few blocks are free (PKV_DEVERR_NO_BLOCKS; then no later
  * request that needs blocks gets any), when its token rows do not fit

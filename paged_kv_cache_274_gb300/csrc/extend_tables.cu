@@ -14,7 +14,11 @@
 // that costs each CTA B reads of three arrays out of L2 (3 KB for 256
 // requests), less than a grid-wide barrier or a second launch.  Then
 // the CTAs share the token rows, the taken and the returned blocks, each found
-// by binary search in its prefix sums.  Counts and the ring's head may be
+// by binary search in its prefix sums.  A request whose blocks to give back
+// hold an id that is no block gives none back, which the other requests' places
+// in the ring depend on: so the CTAs that return blocks look at all of those
+// ids first.  They are the last ones, which have the fewest token rows (all
+// CTAs, before the token rows: 1 us more for the prompts below).  Counts and the ring's head may be
 // updated in place although every CTA reads them: the CTA that arrives last,
 // when all others have read theirs, writes them (with one CTA, or arrays apart,
 // nobody waits).
@@ -32,7 +36,8 @@
 namespace pkv {
 
 constexpr int kExtThreads = 512;
-constexpr int kExtRun = 4;  // token rows of a thread where there are many
+constexpr int kExtRun = 4;   // token rows of a thread where there are many
+constexpr int kExtLook = 8;  // returned blocks that a thread looks at together
 
 struct ExtRequest {
   int seq, add, held, need, gone, borrowed;
@@ -66,16 +71,78 @@ __device__ __forceinline__ int ext_find(const int* pre, int n, int i) {
   return lo;
 }
 
+// Block number k of those given back, rel[b] <= k < rel[b + 1], is at [k].
+__device__ __forceinline__ const int32_t* ext_given_back(const ExtendArgs& a, const int* rel, int b) {
+  return a.block_tables + static_cast<size_t>(b) * a.MB + (a.borrowed != nullptr ? max(a.borrowed[b], 0) : 0) - rel[b];
+}
+
+// Marks the ended requests with an id that is no block among those to give back,
+// and takes them out of rel.  Returns whether there are any.  Whole CTA.
+__device__ __forceinline__ bool ext_faults(const ExtendArgs& a, int* rel, uint32_t* faulty) {
+  const int B = a.B, tid = threadIdx.x, lane = tid & 31, total = rel[B];
+  for (int i = tid; i < (B + 31) / 32; i += kExtThreads) faulty[i] = 0u;
+  __syncthreads();
+  bool wrong = false;
+  // runs of up to kExtLook blocks a thread, which mostly are one request's:
+  // one search, and the loads in flight together
+  const int look = min(kExtLook, (total + kExtThreads - 1) / kExtThreads);
+  for (int k0 = tid * look; k0 < total; k0 += kExtThreads * look) {
+    int id[kExtLook], of[kExtLook];
+    int b = 0, end = 0;
+    const int32_t* row = nullptr;
+#pragma unroll
+    for (int u = 0; u < kExtLook; ++u) {
+      id[u] = 0;
+      const int k = k0 + u;
+      if (u >= look || k >= total) continue;
+      if (k >= end) {
+        b = ext_find(rel, B, k);
+        end = rel[b + 1];
+        row = ext_given_back(a, rel, b);
+      }
+      id[u] = row[k];
+      of[u] = b;
+    }
+#pragma unroll
+    for (int u = 0; u < kExtLook; ++u)
+      if (static_cast<uint32_t>(id[u]) >= static_cast<uint32_t>(a.NB)) {
+        wrong = true;
+        atomicOr(&faulty[of[u] >> 5], 1u << (of[u] & 31));
+      }
+  }
+  if (!__syncthreads_or(wrong)) return false;
+  if (tid < 32) {
+    int carry = 0;
+    for (int c = 0; c <= B; c += 32) {
+      const int b = c + lane;
+      const int gone = b < B && !((faulty[b >> 5] >> (b & 31)) & 1u) ? rel[b + 1] - rel[b] : 0;
+      int x = gone;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncwarp();  // (the next 32 read no entry that is written here)
+      if (b <= B) rel[b] = carry + x - gone;
+      carry += __shfl_sync(kFull, x, 31);
+    }
+  }
+  __syncthreads();
+  return true;
+}
+__device__ __noinline__ bool ext_faults_again(const ExtendArgs& a, int* rel, uint32_t* faulty) { return ext_faults(a, rel, faulty); }
+
 __global__ void __launch_bounds__(kExtThreads) extend_tables_kernel(const ExtendArgs a) {
   extern __shared__ int sm_ext[];
   __shared__ long long warp_tok[kExtThreads / 32];
   __shared__ int warp_need[kExtThreads / 32], warp_gone[kExtThreads / 32];
-  __shared__ int last_s, taken_s;
+  __shared__ int last_s, faults_s, taken_s;
   const int B = a.B, N = a.N;
   const uint32_t NB = static_cast<uint32_t>(a.NB);
   int* tok = sm_ext;         // [B + 1] first token row of each request, at most N
   int* blk = tok + B + 1;    // [B + 1] blocks that the requests before need
   int* rel = blk + B + 1;    // [B + 1] blocks that the requests before give back
+  uint32_t* faulty = reinterpret_cast<uint32_t*>(rel + B + 1);  // [B bits] ended requests with ids that are no blocks
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
   pdl_wait();
@@ -205,6 +272,11 @@ __global__ void __launch_bounds__(kExtThreads) extend_tables_kernel(const Extend
         }
     }
   }
+  // the CTAs that return blocks, from the last one on (the last one in any case)
+  const int last_first = (gridDim.x - 1 - blockIdx.x) * kExtThreads;
+  const bool looked = pool_ok && rel[B] > 0 && (last_first == 0 || last_first < rel[B]);
+  const bool apart = a.counts_out != a.counts_in && a.state_out != a.state_in;
+  bool faults = false;  // (block-uniform)
   if (pool_ok) {
     // taken blocks, into the requests' rows of the table (entries past those
     // that the token rows read)
@@ -213,12 +285,18 @@ __global__ void __launch_bounds__(kExtThreads) extend_tables_kernel(const Extend
       const ExtRequest r = ext_request(a, b);
       if (granted(b, r)) a.block_tables[static_cast<size_t>(b) * a.MB + r.held + (k - blk[b])] = a.ring[ring_at(k)];
     }
-    // returned blocks, behind the free ones (places that no taken block is read from)
-    for (int k = first; k < rel[B]; k += stride) {
-      const int b = ext_find(rel, B, k);
-      const ExtRequest r = ext_request(a, b);
-      const int id = a.block_tables[static_cast<size_t>(b) * a.MB + r.borrowed + (k - rel[b])];
-      if (static_cast<uint32_t>(id) >= NB) err |= PKV_DEVERR_BLOCK_ID;
+    // returned blocks, behind the free ones (places that no taken block is read
+    // from); the thread's first one is on its way while the ids are looked at
+    int k = last_first + tid, id = 0;
+    if (k < rel[B]) id = ext_given_back(a, rel, ext_find(rel, B, k))[k];
+    if (looked && ext_faults(a, rel, faulty)) {
+      faults = true;
+      err |= PKV_DEVERR_BLOCK_ID;
+      if (tid == 0 && gridDim.x > 1 && !apart) atomicOr(reinterpret_cast<unsigned*>(a.state_in) + 3, 1u);
+      if (k < rel[B]) id = ext_given_back(a, rel, ext_find(rel, B, k))[k];
+    }
+    for (; k < rel[B]; k += stride) {
+      if (k >= stride) id = ext_given_back(a, rel, ext_find(rel, B, k))[k];
       a.ring[ring_at(free_blocks + k)] = id;
     }
   } else {
@@ -239,20 +317,23 @@ __global__ void __launch_bounds__(kExtThreads) extend_tables_kernel(const Extend
   if (err) atomicOr(a.err, err);
 
   // Counts and the ring's state, once every CTA has read them: by the only
-  // CTA, by the first where they do not go where they came from, else by the
-  // last one to arrive.
+  // CTA, by the last one where they do not go where they came from, else by
+  // the last one to arrive.
   __syncthreads();
-  const bool apart = a.counts_out != a.counts_in && a.state_out != a.state_in;
   if (gridDim.x > 1 && !apart) {
     if (tid == 0) {
+      unsigned* scratch = reinterpret_cast<unsigned*>(a.state_in) + 2;
       __threadfence();
-      last_s = atomicInc(reinterpret_cast<unsigned*>(a.state_in) + 2, gridDim.x - 1) == gridDim.x - 1;  // wraps to 0
+      last_s = atomicInc(scratch, gridDim.x - 1) == gridDim.x - 1;  // wraps to 0
+      faults_s = last_s && atomicExch(scratch + 1, 0u) != 0u;
     }
     __syncthreads();
     if (!last_s) return;
-  } else if (blockIdx.x > 0) {
+    if (faults_s && !looked) faults = ext_faults_again(a, rel, faulty);
+  } else if (blockIdx.x + 1 < gridDim.x) {
     return;
   }
+  auto stays = [&](int b) { return faults && ((faulty[b >> 5] >> (b & 31)) & 1u) != 0u; };
   int taken = 0;
   for (int b = tid; b < B; b += kExtThreads) {
     const ExtRequest r = ext_request(a, b);
@@ -260,7 +341,7 @@ __global__ void __launch_bounds__(kExtThreads) extend_tables_kernel(const Extend
     if (granted(b, r)) {
       held += r.need;
       if (r.need > 0) taken = max(taken, blk[b] + r.need);
-    } else if (pool_ok && r.valid && r.done) {
+    } else if (pool_ok && r.valid && r.done && !stays(b)) {
       held = 0;
     }
     a.counts_out[b] = held;
@@ -275,7 +356,7 @@ __global__ void __launch_bounds__(kExtThreads) extend_tables_kernel(const Extend
 }
 
 cudaError_t launch_extend_tables(const ExtendArgs& a, int num_sms, cudaStream_t stream) {
-  const size_t smem = sizeof(int) * 3 * (static_cast<size_t>(a.B) + 1);
+  const size_t smem = sizeof(int) * (3 * (static_cast<size_t>(a.B) + 1) + (static_cast<size_t>(a.B) + 31) / 32);  // 199 KB at most
   if (smem > 48 * 1024 - 1024) {
     const cudaError_t e = cudaFuncSetAttribute(extend_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;

@@ -156,7 +156,7 @@ struct ExtendArgs {
   const int32_t* counts_in;
   int32_t* counts_out;
   int32_t* ring;
-  int32_t* state_in;  // head, free blocks, CTAs arrived (scratch)
+  int32_t* state_in;  // head, free blocks, scratch: CTAs arrived, ids that are no blocks seen
   int32_t* state_out;
   int32_t* context_lens;
   int32_t* query_starts;
