@@ -185,21 +185,33 @@ def _stream_handle(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
-# The current stream's handle without a Stream object (0.1 us instead of 3)
-# where torch has the call.
+# The current device, and its current stream's handle without a Stream object
+# (0.1 us instead of 3), by torch's internal calls where it has them.
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _check_device(device: int):
+    """A prepared call launches on the current device: its tensors are there."""
+    here = _get_device() if _get_device is not None else torch.cuda.current_device()
+    if here != device:
+        raise PkvError(1, f"the call's tensors are on cuda:{device}, the current device is cuda:{here}")
 
 
 def _current_handle(device: int):
     """cudaStream_t of the current stream, for a prepared call whose tensors
-    are on this device (the call launches on the current device)."""
-    if _raw_stream is None:
-        here, h = torch.cuda.current_device(), torch.cuda.current_stream(device).cuda_stream
-    else:
-        here, h = torch._C._cuda_getDevice(), _raw_stream(device)
-    if here != device:
-        raise PkvError(1, f"the call's tensors are on cuda:{device}, the current device is cuda:{here}")
-    return h
+    are on this device."""
+    _check_device(device)
+    return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _prepared_handle(device: int, stream, bound):
+    """The stream of a prepared call: the one given, the one it was prepared
+    with, or the current one."""
+    if stream is None and bound is None:
+        return _current_handle(device)
+    _check_device(device)
+    return bound if stream is None else _stream_handle(stream)
 
 
 def _need_cuda(name: str, t: torch.Tensor, dtype=None):
@@ -526,11 +538,7 @@ class PreparedDecode:
         self._device = q.get_device()
 
     def __call__(self, stream=None) -> torch.Tensor:
-        if stream is not None:
-            h = _stream_handle(stream)
-        else:
-            h = self._stream if self._stream is not None else _current_handle(self._device)
-        st = self._fn(*self._args, h)
+        st = self._fn(*self._args, _prepared_handle(self._device, stream, self._stream))
         if st != PKV_OK:
             _check(st)
         return self.out
@@ -740,11 +748,7 @@ class PreparedCall:
         self._device = self._keep[0].get_device()
 
     def __call__(self, stream=None):
-        if stream is not None:
-            h = _stream_handle(stream)
-        else:
-            h = self._stream if self._stream is not None else _current_handle(self._device)
-        st = self._fn(*self._args, h)
+        st = self._fn(*self._args, _prepared_handle(self._device, stream, self._stream))
         if st != PKV_OK:
             _check(st)
         return self.result
