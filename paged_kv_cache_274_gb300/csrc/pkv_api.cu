@@ -426,7 +426,8 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
   const long long mma_rows = !tree || c->dtype != PKV_KV_BF16 ? 16 : c->head_dim == 64 ? 8 : 0;
   if (math == PKV_MATH_AUTO) math = (tc_ok && static_cast<long long>(T) * G > mma_rows) ? PKV_MATH_TC : PKV_MATH_MMA;
   if (math == PKV_MATH_TC && !tc_ok)
-    return fail(PKV_ERR_UNSUPPORTED, "tcgen05 tiles need T > 1, head_dim 128 and G <= 128");
+    return tree ? fail(PKV_ERR_UNSUPPORTED, "G = %d query heads per KV head (tcgen05 tiles of drafted trees support <= 128)", G)
+                : fail(PKV_ERR_UNSUPPORTED, "tcgen05 tiles need T > 1, head_dim 128 and G <= 128");
   if (math == PKV_MATH_MMA && G > 16)
     return fail(PKV_ERR_UNSUPPORTED, "G = %d query heads per KV head (mma supports <= 16)", G);
   if (math == PKV_MATH_FFMA && G != 1 && G != 2 && G != 4 && G != 8)
@@ -435,7 +436,8 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
     return fail(PKV_ERR_INVALID_ARG, "math %d", math);
   const bool tc = math == PKV_MATH_TC;
   if (math == PKV_MATH_FFMA && (T > 1 || tree))
-    return fail(PKV_ERR_UNSUPPORTED, "multi-token queries need the mma back-end");
+    return fail(PKV_ERR_UNSUPPORTED, tree ? "drafted trees need the mma.sync or the tcgen05 back-end"
+                                          : "multi-token queries need the mma back-end");
   if (static_cast<long long>(batch) * T * Hq * c->head_dim >= (1LL << 31))
     return fail(PKV_ERR_UNSUPPORTED, "batch x query tokens x heads x head_dim too large");
   // row tiles of at most 16 (mma.sync) or 128 (tcgen05) (query token, head)
