@@ -351,7 +351,11 @@ pkv_status pkv_decode_multi_describe(const pkv_cache_desc* cache, int32_t batch,
  *   opts           PKV_MATH_TC takes T = 1 and head_dim 64 too (bf16), and
  *                  shares of equal work instead of partitions:
  *                  partition_blocks is the fewest blocks of a share, warps
- *                  and stages have no effect.
+ *                  and stages have no effect.  On one-byte caches it carries
+ *                  the v scales in f16 weights: a page whose v scale is below
+ *                  2^-14 of the largest that its share of the sequence holds
+ *                  has fewer than 11 bits of each weight; PKV_MATH_MMA applies
+ *                  the scales in fp32.
  *   everything else as in pkv_paged_decode_multi.
  */
 pkv_status pkv_paged_decode_tree(const pkv_cache_desc* cache,

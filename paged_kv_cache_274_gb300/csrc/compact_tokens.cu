@@ -13,11 +13,13 @@
 // scale, in fp32) is quantised with the new page's parameters as an append
 // does.
 //
-// One CTA per (sequence, cache slot) takes all KV heads of K and V: bound by
-// HBM, 2 x the moved rows' bytes (32 bf16 slots, 64 sequences, paths of up to
-// 8: 67 MB in 10.3 us, 0.96 of the copy rate; with a 64-bit division per
-// row's offset it was 13), or, with few rows, by the chain of loads from the
-// counts to the rows (8 E4M3 slots, 128 sequences, 17 MB: 8 us cold).
+// One CTA per (sequence, cache slot) takes all KV heads of K and V.  Bound by
+// latency, the chain of loads from the counts to the path, the table, the page
+// parameters and the rows, which every CTA walks for itself: 32 bf16 slots of 64
+// sequences with 1.7 moved rows each, 28.5 MB read and written (4.2 us at the
+// copy rate; a pass after another finds them in L2), take 10 us (13 with a
+// 64-bit division per row's offset); 8 E4M3 slots of 128 sequences with 1.9 rows,
+// 8 MB (1.2 us), 10 us with the host's call, 8 to 10 us cold under a profile.
 #include <algorithm>
 
 #include "kv_append.cuh"

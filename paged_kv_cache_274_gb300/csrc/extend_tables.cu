@@ -23,9 +23,10 @@
 // when all others have read theirs, writes them (with one CTA, or arrays apart,
 // nobody waits).
 //
-// Bound by latency: 256 requests of 8 to 32 new tokens take 10 us under a cold
-// profile and less than the host's call otherwise; 48 prompts of up to 24,000
-// tokens (570,000 rows, 6.9 MB written) 10.5 us.  There a thread takes runs of
+// Bound by latency: 256 requests of 8 to 32 new tokens, of which a tenth end
+// with some 130 blocks each, take 9 to 10 us with the host's call, the longer of
+// the two; 48 prompts of up to 24,000 tokens (570,000 rows, 6.9 MB written) 10.6
+// us.  There a thread takes runs of
 // four rows, which mostly share their request and block: one search, one table
 // entry, wide stores (a row per thread at a time: 15 us).
 #include <algorithm>

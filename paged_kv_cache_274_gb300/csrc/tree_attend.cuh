@@ -17,9 +17,11 @@
 // run at HBM speed (64 sequences of 2048 to 4096 tokens, 32 nodes, 8 KV heads:
 // 156 us with plan and merge, 0.80 of the copy rate), long contexts with many
 // rows at 0.64 of the bf16 peak (4 x 32k tokens, 64 nodes, 8 heads a KV head:
-// 218 us), and one-byte caches at the issue rate of the sub-partitions: 1600
-// instructions a step each, against 940 of bf16 caches, for the page scales
-// and the widening.
+// 218 us).  One-byte caches fill no unit: a sub-partition issues 1600
+// instructions a step, against 940 of bf16 caches, for the page scales and the
+// widening, but only 60% (E4M3) or 53% (INT8) of the time, with DRAM at 41 and
+// 29% and the tensor pipe at 38 and 27%: a step is a chain of hand-overs (codes
+// landed, widened, S, the maximum agreed, P, PV).
 //
 // One CTA per SM, no CTA-wide barrier inside the loop:
 //   * Two streams of eight softmax warps, each stream with its own S and O in
@@ -453,7 +455,9 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           bool plain = true;
           if constexpr (kOneByte) {
             // vref moves when a step's v scales are more than 2^6 above it, so
-            // that P, below 2^8, stays below 2^14 in f16.  A scale that is
+            // that P, below 2^8, stays below 2^14 in f16.  (The weights of a
+            // page whose scale is below 2^-14 of vref lose bits to f16's
+            // subnormals; the mma.sync path has no such limit.)  A scale that is
             // not finite takes no part; P of its page's tokens is NaN, in the
             // rows that attend to them
             const bool finite = fabsf(par.z) < INFINITY;
