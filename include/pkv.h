@@ -83,7 +83,7 @@ typedef enum { PKV_KV_BF16 = 0, PKV_KV_FP8_E4M3 = 1, PKV_KV_INT8 = 2 } pkv_kv_dt
 #define PKV_DEVERR_CONTEXT_LEN 0x4u  /* context length outside [0, MB*bs] */
 #define PKV_DEVERR_TIMEOUT 0x8u      /* a bounded wait on a copy gave up */
 #define PKV_DEVERR_NO_BLOCKS 0x10u   /* too few free blocks for a request's new tokens */
-#define PKV_DEVERR_TREE 0x20u        /* a drafted tree's node count, parent or accepted path */
+#define PKV_DEVERR_TREE 0x20u        /* a drafted tree's node count, parent, token, probabilities or accepted path */
 
 /* Shape of one paged cache (both K and V).  Supported: block_size 16 or 32;
  * head_dim 64 or 128 for bf16, 128 for E4M3 and INT8. */
@@ -158,6 +158,62 @@ pkv_status pkv_kv_append(const pkv_cache_desc* cache, int32_t slot,
                          const void* k, const void* v, const int64_t* slot_mapping,
                          int32_t num_tokens, void* k_cache, void* v_cache,
                          const float* k_scale, const float* v_scale, void* stream);
+
+/* Most position axes of pkv_rope_append. */
+#define PKV_MAX_POSITION_AXES 4
+
+/*
+ * A step's queries and keys made ready for the attention, in one pass over the
+ * rows of their projections: the RMS norm of each head, the rotation by the
+ * tokens' positions, and the append of keys and values (pkv_kv_append).
+ * Source: [BW] "What the KV Cache Stores and Why" (each step computes K and V
+ * for the new token only and stores them); the pages take K as it comes.
+ *
+ * Of a head's row x of q or k, in fp32:
+ *   y = x / sqrt(mean(x^2) + eps) * weight, or x without weights;
+ *   for each pair i < rotary_dim / 2 of elements (a, b), with the angle
+ *   t = positions[freq_axes[i]][token] * inv_freq[i]:
+ *     a' = y_a cos t - y_b sin t,  b' = y_b cos t + y_a sin t;
+ *   elements from rotary_dim on stay y.
+ * Queries are rounded to bf16 once; keys once, to bf16 or to the cache's codes
+ * (from fp32, as pkv_kv_append quantises); values are appended as they are.
+ * Angles are exact to 2^-24 of half a turn at any int32 position.
+ *
+ *   slot           cache slot (layer group) to write, in [0, S).
+ *   q, k, v        device bf16 [N][Hq][D], [N][Hkv][D], [N][Hkv][D]: heads of a
+ *                  token one behind the other, tokens *_stride elements apart
+ *                  (a multiple of 8, at least the heads' size), so that the
+ *                  three may be parts of one projection's rows.
+ *                  k and v NULL: queries only (a layer that reads another
+ *                  layer's cache).
+ *   q_weight, k_weight  device bf16 [D], or NULL: no norm of q, of k.
+ *   eps            >= 0.
+ *   positions      device int32 [num_axes][N] (pkv_extend_tables and
+ *                  pkv_tree_masks make them for one axis).
+ *   inv_freq       HOST double [rotary_dim / 2]: radians per position, finite.
+ *   freq_axes      HOST int32 [rotary_dim / 2] in 0..num_axes-1, or NULL: 0.
+ *   rotary_dim     a multiple of 16 in 0..D (0: no rotation; positions,
+ *                  inv_freq and freq_axes are not read).
+ *   interleaved    0: pair i is elements i and i + rotary_dim / 2; 1: elements
+ *                  2 i and 2 i + 1.
+ *   slot_mapping   as in pkv_kv_append (device int64 [N]); a token whose slot
+ *                  is -1 is padding, of which no query is written either.  NULL
+ *                  with k NULL: no padding.
+ *   q_out          device bf16 [N][Hq][D], tokens q_out_stride elements apart;
+ *                  may be q itself (with the same stride), must not overlap
+ *                  anything else.
+ *   caches, scales as in pkv_kv_append (NULL where k is).
+ * One kernel launch (none when N == 0).
+ */
+pkv_status pkv_rope_append(const pkv_cache_desc* cache, int32_t slot,
+                           const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, int32_t num_tokens, int32_t num_q_heads,
+                           const void* q_weight, const void* k_weight, float eps,
+                           const int32_t* positions, int32_t num_axes,
+                           const double* inv_freq, const int32_t* freq_axes, int32_t rotary_dim,
+                           int32_t interleaved, const int64_t* slot_mapping,
+                           void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache,
+                           const float* k_scale, const float* v_scale, void* stream);
 
 /*
  * Bytes of device workspace pkv_paged_decode needs for these sizes (0 on a
@@ -463,6 +519,63 @@ pkv_status pkv_extend_tables(int32_t batch, int32_t block_size, int32_t max_bloc
                              int32_t* context_lens, int32_t* query_starts,
                              int64_t* slot_mapping, int32_t* positions, int32_t max_tokens,
                              void* stream);
+
+/* Largest vocabulary of pkv_verify_tree. */
+#define PKV_MAX_VOCAB (1 << 20)
+
+/*
+ * Which path of a drafted tree the target model accepts, and the token that
+ * follows it, from given random numbers ([PC] "How does speculative decoding
+ * interact with KV-cache compression?": the target verifies the draft's
+ * proposals).  The call between pkv_paged_decode_tree and pkv_compact_tokens.
+ *
+ * Node 0 is the root, the token that the step before sampled; it is always
+ * accepted.  target_probs row t is the target's distribution of the token that
+ * follows node t, draft_probs row t the draft's.  The walk starts at the root;
+ * at a node u it tries u's children c (tokens x) in order, with P = target row,
+ * Q = draft row and Z = Y = 1 at first:
+ *   r_c Q(x) Z < P(x) Y, r_c = accept_uniforms[b][c]: c is accepted, and the
+ *     walk goes on from c;
+ *   else P = max(P - (Z / Y) Q, 0) (Y <= 0: P as it is), Q(x) = 0, Z = sum P,
+ *     Y = sum Q.
+ * At a node without an accepted child (or once max_accept nodes are accepted)
+ * the next token is the first j whose partial sum of P exceeds
+ * sample_uniforms[b] x sum P; if nothing is left of P, that of the target row.
+ * So the tokens follow the target's distribution if each node's children were
+ * drawn one after another, without replacement, from the draft row.
+ * draft_probs NULL: children chosen without randomness (the draft's best
+ * tokens, a lookup); Q is then 1 at x alone and a rejection sets P(x) = 0.
+ * Values of rows that are negative or not finite count as 0.  Comparisons are
+ * made in fp64, sums to 2^-44 or better of their value.
+ *
+ *   tokens         device int32 [B][T]: the nodes' tokens, in [0, vocab) (node
+ *                  0's is not looked at).
+ *   parents        device int32 [B][T]: -1 for node 0, in 0..t-1 for node t.
+ *   node_counts    device int32 [B], in 0..T; NULL: T each.
+ *   target_probs   device fp32 [B][T][vocab], rows target_stride >= vocab
+ *                  elements apart.
+ *   draft_probs    likewise with draft_stride, or NULL.  Rows of nodes without
+ *                  children are not read.
+ *   accept_uniforms  device fp32 [B][T], in [0, 1).
+ *   sample_uniforms  device fp32 [B], in [0, 1).
+ *   accept_idx     device int32 [B][max_accept] (written): the accepted nodes,
+ *                  the root first; -1 behind them.
+ *   accept_counts  device int32 [B] (written).
+ *   next_tokens    device int32 [B] (written).
+ * A sequence without nodes gets count 0 and token -1.  So does one with a
+ * count, parent or token out of range, and PKV_DEVERR_TREE is set; a target row
+ * without any weight gives token -1 and that bit.
+ * T and max_accept in 1..PKV_MAX_QUERY_TOKENS, vocab in 1..PKV_MAX_VOCAB.  The
+ * arrays that are written overlap no others.  One kernel launch (none when B
+ * == 0), no workspace.
+ */
+pkv_status pkv_verify_tree(const int32_t* tokens, const int32_t* parents, const int32_t* node_counts,
+                           const float* target_probs, int64_t target_stride,
+                           const float* draft_probs, int64_t draft_stride,
+                           int32_t batch, int32_t num_nodes, int32_t vocab,
+                           const float* accept_uniforms, const float* sample_uniforms,
+                           int32_t* accept_idx, int32_t* accept_counts, int32_t max_accept,
+                           int32_t* next_tokens, void* stream);
 
 /*
  * After a drafted tree was verified: move the accepted path's tokens together,

@@ -96,6 +96,10 @@ def load() -> ctypes.CDLL:
         pdesc, popts = ctypes.POINTER(CacheDesc), ctypes.POINTER(DecodeOpts)
         lib.pkv_kv_append.restype = ctypes.c_int
         lib.pkv_kv_append.argtypes = [pdesc, i32, P, P, P, i32, P, P, P, P, P]
+        pf64, i64_ = ctypes.POINTER(ctypes.c_double), ctypes.c_int64
+        lib.pkv_rope_append.restype = ctypes.c_int
+        lib.pkv_rope_append.argtypes = [pdesc, i32, P, i64_, P, i64_, P, i64_, i32, i32, P, P, f32, P, i32, pf64,
+                                        ctypes.POINTER(i32), i32, i32, P, P, i64_, P, P, P, P, P]
         lib.pkv_decode_workspace_bytes.restype = sz
         lib.pkv_decode_workspace_bytes.argtypes = [pdesc, i32, i32, i32, popts]
         lib.pkv_decode_describe.restype = ctypes.c_int
@@ -125,6 +129,8 @@ def load() -> ctypes.CDLL:
         lib.pkv_tree_masks.argtypes = [P, P, P, i32, i32, P, P, P]
         lib.pkv_extend_tables.restype = ctypes.c_int
         lib.pkv_extend_tables.argtypes = [i32, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, P, P, P, i32, P]
+        lib.pkv_verify_tree.restype = ctypes.c_int
+        lib.pkv_verify_tree.argtypes = [P, P, P, P, i64_, P, i64_, i32, i32, i32, P, P, P, P, i32, P, P]
         lib.pkv_compact_tokens.restype = ctypes.c_int
         lib.pkv_compact_tokens.argtypes = [pdesc, P, P, i32, i32, P, P, i32, P, i32, P, P, P, P, P, P]
         lib.pkv_compact_tokens_kept.restype = ctypes.c_int
@@ -285,6 +291,99 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
     _check(load().pkv_kv_append(ctypes.byref(desc), int(slot), _ptr(k), _ptr(v), _ptr(slot_mapping),
                                 N, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
                                 _stream_handle(stream)))
+
+
+def _need_rows(name: str, t: torch.Tensor, shape) -> int:
+    """A bf16 tensor [N][H][D] on the current device whose heads lie one behind
+    the other; returns the elements between its tokens."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise PkvError(1, f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise PkvError(1, f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.get_device() != torch.cuda.current_device():
+        raise PkvError(1, f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.dim() != 3 or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise PkvError(1, f"{name} must be {''.join('[%s]' % ('H' if w is None else w) for w in shape)}, got {list(t.shape)}")
+    N, H, D = t.shape
+    if N == 0:
+        return H * D
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise PkvError(1, f"{name}'s heads must lie one behind the other")
+    return t.stride(0) if N > 1 else H * D
+
+
+def _marshal_rope_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None, slot=0,
+                         q_weight=None, k_weight=None, eps=1e-6, freq_axes=None, interleaved=False, out=None, stream=None):
+    desc = cache_desc(k_cache)
+    D, Hkv = desc.head_dim, desc.num_kv_heads
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise PkvError(1, "q must be [N][Hq][D]")
+    N, Hq = q.shape[0], q.shape[1]
+    q_stride = _need_rows("q", q, (N, None, D))
+    if (k is None) != (v is None):
+        raise PkvError(1, "k and v go together")
+    k_stride = v_stride = Hkv * D
+    _need_here("k_cache", k_cache, k_cache.dtype)
+    if k is not None:
+        k_stride, v_stride = _need_rows("k", k, (N, Hkv, D)), _need_rows("v", v, (N, Hkv, D))
+        _need_here("v_cache", v_cache, k_cache.dtype, tuple(k_cache.shape))
+        if desc.dtype != KV_BF16:
+            _need_page_params(desc, k_scale, "k_scale")
+            _need_page_params(desc, v_scale, "v_scale")
+        if slot_mapping is None:
+            raise PkvError(1, "slot_mapping is required with k and v")
+    if slot_mapping is not None:
+        _need_here("slot_mapping", slot_mapping, torch.int64, (N,))
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _need_here(name, w, torch.bfloat16, (D,))
+    freqs = [] if inv_freq is None else [float(f) for f in (inv_freq.tolist() if hasattr(inv_freq, "tolist") else inv_freq)]
+    axes = 1
+    if freqs:
+        _need_here("positions", positions, torch.int32)
+        if positions.dim() not in (1, 2) or positions.shape[-1] != N:
+            raise PkvError(1, f"positions must be [{N}] or [axes][{N}], got {list(positions.shape)}")
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+    which = None
+    if freq_axes is not None:
+        which = [int(x) for x in (freq_axes.tolist() if hasattr(freq_axes, "tolist") else freq_axes)]
+        if len(which) != len(freqs):
+            raise PkvError(1, f"freq_axes has {len(which)} entries, inv_freq {len(freqs)}")
+    if out is None:
+        with _allocating_on(stream):
+            out = torch.empty((N, Hq, D), dtype=torch.bfloat16, device=q.device)
+    out_stride = _need_rows("out", out, (N, Hq, D))
+    append = k is not None
+    args = (ctypes.byref(desc), int(slot), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, N, Hq, _ptr(q_weight),
+            _ptr(k_weight), float(eps), _ptr(positions) if freqs else None, axes,
+            (ctypes.c_double * len(freqs))(*freqs) if freqs else None,
+            (ctypes.c_int32 * len(which))(*which) if which else None, 2 * len(freqs), 1 if interleaved else 0,
+            _ptr(slot_mapping), _ptr(out), out_stride, _ptr(k_cache) if append else None, _ptr(v_cache) if append else None,
+            _ptr(k_scale) if append else None, _ptr(v_scale) if append else None)
+    return (load().pkv_rope_append, args, out,
+            (q, k, v, positions, slot_mapping, k_cache, v_cache, k_scale, v_scale, q_weight, k_weight))
+
+
+def rope_append(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                inv_freq: Optional[Sequence[float]], slot_mapping: Optional[torch.Tensor], k_cache: torch.Tensor,
+                v_cache: torch.Tensor, k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                slot: int = 0, q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                eps: float = 1e-6, freq_axes: Optional[Sequence[int]] = None, interleaved: bool = False,
+                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """A step's queries and keys made ready for the attention in one pass: the
+    RMS norm of each head (``q_weight`` / ``k_weight``, bf16 [D]; None: no norm),
+    the rotation by ``positions`` (int32 [N] or [axes][N]), and k, v written to
+    ``slot_mapping`` as :func:`kv_append` does.  q [N][Hq][D], k and v [N][Hkv][D]
+    are bf16 and may be parts of one projection's rows.  ``inv_freq``: radians per
+    position of each pair of elements (its length is half of the rotated
+    elements; None: no rotation), ``freq_axes`` the position axis of each.
+    ``interleaved``: pairs are neighbours instead of halves.  Without k and v the
+    queries alone are made.  Tokens with slot -1 are left out.  Returns the
+    queries, [N][Hq][D] (``out`` may be q itself)."""
+    fn, args, result, _ = _marshal_rope_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+                                               slot, q_weight, k_weight, eps, freq_axes, interleaved, out, stream)
+    _check(fn(*args, _stream_handle(stream)))
+    return result
 
 
 def decode_opts(partition_blocks: int = 0, math: int = MATH_AUTO, warps: int = 0,
@@ -667,6 +766,80 @@ def extend_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_tables: 
     return result
 
 
+def _need_probs(name: str, t: torch.Tensor, B: int, T: int, V: Optional[int]) -> int:
+    """fp32 rows [B][T][V] on the current device at equal distances; returns the
+    elements between them."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise PkvError(1, f"{name} must be a CUDA tensor")
+    if t.dtype != torch.float32:
+        raise PkvError(1, f"{name} must be {torch.float32}, got {t.dtype}")
+    if t.get_device() != torch.cuda.current_device():
+        raise PkvError(1, f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.dim() != 3 or t.shape[0] != B or t.shape[1] != T or (V is not None and t.shape[2] != V):
+        raise PkvError(1, f"{name} must be [{B}][{T}][{'vocab' if V is None else V}], got {list(t.shape)}")
+    V = t.shape[2]
+    between = t.stride(1) if T > 1 else t.stride(0) if B > 1 else V
+    if (V > 1 and t.stride(2) != 1) or (T > 1 and B > 1 and t.stride(0) != T * t.stride(1)):
+        raise PkvError(1, f"{name}'s rows must be contiguous and at equal distances")
+    return max(between, V) if B * T <= 1 else between
+
+
+def _marshal_verify_tree(tokens, parents, target_probs, accept_uniforms, sample_uniforms, draft_probs=None, node_counts=None,
+                         max_accept=None, accept_idx=None, accept_counts=None, next_tokens=None, stream=None):
+    i32 = torch.int32
+    _need_here("tokens", tokens, i32)
+    if tokens.dim() != 2:
+        raise PkvError(1, "tokens must be [B][T]")
+    B, T = tokens.shape
+    if not 1 <= T <= MAX_QUERY_TOKENS:
+        raise PkvError(1, f"tokens must have 1..{MAX_QUERY_TOKENS} nodes, got {T}")
+    _need_here("parents", parents, i32, (B, T))
+    target_stride = _need_probs("target_probs", target_probs, B, T, None)
+    V = target_probs.shape[2]
+    draft_stride = 0 if draft_probs is None else _need_probs("draft_probs", draft_probs, B, T, V)
+    _need_here("accept_uniforms", accept_uniforms, torch.float32, (B, T))
+    _need_here("sample_uniforms", sample_uniforms, torch.float32, (B,))
+    if node_counts is not None:
+        _need_here("node_counts", node_counts, i32, (B,))
+    A = T if max_accept is None else int(max_accept)
+    if not 1 <= A <= MAX_QUERY_TOKENS:
+        raise PkvError(1, f"max_accept {A} outside 1..{MAX_QUERY_TOKENS}")
+    with _allocating_on(stream):
+        if accept_idx is None:
+            accept_idx = torch.empty((B, A), dtype=i32, device=tokens.device)
+        if accept_counts is None:
+            accept_counts = torch.empty((B,), dtype=i32, device=tokens.device)
+        if next_tokens is None:
+            next_tokens = torch.empty((B,), dtype=i32, device=tokens.device)
+    _need_here("accept_idx", accept_idx, i32, (B, A))
+    _need_here("accept_counts", accept_counts, i32, (B,))
+    _need_here("next_tokens", next_tokens, i32, (B,))
+    args = (_ptr(tokens), _ptr(parents), _ptr(node_counts), _ptr(target_probs), target_stride, _ptr(draft_probs), draft_stride,
+            B, T, V, _ptr(accept_uniforms), _ptr(sample_uniforms), _ptr(accept_idx), _ptr(accept_counts), A, _ptr(next_tokens))
+    return (load().pkv_verify_tree, args, (accept_idx, accept_counts, next_tokens),
+            (tokens, parents, node_counts, target_probs, draft_probs, accept_uniforms, sample_uniforms))
+
+
+def verify_tree(tokens: torch.Tensor, parents: torch.Tensor, target_probs: torch.Tensor, accept_uniforms: torch.Tensor,
+                sample_uniforms: torch.Tensor, draft_probs: Optional[torch.Tensor] = None,
+                node_counts: Optional[torch.Tensor] = None, max_accept: Optional[int] = None,
+                accept_idx: Optional[torch.Tensor] = None, accept_counts: Optional[torch.Tensor] = None,
+                next_tokens: Optional[torch.Tensor] = None, stream=None):
+    """The path of each drafted tree that the target model accepts, and the token
+    that follows it.  ``tokens`` and ``parents`` (int32 [B][T]; node 0 is the root,
+    parent -1) are the trees, ``target_probs`` (fp32 [B][T][vocab]) the target's
+    distribution behind each node, ``draft_probs`` the distribution that each
+    node's children were drawn from without replacement (None: children chosen
+    without randomness), ``accept_uniforms`` [B][T] and ``sample_uniforms`` [B]
+    random numbers in [0, 1).  Returns (accept_idx int32 [B][max_accept],
+    accept_counts [B], next_tokens [B]); the first two go to
+    :func:`compact_tokens`."""
+    fn, args, result, _ = _marshal_verify_tree(tokens, parents, target_probs, accept_uniforms, sample_uniforms, draft_probs,
+                                               node_counts, max_accept, accept_idx, accept_counts, next_tokens, stream)
+    _check(fn(*args, _stream_handle(stream)))
+    return result
+
+
 def _marshal_compact_tokens(accept_idx, accept_counts, context_lens, block_tables, k_cache, v_cache, num_nodes,
                             node_counts=None, k_scale=None, v_scale=None, seq_lens=None, stream=None, new_lens=None,
                             prev_seq_lens=None):
@@ -732,17 +905,18 @@ def compact_tokens(accept_idx: torch.Tensor, accept_counts: torch.Tensor, contex
 
 
 class PreparedCall:
-    """A call of :func:`tree_masks`, :func:`extend_tables` or
-    :func:`compact_tokens` (``op``, then its arguments) checked and marshalled
+    """A call of :func:`tree_masks`, :func:`extend_tables`,
+    :func:`compact_tokens`, :func:`rope_append` or :func:`verify_tree` (``op``, then its arguments) checked and marshalled
     once, like :class:`PreparedDecode`: each call of the object enqueues the
     same launch again on whatever the bound tensors hold, and returns the
     bound result tensors."""
 
     def __init__(self, op, *args, stream=None, **kwargs):
         marshal = {tree_masks: _marshal_tree_masks, extend_tables: _marshal_extend_tables,
-                   compact_tokens: _marshal_compact_tokens}.get(op)
+                   compact_tokens: _marshal_compact_tokens, rope_append: _marshal_rope_append,
+                   verify_tree: _marshal_verify_tree}.get(op)
         if marshal is None:
-            raise PkvError(1, "PreparedCall takes tree_masks, extend_tables or compact_tokens")
+            raise PkvError(1, "PreparedCall takes tree_masks, extend_tables, compact_tokens, rope_append or verify_tree")
         self._fn, self._args, self.result, self._keep = marshal(*args, stream=stream, **kwargs)
         self._stream = None if stream is None else _stream_handle(stream)
         self._device = self._keep[0].get_device()

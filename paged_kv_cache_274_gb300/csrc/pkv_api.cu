@@ -300,13 +300,10 @@ const char* pkv_last_error_message(void) { return t_last_error.c_str(); }
 
 }  // extern "C"
 
-// Validate a KV append into cache slot `slot` and resolve its launch
-// arguments; *a is left untouched unless PKV_OK.  num_tokens >= 1.
-static pkv_status prepare_append(const pkv_cache_desc* cache, int32_t slot, const void* k, const void* v,
-                                 const int64_t* slot_mapping, int32_t num_tokens, void* k_cache,
-                                 void* v_cache, const float* k_scale, const float* v_scale,
-                                 cudaStream_t s, const DeviceInfo* dev, pkv::AppendArgs* a) {
-  pkv_status st;
+// What the host can see of a KV append into cache slot `slot` (num_tokens >= 1).
+static pkv_status check_append(const pkv_cache_desc* cache, int32_t slot, const void* k, const void* v,
+                               const int64_t* slot_mapping, const void* k_cache, const void* v_cache,
+                               const float* k_scale, const float* v_scale) {
   if (slot < 0 || slot >= cache->num_slots)
     return fail(PKV_ERR_INVALID_ARG, "slot %d outside [0, %d)", slot, cache->num_slots);
   const bool fp8 = cache->dtype != PKV_KV_BF16;  // one-byte elements (E4M3 or INT8)
@@ -319,6 +316,18 @@ static pkv_status prepare_append(const pkv_cache_desc* cache, int32_t slot, cons
     return fail(PKV_ERR_ALIGNMENT, "k, v and caches must be 16-byte aligned");
   if ((reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0)
     return fail(PKV_ERR_ALIGNMENT, "slot_mapping must be 8-byte aligned");
+  return PKV_OK;
+}
+
+// Validate a KV append into cache slot `slot` and resolve its launch
+// arguments; *a is left untouched unless PKV_OK.  num_tokens >= 1.
+static pkv_status prepare_append(const pkv_cache_desc* cache, int32_t slot, const void* k, const void* v,
+                                 const int64_t* slot_mapping, int32_t num_tokens, void* k_cache,
+                                 void* v_cache, const float* k_scale, const float* v_scale,
+                                 cudaStream_t s, const DeviceInfo* dev, pkv::AppendArgs* a) {
+  pkv_status st = check_append(cache, slot, k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale);
+  if (st != PKV_OK) return st;
+  const bool fp8 = cache->dtype != PKV_KV_BF16;  // one-byte elements (E4M3 or INT8)
   const long long nslots = static_cast<long long>(cache->num_blocks) * cache->block_size;
   if (env_flag("PKV_VALIDATE")) {
     std::vector<int64_t> sm;
@@ -366,16 +375,7 @@ pkv_status pkv_kv_append(const pkv_cache_desc* cache, int32_t slot, const void* 
     return fail(PKV_ERR_INVALID_ARG, "slot %d outside [0, %d)", slot, cache->num_slots);
   if (num_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
   if (num_tokens == 0) return PKV_OK;
-  if (!k || !v || !slot_mapping || !k_cache || !v_cache)
-    return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
-  const bool fp8 = cache->dtype != PKV_KV_BF16;
-  if (fp8 && (!k_scale || !v_scale)) return fail(PKV_ERR_INVALID_ARG, "E4M3 and INT8 caches need k_scale and v_scale");
-  if (fp8 && !scales_aligned(cache->dtype, k_scale, v_scale))
-    return fail(PKV_ERR_ALIGNMENT, "k_scale and v_scale must be 4-byte (E4M3) or 8-byte (INT8) aligned");
-  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache))
-    return fail(PKV_ERR_ALIGNMENT, "k, v and caches must be 16-byte aligned");
-  if ((reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0)
-    return fail(PKV_ERR_ALIGNMENT, "slot_mapping must be 8-byte aligned");
+  if ((st = check_append(cache, slot, k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale)) != PKV_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   DeviceInfo dev_info;
   const DeviceInfo* dev = &dev_info;
@@ -386,6 +386,107 @@ pkv_status pkv_kv_append(const pkv_cache_desc* cache, int32_t slot, const void* 
     return st;
   cudaError_t e = pkv::launch_kv_append(cache->dtype, a, s);
   if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
+  return PKV_OK;
+}
+
+pkv_status pkv_rope_append(const pkv_cache_desc* cache, int32_t slot, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, int32_t num_tokens, int32_t num_q_heads,
+                           const void* q_weight, const void* k_weight, float eps, const int32_t* positions,
+                           int32_t num_axes, const double* inv_freq, const int32_t* freq_axes, int32_t rotary_dim,
+                           int32_t interleaved, const int64_t* slot_mapping, void* q_out, int64_t q_out_stride,
+                           void* k_cache, void* v_cache, const float* k_scale, const float* v_scale, void* stream) {
+  pkv_status st = check_cache_desc(cache);
+  if (st != PKV_OK) return st;
+  const int D = cache->head_dim, R = rotary_dim, N = num_tokens;
+  if (slot < 0 || slot >= cache->num_slots)
+    return fail(PKV_ERR_INVALID_ARG, "slot %d outside [0, %d)", slot, cache->num_slots);
+  if (N < 0) return fail(PKV_ERR_INVALID_ARG, "num_tokens %d < 0", N);
+  if (num_q_heads < 1) return fail(PKV_ERR_INVALID_ARG, "num_q_heads %d < 1", num_q_heads);
+  if (R < 0 || R > D || R % 16 != 0)
+    return fail(PKV_ERR_UNSUPPORTED, "rotary_dim %d (supported: multiples of 16 up to the head_dim %d)", R, D);
+  if (interleaved != 0 && interleaved != 1) return fail(PKV_ERR_INVALID_ARG, "interleaved %d", interleaved);
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(PKV_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if ((k == nullptr) != (v == nullptr)) return fail(PKV_ERR_INVALID_ARG, "k and v go together");
+  const bool append = k != nullptr;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * D, kv_row = static_cast<int64_t>(cache->num_kv_heads) * D;
+  if (q_row >= (1LL << 31)) return fail(PKV_ERR_UNSUPPORTED, "num_q_heads %d", num_q_heads);
+  if (q_stride < q_row || q_out_stride < q_row || (append && (k_stride < kv_row || v_stride < kv_row)))
+    return fail(PKV_ERR_INVALID_ARG, "a token stride is below the size of its heads");
+  if ((q_stride | q_out_stride) % 8 != 0 || (append && (k_stride | v_stride) % 8 != 0))
+    return fail(PKV_ERR_ALIGNMENT, "token strides must be multiples of 8 elements");
+  const int64_t strides = std::max(std::max(q_stride, q_out_stride), append ? std::max(k_stride, v_stride) : 0);
+  if (strides >= (1LL << 31)) return fail(PKV_ERR_UNSUPPORTED, "token stride %lld", static_cast<long long>(strides));
+  if (R > 0) {
+    if (num_axes < 1 || num_axes > PKV_MAX_POSITION_AXES)
+      return fail(PKV_ERR_INVALID_ARG, "num_axes %d outside 1..%d", num_axes, PKV_MAX_POSITION_AXES);
+    if (inv_freq == nullptr) return fail(PKV_ERR_INVALID_ARG, "inv_freq is NULL");
+    for (int i = 0; i < R / 2; ++i) {
+      if (!std::isfinite(inv_freq[i])) return fail(PKV_ERR_INVALID_ARG, "inv_freq[%d] is not finite", i);
+      if (freq_axes != nullptr && (freq_axes[i] < 0 || freq_axes[i] >= num_axes))
+        return fail(PKV_ERR_INVALID_ARG, "freq_axes[%d] = %d outside [0, %d)", i, freq_axes[i], num_axes);
+    }
+  }
+  if (N == 0) return PKV_OK;
+  if (!q || !q_out || (R > 0 && !positions) || (append && !slot_mapping))
+    return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(q_weight) || !aligned16(k_weight))
+    return fail(PKV_ERR_ALIGNMENT, "q, q_out and the norms' weights must be 16-byte aligned");
+  if (!aligned4({positions}) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0)
+    return fail(PKV_ERR_ALIGNMENT, "positions must be 4-byte aligned, slot_mapping 8-byte");
+  if (append && (st = check_append(cache, slot, k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale)) != PKV_OK) return st;
+  auto span = [&](const void* p, int64_t stride, int64_t row) {
+    return Span{p, static_cast<size_t>(((N - 1) * stride + row) * 2)};
+  };
+  const bool in_place = q_out == q && q_out_stride == q_stride;
+  const size_t pool = static_cast<size_t>(cache->num_slots) * cache->num_blocks * cache->num_kv_heads * cache->block_size * D *
+                      (cache->dtype == PKV_KV_BF16 ? 2 : 1);
+  const size_t weights = static_cast<size_t>(D) * 2, rows = static_cast<size_t>(N);
+  const Span none{nullptr, 0};
+  // (in place, q_out lies between the rows of k and v as q does)
+  if (!disjoint({span(q_out, q_out_stride, q_row)},
+                {in_place ? none : span(q, q_stride, q_row), in_place || !append ? none : span(k, k_stride, kv_row),
+                 in_place || !append ? none : span(v, v_stride, kv_row), Span{q_weight, weights}, Span{k_weight, weights},
+                 R > 0 ? Span{positions, rows * 4 * num_axes} : none, Span{slot_mapping, rows * 8},
+                 append ? Span{k_cache, pool} : none, append ? Span{v_cache, pool} : none}))
+    return fail(PKV_ERR_INVALID_ARG, "q_out overlaps another array");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != PKV_OK) return st;
+  pkv::RopeArgs a{};
+  if (append) {
+    if ((st = prepare_append(cache, slot, k, v, slot_mapping, N, k_cache, v_cache, k_scale, v_scale, s, &dev, &a.app)) != PKV_OK)
+      return st;
+  } else {
+    a.app.N = N;
+    a.app.Hkv = cache->num_kv_heads;
+    a.app.D = D;
+    a.app.bs = cache->block_size;
+    a.app.nslots = static_cast<int64_t>(cache->num_blocks) * cache->block_size;
+    a.app.slot_mapping = slot_mapping;
+    a.app.err = dev.err_word;
+  }
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.qw = static_cast<const uint16_t*>(q_weight);
+  a.kw = append ? static_cast<const uint16_t*>(k_weight) : nullptr;
+  a.positions = positions;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.out_stride = q_out_stride;
+  a.eps = eps;
+  a.Hq = num_q_heads;
+  a.R = R;
+  a.k_new = append ? 1 : 0;
+  for (int i = 0; i < R / 2; ++i) {
+    const double turns = inv_freq[i] / 6.283185307179586476925, part = turns - std::floor(turns);
+    a.turns[i] = part < 1.0 ? static_cast<uint64_t>(std::ldexp(part, 64)) : 0;
+    a.axis[i] = static_cast<uint8_t>(freq_axes != nullptr ? freq_axes[i] : 0);
+  }
+  cudaError_t e = pkv::launch_rope_append(cache->dtype, D, interleaved == 0, a, dev.num_sms, s);
+  if (e != cudaSuccess) return cuda_fail(e, "rope_append launch");
   return PKV_OK;
 }
 
@@ -963,6 +1064,49 @@ pkv_status pkv_extend_tables(int32_t batch, int32_t block_size, int32_t max_bloc
                           max_blocks_per_seq, num_blocks, block_size, max_tokens};
   cudaError_t e = pkv::launch_extend_tables(a, dev.num_sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "extend_tables launch");
+  return PKV_OK;
+}
+
+pkv_status pkv_verify_tree(const int32_t* tokens, const int32_t* parents, const int32_t* node_counts,
+                           const float* target_probs, int64_t target_stride, const float* draft_probs,
+                           int64_t draft_stride, int32_t batch, int32_t num_nodes, int32_t vocab,
+                           const float* accept_uniforms, const float* sample_uniforms, int32_t* accept_idx,
+                           int32_t* accept_counts, int32_t max_accept, int32_t* next_tokens, void* stream) {
+  if (batch < 0) return fail(PKV_ERR_INVALID_ARG, "batch %d < 0", batch);
+  if (num_nodes < 1 || num_nodes > PKV_MAX_QUERY_TOKENS || max_accept < 1 || max_accept > PKV_MAX_QUERY_TOKENS)
+    return fail(PKV_ERR_INVALID_ARG, "num_nodes %d, max_accept %d outside 1..%d", num_nodes, max_accept,
+                PKV_MAX_QUERY_TOKENS);
+  if (vocab < 1) return fail(PKV_ERR_INVALID_ARG, "vocab %d < 1", vocab);
+  if (vocab > PKV_MAX_VOCAB) return fail(PKV_ERR_UNSUPPORTED, "vocab %d (supported: up to %d)", vocab, PKV_MAX_VOCAB);
+  if (target_stride < vocab || (draft_probs != nullptr && draft_stride < vocab))
+    return fail(PKV_ERR_INVALID_ARG, "a row stride is below the vocabulary %d", vocab);
+  const int64_t stride_max = 1LL << 40;
+  if (target_stride > stride_max || (draft_probs != nullptr && draft_stride > stride_max))
+    return fail(PKV_ERR_UNSUPPORTED, "a row stride is above 2^40");
+  if (static_cast<long long>(batch) * num_nodes >= (1LL << 24) || static_cast<long long>(batch) * max_accept >= (1LL << 24))
+    return fail(PKV_ERR_UNSUPPORTED, "batch x nodes too large");
+  if (batch == 0) return PKV_OK;
+  if (!tokens || !parents || !target_probs || !accept_uniforms || !sample_uniforms || !accept_idx || !accept_counts || !next_tokens)
+    return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned4({tokens, parents, node_counts, target_probs, draft_probs, accept_uniforms, sample_uniforms, accept_idx,
+                 accept_counts, next_tokens}))
+    return fail(PKV_ERR_ALIGNMENT, "every array must be 4-byte aligned");
+  const size_t lens = static_cast<size_t>(batch) * 4, nodes = lens * num_nodes, rows = static_cast<size_t>(batch) * num_nodes - 1;
+  if (!disjoint({{accept_idx, lens * max_accept}, {accept_counts, lens}, {next_tokens, lens}},
+                {{tokens, nodes}, {parents, nodes}, {node_counts, lens}, {accept_uniforms, nodes}, {sample_uniforms, lens},
+                 {target_probs, (rows * target_stride + vocab) * 4},
+                 {draft_probs, draft_probs != nullptr ? (rows * draft_stride + vocab) * 4 : 0}}))
+    return fail(PKV_ERR_INVALID_ARG, "arrays that are written overlap other arrays");
+  DeviceInfo dev;
+  pkv_status st = device_info(&dev);
+  if (st != PKV_OK) return st;
+  const bool vec = vocab % 4 == 0 && aligned16(target_probs) && target_stride % 4 == 0 &&
+                   (draft_probs == nullptr || (aligned16(draft_probs) && draft_stride % 4 == 0));
+  const pkv::VerifyArgs a{tokens, parents, node_counts, target_probs, draft_probs, accept_uniforms, sample_uniforms,
+                          accept_idx, accept_counts, next_tokens, dev.err_word, target_stride, draft_stride,
+                          batch, num_nodes, vocab, max_accept, vec ? 1 : 0};
+  cudaError_t e = pkv::launch_verify_tree(a, dev.num_sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "verify_tree launch");
   return PKV_OK;
 }
 

@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "pkv.h"
@@ -119,6 +120,24 @@ void* current_context();
 // KV append.
 cudaError_t launch_kv_append(int kv_dtype, const AppendArgs& a, cudaStream_t stream);
 
+// Norms and rotation of queries and keys with the append of keys and values.
+struct RopeArgs {
+  AppendArgs app;  // N, the slots and the cache; its k and v are not used
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  __nv_bfloat16* q_out;  // may be q
+  const uint16_t* qw;    // bf16 [D] weights, NULL: no norm
+  const uint16_t* kw;
+  const int32_t* positions;  // [axes][N]
+  long long q_stride, k_stride, v_stride, out_stride;  // elements between tokens
+  float eps;
+  int Hq, R, k_new, parts;
+  uint64_t turns[64];  // turns per position of each pair, in 2^-64
+  uint8_t axis[64];    // its position axis
+};
+cudaError_t launch_rope_append(int kv_dtype, int D, bool halves, RopeArgs a, int num_sms, cudaStream_t stream);
+
 // Block copy between two pools of the same page shape.
 cudaError_t launch_copy_blocks(const void* src_k, const void* src_v, const float* src_ks,
                                const float* src_vs, int src_nb, void* dst_k, void* dst_v,
@@ -185,6 +204,25 @@ struct CompactArgs {
   int B, A, T, MB, S, NB, Hkv, bs, D;
 };
 cudaError_t launch_compact_tokens(int kv_dtype, const CompactArgs& a, cudaStream_t stream);
+
+// Drafted trees against the target's probabilities.
+struct VerifyArgs {
+  const int32_t* tokens;       // [B][T]
+  const int32_t* parents;      // [B][T]
+  const int32_t* node_counts;  // [B], NULL: T each
+  const float* p;              // target rows, p_stride apart
+  const float* q;              // draft rows, NULL: drafts without randomness
+  const float* accept_uniforms;  // [B][T]
+  const float* sample_uniforms;  // [B]
+  int32_t* accept_idx;           // [B][A]
+  int32_t* accept_counts;
+  int32_t* next_tokens;
+  unsigned* err;
+  long long p_stride, q_stride;
+  int B, T, V, A;
+  int vec;  // 1: every row starts on a 16-byte boundary and V is a multiple of 4
+};
+cudaError_t launch_verify_tree(const VerifyArgs& a, int num_sms, cudaStream_t stream);
 
 // Read-only probe: sums the 32-bit words of `bytes` bytes (a multiple of 16,
 // 16-byte aligned) into *sum; one launch of up to 8 CTAs per SM.
