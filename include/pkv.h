@@ -84,6 +84,7 @@ typedef enum { PKV_KV_BF16 = 0, PKV_KV_FP8_E4M3 = 1, PKV_KV_INT8 = 2 } pkv_kv_dt
 #define PKV_DEVERR_TIMEOUT 0x8u      /* a bounded wait on a copy gave up */
 #define PKV_DEVERR_NO_BLOCKS 0x10u   /* too few free blocks for a request's new tokens */
 #define PKV_DEVERR_TREE 0x20u        /* a drafted tree's node count, parent, token, probabilities or accepted path */
+#define PKV_DEVERR_QUERY 0x40u       /* query_starts that do not rise, or too many rows of a sequence */
 
 /* Shape of one paged cache (both K and V).  Supported: block_size 16 or 32;
  * head_dim 64 or 128 for bf16, 128 for E4M3 and INT8. */
@@ -436,6 +437,54 @@ pkv_status pkv_decode_tree_describe(const pkv_cache_desc* cache, int32_t batch,
                                     int32_t num_query_tokens, int32_t num_q_heads,
                                     int32_t max_blocks_per_seq, const pkv_decode_opts* opts,
                                     pkv_decode_plan* plan);
+
+/*
+ * Attention of each sequence's new tokens, as many as it has, packed one
+ * sequence behind the other: the rows that pkv_extend_tables lays out, so that
+ * requests that decode one token, chunks of prompts and whole prompts run in
+ * one call ([BW] "Continuous Batching", chunked prefill).  Rows query_starts[b]
+ * .. query_starts[b + 1] - 1 of q are the last m tokens of the n =
+ * context_lens[b] cached ones of sequence b, causal among themselves:
+ *   out[query_starts[b] + t][h][:] = sum_j softmax_j(scale * q[..][h] . K_j) V_j,
+ *   j = 0 .. n - m + t.
+ * Rows with no position to attend to (n - m + t < 0, including n = 0) get
+ * zeros; rows outside every sequence are left as they were.  K and V of tokens
+ * that a row does not attend to have no influence on it, whatever they hold.  A
+ * row that attends to a new token (behind the first) of its sequence whose V
+ * holds a NaN or an infinity, or to any token of a page whose v scale is not
+ * finite, is NaN in every column.
+ *
+ *   q, out         device bf16 [num_rows][Hq][D]; out must not overlap q or
+ *                  the cache.
+ *   query_starts   device int32 [B + 1], rising, in 0..num_rows.  A sequence
+ *                  whose rows do not rise, leave 0..num_rows or are more than
+ *                  max_query_tokens sets PKV_DEVERR_QUERY; none of its rows is
+ *                  written.
+ *   max_query_tokens  >= 1, the most rows of a sequence (num_rows will do).
+ *   workspace      pkv_decode_packed_workspace_bytes() bytes.
+ *   opts           partition_blocks is the fewest blocks of a work share, math
+ *                  PKV_MATH_AUTO or PKV_MATH_TC; warps and stages have no
+ *                  effect.  (On one-byte caches the v scales are carried as in
+ *                  pkv_paged_decode_tree.)
+ *   everything else as in pkv_paged_decode_multi.  G <= 128.
+ */
+pkv_status pkv_paged_decode_packed(const pkv_cache_desc* cache,
+                                   const void* q, int32_t num_rows, int32_t batch,
+                                   int32_t max_query_tokens, int32_t num_q_heads,
+                                   const void* k_cache, const void* v_cache,
+                                   const float* k_scale, const float* v_scale,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* context_lens, const int32_t* query_starts,
+                                   const int32_t* kv_group_ptr, int32_t num_layers, int32_t layer,
+                                   float scale, void* out,
+                                   void* workspace, size_t workspace_bytes,
+                                   const pkv_decode_opts* opts, void* stream);
+
+/* Workspace bytes of pkv_paged_decode_packed (0 for invalid arguments). */
+size_t pkv_decode_packed_workspace_bytes(const pkv_cache_desc* cache, int32_t num_rows,
+                                         int32_t batch, int32_t max_query_tokens,
+                                         int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                         const pkv_decode_opts* opts);
 
 /*
  * Masks and positions of drafted trees from their nodes' parents, once per

@@ -42,7 +42,7 @@ STATUS_NAMES = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "alignment"
 KV_BF16, KV_FP8_E4M3, KV_INT8 = 0, 1, 2
 MATH_AUTO, MATH_FFMA, MATH_MMA, MATH_TC = 0, 1, 2, 3
 DEVERR_BLOCK_ID, DEVERR_SLOT, DEVERR_CONTEXT_LEN, DEVERR_TIMEOUT = 1, 2, 4, 8
-DEVERR_NO_BLOCKS, DEVERR_TREE = 16, 32
+DEVERR_NO_BLOCKS, DEVERR_TREE, DEVERR_QUERY = 16, 32, 64
 
 
 class PkvError(RuntimeError):
@@ -125,6 +125,11 @@ def load() -> ctypes.CDLL:
         lib.pkv_decode_tree_workspace_bytes.argtypes = [pdesc, i32, i32, i32, i32, popts]
         lib.pkv_decode_tree_describe.restype = ctypes.c_int
         lib.pkv_decode_tree_describe.argtypes = [pdesc, i32, i32, i32, i32, popts, ctypes.POINTER(DecodePlan)]
+        lib.pkv_paged_decode_packed.restype = ctypes.c_int
+        lib.pkv_paged_decode_packed.argtypes = [pdesc, P, i32, i32, i32, i32, P, P, P, P, P, i32, P, P, P, i32, i32, f32, P, P,
+                                                sz, popts, P]
+        lib.pkv_decode_packed_workspace_bytes.restype = sz
+        lib.pkv_decode_packed_workspace_bytes.argtypes = [pdesc, i32, i32, i32, i32, i32, popts]
         lib.pkv_tree_masks.restype = ctypes.c_int
         lib.pkv_tree_masks.argtypes = [P, P, P, i32, i32, P, P, P]
         lib.pkv_extend_tables.restype = ctypes.c_int
@@ -532,6 +537,56 @@ def _marshal_tree(q, k_cache, v_cache, block_tables, context_lens, tree_mask, no
     return load().pkv_paged_decode_tree, args, out, workspace
 
 
+def packed_workspace_bytes(k_cache: torch.Tensor, num_rows: int, batch: int, max_query_tokens: int, num_q_heads: int,
+                           max_blocks_per_seq: int, opts: Optional[DecodeOpts] = None) -> int:
+    """Workspace bytes of :func:`paged_decode_packed`."""
+    desc = cache_desc(k_cache)
+    lib = load()
+    n = lib.pkv_decode_packed_workspace_bytes(ctypes.byref(desc), int(num_rows), int(batch), int(max_query_tokens), int(num_q_heads),
+                                              int(max_blocks_per_seq), ctypes.byref(opts) if opts is not None else None)
+    if n == 0:
+        raise PkvError(1, f"bad arguments for the workspace: {lib.pkv_last_error_message().decode(errors='replace')}")
+    return int(n)
+
+
+def _marshal_packed(q, k_cache, v_cache, block_tables, context_lens, query_starts, max_query_tokens, kv_group_ptr, layer, scale,
+                    out, workspace, k_scale, v_scale, opts, stream=None):
+    """As _marshal_decode, for packed rows."""
+    desc = cache_desc(k_cache)
+    _need_here("q", q, torch.bfloat16)
+    if q.dim() != 3:
+        raise PkvError(1, "q must be [N][Hq][D]")
+    N, Hq, D = q.shape
+    if D != desc.head_dim:
+        raise PkvError(1, "q does not match the cache's head_dim")
+    _need_here("k_cache", k_cache, k_cache.dtype)
+    _need_here("v_cache", v_cache, k_cache.dtype, tuple(k_cache.shape))
+    _need_here("block_tables", block_tables, torch.int32)
+    if block_tables.dim() != 2:
+        raise PkvError(1, "block_tables must be [B][MB]")
+    B, MB = block_tables.shape
+    _need_here("context_lens", context_lens, torch.int32, (B,))
+    _need_here("query_starts", query_starts, torch.int32, (B + 1,))
+    if desc.dtype != KV_BF16:
+        _need_page_params(desc, k_scale, "k_scale")
+        _need_page_params(desc, v_scale, "v_scale")
+    most = max(1, N) if max_query_tokens is None else int(max_query_tokens)
+    with _allocating_on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            n = packed_workspace_bytes(k_cache, N, B, most, Hq, MB, opts)
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    _need_here("out", out, torch.bfloat16, (N, Hq, D))
+    _need_here("workspace", workspace, workspace.dtype)
+    gp = (ctypes.c_int32 * len(kv_group_ptr))(*[int(x) for x in kv_group_ptr])
+    args = (ctypes.byref(desc), _ptr(q), N, B, most, Hq, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(block_tables), MB, _ptr(context_lens), _ptr(query_starts), gp, len(kv_group_ptr), int(layer),
+            float(D ** -0.5 if scale is None else scale), _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+            ctypes.byref(opts) if opts is not None else None)
+    return load().pkv_paged_decode_packed, args, out, workspace
+
+
 def paged_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                  block_tables: torch.Tensor, context_lens: torch.Tensor,
                  kv_group_ptr: Sequence[int] = (0,), layer: int = 0,
@@ -603,10 +658,31 @@ def paged_decode_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     return out
 
 
+def paged_decode_packed(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        block_tables: torch.Tensor, context_lens: torch.Tensor, query_starts: torch.Tensor,
+                        max_query_tokens: Optional[int] = None, kv_group_ptr: Sequence[int] = (0,), layer: int = 0,
+                        scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None,
+                        k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                        opts: Optional[DecodeOpts] = None, stream=None) -> torch.Tensor:
+    """Attention of each sequence's new tokens, as many as it has: rows
+    query_starts[b] .. query_starts[b + 1] - 1 of q [N][Hq][D] (bf16) are the last
+    of the context_lens[b] cached tokens, causal among themselves (the rows that
+    :func:`extend_tables` lays out).  ``max_query_tokens``: the most rows of a
+    sequence (default N; a tight bound is faster where every sequence has few).
+    Rows outside every sequence are left as they were (undefined in a new
+    ``out``).  Returns out [N][Hq][D]."""
+    fn, args, out, _ = _marshal_packed(q, k_cache, v_cache, block_tables, context_lens, query_starts, max_query_tokens,
+                                       kv_group_ptr, layer, scale, out, workspace, k_scale, v_scale, opts, stream)
+    _check(fn(*args, _stream_handle(stream)))
+    return out
+
+
 class PreparedDecode:
     """A decode call (:func:`paged_decode`, :func:`paged_decode_multi`,
     :func:`append_and_decode` when ``k_new`` / ``v_new`` / ``slot_mapping``
-    are given, or :func:`paged_decode_tree` when ``tree_mask`` is) whose arguments were checked and marshalled once.  Each call
+    are given, :func:`paged_decode_tree` when ``tree_mask`` is, or :func:`paged_decode_packed` when ``query_starts`` is)
+    whose arguments were checked and marshalled once.  Each call
     of the object enqueues the same launch again, reading whatever the bound
     tensors hold at that time: the pattern of a serving loop whose step
     buffers stay in place (as under CUDA graph capture) and whose host cost
@@ -616,8 +692,17 @@ class PreparedDecode:
 
     def __init__(self, q, k_cache, v_cache, block_tables, context_lens, kv_group_ptr=(0,), layer=0,
                  scale=None, out=None, workspace=None, k_scale=None, v_scale=None, opts=None,
-                 k_new=None, v_new=None, slot_mapping=None, stream=None, tree_mask=None, node_counts=None):
-        if tree_mask is not None:
+                 k_new=None, v_new=None, slot_mapping=None, stream=None, tree_mask=None, node_counts=None,
+                 query_starts=None, max_query_tokens=None):
+        if max_query_tokens is not None and query_starts is None:
+            raise PkvError(1, "max_query_tokens without query_starts")
+        if query_starts is not None:
+            if tree_mask is not None or node_counts is not None or k_new is not None or v_new is not None or slot_mapping is not None:
+                raise PkvError(1, "a decode of packed rows neither appends nor takes a tree_mask")
+            fn, args, out, workspace = _marshal_packed(q, k_cache, v_cache, block_tables, context_lens, query_starts,
+                                                       max_query_tokens, kv_group_ptr, layer, scale, out, workspace,
+                                                       k_scale, v_scale, opts, stream)
+        elif tree_mask is not None:
             if k_new is not None or v_new is not None or slot_mapping is not None:
                 raise PkvError(1, "a drafted-tree decode does not append: call kv_append before it")
             fn, args, out, workspace = _marshal_tree(q, k_cache, v_cache, block_tables, context_lens, tree_mask,
@@ -631,7 +716,7 @@ class PreparedDecode:
                                                        v_scale, opts, k_new, v_new, slot_mapping)
         self._fn, self._args = fn, args
         self._keep = (q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, opts, k_new,
-                      v_new, slot_mapping, tree_mask, node_counts)
+                      v_new, slot_mapping, tree_mask, node_counts, query_starts)
         self.out, self.workspace = out, workspace
         self._stream = None if stream is None else _stream_handle(stream)
         self._device = q.get_device()

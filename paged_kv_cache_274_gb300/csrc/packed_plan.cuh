@@ -1,0 +1,129 @@
+// Work shares of the tcgen05 attention of packed rows: what its planner writes
+// and its attention and merge kernels read (without CUDA, so that the host can
+// check that the three agree).
+//
+// Sequence b has m rows, the last of its ctx cached tokens; row t sees the
+// positions up to ctx - m + t.  An item is a run of `span` rows (the row tiles
+// of a CTA) on one KV head; it takes the steps of the positions that its last
+// row sees.  The items of all sequences in a row (sequence, KV head, rows) are
+// cut into shares of equal cost, as the drafted trees' are (tree_plan.cuh); a
+// split item's parts have the same places.
+#pragma once
+
+#include "tree_plan.cuh"
+
+namespace pkv {
+
+// A sequence's validated numbers.
+struct PackedSeq {
+  int ctx;    // cached tokens (0: none; its rows are zeros)
+  int start;  // its first row
+  int m;      // its rows (0: none to attend with)
+  int unused;
+};
+
+// Start of a share.
+struct PackedBound {
+  int b, kvh, run;  // item (b = batch, kvh = run = 0: the end)
+  int step;         // step of the item (0: the share starts with the item)
+};
+
+PKV_PLAN_FN int packed_runs(const PackedSeq& s, int span) { return (s.m + span - 1) / span; }
+
+// Positions that the last row of a run sees (0: none of its rows sees any).
+PKV_PLAN_FN int packed_seen(const PackedSeq& s, int run, int span) {
+  const int rows = s.m - run * span < span ? s.m : (run + 1) * span;  // up to the run's end
+  const int n = s.ctx - s.m + rows;
+  return n > 0 ? n : 0;
+}
+
+PKV_PLAN_FN int packed_steps(int seen) { return (seen + kTreeTokens - 1) / kTreeTokens; }
+
+// First run with a position to see (of a sequence with ctx > 0): with more rows
+// than cached tokens, the first rows see none.
+PKV_PLAN_FN int packed_first(const PackedSeq& s, int span) { return s.ctx >= s.m ? 0 : (s.m - s.ctx) / span; }
+
+// Cost in tokens: what an item's last row sees, half a step of rounding, and
+// item_steps for its start and output.
+PKV_PLAN_FN long long packed_item_cost(int item_steps) { return kTreeTokens * static_cast<long long>(item_steps) + kTreeTokens / 2; }
+
+// Of the first x items of a KV head, as if the last run were full.
+PKV_PLAN_FN long long packed_before(const PackedSeq& s, long long x, int span, long long item_cost) {
+  const long long one = static_cast<long long>(s.ctx) - s.m + static_cast<long long>(packed_first(s, span) + 1) * span + item_cost;
+  return x * one + span * (x * (x - 1) / 2);
+}
+
+// Of a KV head of a sequence.
+PKV_PLAN_FN long long packed_cost(const PackedSeq& s, int span, long long item_cost) {
+  if (s.ctx == 0 || s.m == 0) return 0;
+  const int runs = packed_runs(s, span);
+  return packed_before(s, runs - packed_first(s, span), span, item_cost) - (static_cast<long long>(runs) * span - s.m);
+}
+
+// Shares of at least min_steps steps (never less than one: two boundaries in
+// one step would leave a share inside an item without steps).
+PKV_PLAN_FN int packed_share_count(long long total, int min_steps, int max_shares) {
+  const long long n = total / (static_cast<long long>(min_steps) * kTreeTokens);
+  return total == 0 ? 0 : n < 1 ? 1 : static_cast<int>(n < max_shares ? n : max_shares);
+}
+
+// Start of share s (s == shares: the end).  start: the prefix sums of the
+// sequences' costs (all KV heads).  A boundary within `near` steps of an item's
+// start or end moves there.
+PKV_PLAN_FN PackedBound packed_bound(int s, int shares, long long total, const long long* start, const PackedSeq* seqs, int B, int Hkv,
+                                     int span, int item_steps) {
+  PackedBound r{B, 0, 0, 0};
+  if (s >= shares) return r;
+  const long long apart = total / shares / (4 * kTreeTokens), item_cost = packed_item_cost(item_steps);
+  const int near = apart < 2 ? static_cast<int>(apart) : 2;
+  // (total * s may pass 64 bits)
+  const long long pos = total / shares * s + total % shares * s / shares;
+  r.b = tree_find(start, B, pos);
+  const PackedSeq q = seqs[r.b];
+  const long long cost = (start[r.b + 1] - start[r.b]) / Hkv, in = pos - start[r.b];
+  r.kvh = static_cast<int>(in / cost);
+  const long long rest = in - r.kvh * cost;
+  const int first = packed_first(q, span), runs = packed_runs(q, span);
+  int lo = 0, hi = runs - first - 1;  // the last item that starts at or before `rest`
+#pragma unroll 1
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (packed_before(q, mid, span, item_cost) <= rest) lo = mid; else hi = mid - 1;
+  }
+  r.run = first + lo;
+  const long long off = rest - packed_before(q, lo, span, item_cost) - item_cost;
+  const int step = off <= 0 ? 0 : static_cast<int>(off / kTreeTokens);
+  if (step <= near) return r;
+  if (packed_steps(packed_seen(q, r.run, span)) - step > near) {
+    r.step = step;
+  } else if (++r.run == runs) {
+    r.run = first;
+    if (++r.kvh == Hkv) {
+      r.kvh = 0;
+      const long long next = start[r.b + 1];
+      r.b = next < total ? tree_find(start, B, next) : B;
+      r.run = r.b < B ? packed_first(seqs[r.b], span) : 0;
+    }
+  }
+  return r;
+}
+
+PKV_PLAN_FN bool packed_same_item(const PackedBound& x, const PackedBound& y) { return x.b == y.b && x.kvh == y.kvh && x.run == y.run; }
+
+// Whether the place (b, kvh, run, step) lies before `end`.
+PKV_PLAN_FN bool packed_is_before(int b, int kvh, int run, int step, const PackedBound& end) {
+  if (b != end.b) return b < end.b;
+  if (kvh != end.kvh) return kvh < end.kvh;
+  if (run != end.run) return run < end.run;
+  return step < end.step;
+}
+
+// As tree_splits, tree_split_place and tree_item_ends.
+PKV_PLAN_FN bool packed_splits(const PackedBound& mine, const PackedBound& next, int share, int shares) {
+  if (share + 1 >= shares || next.step == 0) return false;
+  return !(packed_same_item(mine, next) && mine.step > 0);
+}
+PKV_PLAN_FN int packed_split_place(const PackedBound& mine, const PackedBound& next) { return packed_same_item(mine, next) ? 0 : 1; }
+PKV_PLAN_FN bool packed_item_ends(const PackedBound& at, const PackedBound& e) { return !packed_same_item(at, e) || e.step == 0; }
+
+}  // namespace pkv

@@ -711,6 +711,56 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
   return PKV_OK;
 }
 
+// Likewise for packed rows: N rows of `batch` sequences, at most T of each.
+static pkv_status resolve_packed(const pkv_cache_desc* c, int32_t N, int32_t batch, int32_t T, int32_t Hq, int32_t MB,
+                                 const pkv_decode_opts* opts, pkv::DecodeLaunch* L) {
+  pkv_status st = check_cache_desc(c);
+  if (st != PKV_OK) return st;
+  if (batch < 0 || N < 0) return fail(PKV_ERR_INVALID_ARG, "batch %d, num_rows %d < 0", batch, N);
+  if (T < 1) return fail(PKV_ERR_INVALID_ARG, "max_query_tokens %d < 1", T);
+  if (MB < 1) return fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq %d < 1", MB);
+  if (Hq < 1 || Hq % c->num_kv_heads != 0)
+    return fail(PKV_ERR_INVALID_ARG, "num_q_heads %d is not a multiple of num_kv_heads %d", Hq, c->num_kv_heads);
+  if (static_cast<long long>(MB) * c->block_size >= (1LL << 31) - 256 || static_cast<long long>(batch) * MB >= (1LL << 40))
+    return fail(PKV_ERR_UNSUPPORTED, "max_blocks_per_seq too large");
+  const int G = Hq / c->num_kv_heads;
+  if (G > 128) return fail(PKV_ERR_UNSUPPORTED, "G = %d query heads per KV head (packed rows support <= 128)", G);
+  pkv_decode_opts o{};
+  if (opts) o = *opts;
+  if (o.math != PKV_MATH_AUTO && o.math != PKV_MATH_TC)
+    return fail(PKV_ERR_UNSUPPORTED, "math %d (packed rows have the tcgen05 back-end only)", o.math);
+  if (o.partition_blocks < 0 || o.partition_blocks > pkv::kTcUnitMaxPages)
+    return fail(PKV_ERR_INVALID_ARG, "partition_blocks %d outside 1..%d", o.partition_blocks, pkv::kTcUnitMaxPages);
+  if (static_cast<long long>(N) * Hq * c->head_dim >= (1LL << 31) || static_cast<long long>(N) * c->num_kv_heads >= (1LL << 31) || batch >= (1 << 24))
+    return fail(PKV_ERR_UNSUPPORTED, "rows x heads x head_dim or batch too large");
+  *L = pkv::DecodeLaunch{};
+  L->packed = 1;
+  L->N = N;
+  L->B = batch;
+  L->Hq = Hq;
+  L->Hkv = c->num_kv_heads;
+  L->G = G;
+  L->T = std::min(T, std::max(N, 1));
+  // tiles of 128 (row, head) rows; a pair of them per CTA where a sequence may
+  // have more than one
+  L->Tt = std::max(1, std::min(L->T, 128 / G));
+  L->NT = L->T > L->Tt ? 2 : 1;
+  L->MB = MB;
+  L->NB = c->num_blocks;
+  L->bs = c->block_size;
+  L->D = c->head_dim;
+  L->kv_fp8 = c->dtype != PKV_KV_BF16;
+  L->kv_dtype = c->dtype;
+  L->math = PKV_MATH_TC;
+  L->tree_shares = 152;
+  L->tree_min_steps = std::max(1, o.partition_blocks * c->block_size / 128);
+  return PKV_OK;
+}
+
+static size_t packed_total(const pkv::DecodeLaunch& L) {
+  return pkv::packed_workspace(L.B, L.N, L.Hkv, L.D, L.NT, L.tree_shares).total;
+}
+
 static size_t workspace_total(const pkv::DecodeLaunch& L) {
   if (L.tree_tc) return pkv::tree_workspace(L.B, L.Hkv, L.D, L.NT, L.tree_words, L.tree_shares).total;
   return pkv::workspace_layout(L.B, L.T, L.Hq, L.Hkv, L.NT, L.D, L.pmax, L.tree_words).total;
@@ -742,6 +792,14 @@ size_t pkv_decode_tree_workspace_bytes(const pkv_cache_desc* cache, int32_t batc
                                        int32_t num_query_tokens, int32_t num_q_heads,
                                        int32_t max_blocks_per_seq, const pkv_decode_opts* opts) {
   return workspace_bytes_of(cache, batch, num_query_tokens, num_q_heads, max_blocks_per_seq, opts, true);
+}
+
+size_t pkv_decode_packed_workspace_bytes(const pkv_cache_desc* cache, int32_t num_rows, int32_t batch,
+                                         int32_t max_query_tokens, int32_t num_q_heads,
+                                         int32_t max_blocks_per_seq, const pkv_decode_opts* opts) {
+  pkv::DecodeLaunch L;
+  if (resolve_packed(cache, num_rows, batch, max_query_tokens, num_q_heads, max_blocks_per_seq, opts, &L) != PKV_OK) return 0;
+  return packed_total(L);
 }
 
 size_t pkv_decode_workspace_bytes(const pkv_cache_desc* cache, int32_t batch, int32_t num_q_heads,
@@ -997,6 +1055,91 @@ pkv_status pkv_paged_decode_tree(const pkv_cache_desc* cache, const void* q, int
   return decode_call(cache, q, batch, num_query_tokens, num_q_heads, k_cache, v_cache, k_scale, v_scale,
                      block_tables, max_blocks_per_seq, context_lens, kv_group_ptr, num_layers, layer, scale,
                      out, workspace, workspace_bytes, opts, stream, nullptr, &tree);
+}
+
+pkv_status pkv_paged_decode_packed(const pkv_cache_desc* cache, const void* q, int32_t num_rows, int32_t batch,
+                                   int32_t max_query_tokens, int32_t num_q_heads, const void* k_cache,
+                                   const void* v_cache, const float* k_scale, const float* v_scale,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* context_lens, const int32_t* query_starts,
+                                   const int32_t* kv_group_ptr, int32_t num_layers, int32_t layer, float scale,
+                                   void* out, void* workspace, size_t workspace_bytes,
+                                   const pkv_decode_opts* opts, void* stream) {
+  pkv::DecodeLaunch L;
+  pkv_status st = resolve_packed(cache, num_rows, batch, max_query_tokens, num_q_heads, max_blocks_per_seq, opts, &L);
+  if (st != PKV_OK) return st;
+  if (kv_group_ptr == nullptr || num_layers < 1 || layer < 0 || layer >= num_layers)
+    return fail(PKV_ERR_INVALID_ARG, "layer %d / num_layers %d / kv_group_ptr", layer, num_layers);
+  const int32_t slot = kv_group_ptr[layer];
+  if (slot < 0 || slot >= cache->num_slots)
+    return fail(PKV_ERR_INVALID_ARG, "kv_group_ptr[%d] = %d outside [0, %d)", layer, slot, cache->num_slots);
+  if (!std::isfinite(scale)) return fail(PKV_ERR_INVALID_ARG, "scale is not finite");
+  if (batch == 0 || num_rows == 0) return PKV_OK;
+  const bool fp8 = cache->dtype != PKV_KV_BF16;  // one-byte elements (E4M3 or INT8)
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !query_starts || !out)
+    return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (fp8 && (!k_scale || !v_scale)) return fail(PKV_ERR_INVALID_ARG, "E4M3 and INT8 caches need k_scale and v_scale");
+  if (fp8 && !scales_aligned(cache->dtype, k_scale, v_scale))
+    return fail(PKV_ERR_ALIGNMENT, "k_scale and v_scale must be 4-byte (E4M3) or 8-byte (INT8) aligned");
+  if (!aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(workspace))
+    return fail(PKV_ERR_ALIGNMENT, "q, out, caches and workspace must be 16-byte aligned");
+  if (!aligned4({block_tables, context_lens, query_starts}))
+    return fail(PKV_ERR_ALIGNMENT, "block_tables, context_lens and query_starts must be 4-byte aligned");
+  const size_t row = static_cast<size_t>(num_q_heads) * cache->head_dim * 2, lens = static_cast<size_t>(batch) * 4;
+  const size_t slot_rows = static_cast<size_t>(cache->num_blocks) * cache->num_kv_heads;  // pages of a slot
+  const size_t pool = cache->num_slots * slot_rows * cache->block_size * cache->head_dim * (fp8 ? 1 : 2);
+  if (!disjoint({{out, num_rows * row}}, {{q, num_rows * row}, {block_tables, lens * max_blocks_per_seq}, {context_lens, lens},
+                                          {query_starts, lens + 4}, {k_cache, pool}, {v_cache, pool}}))
+    return fail(PKV_ERR_INVALID_ARG, "out overlaps another array");
+  const size_t need = packed_total(L);
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(PKV_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace_bytes);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != PKV_OK) return st;
+  if (env_flag("PKV_VALIDATE")) {
+    std::vector<int32_t> ctx, starts, bt;
+    if ((st = fetch(ctx, context_lens, static_cast<size_t>(batch), s)) != PKV_OK) return st;
+    if ((st = fetch(starts, query_starts, static_cast<size_t>(batch) + 1, s)) != PKV_OK) return st;
+    if ((st = fetch(bt, block_tables, static_cast<size_t>(batch) * max_blocks_per_seq, s)) != PKV_OK) return st;
+    for (int b = 0; b < batch; ++b) {
+      if (starts[b] < 0 || starts[b + 1] < starts[b] || starts[b + 1] > num_rows || starts[b + 1] - starts[b] > L.T)
+        return fail(PKV_ERR_INVALID_ARG, "query_starts[%d], [%d] = %d, %d", b, b + 1, starts[b], starts[b + 1]);
+      if (ctx[b] < 0 || static_cast<long long>(ctx[b]) > static_cast<long long>(max_blocks_per_seq) * cache->block_size)
+        return fail(PKV_ERR_INVALID_ARG, "context_lens[%d] = %d out of range", b, ctx[b]);
+      if (starts[b + 1] == starts[b]) continue;
+      for (int j = 0; j < (ctx[b] + cache->block_size - 1) / cache->block_size; ++j) {
+        const int32_t blk = bt[static_cast<size_t>(b) * max_blocks_per_seq + j];
+        if (blk < 0 || blk >= cache->num_blocks)
+          return fail(PKV_ERR_INVALID_ARG, "block_tables[%d][%d] = %d outside [0, %d)", b, j, blk, cache->num_blocks);
+      }
+    }
+  }
+  if ((st = encode_cache_map(&L.kmap, k_cache, cache)) != PKV_OK) return st;
+  if ((st = encode_cache_map(&L.vmap, v_cache, cache)) != PKV_OK) return st;
+  if (!fp8 && (st = encode_query_map(&L.qmap, q, 1, num_rows, L.Hq, L.D, L.G, L.Tt)) != PKV_OK) return st;
+  L.q = q;
+  L.out = out;
+  L.block_tables = block_tables;
+  L.context_lens = context_lens;
+  L.query_starts = query_starts;
+  const size_t scale_off = slot * slot_rows * (cache->dtype == PKV_KV_INT8 ? 2 : 1);
+  L.k_scale = fp8 ? k_scale + scale_off : nullptr;
+  L.v_scale = fp8 ? v_scale + scale_off : nullptr;
+  L.v_cache = static_cast<const uint8_t*>(v_cache) + slot * slot_rows * cache->block_size * cache->head_dim * (fp8 ? 1 : 2);
+  L.err = dev.err_word;
+  L.row_base = static_cast<int>(static_cast<long long>(slot) * slot_rows * cache->block_size);
+  L.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  L.stream = s;
+  L.num_sms = dev.num_sms;
+  if (opts != nullptr) {
+    L.ev_start = static_cast<cudaEvent_t>(opts->event_decode_start);
+    L.ev_end = static_cast<cudaEvent_t>(opts->event_decode_end);
+  }
+  int launched = 0;
+  cudaError_t e = pkv::launch_packed_attend(L, static_cast<uint8_t*>(workspace), &launched);
+  if (e != cudaSuccess) return cuda_fail(e, "paged_decode_packed launch");
+  return PKV_OK;
 }
 
 pkv_status pkv_tree_masks(const int32_t* parents, const int32_t* context_lens, const int32_t* node_counts,

@@ -80,6 +80,10 @@ struct DecodeLaunch {
   int tree_tc;                  // 1: the tcgen05 drafted-tree kernels (launch_tree_attend)
   int tree_shares;              // most work shares (CTAs per pair of row tiles)
   int tree_min_steps;           // fewest 128-token steps of a share
+  // packed rows (pkv_paged_decode_packed): rows query_starts[b] .. [b + 1] - 1
+  // are sequence b's, at most T of them; N rows in all
+  int packed, N;
+  const int32_t* query_starts;
   const AppendArgs* append;  // optional: append run by the planner launch (the decode sees it)
   int append_kind;           // pkv_kv_dtype of that append
 };
@@ -153,6 +157,17 @@ struct TreeWorkspace {
 TreeWorkspace tree_workspace(int B, int Hkv, int D, int NT, int tree_words, int max_shares);
 size_t tree_attend_smem_bytes(int kv_dtype, int D, int pair);
 cudaError_t launch_tree_attend(const DecodeLaunch& L, uint8_t* workspace, int* launched_kernels);
+
+// Raises a kernel's dynamic shared memory limit, once per (device, context,
+// kernel), and checks the registers that it is launched with.
+cudaError_t allow_smem(const void* fn, size_t smem, int regs);
+
+// The tcgen05 attention of packed rows, likewise.
+struct PackedWorkspace {
+  size_t shares, seqs, start, bounds, poison, part_ml, part_o, total;
+};
+PackedWorkspace packed_workspace(int B, int N, int Hkv, int D, int tiles, int max_shares);
+cudaError_t launch_packed_attend(const DecodeLaunch& L, uint8_t* workspace, int* launched_kernels);
 
 // Node masks and positions of drafted trees.
 struct TreeMaskArgs {

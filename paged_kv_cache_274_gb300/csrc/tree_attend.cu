@@ -1,4 +1,4 @@
-// Planner, merge and launch of the tcgen05 drafted-tree attention
+// Planner and launch of the tcgen05 drafted-tree attention
 // (tree_attend.cuh), and its kernel instances.
 #include <algorithm>
 #include <mutex>
@@ -6,6 +6,7 @@
 #include <vector>
 
 #include "tree_attend.cuh"
+#include "tree_merge.cuh"
 #include "tree_scan.cuh"
 
 namespace pkv {
@@ -131,139 +132,12 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const TreeP
 }
 
 // ---------------------------------------------------------------------------
-// merge: out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p over the partials
-// of an item that shares split.  The share in which the item starts leaves it
-// as its last unit; the shares after it continue it with their first unit
-// until one ends it.
-//
-// One CTA per (share, row tiles of a CTA, 16 rows), a warp per two rows.  The
-// partials are in L2 and few, so it is a chain of loads: bounds, a lane each,
-// then m and l of up to 16 parts of both rows by one load of the warp, next to
-// the rows of the first four parts.  (A warp per row in turn, with the loads
-// after the maxima, took 5 us longer for 151 split items of 128 rows.)
-// ---------------------------------------------------------------------------
-constexpr int kTreeMergeThreads = 256;
-constexpr int kTreeMergeRows = 2;                                        // of a warp
-constexpr int kTreeMergeCta = kTreeMergeThreads / 32 * kTreeMergeRows;   // of a CTA
-
-struct TreeMergeArgs {
-  const TreeBound* bounds;
-  const int32_t* shares;
-  const float2* part_ml;
-  const float* part_o;
-  __nv_bfloat16* out;
-  int Hq, G, T, Tt, NP, tiles /* per CTA */;
-};
-
-template <int D>
-__global__ void __launch_bounds__(kTreeMergeThreads, 3) tree_merge_kernel(const TreeMergeArgs a) {
-  constexpr int kPer = D / 32, kRows = kTreeMergeRows, kLanes = 32 / kRows, kBatch = 4;
-  pdl_trigger();
-  pdl_wait();
-  const int rows = a.tiles * kTaRows, slices = rows / kTreeMergeCta;
-  const int slice = blockIdx.x % slices;
-  const int cta = blockIdx.x / slices;
-  const int share = cta / a.NP, pair = cta - share * a.NP;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // (the grid leaves out the last share that the workspace has room for)
-  const int shares = *a.shares;
-  const TreeBound mine = a.bounds[share], next = a.bounds[share + 1];
-  if (!tree_splits(mine, next, share, shares)) return;
-  int last = share + 1;  // the share that ends the item
-#pragma unroll 1
-  for (;;) {
-    const int s = last + 1 + lane;
-    bool ends = true;
-    if (s < shares) ends = tree_item_ends(next, a.bounds[s]);
-    const unsigned found = __ballot_sync(kFull, ends);
-    last += found ? __ffs(found) - 1 : 32;
-    if (found) break;
-  }
-  const int parts = last - share + 1;
-  const size_t first = (static_cast<size_t>(cta) * 2 + tree_split_place(mine, next)) * rows;
-  const size_t stride = static_cast<size_t>(a.NP) * 2 * rows;  // from a share's partials to the next one's
-  const size_t cont = (static_cast<size_t>(cta) * 2) * rows;
-  const int rr0 = slice * kTreeMergeCta + warp * kRows;
-  const int tile = (a.tiles == 2 ? 2 * pair : 0) + rr0 / kTaRows;
-  unsigned live = 0;  // rows with a node
-#pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    const int tl = (rr0 + k) % kTaRows / a.G;
-    if (tl < a.Tt && tile * a.Tt + tl < a.T) live |= 1u << k;
-  }
-  if (live == 0) return;
-  auto at = [&](int k, int p) { return (p == 0 ? first : cont + stride * p) + rr0 + k; };
-  using Vec = std::conditional_t<kPer == 4, float4, float2>;
-  auto load = [&](int k, int p) -> Vec {
-    Vec v{};
-    if (p < parts && ((live >> k) & 1u)) v = *reinterpret_cast<const Vec*>(a.part_o + at(k, p) * D + lane * kPer);
-    return v;
-  };
-  Vec v[kBatch][kRows];  // parts at a time
-#pragma unroll
-  for (int q = 0; q < kBatch; ++q)
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) v[q][k] = load(k, q);
-  const int mk = lane / kLanes, mp = lane % kLanes;  // this lane's row and part
-  auto load_ml = [&](int p) { return p < parts && ((live >> mk) & 1u) ? a.part_ml[at(mk, p)] : make_float2(-INFINITY, 0.f); };
-  float2 ml = load_ml(mp);
-  float M = ml.x;
-#pragma unroll 1
-  for (int p = mp + kLanes; p < parts; p += kLanes) M = fmaxf(M, load_ml(p).x);
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-  float acc[kRows][kPer], sum = 0.f;
-#pragma unroll
-  for (int k = 0; k < kRows; ++k)
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) acc[k][j] = 0.f;
-#pragma unroll 1
-  for (int p0 = 0; p0 < parts; p0 += kLanes) {
-    if (p0 > 0) ml = load_ml(p0 + mp);
-    // (an empty partial has O = 0, or the row's fixed value)
-    const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-    sum = fmaf(w, ml.y, sum);
-    const int pn = min(kLanes, parts - p0);
-#pragma unroll 1
-    for (int pp = 0; pp < pn; pp += kBatch) {
-#pragma unroll
-      for (int q = 0; q < kBatch; ++q)
-#pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-          const float wq = __shfl_sync(kFull, w, kLanes * k + pp + q);  // (0 past the last part, and its row zeros)
-          const float* x = reinterpret_cast<const float*>(&v[q][k]);
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) acc[k][j] = fmaf(wq, x[j], acc[k][j]);
-          v[q][k] = load(k, p0 + pp + kBatch + q);
-        }
-    }
-  }
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  const float inv_mine = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    const float inv = __shfl_sync(kFull, inv_mine, kLanes * k);
-    if (!((live >> k) & 1u)) continue;
-    const int r = (rr0 + k) % kTaRows, tl = r / a.G;
-    __nv_bfloat16* o = a.out + (static_cast<size_t>(next.b * a.T + tile * a.Tt + tl) * a.Hq + next.kvh * a.G + (r - tl * a.G)) * D + lane * kPer;
-    uint32_t w[kPer / 2];
-#pragma unroll
-    for (int j = 0; j < kPer; j += 2) w[j / 2] = pack_bf16x2(acc[k][j] * inv, acc[k][j + 1] * inv);
-    if constexpr (kPer == 4)
-      *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
-    else
-      *reinterpret_cast<uint32_t*>(o) = w[0];
-  }
-}
-
-// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 template <int D, int KV, bool PAIR>
 static const void* attend_instance(int bs) {
-  return bs == 16 ? reinterpret_cast<const void*>(&tree_attend_kernel<D, 16, KV, PAIR>)
-                  : reinterpret_cast<const void*>(&tree_attend_kernel<D, 32, KV, PAIR>);
+  return bs == 16 ? reinterpret_cast<const void*>(&tree_attend_kernel<D, 16, KV, PAIR, false>)
+                  : reinterpret_cast<const void*>(&tree_attend_kernel<D, 32, KV, PAIR, false>);
 }
 
 struct TreeKernel {
@@ -312,7 +186,7 @@ TreeWorkspace tree_workspace(int B, int Hkv, int D, int NT, int tree_words, int 
 // Raises a kernel's dynamic shared memory limit, once per (device, context,
 // kernel); checks that it is launched with the registers that its warps share
 // out (a warp that waits for more than there are would wait forever).
-static cudaError_t allow_smem(const void* fn, size_t smem, int regs) {
+cudaError_t allow_smem(const void* fn, size_t smem, int regs) {
   struct Entry {
     int dev;
     void* ctx;
@@ -413,12 +287,12 @@ cudaError_t launch_tree_attend(const DecodeLaunch& L, uint8_t* ws, int* launched
 
   // 3. merge of the items that shares split
   if (L.tree_shares > 1) {
-    const TreeMergeArgs ma{bounds, shares, p.part_ml, p.part_o, p.out, L.Hq, L.G, L.T, L.Tt, NP, pair ? 2 : 1};
+    const TreeMergeArgs ma{bounds, nullptr, nullptr, shares, p.part_ml, p.part_o, p.out, L.Hq, L.G, L.T, L.Tt, NP, pair ? 2 : 1};
     cfg.gridDim = dim3(static_cast<unsigned>((L.tree_shares - 1) * NP * (ma.tiles * kTaRows / kTreeMergeCta)));
     cfg.blockDim = dim3(kTreeMergeThreads);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = (L.ev_end == nullptr) ? 1 : 0;
-    e = L.D == 64 ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<64>, ma) : cudaLaunchKernelEx(&cfg, tree_merge_kernel<128>, ma);
+    e = L.D == 64 ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<64, false>, ma) : cudaLaunchKernelEx(&cfg, tree_merge_kernel<128, false>, ma);
     if (e != cudaSuccess) return e;
     *launched += 1;
   }

@@ -63,8 +63,10 @@
 #pragma once
 
 #include <cstddef>
+#include <type_traits>
 
 #include "paged_decode_tc2.cuh"
+#include "packed_plan.cuh"
 #include "tree_plan.cuh"
 
 namespace pkv {
@@ -88,6 +90,9 @@ struct TaParams {
   TreeArgs tree;
   int Hq, Hkv, G, T, Tt, NT, NP, MB, NB, row_base;
   float scale_log2;
+  // packed rows
+  const PackedSeq* seqs;        // [B]
+  const PackedBound* pbounds;   // [shares + 1]
 };
 
 // Step flags; a step without any is every row's in whole, with scores whose
@@ -107,6 +112,9 @@ struct TaStep {
   uint8_t bad[8];   // page id out of range
   int flags;        // kStepMasked, kStepScales
   float vref;       // one-byte caches: P carries v scale / vref
+  // packed rows: the item's first row and its rows, the positions that its
+  // first row sees, the sequence's tokens before its rows
+  int row0, rows, seen0, base;
   // one-byte caches, per page: k scale, INT8 K bias 1152 + zero, v scale /
   // vref and its log2
   float4 par[8];
@@ -261,10 +269,12 @@ __device__ __forceinline__ void widen_rows(uint8_t* stage, uint32_t region, int 
   }
 }
 
-template <int D, int BS, int KV, bool PAIR>
+// PACKED: the rows of a sequence are consecutive rows of q and out, causal among
+// themselves (packed_plan.cuh), instead of a tree's nodes.
+template <int D, int BS, int KV, bool PAIR, bool PACKED>
 __global__ void __launch_bounds__(ta_threads(KV), 1)
     tree_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                       const __grid_constant__ CUtensorMap qmap,  // bf16: q [B][T][Hq][D], box 64 x G x Tt
+                       const __grid_constant__ CUtensorMap qmap,  // bf16: q [B][T][Hq][D], box 64 x G x Tt (packed: [1][N])
                        const TaParams p) {
   using L = TaLayout<D, KV, PAIR>;
   constexpr bool kOneByte = L::kOneByte, kF8K = L::kF8K, kI8 = KV == PKV_KV_INT8;
@@ -354,41 +364,83 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
   if (warp == 17) {
     // K copy warp: the share's units, a descriptor and the K pages per step
     uint32_t g = 0;
-    TreeBound at{0, 0, 0, 0}, end{0, 0, 0, 0};
+    using Bound = std::conditional_t<PACKED, PackedBound, TreeBound>;
+    Bound at{0, 0, 0, 0}, end{0, 0, 0, 0};
     {  // (loaded side by side: every share has its place)
       const int shares = __ldg(p.shares);
-      const TreeBound b0 = p.bounds[share], b1 = p.bounds[share + 1];
+      Bound b0, b1;
+      if constexpr (PACKED) {
+        b0 = p.pbounds[share];
+        b1 = p.pbounds[share + 1];
+      } else {
+        b0 = p.bounds[share];
+        b1 = p.bounds[share + 1];
+      }
       if (share < shares) {
         at = b0;
         end = b1;
       }
     }
     int b = at.b, kvh = at.kvh, j0 = at.step;
+    [[maybe_unused]] int run = 0;
+    if constexpr (PACKED) run = at.run;
+    auto more = [&]() {
+      if constexpr (PACKED)
+        return packed_is_before(b, kvh, run, j0, end);
+      else
+        return b < end.b || (b == end.b && (kvh < end.kvh || (kvh == end.kvh && j0 < end.step)));
+    };
     const uint64_t policy = p.NP > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
     bool first_unit = true;
     float vref = 0.f;
-    while (!timed_out && (b < end.b || (b == end.b && (kvh < end.kvh || (kvh == end.kvh && j0 < end.step))))) {
-      const int ctx = b == at.b ? at.ctx : __ldg(p.ctx_eff + b);
+    while (!timed_out && more()) {
+      // the item's tokens: the sequence's, packed: those that its last row sees
+      int ctx;
+      bool last_item = b == end.b && kvh == end.kvh;
+      [[maybe_unused]] PackedSeq seq{0, 0, 0, 0};
+      if constexpr (PACKED) {
+        constexpr int kTiles = PAIR ? 2 : 1;
+        const int4 w = __ldg(reinterpret_cast<const int4*>(p.seqs) + b);
+        seq = PackedSeq{w.x, w.y, w.z, 0};
+        if (seq.ctx > 0 && seq.m > 0) run = max(run, packed_first(seq, kTiles * p.Tt));
+        if (!more()) break;  // (the share ends with runs that see nothing)
+        last_item = last_item && run == end.run;
+        ctx = seq.ctx > 0 && seq.m > 0 ? packed_seen(seq, run, kTiles * p.Tt) : 0;
+      } else {
+        ctx = b == at.b ? at.ctx : __ldg(p.ctx_eff + b);
+      }
       const int nt = (ctx + kTreeTokens - 1) / kTreeTokens;
       if (nt == 0) {  // an inactive sequence
         ++b;
+        run = 0;
         continue;
       }
-      const int n = (b == end.b && kvh == end.kvh ? end.step : nt) - j0;
+      const int n = (last_item ? end.step : nt) - j0;
       const int t0 = j0 * kTreeTokens, t1 = min(ctx, (j0 + n) * kTreeTokens);
       const int part = tree_unit_part(j0, n, nt, first_unit);
       first_unit = false;
       vref = 0.f;  // of the unit; 0: no page with a scale yet
       const int npages = (t1 - t0 + BS - 1) / BS;
-      const int base = ctx - (p.tree.node_counts != nullptr ? __ldg(p.tree.node_counts + b) : p.T);
+      // packed: the item's rows, and the positions that its first row sees
+      [[maybe_unused]] int row0 = 0, rows = 0;
+      int base;  // tokens that every row attends to
+      if constexpr (PACKED) {
+        constexpr int kTiles = PAIR ? 2 : 1;
+        const int t_first = run * kTiles * p.Tt;
+        row0 = seq.start + t_first;
+        rows = min(kTiles * p.Tt, seq.m - t_first);
+        base = seq.ctx - seq.m + t_first + 1;
+      } else {
+        base = ctx - (p.tree.node_counts != nullptr ? __ldg(p.tree.node_counts + b) : p.T);
+      }
       const int* trow = p.block_tables + static_cast<size_t>(b) * p.MB + t0 / BS;
       if constexpr (kOneByte) {  // the unit's queries, which the converters read once the unit before is done
         const int lines = 2 * p.G;
 #pragma unroll 1
         for (int x = lane; x < L::kQTiles * p.Tt * lines; x += 32) {
           const int t = 2 * pair * p.Tt + x / lines;
-          if (t < p.T)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (static_cast<size_t>(b * p.T + t) * p.Hq + kvh * p.G) * D + x % lines * 64));
+          if (t < (PACKED ? rows : p.T))
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (static_cast<size_t>(PACKED ? row0 + t : b * p.T + t) * p.Hq + kvh * p.G) * D + x % lines * 64));
         }
       }
       // lane i holds page i of a run of 32 pages, and of the next run (its id:
@@ -489,6 +541,12 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             st->ctx = ctx;
             st->flags = flags;
             st->vref = vref;
+            if constexpr (PACKED) {
+              st->row0 = row0;
+              st->rows = rows;
+              st->seen0 = base;
+              st->base = seq.ctx - seq.m;
+            }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&step_full[g % kTaRing]);  // release: the descriptor
@@ -504,6 +562,11 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         }
       }
       j0 = 0;
+      if constexpr (PACKED) {
+        constexpr int kTiles = PAIR ? 2 : 1;
+        if (++run < packed_runs(seq, kTiles * p.Tt)) continue;
+        run = 0;
+      }
       if (++kvh == p.Hkv) {
         kvh = 0;
         ++b;
@@ -562,13 +625,14 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           break;
         }
         const volatile TaStep* st = step_at(g0);
-        const int n = st->n, b = st->b, kvh = st->kvh;
+        const int n = st->n, b = PACKED ? 0 : st->b, kvh = st->kvh;
+        const int t0 = PACKED ? st->row0 : 2 * pair * p.Tt;
         if (n == 0) break;
         if (lane == 0) mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(L::kQTiles * kHalves) * 128u * static_cast<uint32_t>(p.G * p.Tt));
         __syncwarp();
         if (lane < L::kQTiles * kHalves) {  // rows past T are zero-filled
           const int i = lane / kHalves, half = lane % kHalves;
-          tma_load_4d(sm + L::kQ + i * L::kTile + half * L::kRegion, &qmap, q_full, 64 * half, kvh * p.G, (2 * pair + i) * p.Tt, b);
+          tma_load_4d(sm + L::kQ + i * L::kTile + half * L::kRegion, &qmap, q_full, 64 * half, kvh * p.G, t0 + i * p.Tt, b);
         }
         ++q_loads;
         g0 += static_cast<uint32_t>(n);
@@ -707,6 +771,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           break;
         }
         const int n = step_at(g0)->n, b = step_at(g0)->b, kvh = step_at(g0)->kvh;
+        const int row0 = PACKED ? step_at(g0)->row0 : 0, rows_here = PACKED ? step_at(g0)->rows : p.T;
         if (n == 0) break;
         // the query tiles of the unit before are done with, and every softmax
         // warp has seen its q_full: a stream without a step in that unit would
@@ -727,9 +792,9 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
 #pragma unroll 1
         for (int i = 0; i < L::kQTiles; ++i) {
           const int tl = r / p.G, t = (2 * pair + i) * p.Tt + tl;
-          const bool in = tl < p.Tt && t < p.T;
+          const bool in = tl < p.Tt && t < rows_here;
           const uint4* src = reinterpret_cast<const uint4*>(
-              p.q + (static_cast<size_t>(b * p.T + (in ? t : 0)) * p.Hq + kvh * p.G + (in ? r - tl * p.G : 0)) * D + 64 * half);
+              p.q + (static_cast<size_t>((PACKED ? row0 : b * p.T) + (in ? t : 0)) * p.Hq + kvh * p.G + (in ? r - tl * p.G : 0)) * D + 64 * half);
           uint32_t mx = 0;  // largest |q| as bf16 bits, of both 16-bit halves
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
@@ -828,10 +893,10 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
     const uint32_t t_o = tmem + lane_base + 256u;  // O0; O1 is 128 columns on
     const float c = p.scale_log2;
     const int tile = PAIR ? 2 * pair + i : 0;
-    const int tl = r / p.G, t = tile * p.Tt + tl;
-    const bool in_tile = tl < p.Tt && t < p.T;
+    const int tl = r / p.G, t = tile * p.Tt + tl;  // packed: row of the item
+    bool in_tile = tl < p.Tt && t < p.T;
     // warps without rows only keep the barriers' counts and clear stale V rows
-    const bool warp_dead = !__any_sync(kFull, in_tile);
+    bool warp_dead = !__any_sync(kFull, in_tile);
     float* xch = reinterpret_cast<float*>(sm + L::kXml);
     float* x_mine = xch + (2 * i + hh) * kTaRows + r;
     const float* x_other = xch + (2 * i + (hh ^ 1)) * kTaRows + r;
@@ -846,6 +911,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         break;
       }
       int n, b, kvh, t0, t1, part, base, mrow, prow, row_state;
+      [[maybe_unused]] int row0 = 0, seen = 0, item0 = 0;  // packed: the item's first row, what the row sees, the first row's position
       {
         const volatile TaStep* st = step_at(g0);
         n = st->n;
@@ -855,12 +921,24 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         t0 = st->t0;
         t1 = st->t1;
         part = st->part;
-        const int nodes = p.tree.node_counts != nullptr ? __ldg(p.tree.node_counts + b) : p.T;
-        base = st->ctx - nodes;
-        const bool live = in_tile && t < nodes;
-        mrow = live ? b * p.tree.stride + t * p.tree.words : -1;
-        prow = (b * p.Hkv + kvh) * p.tree.words;
-        row_state = live ? kTreeRowNormal : kTreeRowZero;
+        if constexpr (PACKED) {
+          row0 = st->row0;
+          item0 = st->seen0 - 1;
+          seen = st->seen0 + t;
+          base = st->base;
+          in_tile = tl < p.Tt && t < st->rows;
+          warp_dead = !__any_sync(kFull, in_tile);
+          mrow = -1;
+          prow = kvh * p.tree.words;
+          row_state = in_tile ? kTreeRowNormal : kTreeRowZero;
+        } else {
+          const int nodes = p.tree.node_counts != nullptr ? __ldg(p.tree.node_counts + b) : p.T;
+          base = st->ctx - nodes;
+          const bool live = in_tile && t < nodes;
+          mrow = live ? b * p.tree.stride + t * p.tree.words : -1;
+          prow = (b * p.Hkv + kvh) * p.tree.words;
+          row_state = live ? kTreeRowNormal : kTreeRowZero;
+        }
       }
       float cq = c, qsum = 0.f, vref = 1.f;
       if constexpr (kOneByte) {
@@ -890,15 +968,20 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           badw = PPI == 8 ? *reinterpret_cast<const volatile uint64_t*>(st->bad) : *reinterpret_cast<const volatile uint32_t*>(st->bad);
           const bool nodes_here = pos0 + kTreeTokens > base;
           if (nodes_here && p.tree.poison != nullptr) {
-            bad0 = tree_window64(p.tree.poison + prow, p.tree.words, pos0 - base);
-            bad1 = tree_window64(p.tree.poison + prow, p.tree.words, pos0 - base + 64);
+            if constexpr (PACKED) {  // (a bit per row of q; those before `base` are other sequences')
+              bad0 = tree_window64(p.tree.poison + prow, p.tree.words, row0 + pos0 - item0) & ~low_bits64(base - pos0);
+              bad1 = tree_window64(p.tree.poison + prow, p.tree.words, row0 + pos0 - item0 + 64) & ~low_bits64(base - pos0 - 64);
+            } else {
+              bad0 = tree_window64(p.tree.poison + prow, p.tree.words, pos0 - base);
+              bad1 = tree_window64(p.tree.poison + prow, p.tree.words, pos0 - base + 64);
+            }
           }
           rm = low_bits64(nvs - 64 * hh);
 #pragma unroll
           for (int q = 0; q < PPI / 2; ++q)
             if ((badw >> (8 * (q + hh * (PPI / 2)))) & 0xffu) rm &= ~(((1ull << BS) - 1ull) << (q * BS));
-          uint64_t see = low_bits64(base - pos0 - 64 * hh);
-          if (nodes_here && mrow >= 0) see |= tree_window64(p.tree.mask + mrow, p.tree.words, pos0 - base + 64 * hh);
+          uint64_t see = low_bits64((PACKED ? seen : base) - pos0 - 64 * hh);
+          if (!PACKED && nodes_here && mrow >= 0) see |= tree_window64(p.tree.mask + mrow, p.tree.words, pos0 - base + 64 * hh);
           rm &= see;
           const uint64_t badh = hh ? bad1 : bad0;
           if ((rm & badh) && row_state == kTreeRowNormal) row_state = kTreeRowNan;
@@ -1158,7 +1241,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       tc_fence_after_sync();
       if (!warp_dead) {
         const int h = kvh * p.G + (r - tl * p.G);
-        const size_t qrow = static_cast<size_t>(b * p.T + t) * p.Hq + h;
+        const size_t qrow = static_cast<size_t>(PACKED ? row0 + t : b * p.T + t) * p.Hq + h;
         const size_t prow_o = (static_cast<size_t>(blockIdx.x) * 2 + (part - 1)) * (L::kQTiles * kTaRows) + (PAIR ? i * kTaRows : 0) + r;
         if (part == 0) {
           const float inv = l == 0.f ? 0.f : 1.f / l;

@@ -11,7 +11,7 @@
 
 #ifdef __CUDACC__
 #define PKV_PLAN_FN __host__ __device__ __forceinline__
-#define PKV_PLAN_CALL __host__ __device__ __noinline__
+#define PKV_PLAN_CALL inline __host__ __device__ __noinline__
 #else
 #define PKV_PLAN_FN inline
 #define PKV_PLAN_CALL inline

@@ -37,20 +37,12 @@ __device__ __forceinline__ bool not_finite(const uint4& x, bool e4m3) {
   return ((((x.x & bits) + one) | ((x.y & bits) + one) | ((x.z & bits) + one) | ((x.w & bits) + one)) & top) != 0u;
 }
 
+// Bits of the rows of this warp's lanes that hold a value that is not finite;
+// `row` is the first byte of the lane's row in v, -1 if it has none.
 template <int kLanes>  // lanes of one row
-__device__ __forceinline__ uint32_t tree_scan_word(const TreeScan& t, int b, int h, int w, int n, int nodes) {
+__device__ __forceinline__ uint32_t scan_rows(const uint8_t* v, long long row, bool e4m3) {
   constexpr int kRows = 32 / kLanes;  // rows at a time
   const int lane = threadIdx.x & 31, sub = lane / kLanes, chunk = lane % kLanes;
-  // lane i: the first byte of node 32 w + i's row, -1 if there is none
-  long long row = -1;
-  {
-    const int u = 32 * w + lane, pos = n - nodes + u;
-    if (u < nodes && pos >= 0) {
-      const int blk = t.block_tables[static_cast<size_t>(b) * t.MB + pos / t.bs];
-      if (static_cast<unsigned>(blk) < static_cast<unsigned>(t.NB))
-        row = ((static_cast<long long>(blk) * t.Hkv + h) * t.bs + pos % t.bs) * t.row_bytes;
-    }
-  }
   uint32_t word = 0u;
 #pragma unroll 1
   for (int r0 = 0; r0 < 32; r0 += 8 * kRows) {
@@ -58,11 +50,11 @@ __device__ __forceinline__ uint32_t tree_scan_word(const TreeScan& t, int b, int
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const long long at = __shfl_sync(kFull, row, (r0 + k * kRows + sub) & 31);
-      x[k] = at >= 0 ? __ldcg(reinterpret_cast<const uint4*>(t.v + at + 16 * chunk)) : make_uint4(0, 0, 0, 0);
+      x[k] = at >= 0 ? __ldcg(reinterpret_cast<const uint4*>(v + at + 16 * chunk)) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const uint32_t votes = __ballot_sync(kFull, not_finite(x[k], t.e4m3 != 0));
+      const uint32_t votes = __ballot_sync(kFull, not_finite(x[k], e4m3));
 #pragma unroll
       for (int s = 0; s < kRows; ++s) {
         constexpr uint32_t kGroup = (1u << kLanes) - 1u;
@@ -71,6 +63,21 @@ __device__ __forceinline__ uint32_t tree_scan_word(const TreeScan& t, int b, int
     }
   }
   return word;
+}
+
+// A word of a tree's nodes.
+__device__ __forceinline__ uint32_t tree_scan_word(const TreeScan& t, int b, int h, int w, int n, int nodes) {
+  // lane i: the first byte of node 32 w + i's row, -1 if there is none
+  long long row = -1;
+  {
+    const int u = 32 * w + (threadIdx.x & 31), pos = n - nodes + u;
+    if (u < nodes && pos >= 0) {
+      const int blk = t.block_tables[static_cast<size_t>(b) * t.MB + pos / t.bs];
+      if (static_cast<unsigned>(blk) < static_cast<unsigned>(t.NB))
+        row = ((static_cast<long long>(blk) * t.Hkv + h) * t.bs + pos % t.bs) * t.row_bytes;
+    }
+  }
+  return t.row_bytes == 256 ? scan_rows<16>(t.v, row, t.e4m3 != 0) : scan_rows<8>(t.v, row, t.e4m3 != 0);
 }
 
 // Words warp0, warp0 + nwarps, ... of the B x Hkv x words.
@@ -84,7 +91,7 @@ __device__ __forceinline__ void tree_scan_values(const TreeScan& t, int warp0, i
     const int nodes = t.node_counts != nullptr ? t.node_counts[b] : t.T;
     uint32_t word = 0u;
     if (n >= 0 && n <= t.MB * t.bs && nodes >= 0 && nodes <= t.T)
-      word = t.row_bytes == 256 ? tree_scan_word<16>(t, b, h, w, n, nodes) : tree_scan_word<8>(t, b, h, w, n, nodes);
+      word = tree_scan_word(t, b, h, w, n, nodes);
     if ((threadIdx.x & 31) == 0) t.poison[it] = word;
   }
 }
