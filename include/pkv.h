@@ -595,7 +595,7 @@ pkv_status pkv_extend_tables(int32_t batch, int32_t block_size, int32_t max_bloc
  * draft_probs NULL: children chosen without randomness (the draft's best
  * tokens, a lookup); Q is then 1 at x alone and a rejection sets P(x) = 0.
  * Values of rows that are negative or not finite count as 0.  Comparisons are
- * made in fp64, sums to 2^-44 or better of their value.
+ * made in fp64, sums to 2^-32 or better of their value.
  *
  *   tokens         device int32 [B][T]: the nodes' tokens, in [0, vocab) (node
  *                  0's is not looked at).

@@ -1243,11 +1243,9 @@ pkv_status pkv_verify_tree(const int32_t* tokens, const int32_t* parents, const 
   DeviceInfo dev;
   pkv_status st = device_info(&dev);
   if (st != PKV_OK) return st;
-  const bool vec = vocab % 4 == 0 && aligned16(target_probs) && target_stride % 4 == 0 &&
-                   (draft_probs == nullptr || (aligned16(draft_probs) && draft_stride % 4 == 0));
   const pkv::VerifyArgs a{tokens, parents, node_counts, target_probs, draft_probs, accept_uniforms, sample_uniforms,
                           accept_idx, accept_counts, next_tokens, dev.err_word, target_stride, draft_stride,
-                          batch, num_nodes, vocab, max_accept, vec ? 1 : 0};
+                          batch, num_nodes, vocab, max_accept};
   cudaError_t e = pkv::launch_verify_tree(a, dev.num_sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "verify_tree launch");
   return PKV_OK;

@@ -235,7 +235,6 @@ struct VerifyArgs {
   unsigned* err;
   long long p_stride, q_stride;
   int B, T, V, A;
-  int vec;  // 1: every row starts on a 16-byte boundary and V is a multiple of 4
 };
 cudaError_t launch_verify_tree(const VerifyArgs& a, int num_sms, cudaStream_t stream);
 

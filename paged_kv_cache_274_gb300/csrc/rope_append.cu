@@ -6,12 +6,12 @@
 //   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)   for each pair i
 // with the angle positions[axis(i)] * inv_freq[i].
 //
-// A row takes D / 8 lanes, 16 bytes each, so a warp loads two (D 128) or four
-// rows at a time.  What depends on the token alone is made once per warp:
-// out_j = r (x_j A_j + x_p B_j), where r is the row's norm factor, x_p the
-// pair's other element, A = w_j cos and B = -/+ w_p sin.  A pair's elements lie
-// in one lane (neighbours) or R / 16 lanes apart (halves; four shuffles of raw
-// bf16 words).
+// A row takes D / 8 lanes, so a warp has two (D 128) or four rows at a time.  A
+// lane holds four pairs, two runs of four values: both elements of its pairs, so
+// the rotation needs no exchange (with 16 consecutive bytes a lane, the halves'
+// partners came by four shuffles and eight more conversions a row group).  What
+// depends on the token alone is made once per warp: the row's factor r times
+// x_a (w_a cos) - x_b (w_b sin), and likewise for b.
 //
 // Angles are kept in turns: the host gives each frequency as a fraction of a
 // turn per position in 2^-64, and position x frequency modulo 2^64 is an
@@ -28,183 +28,233 @@ namespace pkv {
 
 constexpr int kRopeThreads = 128;
 constexpr int kRopeBatch = 4;  // row groups whose loads are in flight together
+constexpr int kRopePair = 2;   // and are turned together
+constexpr int kRopeCtas = 8;   // of an SM
 
-// Coefficients of one tensor's rows in this lane: out = r (x a + x_p b).
-struct RopeCoef {
-  float a[8], b[8];
-};
+// A lane's values: x[0..3] the first run, x[4..7] the second.  Pair k is x[k],
+// x[k + 4] (halves) or x[2 k], x[2 k + 1] (neighbours).
+template <bool HALVES>
+__device__ __forceinline__ constexpr int rope_first(int k) {
+  return HALVES ? k : 2 * k;
+}
+template <bool HALVES>
+__device__ __forceinline__ constexpr int rope_second(int k) {
+  return HALVES ? k + 4 : 2 * k + 1;
+}
 
+__device__ __forceinline__ void unpack8(float (&x)[8], const uint2& a, const uint2& b) {
+  x[0] = bf16lo_to_f32(a.x);
+  x[1] = bf16hi_to_f32(a.x);
+  x[2] = bf16lo_to_f32(a.y);
+  x[3] = bf16hi_to_f32(a.y);
+  x[4] = bf16lo_to_f32(b.x);
+  x[5] = bf16hi_to_f32(b.x);
+  x[6] = bf16lo_to_f32(b.y);
+  x[7] = bf16hi_to_f32(b.y);
+}
+
+// The norm and the rotation of two row groups, so that the norms' chains of
+// shuffles run side by side.  w: the lane's weights (bf16), cs, sn of its pairs.
 template <int D, bool HALVES>
-__device__ __forceinline__ void rope_coef(RopeCoef& f, const uint16_t* weight, int c, int partner, bool turned, const float (&cs)[8],
-                                          const float (&sn)[8]) {
-  uint4 w = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), v = w;  // ones
-  if (weight != nullptr) {
-    w = __ldg(reinterpret_cast<const uint4*>(weight) + c);
-    if (HALVES) v = __ldg(reinterpret_cast<const uint4*>(weight) + partner);
-  }
-  const uint32_t ww[4] = {w.x, w.y, w.z, w.w}, vw[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void turn_rows(float (&y)[kRopePair][8], const uint2& w0, const uint2& w1, const float (&cs)[4], const float (&sn)[4],
+                                          bool norm, float eps, bool turned) {
+  constexpr int kLanes = D / 8;
+  if (norm) {
+    float r[kRopePair];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    auto at = [&](const uint32_t (&t)[4], int k) { return (k & 1) ? bf16hi_to_f32(t[k >> 1]) : bf16lo_to_f32(t[k >> 1]); };
-    f.a[j] = at(ww, j) * (turned ? cs[j] : 1.f);
-    f.b[j] = turned ? (HALVES ? at(vw, j) : at(ww, j ^ 1)) * sn[j] : 0.f;
+    for (int u = 0; u < kRopePair; ++u) {
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) ffma2(s0, s1, y[u][j], y[u][j + 1], y[u][j], y[u][j + 1], s0, s1);
+      r[u] = s0 + s1;
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int u = 0; u < kRopePair; ++u) r[u] += __shfl_xor_sync(kFull, r[u], o);
+    float w[8];
+    unpack8(w, w0, w1);
+#pragma unroll
+    for (int u = 0; u < kRopePair; ++u) {
+      r[u] = rsqrtf(fmaf(r[u], 1.f / D, eps));
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        fmul2(y[u][j], y[u][j + 1], y[u][j], y[u][j + 1], r[u], r[u]);
+        fmul2(y[u][j], y[u][j + 1], y[u][j], y[u][j + 1], w[j], w[j + 1]);
+      }
+    }
+  }
+  if (turned) {
+#pragma unroll
+    for (int u = 0; u < kRopePair; ++u) {
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        float& a0 = y[u][rope_first<HALVES>(k)];
+        float& a1 = y[u][rope_first<HALVES>(k + 1)];
+        float& b0 = y[u][rope_second<HALVES>(k)];
+        float& b1 = y[u][rope_second<HALVES>(k + 1)];
+        float t0, t1, v0, v1;
+        if constexpr (HALVES) {  // (two pairs to a register pair)
+          fmul2(t0, t1, b0, b1, -sn[k], -sn[k + 1]);
+          fmul2(v0, v1, a0, a1, sn[k], sn[k + 1]);
+          ffma2(a0, a1, a0, a1, cs[k], cs[k + 1], t0, t1);
+          ffma2(b0, b1, b0, b1, cs[k], cs[k + 1], v0, v1);
+        } else {
+          t0 = b0 * sn[k];
+          t1 = b1 * sn[k + 1];
+          v0 = a0 * sn[k];
+          v1 = a1 * sn[k + 1];
+          a0 = fmaf(a0, cs[k], -t0);
+          a1 = fmaf(a1, cs[k + 1], -t1);
+          b0 = fmaf(b0, cs[k], v0);
+          b1 = fmaf(b1, cs[k + 1], v1);
+        }
+      }
+    }
   }
 }
 
 template <int D, int KV, bool HALVES>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kHeads = kRopeBatch * kRows;  // heads of a batch
+  __shared__ uint64_t freq[64];
+  __shared__ int axis[64];
   pdl_trigger();
-  pdl_wait();
+  // (once per CTA: lanes that read constants apart take a turn each)
+  if (threadIdx.x < a.R / 2) {
+    freq[threadIdx.x] = a.turns[threadIdx.x];
+    axis[threadIdx.x] = a.axis[threadIdx.x];
+  }
+  __syncthreads();
   const int lane = threadIdx.x & 31, c = lane % kLanes, sub = lane / kLanes;
-  const long long item = static_cast<long long>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
-  const long long token = item / a.parts;
-  if (token >= a.app.N) return;
-  const int part = static_cast<int>(item - token * a.parts);
-  long long slot = 0;
-  if (a.app.slot_mapping != nullptr) {
-    slot = __ldg(a.app.slot_mapping + token);
-    if (slot < 0 || slot >= a.app.nslots) {
-      if (slot != -1 && part == 0 && lane == 0) atomicOr(a.app.err, PKV_DEVERR_SLOT);
-      return;
-    }
-  }
-  // lane t: angles 2 t and 2 t + 1
-  float cs2[2] = {1.f, 1.f}, sn2[2] = {0.f, 0.f};
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int i = 2 * lane + s;
-    if (i < a.R / 2) {
-      const long long pos = __ldg(a.positions + static_cast<size_t>(a.axis[i]) * a.app.N + token);
-      const uint64_t turn = static_cast<uint64_t>(pos) * a.turns[i];
-      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn2[s], &cs2[s]);
-    }
-  }
-  const int half = a.R / 16;  // lanes of a half of the rotated part
-  const bool turned = 8 * c < a.R, second = HALVES && c >= half;
-  const int partner = !HALVES || !turned ? c : second ? c - half : c + half;
-  float cs[8], sn[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    // halves: angles 8 (c mod half) + j; neighbours: 4 c + j / 2
-    const int from = HALVES ? 4 * (second ? c - half : c) + j / 2 : 2 * c + j / 4;
-    const int k = HALVES ? j & 1 : (j >> 1) & 1;
-    cs[j] = __shfl_sync(kFull, cs2[k], from);
-    const float s = __shfl_sync(kFull, sn2[k], from);
-    sn[j] = (HALVES ? second : (j & 1) != 0) ? s : -s;
-  }
-  const int gq = (a.Hq + kRows - 1) / kRows, gk = a.k_new ? (a.app.Hkv + kRows - 1) / kRows : 0;
-  const int groups = gq + 2 * gk, per = (groups + a.parts - 1) / a.parts;
-  const int g_end = min(groups, (part + 1) * per);
-  const long long blk = slot / a.app.bs;
-  const int off = static_cast<int>(slot - blk * a.app.bs);
-
-  // rows of q (which 0), k (1) or v (2): groups g0 .. g1 - 1 of that tensor
-  auto rows = [&](auto which_tag, int g0, int g1) {
-    constexpr int which = decltype(which_tag)::value;
-    const int heads = which == 0 ? a.Hq : a.app.Hkv;
-    const uint4* src = reinterpret_cast<const uint4*>((which == 0 ? a.q + token * a.q_stride : which == 1 ? a.k + token * a.k_stride : a.v + token * a.v_stride));
-    RopeCoef f;
-    bool norm = false;
-    if constexpr (which < 2) {
-      const uint16_t* w = which == 0 ? a.qw : a.kw;
-      norm = w != nullptr;
-      rope_coef<D, HALVES>(f, w, c, partner, turned, cs, sn);
-    }
+  // the lane's runs of four values; lanes past the rotated part have eight in a row
+  const bool turned = 8 * c < a.R;
+  const int e0 = HALVES && turned ? 4 * c : 8 * c, e1 = HALVES && turned ? a.R / 2 + 4 * c : 8 * c + 4;
+  const int nq = (a.Hq + kHeads - 1) / kHeads, nk = a.k_new ? (a.app.Hkv + kHeads - 1) / kHeads : 0;  // batches
+  const int batches = nq + 2 * nk, per = (batches + a.parts - 1) / a.parts;
+  pdl_wait();
+  const unsigned items = static_cast<unsigned>(a.app.N) * a.parts;  // (less than 2^31, as the host checks)
 #pragma unroll 1
-    for (int g = g0; g < g1; g += kRopeBatch) {
-      uint4 x[kRopeBatch];
-#pragma unroll
-      for (int u = 0; u < kRopeBatch; ++u) {
-        const int h = (g + u) * kRows + sub;
-        x[u] = g + u < g1 && h < heads ? __ldcs(src + h * kLanes + c) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int u = 0; u < kRopeBatch; ++u) {
-        const int h = (g + u) * kRows + sub;
-        const bool live = g + u < g1 && h < heads;
-        const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-        float y[8] = {};
-        if constexpr (which < 2) {
-          float xf[8], r = 1.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            xf[2 * j] = bf16lo_to_f32(xw[j]);
-            xf[2 * j + 1] = bf16hi_to_f32(xw[j]);
-          }
-          if (norm) {
-            float ss = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(xf[j], xf[j], ss);
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-            r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-          }
-          float p[8];
-          if constexpr (HALVES) {
-            const int from = (lane & ~(kLanes - 1)) | partner;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t w = __shfl_sync(kFull, xw[j], from);
-              if (!turned) w = 0u;  // (an infinity times b = 0 would be NaN)
-              p[2 * j] = bf16lo_to_f32(w);
-              p[2 * j + 1] = bf16hi_to_f32(w);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) p[j] = turned ? xf[j ^ 1] : 0.f;
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = r * fmaf(xf[j], f.a[j], p[j] * f.b[j]);
-        }
-        if (!live) continue;
-        if constexpr (which == 0) {
-          uint4* dst = reinterpret_cast<uint4*>(a.q_out + token * a.out_stride) + h * kLanes + c;
-          *dst = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-        } else {
-          const long long page = blk * a.app.Hkv + h;
-          const long long elem = (page * a.app.bs + off) * D + 8 * c;
-          uint8_t* cache = which == 1 ? a.app.kc : a.app.vc;
-          [[maybe_unused]] const float* scales = which == 1 ? a.app.ks : a.app.vs;
-          if constexpr (which == 2 && KV != PKV_KV_BF16) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              y[2 * j] = bf16lo_to_f32(xw[j]);
-              y[2 * j + 1] = bf16hi_to_f32(xw[j]);
-            }
-          }
-          if constexpr (KV == PKV_KV_BF16) {
-            *reinterpret_cast<uint4*>(cache + 2 * elem) =
-                which == 2 ? x[u]
-                           : make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-          } else {
-            uint32_t w[2] = {0u, 0u};
-            if constexpr (KV == PKV_KV_INT8) {
-              const float2 sz = __ldg(reinterpret_cast<const float2*>(scales) + page);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) w[j >> 2] |= int8_code(y[j], sz.x, sz.y) << (8 * (j & 3));
-            } else {
-              const float scale = __ldg(scales + page);
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                w[j >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(y[2 * j], scale), __fdiv_rn(y[2 * j + 1], scale)),
-                                                                            __NV_SATFINITE, __NV_E4M3))
-                             << (16 * (j & 1));
-            }
-            *reinterpret_cast<uint2*>(cache + elem) = make_uint2(w[0], w[1]);
-          }
-        }
+  for (unsigned item = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); item < items; item += gridDim.x * (kRopeThreads / 32)) {
+    const unsigned token = item / a.parts;
+    const int begin = static_cast<int>(item - token * a.parts) * per, end = min(batches, begin + per);
+    long long slot = 0;
+    if (a.app.slot_mapping != nullptr) {
+      slot = __ldg(a.app.slot_mapping + token);
+      if (slot < 0 || slot >= a.app.nslots) {
+        if (slot != -1 && begin == 0 && lane == 0) atomicOr(a.app.err, PKV_DEVERR_SLOT);
+        continue;
       }
     }
-  };
-  const int g_begin = part * per;
-  auto span = [&](auto tag, int base, int n) {
-    const int lo = max(g_begin - base, 0), hi = min(g_end - base, n);
-    if (lo < hi) rows(tag, lo, hi);
-  };
-  span(std::integral_constant<int, 0>{}, 0, gq);
-  span(std::integral_constant<int, 1>{}, gq, gk);
-  span(std::integral_constant<int, 2>{}, gq + gk, gk);
+    float cs[4], sn[4];  // of the lane's pairs: angles 4 c .. 4 c + 3
+    {
+      float cs2[2] = {1.f, 1.f}, sn2[2] = {0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {  // lane t makes the angles 2 t and 2 t + 1
+        const int i = 2 * lane + s;
+        if (i < a.R / 2) {
+          const long long pos = __ldg(a.positions + static_cast<size_t>(axis[i]) * a.app.N + token);
+          const uint64_t turn = static_cast<uint64_t>(pos) * freq[i];
+          sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn2[s], &cs2[s]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        cs[k] = __shfl_sync(kFull, cs2[k & 1], 2 * c + k / 2);
+        sn[k] = __shfl_sync(kFull, sn2[k & 1], 2 * c + k / 2);
+      }
+    }
+    const int shift = a.app.bs == 32 ? 5 : 4;  // (blocks of 16 or 32 tokens)
+    const int blk = static_cast<int>(slot >> shift), off = static_cast<int>(slot) & (a.app.bs - 1);
+
+    // batches lo .. hi - 1 of the queries' (0), keys' (1) or values' (2) rows
+    auto rows = [&](auto tag, int lo, int hi) {
+      constexpr int which = decltype(tag)::value;
+      const int heads = which == 0 ? a.Hq : a.app.Hkv;
+      const __nv_bfloat16* src = which == 0 ? a.q + token * a.q_stride : which == 1 ? a.k + token * a.k_stride : a.v + token * a.v_stride;
+      const uint16_t* weight = which == 0 ? a.qw : which == 1 ? a.kw : nullptr;
+      uint2 w0 = make_uint2(0, 0), w1 = w0;
+      if (weight != nullptr) {
+        w0 = __ldg(reinterpret_cast<const uint2*>(weight + e0));
+        w1 = __ldg(reinterpret_cast<const uint2*>(weight + e1));
+      }
+      // where head 0's row goes, and how far apart the heads' rows are there
+      constexpr int elem = which == 0 || KV == PKV_KV_BF16 ? 2 : 1;
+      uint8_t* dst;
+      int apart;
+      [[maybe_unused]] const float* scales = nullptr;
+      if constexpr (which == 0) {
+        dst = reinterpret_cast<uint8_t*>(a.q_out + token * a.out_stride);
+        apart = D * elem;
+      } else {
+        const long long page = static_cast<long long>(blk) * a.app.Hkv;
+        dst = (which == 1 ? a.app.kc : a.app.vc) + (page * a.app.bs + off) * (D * elem);
+        apart = a.app.bs * (D * elem);
+        if constexpr (KV != PKV_KV_BF16) scales = (which == 1 ? a.app.ks : a.app.vs) + page * (KV == PKV_KV_INT8 ? 2 : 1);
+      }
+#pragma unroll 1
+      for (int i = lo; i < hi; ++i) {
+        const int h0 = i * kHeads + sub;
+        const __nv_bfloat16* from = src + h0 * D;
+        uint8_t* out = dst + static_cast<long long>(h0) * apart;
+        uint2 xa[kRopeBatch], xb[kRopeBatch];
+#pragma unroll
+        for (int u = 0; u < kRopeBatch; ++u) {
+          const int h = h0 + u * kRows;
+          xa[u] = xb[u] = make_uint2(0, 0);
+          if (h < heads) {
+            xa[u] = __ldcs(reinterpret_cast<const uint2*>(from + u * kRows * D + e0));
+            xb[u] = __ldcs(reinterpret_cast<const uint2*>(from + u * kRows * D + e1));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kRopeBatch; u += kRopePair) {
+          float y[kRopePair][8];
+          if constexpr (which < 2 || elem == 1) {
+#pragma unroll
+            for (int v = 0; v < kRopePair; ++v) unpack8(y[v], xa[u + v], xb[u + v]);
+          }
+          if constexpr (which < 2) turn_rows<D, HALVES>(y, w0, w1, cs, sn, weight != nullptr, a.eps, turned);
+#pragma unroll
+          for (int v = 0; v < kRopePair; ++v) {
+            const int h = h0 + (u + v) * kRows;
+            if (h >= heads) continue;
+            uint8_t* to = out + (u + v) * kRows * apart;
+            if constexpr (elem == 2) {
+              // (values keep their bits, NaNs too)
+              *reinterpret_cast<uint2*>(to + 2 * e0) =
+                  which == 2 ? xa[u + v] : make_uint2(pack_bf16x2(y[v][0], y[v][1]), pack_bf16x2(y[v][2], y[v][3]));
+              *reinterpret_cast<uint2*>(to + 2 * e1) =
+                  which == 2 ? xb[u + v] : make_uint2(pack_bf16x2(y[v][4], y[v][5]), pack_bf16x2(y[v][6], y[v][7]));
+            } else {
+              uint32_t w[2] = {0u, 0u};
+              if constexpr (KV == PKV_KV_INT8) {
+                const float2 sz = __ldg(reinterpret_cast<const float2*>(scales) + h);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j >> 2] |= int8_code(y[v][j], sz.x, sz.y) << (8 * (j & 3));
+              } else {
+                const float scale = __ldg(scales + h);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  w[j >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
+                                   make_float2(__fdiv_rn(y[v][2 * j], scale), __fdiv_rn(y[v][2 * j + 1], scale)), __NV_SATFINITE, __NV_E4M3))
+                               << (16 * (j & 1));
+              }
+              *reinterpret_cast<uint32_t*>(to + e0) = w[0];
+              *reinterpret_cast<uint32_t*>(to + e1) = w[1];
+            }
+          }
+        }
+      }
+    };
+    auto span = [&](auto tag, int base, int n) {
+      const int lo = max(begin - base, 0), hi = min(end - base, n);
+      if (lo < hi) rows(tag, lo, hi);
+    };
+    span(std::integral_constant<int, 0>{}, 0, nq);
+    span(std::integral_constant<int, 1>{}, nq, nk);
+    span(std::integral_constant<int, 2>{}, nq + nk, nk);
+  }
 }
 
 template <int D, int KV>
@@ -213,21 +263,19 @@ static cudaError_t launch_rope(const RopeArgs& a, bool halves, const cudaLaunchC
 }
 
 cudaError_t launch_rope_append(int kv_dtype, int D, bool halves, RopeArgs a, int num_sms, cudaStream_t stream) {
-  const int rows = 32 / (D / 8);
-  const int groups = (a.Hq + rows - 1) / rows + (a.k_new ? 2 * ((a.app.Hkv + rows - 1) / rows) : 0);
-  // A warp takes two batches of groups, one group where that leaves the GPU
-  // without 16 warps an SM.
-  const long long full = static_cast<long long>(num_sms) * 16;
-  int parts = (groups + 2 * kRopeBatch - 1) / (2 * kRopeBatch);
-  if (static_cast<long long>(a.app.N) * parts < full)
-    parts = static_cast<int>(std::min<long long>(groups, (full + a.app.N - 1) / a.app.N));
+  const int heads = kRopeBatch * (32 / (D / 8));
+  const int batches = (a.Hq + heads - 1) / heads + (a.k_new ? 2 * ((a.app.Hkv + heads - 1) / heads) : 0);
+  const long long warps = static_cast<long long>(num_sms) * kRopeCtas * (kRopeThreads / 32);
+  int parts = (batches + 1) / 2;
+  if (static_cast<long long>(a.app.N) * parts < warps)
+    parts = static_cast<int>(std::min<long long>(batches, (warps + a.app.N - 1) / a.app.N));
   a.parts = parts;
   const long long items = static_cast<long long>(a.app.N) * parts;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((items + kRopeThreads / 32 - 1) / (kRopeThreads / 32)));
+  cfg.gridDim = dim3(static_cast<unsigned>((std::min(items, warps) + kRopeThreads / 32 - 1) / (kRopeThreads / 32)));
   cfg.blockDim = dim3(kRopeThreads);
   cfg.stream = stream;
   cfg.attrs = attr;

@@ -16,13 +16,14 @@
 // but A, and a removed token's P is 0 by itself.
 //
 // The drawn token is a border among sums over the vocabulary, so everything is
-// summed to 2^-44 or better: p - A q is kept as an unevaluated sum of two
+// summed to 2^-32 or better: p - A q is kept as an unevaluated sum of two
 // floats (error-free transformations of addition and product, T. J. Dekker and
-// D. E. Knuth), so are the running sums; a chunk's sum is a double.  Doubles
-// per element would be bound by the fp64 units (2 operations a clock and SM).
+// D. E. Knuth), so is everything that is summed or compared.  There are no
+// doubles: fp64 units do 2 operations a clock and SM, and with doubles in the
+// draw alone it took 9 to 12 us of a call instead of 2.
 //
 // What bounds it: the rows of the nodes where the walk loses a child or ends,
-// from HBM, and for a small batch the chain of loads.  One cluster of up to 8
+// from HBM, and for a small batch the chain of loads.  One cluster of up to 16
 // CTAs per sequence.  Its first CTA walks (a warp; the nodes' own p and q are
 // gathered beforehand, side by side) and tells the others by distributed shared
 // memory which row to sum next; the CTAs take its chunks of 512 values in turn.
@@ -42,7 +43,7 @@ constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyChunk = 512;  // values that a warp sums at a time
 constexpr int kPer = kVerifyChunk / 32;
-constexpr int kVerifyCluster = 8;
+constexpr int kVerifyCluster = 16;  // most CTAs of a cluster (more than 8 by a launch attribute of the kernel)
 
 // An unevaluated sum hi + lo.
 struct Pair {
@@ -52,24 +53,43 @@ __device__ __forceinline__ Pair two_sum(float a, float b) {
   const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
   return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
+// hi takes what it can hold of the sum (|hi| >= |lo|).
+__device__ __forceinline__ Pair joined(float hi, float lo) {
+  const float s = __fadd_rn(hi, lo);
+  return {s, __fsub_rn(lo, __fsub_rn(s, hi))};
+}
 __device__ __forceinline__ void add_to(Pair& x, const Pair& y) {
   const Pair s = two_sum(x.hi, y.hi);
-  const float lo = __fadd_rn(s.lo, __fadd_rn(x.lo, y.lo));
-  x.hi = __fadd_rn(s.hi, lo);
-  x.lo = __fsub_rn(lo, __fsub_rn(x.hi, s.hi));
+  x = joined(s.hi, __fadd_rn(s.lo, __fadd_rn(x.lo, y.lo)));
 }
+__device__ __forceinline__ Pair times(const Pair& x, const Pair& y) {
+  const float h = __fmul_rn(x.hi, y.hi);
+  return joined(h, fmaf(x.lo, y.hi, fmaf(x.hi, y.lo, fmaf(x.hi, y.hi, -h))));
+}
+// x / y in two steps of long division
+__device__ __forceinline__ Pair over(const Pair& x, const Pair& y) {
+  const float q = __fdiv_rn(x.hi, y.hi);
+  const Pair p = times(y, Pair{q, 0.f}), d = two_sum(x.hi, -p.hi);
+  return joined(q, __fdiv_rn(__fadd_rn(d.hi, __fadd_rn(d.lo, __fsub_rn(x.lo, p.lo))), y.hi));
+}
+// (of joined pairs)
+__device__ __forceinline__ bool below(const Pair& x, const Pair& y) { return x.hi < y.hi || (x.hi == y.hi && x.lo < y.lo); }
+__device__ __forceinline__ bool positive(const Pair& x) { return x.hi > 0.f || (x.hi == 0.f && x.lo > 0.f); }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // What is negative or not finite counts as 0.
 __device__ __forceinline__ Pair weight(float p) { return {p > 0.f && p < INFINITY ? p : 0.f, 0.f}; }
-// max(p - (ah + al) q, 0), likewise.
+// max(p - (ah + al) q, 0), likewise.  (Where p >= ah q, three operations give
+// the difference and what it rounds away; elsewhere the result is 0.)
 __device__ __forceinline__ Pair weight_left(float p, float q, float ah, float al) {
   const float h = __fmul_rn(ah, q);
   const float l = fmaf(al, q, fmaf(ah, q, -h));
-  const Pair d = two_sum(p, -h);
-  const float lo = __fsub_rn(d.lo, l);
-  const bool some = __fadd_rn(d.hi, lo) > 0.f;
-  return {some ? d.hi : 0.f, some ? lo : 0.f};
+  const float d = __fsub_rn(p, h);
+  const float lo = __fsub_rn(__fsub_rn(__fsub_rn(p, d), h), l);
+  const bool some = __fadd_rn(d, lo) > 0.f;
+  return {some ? d : 0.f, some ? lo : 0.f};
 }
-__device__ __forceinline__ double value(const Pair& x) { return static_cast<double>(x.hi) + static_cast<double>(x.lo); }
 __device__ __forceinline__ Pair warp_total(Pair x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -84,177 +104,244 @@ struct VerifyShared {
   int row;       // of the sequence; -1: nothing more
   int removed;   // tokens in `gone`
   int want_y;
+  int last;      // the walk ends with these sums: only its warp goes on
   float ah, al;
-  double y_part[kVerifyCluster * kVerifyWarps];  // (first CTA)
-  int gone[PKV_MAX_QUERY_TOKENS];                // tokens of the rejected children
+  Pair y_part[kVerifyCluster * kVerifyWarps];  // (first CTA)
+  int gone[PKV_MAX_QUERY_TOKENS];              // tokens of the rejected children
   // the nodes (first CTA)
   int token[PKV_MAX_QUERY_TOKENS], parent[PKV_MAX_QUERY_TOKENS];
   float r[PKV_MAX_QUERY_TOKENS], p[PKV_MAX_QUERY_TOKENS], q[PKV_MAX_QUERY_TOKENS];
+  Pair weights[kVerifyChunk / 16 * 17];  // of the chunk that the token is drawn from (verify_pad)
 };
 
-// 512 values of a row from e0 on, 16 a lane: lane's value k is at
-// e0 + verify_at(k, lane); 0 past the row.
-template <bool VEC>
-__device__ __forceinline__ int verify_at(int k, int lane) {
-  return VEC ? (k / 4) * 128 + lane * 4 + k % 4 : k * 32 + lane;
+// Rows start at any float.  Their chunks are counted from the 16-byte boundary
+// before them, `shift` floats back, so that a lane's four values are one load;
+// with a draft row on another shift they are single loads (shift 0).
+struct VerifyRows {
+  const float* p;
+  const float* q;  // NULL: no draft rows
+  int shift;
+  bool vec;
+};
+__device__ __forceinline__ VerifyRows verify_rows(const VerifyArgs& a, size_t row) {
+  VerifyRows r;
+  r.p = a.p + row * a.p_stride;
+  r.q = a.q != nullptr ? a.q + row * a.q_stride : nullptr;
+  const int sp = static_cast<int>(reinterpret_cast<uintptr_t>(r.p) >> 2) & 3;
+  r.vec = r.q == nullptr || (static_cast<int>(reinterpret_cast<uintptr_t>(r.q) >> 2) & 3) == sp;
+  r.shift = r.vec ? sp : 0;
+  return r;
 }
-template <bool VEC>
-__device__ __forceinline__ void verify_load(float (&x)[kPer], const float* row, int e0, int V, int lane) {
-  if constexpr (VEC) {  // (V is a multiple of 4)
+
+// A chunk's values, 16 a lane: lane's value k is at e0 + verify_at(k, lane).
+__device__ __forceinline__ int verify_at(int k, int lane) { return (k / 4) * 128 + lane * 4 + k % 4; }
+// (0 outside the row)
+__device__ __forceinline__ void verify_load(float (&x)[kPer], const float* row, int e0, int V, int lane, bool vec) {
 #pragma unroll
-    for (int k = 0; k < kPer / 4; ++k) {
-      const int e = e0 + verify_at<true>(4 * k, lane);
-      const float4 v = e < V ? __ldg(reinterpret_cast<const float4*>(row + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      x[4 * k] = v.x;
-      x[4 * k + 1] = v.y;
-      x[4 * k + 2] = v.z;
-      x[4 * k + 3] = v.w;
-    }
-  } else {
+  for (int k = 0; k < kPer; k += 4) {
+    const int e = e0 + verify_at(k, lane);
+    if (vec && e >= 0 && e + 4 <= V) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(row + e));
+      x[k] = v.x;
+      x[k + 1] = v.y;
+      x[k + 2] = v.z;
+      x[k + 3] = v.w;
+    } else {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int e = e0 + verify_at<false>(k, lane);
-      x[k] = e < V ? __ldg(row + e) : 0.f;
+      for (int j = 0; j < 4; ++j) x[k + j] = e + j >= 0 && e + j < V ? __ldg(row + e + j) : 0.f;
     }
   }
+}
+
+// 0 for the rejected children's tokens.
+__device__ __forceinline__ void verify_drop(float (&x)[kPer], const VerifyShared* s, int removed, int e0, int lane) {
+#pragma unroll 1
+  for (int g = 0; g < removed; ++g) {
+    const int d = s->gone[g] - e0;
+    if (static_cast<unsigned>(d) < static_cast<unsigned>(kVerifyChunk)) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (verify_at(k, lane) == d) x[k] = 0.f;
+    }
+  }
+}
+
+// Sum of a lane's values, four running sums side by side.  Each keeps what its
+// additions round away in `lo`.
+template <typename F>
+__device__ __forceinline__ Pair verify_sum(F&& at) {
+  Pair s[4];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const Pair w = at(k);
+    if (k < 4) {
+      s[k] = w;
+    } else {
+      const Pair t = two_sum(s[k % 4].hi, w.hi);
+      s[k % 4] = {t.hi, __fadd_rn(s[k % 4].lo, __fadd_rn(t.lo, w.lo))};
+    }
+  }
+  add_to(s[0], s[1]);
+  add_to(s[2], s[3]);
+  add_to(s[0], s[2]);
+  return s[0];
+}
+
+// Sum of chunk i of the target's weights without the removed tokens.
+__device__ __noinline__ Pair verify_chunk_alone(const VerifyArgs& a, const VerifyShared* s, const VerifyRows& r, int i, int removed) {
+  const int lane = threadIdx.x & 31, e0 = i * kVerifyChunk - r.shift;
+  float pv[kPer];
+  verify_load(pv, r.p, e0, a.V, lane, r.vec);
+  verify_drop(pv, s, removed, e0, lane);
+  return warp_total(verify_sum([&](int k) { return weight(pv[k]); }));
 }
 
 // This CTA's chunks of the row: sums of max(p - A q, 0) to the first CTA's
 // `sums`, this warp's sum of the Q that are left to its y_part.
-template <bool VEC, bool DRAFT>
-__device__ __forceinline__ void verify_pass(const VerifyArgs& a, const VerifyShared* s, double* sums0, double* y_part0, const float* p,
-                                            const float* q, int chunks, int rank, int ranks) {
+template <bool DRAFT>
+__device__ __forceinline__ void verify_pass(const VerifyArgs& a, const VerifyShared* s, Pair* sums0, Pair* y_part0, const VerifyRows& r,
+                                            int rank, int ranks) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float ah = s->ah, al = s->al;
-  const int removed = s->removed;
+  const int removed = s->removed, chunks = (a.V + r.shift + kVerifyChunk - 1) / kVerifyChunk;
   const bool want_y = s->want_y != 0;
   Pair y{0.f, 0.f};
 #pragma unroll 1
   for (int i = warp * ranks + rank; i < chunks; i += kVerifyWarps * ranks) {
-    const int e0 = i * kVerifyChunk;
-    float pv[kPer], qv[kPer];
-    verify_load<VEC>(pv, p, e0, a.V, lane);
-    if constexpr (DRAFT) verify_load<VEC>(qv, q, e0, a.V, lane);
-    Pair z{0.f, 0.f};
-    auto drop = [&](float (&x)[kPer]) {  // rejected children's tokens
-#pragma unroll 1
-      for (int g = 0; g < removed; ++g) {
-        const int d = s->gone[g] - e0;
-        if (static_cast<unsigned>(d) < static_cast<unsigned>(kVerifyChunk)) {
-#pragma unroll
-          for (int k = 0; k < kPer; ++k)
-            if (verify_at<VEC>(k, lane) == d) x[k] = 0.f;
-        }
-      }
-    };
-    if constexpr (!DRAFT) drop(pv);
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) add_to(z, DRAFT ? weight_left(pv[k], qv[k], ah, al) : weight(pv[k]));
-    if constexpr (DRAFT) {
+    if constexpr (!DRAFT) {
+      const Pair z = verify_chunk_alone(a, s, r, i, removed);
+      if (lane == 0) sums0[i] = z;
+    } else {
+      const int e0 = i * kVerifyChunk - r.shift;
+      float pv[kPer], qv[kPer];
+      verify_load(pv, r.p, e0, a.V, lane, r.vec);
+      verify_load(qv, r.q, e0, a.V, lane, r.vec);
+      const Pair z = warp_total(verify_sum([&](int k) { return weight_left(pv[k], qv[k], ah, al); }));
+      if (lane == 0) sums0[i] = z;
       if (want_y) {
-        drop(qv);
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) add_to(y, Pair{qv[k], 0.f});
+        verify_drop(qv, s, removed, e0, lane);
+        add_to(y, verify_sum([&](int k) { return weight(qv[k]); }));
       }
     }
-    z = warp_total(z);
-    if (lane == 0) sums0[i] = value(z);
   }
   if (want_y) {
     y = warp_total(y);
-    if (lane == 0) y_part0[rank * kVerifyWarps + warp] = value(y);
+    if (lane == 0) y_part0[rank * kVerifyWarps + warp] = y;
   }
 }
 
-// Inclusive scan over the warp.
-__device__ __forceinline__ double warp_scan(double x, int lane) {
+// Inclusive scan over the warp.  (Not inlined: code that runs once costs its
+// fetch, 5 cycles and more an instruction.)
+__device__ __noinline__ Pair warp_scan(Pair x) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(kFull, x, o);
-    if (lane >= o) x += y;
+    const Pair y{__shfl_up_sync(kFull, x.hi, o), __shfl_up_sync(kFull, x.lo, o)};
+    Pair t = x;
+    add_to(t, y);
+    if (lane >= o) x = t;
   }
   return x;
 }
-__device__ __forceinline__ double warp_sum(double x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-  return x;
+__device__ __forceinline__ Pair from_lane(const Pair& x, int lane) { return {__shfl_sync(kFull, x.hi, lane), __shfl_sync(kFull, x.lo, lane)}; }
+// What the lanes before this one have, of an inclusive scan.
+__device__ __forceinline__ Pair warp_before(const Pair& upto) {
+  const Pair y{__shfl_up_sync(kFull, upto.hi, 1), __shfl_up_sync(kFull, upto.lo, 1)};
+  return (threadIdx.x & 31) > 0 ? y : Pair{0.f, 0.f};
 }
 
-// The first index whose partial sum exceeds u times the whole (the last with
-// any weight, should rounding leave none).  One warp.
-__device__ __forceinline__ int verify_draw(const VerifyArgs& a, const VerifyShared* s, const double* sums, int chunks, const float* p,
-                                           const float* q, float ah, float al, int removed, double target) {
-  const int lane = threadIdx.x & 31;
-  // chunk by chunk, a run of chunks per lane
-  const int per = (chunks + 31) / 32, c0 = min(lane * per, chunks), c1 = min(c0 + per, chunks);
-  double mine = 0.0;
-  for (int i = c0; i < c1; ++i) mine += sums[i];
-  const double upto = warp_scan(mine, lane);
-  double before = upto - mine;
-  int chunk = -1, any = -1;
-  double base = 0.0;
-  for (int i = c0; i < c1; ++i) {
-    if (sums[i] > 0.0) {
-      any = i;
-      if (chunk < 0 && before + sums[i] > target) {
-        chunk = i;
-        base = before;
-      }
-    }
-    before += sums[i];
-  }
-  const unsigned found = __ballot_sync(kFull, chunk >= 0), some = __ballot_sync(kFull, any >= 0);
-  if (some == 0) return -1;
+// Sums of n pairs, a run of them per lane: up to each run's end.  One warp.
+__device__ __forceinline__ int verify_run(int n) { return (n + 31) / 32; }
+__device__ __forceinline__ Pair verify_runs(const Pair* x, int n) {
+  const int per = verify_run(n), i0 = min((static_cast<int>(threadIdx.x) & 31) * per, n), i1 = min(i0 + per, n);
+  Pair t{0.f, 0.f};
+#pragma unroll 1
+  for (int i = i0; i < i1; ++i) add_to(t, x[i]);
+  return warp_scan(t);
+}
+
+// A lane's 16 values in a row, without bank conflicts among the lanes.
+__device__ __forceinline__ int verify_pad(int i) { return i + (i >> 4); }
+
+// The first index whose partial sum exceeds `target` (the last with any weight,
+// should rounding leave none); `upto`: verify_runs of the chunks.  One warp.
+__device__ __forceinline__ int verify_draw(const VerifyArgs& a, VerifyShared* s, const Pair* sums, const VerifyRows& r, const Pair& A,
+                                           int removed, const Pair& upto, const Pair& target) {
+  const int lane = threadIdx.x & 31, chunks = (a.V + r.shift + kVerifyChunk - 1) / kVerifyChunk, per = verify_run(chunks);
+  const Pair runs_before = warp_before(upto);
+  unsigned found = __ballot_sync(kFull, below(target, upto));
   const bool last = found == 0;
-  const int from = last ? 31 - __clz(some) : __ffs(found) - 1;
-  chunk = __shfl_sync(kFull, last ? any : chunk, from);
-  base = __shfl_sync(kFull, base, from);
-  // 16 values a lane in their order
-  const int e0 = chunk * kVerifyChunk + lane * kPer;
-  double w[kPer], sum = 0.0;
+  if (last) found = __ballot_sync(kFull, below(runs_before, upto));  // runs with any weight
+  if (found == 0) return -1;
+  const int run = last ? 31 - __clz(found) : __ffs(found) - 1, c1 = min((run + 1) * per, chunks);
+  Pair base = from_lane(runs_before, run);
+  int chunk = -1;
+#pragma unroll 1
+  for (int c = run * per; c < c1 && (last || chunk < 0); c += 32) {  // (once, up to 512k tokens)
+    const Pair w = c + lane < c1 ? sums[c + lane] : Pair{0.f, 0.f};
+    const Pair in = warp_scan(w);
+    Pair at = base;
+    add_to(at, in);
+    unsigned m = __ballot_sync(kFull, positive(w) && (last || below(target, at)));
+    if (m != 0) {
+      const int k = last ? 31 - __clz(m) : __ffs(m) - 1;
+      chunk = c + k;
+      if (!last && k > 0) add_to(base, from_lane(in, k - 1));
+    } else {
+      add_to(base, from_lane(in, 31));
+      m = __ballot_sync(kFull, positive(w));  // (kept, should the sums disagree in their last bits)
+      if (m != 0 && !last && c + 32 >= c1) chunk = c + 31 - __clz(m);
+    }
+  }
+  if (chunk < 0) return -1;
+  // its weights, 16 in a row a lane
+  const int e0 = chunk * kVerifyChunk - r.shift;
+  {
+    float pv[kPer], qv[kPer];
+    verify_load(pv, r.p, e0, a.V, lane, r.vec);
+    if (r.q != nullptr) verify_load(qv, r.q, e0, a.V, lane, r.vec);
 #pragma unroll
+    for (int k = 0; k < kPer; ++k) s->weights[verify_pad(verify_at(k, lane))] = Pair{pv[k], r.q != nullptr ? qv[k] : 0.f};
+  }
+  __syncwarp();
+  if (r.q == nullptr)
+#pragma unroll 1
+    for (int g = lane; g < removed; g += 32)
+      if (static_cast<unsigned>(s->gone[g] - e0) < static_cast<unsigned>(kVerifyChunk)) s->weights[verify_pad(s->gone[g] - e0)].hi = 0.f;
+  __syncwarp();
+  Pair own{0.f, 0.f};
+#pragma unroll 4
   for (int k = 0; k < kPer; ++k) {
-    const int e = e0 + k;
-    Pair x{0.f, 0.f};
-    if (e < a.V) {
-      const float pv = __ldg(p + e);
-      x = q != nullptr ? weight_left(pv, __ldg(q + e), ah, al) : weight(pv);
-    }
-    w[k] = value(x);
+    Pair& w = s->weights[verify_pad(lane * kPer + k)];
+    w = weight_left(w.hi, w.lo, A.hi, A.lo);
+    add_to(own, w);
   }
-  if (q == nullptr) {
-    for (int g = 0; g < removed; ++g) {
-      const int d = s->gone[g] - e0;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k)
-        if (k == d) w[k] = 0.0;
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) sum += w[k];
-  double at = base + (warp_scan(sum, lane) - sum);
-  int hit = -1, tail = -1;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    at += w[k];
-    if (w[k] > 0.0) {
-      tail = e0 + k;
-      if (hit < 0 && at > target) hit = e0 + k;
-    }
-  }
-  const unsigned hits = last ? 0u : __ballot_sync(kFull, hit >= 0), tails = __ballot_sync(kFull, tail >= 0);
-  if (hits != 0) return __shfl_sync(kFull, hit, __ffs(hits) - 1);
-  return tails != 0 ? __shfl_sync(kFull, tail, 31 - __clz(tails)) : -1;
+  __syncwarp();
+  const Pair in = warp_scan(own), own_before = warp_before(in);
+  Pair at = base;
+  add_to(at, in);
+  unsigned m = last ? 0u : __ballot_sync(kFull, below(target, at));
+  const bool hit_lane = m != 0;
+  if (!hit_lane) m = __ballot_sync(kFull, positive(own));
+  if (m == 0) return -1;
+  const int owner = hit_lane ? __ffs(m) - 1 : 31 - __clz(m);
+  add_to(base, from_lane(own_before, owner));
+  const Pair w = lane < kPer ? s->weights[verify_pad(owner * kPer + lane)] : Pair{0.f, 0.f};
+  at = base;
+  add_to(at, warp_scan(w));
+  const bool any = positive(w);
+  const int hit = hit_lane && any && below(target, at) ? e0 + owner * kPer + lane : -1, tail = any ? e0 + owner * kPer + lane : -1;
+  const unsigned hits = __ballot_sync(kFull, hit >= 0);
+  return hits != 0 ? __shfl_sync(kFull, hit, __ffs(hits) - 1) : __reduce_max_sync(kFull, tail);
 }
 
-__global__ void __launch_bounds__(kVerifyThreads) verify_tree_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const VerifyArgs a) {
   __shared__ VerifyShared s;
-  extern __shared__ double sums[];  // (first CTA) of the chunks
+  extern __shared__ Pair sums[];  // (first CTA) of the chunks
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
   const int b = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int chunks = (a.V + kVerifyChunk - 1) / kVerifyChunk;
+  cluster_arrive();
   pdl_trigger();
   pdl_wait();
   const size_t seq = static_cast<size_t>(b) * a.T;
@@ -264,7 +351,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_tree_kernel(const Verif
   // the nodes, and what the target and the draft give them
   int nodes = 0;
   bool bad = false;
+  float u = 0.f;
   if (rank == 0) {
+    u = a.sample_uniforms[b];
     nodes = a.node_counts != nullptr ? a.node_counts[b] : a.T;
     if (nodes < 0 || nodes > a.T) {
       bad = true;
@@ -288,9 +377,13 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_tree_kernel(const Verif
 
   // the walk's state (the first CTA's warp 0, the same in every lane)
   int at = 0, count = 0, next = 1, removed = 0, token = -1;
-  double A = 0.0, Z = 1.0, Y = 1.0;
+  const Pair none{0.f, 0.f}, one{1.f, 0.f};
+  Pair A = none, Z = one, Y = one;
   bool summed = false;    // `sums` are those of P as it is
-  bool walking = nodes > 0, whole = false;
+  Pair y_sum{-1.f, 0.f};  // Y as it was last summed (< 0: not at this node)
+  Pair z_sum = none, upto = none;  // Z as it was last summed, and the runs' ends then
+  bool stale = false;     // `sums` have changed since
+  bool walking = nodes > 0, done = false;
   if (rank == 0 && warp == 0 && walking) {
     count = 1;
     if (lane == 0) a.accept_idx[static_cast<size_t>(b) * a.A] = 0;
@@ -303,22 +396,22 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_tree_kernel(const Verif
     return -1;
   };
   // the first CTA's warp 0 tells every CTA what to sum
-  auto tell = [&](int row, bool want_y) {
-    const float ah = static_cast<float>(A), al = static_cast<float>(A - static_cast<double>(ah));
+  auto tell = [&](int row, bool want_y, bool last) {
     if (lane < ranks) {
       VerifyShared* to = cluster.map_shared_rank(&s, lane);
       to->row = row;
       to->removed = removed;
       to->want_y = want_y ? 1 : 0;
-      to->ah = ah;
-      to->al = al;
+      to->last = last ? 1 : 0;
+      to->ah = A.hi;
+      to->al = A.lo;
       if (removed > 0) to->gone[removed - 1] = s.token[next - 1];
     }
   };
-  double* sums0 = cluster.map_shared_rank(sums, 0);
-  double* y_part0 = cluster.map_shared_rank(s.y_part, 0);
+  Pair* sums0 = cluster.map_shared_rank(sums, 0);
+  Pair* y_part0 = cluster.map_shared_rank(s.y_part, 0);
 
-  cluster.sync();  // every CTA of the cluster runs
+  cluster_wait();  // every CTA of the cluster runs
   for (;;) {
     if (rank == 0 && warp == 0) {
       bool ask = false;
@@ -333,73 +426,116 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_tree_kernel(const Verif
         bool was = false;  // its token was a rejected sibling's
         for (int g = lane; g < removed; g += 32) was |= s.gone[g] == x;
         was = __any_sync(kFull, was);
-        const double q = was ? 0.0 : static_cast<double>(s.q[c]);
-        double left = static_cast<double>(s.p[c]) - (a.q != nullptr ? A * static_cast<double>(s.q[c]) : 0.0);
-        if (!(left > 0.0) || (a.q == nullptr && was)) left = 0.0;
-        if (static_cast<double>(s.r[c]) * (a.q != nullptr ? q : 1.0) * Z < left * Y) {
+        const float q0 = weight(s.q[c]).hi;
+        const Pair q{was && a.q != nullptr ? 0.f : q0, 0.f};
+        Pair left = weight_left(s.p[c], a.q != nullptr ? q0 : 0.f, A.hi, A.lo);
+        left = a.q == nullptr && was ? none : joined(left.hi, left.lo);
+        const Pair rq = times(Pair{s.r[c], 0.f}, q);
+        if (removed == 0 ? below(rq, left) : below(times(rq, Z), times(left, Y))) {
           if (lane == 0) a.accept_idx[static_cast<size_t>(b) * a.A + count] = c;
           ++count;
           at = c;
           removed = 0;
-          A = 0.0;
-          Z = Y = 1.0;
+          A = none;
+          Z = Y = one;
+          y_sum.hi = -1.f;
           summed = false;
         } else {
-          A += Y > 0.0 ? Z / Y : 0.0;
-          ++removed;
-          tell(at, a.q != nullptr && child(next) >= 0);
-          ask = true;
+          if (removed++ == 0)
+            A = one;
+          else if (Y.hi > 0.f)
+            add_to(A, over(Z, Y));
+          const bool more = count < a.A && child(next) >= 0;
+          if (a.q == nullptr && summed) {
+            // Only this token's chunk changes.  Summed anew where the difference
+            // may be nothing but rounding, everything where Z has lost 8 bits.
+            if (lane == 0) s.gone[removed - 1] = x;
+            __syncwarp();
+            if (!was && q0 > 0.f) {
+              const VerifyRows r = verify_rows(a, seq + at);
+              const int i = (x + r.shift) / kVerifyChunk;
+              const float px = weight(s.p[c]).hi, whole_sum = sums[i].hi;
+              Pair z = sums[i];
+              add_to(z, Pair{-px, 0.f});
+              if (!(z.hi > whole_sum * 0x1p-38f)) z = verify_chunk_alone(a, &s, r, i, removed);
+              __syncwarp();
+              if (lane == 0) sums[i] = z;
+              __syncwarp();
+              add_to(Z, Pair{-px, 0.f});
+              stale = true;
+            }
+            if (!(Z.hi >= z_sum.hi / 256)) {
+              for (int rr = 0; rr < ranks; ++rr)
+                for (int g = lane; g < removed; g += 32) cluster.map_shared_rank(&s, rr)->gone[g] = s.gone[g];
+              tell(at, false, !more);
+              ask = true;
+            }
+          } else {
+            // Y without this token: summed again only where the difference would
+            // lose more than 8 bits
+            bool want_y = false;
+            if (a.q != nullptr && more) {
+              add_to(Y, Pair{-q.hi, 0.f});
+              want_y = !(y_sum.hi >= 0.f && Y.hi >= y_sum.hi / 256);
+            }
+            tell(at, want_y, !more);
+            ask = true;
+          }
         }
       }
-      if (!ask && nodes > 0) {
-        if (!summed) {  // the target's own weights
-          tell(at, false);
-          ask = true;
-        } else if (!(Z > 0.0) && !whole) {
-          // nothing is left: the draft has as much everywhere
-          whole = true;
-          removed = 0;
-          A = 0.0;
-          tell(at, false);
-          ask = true;
-        }
+      if (!ask && nodes > 0 && !summed) {  // the target's own weights
+        tell(at, false, true);
+        ask = true;
       }
-      if (!ask) tell(-1, false);
+      done = !ask;
+      if (done) tell(-1, false, true);
       summed = true;
     }
-    cluster.sync();  // the request is there
+    cluster_arrive();  // the request is there
+    if (done) break;   // (the walking warp goes on, and waits when it is through)
+    cluster_wait();
     const int row = s.row;
-    if (row < 0) break;
-    const float* p = row_p(row);
-    const float* q = a.q != nullptr ? row_q(row) : nullptr;
-    // (one test for all rows: strides and bases of 16 bytes)
+    if (row < 0) return;
+    const VerifyRows r = verify_rows(a, seq + row);
     if (a.q != nullptr)
-      a.vec ? verify_pass<true, true>(a, &s, sums0, y_part0, p, q, chunks, rank, ranks)
-            : verify_pass<false, true>(a, &s, sums0, y_part0, p, q, chunks, rank, ranks);
+      verify_pass<true>(a, &s, sums0, y_part0, r, rank, ranks);
     else
-      a.vec ? verify_pass<true, false>(a, &s, sums0, y_part0, p, q, chunks, rank, ranks)
-            : verify_pass<false, false>(a, &s, sums0, y_part0, p, q, chunks, rank, ranks);
-    cluster.sync();  // the sums are there
+      verify_pass<false>(a, &s, sums0, y_part0, r, rank, ranks);
+    const bool last = s.last != 0;
+    cluster_arrive();  // the sums are there
+    if (last && (rank != 0 || warp != 0)) return;
+    cluster_wait();
     if (rank == 0 && warp == 0) {
-      double z = 0.0, y = 0.0;
-      for (int i = lane; i < chunks; i += 32) z += sums[i];
-      Z = warp_sum(z);
-      if (a.q != nullptr && s.want_y) {
-        for (int i = lane; i < ranks * kVerifyWarps; i += 32) y += s.y_part[i];
-        Y = warp_sum(y);
-      } else {
-        Y = 1.0;
-      }
+      upto = verify_runs(sums, (a.V + r.shift + kVerifyChunk - 1) / kVerifyChunk);
+      stale = false;
+      z_sum = Z = from_lane(upto, 31);
+      if (s.want_y) y_sum = Y = from_lane(verify_runs(s.y_part, ranks * kVerifyWarps), 31);
+      if (last) break;
     }
   }
-  if (rank != 0 || warp != 0) return;
   if (nodes > 0) {
-    const bool finite = Z > 0.0 && Z < INFINITY;
-    if (finite) {
-      const float ah = static_cast<float>(A), al = static_cast<float>(A - static_cast<double>(ah));
-      token = verify_draw(a, &s, sums, chunks, row_p(at), a.q != nullptr ? row_q(at) : nullptr, ah, al, removed,
-                          static_cast<double>(a.sample_uniforms[b]) * Z);
+    const VerifyRows r = verify_rows(a, seq + at);
+    const int chunks = (a.V + r.shift + kVerifyChunk - 1) / kVerifyChunk;
+    if (stale) {
+      upto = verify_runs(sums, chunks);
+      Z = from_lane(upto, 31);
     }
+    if (!(Z.hi > 0.f) && removed > 0) {
+      // nothing is left: the draft has as much everywhere.  The target's own
+      // weights then, summed by this warp alone
+      removed = 0;
+      A = none;
+#pragma unroll 1
+      for (int i = 0; i < chunks; ++i) {
+        const Pair z = verify_chunk_alone(a, &s, r, i, 0);
+        if (lane == 0) sums[i] = z;
+      }
+      __syncwarp();
+      upto = verify_runs(sums, chunks);
+      Z = from_lane(upto, 31);
+    }
+    if (Z.hi > 0.f && Z.hi < INFINITY)
+      token = verify_draw(a, &s, sums, r, A, removed, upto, times(Pair{u, 0.f}, Z));
     bad = token < 0;
   }
   for (int i = count + lane; i < a.A; i += 32) a.accept_idx[static_cast<size_t>(b) * a.A + i] = -1;
@@ -408,13 +544,18 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_tree_kernel(const Verif
     a.next_tokens[b] = token;
     if (bad) atomicOr(a.err, PKV_DEVERR_TREE);
   }
+  if (done) cluster_wait();
 }
 
 cudaError_t launch_verify_tree(const VerifyArgs& a, int num_sms, cudaStream_t stream) {
-  const int chunks = (a.V + kVerifyChunk - 1) / kVerifyChunk;
-  // CTAs a sequence: two for each SM in all, and no more than have chunks
+  const int chunks = (a.V + 3 + kVerifyChunk - 1) / kVerifyChunk;
+  // CTAs a sequence: up to four for each SM in all, and no more than have chunks
   int ranks = 1;
   while (ranks < kVerifyCluster && ranks * kVerifyWarps < chunks && 2 * ranks * static_cast<long long>(a.B) <= 4LL * num_sms) ranks *= 2;
+  if (ranks > 8) {
+    cudaError_t e = cudaFuncSetAttribute(verify_tree_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
@@ -424,7 +565,7 @@ cudaError_t launch_verify_tree(const VerifyArgs& a, int num_sms, cudaStream_t st
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(a.B) * ranks);
   cfg.blockDim = dim3(kVerifyThreads);
-  cfg.dynamicSmemBytes = sizeof(double) * static_cast<size_t>(chunks);
+  cfg.dynamicSmemBytes = sizeof(Pair) * static_cast<size_t>(chunks);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;

@@ -244,6 +244,14 @@ def test_stream_graph_and_prepared():
     assert torch.equal(b.kc[0, blk, :, off], a.kc[0, blk, :, off])
 
 
+def test_values_keep_their_bits():
+    c = Case(9610, 64, 4, 4, 128, 16)
+    c.v.view(torch.int16).copy_(torch.arange(-32768, 32768, 2, device=DEV).to(torch.int16).view(64, 4, 128))  # NaNs with payloads
+    c.call(_freq(128), True)
+    blk, off = torch.from_numpy(c.slots // 16).to(DEV), torch.from_numpy(c.slots % 16).to(DEV)
+    assert torch.equal(c.vc[0, blk, :, off].view(torch.int16), c.v.view(torch.int16))
+
+
 def test_empty_and_zero_rows():
     c = Case(9600, 4, 4, 2, 64, 16)
     empty = pkv.rope_append(c.q[:0], c.k[:0], c.v[:0], to_dev(c.pos[0, :0]), _freq(64), to_dev(c.slots[:0]), c.kc, c.vc)
