@@ -18,6 +18,10 @@ constexpr int kPackedPlanSmem = 1024;  // sequences whose sums are searched in s
 // Cost of an item besides its steps, in steps (tree_attend.cu).
 static int packed_item_steps(int kv_dtype, bool pair) { return pair ? 3 : kv_dtype == PKV_KV_BF16 ? 4 : 6; }
 
+// What a step of an item with one row tile costs where CTAs serve pairs of
+// tiles, of kPackedWeight.
+static int packed_alone(int kv_dtype) { return kv_dtype == PKV_KV_BF16 ? 6 : 5; }
+
 struct PackedPlanArgs {
   const int32_t* context_lens;
   const int32_t* query_starts;
@@ -31,7 +35,7 @@ struct PackedPlanArgs {
   __nv_bfloat16* out;
   unsigned* err;
   int B, N, T, Hkv, MB, NB, bs, words, row_bytes, e4m3;
-  int span, max_shares, min_steps, item_steps, row_elems /* Hq * D */;
+  int span, tile, alone, max_shares, min_steps, item_steps, row_elems /* Hq * D */;
 };
 
 // A sequence as the caller gives it, checked.
@@ -126,7 +130,7 @@ __global__ void __launch_bounds__(kPackedPlanThreads) packed_plan_kernel(const P
       const PackedSeq s = packed_seq(a, b, err);
       a.seqs[b] = s;
       if (fits) seq_s[b] = s;
-      cost = packed_cost(s, a.span, item_cost) * a.Hkv;
+      cost = packed_cost(s, a.span, item_cost) * packed_weight(s, a.tile, a.alone) * a.Hkv;
     }
     long long x = cost;
 #pragma unroll
@@ -166,7 +170,7 @@ __global__ void __launch_bounds__(kPackedPlanThreads) packed_plan_kernel(const P
   if (tid == 0) *a.shares = shares;
 #pragma unroll 1
   for (int s = tid; s <= shares; s += threads)
-    a.bounds[s] = packed_bound(s, shares, total, fits ? start_s : a.start, fits ? seq_s : a.seqs, a.B, a.Hkv, a.span, a.item_steps);
+    a.bounds[s] = packed_bound(s, shares, total, fits ? start_s : a.start, fits ? seq_s : a.seqs, a.B, a.Hkv, a.span, a.tile, a.alone, a.item_steps);
 }
 
 // ---------------------------------------------------------------------------
@@ -237,7 +241,7 @@ cudaError_t launch_packed_attend(const DecodeLaunch& L, uint8_t* ws, int* launch
   const PackedPlanArgs pa{L.context_lens, L.query_starts, L.block_tables, static_cast<const uint8_t*>(L.v_cache), seqs,
                           reinterpret_cast<long long*>(ws + w.start), bounds, shares, poison, static_cast<__nv_bfloat16*>(L.out), L.err,
                           L.B, L.N, L.T, L.Hkv, L.MB, L.NB, L.bs, words, L.D * (L.kv_fp8 ? 1 : 2), L.kv_dtype == PKV_KV_FP8_E4M3 ? 1 : 0,
-                          tiles * L.Tt, L.tree_shares, L.tree_min_steps, packed_item_steps(L.kv_dtype, pair), L.Hq * L.D};
+                          tiles * L.Tt, L.Tt, pair ? packed_alone(L.kv_dtype) : kPackedWeight, L.tree_shares, L.tree_min_steps, packed_item_steps(L.kv_dtype, pair), L.Hq * L.D};
   const int plan_threads = L.B <= 192 ? 192 : kPackedPlanThreads;
   const long long scans = static_cast<long long>(poison != nullptr ? L.Hkv : 1) * words;
   const int warps = plan_threads / 32;

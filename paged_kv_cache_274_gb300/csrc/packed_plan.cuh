@@ -43,9 +43,13 @@ PKV_PLAN_FN int packed_steps(int seen) { return (seen + kTreeTokens - 1) / kTree
 // than cached tokens, the first rows see none.
 PKV_PLAN_FN int packed_first(const PackedSeq& s, int span) { return s.ctx >= s.m ? 0 : (s.m - s.ctx) / span; }
 
-// Cost in tokens: what an item's last row sees, half a step of rounding, and
-// item_steps for its start and output.
+// Cost in tokens x kPackedWeight: what an item's last row sees, half a step of
+// rounding, and item_steps for its start and output.  The items of a sequence
+// whose rows fit one tile, where CTAs serve pairs of them, weigh `alone` in the
+// place of kPackedWeight: their steps take half of the products.
+constexpr int kPackedWeight = 8;
 PKV_PLAN_FN long long packed_item_cost(int item_steps) { return kTreeTokens * static_cast<long long>(item_steps) + kTreeTokens / 2; }
+PKV_PLAN_FN int packed_weight(const PackedSeq& s, int tile, int alone) { return s.m <= tile ? alone : kPackedWeight; }
 
 // Of the first x items of a KV head, as if the last run were full.
 PKV_PLAN_FN long long packed_before(const PackedSeq& s, long long x, int span, long long item_cost) {
@@ -53,7 +57,7 @@ PKV_PLAN_FN long long packed_before(const PackedSeq& s, long long x, int span, l
   return x * one + span * (x * (x - 1) / 2);
 }
 
-// Of a KV head of a sequence.
+// Of a KV head of a sequence, unweighted.
 PKV_PLAN_FN long long packed_cost(const PackedSeq& s, int span, long long item_cost) {
   if (s.ctx == 0 || s.m == 0) return 0;
   const int runs = packed_runs(s, span);
@@ -63,26 +67,27 @@ PKV_PLAN_FN long long packed_cost(const PackedSeq& s, int span, long long item_c
 // Shares of at least min_steps steps (never less than one: two boundaries in
 // one step would leave a share inside an item without steps).
 PKV_PLAN_FN int packed_share_count(long long total, int min_steps, int max_shares) {
-  const long long n = total / (static_cast<long long>(min_steps) * kTreeTokens);
+  const long long n = total / (static_cast<long long>(min_steps) * kTreeTokens * kPackedWeight);
   return total == 0 ? 0 : n < 1 ? 1 : static_cast<int>(n < max_shares ? n : max_shares);
 }
 
 // Start of share s (s == shares: the end).  start: the prefix sums of the
-// sequences' costs (all KV heads).  A boundary within `near` steps of an item's
+// sequences' weighted costs (all KV heads).  A boundary within `near` steps of an item's
 // start or end moves there.
 PKV_PLAN_FN PackedBound packed_bound(int s, int shares, long long total, const long long* start, const PackedSeq* seqs, int B, int Hkv,
-                                     int span, int item_steps) {
+                                     int span, int tile, int alone, int item_steps) {
   PackedBound r{B, 0, 0, 0};
   if (s >= shares) return r;
-  const long long apart = total / shares / (4 * kTreeTokens), item_cost = packed_item_cost(item_steps);
+  const long long apart = total / shares / (4 * kTreeTokens * kPackedWeight), item_cost = packed_item_cost(item_steps);
   const int near = apart < 2 ? static_cast<int>(apart) : 2;
   // (total * s may pass 64 bits)
   const long long pos = total / shares * s + total % shares * s / shares;
   r.b = tree_find(start, B, pos);
   const PackedSeq q = seqs[r.b];
+  const int weight = packed_weight(q, tile, alone);
   const long long cost = (start[r.b + 1] - start[r.b]) / Hkv, in = pos - start[r.b];
   r.kvh = static_cast<int>(in / cost);
-  const long long rest = in - r.kvh * cost;
+  const long long rest = (in - r.kvh * cost) / weight;
   const int first = packed_first(q, span), runs = packed_runs(q, span);
   int lo = 0, hi = runs - first - 1;  // the last item that starts at or before `rest`
 #pragma unroll 1

@@ -128,7 +128,7 @@ __host__ __device__ constexpr int ta_threads(int kv) { return kv == PKV_KV_BF16 
 // Registers a thread at the launch (65,536 / threads, a multiple of 8), and
 // after the warps have shared them out.
 __host__ __device__ constexpr int ta_launch_regs(int kv) { return kv == PKV_KV_BF16 ? 96 : 72; }
-__host__ __device__ constexpr int ta_role_regs(int kv) { return kv == PKV_KV_BF16 ? 48 : 40; }
+__host__ __device__ constexpr int ta_role_regs(int kv) { return kv == PKV_KV_BF16 ? 64 : 40; }
 __host__ __device__ constexpr int ta_soft_regs(int kv) {
   return (ta_threads(kv) * ta_launch_regs(kv) - (ta_threads(kv) - 512) * ta_role_regs(kv)) / 512 / 8 * 8;
 }
@@ -159,7 +159,7 @@ struct TaLayout {  // byte offsets from the 1024-aligned shared-memory base
   // streams: sums too); one tile: [stream][half][128] sums, [stream][128] m,
   // [stream] vref, apart because a stream may be in the next unit already
   static constexpr uint32_t kXml = kRing + kTaRing * kStep;
-  static constexpr uint32_t kQrow = kXml + 4 * kTaRows * 4 + (PAIR ? 0 : 6 * kTaRows * 4 + 16);
+  static constexpr uint32_t kQrow = kXml + 4 * kTaRows * 4 + 6 * kTaRows * 4 + 16;
   // one-byte caches: (2^kq, sum of q) per query row
   static constexpr uint32_t kEnd = kQrow + (kOneByte ? kQTiles * kTaRows * 8 : 0);
   static constexpr size_t kBytes = 1024 + kEnd;
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 8);  // one lane per warp of the stream
       mbar_init(&o_full[s], 1);
-      mbar_init(&o_free[s], PAIR ? 8 : 16);
+      mbar_init(&o_free[s], 16);
     }
     for (int s = 0; s < kTaRing; ++s) mbar_init(&step_full[s], 1);
     mbar_init(q_full, kOneByte ? kConvWarps : 1);
@@ -344,6 +344,9 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
   pdl_trigger();
   pdl_wait();
 
+  // Whether a unit has two row tiles: always with PAIR, but packed rows tell by
+  // their count (a sequence that decodes a token among prompts has one).
+  auto two_tiles = [&](int rows) { return PAIR && (!PACKED || rows > p.Tt); };
   const int share = blockIdx.x / p.NP, pair = blockIdx.x - share * p.NP;
   bool timed_out = false;
   uint32_t k_issued = 0, v_issued = 0, q_loads = 0, mma_issued = 0;  // for the drain after a timeout
@@ -628,9 +631,10 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         const int n = st->n, b = PACKED ? 0 : st->b, kvh = st->kvh;
         const int t0 = PACKED ? st->row0 : 2 * pair * p.Tt;
         if (n == 0) break;
-        if (lane == 0) mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(L::kQTiles * kHalves) * 128u * static_cast<uint32_t>(p.G * p.Tt));
+        const int tiles = two_tiles(PACKED ? st->rows : 0) ? 2 : 1;
+        if (lane == 0) mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(tiles * kHalves) * 128u * static_cast<uint32_t>(p.G * p.Tt));
         __syncwarp();
-        if (lane < L::kQTiles * kHalves) {  // rows past T are zero-filled
+        if (lane < tiles * kHalves) {  // rows past T are zero-filled
           const int i = lane / kHalves, half = lane % kHalves;
           tma_load_4d(sm + L::kQ + i * L::kTile + half * L::kRegion, &qmap, q_full, 64 * half, kvh * p.G, t0 + i * p.Tt, b);
         }
@@ -653,8 +657,9 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       // S_i = Q . K^T; A and B K-major with the 128-byte swizzle, 32 bytes of
       // each row per product.  (Loops of two products: the issuing thread's
       // code is fetched anew each step, between the softmax warps'.)
+      bool two = PAIR;  // of the unit
       auto issue_s = [&](int i, uint32_t stage) {
-        const uint64_t qd = q_desc + (PAIR ? i * (L::kTile >> 4) : 0u), kd = k_desc + stage * (L::kKTile >> 4);
+        const uint64_t qd = q_desc + (two ? i * (L::kTile >> 4) : 0u), kd = k_desc + stage * (L::kKTile >> 4);
         constexpr int kParts = kF8K ? 2 : kHalves;  // regions of the query: E4M3 both parts against the same codes
 #pragma unroll 1
         for (int h = 0; h < kParts; ++h) {
@@ -677,7 +682,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       auto issue_pv = [&](int i, bool first, uint32_t iu) -> bool {
         if (!ta_wait(&p_full[i], pc[i] & 1u)) return false;
         ++pc[i];
-        if ((!PAIR || i == 0) && !ta_wait(&v_full[vs], vph)) return false;
+        if ((!two || i == 0) && !ta_wait(&v_full[vs], vph)) return false;
         if (first && iu > 0 && !ta_wait(&o_free[i], (iu - 1) & 1u)) return false;
         tc_fence_after_sync();
         const uint64_t vd = v_desc + vs * (L::kTile >> 4);
@@ -688,7 +693,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             tc_mma_bf16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 64u * h + 8u * kk, vd + (h * 4 + kk) * (2048 >> 4), kIdescO,
                            !first || h > 0 || kk > 0);
         ++mma_issued;
-        if (!PAIR || i == 1) {
+        if (!two || i == 1) {
           tc_commit(&v_free[vs]);
           if (++vs == VS) {
             vs = 0;
@@ -704,16 +709,17 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         const int n = step_at(g0)->n;
         if (n == 0) break;
         if (!(ok = ta_wait(q_full, iu & 1u))) break;
-        const int events = PAIR ? 2 * n : n;
+        if constexpr (PAIR && PACKED) two = two_tiles(step_at(g0)->rows);
+        const int events = two ? 2 * n : n;
 #pragma unroll 1
         for (int e = 0; ok && e < events; ++e) {
           const int i = e & 1, k = e >> 1;  // stream, its step
           if (k > 0 && !(ok = issue_pv(i, k == 1, iu))) break;
-          if ((!PAIR || i == 0) && !(ok = ta_wait(&k_full[ks], kph))) break;
+          if ((!two || i == 0) && !(ok = ta_wait(&k_full[ks], kph))) break;
           tc_fence_after_sync();
           issue_s(i, ks);
           tc_commit(&s_full[i]);
-          if (!PAIR || i == 1) {
+          if (!two || i == 1) {
             tc_commit(&k_free[ks]);
             if (++ks == KS) {
               ks = 0;
@@ -725,8 +731,8 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         // the last products of both streams, the earlier step's first
 #pragma unroll 1
         for (int x = 0; ok && x < 2; ++x) {
-          const int i = (!PAIR && (n & 1)) ? 1 - x : x;
-          const int ni = PAIR ? n : (n + 1 - i) / 2;  // the stream's steps
+          const int i = (!two && (n & 1)) ? 1 - x : x;
+          const int ni = two ? n : (n + 1 - i) / 2;  // the stream's steps
           if (ni == 0) continue;
           if (!(ok = issue_pv(i, ni == 1, iu))) break;
           tc_commit(&o_full[i]);
@@ -790,7 +796,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         float2* qrow = reinterpret_cast<float2*>(sm + L::kQrow);
         const int r = kRows * cw + (lane & 15), half = lane >> 4;
 #pragma unroll 1
-        for (int i = 0; i < L::kQTiles; ++i) {
+        for (int i = 0; i < (two_tiles(rows_here) ? 2 : 1); ++i) {
           const int tl = r / p.G, t = (2 * pair + i) * p.Tt + tl;
           const bool in = tl < p.Tt && t < rows_here;
           const uint4* src = reinterpret_cast<const uint4*>(
@@ -892,71 +898,42 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
     const uint32_t t_s = tmem + lane_base + 128u * i;
     const uint32_t t_o = tmem + lane_base + 256u;  // O0; O1 is 128 columns on
     const float c = p.scale_log2;
-    const int tile = PAIR ? 2 * pair + i : 0;
-    const int tl = r / p.G, t = tile * p.Tt + tl;  // packed: row of the item
-    bool in_tile = tl < p.Tt && t < p.T;
-    // warps without rows only keep the barriers' counts and clear stale V rows
-    bool warp_dead = !__any_sync(kFull, in_tile);
+    const int tl = r / p.G;
     float* xch = reinterpret_cast<float*>(sm + L::kXml);
     float* x_mine = xch + (2 * i + hh) * kTaRows + r;
     const float* x_other = xch + (2 * i + (hh ^ 1)) * kTaRows + r;
-    uint32_t g0 = 0, steps = 0, units1 = 0;  // steps of this stream, units with a step for stream 1
+    uint32_t g0 = 0, steps = 0, units1 = 0, alone = 0;  // steps of this stream, units with a step for stream 1, of one tile
     // A wait of this warp gave up: it waits for nothing more, and leaves with
     // the warp that shares its rows, at their next barrier
     bool fail = false, left = false;
-    for (uint32_t iu = 0;; ++iu) {
-      if (!wait_step(g0)) fail = true;
-      if (bar_red_or(pair_bar, 64, fail)) {
-        fail = true;
-        break;
-      }
-      int n, b, kvh, t0, t1, part, base, mrow, prow, row_state;
-      [[maybe_unused]] int row0 = 0, seen = 0, item0 = 0;  // packed: the item's first row, what the row sees, the first row's position
-      {
-        const volatile TaStep* st = step_at(g0);
-        n = st->n;
-        if (n == 0) break;
-        b = st->b;
-        kvh = st->kvh;
-        t0 = st->t0;
-        t1 = st->t1;
-        part = st->part;
-        if constexpr (PACKED) {
-          row0 = st->row0;
-          item0 = st->seen0 - 1;
-          seen = st->seen0 + t;
-          base = st->base;
-          in_tile = tl < p.Tt && t < st->rows;
-          warp_dead = !__any_sync(kFull, in_tile);
-          mrow = -1;
-          prow = kvh * p.tree.words;
-          row_state = in_tile ? kTreeRowNormal : kTreeRowZero;
-        } else {
-          const int nodes = p.tree.node_counts != nullptr ? __ldg(p.tree.node_counts + b) : p.T;
-          base = st->ctx - nodes;
-          const bool live = in_tile && t < nodes;
-          mrow = live ? b * p.tree.stride + t * p.tree.words : -1;
-          prow = (b * p.Hkv + kvh) * p.tree.words;
-          row_state = live ? kTreeRowNormal : kTreeRowZero;
-        }
-      }
+    // Unit iu of n steps, with one or two row tiles (apart, so that neither's
+    // steps pay registers for the other); false: this warp leaves.
+    auto unit = [&](auto tiles, uint32_t iu, int n) -> bool {
+      constexpr bool two = decltype(tiles)::value == 2;
+      // (Everything but this is read again where it is needed, in a masked step
+      // or at the unit's end: registers are what the steps are short of.)
+      const int t = (PACKED ? (two ? i * p.Tt : 0) : (two ? 2 * pair + i : 0) * p.Tt) + tl;  // packed: row of the item
+      const bool in_tile = tl < p.Tt && t < (PACKED ? const_cast<const volatile TaStep*>(step_at(g0))->rows : p.T);
+      // the row is of the unit; it attends to a V row that is not finite
+      bool row_live = in_tile, row_nan = false;
+      if constexpr (!PACKED) row_live = in_tile && t < (p.tree.node_counts != nullptr ? __ldg(p.tree.node_counts + step_at(g0)->b) : p.T);
+      // warps without rows only keep the barriers' counts and clear stale V rows
+      const bool warp_dead = !__any_sync(kFull, in_tile);
       float cq = c, qsum = 0.f, vref = 1.f;
       if constexpr (kOneByte) {
         if (!fail && !warp_wait(q_full, iu & 1u)) fail = true;
-        const float2 qr = reinterpret_cast<const float2*>(sm + L::kQrow)[(PAIR ? i * kTaRows : 0) + r];
+        const float2 qr = reinterpret_cast<const float2*>(sm + L::kQrow)[(two ? i * kTaRows : 0) + r];
         cq = c * qr.x;
         qsum = qr.y;
         __syncwarp();
         if (lane == 0) mbar_arrive(q_read);
       }
       float m = -INFINITY, l = 0.f;  // log2-domain lazy running maximum of the row, sum of this half
-      const int ni = PAIR ? n : (n + 1 - i) / 2;  // this stream's steps
+      const int ni = two ? n : (n + 1 - i) / 2;  // this stream's steps
 #pragma unroll 1
       for (int k = 0; k < ni; ++k, ++steps) {
-        const int j = PAIR ? k : 2 * k + i;
+        const int j = two ? k : 2 * k + i;
         const uint32_t g = g0 + j;
-        const int pos0 = t0 + j * kTreeTokens;
-        const int nvs = t1 - pos0;  // tokens of the step in the sequence
         if (!fail && !ta_wait(&step_full[g % kTaRing], (g / kTaRing) & 1u)) fail = true;
         const TaStep* st = const_cast<const TaStep*>(step_at(g));
         const int flags = *reinterpret_cast<const volatile int*>(&st->flags);
@@ -964,27 +941,40 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         uint64_t rm = ~0ull;                             // this half's tokens that the row attends to
         // (rows past the sequence's nodes attend to every token before them
         // too: their output is zero whatever they attend to)
+        int nvs = kTreeTokens;  // tokens of the step in the sequence
         if (flags & kStepMasked) {
+          const volatile TaStep* sv = st;
+          const int pos0 = sv->t0 + j * kTreeTokens;
+          nvs = sv->t1 - pos0;
           badw = PPI == 8 ? *reinterpret_cast<const volatile uint64_t*>(st->bad) : *reinterpret_cast<const volatile uint32_t*>(st->bad);
-          const bool nodes_here = pos0 + kTreeTokens > base;
-          if (nodes_here && p.tree.poison != nullptr) {
-            if constexpr (PACKED) {  // (a bit per row of q; those before `base` are other sequences')
-              bad0 = tree_window64(p.tree.poison + prow, p.tree.words, row0 + pos0 - item0) & ~low_bits64(base - pos0);
-              bad1 = tree_window64(p.tree.poison + prow, p.tree.words, row0 + pos0 - item0 + 64) & ~low_bits64(base - pos0 - 64);
-            } else {
-              bad0 = tree_window64(p.tree.poison + prow, p.tree.words, pos0 - base);
-              bad1 = tree_window64(p.tree.poison + prow, p.tree.words, pos0 - base + 64);
+          uint64_t see;
+          if constexpr (PACKED) {
+            const int base = sv->base, seen0 = sv->seen0;
+            if (pos0 + kTreeTokens > base && p.tree.poison != nullptr) {  // (a bit per row of q; those before `base` are other sequences')
+              const uint32_t* bits = p.tree.poison + sv->kvh * p.tree.words;
+              const int u0 = sv->row0 + pos0 - (seen0 - 1);
+              bad0 = tree_window64(bits, p.tree.words, u0) & ~low_bits64(base - pos0);
+              bad1 = tree_window64(bits, p.tree.words, u0 + 64) & ~low_bits64(base - pos0 - 64);
             }
+            see = low_bits64(seen0 + t - pos0 - 64 * hh);
+          } else {
+            const int b = sv->b, base = sv->ctx - (p.tree.node_counts != nullptr ? __ldg(p.tree.node_counts + b) : p.T);
+            const bool nodes_here = pos0 + kTreeTokens > base;
+            if (nodes_here && p.tree.poison != nullptr) {
+              const uint32_t* bits = p.tree.poison + (b * p.Hkv + sv->kvh) * p.tree.words;
+              bad0 = tree_window64(bits, p.tree.words, pos0 - base);
+              bad1 = tree_window64(bits, p.tree.words, pos0 - base + 64);
+            }
+            see = low_bits64(base - pos0 - 64 * hh);
+            if (nodes_here && row_live) see |= tree_window64(p.tree.mask + b * p.tree.stride + t * p.tree.words, p.tree.words, pos0 - base + 64 * hh);
           }
           rm = low_bits64(nvs - 64 * hh);
 #pragma unroll
           for (int q = 0; q < PPI / 2; ++q)
             if ((badw >> (8 * (q + hh * (PPI / 2)))) & 0xffu) rm &= ~(((1ull << BS) - 1ull) << (q * BS));
-          uint64_t see = low_bits64((PACKED ? seen : base) - pos0 - 64 * hh);
-          if (!PACKED && nodes_here && mrow >= 0) see |= tree_window64(p.tree.mask + mrow, p.tree.words, pos0 - base + 64 * hh);
           rm &= see;
           const uint64_t badh = hh ? bad1 : bad0;
-          if ((rm & badh) && row_state == kTreeRowNormal) row_state = kTreeRowNan;
+          if (rm & badh) row_nan = true;
           rm &= ~badh;
         }
         bool vgrow = false;
@@ -1033,10 +1023,12 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             tc_wait_st();
           }
           uint32_t x0[32], x1[32];
-          tc_ld32(t_h, x0);
-          tc_ld32(t_h + 32u, x1);
-          tc_wait_ld_regs(x0);
-          tc_regs_loaded(x1);
+          if constexpr (kOneByte) {
+            tc_ld32(t_h, x0);
+            tc_ld32(t_h + 32u, x1);
+            tc_wait_ld_regs(x0);
+            tc_regs_loaded(x1);
+          }
           // coefficients of the scores of page h of the half's 32 tokens c32:
           // a score in log2 units is x ck + add, P x v scale / vref is
           // 2^(score - m + lv)
@@ -1062,16 +1054,25 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
               return fmaxf(e0, fmaf(max16(x, 16), ck, add));
             }
           };
-          float smax = fmaxf(ext32(x0, 0), ext32(x1, 1));
-          // lazy maximum: moved when the row's exceeds it by more than 2^8
-          const bool want = m == -INFINITY ? smax != -INFINITY : smax > m + 8.f;
-          bool grow = false;
-          if (bar_red_or(pair_bar, 64, want || fail)) {
-            *x_mine = smax;
-            if (bar_red_or(pair_bar, 64, fail)) {
-              fail = left = true;
-              break;
+          float smax = -INFINITY;
+          if constexpr (kOneByte) {
+            smax = fmaxf(ext32(x0, 0), ext32(x1, 1));
+          } else if (k == 0) {  // (32 at a time: these registers are not kept)
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+              uint32_t y[32];
+              tc_ld32(t_h + 32u * q, y);
+              tc_wait_ld_regs(y);
+              smax = fmaxf(smax, ext32(y, q));
             }
+          }
+          // lazy maximum: moved when the row's exceeds it by more than 2^8
+          auto wants = [&]() { return m == -INFINITY ? smax != -INFINITY : smax > m + 8.f; };
+          bool grow = false;
+          // the two warps' new maximum; false: one of them gave up
+          auto agree = [&]() -> bool {
+            *x_mine = smax;
+            if (bar_red_or(pair_bar, 64, fail)) return false;
             smax = fmaxf(smax, *x_other);
             grow = m == -INFINITY ? smax != -INFINITY : smax > m + 8.f;
             if (grow) {
@@ -1081,8 +1082,13 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
               m = smax;
             }
             __syncwarp();
+            return true;
+          };
+          if ((kOneByte || k == 0) && bar_red_or(pair_bar, 64, wants() || fail) && !agree()) {
+            fail = left = true;
+            break;
           }
-          const float neg_m = (m == -INFINITY) ? 0.f : -m;
+          float neg_m = (m == -INFINITY) ? 0.f : -m;
           float ps0 = 0.f, ps1 = 0.f;
           auto write_p = [&](const uint32_t (&x)[32], int c32) {
             float ck = c_u, add = 0.f, lv = 0.f;
@@ -1122,8 +1128,50 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
               tc_wait_ld_regs(x1);
               write_p(x1, 1);
             } else {
-              write_p(x0, 0);
-              write_p(x1, 1);
+              // After a unit's first step the exponentials are made while the
+              // warps have yet to agree that the maximum stays (and the scores'
+              // second half is on its way), and made again where it does not.
+              auto exps = [&](const uint32_t* x, uint32_t* pw, int pairs) {
+#pragma unroll
+                for (int e = 0; e < pairs; ++e) {
+                  float a0, a1;
+                  ffma2(a0, a1, __uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), c_u, c_u, neg_m, neg_m);
+                  const float p0 = ex2_approx(a0);
+                  const float p1 = ex2_approx(a1);
+                  fadd2(ps0, ps1, ps0, ps1, p0, p1);
+                  pw[e] = pack_bf16x2(p0, p1);
+                }
+              };
+              uint32_t pw[32];
+              tc_ld32(t_h, x0);
+              tc_wait_ld_regs(x0);
+              tc_ld32(t_h + 32u, x1);
+              exps(x0, pw, 16);
+              smax = ext32(x0, 0);
+              tc_wait_ld_regs(x1);
+              exps(x1, pw + 16, 16);
+              smax = fmaxf(smax, ext32(x1, 1));
+              const bool again = k > 0 && bar_red_or(pair_bar, 64, wants() || fail);
+              if (again) {
+                if (!agree()) {
+                  fail = left = true;
+                  break;
+                }
+                neg_m = (m == -INFINITY) ? 0.f : -m;
+                ps0 = ps1 = 0.f;
+              } else {
+                tc_st32(t_h, pw);
+              }
+              if (again) {
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {  // (P covers only columns that are done with)
+                  uint32_t y[16], pq[8];
+                  tc_ld16(t_h + 16u * q, y);
+                  tc_wait_ld_regs16(y);
+                  exps(y, pq, 8);
+                  tc_st8(t_h + 8u * q, pq);
+                }
+              }
               l += ps0 + ps1;
             }
           } else {
@@ -1187,23 +1235,24 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[i]);
       }
-      if (left) break;
+      if (left) return false;
 
       // the unit's output: O / l as bf16, or a partial (m, l, O)
       // a row that attends to a node with a non-finite V row is NaN in every
       // column, also those that other warps write: through its sum
-      if (row_state == kTreeRowNan) l = tree_row_value(kTreeRowNan);
-      if (row_state == kTreeRowZero) {  // whatever its query held
+      if (row_nan) l = tree_row_value(kTreeRowNan);
+      if (!row_live) {  // whatever its query held
         m = -INFINITY;
         l = 0.f;
       }
       float f0 = kOneByte ? vref : 1.f, f1 = 0.f;
-      if constexpr (PAIR) {
-        if (!fail && !warp_wait(&o_full[i], iu & 1u)) fail = true;
+      if constexpr (two) {
+        if (!fail && !warp_wait(&o_full[i], (i == 0 ? iu : units1) & 1u)) fail = true;
+        ++units1;
         *x_mine = l;
         if (bar_red_or(pair_bar, 64, fail)) {
           fail = true;
-          break;
+          return false;
         }
         l += *x_other;
       } else {
@@ -1222,10 +1271,10 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         if (kOneByte && hh == 0 && r == 0) xv[i] = vref;
         __syncwarp();
         if (lane == 0) mbar_arrive(x_full);
-        if (!fail && !warp_wait(x_full, iu & 1u)) fail = true;
+        if (!fail && !warp_wait(x_full, alone++ & 1u)) fail = true;
         if (bar_red_or(pair_bar, 64, fail)) {
           fail = true;
-          break;
+          return false;
         }
         const float m0 = xm[r], m1 = xm[kTaRows + r];
         const float l0 = xl[r] + xl[kTaRows + r], l1 = xl[2 * kTaRows + r] + xl[3 * kTaRows + r];
@@ -1240,62 +1289,113 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       }
       tc_fence_after_sync();
       if (!warp_dead) {
-        const int h = kvh * p.G + (r - tl * p.G);
-        const size_t qrow = static_cast<size_t>(PACKED ? row0 + t : b * p.T + t) * p.Hq + h;
-        const size_t prow_o = (static_cast<size_t>(blockIdx.x) * 2 + (part - 1)) * (L::kQTiles * kTaRows) + (PAIR ? i * kTaRows : 0) + r;
+        // (the last step's descriptor is still there: the copies are at most the
+        // K stages and two steps ahead of the products, which wait for o_free)
+        const volatile TaStep* st = step_at(g0 + static_cast<uint32_t>(n) - 1u);
+        const int part = st->part;
+        const int first = PACKED ? st->row0 : st->b * p.T;
+        const int row_out = (first + t) * p.Hq + st->kvh * p.G + (r - tl * p.G);  // (rows x heads x head_dim is below 2^31)
+        const size_t part0 = (static_cast<size_t>(blockIdx.x) * 2 + (part - 1)) * (L::kQTiles * kTaRows) + (two ? i * kTaRows : 0);
         if (part == 0) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           f0 *= inv;
           f1 *= inv;
         }
-        // a pair's warp: half of its tile's columns; else a quarter of the one tile's
-        constexpr int kCols = PAIR ? D / 2 : D / 4;
-        const int c0 = (PAIR ? hh : 2 * i + hh) * kCols;
-#pragma unroll 1
-        for (int cc = c0; cc < c0 + kCols; cc += 16) {
+        // O's columns cc .. cc + 15 of the row, joined over the streams
+        auto columns = [&](int cc, float (&o)[16]) {
           uint32_t ov[16], o1[16];
-          tc_ld16(t_o + (PAIR ? 128u * i : 0u) + cc, ov);
-          if constexpr (!PAIR) {  // (O1 of a unit with one step holds anything)
-            tc_ld16(t_o + 128u + cc, o1);
-          }
+          tc_ld16(t_o + (two ? 128u * i : 0u) + cc, ov);
+          if (!two) tc_ld16(t_o + 128u + cc, o1);  // (O1 of a unit with one step holds anything)
           tc_wait_ld_regs16(ov);
-          if constexpr (!PAIR) tc_regs_loaded16(o1);
+          if (!two) tc_regs_loaded16(o1);
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
             float a, b2;
             fmul2(a, b2, __uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), f0, f0);
-            if constexpr (!PAIR) {
+            if (!two) {
               const float z0 = n > 1 ? __uint_as_float(o1[e]) : 0.f, z1 = n > 1 ? __uint_as_float(o1[e + 1]) : 0.f;
               a = fmaf(z0, f1, a);
               b2 = fmaf(z1, f1, b2);
             }
-            ov[e] = row_state == kTreeRowZero ? 0u : __float_as_uint(a);
-            ov[e + 1] = row_state == kTreeRowZero ? 0u : __float_as_uint(b2);
+            o[e] = row_live ? a : 0.f;
+            o[e + 1] = row_live ? b2 : 0.f;
           }
-          if (in_tile) {
-            if (part == 0) {
-              uint4* dst = reinterpret_cast<uint4*>(p.out + qrow * D + cc);
+        };
+        // A lane's row is 64 bytes here, four chunks: four lanes exchange theirs,
+        // so that they store a row's 64 bytes side by side, row by row (with 16
+        // bytes of 32 rows a store, the LSU took 4000 cycles for two tiles).
+        const int quad = lane & 3;
+        auto turn_chunks = [&](uint32_t (&w)[16]) {
 #pragma unroll
-              for (int c8 = 0; c8 < 2; ++c8) {
-                const float* f = reinterpret_cast<const float*>(ov + 8 * c8);
-                dst[c8] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+          for (int x = 1; x <= 2; x *= 2)
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+              if (ch & x) continue;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t& lo = w[4 * ch + e];
+                uint32_t& hi = w[4 * (ch | x) + e];
+                const uint32_t got = __shfl_xor_sync(kFull, (quad & x) ? lo : hi, x);
+                if (quad & x) lo = got; else hi = got;
               }
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow_o * D + cc);
-#pragma unroll
-              for (int c4 = 0; c4 < 4; ++c4) dst[c4] = make_uint4(ov[4 * c4], ov[4 * c4 + 1], ov[4 * c4 + 2], ov[4 * c4 + 3]);
             }
+        };
+        int rows4[4];  // where the four rows go (-1: not in the unit)
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) rows4[ch] = __shfl_sync(kFull, in_tile ? (part == 0 ? row_out : r) : -1, (lane & ~3) + ch);
+        // a pair's warp: half of its tile's columns; else a quarter of the one
+        // tile's (head_dim 64: the first stream's warps a half)
+        const int cols = two ? D / 2 : (D == 64 ? 32 : D / 4), c0 = (two ? hh : 2 * i + hh) * cols;
+#pragma unroll 1
+        for (int cc = c0; cc < min(c0 + cols, D); cc += part == 0 ? 32 : 16) {
+          uint32_t w[16];
+          float o[16];
+          columns(cc, o);
+          if (part == 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+            columns(cc + 16, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[8 + e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e]);
           }
+          turn_chunks(w);
+          uint8_t* dst = part == 0 ? reinterpret_cast<uint8_t*>(p.out + cc) : reinterpret_cast<uint8_t*>(p.part_o + part0 * D + cc);
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch)
+            if (rows4[ch] >= 0)
+              *reinterpret_cast<uint4*>(dst + static_cast<size_t>(rows4[ch]) * (part == 0 ? 2 * D : 4 * D) + 16 * quad) =
+                  make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
           __syncwarp();  // the next TMEM load is warp-collective
         }
-        if (in_tile && part != 0 && hh == 0 && (PAIR || i == 0)) p.part_ml[prow_o] = make_float2(m, l);
+        if (in_tile && part != 0 && hh == 0 && (two || i == 0)) p.part_ml[part0 + r] = make_float2(m, l);
       }
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&o_free[i]);
-        if (!PAIR) mbar_arrive(&o_free[1 - i]);
+        mbar_arrive(&o_free[two ? i : 1 - i]);
       }
+      return true;
+    };
+    for (uint32_t iu = 0;; ++iu) {
+      if (!wait_step(g0)) fail = true;
+      if (bar_red_or(pair_bar, 64, fail)) {
+        fail = true;
+        break;
+      }
+      const volatile TaStep* st = step_at(g0);
+      const int n = st->n;
+      if (n == 0) break;
+      bool go;
+      if constexpr (PAIR && PACKED) {
+        go = two_tiles(st->rows) ? unit(std::integral_constant<int, 2>{}, iu, n) : unit(std::integral_constant<int, 1>{}, iu, n);
+      } else {
+        go = unit(std::integral_constant<int, PAIR ? 2 : 1>{}, iu, n);
+      }
+      if (!go) break;
       g0 += static_cast<uint32_t>(n);
     }
     if (fail) timed_out = true;

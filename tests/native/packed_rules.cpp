@@ -22,7 +22,8 @@ extern "C" {
 //   6  a bound names no item, or a step outside it
 //   7  a unit has no steps
 //   8  more shares, or places of a share, than the workspace has
-int packed_shares_check(const int* ctx, const int* m, int B, int Hkv, int span, int item_steps, int min_steps, int max_shares, int* what) {
+int packed_shares_check(const int* ctx, const int* m, int B, int Hkv, int span, int tile, int alone, int item_steps, int min_steps, int max_shares,
+                        int* what) {
   std::vector<PackedSeq> seqs(B + 1);
   int row = 0;
   for (int b = 0; b < B; ++b) {
@@ -31,7 +32,7 @@ int packed_shares_check(const int* ctx, const int* m, int B, int Hkv, int span, 
   }
   std::vector<long long> start(B + 1, 0);
   const long long item_cost = packed_item_cost(item_steps);
-  for (int b = 0; b < B; ++b) start[b + 1] = start[b] + packed_cost(seqs[b], span, item_cost) * Hkv;
+  for (int b = 0; b < B; ++b) start[b + 1] = start[b] + packed_cost(seqs[b], span, item_cost) * packed_weight(seqs[b], tile, alone) * Hkv;
   const long long total = start[B];
   const int shares = packed_share_count(total, min_steps, max_shares);
   what[0] = shares;
@@ -45,7 +46,7 @@ int packed_shares_check(const int* ctx, const int* m, int B, int Hkv, int span, 
   if (shares > max_shares) say(8, 0, 0, 0, 0);
   std::vector<PackedBound> bounds(shares + 1);
   for (int s = 0; s <= shares; ++s) {
-    bounds[s] = packed_bound(s, shares, total, start.data(), seqs.data(), B, Hkv, span, item_steps);
+    bounds[s] = packed_bound(s, shares, total, start.data(), seqs.data(), B, Hkv, span, tile, alone, item_steps);
     const PackedBound& x = bounds[s];
     if (x.b < B) {
       const PackedSeq& q = seqs[x.b];

@@ -22,11 +22,11 @@ def rules(tmp_path_factory):
     return ctypes.CDLL(so)
 
 
-def shares(rules, ctx, m, Hkv, span, item_steps=3, min_steps=1, max_shares=152):
+def shares(rules, ctx, m, Hkv, span, item_steps=3, min_steps=1, max_shares=152, alone=8):
     ctx, m = np.ascontiguousarray(ctx, np.int32), np.ascontiguousarray(m, np.int32)
     what = np.full(8, -1, np.int32)
-    fault = rules.packed_shares_check(ctypes.c_void_p(ctx.ctypes.data), ctypes.c_void_p(m.ctypes.data), len(ctx), Hkv, span, item_steps,
-                                      min_steps, max_shares, ctypes.c_void_p(what.ctypes.data))
+    fault = rules.packed_shares_check(ctypes.c_void_p(ctx.ctypes.data), ctypes.c_void_p(m.ctypes.data), len(ctx), Hkv, span, span if alone == 8 else (span + 1) // 2, alone,
+                                      item_steps, min_steps, max_shares, ctypes.c_void_p(what.ctypes.data))
     return fault, what.tolist()
 
 
@@ -47,8 +47,9 @@ def test_parts_are_read_where_they_were_written(rules, B, most_new, most_before,
         if m.sum() / span * Hkv > 20000:
             span = 256
         item, least, most = int(rng.choice([3, 4, 6])), int(rng.choice([1, 1, 2, 8, 31])), int(rng.choice([152, 152, 76, 9, 1]))
-        fault, what = shares(rules, ctx, m, Hkv, span, item, least, most)
-        assert fault == 0, (fault, what, ctx.tolist(), m.tolist(), span, item, least, most)
+        alone = int(rng.choice([8, 8, 6, 4, 1]))
+        fault, what = shares(rules, ctx, m, Hkv, span, item, least, most, alone)
+        assert fault == 0, (fault, what, ctx.tolist(), m.tolist(), span, item, least, most, alone)
         joined += what[1]
     assert joined > 0 or most_new + most_before < 640  # (items of four steps are not split)
 
