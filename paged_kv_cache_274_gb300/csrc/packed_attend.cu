@@ -15,8 +15,13 @@ namespace pkv {
 constexpr int kPackedPlanThreads = 1024;
 constexpr int kPackedPlanSmem = 1024;  // sequences whose sums are searched in shared memory
 
-// Cost of an item besides its steps, in steps (tree_attend.cu).
-static int packed_item_steps(int kv_dtype, bool pair) { return pair ? 3 : kv_dtype == PKV_KV_BF16 ? 4 : 6; }
+// Cost of an item besides its steps, in steps (tree_attend.cu).  Pairs of tiles,
+// measured: bf16 2 (head_dim 64: 4, 163 instead of 173 us for ragged prompts with
+// 2), E4M3 6 (377 us; 3: 429, 12: 384), INT8 9 (113 us; 3: 119, 12: 116).
+static int packed_item_steps(int kv_dtype, int D, bool pair) {
+  if (kv_dtype == PKV_KV_BF16) return pair && D == 128 ? 2 : 4;
+  return !pair || kv_dtype == PKV_KV_FP8_E4M3 ? 6 : 9;
+}
 
 // What a step of an item with one row tile costs where CTAs serve pairs of
 // tiles, of kPackedWeight.
@@ -210,6 +215,7 @@ PackedWorkspace packed_workspace(int B, int N, int Hkv, int D, int tiles, int ma
   w.seqs = take(sizeof(PackedSeq) * static_cast<size_t>(B));
   w.start = take(sizeof(long long) * (static_cast<size_t>(B) + 1));
   w.bounds = take(sizeof(PackedBound) * (static_cast<size_t>(max_shares) + 1));
+  w.merge = take(sizeof(PackedMerge) * static_cast<size_t>(max_shares));
   w.poison = take(sizeof(uint32_t) * static_cast<size_t>(Hkv) * ((static_cast<size_t>(N) + 31) / 32));
   w.part_ml = take(sizeof(float2) * rows);
   w.part_o = take(sizeof(float) * D * rows);
@@ -241,7 +247,7 @@ cudaError_t launch_packed_attend(const DecodeLaunch& L, uint8_t* ws, int* launch
   const PackedPlanArgs pa{L.context_lens, L.query_starts, L.block_tables, static_cast<const uint8_t*>(L.v_cache), seqs,
                           reinterpret_cast<long long*>(ws + w.start), bounds, shares, poison, static_cast<__nv_bfloat16*>(L.out), L.err,
                           L.B, L.N, L.T, L.Hkv, L.MB, L.NB, L.bs, words, L.D * (L.kv_fp8 ? 1 : 2), L.kv_dtype == PKV_KV_FP8_E4M3 ? 1 : 0,
-                          tiles * L.Tt, L.Tt, pair ? packed_alone(L.kv_dtype) : kPackedWeight, L.tree_shares, L.tree_min_steps, packed_item_steps(L.kv_dtype, pair), L.Hq * L.D};
+                          tiles * L.Tt, L.Tt, pair ? packed_alone(L.kv_dtype) : kPackedWeight, L.tree_shares, L.tree_min_steps, packed_item_steps(L.kv_dtype, L.D, pair), L.Hq * L.D};
   const int plan_threads = L.B <= 192 ? 192 : kPackedPlanThreads;
   const long long scans = static_cast<long long>(poison != nullptr ? L.Hkv : 1) * words;
   const int warps = plan_threads / 32;
@@ -277,6 +283,7 @@ cudaError_t launch_packed_attend(const DecodeLaunch& L, uint8_t* ws, int* launch
   p.scale_log2 = L.scale_log2;
   p.seqs = seqs;
   p.pbounds = bounds;
+  p.merge = reinterpret_cast<PackedMerge*>(ws + w.merge);
   CUtensorMap kmap = L.kmap, vmap = L.vmap, qmap = L.qmap;
   void* args[] = {&kmap, &vmap, &qmap, &p};
   cfg.gridDim = dim3(static_cast<unsigned>(L.tree_shares));
@@ -291,12 +298,14 @@ cudaError_t launch_packed_attend(const DecodeLaunch& L, uint8_t* ws, int* launch
 
   // 3. merge of the items that shares split
   if (L.tree_shares > 1) {
-    const TreeMergeArgs ma{nullptr, bounds, seqs, shares, p.part_ml, p.part_o, p.out, L.Hq, L.G, L.T, L.Tt, 1, tiles};
-    cfg.gridDim = dim3(static_cast<unsigned>((L.tree_shares - 1) * (tiles * kTaRows / kTreeMergeCta)));
+    const TreeMergeArgs ma{nullptr, p.merge, shares, p.part_ml, p.part_o, p.out, L.Hq, L.G, L.T, L.Tt, 1, tiles};
+    cfg.gridDim = dim3(static_cast<unsigned>((L.tree_shares - 1) * (tiles * kTaRows / merge_cta_rows(2 * tiles))));
     cfg.blockDim = dim3(kTreeMergeThreads);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = (L.ev_end == nullptr) ? 1 : 0;
-    e = L.D == 64 ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<64, true>, ma) : cudaLaunchKernelEx(&cfg, tree_merge_kernel<128, true>, ma);
+    auto merge = pair ? (L.D == 64 ? tree_merge_kernel<64, true, 4> : tree_merge_kernel<128, true, 4>)
+                      : (L.D == 64 ? tree_merge_kernel<64, true, 2> : tree_merge_kernel<128, true, 2>);
+    e = cudaLaunchKernelEx(&cfg, merge, ma);
     if (e != cudaSuccess) return e;
     *launched += 1;
   }

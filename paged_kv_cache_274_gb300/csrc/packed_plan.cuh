@@ -115,6 +115,16 @@ PKV_PLAN_FN PackedBound packed_bound(int s, int shares, long long total, const l
 
 PKV_PLAN_FN bool packed_same_item(const PackedBound& x, const PackedBound& y) { return x.b == y.b && x.kvh == y.kvh && x.run == y.run; }
 
+// What the merge joins in a share's name (of the share in which the item starts).
+struct PackedMerge {
+  int parts;   // 0: nothing
+  int place;   // of the share's own part; the others' are their first units'
+  int row0;    // first row of the item
+  int rows;    // rows of the sequence from there on
+  int kvh;
+  int unused[3];
+};
+
 // Whether the place (b, kvh, run, step) lies before `end`.
 PKV_PLAN_FN bool packed_is_before(int b, int kvh, int run, int step, const PackedBound& end) {
   if (b != end.b) return b < end.b;

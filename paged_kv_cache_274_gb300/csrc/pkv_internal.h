@@ -164,7 +164,7 @@ cudaError_t allow_smem(const void* fn, size_t smem, int regs);
 
 // The tcgen05 attention of packed rows, likewise.
 struct PackedWorkspace {
-  size_t shares, seqs, start, bounds, poison, part_ml, part_o, total;
+  size_t shares, seqs, start, bounds, merge, poison, part_ml, part_o, total;
 };
 PackedWorkspace packed_workspace(int B, int N, int Hkv, int D, int tiles, int max_shares);
 cudaError_t launch_packed_attend(const DecodeLaunch& L, uint8_t* workspace, int* launched_kernels);

@@ -287,12 +287,12 @@ cudaError_t launch_tree_attend(const DecodeLaunch& L, uint8_t* ws, int* launched
 
   // 3. merge of the items that shares split
   if (L.tree_shares > 1) {
-    const TreeMergeArgs ma{bounds, nullptr, nullptr, shares, p.part_ml, p.part_o, p.out, L.Hq, L.G, L.T, L.Tt, NP, pair ? 2 : 1};
-    cfg.gridDim = dim3(static_cast<unsigned>((L.tree_shares - 1) * NP * (ma.tiles * kTaRows / kTreeMergeCta)));
+    const TreeMergeArgs ma{bounds, nullptr, shares, p.part_ml, p.part_o, p.out, L.Hq, L.G, L.T, L.Tt, NP, pair ? 2 : 1};
+    cfg.gridDim = dim3(static_cast<unsigned>((L.tree_shares - 1) * NP * (ma.tiles * kTaRows / merge_cta_rows(2))));
     cfg.blockDim = dim3(kTreeMergeThreads);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = (L.ev_end == nullptr) ? 1 : 0;
-    e = L.D == 64 ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<64, false>, ma) : cudaLaunchKernelEx(&cfg, tree_merge_kernel<128, false>, ma);
+    e = L.D == 64 ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<64, false, 2>, ma) : cudaLaunchKernelEx(&cfg, tree_merge_kernel<128, false, 2>, ma);
     if (e != cudaSuccess) return e;
     *launched += 1;
   }

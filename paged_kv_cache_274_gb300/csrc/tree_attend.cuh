@@ -93,6 +93,7 @@ struct TaParams {
   // packed rows
   const PackedSeq* seqs;        // [B]
   const PackedBound* pbounds;   // [shares + 1]
+  PackedMerge* merge;           // [shares] (written)
 };
 
 // Step flags; a step without any is every row's in whole, with scores whose
@@ -615,6 +616,29 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       }
       v_issued = g + 1;
     }
+    // what the merge will join in this share's name (there it would be a chain of
+    // loads per 32 rows; here, with the last steps still to come, it is hidden)
+    if constexpr (PACKED) {
+      const int shares = __ldg(p.shares);
+      PackedMerge d{0, 0, 0, 0, 0, {0, 0, 0}};
+      if (share < shares) {
+        const PackedBound mine = p.pbounds[share], next = p.pbounds[share + 1];
+        if (packed_splits(mine, next, share, shares)) {
+          int last = share + 1;  // the share that ends the item
+#pragma unroll 1
+          for (;;) {
+            const int s = last + 1 + lane;
+            const unsigned found = __ballot_sync(kFull, s >= shares || packed_item_ends(next, p.pbounds[s]));
+            last += found ? __ffs(found) - 1 : 32;
+            if (found) break;
+          }
+          const PackedSeq q = p.seqs[next.b];
+          const int t0 = next.run * (PAIR ? 2 : 1) * p.Tt;
+          d = PackedMerge{last - share + 1, packed_split_place(mine, next), q.start + t0, q.m - t0, next.kvh, {0, 0, 0}};
+        }
+      }
+      if (lane == 0) p.merge[share] = d;
+    }
   } else if (warp == 19) {
     if constexpr (!kOneByte) {
       // query warp (bf16 caches): each unit's query tiles, once the products
@@ -1022,8 +1046,15 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             }
             tc_wait_st();
           }
+          // After a unit's first step the exponentials are made while the warps
+          // have yet to agree that the maximum stays, and made again where it
+          // does not (1.65 -> 1.5 us a step of two bf16 tiles).  Not for one tile
+          // of head_dim 64, whose items are short (71 instead of 64 us for the
+          // drafted trees' batch), and INT8 (239 instead of 202 us).
+          constexpr bool kAhead = !kI8 && (PAIR || D == 128);
+          const bool ahead = kAhead && k > 0 && !(kOneByte && (flags & kStepScales));
           uint32_t x0[32], x1[32];
-          if constexpr (kOneByte) {
+          if constexpr (!kAhead) {
             tc_ld32(t_h, x0);
             tc_ld32(t_h + 32u, x1);
             tc_wait_ld_regs(x0);
@@ -1055,9 +1086,9 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             }
           };
           float smax = -INFINITY;
-          if constexpr (kOneByte) {
+          if constexpr (!kAhead) {
             smax = fmaxf(ext32(x0, 0), ext32(x1, 1));
-          } else if (k == 0) {  // (32 at a time: these registers are not kept)
+          } else if (!ahead) {  // (32 at a time: these registers are not kept)
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
               uint32_t y[32];
@@ -1084,96 +1115,81 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             __syncwarp();
             return true;
           };
-          if ((kOneByte || k == 0) && bar_red_or(pair_bar, 64, wants() || fail) && !agree()) {
+          if (!ahead && bar_red_or(pair_bar, 64, wants() || fail) && !agree()) {
             fail = left = true;
             break;
           }
           float neg_m = (m == -INFINITY) ? 0.f : -m;
-          float ps0 = 0.f, ps1 = 0.f;
-          auto write_p = [&](const uint32_t (&x)[32], int c32) {
-            float ck = c_u, add = 0.f, lv = 0.f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {  // 16 scores
+          if (!kOneByte || !(flags & kStepScales)) {
+            float ps0 = 0.f, ps1 = 0.f, l2 = l, ck = c_u, add = 0.f, lv = 0.f;
+            // P of 16 scores, tokens tok .. tok + 15 of the half, and their sums
+            auto exps = [&](const uint32_t* x, uint32_t* pw, int tok) {
               if constexpr (kOneByte) {
-                if (h == 0 || BS == 16) {
-                  page(c32, h, ck, add, lv);
+                if (tok % BS == 0) {
+                  page(tok / 32, tok % 32 / 16, ck, add, lv);
                   ps0 = ps1 = 0.f;
                 }
               }
-              uint32_t pw[8];
               const float bias = add + neg_m + lv;
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const int k2 = 16 * h + 2 * e;
                 float a0, a1;
-                ffma2(a0, a1, __uint_as_float(x[k2]), __uint_as_float(x[k2 + 1]), ck, ck, bias, bias);
+                ffma2(a0, a1, __uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), ck, ck, bias, bias);
                 const float p0 = ex2_approx(a0);
                 const float p1 = ex2_approx(a1);
                 fadd2(ps0, ps1, ps0, ps1, p0, p1);
                 pw[e] = kOneByte ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
               }
               if constexpr (kOneByte) {
-                if (h == 1 || BS == 16) l = fmaf(ps0 + ps1, ex2_approx(-lv), l);
+                if (tok % BS + 16 == BS) l2 = fmaf(ps0 + ps1, ex2_approx(-lv), l2);
               }
-              tc_st8(t_h + 16 * c32 + 8 * h, pw);
-            }
-          };
-          if (!kOneByte || !(flags & kStepScales)) {
-            if constexpr (kOneByte) {
-              // one-byte caches: the second 32 scores are read again, so that
-              // 32 registers less are held meanwhile (the first 32's P covers
-              // only columns that are done with)
-              write_p(x0, 0);
-              tc_ld32(t_h + 32u, x1);
-              tc_wait_ld_regs(x1);
-              write_p(x1, 1);
-            } else {
-              // After a unit's first step the exponentials are made while the
-              // warps have yet to agree that the maximum stays (and the scores'
-              // second half is on its way), and made again where it does not.
-              auto exps = [&](const uint32_t* x, uint32_t* pw, int pairs) {
-#pragma unroll
-                for (int e = 0; e < pairs; ++e) {
-                  float a0, a1;
-                  ffma2(a0, a1, __uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), c_u, c_u, neg_m, neg_m);
-                  const float p0 = ex2_approx(a0);
-                  const float p1 = ex2_approx(a1);
-                  fadd2(ps0, ps1, ps0, ps1, p0, p1);
-                  pw[e] = pack_bf16x2(p0, p1);
-                }
-              };
-              uint32_t pw[32];
+            };
+            uint32_t pw[32];
+            if constexpr (kAhead) {
               tc_ld32(t_h, x0);
               tc_wait_ld_regs(x0);
-              tc_ld32(t_h + 32u, x1);
-              exps(x0, pw, 16);
-              smax = ext32(x0, 0);
-              tc_wait_ld_regs(x1);
-              exps(x1, pw + 16, 16);
-              smax = fmaxf(smax, ext32(x1, 1));
-              const bool again = k > 0 && bar_red_or(pair_bar, 64, wants() || fail);
-              if (again) {
-                if (!agree()) {
-                  fail = left = true;
-                  break;
-                }
-                neg_m = (m == -INFINITY) ? 0.f : -m;
-                ps0 = ps1 = 0.f;
-              } else {
-                tc_st32(t_h, pw);
-              }
-              if (again) {
-#pragma unroll 1
-                for (int q = 0; q < 4; ++q) {  // (P covers only columns that are done with)
-                  uint32_t y[16], pq[8];
-                  tc_ld16(t_h + 16u * q, y);
-                  tc_wait_ld_regs16(y);
-                  exps(y, pq, 8);
-                  tc_st8(t_h + 8u * q, pq);
-                }
-              }
-              l += ps0 + ps1;
+              if constexpr (!kOneByte) tc_ld32(t_h + 32u, x1);  // (one-byte caches have no registers for it yet)
             }
+            exps(x0, pw, 0);
+            exps(x0 + 16, pw + 8, 16);
+            if constexpr (kI8) {
+              // the second 32 scores are read again, so that 32 registers less
+              // are held meanwhile (the first 32's P covers only columns that
+              // are done with)
+              tc_st16(t_h, *reinterpret_cast<uint32_t(*)[16]>(pw));
+              tc_ld32(t_h + 32u, x1);
+              tc_wait_ld_regs(x1);
+            }
+            if constexpr (kAhead) {
+              smax = fmaxf(smax, ext32(x0, 0));
+              if constexpr (kOneByte) tc_ld32(t_h + 32u, x1);
+              tc_wait_ld_regs(x1);
+            }
+            exps(x1, pw + 16, 32);
+            exps(x1 + 16, pw + 24, 48);
+            if constexpr (kAhead) smax = fmaxf(smax, ext32(x1, 1));
+            if (ahead && bar_red_or(pair_bar, 64, wants() || fail)) {
+              if (!agree()) {
+                fail = left = true;
+                break;
+              }
+              neg_m = (m == -INFINITY) ? 0.f : -m;
+              ps0 = ps1 = 0.f;
+              l2 = l;
+#pragma unroll 1
+              for (int q = 0; q < 4; ++q) {  // (P covers only columns that are done with)
+                uint32_t y[16], pq[8];
+                tc_ld16(t_h + 16u * q, y);
+                tc_wait_ld_regs16(y);
+                exps(y, pq, 16 * q);
+                tc_st8(t_h + 8u * q, pq);
+              }
+            } else if constexpr (kI8) {
+              tc_st16(t_h + 16u, *reinterpret_cast<uint32_t(*)[16]>(pw + 16));
+            } else {
+              tc_st32(t_h, pw);
+            }
+            l = kOneByte ? l2 : l + (ps0 + ps1);
           } else {
             // a page's v scale is zero, negative or not finite
 #pragma unroll 1
@@ -1317,8 +1333,8 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
               a = fmaf(z0, f1, a);
               b2 = fmaf(z1, f1, b2);
             }
-            o[e] = row_live ? a : 0.f;
-            o[e + 1] = row_live ? b2 : 0.f;
+            o[e] = PACKED || row_live ? a : 0.f;  // (packed: rows that are not live are not stored)
+            o[e + 1] = PACKED || row_live ? b2 : 0.f;
           }
         };
         // A lane's row is 64 bytes here, four chunks: four lanes exchange theirs,
@@ -1343,14 +1359,30 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         int rows4[4];  // where the four rows go (-1: not in the unit)
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) rows4[ch] = __shfl_sync(kFull, in_tile ? (part == 0 ? row_out : r) : -1, (lane & ~3) + ch);
-        // a pair's warp: half of its tile's columns; else a quarter of the one
-        // tile's (head_dim 64: the first stream's warps a half)
-        const int cols = two ? D / 2 : (D == 64 ? 32 : D / 4), c0 = (two ? hh : 2 * i + hh) * cols;
+        // a pair's warp: half of its tile's columns; else a quarter of the one tile's
+        constexpr int cols = two ? D / 2 : D / 4;
+        const int c0 = (two ? hh : 2 * i + hh) * cols;
 #pragma unroll 1
-        for (int cc = c0; cc < min(c0 + cols, D); cc += part == 0 ? 32 : 16) {
+        for (int cc = c0; cc < c0 + cols; cc += part == 0 ? 32 : 16) {
           uint32_t w[16];
           float o[16];
           columns(cc, o);
+          if (cols == 16 && part == 0) {  // 32 bytes a row: two lanes
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t got = __shfl_xor_sync(kFull, (quad & 1) ? w[e] : w[4 + e], 1);
+              if (quad & 1) w[e] = got; else w[4 + e] = got;
+            }
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+              const int to = (quad & 2) ? rows4[2 + ch] : rows4[ch];
+              if (to >= 0)
+                *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(to) * D + cc + 8 * (quad & 1)) = make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
+            }
+            continue;
+          }
           if (part == 0) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);

@@ -13,19 +13,21 @@ namespace pkv {
 // as its last unit; the shares after it continue it with their first unit
 // until one ends it.
 //
-// One CTA per (share, row tiles of a CTA, 16 rows), a warp per two rows.  The
-// partials are in L2 and few, so it is a chain of loads: bounds, a lane each,
-// then m and l of up to 16 parts of both rows by one load of the warp, next to
-// the rows of the first four parts.  (A warp per row in turn, with the loads
-// after the maxima, took 5 us longer for 151 split items of 128 rows.)
+// One CTA per (share, row tiles of a CTA, 16 or 32 rows), a warp per two or four
+// rows.  The partials are in L2 and few, so it is a chain of loads: bounds, a
+// lane each (packed rows: one record of the share), then m and l of the parts of
+// all rows by one load of the warp, next to the rows of the first parts.  (A
+// warp per row in turn, with the loads after the maxima, took 5 us longer for
+// 151 split items of 128 rows.)  Four rows a warp for the packed rows' pairs of
+// tiles, where items are long and have two or three parts: 151 items of 256 rows
+// 11 us instead of 16 after a cold start; two elsewhere, where a short item may
+// have many (one request of five rows: 15.8 us a call instead of 17.6).
 constexpr int kTreeMergeThreads = 256;
-constexpr int kTreeMergeRows = 2;                                        // of a warp
-constexpr int kTreeMergeCta = kTreeMergeThreads / 32 * kTreeMergeRows;   // of a CTA
+__host__ __device__ constexpr int merge_cta_rows(int rows) { return kTreeMergeThreads / 32 * rows; }  // of a CTA
 
 struct TreeMergeArgs {
   const TreeBound* bounds;
-  const PackedBound* pbounds;  // packed rows
-  const PackedSeq* seqs;
+  const PackedMerge* merge;  // packed rows
   const int32_t* shares;
   const float2* part_ml;
   const float* part_o;
@@ -33,55 +35,51 @@ struct TreeMergeArgs {
   int Hq, G, T, Tt, NP, tiles /* per CTA */;
 };
 
-template <int D, bool PACKED>
+template <int D, bool PACKED, int ROWS>  // rows of a warp
 __global__ void __launch_bounds__(kTreeMergeThreads, 3) tree_merge_kernel(const TreeMergeArgs a) {
-  constexpr int kPer = D / 32, kRows = kTreeMergeRows, kLanes = 32 / kRows, kBatch = 4;
+  constexpr int kPer = D / 32, kRows = ROWS, kLanes = 32 / kRows, kBatch = 8 / ROWS;  // (parts at a time)
   pdl_trigger();
   pdl_wait();
-  const int rows = a.tiles * kTaRows, slices = rows / kTreeMergeCta;
+  const int rows = a.tiles * kTaRows, slices = rows / merge_cta_rows(ROWS);
   const int slice = blockIdx.x % slices;
   const int cta = blockIdx.x / slices;
   const int share = cta / a.NP, pair = cta - share * a.NP;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // (the grid leaves out the last share that the workspace has room for)
-  const int shares = *a.shares;
-  using Bound = std::conditional_t<PACKED, PackedBound, TreeBound>;
-  const Bound* bounds;
-  if constexpr (PACKED) bounds = a.pbounds; else bounds = a.bounds;
-  const Bound mine = bounds[share], next = bounds[share + 1];
-  int place;
+  int parts, place, kvh, first_row, tokens;  // the rows of q that tile 0 starts with, and how many there are
   if constexpr (PACKED) {
-    if (!packed_splits(mine, next, share, shares)) return;
-    place = packed_split_place(mine, next);
+    const int4 d = __ldg(reinterpret_cast<const int4*>(a.merge + share));
+    kvh = __ldg(&a.merge[share].kvh);
+    if (d.x == 0) return;
+    parts = d.x;
+    place = d.y;
+    first_row = d.z;
+    tokens = d.w;
   } else {
+    // (the grid leaves out the last share that the workspace has room for)
+    const int shares = *a.shares;
+    const TreeBound mine = a.bounds[share], next = a.bounds[share + 1];
     if (!tree_splits(mine, next, share, shares)) return;
     place = tree_split_place(mine, next);
-  }
-  int last = share + 1;  // the share that ends the item
+    int last = share + 1;  // the share that ends the item
 #pragma unroll 1
-  for (;;) {
-    const int s = last + 1 + lane;
-    bool ends = true;
-    if (s < shares) {
-      if constexpr (PACKED) ends = packed_item_ends(next, bounds[s]); else ends = tree_item_ends(next, bounds[s]);
+    for (;;) {
+      const int s = last + 1 + lane;
+      bool ends = true;
+      if (s < shares) ends = tree_item_ends(next, a.bounds[s]);
+      const unsigned found = __ballot_sync(kFull, ends);
+      last += found ? __ffs(found) - 1 : 32;
+      if (found) break;
     }
-    const unsigned found = __ballot_sync(kFull, ends);
-    last += found ? __ffs(found) - 1 : 32;
-    if (found) break;
+    parts = last - share + 1;
+    kvh = next.kvh;
+    first_row = next.b * a.T;
+    tokens = a.T;
   }
-  const int parts = last - share + 1;
   const size_t first = (static_cast<size_t>(cta) * 2 + place) * rows;
   const size_t stride = static_cast<size_t>(a.NP) * 2 * rows;  // from a share's partials to the next one's
   const size_t cont = (static_cast<size_t>(cta) * 2) * rows;
-  const int rr0 = slice * kTreeMergeCta + warp * kRows;
+  const int rr0 = slice * merge_cta_rows(ROWS) + warp * kRows;
   const int tile = (a.tiles == 2 ? 2 * pair : 0) + rr0 / kTaRows;
-  int first_row = next.b * a.T, tokens = a.T;  // the rows of q that tile 0 starts with, and how many there are
-  if constexpr (PACKED) {
-    const PackedSeq q = a.seqs[next.b];
-    const int t0 = next.run * a.tiles * a.Tt;
-    first_row = q.start + t0;
-    tokens = q.m - t0;
-  }
   unsigned live = 0;  // rows with a node
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
@@ -143,7 +141,7 @@ __global__ void __launch_bounds__(kTreeMergeThreads, 3) tree_merge_kernel(const 
     const float inv = __shfl_sync(kFull, inv_mine, kLanes * k);
     if (!((live >> k) & 1u)) continue;
     const int r = (rr0 + k) % kTaRows, tl = r / a.G;
-    __nv_bfloat16* o = a.out + (static_cast<size_t>(first_row + tile * a.Tt + tl) * a.Hq + next.kvh * a.G + (r - tl * a.G)) * D + lane * kPer;
+    __nv_bfloat16* o = a.out + (static_cast<size_t>(first_row + tile * a.Tt + tl) * a.Hq + kvh * a.G + (r - tl * a.G)) * D + lane * kPer;
     uint32_t w[kPer / 2];
 #pragma unroll
     for (int j = 0; j < kPer; j += 2) w[j / 2] = pack_bf16x2(acc[k][j] * inv, acc[k][j + 1] * inv);
