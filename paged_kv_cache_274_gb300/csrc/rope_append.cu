@@ -15,8 +15,11 @@
 //
 // Angles are kept in turns: the host gives each frequency as a fraction of a
 // turn per position in 2^-64, and position x frequency modulo 2^64 is an
-// integer product, exact at any position.  Its upper 32 bits go to sincospif,
-// so an angle is off by less than 2^-24 of half a turn wherever the token is.
+// integer product, exact at any position.  The nearest quarter turn comes off as
+// an integer too, and the rest, at most an eighth of a turn, goes to sincospif as
+// a float: an angle is off by less than 2^-26 of half a turn wherever the token
+// is.  (With the whole turn as one float, 2^-24, E4M3 keys took the other
+// neighbour twice as often.)
 //
 // What bounds it: every row is read and written once; see the times at
 // launch_rope_append.
@@ -154,8 +157,16 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(co
         const int i = 2 * lane + s;
         if (i < a.R / 2) {
           const long long pos = __ldg(a.positions + static_cast<size_t>(axis[i]) * a.app.N + token);
-          const uint64_t turn = static_cast<uint64_t>(pos) * freq[i];
-          sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn2[s], &cs2[s]);
+          const uint64_t turn = static_cast<uint64_t>(pos) * freq[i], quarter = (turn + (1ull << 61)) >> 62;
+          float sn, cs;
+          sincospif(static_cast<float>(static_cast<int64_t>(turn - (quarter << 62))) * 0x1p-63f, &sn, &cs);
+          if (quarter & 1) {
+            const float was = sn;
+            sn = cs;
+            cs = -was;
+          }
+          sn2[s] = (quarter & 2) ? -sn : sn;
+          cs2[s] = (quarter & 2) ? -cs : cs;
         }
       }
 #pragma unroll
