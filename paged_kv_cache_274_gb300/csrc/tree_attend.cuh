@@ -73,7 +73,12 @@ namespace pkv {
 
 constexpr int kTaRows = 128;    // query rows per tile
 constexpr int kTaRing = 8;      // step descriptors: a step's is read until its softmax is done, at most 5 steps back
-constexpr uint32_t kTaCols = 512;  // TMEM: S0 0, S1 128, O0 256, O1 384
+constexpr uint32_t kTaCols = 512;
+// TMEM: S buffers of 128 columns from 0 on, then O0 and O1 of D columns.  With
+// head_dim 128 a buffer per stream, with 64 three in turn.
+__host__ __device__ constexpr int ta_buffers(int D) { return D == 64 ? 3 : 2; }
+__host__ __device__ constexpr uint32_t ta_o_col(int D, int i) { return static_cast<uint32_t>(128 * ta_buffers(D) + D * i); }
+static_assert(ta_o_col(64, 2) <= kTaCols && ta_o_col(128, 2) <= kTaCols, "");
 
 struct TaParams {
   const __nv_bfloat16* q;
@@ -150,9 +155,9 @@ struct TaLayout {  // byte offsets from the 1024-aligned shared-memory base
   static constexpr uint32_t kK = kQ + kQTiles * kTile;
   static constexpr uint32_t kV = kK + kKStages * kKTile;
   static constexpr uint32_t kBars = kV + kVStages * kTile;
-  // k_full k_free tma_k [K], v_full v_free tma_v [V], s_full p_full o_full
-  // o_free [2], step_full [ring], q_full q_free q_read x_full mma_drain
-  static constexpr int kNumBars = 3 * kKStages + 3 * kVStages + 8 + kTaRing + 5;
+  // k_full k_free tma_k [K], v_full v_free tma_v [V], s_full p_full [buffers],
+  // o_full o_free pv_done [2], step_full [ring], q_full q_free q_read x_full mma_drain
+  static constexpr int kNumBars = 3 * kKStages + 3 * kVStages + 2 * ta_buffers(D) + 6 + kTaRing + 5;
   static constexpr uint32_t kMisc = kBars + 8 * kNumBars;
   static constexpr uint32_t kRing = (kMisc + 4 + 15) & ~15u;
   static constexpr uint32_t kStep = kOneByte ? sizeof(TaStep) : offsetof(TaStep, par);
@@ -282,7 +287,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
   static_assert(!kOneByte || D == 128, "one-byte pages need head_dim 128");
   constexpr int PPI = kTreeTokens / BS;  // pages per step
   constexpr int KS = L::kKStages, VS = L::kVStages;
-  constexpr int kHalves = D / 64;
+  constexpr int kHalves = D / 64, kBufs = ta_buffers(D);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   // Barrier phases: k_* and v_* rings by the CTA's running step index g (stage
@@ -296,11 +301,12 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
   uint64_t* v_full = tma_k + KS;
   uint64_t* v_free = v_full + VS;   // the step's PV done
   uint64_t* tma_v = v_free + VS;    // one-byte: V codes landed
-  uint64_t* s_full = tma_v + VS;    // [stream] S_i (and every product before it) done
-  uint64_t* p_full = s_full + 2;    // [stream] P_i in TMEM, stale V rows cleared
-  uint64_t* o_full = p_full + 2;    // [stream] the unit's last PV_i done
+  uint64_t* s_full = tma_v + VS;    // [buffer] S (and every product before it) done
+  uint64_t* p_full = s_full + kBufs;  // [buffer] P in TMEM, stale V rows cleared
+  uint64_t* o_full = p_full + kBufs;  // [stream] the unit's last PV_i done
   uint64_t* o_free = o_full + 2;    // [stream] the unit's O_i read
-  uint64_t* step_full = o_free + 2; // [ring] descriptor written
+  uint64_t* pv_done = o_free + 2;   // [stream] three buffers: a step's PV_i done
+  uint64_t* step_full = pv_done + 2; // [ring] descriptor written
   uint64_t* q_full = step_full + kTaRing;
   uint64_t* q_free = q_full + 1;    // the unit's last S done
   uint64_t* q_read = q_free + 1;    // one-byte: the unit's row factors read by every softmax warp
@@ -321,10 +327,13 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       mbar_init(&tma_v[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 8);  // one lane per warp of the stream
+      mbar_init(&pv_done[s], 1);
       mbar_init(&o_full[s], 1);
       mbar_init(&o_free[s], 16);
+    }
+    for (int s = 0; s < kBufs; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 8);  // one lane per warp of the stream
     }
     for (int s = 0; s < kTaRing; ++s) mbar_init(&step_full[s], 1);
     mbar_init(q_full, kOneByte ? kConvWarps : 1);
@@ -682,7 +691,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       // each row per product.  (Loops of two products: the issuing thread's
       // code is fetched anew each step, between the softmax warps'.)
       bool two = PAIR;  // of the unit
-      auto issue_s = [&](int i, uint32_t stage) {
+      auto issue_s = [&](int i, uint32_t buf, uint32_t stage) {
         const uint64_t qd = q_desc + (two ? i * (L::kTile >> 4) : 0u), kd = k_desc + stage * (L::kKTile >> 4);
         constexpr int kParts = kF8K ? 2 : kHalves;  // regions of the query: E4M3 both parts against the same codes
 #pragma unroll 1
@@ -691,9 +700,9 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             if constexpr (kF8K)
-              tc_mma_e4m3(tmem + 128u * i, qh + 2 * kk, kh + 2 * kk, kIdescS, h > 0 || kk > 0);
+              tc_mma_e4m3(tmem + 128u * buf, qh + 2 * kk, kh + 2 * kk, kIdescS, h > 0 || kk > 0);
             else
-              tc_mma_bf16(tmem + 128u * i, qh + 2 * kk, kh + 2 * kk, kIdescS, h > 0 || kk > 0);
+              tc_mma_bf16(tmem + 128u * buf, qh + 2 * kk, kh + 2 * kk, kIdescS, h > 0 || kk > 0);
           }
         }
         ++mma_issued;
@@ -701,10 +710,15 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       // O_i (+)= P_i . V: P of a half's tokens 16kk .. 16kk + 15 in columns
       // 8kk .. +7 of the half's 64 columns of S_i, V MN-major as the pages hold
       // it (64-d halves kRegion apart, 8-token groups 1024 B apart)
-      uint32_t pc[2] = {0, 0};  // P tiles taken, per stream
+      uint32_t pc[2] = {0, 0};  // P tiles taken, per stream (a buffer each)
       uint32_t ks = 0, kph = 0, vs = 0, vph = 0;  // stage and phase of the next K and V
-      auto issue_pv = [&](int i, bool first, uint32_t iu) -> bool {
-        if (!ta_wait(&p_full[i], pc[i] & 1u)) return false;
+      uint32_t done = 0;  // events (S and PV of a stream's step) of the units before
+      // PV of the unit's event f: stream f % 2, its step f / 2
+      auto issue_pv = [&](int f, int events, uint32_t iu) -> bool {
+        const int i = f & 1;
+        const bool first = f < 2;
+        const uint32_t buf = kBufs == 2 ? i : (done + f) % kBufs, ph = kBufs == 2 ? pc[i] : (done + f) / kBufs;
+        if (!ta_wait(&p_full[buf], ph & 1u)) return false;
         ++pc[i];
         if ((!two || i == 0) && !ta_wait(&v_full[vs], vph)) return false;
         if (first && iu > 0 && !ta_wait(&o_free[i], (iu - 1) & 1u)) return false;
@@ -714,7 +728,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_bf16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 64u * h + 8u * kk, vd + (h * 4 + kk) * (2048 >> 4), kIdescO,
+            tc_mma_bf16_ts(tmem + ta_o_col(D, 0) + D * i, tmem + 128u * buf + 64u * h + 8u * kk, vd + (h * 4 + kk) * (2048 >> 4), kIdescO,
                            !first || h > 0 || kk > 0);
         ++mma_issued;
         if (!two || i == 1) {
@@ -724,6 +738,8 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             vph ^= 1u;
           }
         }
+        if constexpr (kBufs > 2) tc_commit(&pv_done[i]);
+        if (f >= events - 2) tc_commit(&o_full[i]);  // the stream's last of the unit
         return true;
       };
       uint32_t g0 = 0;
@@ -735,14 +751,18 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         if (!(ok = ta_wait(q_full, iu & 1u))) break;
         if constexpr (PAIR && PACKED) two = two_tiles(step_at(g0)->rows);
         const int events = two ? 2 * n : n;
+        // S of an event once PV of the one that had its buffer is issued: two
+        // events back, or three
 #pragma unroll 1
-        for (int e = 0; ok && e < events; ++e) {
-          const int i = e & 1, k = e >> 1;  // stream, its step
-          if (k > 0 && !(ok = issue_pv(i, k == 1, iu))) break;
+        for (int e = 0; e < events + kBufs; ++e) {
+          if (e >= kBufs && !(ok = issue_pv(e - kBufs, events, iu))) break;
+          if (e >= events) continue;
+          const int i = e & 1;  // stream
+          const uint32_t buf = kBufs == 2 ? i : (done + e) % kBufs;
           if ((!two || i == 0) && !(ok = ta_wait(&k_full[ks], kph))) break;
           tc_fence_after_sync();
-          issue_s(i, ks);
-          tc_commit(&s_full[i]);
+          issue_s(i, buf, ks);
+          tc_commit(&s_full[buf]);
           if (!two || i == 1) {
             tc_commit(&k_free[ks]);
             if (++ks == KS) {
@@ -752,15 +772,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           }
           if (e == events - 1) tc_commit(q_free);
         }
-        // the last products of both streams, the earlier step's first
-#pragma unroll 1
-        for (int x = 0; ok && x < 2; ++x) {
-          const int i = (!two && (n & 1)) ? 1 - x : x;
-          const int ni = two ? n : (n + 1 - i) / 2;  // the stream's steps
-          if (ni == 0) continue;
-          if (!(ok = issue_pv(i, ni == 1, iu))) break;
-          tc_commit(&o_full[i]);
-        }
+        done += static_cast<uint32_t>(events);
         if (!ok) break;
         g0 += static_cast<uint32_t>(n);
       }
@@ -919,13 +931,13 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
     const int i = warp >> 3, hh = (warp >> 2) & 1, r = 32 * (warp & 3) + lane;
     const int pair_bar = 1 + (warp & 3) + 4 * i;  // named barrier of the two warps
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lane_base + 128u * i;
-    const uint32_t t_o = tmem + lane_base + 256u;  // O0; O1 is 128 columns on
+    const uint32_t t_o = tmem + lane_base + ta_o_col(D, 0);  // O0; O1 is D columns on
     const float c = p.scale_log2;
     const int tl = r / p.G;
     float* xch = reinterpret_cast<float*>(sm + L::kXml);
     float* x_mine = xch + (2 * i + hh) * kTaRows + r;
     const float* x_other = xch + (2 * i + (hh ^ 1)) * kTaRows + r;
+    uint32_t done = 0;  // three buffers: events of the units before
     uint32_t g0 = 0, steps = 0, units1 = 0, alone = 0;  // steps of this stream, units with a step for stream 1, of one tile
     // A wait of this warp gave up: it waits for nothing more, and leaves with
     // the warp that shares its rows, at their next barrier
@@ -1014,7 +1026,10 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           }
         }
         const bool plain = flags == 0 && c >= 0.f;  // (a lower scale turns the order of the scores)
-        if (!fail && !ta_wait(&s_full[i], steps & 1u)) fail = true;
+        // this step's event, and its S buffer
+        const uint32_t event = done + static_cast<uint32_t>(2 * k + i), buf = kBufs == 2 ? static_cast<uint32_t>(i) : event % kBufs;
+        const uint32_t t_s = tmem + lane_base + 128u * buf;
+        if (!fail && !ta_wait(&s_full[buf], (kBufs == 2 ? steps : event / kBufs) & 1u)) fail = true;
         __syncwarp();
         tc_fence_after_sync();
         if (!warp_dead) {
@@ -1211,13 +1226,17 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             }
           }
           // O_i of the steps before, rarely, half of the columns by each warp
-          // (quiescent: PV_i of the step before was done before this S_i, the
-          // next waits for p_full)
+          // (quiescent: PV_i of the step before was done before this S_i, or is
+          // waited for; the next waits for p_full)
           if (k > 0 && __any_sync(kFull, grow || vgrow)) {
+            if constexpr (kBufs > 2) {
+              if (!fail && !warp_wait(&pv_done[i], (steps - 1) & 1u)) fail = true;
+              tc_fence_after_sync();
+            }
 #pragma unroll 1
             for (int oc = hh * (D / 2); oc < (hh + 1) * (D / 2); oc += 32) {
               uint32_t ov[32];
-              tc_ld32(t_o + 128u * i + oc, ov);
+              tc_ld32(t_o + D * i + oc, ov);
               tc_wait_ld_regs(ov);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
@@ -1226,7 +1245,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
                 ov[e] = __float_as_uint(a);
                 ov[e + 1] = __float_as_uint(b2);
               }
-              tc_st32(t_o + 128u * i + oc, ov);
+              tc_st32(t_o + D * i + oc, ov);
             }
           }
         }
@@ -1249,7 +1268,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         tc_wait_st();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[i]);
+        if (lane == 0) mbar_arrive(&p_full[buf]);
       }
       if (left) return false;
 
@@ -1320,8 +1339,8 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         // O's columns cc .. cc + 15 of the row, joined over the streams
         auto columns = [&](int cc, float (&o)[16]) {
           uint32_t ov[16], o1[16];
-          tc_ld16(t_o + (two ? 128u * i : 0u) + cc, ov);
-          if (!two) tc_ld16(t_o + 128u + cc, o1);  // (O1 of a unit with one step holds anything)
+          tc_ld16(t_o + (two ? D * i : 0) + cc, ov);
+          if (!two) tc_ld16(t_o + D + cc, o1);  // (O1 of a unit with one step holds anything)
           tc_wait_ld_regs16(ov);
           if (!two) tc_regs_loaded16(o1);
 #pragma unroll
@@ -1421,13 +1440,15 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       const volatile TaStep* st = step_at(g0);
       const int n = st->n;
       if (n == 0) break;
+      const bool two = two_tiles(PACKED ? st->rows : 0);
       bool go;
       if constexpr (PAIR && PACKED) {
-        go = two_tiles(st->rows) ? unit(std::integral_constant<int, 2>{}, iu, n) : unit(std::integral_constant<int, 1>{}, iu, n);
+        go = two ? unit(std::integral_constant<int, 2>{}, iu, n) : unit(std::integral_constant<int, 1>{}, iu, n);
       } else {
         go = unit(std::integral_constant<int, PAIR ? 2 : 1>{}, iu, n);
       }
       if (!go) break;
+      done += static_cast<uint32_t>(two ? 2 * n : n);
       g0 += static_cast<uint32_t>(n);
     }
     if (fail) timed_out = true;
