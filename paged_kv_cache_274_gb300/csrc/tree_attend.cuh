@@ -1101,9 +1101,8 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             }
           };
           float smax = -INFINITY;
-          if constexpr (!kAhead) {
-            smax = fmaxf(ext32(x0, 0), ext32(x1, 1));
-          } else if (!ahead) {  // (32 at a time: these registers are not kept)
+          // (32 at a time: these registers are not kept)
+          auto find_max = [&]() {
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
               uint32_t y[32];
@@ -1111,7 +1110,11 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
               tc_wait_ld_regs(y);
               smax = fmaxf(smax, ext32(y, q));
             }
-          }
+          };
+          if constexpr (!kAhead)
+            smax = fmaxf(ext32(x0, 0), ext32(x1, 1));
+          else if (!ahead)
+            find_max();
           // lazy maximum: moved when the row's exceeds it by more than 2^8
           auto wants = [&]() { return m == -INFINITY ? smax != -INFINITY : smax > m + 8.f; };
           bool grow = false;
@@ -1137,6 +1140,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           float neg_m = (m == -INFINITY) ? 0.f : -m;
           if (!kOneByte || !(flags & kStepScales)) {
             float ps0 = 0.f, ps1 = 0.f, l2 = l, ck = c_u, add = 0.f, lv = 0.f;
+            [[maybe_unused]] float sum = 0.f;  // of the step's weights
             // P of 16 scores, tokens tok .. tok + 15 of the half, and their sums
             auto exps = [&](const uint32_t* x, uint32_t* pw, int tok) {
               if constexpr (kOneByte) {
@@ -1156,7 +1160,11 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
                 pw[e] = kOneByte ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
               }
               if constexpr (kOneByte) {
-                if (tok % BS + 16 == BS) l2 = fmaf(ps0 + ps1, ex2_approx(-lv), l2);
+                if (tok % BS + 16 == BS) {
+                  const float r = ex2_approx(-lv), pp = ps0 + ps1;
+                  l2 = fmaf(pp, r, l2);
+                  sum = fmaf(pp, r, sum);
+                }
               }
             };
             uint32_t pw[32];
@@ -1176,14 +1184,23 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
               tc_wait_ld_regs(x1);
             }
             if constexpr (kAhead) {
-              smax = fmaxf(smax, ext32(x0, 0));
               if constexpr (kOneByte) tc_ld32(t_h + 32u, x1);
               tc_wait_ld_regs(x1);
             }
             exps(x1, pw + 16, 32);
             exps(x1 + 16, pw + 24, 48);
-            if constexpr (kAhead) smax = fmaxf(smax, ext32(x1, 1));
-            if (ahead && bar_red_or(pair_bar, 64, wants() || fail)) {
+            // Weights that add up to 2^8 at most have none above it, so the maximum
+            // stays; only else it is looked for (without weights' sums, 32
+            // instructions a step).  Nothing is known of a row without a maximum.
+            bool again = false;
+            if constexpr (kAhead) {
+              if constexpr (!kOneByte) sum = ps0 + ps1;
+              if (ahead && bar_red_or(pair_bar, 64, !(sum <= 256.f) || m == -INFINITY || fail)) {
+                find_max();
+                again = bar_red_or(pair_bar, 64, wants() || fail);
+              }
+            }
+            if (again) {
               if (!agree()) {
                 fail = left = true;
                 break;
