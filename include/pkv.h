@@ -594,8 +594,8 @@ pkv_status pkv_extend_tables(int32_t batch, int32_t block_size, int32_t max_bloc
  * drawn one after another, without replacement, from the draft row.
  * draft_probs NULL: children chosen without randomness (the draft's best
  * tokens, a lookup); Q is then 1 at x alone and a rejection sets P(x) = 0.
- * Values of rows that are negative or not finite count as 0.  Comparisons are
- * made in fp64, sums to 2^-32 or better of their value.
+ * Values of rows that are negative or not finite count as 0.  Sums are taken to
+ * 2^-32 or better of their value, and compared as they are, unrounded.
  *
  *   tokens         device int32 [B][T]: the nodes' tokens, in [0, vocab) (node
  *                  0's is not looked at).
@@ -603,8 +603,8 @@ pkv_status pkv_extend_tables(int32_t batch, int32_t block_size, int32_t max_bloc
  *   node_counts    device int32 [B], in 0..T; NULL: T each.
  *   target_probs   device fp32 [B][T][vocab], rows target_stride >= vocab
  *                  elements apart.
- *   draft_probs    likewise with draft_stride, or NULL.  Rows of nodes without
- *                  children are not read.
+ *   draft_probs    likewise with draft_stride, or NULL.  Rows of nodes
+ *                  without children are not read.
  *   accept_uniforms  device fp32 [B][T], in [0, 1).
  *   sample_uniforms  device fp32 [B], in [0, 1).
  *   accept_idx     device int32 [B][max_accept] (written): the accepted nodes,

@@ -410,6 +410,9 @@ pkv_status pkv_rope_append(const pkv_cache_desc* cache, int32_t slot, const void
   const bool append = k != nullptr;
   const int64_t q_row = static_cast<int64_t>(num_q_heads) * D, kv_row = static_cast<int64_t>(cache->num_kv_heads) * D;
   if (q_row >= (1LL << 31)) return fail(PKV_ERR_UNSUPPORTED, "num_q_heads %d", num_q_heads);
+  // (then the kernel's items, at most half a part for 8 heads, fit 31 bits)
+  if (N * (num_q_heads + 2LL * cache->num_kv_heads) >= (1LL << 31))
+    return fail(PKV_ERR_UNSUPPORTED, "%d tokens of %d and %d heads", N, num_q_heads, cache->num_kv_heads);
   if (q_stride < q_row || q_out_stride < q_row || (append && (k_stride < kv_row || v_stride < kv_row)))
     return fail(PKV_ERR_INVALID_ARG, "a token stride is below the size of its heads");
   if ((q_stride | q_out_stride) % 8 != 0 || (append && (k_stride | v_stride) % 8 != 0))

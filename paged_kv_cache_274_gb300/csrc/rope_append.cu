@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(co
   const int nq = (a.Hq + kHeads - 1) / kHeads, nk = a.k_new ? (a.app.Hkv + kHeads - 1) / kHeads : 0;  // batches
   const int batches = nq + 2 * nk, per = (batches + a.parts - 1) / a.parts;
   pdl_wait();
-  const unsigned items = static_cast<unsigned>(a.app.N) * a.parts;  // (less than 2^31, as the host checks)
+  const unsigned items = static_cast<unsigned>(a.app.N) * a.parts;  // (less than 2^31, as the host sees to)
 #pragma unroll 1
   for (unsigned item = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); item < items; item += gridDim.x * (kRopeThreads / 32)) {
     const unsigned token = item / a.parts;

@@ -78,11 +78,15 @@ __device__ __forceinline__ bool positive(const Pair& x) { return x.hi > 0.f || (
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
-// What is negative or not finite counts as 0.
-__device__ __forceinline__ Pair weight(float p) { return {p > 0.f && p < INFINITY ? p : 0.f, 0.f}; }
+// What is negative or not finite counts as 0.  (The bits of those, and of -0, are
+// at least infinity's.)
+__device__ __forceinline__ float clean(float x) { return __float_as_uint(x) < 0x7f800000u ? x : 0.f; }
+__device__ __forceinline__ Pair weight(float p) { return {clean(p), 0.f}; }
 // max(p - (ah + al) q, 0), likewise.  (Where p >= ah q, three operations give
-// the difference and what it rounds away; elsewhere the result is 0.)
+// the difference and what it rounds away; elsewhere the result is 0.  It is 0 by
+// itself for p < 0, and for p that is not finite: d + lo is NaN then.)
 __device__ __forceinline__ Pair weight_left(float p, float q, float ah, float al) {
+  q = clean(q);
   const float h = __fmul_rn(ah, q);
   const float l = fmaf(al, q, fmaf(ah, q, -h));
   const float d = __fsub_rn(p, h);
@@ -119,14 +123,15 @@ struct VerifyShared {
 // with a draft row on another shift they are single loads (shift 0).
 struct VerifyRows {
   const float* p;
-  const float* q;  // NULL: no draft rows
+  const float* q;  // NULL: no draft row
   int shift;
   bool vec;
 };
-__device__ __forceinline__ VerifyRows verify_rows(const VerifyArgs& a, size_t row) {
+// draft: the draft row counts (a child was rejected).
+__device__ __forceinline__ VerifyRows verify_rows(const VerifyArgs& a, size_t row, bool draft) {
   VerifyRows r;
   r.p = a.p + row * a.p_stride;
-  r.q = a.q != nullptr ? a.q + row * a.q_stride : nullptr;
+  r.q = draft && a.q != nullptr ? a.q + row * a.q_stride : nullptr;
   const int sp = static_cast<int>(reinterpret_cast<uintptr_t>(r.p) >> 2) & 3;
   r.vec = r.q == nullptr || (static_cast<int>(reinterpret_cast<uintptr_t>(r.q) >> 2) & 3) == sp;
   r.shift = r.vec ? sp : 0;
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
             if (lane == 0) s.gone[removed - 1] = x;
             __syncwarp();
             if (!was && q0 > 0.f) {
-              const VerifyRows r = verify_rows(a, seq + at);
+              const VerifyRows r = verify_rows(a, seq + at, false);
               const int i = (x + r.shift) / kVerifyChunk;
               const float px = weight(s.p[c]).hi, whole_sum = sums[i].hi;
               Pair z = sums[i];
@@ -496,8 +501,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
     cluster_wait();
     const int row = s.row;
     if (row < 0) return;
-    const VerifyRows r = verify_rows(a, seq + row);
-    if (a.q != nullptr)
+    const VerifyRows r = verify_rows(a, seq + row, s.removed > 0);
+    if (r.q != nullptr)
       verify_pass<true>(a, &s, sums0, y_part0, r, rank, ranks);
     else
       verify_pass<false>(a, &s, sums0, y_part0, r, rank, ranks);
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
     }
   }
   if (nodes > 0) {
-    const VerifyRows r = verify_rows(a, seq + at);
+    VerifyRows r = verify_rows(a, seq + at, removed > 0);
     const int chunks = (a.V + r.shift + kVerifyChunk - 1) / kVerifyChunk;
     if (stale) {
       upto = verify_runs(sums, chunks);
@@ -525,6 +530,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
       // weights then, summed by this warp alone
       removed = 0;
       A = none;
+      r.q = nullptr;
 #pragma unroll 1
       for (int i = 0; i < chunks; ++i) {
         const Pair z = verify_chunk_alone(a, &s, r, i, 0);

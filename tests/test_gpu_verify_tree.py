@@ -262,3 +262,28 @@ def test_binding_refuses():
     for kw in (dict(max_accept=0), dict(max_accept=513), dict(draft_probs=t(c.p[:, :, :39])), dict(node_counts=t(c.nodes[:3]))):
         with pytest.raises(pkv.PkvError):
             pkv.verify_tree(*good, **kw)
+
+
+def test_draft_values_that_are_no_probabilities():
+    # in rows that lose children: each counts as 0, at the children's own tokens too
+    rng = np.random.Generator(np.random.PCG64(8370))
+    c = Case(8370, 24, 7, 700, noise=2.0, reach=3)
+    c.r[:] = np.float32(0.999)
+    for value in (-0.25, -np.inf, np.inf, np.nan):
+        for b in range(c.B):
+            c.q[b, :, rng.choice(c.V, 20, replace=False)] = value
+    at = c.tokens[:12, 1]
+    c.q[np.arange(12), c.parents[:12, 1], at] = np.array([np.nan, np.inf, -np.inf, -1.0] * 3, np.float32)
+    _, count, _ = c.check()
+    assert (count == 1).any() and (count > 1).any()
+
+
+@pytest.mark.parametrize("pad", [0, 1])
+def test_draft_rows_of_nodes_without_children_are_not_read(pad):
+    c = Case(8380, 20, 9, 1500, noise=0.3)
+    for b in range(c.B):
+        leaf = ~np.isin(np.arange(c.T), c.parents[b])
+        c.q[b, leaf] = np.nan
+    c.r[:10] = 0.0  # (the walk ends at a leaf)
+    want, count, _ = c.check(pad)
+    assert all(want[b, count[b] - 1] not in c.parents[b] for b in range(10))

@@ -44,7 +44,7 @@ def _rope(lib, desc=None, freqs=None, axes=None, **kw):
     (3, dict(pos=ctypes.c_void_p(0x40000002))), (3, dict(slots=ctypes.c_void_p(0x50000004))), (1, dict(out=_p(2))), (1, dict(out=_p(5))),
     (1, dict(out=ctypes.c_void_p(0x10000000 + 4096))), (1, dict(out=_p(7))), (1, dict(os=32 * 128 + 8, out=_p(1))),
     (1, dict(desc=dict(dtype=1))), (1, dict(desc=dict(dtype=2), ksc=_p(9))), (3, dict(desc=dict(dtype=2), ksc=_p(9), vsc=ctypes.c_void_p(0xa0000004))),
-    (2, dict(desc=dict(head_dim=96))), (2, dict(desc=dict(dtype=1, head_dim=64), R=64)),
+    (2, dict(desc=dict(head_dim=96))), (2, dict(desc=dict(dtype=1, head_dim=64), R=64)), (2, dict(N=1 << 26)), (2, dict(N=(1 << 31) - 1)),
 ])
 def test_rope_append_refuses(lib, want, kw):
     assert _rope(lib, **kw) == want, lib.pkv_last_error_message()
