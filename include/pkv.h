@@ -464,8 +464,9 @@ pkv_status pkv_decode_tree_describe(const pkv_cache_desc* cache, int32_t batch,
  *   workspace      pkv_decode_packed_workspace_bytes() bytes.
  *   opts           partition_blocks is the fewest blocks of a work share, math
  *                  PKV_MATH_AUTO or PKV_MATH_TC; warps and stages have no
- *                  effect.  (On one-byte caches the v scales are carried as in
- *                  pkv_paged_decode_tree.)
+ *                  effect.  (On one-byte caches the weights are f16, with
+ *                  fewer than 11 bits below 2^-14 of the row's largest, and
+ *                  carry the v scales as in pkv_paged_decode_tree.)
  *   everything else as in pkv_paged_decode_multi.  G <= 128.
  */
 pkv_status pkv_paged_decode_packed(const pkv_cache_desc* cache,

@@ -287,3 +287,14 @@ def test_draft_rows_of_nodes_without_children_are_not_read(pad):
     c.r[:10] = 0.0  # (the walk ends at a leaf)
     want, count, _ = c.check(pad)
     assert all(want[b, count[b] - 1] not in c.parents[b] for b in range(10))
+
+
+@pytest.mark.parametrize("draft", [True, False])
+def test_the_largest_vocabulary(draft):
+    V = 1 << 20
+    c = Case(8390, 6, 3, V, draft, sharp=0.3)
+    c.tokens[3:, 1:] = V - 1  # (unlikely children: rejected)
+    c.r[3:] = np.float32(0.999)
+    c.u[:] = [0.0, 0.3, 0.9999, 0.01, 0.51, 0.99]
+    c.check()
+    c.check(pad=1)
