@@ -28,6 +28,14 @@
 // gathered beforehand, side by side) and tells the others by distributed shared
 // memory which row to sum next; the CTAs take its chunks of 512 values in turn.
 // Only the first CTA decides, so the others cannot come to another end.
+//
+// Measured: 64 sequences, 32 nodes, 128,256 tokens, drawn drafts 48 us (1.75 passes
+// a sequence on average, 5 in the slowest: the first from HBM together, then a few
+// sequences' in turn, each with two cluster barriers of 0.8 us, the rows' latency
+// and the first warp's decision); 48 sequences, 21 nodes, 50,257 tokens, drafts
+// without randomness 16 us (one pass each); one sequence, 8 nodes, 32,000 tokens 9
+// to 17 us, by its passes.  (A pass without the copies ahead: 54 us; with its later
+// chunks prefetched to L2 instead: 58.)
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -43,6 +51,7 @@ constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyChunk = 512;  // values that a warp sums at a time
 constexpr int kPer = kVerifyChunk / 32;
+constexpr int kVerifyMaxChunks = (PKV_MAX_VOCAB + 3 + kVerifyChunk - 1) / kVerifyChunk;
 constexpr int kVerifyCluster = 16;  // most CTAs of a cluster (more than 8 by a launch attribute of the kernel)
 
 // An unevaluated sum hi + lo.
@@ -115,7 +124,11 @@ struct VerifyShared {
   // the nodes (first CTA)
   int token[PKV_MAX_QUERY_TOKENS], parent[PKV_MAX_QUERY_TOKENS];
   float r[PKV_MAX_QUERY_TOKENS], p[PKV_MAX_QUERY_TOKENS], q[PKV_MAX_QUERY_TOKENS];
-  Pair weights[kVerifyChunk / 16 * 17];  // of the chunk that the token is drawn from (verify_pad)
+  union {
+    // the next chunk of a warp's pass, p and q, on its way
+    alignas(16) float stage[kVerifyWarps][2][kVerifyChunk];
+    Pair weights[kVerifyChunk / 16 * 17];  // of the chunk that the token is drawn from (verify_pad)
+  };
 };
 
 // Rows start at any float.  Their chunks are counted from the 16-byte boundary
@@ -201,26 +214,69 @@ __device__ __noinline__ Pair verify_chunk_alone(const VerifyArgs& a, const Verif
   return warp_total(verify_sum([&](int k) { return weight(pv[k]); }));
 }
 
+// A lane's 16 bytes from global to shared memory, asynchronously.
+__device__ __forceinline__ void copy_16(float* to, const float* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))), "l"(from) : "memory");
+}
+
 // This CTA's chunks of the row: sums of max(p - A q, 0) to the first CTA's
-// `sums`, this warp's sum of the Q that are left to its y_part.
+// `sums`, this warp's sum of the Q that are left to its y_part.  A warp's next
+// chunk is on its way to shared memory while it sums one; each lane reads what
+// it copied itself.
 template <bool DRAFT>
-__device__ __forceinline__ void verify_pass(const VerifyArgs& a, const VerifyShared* s, Pair* sums0, Pair* y_part0, const VerifyRows& r,
+__device__ __forceinline__ void verify_pass(const VerifyArgs& a, VerifyShared* s, Pair* sums0, Pair* y_part0, const VerifyRows& r,
                                             int rank, int ranks) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float ah = s->ah, al = s->al;
-  const int removed = s->removed, chunks = (a.V + r.shift + kVerifyChunk - 1) / kVerifyChunk;
+  const int removed = s->removed, chunks = (a.V + r.shift + kVerifyChunk - 1) / kVerifyChunk, apart = kVerifyWarps * ranks;
   const bool want_y = s->want_y != 0;
+  float* p_stage = s->stage[warp][0] + 4 * lane;
+  float* q_stage = s->stage[warp][1] + 4 * lane;
+  // whole chunks of aligned rows are copied, others loaded when their turn comes
+  auto copied = [&](int i) { return r.vec && i * kVerifyChunk >= r.shift && (i + 1) * kVerifyChunk - r.shift <= a.V; };
+  auto fetch = [&](int i) {
+    if (i < chunks && copied(i)) {
+      const int e = i * kVerifyChunk - r.shift + 4 * lane;
+#pragma unroll
+      for (int k = 0; k < kVerifyChunk; k += 128) {
+        copy_16(p_stage + k, r.p + e + k);
+        if constexpr (DRAFT) copy_16(q_stage + k, r.q + e + k);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto take = [&](float (&x)[kPer], const float* from) {
+#pragma unroll
+    for (int k = 0; k < kPer; k += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(from + 32 * k);
+      x[k] = v.x;
+      x[k + 1] = v.y;
+      x[k + 2] = v.z;
+      x[k + 3] = v.w;
+    }
+  };
   Pair y{0.f, 0.f};
+  fetch(warp * ranks + rank);
 #pragma unroll 1
-  for (int i = warp * ranks + rank; i < chunks; i += kVerifyWarps * ranks) {
+  for (int i = warp * ranks + rank; i < chunks; i += apart) {
+    const int e0 = i * kVerifyChunk - r.shift;
+    float pv[kPer];
+    [[maybe_unused]] float qv[kPer];
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (copied(i)) {
+      take(pv, p_stage);
+      if constexpr (DRAFT) take(qv, q_stage);
+    } else {
+      verify_load(pv, r.p, e0, a.V, lane, r.vec);
+      if constexpr (DRAFT) verify_load(qv, r.q, e0, a.V, lane, r.vec);
+    }
+    __syncwarp();  // (read before it is written again)
+    fetch(i + apart);
     if constexpr (!DRAFT) {
-      const Pair z = verify_chunk_alone(a, s, r, i, removed);
+      verify_drop(pv, s, removed, e0, lane);
+      const Pair z = warp_total(verify_sum([&](int k) { return weight(pv[k]); }));
       if (lane == 0) sums0[i] = z;
     } else {
-      const int e0 = i * kVerifyChunk - r.shift;
-      float pv[kPer], qv[kPer];
-      verify_load(pv, r.p, e0, a.V, lane, r.vec);
-      verify_load(qv, r.q, e0, a.V, lane, r.vec);
       const Pair z = warp_total(verify_sum([&](int k) { return weight_left(pv[k], qv[k], ah, al); }));
       if (lane == 0) sums0[i] = z;
       if (want_y) {
@@ -568,10 +624,15 @@ cudaError_t launch_verify_tree(const VerifyArgs& a, int num_sms, cudaStream_t st
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  const size_t smem = sizeof(Pair) * static_cast<size_t>(chunks);
+  if (sizeof(VerifyShared) + smem > 48 * 1024) {  // (above 350,000 tokens)
+    cudaError_t e = cudaFuncSetAttribute(verify_tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Pair) * kVerifyMaxChunks);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(a.B) * ranks);
   cfg.blockDim = dim3(kVerifyThreads);
-  cfg.dynamicSmemBytes = sizeof(Pair) * static_cast<size_t>(chunks);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
