@@ -7,32 +7,45 @@
 // tree and to the nodes of its mask row (tree_mask.cuh).  The rows form tiles
 // of 128 (M of the MMA); the cache is stepped through 128 tokens at a time.
 //
+// PACKED: sequences of any count of rows, the last m of their n tokens, causal
+// among themselves, packed one behind the other (packed_plan.cuh); a work item is
+// a run of rows (the tiles of a CTA) on one KV head, and its steps end where its
+// last row's positions do.
+//
 // What bounds it: with one tile of rows the cache bytes, 64 KiB (bf16, D 128)
 // or 32 KiB (one byte) per 128 tokens of one KV head, 1.47 or 0.73 us of an
 // SM's share of the measured HBM rate, next to 0.67 us of tensor pipe (at the
 // measured bf16 rate) for S = Q K^T and O += P V; with two tiles the tensor
 // pipe, 1.34 us.  Measured per step of 128 tokens with the cache in L2: bf16
-// 0.87 to 1.0 us with one tile, 1.65 with two (D 64: 0.70 to 0.76, 1.42), E4M3
-// 1.15 to 1.35 and 2.3, INT8 1.65 to 1.75 and 2.7.  So bf16 batches of one tile
-// run at HBM speed (64 sequences of 2048 to 4096 tokens, 32 nodes, 8 KV heads:
-// 156 us with plan and merge, 0.80 of the copy rate), long contexts with many
-// rows at 0.64 of the bf16 peak (4 x 32k tokens, 64 nodes, 8 heads a KV head:
-// 218 us).  One-byte caches fill no unit: a sub-partition issues 1600
+// 0.87 to 1.0 us with one tile, 1.5 to 1.6 with two (D 64: 0.70 to 0.76, 1.4),
+// E4M3 1.15 to 1.35 and 2.2, INT8 1.65 to 1.75 and 2.7.  So bf16 batches of one
+// tile run at HBM speed (64 sequences of 2048 to 4096 tokens, 32 nodes, 8 KV
+// heads: 151 us with plan and merge, 0.83 of the copy rate), long contexts with
+// many rows at 0.70 of the bf16 peak (4 x 32k tokens, 64 nodes, 8 heads a KV head:
+// 198 us), a prompt of 8192 tokens (32 / 8 heads, packed) at 0.68 (418 us).
+// One-byte caches fill no unit: a sub-partition issues 1600
 // instructions a step, against 940 of bf16 caches, for the page scales and the
 // widening, but only 60% (E4M3) or 53% (INT8) of the time, with DRAM at 41 and
 // 29% and the tensor pipe at 38 and 27%: a step is a chain of hand-overs (codes
-// landed, widened, S, the maximum agreed, P, PV).
+// landed, widened, S, the maximum agreed, P, PV).  So are D 64 pairs (tensor pipe
+// 28%, issue slots 58%): the softmax of a step takes as long as with D 128, its
+// products half.
 //
 // One CTA per SM, no CTA-wide barrier inside the loop:
-//   * Two streams of eight softmax warps, each stream with its own S and O in
-//     tensor memory (S0 S1 O0 O1, 128 columns each), so that the products of
-//     one run while the other's softmax does.  Two warps share 32 rows, one
+//   * Two streams of eight softmax warps, each stream with its own O in tensor
+//     memory, so that the products of one run while the other's softmax does.
+//     D 128: an S buffer a stream (S0 S1 O0 O1, 128 columns each); D 64: three S
+//     buffers in turn (S0 S1 S2, then O0 O1 of 64 columns), so that S of the next
+//     step does not wait for PV of this one (packed prompts 163 -> 161 us).  Two warps share 32 rows, one
 //     half of the step's tokens each: a row's exponentials then take half as
 //     long between S and PV (one warp per 32 rows: 90 instead of 79 us for the
 //     D 64 batch).  PAIR: the streams hold two row tiles of one KV head and
-//     read every step of the cache together.  Otherwise there is one row tile,
-//     stream 0 takes the even steps and stream 1 the odd ones, and a work unit
-//     ends with the sum of the two (as split-K partials would be joined).
+//     read every step of the cache together; a unit whose rows fit one tile runs
+//     the loop for a single tile instead (packed batches of prompts' chunks and
+//     single tokens: 441 -> 348 us with the items' weights).  Without PAIR there
+//     is one row tile, stream 0 takes the even steps and stream 1 the odd ones,
+//     and a work unit ends with the sum of the two (as split-K partials would be
+//     joined).
 //   * One thread issues, step after step, PV_i of the stream's step before and
 //     S_i of this one; P (16 bits) overwrites the S columns it came from and is
 //     the A operand of PV.  tcgen05 operations of one thread complete in order,
@@ -40,6 +53,12 @@
 //     three S buffers with one O, 0.95 instead of 0.87 us a step; PV of the
 //     first 32 tokens of each half while the others' P is made, 1.71 instead
 //     of 1.65 for two tiles.)
+//   * The two halves of a row agree on its maximum.  But for single tiles of D 64,
+//     whose items are short, the weights are made ahead, with the maximum of the
+//     steps before, while the agreement is under way, and made again only where it
+//     moved.  It can only move where a step's weights add up to more than 2^8, so else
+//     it is not even looked for.  (Agreed first: packed prompt 448 instead of 421 us,
+//     head_dim 64 164 instead of 155, E4M3 383 instead of 361.)
 //   * A K copy warp walks the CTA's share of the work, publishes a descriptor
 //     per step (page ids, page parameters) in a ring, and copies K pages; a V
 //     copy warp copies V pages; for bf16 caches a query warp the query tiles.
@@ -48,6 +67,9 @@
 //     in the type of the K operand (E4M3 K pages feed the products as they
 //     are, against a query of two E4M3 parts).  Four of them took 2.25 instead
 //     of 1.68 us an INT8 step.  The page scales multiply the scores and P.
+//   * Rows are stored from registers: four lanes exchange their 16-byte pieces, so
+//     that each store instruction fills 64 bytes of a row (staged in shared memory
+//     first: no faster, and it waits for the query tile's last product).
 //
 // Work split ("stream-K"): the steps of all (sequence, KV head) items in a row
 // are cut into equal shares, one per SM, whatever the lengths; a share that
@@ -1063,10 +1085,10 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           }
           // After a unit's first step the exponentials are made while the warps
           // have yet to agree that the maximum stays, and made again where it
-          // does not (1.65 -> 1.5 us a step of two bf16 tiles).  Not for one tile
-          // of head_dim 64, whose items are short (71 instead of 64 us for the
-          // drafted trees' batch), and INT8 (239 instead of 202 us).
-          constexpr bool kAhead = !kI8 && (PAIR || D == 128);
+          // does not (1.65 -> 1.5 us a step of two bf16 tiles; drafted trees'
+          // batch on an INT8 cache 204 -> 190 us).  Not for one tile of head_dim
+          // 64, whose items are short (67 to 71 instead of 65 us).
+          constexpr bool kAhead = PAIR || D == 128;
           const bool ahead = kAhead && k > 0 && !(kOneByte && (flags & kStepScales));
           uint32_t x0[32], x1[32];
           if constexpr (!kAhead) {
@@ -1175,14 +1197,6 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             }
             exps(x0, pw, 0);
             exps(x0 + 16, pw + 8, 16);
-            if constexpr (kI8) {
-              // the second 32 scores are read again, so that 32 registers less
-              // are held meanwhile (the first 32's P covers only columns that
-              // are done with)
-              tc_st16(t_h, *reinterpret_cast<uint32_t(*)[16]>(pw));
-              tc_ld32(t_h + 32u, x1);
-              tc_wait_ld_regs(x1);
-            }
             if constexpr (kAhead) {
               if constexpr (kOneByte) tc_ld32(t_h + 32u, x1);
               tc_wait_ld_regs(x1);
@@ -1216,8 +1230,6 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
                 exps(y, pq, 16 * q);
                 tc_st8(t_h + 8u * q, pq);
               }
-            } else if constexpr (kI8) {
-              tc_st16(t_h + 16u, *reinterpret_cast<uint32_t(*)[16]>(pw + 16));
             } else {
               tc_st32(t_h, pw);
             }
