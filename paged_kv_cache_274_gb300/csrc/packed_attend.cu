@@ -16,15 +16,17 @@ constexpr int kPackedPlanThreads = 1024;
 constexpr int kPackedPlanSmem = 1024;  // sequences whose sums are searched in shared memory
 
 // Cost of an item besides its steps, in steps (tree_attend.cu).  Pairs of tiles,
-// measured: bf16 2 (head_dim 64: 4, 163 instead of 173 us for ragged prompts with
-// 2), E4M3 6 (377 us; 3: 429, 12: 384), INT8 9 (113 us; 3: 119, 12: 116).
+// measured: bf16 4 (a prompt of 8192 tokens 415 us; 2: 425, 3: 418, 5: 422), head_dim
+// 64 5 (ragged prompts 152 us; 3: 158, 4: 156, 7: 153), E4M3 6 (360 us; 3: 429, 5: 371,
+// 12: 384), INT8 9 (104 us; 5: 107, 12: 116).
 static int packed_item_steps(int kv_dtype, int D, bool pair) {
-  if (kv_dtype == PKV_KV_BF16) return pair && D == 128 ? 2 : 4;
+  if (kv_dtype == PKV_KV_BF16) return pair && D == 64 ? 5 : 4;
   return !pair || kv_dtype == PKV_KV_FP8_E4M3 ? 6 : 9;
 }
 
 // What a step of an item with one row tile costs where CTAs serve pairs of
-// tiles, of kPackedWeight.
+// tiles, of kPackedWeight (chunks of prompts beside single tokens, bf16 6: 345 us,
+// 5: 356, 7: 365; INT8 5: 104 us, 4: 106, 6: 115; E4M3 5: 360 us, 4: 379, 6: 361).
 static int packed_alone(int kv_dtype) { return kv_dtype == PKV_KV_BF16 ? 6 : 5; }
 
 struct PackedPlanArgs {
