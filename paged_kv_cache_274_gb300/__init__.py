@@ -14,13 +14,22 @@ Layouts (see the header for the full contract):
   q, out            bfloat16 [B][Hq][D];
   block_tables      int32 [B][MB];  context_lens int32 [B];
   kv_group_ptr      host int32 [L] (shared-with pointer per layer);
-  tree_mask         int32 [B or 1][T][ceil(T / 32)], the bits of a drafted tree's nodes.
+  tree_mask         int32 [B or 1][T][ceil(T / 32)], the bits of a drafted tree's nodes;
+  packed rows       bfloat16 [N][Hq][D], request b's at query_starts[b] ..
+                    query_starts[b + 1] - 1 (int32 [B + 1]).
+
+A step of continuous batching (prompts, chunks of them and single tokens in one
+batch):
+  :func:`extend_tables` (blocks, slots and positions of the packed rows), then
+  per layer :func:`rope_append` (norms and rotation of queries and keys, keys
+  and values into their slots) and :func:`paged_decode_packed`.
 
 A step of speculative decoding with drafted trees:
-  :func:`extend_tables` (blocks and slots for the nodes), :func:`kv_append`,
-  :func:`tree_masks` (what each node sees, and its position),
-  :func:`paged_decode_tree` per layer, and, once the target model has chosen
-  a path, :func:`compact_tokens` (with the step's ``new_lens`` and
+  :func:`extend_tables` (blocks and slots for the nodes), :func:`tree_masks`
+  (what each node sees, and its position), per layer :func:`rope_append` (or
+  :func:`kv_append`) and :func:`paged_decode_tree`, then :func:`verify_tree`
+  (the path that the target model's probabilities accept, and the token behind
+  it) and :func:`compact_tokens` (with the step's ``new_lens`` and
   ``prev_seq_lens``, so that a request without room keeps its tokens).
 """
 from __future__ import annotations

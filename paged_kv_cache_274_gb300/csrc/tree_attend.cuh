@@ -34,7 +34,7 @@
 // One CTA per SM, no CTA-wide barrier inside the loop:
 //   * Two streams of eight softmax warps, each stream with its own O in tensor
 //     memory, so that the products of one run while the other's softmax does.
-//     D 128: an S buffer a stream (S0 S1 O0 O1, 128 columns each); D 64: three S
+//     An S buffer a stream (S0 S1 O0 O1, 128 columns each); pairs of D 64: three S
 //     buffers in turn (S0 S1 S2, then O0 O1 of 64 columns), so that S of the next
 //     step does not wait for PV of this one (packed prompts 163 -> 161 us).  Two warps share 32 rows, one
 //     half of the step's tokens each: a row's exponentials then take half as
@@ -69,7 +69,7 @@
 //     of 1.68 us an INT8 step.  The page scales multiply the scores and P.
 //   * Rows are stored from registers: four lanes exchange their 16-byte pieces, so
 //     that each store instruction fills 64 bytes of a row (staged in shared memory
-//     first: no faster, and it waits for the query tile's last product).
+//     first: no faster).
 //
 // Work split ("stream-K"): the steps of all (sequence, KV head) items in a row
 // are cut into equal shares, one per SM, whatever the lengths; a share that
@@ -96,11 +96,11 @@ namespace pkv {
 constexpr int kTaRows = 128;    // query rows per tile
 constexpr int kTaRing = 8;      // step descriptors: a step's is read until its softmax is done, at most 5 steps back
 constexpr uint32_t kTaCols = 512;
-// TMEM: S buffers of 128 columns from 0 on, then O0 and O1 of D columns.  With
-// head_dim 128 a buffer per stream, with 64 three in turn.
-__host__ __device__ constexpr int ta_buffers(int D) { return D == 64 ? 3 : 2; }
-__host__ __device__ constexpr uint32_t ta_o_col(int D, int i) { return static_cast<uint32_t>(128 * ta_buffers(D) + D * i); }
-static_assert(ta_o_col(64, 2) <= kTaCols && ta_o_col(128, 2) <= kTaCols, "");
+// TMEM: S buffers of 128 columns from 0 on, then O0 and O1 of D columns.  A buffer
+// per stream; pairs of head_dim 64 have three in turn.
+__host__ __device__ constexpr int ta_buffers(int D, bool pair) { return D == 64 && pair ? 3 : 2; }
+__host__ __device__ constexpr uint32_t ta_o_col(int D, bool pair, int i) { return static_cast<uint32_t>(128 * ta_buffers(D, pair) + D * i); }
+static_assert(ta_o_col(64, true, 2) <= kTaCols && ta_o_col(128, true, 2) <= kTaCols, "");
 
 struct TaParams {
   const __nv_bfloat16* q;
@@ -179,7 +179,7 @@ struct TaLayout {  // byte offsets from the 1024-aligned shared-memory base
   static constexpr uint32_t kBars = kV + kVStages * kTile;
   // k_full k_free tma_k [K], v_full v_free tma_v [V], s_full p_full [buffers],
   // o_full o_free pv_done [2], step_full [ring], q_full q_free q_read x_full mma_drain
-  static constexpr int kNumBars = 3 * kKStages + 3 * kVStages + 2 * ta_buffers(D) + 6 + kTaRing + 5;
+  static constexpr int kNumBars = 3 * kKStages + 3 * kVStages + 2 * ta_buffers(D, PAIR) + 6 + kTaRing + 5;
   static constexpr uint32_t kMisc = kBars + 8 * kNumBars;
   static constexpr uint32_t kRing = (kMisc + 4 + 15) & ~15u;
   static constexpr uint32_t kStep = kOneByte ? sizeof(TaStep) : offsetof(TaStep, par);
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
   static_assert(!kOneByte || D == 128, "one-byte pages need head_dim 128");
   constexpr int PPI = kTreeTokens / BS;  // pages per step
   constexpr int KS = L::kKStages, VS = L::kVStages;
-  constexpr int kHalves = D / 64, kBufs = ta_buffers(D);
+  constexpr int kHalves = D / 64, kBufs = ta_buffers(D, PAIR);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   // Barrier phases: k_* and v_* rings by the CTA's running step index g (stage
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_bf16_ts(tmem + ta_o_col(D, 0) + D * i, tmem + 128u * buf + 64u * h + 8u * kk, vd + (h * 4 + kk) * (2048 >> 4), kIdescO,
+            tc_mma_bf16_ts(tmem + ta_o_col(D, PAIR, 0) + D * i, tmem + 128u * buf + 64u * h + 8u * kk, vd + (h * 4 + kk) * (2048 >> 4), kIdescO,
                            !first || h > 0 || kk > 0);
         ++mma_issued;
         if (!two || i == 1) {
@@ -953,7 +953,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
     const int i = warp >> 3, hh = (warp >> 2) & 1, r = 32 * (warp & 3) + lane;
     const int pair_bar = 1 + (warp & 3) + 4 * i;  // named barrier of the two warps
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_o = tmem + lane_base + ta_o_col(D, 0);  // O0; O1 is D columns on
+    const uint32_t t_o = tmem + lane_base + ta_o_col(D, PAIR, 0);  // O0; O1 is D columns on
     const float c = p.scale_log2;
     const int tl = r / p.G;
     float* xch = reinterpret_cast<float*>(sm + L::kXml);
@@ -1197,6 +1197,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             }
             exps(x0, pw, 0);
             exps(x0 + 16, pw + 8, 16);
+            if constexpr (!kAhead) tc_st16(t_h, *reinterpret_cast<uint32_t(*)[16]>(pw));
             if constexpr (kAhead) {
               if constexpr (kOneByte) tc_ld32(t_h + 32u, x1);
               tc_wait_ld_regs(x1);
@@ -1230,6 +1231,8 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
                 exps(y, pq, 16 * q);
                 tc_st8(t_h + 8u * q, pq);
               }
+            } else if constexpr (!kAhead) {
+              tc_st16(t_h + 16u, *reinterpret_cast<uint32_t(*)[16]>(pw + 16));
             } else {
               tc_st32(t_h, pw);
             }
@@ -1415,19 +1418,13 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           uint32_t w[16];
           float o[16];
           columns(cc, o);
-          if (cols == 16 && part == 0) {  // 32 bytes a row: two lanes
+          if (cols == 16 && part == 0) {  // 32 bytes a row: nothing to gain
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t got = __shfl_xor_sync(kFull, (quad & 1) ? w[e] : w[4 + e], 1);
-              if (quad & 1) w[e] = got; else w[4 + e] = got;
-            }
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-              const int to = (quad & 2) ? rows4[2 + ch] : rows4[ch];
-              if (to >= 0)
-                *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(to) * D + cc + 8 * (quad & 1)) = make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
+            if (in_tile) {
+              uint4* to = reinterpret_cast<uint4*>(p.out + static_cast<size_t>(row_out) * D + cc);
+              to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              to[1] = make_uint4(w[4], w[5], w[6], w[7]);
             }
             continue;
           }
