@@ -111,6 +111,16 @@ __device__ __forceinline__ Pair warp_total(Pair x) {
   }
   return x;
 }
+// Of two, side by side.
+__device__ __forceinline__ void warp_totals(Pair& x, Pair& y) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Pair u{__shfl_xor_sync(kFull, x.hi, o), __shfl_xor_sync(kFull, x.lo, o)};
+    const Pair v{__shfl_xor_sync(kFull, y.hi, o), __shfl_xor_sync(kFull, y.lo, o)};
+    add_to(x, u);
+    add_to(y, v);
+  }
+}
 
 struct VerifyShared {
   // what to sum next, written by the cluster's first CTA
@@ -255,13 +265,19 @@ __device__ __forceinline__ void verify_pass(const VerifyArgs& a, VerifyShared* s
       x[k + 3] = v.w;
     }
   };
-  Pair y{0.f, 0.f};
+  Pair y{0.f, 0.f}, held{0.f, 0.f};  // the lane's part of the chunk before
+  int held_at = -1;
   fetch(warp * ranks + rank);
 #pragma unroll 1
   for (int i = warp * ranks + rank; i < chunks; i += apart) {
     const int e0 = i * kVerifyChunk - r.shift;
     float pv[kPer];
     [[maybe_unused]] float qv[kPer];
+    if (held_at >= 0) {  // (while the copies are on their way)
+      const Pair z = warp_total(held);
+      if (lane == 0) sums0[held_at] = z;
+    }
+    held_at = i;
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (copied(i)) {
       take(pv, p_stage);
@@ -274,20 +290,19 @@ __device__ __forceinline__ void verify_pass(const VerifyArgs& a, VerifyShared* s
     fetch(i + apart);
     if constexpr (!DRAFT) {
       verify_drop(pv, s, removed, e0, lane);
-      const Pair z = warp_total(verify_sum([&](int k) { return weight(pv[k]); }));
-      if (lane == 0) sums0[i] = z;
+      held = verify_sum([&](int k) { return weight(pv[k]); });
     } else {
-      const Pair z = warp_total(verify_sum([&](int k) { return weight_left(pv[k], qv[k], ah, al); }));
-      if (lane == 0) sums0[i] = z;
+      held = verify_sum([&](int k) { return weight_left(pv[k], qv[k], ah, al); });
       if (want_y) {
         verify_drop(qv, s, removed, e0, lane);
         add_to(y, verify_sum([&](int k) { return weight(qv[k]); }));
       }
     }
   }
-  if (want_y) {
-    y = warp_total(y);
-    if (lane == 0) y_part0[rank * kVerifyWarps + warp] = y;
+  warp_totals(held, y);
+  if (lane == 0) {
+    if (held_at >= 0) sums0[held_at] = held;
+    if (want_y) y_part0[rank * kVerifyWarps + warp] = y;
   }
 }
 
@@ -313,13 +328,14 @@ __device__ __forceinline__ Pair warp_before(const Pair& upto) {
 
 // Sums of n pairs, a run of them per lane: up to each run's end.  One warp.
 __device__ __forceinline__ int verify_run(int n) { return (n + 31) / 32; }
-__device__ __forceinline__ Pair verify_runs(const Pair* x, int n) {
+__device__ __forceinline__ Pair verify_lane_run(const Pair* x, int n) {
   const int per = verify_run(n), i0 = min((static_cast<int>(threadIdx.x) & 31) * per, n), i1 = min(i0 + per, n);
   Pair t{0.f, 0.f};
 #pragma unroll 1
   for (int i = i0; i < i1; ++i) add_to(t, x[i]);
-  return warp_scan(t);
+  return t;
 }
+__device__ __forceinline__ Pair verify_runs(const Pair* x, int n) { return warp_scan(verify_lane_run(x, n)); }
 
 // A lane's 16 values in a row, without bank conflicts among the lanes.
 __device__ __forceinline__ int verify_pad(int i) { return i + (i >> 4); }
@@ -567,11 +583,20 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
     if (last && (rank != 0 || warp != 0)) return;
     cluster_wait();
     if (rank == 0 && warp == 0) {
-      upto = verify_runs(sums, (a.V + r.shift + kVerifyChunk - 1) / kVerifyChunk);
+      const int n = (a.V + r.shift + kVerifyChunk - 1) / kVerifyChunk;
       stale = false;
-      z_sum = Z = from_lane(upto, 31);
-      if (s.want_y) y_sum = Y = from_lane(verify_runs(s.y_part, ranks * kVerifyWarps), 31);
-      if (last) break;
+      if (last) {
+        upto = verify_runs(sums, n);
+        z_sum = Z = from_lane(upto, 31);
+        break;
+      }
+      // (the runs' ends wait until a token is drawn)
+      stale = true;
+      Z = verify_lane_run(sums, n);
+      Pair y = s.want_y ? verify_lane_run(s.y_part, ranks * kVerifyWarps) : none;
+      warp_totals(Z, y);
+      z_sum = Z;
+      if (s.want_y) y_sum = Y = y;
     }
   }
   if (nodes > 0) {
