@@ -194,25 +194,70 @@ __device__ __forceinline__ void verify_drop(float (&x)[kPer], const VerifyShared
   }
 }
 
-// Sum of a lane's values, four running sums side by side.  Each keeps what its
-// additions round away in `lo`.
-template <typename F>
+// Two floats a register pair: one instruction rounds both as it would each.
+using F2 = uint64_t;
+__device__ __forceinline__ F2 both(float x, float y) { return static_cast<uint64_t>(__float_as_uint(y)) << 32 | __float_as_uint(x); }
+__device__ __forceinline__ float first(F2 x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float second(F2 x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
+__device__ __forceinline__ F2 add2(F2 x, F2 y) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return d;
+}
+__device__ __forceinline__ F2 mul2(F2 x, F2 y) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return d;
+}
+__device__ __forceinline__ F2 fma2(F2 x, F2 y, F2 z) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  return d;
+}
+__device__ __forceinline__ F2 sub2(F2 x, F2 y) { return fma2(y, both(-1.f, -1.f), x); }
+
+// Two unevaluated sums.
+struct Pairs {
+  F2 hi, lo;
+};
+// weight_left of two elements, q cleaned.
+__device__ __forceinline__ Pairs weights_left(F2 p, F2 q, float ah, float al) {
+  const F2 nh = mul2(both(-ah, -ah), q);
+  const F2 l = fma2(both(al, al), q, fma2(both(ah, ah), q, nh));
+  const F2 d = add2(p, nh);
+  const F2 lo = sub2(add2(sub2(p, d), nh), l), v = add2(d, lo);
+  const bool some0 = first(v) > 0.f, some1 = second(v) > 0.f;
+  return {both(some0 ? first(d) : 0.f, some1 ? second(d) : 0.f), both(some0 ? first(lo) : 0.f, some1 ? second(lo) : 0.f)};
+}
+
+// Sum of a lane's values, at(k) those of k and k + 1, four running sums side by
+// side.  Each keeps what its additions round away in `lo`.  PARTS: the values
+// have low parts.
+template <bool PARTS, typename F>
 __device__ __forceinline__ Pair verify_sum(F&& at) {
-  Pair s[4];
+  Pairs s[2];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const Pair w = at(k);
+  for (int k = 0; k < kPer; k += 2) {
+    const Pairs w = at(k);
+    Pairs& t = s[k / 2 % 2];
     if (k < 4) {
-      s[k] = w;
+      t = w;
     } else {
-      const Pair t = two_sum(s[k % 4].hi, w.hi);
-      s[k % 4] = {t.hi, __fadd_rn(s[k % 4].lo, __fadd_rn(t.lo, w.lo))};
+      const F2 a = t.hi, sum = add2(a, w.hi), u = sub2(sum, a);
+      F2 lost = add2(sub2(a, sub2(sum, u)), sub2(w.hi, u));
+      if (PARTS) lost = add2(lost, w.lo);
+      t = {sum, add2(t.lo, lost)};
     }
   }
-  add_to(s[0], s[1]);
-  add_to(s[2], s[3]);
-  add_to(s[0], s[2]);
-  return s[0];
+  Pair x{first(s[0].hi), first(s[0].lo)}, y{first(s[1].hi), first(s[1].lo)};
+  add_to(x, Pair{second(s[0].hi), second(s[0].lo)});
+  add_to(y, Pair{second(s[1].hi), second(s[1].lo)});
+  add_to(x, y);
+  return x;
+}
+// Of plain weights.
+__device__ __forceinline__ Pair verify_sum_of(const float (&x)[kPer]) {
+  return verify_sum<false>([&](int k) { return Pairs{both(clean(x[k]), clean(x[k + 1])), 0ull}; });
 }
 
 // Sum of chunk i of the target's weights without the removed tokens.
@@ -221,7 +266,7 @@ __device__ __noinline__ Pair verify_chunk_alone(const VerifyArgs& a, const Verif
   float pv[kPer];
   verify_load(pv, r.p, e0, a.V, lane, r.vec);
   verify_drop(pv, s, removed, e0, lane);
-  return warp_total(verify_sum([&](int k) { return weight(pv[k]); }));
+  return warp_total(verify_sum_of(pv));
 }
 
 // A lane's 16 bytes from global to shared memory, asynchronously.
@@ -290,12 +335,14 @@ __device__ __forceinline__ void verify_pass(const VerifyArgs& a, VerifyShared* s
     fetch(i + apart);
     if constexpr (!DRAFT) {
       verify_drop(pv, s, removed, e0, lane);
-      held = verify_sum([&](int k) { return weight(pv[k]); });
+      held = verify_sum_of(pv);
     } else {
-      held = verify_sum([&](int k) { return weight_left(pv[k], qv[k], ah, al); });
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) qv[k] = clean(qv[k]);
+      held = verify_sum<true>([&](int k) { return weights_left(both(pv[k], pv[k + 1]), both(qv[k], qv[k + 1]), ah, al); });
       if (want_y) {
         verify_drop(qv, s, removed, e0, lane);
-        add_to(y, verify_sum([&](int k) { return weight(qv[k]); }));
+        add_to(y, verify_sum<false>([&](int k) { return Pairs{both(qv[k], qv[k + 1]), 0ull}; }));
       }
     }
   }
