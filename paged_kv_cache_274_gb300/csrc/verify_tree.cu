@@ -29,13 +29,16 @@
 // memory which row to sum next; the CTAs take its chunks of 512 values in turn.
 // Only the first CTA decides, so the others cannot come to another end.
 //
-// Measured: 64 sequences, 32 nodes, 128,256 tokens, drawn drafts 48 us (1.75 passes
-// a sequence on average, 5 in the slowest: the first from HBM together, then a few
-// sequences' in turn, each with two cluster barriers of 0.8 us, the rows' latency
-// and the first warp's decision); 48 sequences, 21 nodes, 50,257 tokens, drafts
-// without randomness 16 us (one pass each); one sequence, 8 nodes, 32,000 tokens 9
-// to 17 us, by its passes.  (A pass without the copies ahead: 54 us; with its later
-// chunks prefetched to L2 instead: 58.)
+// Measured: 64 sequences, 32 nodes, 128,256 tokens, drawn drafts 44 us (1.75 passes
+// a sequence on average, 5 or 6 in the slowest: the first from HBM together, 7 to 10
+// us, then a few sequences' in turn, each 3.7 us of sums, a chunk's latency from L2 at
+// a time, 2.2 of a cluster barrier and the first warp's decision and 0.7 of the other
+// barrier; 4 us at the end for the draw); 48 sequences, 21 nodes, 50,257 tokens,
+// drafts without randomness 15 to 17 us (a pass at each node that loses a child); one
+// sequence, 8 nodes, 32,000 tokens 8 to 19 us, by its passes.  Kept one by one for
+// the batch: the copies ahead 54 -> 48, two elements an instruction 46.4 -> 43.8.
+// (Later chunks prefetched to L2 at a pass's start: 58 instead of 54; the first chunk
+// by loads and the second copied beside it: 66, with 600 bytes of registers spilt.)
 #include <algorithm>
 
 #include <cooperative_groups.h>
