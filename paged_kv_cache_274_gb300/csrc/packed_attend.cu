@@ -15,13 +15,13 @@ namespace pkv {
 constexpr int kPackedPlanThreads = 1024;
 constexpr int kPackedPlanSmem = 1024;  // sequences whose sums are searched in shared memory
 
-// Cost of an item besides its steps, in steps (tree_attend.cu).  Pairs of tiles,
-// measured: bf16 4 (a prompt of 8192 tokens 415 us; 2: 425, 3: 418, 5: 422), head_dim
-// 64 5 (ragged prompts 152 us; 3: 158, 4: 156, 7: 153), E4M3 6 (360 us; 3: 429, 5: 371,
-// 12: 384), INT8 9 (104 us; 5: 107, 12: 116).
+// Cost of an item besides its steps, in steps (tree_attend.cu), measured for pairs
+// of tiles: bf16 4 (a prompt of 8192 tokens 405 us; with 2 and 5 some 5 us more),
+// head_dim 64 5 (ragged prompts 145 us; 3: 150, 4: 148), one byte 6 (E4M3 307 us; 2:
+// 350, 3: 329, 4: 310; INT8 90 us with 3 to 9).
 static int packed_item_steps(int kv_dtype, int D, bool pair) {
   if (kv_dtype == PKV_KV_BF16) return pair && D == 64 ? 5 : 4;
-  return !pair || kv_dtype == PKV_KV_FP8_E4M3 ? 6 : 9;
+  return 6;
 }
 
 // What a step of an item with one row tile costs where CTAs serve pairs of
