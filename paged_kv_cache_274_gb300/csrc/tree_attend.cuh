@@ -503,15 +503,6 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         base = ctx - (p.tree.node_counts != nullptr ? __ldg(p.tree.node_counts + b) : p.T);
       }
       const int* trow = p.block_tables + static_cast<size_t>(b) * p.MB + t0 / BS;
-      if constexpr (kOneByte) {  // the unit's queries, which the converters read once the unit before is done
-        const int lines = 2 * p.G;
-#pragma unroll 1
-        for (int x = lane; x < L::kQTiles * p.Tt * lines; x += 32) {
-          const int t = 2 * pair * p.Tt + x / lines;
-          if (t < (PACKED ? rows : p.T))
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (static_cast<size_t>(PACKED ? row0 + t : b * p.T + t) * p.Hq + kvh * p.G) * D + x % lines * 64));
-        }
-      }
       // lane i holds page i of a run of 32 pages, and of the next run (its id:
       // of the two next)
       auto load_ids = [&](int q) { return q < npages ? __ldg(trow + q) : 0; };
