@@ -18,15 +18,13 @@
 // measured bf16 rate) for S = Q K^T and O += P V; with two tiles the tensor
 // pipe, 1.34 us.  Measured per step of 128 tokens with the cache in L2: bf16
 // 0.87 to 1.0 us with one tile, 1.5 to 1.6 with two (D 64: 0.70 to 0.76, 1.4),
-// E4M3 1.15 to 1.35 and 2.2, INT8 1.65 to 1.75 and 2.7.  So bf16 batches of one
+// E4M3 1.15 to 1.35 and 2.0, INT8 1.5 and 2.2.  So bf16 batches of one
 // tile run at HBM speed (64 sequences of 2048 to 4096 tokens, 32 nodes, 8 KV
 // heads: 151 us with plan and merge, 0.83 of the copy rate), long contexts with
-// many rows at 0.70 of the bf16 peak (4 x 32k tokens, 64 nodes, 8 heads a KV head:
-// 198 us), a prompt of 8192 tokens (32 / 8 heads, packed) at 0.68 (418 us).
-// One-byte caches fill no unit: a sub-partition issues 1600
-// instructions a step, against 940 of bf16 caches, for the page scales and the
-// widening, but only 60% (E4M3) or 53% (INT8) of the time, with DRAM at 41 and
-// 29% and the tensor pipe at 38 and 27%: a step is a chain of hand-overs (codes
+// many rows at 0.72 of the bf16 peak (4 x 32k tokens, 64 nodes, 8 heads a KV head:
+// 194 us), a prompt of 8192 tokens (32 / 8 heads, packed) at 0.71 (401 us).
+// One-byte caches fill no unit: page scales and widening add two thirds to the
+// instructions of a step, and a step is a chain of hand-overs (codes
 // landed, widened, S, the maximum agreed, P, PV).  So are D 64 pairs (tensor pipe
 // 28%, issue slots 58%): the softmax of a step takes as long as with D 128, its
 // products half.
@@ -57,8 +55,8 @@
 //     whose items are short, the weights are made ahead, with the maximum of the
 //     steps before, while the agreement is under way, and made again only where it
 //     moved.  It can only move where a step's weights add up to more than 2^8, so else
-//     it is not even looked for.  (Agreed first: packed prompt 448 instead of 421 us,
-//     head_dim 64 164 instead of 155, E4M3 383 instead of 361.)
+//     it is not even looked for.  (Agreed first, when it was built: packed prompt 448
+//     instead of 421 us, head_dim 64 164 instead of 155, E4M3 383 instead of 361.)
 //   * A K copy warp walks the CTA's share of the work, publishes a descriptor
 //     per step (page ids, page parameters) in a ring, and copies K pages; a V
 //     copy warp copies V pages; for bf16 caches a query warp the query tiles.
