@@ -92,7 +92,7 @@
 namespace pkv {
 
 constexpr int kTaRows = 128;    // query rows per tile
-constexpr int kTaRing = 8;      // step descriptors: a step's is read until its softmax is done, at most 5 steps back
+constexpr int kTaRing = 8;      // step descriptors: a unit's last is read until its output is written, at most 7 steps back
 constexpr uint32_t kTaCols = 512;
 // TMEM: S buffers of 128 columns from 0 on, then O0 and O1 of D columns.  A buffer
 // per stream; pairs of head_dim 64 have three in turn.
@@ -532,7 +532,16 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           par_next = load_par(q0 + 32 + lane, id_next);
           id_after = load_ids(q0 + 64 + lane);
         }
-        if (g >= KS && !warp_wait(&k_free[g % KS], ((g - KS) / KS) & 1u)) {
+        // One-byte caches, one tile: this warp's descriptors and copies are what the
+        // steps wait for, so where the stage is not free yet, the descriptor comes
+        // first (its place is free a step earlier: kTaRing): 237 -> 233 us for the
+        // drafted trees' E4M3 batch.  With pairs V is not short, and widened sooner it
+        // is in the softmax's way (packed E4M3 336 instead of 306 us).
+        constexpr bool kEarly = kOneByte && !PAIR;
+        bool stage_free = true;
+        if constexpr (kEarly) {
+          stage_free = g < KS || __all_sync(kFull, mbar_test_wait(&k_free[g % KS], ((g - KS) / KS) & 1u));
+        } else if (g >= KS && !warp_wait(&k_free[g % KS], ((g - KS) / KS) & 1u)) {
           timed_out = true;
           break;
         }
@@ -611,7 +620,14 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         };
         // one-byte caches: the descriptor takes some 1500 cycles, so the copy
         // first; bf16: the queries wait for the descriptor
-        if constexpr (kOneByte) {
+        if (kEarly && !stage_free) {
+          describe();
+          if (!warp_wait(&k_free[g % KS], ((g - KS) / KS) & 1u)) {
+            timed_out = true;
+            break;
+          }
+          copy();
+        } else if constexpr (kOneByte) {
           copy();
           describe();
         } else {
