@@ -140,7 +140,10 @@ struct TaParams {
 // Step flags; a step without any is every row's in whole, with scores whose
 // order the page scales keep.
 constexpr int kStepMasked = 1;  // the sequence's end, nodes, or a bad page
-constexpr int kStepScales = 2;  // a k scale < 0, a v scale <= 0, or one that is not finite
+constexpr int kStepScales = 2;  // a k scale < 0, a v scale <= 0 or next to nothing, or one that is not finite
+// Least v scale / vref of a step whose weights are made with it in the exponent:
+// ex2 gives 0 below 2^-126, so weights from 2^-66 of a row's largest on count.
+constexpr float kTaLeastRatio = 0x1p-60f;
 
 // One step's descriptor in the ring.
 struct TaStep {
@@ -583,7 +586,10 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             const float vm = __uint_as_float(__reduce_max_sync(kFull, mine && finite ? __float_as_uint(fabsf(par.z)) : 0u));
             if (vm > 64.f * vref) vref = vm;
             const float ratio = !mine ? 0.f : !finite ? __uint_as_float(0x7fffffffu) : vref > 0.f ? par.z / vref : 0.f;
-            plain = __all_sync(kFull, !mine || (par.x >= 0.f && par.x < INFINITY && par.z > 0.f && par.z < INFINITY));
+            // (The sum of weights is taken from what the ratio has scaled: below
+            // kTaLeastRatio weights would leave fp32's range there, so the page
+            // goes the way of a scale of 0, which sums before it scales.)
+            plain = __all_sync(kFull, !mine || (par.x >= 0.f && par.x < INFINITY && ratio >= kTaLeastRatio && par.z < INFINITY));
             if (q >= 0 && q < PPI) {
               const_cast<TaStep*>(step_at(g))->par[q] =
                   make_float4(mine ? par.x : 0.f, kInt8Bias + (mine ? par.y : 0.f), ratio, ratio > 0.f ? __log2f(ratio) : 0.f);
@@ -1288,7 +1294,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
             }
             l = kOneByte ? l2 : l + (ps0 + ps1);
           } else {
-            // a page's v scale is zero, negative or not finite
+            // a page's v scale is zero, negative, next to nothing or not finite
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
               uint32_t y[16], pw[8];
