@@ -178,7 +178,8 @@ pkv_status pkv_kv_append(const pkv_cache_desc* cache, int32_t slot,
  *   elements from rotary_dim on stay y.
  * Queries are rounded to bf16 once; keys once, to bf16 or to the cache's codes
  * (from fp32, as pkv_kv_append quantises); values are appended as they are.
- * Angles are exact to 2^-26 of half a turn at any int32 position.
+ * Angles are right to 2^-26 of half a turn at any int32 position, for
+ * frequencies of up to 2^40 radians per position as the doubles they are.
  *
  *   slot           cache slot (layer group) to write, in [0, S).
  *   q, k, v        device bf16 [N][Hq][D], [N][Hkv][D], [N][Hkv][D]: heads of a

@@ -15,6 +15,7 @@
 #include <cudaTypedefs.h>
 
 #include "pkv_internal.h"
+#include "rope_turns.h"
 
 namespace {
 
@@ -484,8 +485,7 @@ pkv_status pkv_rope_append(const pkv_cache_desc* cache, int32_t slot, const void
   a.R = R;
   a.k_new = append ? 1 : 0;
   for (int i = 0; i < R / 2; ++i) {
-    const double turns = inv_freq[i] / 6.283185307179586476925, part = turns - std::floor(turns);
-    a.turns[i] = part < 1.0 ? static_cast<uint64_t>(part * 18446744073709551616.0) : 0;  // (x 2^64)
+    a.turns[i] = pkv::rope_turns(inv_freq[i]);
     a.axis[i] = static_cast<uint8_t>(freq_axes != nullptr ? freq_axes[i] : 0);
   }
   cudaError_t e = pkv::launch_rope_append(cache->dtype, D, interleaved == 0, a, dev.num_sms, s);

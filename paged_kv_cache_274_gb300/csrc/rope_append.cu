@@ -14,12 +14,13 @@
 // x_a (w_a cos) - x_b (w_b sin), and likewise for b.
 //
 // Angles are kept in turns: the host gives each frequency as a fraction of a
-// turn per position in 2^-64, and position x frequency modulo 2^64 is an
-// integer product, exact at any position.  The nearest quarter turn comes off as
-// an integer too, and the rest, at most an eighth of a turn, goes to sincospif as
-// a float: an angle is off by less than 2^-26 of half a turn wherever the token
-// is.  (With the whole turn as one float, 2^-24, E4M3 keys took the other
-// neighbour twice as often.)
+// turn per position in 2^-64, to two units (rope_turns.h), and position x
+// frequency modulo 2^64 is an integer product: 2^-31 of half a turn at the last
+// int32 position.  The nearest quarter turn comes off as an integer too, and the
+// rest, at most an eighth of a turn, goes to sincospif as a float, off by up to
+// 2^-27: an angle is off by less than 2^-26 of half a turn wherever the token is.
+// (With the whole turn as one float, 2^-24, E4M3 keys took the other neighbour
+// twice as often.)
 //
 // What bounds it: HBM for long prompts, the call on the host for a decode step;
 // see the times at launch_rope_append.
