@@ -13,7 +13,9 @@
 //
 // Since q >= 0, the rounds at one node join: P = max(p - A q, 0) with A the sum
 // of the rounds' Z / Y, so a round is one pass over p and q that needs nothing
-// but A, and a removed token's P is 0 by itself.
+// but A, and a removed token's P is 0 by itself.  Where Y is next to nothing (a
+// draft row with all but 1e-30 of its weight on a rejected token), A would leave
+// fp32's range: it is kept as -A 2^-64 then, and multiplies -q 2^64.
 //
 // The drawn token is a border among sums over the vocabulary, so everything is
 // summed to 2^-32 or better: p - A q is kept as an unevaluated sum of two
@@ -55,6 +57,10 @@ constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyChunk = 512;  // values that a warp sums at a time
 constexpr int kPer = kVerifyChunk / 32;
 constexpr int kVerifyMaxChunks = (PKV_MAX_VOCAB + 3 + kVerifyChunk - 1) / kVerifyChunk;
+// From Y below this much of Z on, A is kept times -2^-64 and q times -2^64.  (Y is
+// 2^-149 or more, so A is at most 2^149 Z; the q that are left are below Y.)
+constexpr float kVerifyLeastY = 0x1p-100f;
+constexpr float kVerifyRaise = -0x1p64f;
 constexpr int kVerifyCluster = 16;  // most CTAs of a cluster (more than 8 by a launch attribute of the kernel)
 
 // An unevaluated sum hi + lo.
@@ -86,6 +92,8 @@ __device__ __forceinline__ Pair over(const Pair& x, const Pair& y) {
 }
 // (of joined pairs)
 __device__ __forceinline__ bool below(const Pair& x, const Pair& y) { return x.hi < y.hi || (x.hi == y.hi && x.lo < y.lo); }
+// x times a power of two
+__device__ __forceinline__ Pair scaled(const Pair& x, float f) { return {__fmul_rn(x.hi, f), __fmul_rn(x.lo, f)}; }
 __device__ __forceinline__ bool positive(const Pair& x) { return x.hi > 0.f || (x.hi == 0.f && x.lo > 0.f); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
@@ -106,6 +114,9 @@ __device__ __forceinline__ Pair weight_left(float p, float q, float ah, float al
   const bool some = __fadd_rn(d, lo) > 0.f;
   return {some ? d : 0.f, some ? lo : 0.f};
 }
+// -q times kVerifyRaise, finite (a rejected token's may be anything; it takes all of
+// P as the largest number does).
+__device__ __forceinline__ float raised(float q) { return fminf(__fmul_rn(clean(q), -kVerifyRaise), 0x1.fffffep127f); }
 __device__ __forceinline__ Pair warp_total(Pair x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -342,10 +353,16 @@ __device__ __forceinline__ void verify_pass(const VerifyArgs& a, VerifyShared* s
     } else {
 #pragma unroll
       for (int k = 0; k < kPer; ++k) qv[k] = clean(qv[k]);
+      if (ah < 0.f) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) qv[k] *= kVerifyRaise;
+      }
       held = verify_sum<true>([&](int k) { return weights_left(both(pv[k], pv[k + 1]), both(qv[k], qv[k + 1]), ah, al); });
       if (want_y) {
         verify_drop(qv, s, removed, e0, lane);
-        add_to(y, verify_sum<false>([&](int k) { return Pairs{both(qv[k], qv[k + 1]), 0ull}; }));
+        Pair left = verify_sum<false>([&](int k) { return Pairs{both(qv[k], qv[k + 1]), 0ull}; });
+        if (ah < 0.f) left = scaled(left, 1.f / kVerifyRaise);
+        add_to(y, left);
       }
     }
   }
@@ -436,11 +453,15 @@ __device__ __forceinline__ int verify_draw(const VerifyArgs& a, VerifyShared* s,
     for (int g = lane; g < removed; g += 32)
       if (static_cast<unsigned>(s->gone[g] - e0) < static_cast<unsigned>(kVerifyChunk)) s->weights[verify_pad(s->gone[g] - e0)].hi = 0.f;
   __syncwarp();
+  if (A.hi < 0.f)
+#pragma unroll 1
+    for (int k = 0; k < kPer; ++k) s->weights[verify_pad(lane * kPer + k)].lo = raised(s->weights[verify_pad(lane * kPer + k)].lo);
+  const float ah = fabsf(A.hi), al = A.hi < 0.f ? -A.lo : A.lo;
   Pair own{0.f, 0.f};
 #pragma unroll 4
   for (int k = 0; k < kPer; ++k) {
     Pair& w = s->weights[verify_pad(lane * kPer + k)];
-    w = weight_left(w.hi, w.lo, A.hi, A.lo);
+    w = weight_left(w.hi, w.lo, ah, al);
     add_to(own, w);
   }
   __syncwarp();
@@ -555,9 +576,16 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
         was = __any_sync(kFull, was);
         const float q0 = weight(s.q[c]).hi;
         const Pair q{was && a.q != nullptr ? 0.f : q0, 0.f};
-        Pair left = weight_left(s.p[c], a.q != nullptr ? q0 : 0.f, A.hi, A.lo);
+        Pair left = A.hi < 0.f ? weight_left(s.p[c], raised(q0), -A.hi, -A.lo) : weight_left(s.p[c], a.q != nullptr ? q0 : 0.f, A.hi, A.lo);
         left = a.q == nullptr && was ? none : joined(left.hi, left.lo);
-        const Pair rq = times(Pair{s.r[c], 0.f}, q);
+        Pair rq{s.r[c], 0.f};
+        // (both sides times 2^64 where a factor is small: a product's low part has to
+        // stay within fp32's range)
+        if (fminf(fminf(q0, left.hi), Y.hi) < 0x1p-40f && fmaxf(fmaxf(q0, left.hi), fmaxf(Y.hi, Z.hi)) < 0x1p30f) {
+          rq.hi *= 0x1p64f;
+          left = scaled(left, 0x1p64f);
+        }
+        rq = times(rq, q);
         if (removed == 0 ? below(rq, left) : below(times(rq, Z), times(left, Y))) {
           if (lane == 0) a.accept_idx[static_cast<size_t>(b) * a.A + count] = c;
           ++count;
@@ -570,8 +598,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
         } else {
           if (removed++ == 0)
             A = one;
-          else if (Y.hi > 0.f)
-            add_to(A, over(Z, Y));
+          else if (a.q != nullptr && Y.hi > 0.f) {
+            if (A.hi > 0.f && Y.hi < Z.hi * kVerifyLeastY) A = scaled(A, 1.f / kVerifyRaise);
+            add_to(A, over(Z, A.hi > 0.f ? Y : scaled(Y, kVerifyRaise)));
+          }
           const bool more = count < a.A && child(next) >= 0;
           if (a.q == nullptr && summed) {
             // Only this token's chunk changes.  Summed anew where the difference
