@@ -458,9 +458,11 @@ pkv_status pkv_decode_tree_describe(const pkv_cache_desc* cache, int32_t batch,
  *   q, out         device bf16 [num_rows][Hq][D]; out must not overlap q or
  *                  the cache.
  *   query_starts   device int32 [B + 1], rising, in 0..num_rows.  A sequence
- *                  whose rows do not rise, leave 0..num_rows or are more than
- *                  max_query_tokens sets PKV_DEVERR_QUERY; none of its rows is
- *                  written.
+ *                  whose rows leave 0..num_rows or are more than
+ *                  max_query_tokens sets PKV_DEVERR_QUERY, and none of its rows
+ *                  is written; the same goes for the first sequence whose entry
+ *                  lies above the next one's and for every one behind it (their
+ *                  rows could be others' as well).
  *   max_query_tokens  >= 1, the most rows of a sequence (num_rows will do).
  *   workspace      pkv_decode_packed_workspace_bytes() bytes.
  *   opts           partition_blocks is the fewest blocks of a work share, math

@@ -45,11 +45,34 @@ struct PackedPlanArgs {
   int span, tile, alone, max_shares, min_steps, item_steps, row_elems /* Hq * D */;
 };
 
-// A sequence as the caller gives it, checked.
-__device__ __forceinline__ PackedSeq packed_seq(const PackedPlanArgs& a, int b, unsigned& err) {
-  const int s0 = a.query_starts[b], s1 = a.query_starts[b + 1];
-  int c = a.context_lens[b], m = 0;
-  if (s0 >= 0 && s0 <= s1 && s1 <= a.N && s1 - s0 <= a.T)
+// A sequence as the caller gives it.
+struct PackedGiven {
+  int s0, s1, ctx;
+};
+__device__ __forceinline__ PackedGiven packed_given(const PackedPlanArgs& a, int b) {
+  return b < a.B ? PackedGiven{a.query_starts[b], a.query_starts[b + 1], a.context_lens[b]} : PackedGiven{0, 0, 0};
+}
+
+// The first sequence whose entries of query_starts fall, or B.  The whole CTA;
+// a barrier.  (`own`: this thread's first sequence, loaded before it.)
+__device__ __forceinline__ int packed_first_fall(const PackedPlanArgs& a, const PackedGiven& own) {
+  __shared__ int fall_s;
+  int mine = own.s1 < own.s0 ? static_cast<int>(threadIdx.x) : a.B;
+#pragma unroll 1
+  for (int b = threadIdx.x + blockDim.x; b < a.B && mine == a.B; b += blockDim.x)
+    if (packed_falls(a.query_starts, b)) mine = b;
+  if (threadIdx.x == 0) fall_s = a.B;
+  if (!__syncthreads_or(mine < a.B)) return a.B;
+  atomicMin(&fall_s, mine);
+  __syncthreads();
+  return fall_s;
+}
+
+// Sequence b, checked.
+__device__ __forceinline__ PackedSeq packed_seq(const PackedPlanArgs& a, const PackedGiven& x, int b, int fall, unsigned& err) {
+  const int s0 = x.s0, s1 = x.s1;
+  int c = x.ctx, m = 0;
+  if (packed_rows_fit(s0, s1, b, fall, a.N, a.T))
     m = s1 - s0;
   else
     err |= PKV_DEVERR_QUERY;
@@ -64,7 +87,7 @@ __device__ __forceinline__ PackedSeq packed_seq(const PackedPlanArgs& a, int b, 
 // (with the first KV head's words), and which V rows are not finite: those
 // would reach every row of a tile through 0 x NaN, so the attention leaves them
 // out of the products and sets the rows that see them to NaN (tree_scan.cuh).
-__device__ __forceinline__ void packed_scan(const PackedPlanArgs& a, int warp0, int nwarps) {
+__device__ __forceinline__ void packed_scan(const PackedPlanArgs& a, int fall, int warp0, int nwarps) {
   const int lane = threadIdx.x & 31;
   const int heads = a.poison != nullptr ? a.Hkv : 1;
 #pragma unroll 1
@@ -73,16 +96,10 @@ __device__ __forceinline__ void packed_scan(const PackedPlanArgs& a, int warp0, 
     bool zero = false;
     long long at = -1;
     if (row < a.N) {
-      int lo = 0, hi = a.B;  // the first sequence that starts behind the row
-#pragma unroll 1
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(a.query_starts + mid) > row) hi = mid; else lo = mid + 1;
-      }
-      const int b = lo - 1;
+      const int b = packed_owner(a.query_starts, fall, row);
       if (b >= 0) {
         unsigned err = 0;  // (the planner reports it)
-        const PackedSeq s = packed_seq(a, b, err);
+        const PackedSeq s = packed_seq(a, packed_given(a, b), b, fall, err);
         const int t = row - s.start, pos = s.ctx - s.m + t;
         if (t < s.m) {
           zero = pos < 0;
@@ -115,26 +132,28 @@ __device__ __forceinline__ void packed_scan(const PackedPlanArgs& a, int warp0, 
 __global__ void __launch_bounds__(kPackedPlanThreads) packed_plan_kernel(const PackedPlanArgs a) {
   pdl_trigger();
   pdl_wait();
+  __shared__ long long carry_s;
+  if (threadIdx.x == 0) carry_s = 0;
+  PackedGiven given = packed_given(a, threadIdx.x);
+  const int fall = packed_first_fall(a, given);
   if (blockIdx.x > 0) {  // block-uniform: these CTAs never reach the barriers below
-    packed_scan(a, (blockIdx.x - 1) * (blockDim.x / 32) + (threadIdx.x >> 5), static_cast<int>(gridDim.x - 1) * (blockDim.x / 32));
+    packed_scan(a, fall, (blockIdx.x - 1) * (blockDim.x / 32) + (threadIdx.x >> 5), static_cast<int>(gridDim.x - 1) * (blockDim.x / 32));
     return;
   }
   __shared__ long long warp_tot[kPackedPlanThreads / 32];
-  __shared__ long long carry_s;
   __shared__ long long start_s[kPackedPlanSmem + 1];
   __shared__ PackedSeq seq_s[kPackedPlanSmem];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   const bool fits = a.B <= kPackedPlanSmem;
   const long long item_cost = packed_item_cost(a.item_steps);
-  if (tid == 0) carry_s = 0;
-  __syncthreads();
   unsigned err = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < a.B; b0 += threads) {
     const int b = b0 + tid;
     long long cost = 0;
+    if (b0 > 0) given = packed_given(a, b);
     if (b < a.B) {
-      const PackedSeq s = packed_seq(a, b, err);
+      const PackedSeq s = packed_seq(a, given, b, fall, err);
       a.seqs[b] = s;
       if (fits) seq_s[b] = s;
       cost = packed_cost(s, a.span, item_cost) * packed_weight(s, a.tile, a.alone) * a.Hkv;

@@ -28,6 +28,27 @@ struct PackedBound {
   int step;         // step of the item (0: the share starts with the item)
 };
 
+// Sequences' rows as the caller gives them.  Where an entry of query_starts lies
+// below the one before it, that sequence and every one behind it are refused
+// (`fall`: the first such sequence, or B): their rows could be others' too.
+// Before it the entries rise, so the rows are their own, and a row's sequence is
+// found among them by bisection.
+PKV_PLAN_FN bool packed_falls(const int32_t* starts, int b) { return starts[b + 1] < starts[b]; }
+// Whether the rows s0 .. s1 - 1 of sequence b can be served, of N rows, T a sequence at most.
+PKV_PLAN_FN bool packed_rows_fit(int s0, int s1, int b, int fall, int N, int T) {
+  return b < fall && s0 >= 0 && s0 <= s1 && s1 <= N && s1 - s0 <= T;
+}
+// The one sequence that `row` can belong to (-1: none).
+PKV_PLAN_FN int packed_owner(const int32_t* starts, int fall, int row) {
+  int lo = 0, hi = fall;  // the first sequence that starts behind the row
+#pragma unroll 1
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (starts[mid] > row) hi = mid; else lo = mid + 1;
+  }
+  return lo - 1;
+}
+
 PKV_PLAN_FN int packed_runs(const PackedSeq& s, int span) { return (s.m + span - 1) / span; }
 
 // Positions that the last row of a run sees (0: none of its rows sees any).
