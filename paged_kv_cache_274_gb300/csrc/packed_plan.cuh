@@ -85,6 +85,12 @@ PKV_PLAN_FN long long packed_cost(const PackedSeq& s, int span, long long item_c
   return packed_before(s, runs - packed_first(s, span), span, item_cost) - (static_cast<long long>(runs) * span - s.m);
 }
 
+// Most shares of a call: a CTA each, which holds an SM alone, so no more than there
+// are SMs (the others would run behind them, as long again).  The workspace has
+// room for kPackedShares.
+constexpr int kPackedShares = 152;
+PKV_PLAN_FN int packed_most_shares(int num_sms) { return num_sms < kPackedShares ? (num_sms < 1 ? 1 : num_sms) : kPackedShares; }
+
 // Shares of at least min_steps steps (never less than one: two boundaries in
 // one step would leave a share inside an item without steps).
 PKV_PLAN_FN int packed_share_count(long long total, int min_steps, int max_shares) {

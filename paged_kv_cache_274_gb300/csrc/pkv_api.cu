@@ -14,6 +14,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "packed_plan.cuh"
 #include "pkv_internal.h"
 #include "rope_turns.h"
 
@@ -755,7 +756,7 @@ static pkv_status resolve_packed(const pkv_cache_desc* c, int32_t N, int32_t bat
   L->kv_fp8 = c->dtype != PKV_KV_BF16;
   L->kv_dtype = c->dtype;
   L->math = PKV_MATH_TC;
-  L->tree_shares = 152;
+  L->tree_shares = pkv::kPackedShares;
   L->tree_min_steps = std::max(1, o.partition_blocks * c->block_size / 128);
   return PKV_OK;
 }
@@ -1135,6 +1136,7 @@ pkv_status pkv_paged_decode_packed(const pkv_cache_desc* cache, const void* q, i
   L.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   L.stream = s;
   L.num_sms = dev.num_sms;
+  L.tree_shares = pkv::packed_most_shares(dev.num_sms);  // (the workspace was checked for the most)
   if (opts != nullptr) {
     L.ev_start = static_cast<cudaEvent_t>(opts->event_decode_start);
     L.ev_end = static_cast<cudaEvent_t>(opts->event_decode_end);
