@@ -202,8 +202,9 @@ pkv_status pkv_kv_append(const pkv_cache_desc* cache, int32_t slot,
  *                  is -1 is padding, of which no query is written either.  NULL
  *                  with k NULL: no padding.
  *   q_out          device bf16 [N][Hq][D], tokens q_out_stride elements apart;
- *                  may be q itself (with the same stride), must not overlap
- *                  anything else.
+ *                  may be q itself (with the same stride) or lie between the
+ *                  rows of q, k and v (one stride), must not overlap anything
+ *                  else.
  *   caches, scales as in pkv_kv_append (NULL where k is).
  * One kernel launch (none when N == 0).
  */

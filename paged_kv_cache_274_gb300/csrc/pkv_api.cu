@@ -121,6 +121,23 @@ struct Span {
   size_t bytes;
 };
 
+// Rows of `row` bytes, `stride` apart.
+struct Rows {
+  const void* p;
+  int64_t stride, row;
+};
+
+// Whether no row of `a` overlaps one of `b` (n of each; NULL: none).  Rows that lie
+// between each other's are told apart where both have one stride.
+bool rows_disjoint(const Rows& a, const Rows& b, int64_t n) {
+  if (a.p == nullptr || b.p == nullptr || n < 1) return true;
+  const int64_t x = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.p)), y = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p));
+  if (x >= y + (n - 1) * b.stride + b.row || y >= x + (n - 1) * a.stride + a.row) return true;
+  if (a.stride != b.stride || n == 1) return false;
+  const int64_t off = ((y - x) % a.stride + a.stride) % a.stride;  // of b's rows behind a's
+  return off >= a.row && off + b.row <= a.stride;
+}
+
 // Whether no array of `written` overlaps another one of them or one of `read`
 // (NULL and empty arrays overlap nothing).
 bool disjoint(std::initializer_list<Span> written, std::initializer_list<Span> read) {
@@ -439,18 +456,17 @@ pkv_status pkv_rope_append(const pkv_cache_desc* cache, int32_t slot, const void
   if (!aligned4({positions}) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0)
     return fail(PKV_ERR_ALIGNMENT, "positions must be 4-byte aligned, slot_mapping 8-byte");
   if (append && (st = check_append(cache, slot, k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale)) != PKV_OK) return st;
-  auto span = [&](const void* p, int64_t stride, int64_t row) {
-    return Span{p, static_cast<size_t>(((N - 1) * stride + row) * 2)};
-  };
+  const Rows out_rows{q_out, 2 * q_out_stride, 2 * q_row}, q_rows{q, 2 * q_stride, 2 * q_row};
+  const Rows k_rows{k, 2 * k_stride, 2 * kv_row}, v_rows{v, 2 * v_stride, 2 * kv_row};
   const bool in_place = q_out == q && q_out_stride == q_stride;
   const size_t pool = static_cast<size_t>(cache->num_slots) * cache->num_blocks * cache->num_kv_heads * cache->block_size * D *
                       (cache->dtype == PKV_KV_BF16 ? 2 : 1);
   const size_t weights = static_cast<size_t>(D) * 2, rows = static_cast<size_t>(N);
   const Span none{nullptr, 0};
-  // (in place, q_out lies between the rows of k and v as q does)
-  if (!disjoint({span(q_out, q_out_stride, q_row)},
-                {in_place ? none : span(q, q_stride, q_row), in_place || !append ? none : span(k, k_stride, kv_row),
-                 in_place || !append ? none : span(v, v_stride, kv_row), Span{q_weight, weights}, Span{k_weight, weights},
+  // (q_out may lie between the rows of q, k and v: in place it does where they are one projection's)
+  if ((!in_place && !rows_disjoint(out_rows, q_rows, N)) || !rows_disjoint(out_rows, k_rows, N) || !rows_disjoint(out_rows, v_rows, N) ||
+      !disjoint({Span{q_out, static_cast<size_t>((N - 1) * 2 * q_out_stride + 2 * q_row)}},
+                {Span{q_weight, weights}, Span{k_weight, weights},
                  R > 0 ? Span{positions, rows * 4 * num_axes} : none, Span{slot_mapping, rows * 8},
                  append ? Span{k_cache, pool} : none, append ? Span{v_cache, pool} : none}))
     return fail(PKV_ERR_INVALID_ARG, "q_out overlaps another array");
