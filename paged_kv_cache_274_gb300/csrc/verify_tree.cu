@@ -21,8 +21,9 @@
 // summed to 2^-32 or better: p - A q is kept as an unevaluated sum of two
 // floats (error-free transformations of addition and product, T. J. Dekker and
 // D. E. Knuth), so is everything that is summed or compared.  There are no
-// doubles: fp64 units do 2 operations a clock and SM, and with doubles in the
-// draw alone it took 9 to 12 us of a call instead of 2.
+// doubles in it: fp64 units do 2 operations a clock and SM, and with doubles in the
+// draw alone it took 9 to 12 us of a call instead of 2.  (Only a comparison whose
+// products leave fp32's range is made of doubles.)
 //
 // What bounds it: the rows of the nodes where the walk loses a child or ends,
 // from HBM, and for a small batch the chain of loads.  One cluster of up to 16
@@ -94,6 +95,7 @@ __device__ __forceinline__ Pair over(const Pair& x, const Pair& y) {
 __device__ __forceinline__ bool below(const Pair& x, const Pair& y) { return x.hi < y.hi || (x.hi == y.hi && x.lo < y.lo); }
 // x times a power of two
 __device__ __forceinline__ Pair scaled(const Pair& x, float f) { return {__fmul_rn(x.hi, f), __fmul_rn(x.lo, f)}; }
+__device__ __forceinline__ double whole(const Pair& x) { return static_cast<double>(x.hi) + x.lo; }
 __device__ __forceinline__ bool positive(const Pair& x) { return x.hi > 0.f || (x.hi == 0.f && x.lo > 0.f); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
@@ -373,6 +375,11 @@ __device__ __forceinline__ void verify_pass(const VerifyArgs& a, VerifyShared* s
   }
 }
 
+// r q Z < left Y where the products, or their low parts, may leave fp32's range.
+__device__ __noinline__ bool verify_accepts(float r, float q, Pair left, Pair Y, Pair Z) {
+  return static_cast<double>(r) * q * whole(Z) < whole(left) * whole(Y);
+}
+
 // Inclusive scan over the warp.  (Not inlined: code that runs once costs its
 // fetch, 5 cycles and more an instruction.)
 __device__ __noinline__ Pair warp_scan(Pair x) {
@@ -578,15 +585,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
         const Pair q{was && a.q != nullptr ? 0.f : q0, 0.f};
         Pair left = A.hi < 0.f ? weight_left(s.p[c], raised(q0), -A.hi, -A.lo) : weight_left(s.p[c], a.q != nullptr ? q0 : 0.f, A.hi, A.lo);
         left = a.q == nullptr && was ? none : joined(left.hi, left.lo);
-        Pair rq{s.r[c], 0.f};
-        // (both sides times 2^64 where a factor is small: a product's low part has to
-        // stay within fp32's range)
-        if (fminf(fminf(q0, left.hi), Y.hi) < 0x1p-40f && fmaxf(fmaxf(q0, left.hi), fmaxf(Y.hi, Z.hi)) < 0x1p30f) {
-          rq.hi *= 0x1p64f;
-          left = scaled(left, 0x1p64f);
-        }
-        rq = times(rq, q);
-        if (removed == 0 ? below(rq, left) : below(times(rq, Z), times(left, Y))) {
+        const Pair rqz = times(times(Pair{s.r[c], 0.f}, q), Z), py = times(left, Y);
+        bool accepted = below(rqz, py);
+        if (left.hi > 0.f && !(fminf(rqz.hi, py.hi) >= 0x1p-70f && fmaxf(rqz.hi, py.hi) < 0x1p100f))
+          accepted = verify_accepts(s.r[c], q.hi, left, Y, Z);
+        if (accepted) {
           if (lane == 0) a.accept_idx[static_cast<size_t>(b) * a.A + count] = c;
           ++count;
           at = c;

@@ -79,3 +79,14 @@ def test_large_target_rows_without_draft_rows():
     _, count, _ = c.check()
     assert (count == 1).any()
     assert pkv.read_device_error() == 0
+
+
+def test_children_that_the_draft_row_denies():
+    # Q(x) = 0: accepted against anything that is left of P(x), however small its product with Y
+    B = 40
+    c = peaked(8950, B, 4, 60, 1e-40)
+    at, x = np.arange(B), c.tokens[:, 2]
+    c.q[at, 0, x] = 0.0
+    c.p[at, 0, x] = 10.0 ** -np.linspace(5, 37, B)
+    _, count, _ = c.check()
+    assert (count == 2).sum() > B // 2
