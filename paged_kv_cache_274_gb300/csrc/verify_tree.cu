@@ -469,6 +469,7 @@ __device__ __forceinline__ int verify_draw(const VerifyArgs& a, VerifyShared* s,
   for (int k = 0; k < kPer; ++k) {
     Pair& w = s->weights[verify_pad(lane * kPer + k)];
     w = weight_left(w.hi, w.lo, ah, al);
+    w = two_sum(w.hi, w.lo);  // (where p is near A q, the low part may be the larger)
     add_to(own, w);
   }
   __syncwarp();
@@ -584,7 +585,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
         const float q0 = weight(s.q[c]).hi;
         const Pair q{was && a.q != nullptr ? 0.f : q0, 0.f};
         Pair left = A.hi < 0.f ? weight_left(s.p[c], raised(q0), -A.hi, -A.lo) : weight_left(s.p[c], a.q != nullptr ? q0 : 0.f, A.hi, A.lo);
-        left = a.q == nullptr && was ? none : joined(left.hi, left.lo);
+        left = a.q == nullptr && was ? none : two_sum(left.hi, left.lo);
         const Pair rqz = times(times(Pair{s.r[c], 0.f}, q), Z), py = times(left, Y);
         bool accepted = below(rqz, py);
         if (left.hi > 0.f && !(fminf(rqz.hi, py.hi) >= 0x1p-70f && fmaxf(rqz.hi, py.hi) < 0x1p100f))
