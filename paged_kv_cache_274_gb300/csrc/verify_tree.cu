@@ -539,6 +539,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
   Pair y_sum{-1.f, 0.f};  // Y as it was last summed (< 0: not at this node)
   Pair z_sum = none, upto = none;  // Z as it was last summed, and the runs' ends then
   bool stale = false;     // `sums` have changed since
+  // Sums of P below this are nothing but what A and its products were rounded by (P
+  // is 0 by the definition where it was a multiple of Q), or of a P that was nothing
+  float least = 0.f;
   bool walking = nodes > 0, done = false;
   if (rank == 0 && warp == 0 && walking) {
     count = 1;
@@ -585,7 +588,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
         const float q0 = weight(s.q[c]).hi;
         const Pair q{was && a.q != nullptr ? 0.f : q0, 0.f};
         Pair left = A.hi < 0.f ? weight_left(s.p[c], raised(q0), -A.hi, -A.lo) : weight_left(s.p[c], a.q != nullptr ? q0 : 0.f, A.hi, A.lo);
-        left = a.q == nullptr && was ? none : two_sum(left.hi, left.lo);
+        left = was || !(Z.hi > 0.f) ? none : two_sum(left.hi, left.lo);
         const Pair rqz = times(times(Pair{s.r[c], 0.f}, q), Z), py = times(left, Y);
         bool accepted = below(rqz, py);
         if (left.hi > 0.f && !(fminf(rqz.hi, py.hi) >= 0x1p-70f && fmaxf(rqz.hi, py.hi) < 0x1p100f))
@@ -597,14 +600,22 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
           removed = 0;
           A = none;
           Z = Y = one;
+          least = 0.f;
           y_sum.hi = -1.f;
           summed = false;
         } else {
+          least = a.q == nullptr || Z.hi > 0.f ? 0.f : INFINITY;
           if (removed++ == 0)
             A = one;
           else if (a.q != nullptr && Y.hi > 0.f) {
             if (A.hi > 0.f && Y.hi < Z.hi * kVerifyLeastY) A = scaled(A, 1.f / kVerifyRaise);
-            add_to(A, over(Z, A.hi > 0.f ? Y : scaled(Y, kVerifyRaise)));
+            const Pair y = A.hi > 0.f ? Y : scaled(Y, kVerifyRaise);
+            add_to(A, over(Z, y));
+            // (where no token comes twice, P is a multiple of Q by chance alone)
+            if (was) {
+              const float rough = (__float_as_uint(A.hi) & 0x7fffffu) != 0u ? fabsf(A.hi) * 0x1p-46f : 0.f;
+              least += fmaf(fmaf(fabsf(A.lo), 0x1p-22f, rough), fabsf(y.hi), Z.hi * 0x1p-44f);
+            }
           }
           const bool more = count < a.A && child(next) >= 0;
           if (a.q == nullptr && summed) {
@@ -672,6 +683,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
       if (last) {
         upto = verify_runs(sums, n);
         z_sum = Z = from_lane(upto, 31);
+        if (Z.hi < least) Z = none;
         break;
       }
       // (the runs' ends wait until a token is drawn)
@@ -679,6 +691,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
       Z = verify_lane_run(sums, n);
       Pair y = s.want_y ? verify_lane_run(s.y_part, ranks * kVerifyWarps) : none;
       warp_totals(Z, y);
+      if (Z.hi < least) Z = none;
       z_sum = Z;
       if (s.want_y) y_sum = Y = y;
     }
@@ -688,7 +701,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
     const int chunks = (a.V + r.shift + kVerifyChunk - 1) / kVerifyChunk;
     if (stale) {
       upto = verify_runs(sums, chunks);
-      Z = from_lane(upto, 31);
+      if (Z.hi > 0.f || a.q == nullptr) Z = from_lane(upto, 31);
     }
     if (!(Z.hi > 0.f) && removed > 0) {
       // nothing is left: the draft has as much everywhere.  The target's own
