@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
       const int npages = (t1 - t0 + BS - 1) / BS;
       // packed: the item's rows, and the positions that its first row sees
       [[maybe_unused]] int row0 = 0, rows = 0;
+      [[maybe_unused]] bool dirty = false;
       int base;  // tokens that every row attends to
       if constexpr (PACKED) {
         constexpr int kTiles = PAIR ? 2 : 1;
@@ -500,6 +501,16 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
         row0 = seq.start + t_first;
         rows = min(kTiles * p.Tt, seq.m - t_first);
         base = seq.ctx - seq.m + t_first + 1;
+        // a row of the sequence before the item's (or of a neighbour in its words)
+        // whose V is not finite: the steps that hold it are every row's in whole, but
+        // the rows have to be told
+        if constexpr (!kI8) {
+          const uint32_t* bits = p.tree.poison + static_cast<size_t>(kvh) * p.tree.words;
+          uint32_t some = 0u;
+#pragma unroll 1
+          for (int w = seq.start / 32 + lane; 32 * w < row0; w += 32) some |= __ldg(bits + w);
+          dirty = t_first > 0 && __any_sync(kFull, some != 0u);
+        }
       } else {
         base = ctx - (p.tree.node_counts != nullptr ? __ldg(p.tree.node_counts + b) : p.T);
       }
@@ -602,7 +613,9 @@ __global__ void __launch_bounds__(ta_threads(KV), 1)
           }
           if (bad) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
           const int seen = min(t1, base) - (t0 + j * kTreeTokens);  // tokens of the step that every row attends to
-          const int flags = (seen < kTreeTokens || __any_sync(kFull, bad) ? kStepMasked : 0) | (plain ? 0 : kStepScales);
+          bool masked = seen < kTreeTokens || __any_sync(kFull, bad);
+          if constexpr (PACKED && !kI8) masked |= dirty && t0 + (j + 1) * kTreeTokens > seq.ctx - seq.m;
+          const int flags = (masked ? kStepMasked : 0) | (plain ? 0 : kStepScales);
           if (lane == 0) {
             st->n = n;
             st->b = b;
