@@ -84,7 +84,7 @@ typedef enum { PKV_KV_BF16 = 0, PKV_KV_FP8_E4M3 = 1, PKV_KV_INT8 = 2 } pkv_kv_dt
 #define PKV_DEVERR_TIMEOUT 0x8u      /* a bounded wait on a copy gave up */
 #define PKV_DEVERR_NO_BLOCKS 0x10u   /* too few free blocks for a request's new tokens */
 #define PKV_DEVERR_TREE 0x20u        /* a drafted tree's node count, parent, token, probabilities or accepted path */
-#define PKV_DEVERR_QUERY 0x40u       /* query_starts that do not rise, or too many rows of a sequence */
+#define PKV_DEVERR_QUERY 0x40u       /* query_starts that fall or leave the rows, or too many rows of a sequence */
 
 /* Shape of one paged cache (both K and V).  Supported: block_size 16 or 32;
  * head_dim 64 or 128 for bf16, 128 for E4M3 and INT8. */
@@ -472,6 +472,11 @@ pkv_status pkv_decode_tree_describe(const pkv_cache_desc* cache, int32_t batch,
  *                  fewer than 11 bits below 2^-14 of the row's largest, and
  *                  carry the v scales as in pkv_paged_decode_tree.)
  *   everything else as in pkv_paged_decode_multi.  G <= 128.
+ * A step in which every request decodes one token is one of pkv_paged_decode,
+ * too, which reads one-byte caches faster where there is much to read: 64 x 4096
+ * tokens, 32 / 8 heads of 128, on one GB300: bf16 162 instead of 171 us, E4M3 124
+ * instead of 156, INT8 123 instead of 202; 16 x 1000 to 4000 tokens: 72 instead
+ * of 41, 69 instead of 43, 67 instead of 53.
  */
 pkv_status pkv_paged_decode_packed(const pkv_cache_desc* cache,
                                    const void* q, int32_t num_rows, int32_t batch,
@@ -600,7 +605,9 @@ pkv_status pkv_extend_tables(int32_t batch, int32_t block_size, int32_t max_bloc
  * draft_probs NULL: children chosen without randomness (the draft's best
  * tokens, a lookup); Q is then 1 at x alone and a rejection sets P(x) = 0.
  * Values of rows that are negative or not finite count as 0.  Sums are taken to
- * 2^-32 or better of their value, and compared as they are, unrounded.
+ * 2^-32 or better of their value, and compared as they are, unrounded; the
+ * differences P are exact behind a node's first rejection and right to 2^-44 of
+ * what was subtracted behind later ones.
  *
  *   tokens         device int32 [B][T]: the nodes' tokens, in [0, vocab) (node
  *                  0's is not looked at).

@@ -16,17 +16,22 @@ constexpr int kPackedPlanThreads = 1024;
 constexpr int kPackedPlanSmem = 1024;  // sequences whose sums are searched in shared memory
 
 // Cost of an item besides its steps, in steps (tree_attend.cu), measured for pairs
-// of tiles: bf16 4 (a prompt of 8192 tokens 405 us; with 2 and 5 some 5 us more),
-// head_dim 64 5 (ragged prompts 145 us; 3: 150, 4: 148), one byte 6 (E4M3 307 us; 2:
-// 350, 3: 329, 4: 310; INT8 90 us with 3 to 9).
+// of tiles on three batches of each kind (us): head_dim 64 5 (ragged prompts 146, 138,
+// 168; 3: 149, 143, 171; 4: 145, 144, 170; 8: 148, 140, 169), one byte 6 (E4M3 359, 247,
+// 271; 2: 406, 279, 315; 4: 362, 246, 272; 8: 366, 250, 277; INT8 82, 104, 90; 3: 83, 99,
+// 92; 8: 84, 103, 91), bf16 4, where nothing stands out (a prompt of 8192 tokens 428 to
+// 447 in one loop, with 2 437, 3 446 to 459, 5 444 to 447, 8 453; chunks beside single
+// tokens 2 to 8 within 3%).
 static int packed_item_steps(int kv_dtype, int D, bool pair) {
   if (kv_dtype == PKV_KV_BF16) return pair && D == 64 ? 5 : 4;
   return 6;
 }
 
 // What a step of an item with one row tile costs where CTAs serve pairs of
-// tiles, of kPackedWeight (chunks of prompts beside single tokens, bf16 6: 345 us,
-// 5: 356, 7: 365; INT8 5: 104 us, 4: 106, 6: 115; E4M3 5: 360 us, 4: 379, 6: 361).
+// tiles, of kPackedWeight (chunks of prompts beside single tokens, three batches, us:
+// bf16 6: 311 to 331, 378, 395; 5: 313, 368, 391; 4: 329, 402, 422; 8: 358, 407, 432;
+// E4M3 5: 360, 248, 272; 4: 389, 270, 294; 6: 362, 249, 274; INT8 5: 82, 104, 89; 4: 81,
+// 96, 86; 6: 86, 105, 97).
 static int packed_alone(int kv_dtype) { return kv_dtype == PKV_KV_BF16 ? 6 : 5; }
 
 struct PackedPlanArgs {

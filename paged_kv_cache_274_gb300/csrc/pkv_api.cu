@@ -538,12 +538,14 @@ static pkv_status resolve_decode(const pkv_cache_desc* c, int32_t batch, int32_t
   // 16 rows per KV head (172 us at 4 tokens, one tile), tcgen05 tiles from 32
   // rows on (kernel 173 vs 234 us at 8 tokens, 173 vs 451 at 16, 183 vs 865
   // at 32, 583 vs 3402 at 128)
-  // drafted trees, 8 KV heads, mma.sync against tcgen05: bf16 with head_dim 128
-  // no case for mma.sync (8 rows: 30 vs 15 us for 1 x 1024 tokens, 25 vs 24 for
-  // 1 x 16384, 173 vs 168 for 64 x 4096); head_dim 64 up to 8 rows (64 x 4096:
-  // 91 vs 113 us, 16 rows: 106 vs 112, and 36 vs 22 for 16 x 1024); one-byte
-  // caches up to 16 rows (64 x 4096: E4M3 155 vs 190 us, INT8 145 vs 239; 20
-  // rows: 264 vs 190, 248 vs 239)
+  // drafted trees, 8 KV heads, mma.sync against tcgen05, us a call: bf16 with
+  // head_dim 128 no case for mma.sync from 8 rows on (64 x 4096 tokens 174 vs 173,
+  // 16 x 1024 34 vs 26, 1 x 16384 26 vs 27); head_dim 64 up to 8 rows (64 x 4096:
+  // 91 vs 105, 12 rows: 104 vs 104, and 28 vs 21 for 16 x 1024); one-byte caches up
+  // to 16 rows, which is right for large batches (64 x 4096: E4M3 156 vs 160, INT8
+  // 148 vs 202; 20 rows: 266 vs 160, 252 vs 202) and for long single requests (1 x
+  // 16384: 29 vs 29, 29 vs 32), while 16 x 1024 would be faster with tcgen05 from 8
+  // rows on (E4M3 33 vs 29; INT8 31 vs 32, 12 rows: 36 vs 32)
   const long long mma_rows = !tree || c->dtype != PKV_KV_BF16 ? 16 : c->head_dim == 64 ? 8 : 0;
   if (math == PKV_MATH_AUTO) math = (tc_ok && static_cast<long long>(T) * G > mma_rows) ? PKV_MATH_TC : PKV_MATH_MMA;
   if (math == PKV_MATH_TC && !tc_ok)

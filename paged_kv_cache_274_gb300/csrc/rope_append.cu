@@ -279,7 +279,9 @@ static cudaError_t launch_rope(const RopeArgs& a, bool halves, const cudaLaunchC
 // (195 MB): 38 us, 0.78.  64 tokens (1.6 MB): 2.9 us in a graph, 5.8 a call, of
 // which 5.3 are the host's.  A part of a token is two batches, so that its angles
 // serve 16 rows or more (head_dim 64: 32); in us for these three: half the batches
-// 36, 38, 5.8; one part 38, 47, 6.1; a batch a part 40, 41, 5.9.  Tokens are cut
+// 36, 38, 5.8; one part 38, 47, 6.1; a batch a part 40, 41, 5.9.  The other forms of
+// the first: head_dim 64 (101 MB) 20.9 us, 0.72, with 64 heads (168 MB) 32.0, 0.79;
+// E4M3 cache (185 MB) 39 us, 0.71; INT8 (185 MB) 47 us, 0.59.  Tokens are cut
 // into more parts only where that leaves warps idle.  (6 CTAs an SM: 37 and 38; 12:
 // 55 and 45, with registers spilt.)
 cudaError_t launch_rope_append(int kv_dtype, int D, bool halves, RopeArgs a, int num_sms, cudaStream_t stream) {

@@ -22,7 +22,8 @@
 // tile run at HBM speed (64 sequences of 2048 to 4096 tokens, 32 nodes, 8 KV
 // heads: 151 us with plan and merge, 0.83 of the copy rate), long contexts with
 // many rows at 0.72 of the bf16 peak (4 x 32k tokens, 64 nodes, 8 heads a KV head:
-// 194 us), a prompt of 8192 tokens (32 / 8 heads, packed) at 0.71 (401 us).
+// 194 us), a prompt of 8192 tokens (32 / 8 heads, packed) at 0.62 to 0.71 (401 to 459
+// us, by the box and by how long it has been at work: power).
 // One-byte caches fill no unit: page scales and widening add two thirds to the
 // instructions of a step, and a step is a chain of hand-overs (codes
 // landed, widened, S, the maximum agreed, P, PV).  So are D 64 pairs (tensor pipe

@@ -20,7 +20,9 @@
 // The drawn token is a border among sums over the vocabulary, so everything is
 // summed to 2^-32 or better: p - A q is kept as an unevaluated sum of two
 // floats (error-free transformations of addition and product, T. J. Dekker and
-// D. E. Knuth), so is everything that is summed or compared.  There are no
+// D. E. Knuth), so is everything that is summed or compared.  (A is right to some
+// 2^-46, so p - A q to 2^-44 of A q where a node loses two children or more; behind
+// the first it is exact.)  There are no
 // doubles in it: fp64 units do 2 operations a clock and SM, and with doubles in the
 // draw alone it took 9 to 12 us of a call instead of 2.  (Only a comparison whose
 // products leave fp32's range is made of doubles.)
@@ -32,12 +34,12 @@
 // memory which row to sum next; the CTAs take its chunks of 512 values in turn.
 // Only the first CTA decides, so the others cannot come to another end.
 //
-// Measured: 64 sequences, 32 nodes, 128,256 tokens, drawn drafts 44 us (1.75 passes
+// Measured: 64 sequences, 32 nodes, 128,256 tokens, drawn drafts 44 to 47 us (1.75 passes
 // a sequence on average, 5 or 6 in the slowest: the first from HBM together, 7 to 10
 // us, then a few sequences' in turn, each 3.7 us of sums, a chunk's latency from L2 at
 // a time, 2.2 of a cluster barrier and the first warp's decision and 0.7 of the other
 // barrier; 4 us at the end for the draw); 48 sequences, 21 nodes, 50,257 tokens,
-// drafts without randomness 15 to 17 us (a pass at each node that loses a child); one
+// drafts without randomness 15 to 18 us (a pass at each node that loses a child); one
 // sequence, 8 nodes, 32,000 tokens 8 to 19 us, by its passes.  Kept one by one for
 // the batch: the copies ahead 54 -> 48, two elements an instruction 46.4 -> 43.8.
 // (Later chunks prefetched to L2 at a pass's start: 58 instead of 54; the first chunk
@@ -747,7 +749,7 @@ cudaError_t launch_verify_tree(const VerifyArgs& a, int num_sms, cudaStream_t st
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
   const size_t smem = sizeof(Pair) * static_cast<size_t>(chunks);
-  if (sizeof(VerifyShared) + smem > 48 * 1024) {  // (above 350,000 tokens)
+  if (sizeof(VerifyShared) + smem > 48 * 1024) {  // (above 194,557 tokens: 380 chunk sums fit beside VerifyShared)
     cudaError_t e = cudaFuncSetAttribute(verify_tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Pair) * kVerifyMaxChunks);
     if (e != cudaSuccess) return e;
   }
